@@ -39,12 +39,13 @@ def _nvcc() -> str:
 
 def _sources():
     return [os.path.join(CSRC, f) for f in ("attn_api.cu", "attn_fwd_1q_sm103.cu", "attn_fwd_1qp_sm103.cu",
-                                            "attn_noalloc.cu", "attn_bwd_api.cu", "attn_bwd_sm103.cu", "attn_bwd256_sm103.cu")]
+                                            "attn_noalloc.cu", "attn_bwd_api.cu", "attn_bwd_sm103.cu", "attn_bwd256_sm103.cu",
+                                            "cache_api.cu", "cache_fwd_sm103.cu", "cache_pages_sm103.cu", "cache_select_sm103.cu")]
 
 
 def _deps():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(ROOT, "include", "attn.h"))
+    files += [os.path.join(ROOT, "include", f) for f in ("attn.h", "attn_cache.h")]
     return files
 
 

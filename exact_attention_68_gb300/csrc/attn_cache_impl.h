@@ -1,0 +1,104 @@
+// attn_cache_impl.h — kernel parameters and launch entries shared by the host
+// API of the 8-bit cache and its kernel translation units (host-compilable).
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime_api.h>
+
+namespace ea {
+
+// The pool of pages (see include/attn_cache.h for the layout).
+struct CacheView {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int8_t* k_bounds;
+  int pages, heads;
+  int D, pitch;         // channels, bytes of one row
+  int page, log2_page;  // token slots of a page
+};
+
+// The sequences of a call.
+struct SeqView {
+  const int* table;
+  const int* lens;
+  const int* fresh;  // may be null: T new tokens each
+  int batch, width, T;
+  int* status;
+};
+
+struct CacheAppendParams {
+  CacheView c;
+  SeqView s;
+  const uint16_t* k;  // [batch, heads, T, D]
+  const uint16_t* v;
+  int pages_per_seq;  // pages T tokens can touch
+};
+cudaError_t cache_append_launch(const CacheAppendParams& p, bool f16, cudaStream_t stream);
+
+struct CacheEvictParams {
+  CacheView c;
+  SeqView s;
+  const float* mass;
+  const int* dst_table;
+  int dst_width;
+  int keep, recent;
+  int* kept;
+  int* new_lens;
+  float* mass_out;
+  uint32_t* used;   // workspace: two bits per page of the pool, [2][words]
+  int used_words;
+  int* dst_page;    // workspace: dst_table after its checks, -1: not to be written
+};
+cudaError_t cache_evict_launch(const CacheEvictParams& p, cudaStream_t stream);
+
+struct CacheSelectParams {
+  CacheView c;
+  SeqView s;
+  const uint16_t* q;  // [batch, heads·G, T, D]
+  int G;
+  int count;
+  int* pages;     // [batch, heads, count]
+  float* scores;  // [batch, heads, width]
+};
+cudaError_t cache_select_launch(const CacheSelectParams& p, bool f16, cudaStream_t stream);
+
+// Tokens of one chunk, the unit of work of the attention: one warp's step.
+constexpr int kCacheChunk = 64;
+// Query rows of one pass over a (sequence, head)'s keys.
+constexpr int kCacheRows = 16;
+
+struct CacheFwdParams {
+  CUtensorMap tm_k, tm_v;  // (channel, slot, page·head), box: a swizzled row x one page
+  CacheView c;
+  SeqView s;
+  const uint16_t* q;   // [batch, heads·G, T, D]
+  uint16_t* out;
+  float* lse;
+  const int* list;     // [batch, heads, listed] or null
+  int listed;
+  int G, row_tiles;    // query heads per key head; ceil(G·T / kCacheRows)
+  float scale_log2;
+  int workers;         // parts the chunks of all (sequence, head, row tile) are dealt to
+  int min_chunks;      // fewest chunks worth a worker of their own
+  float* part;         // workspace: partial results, two slots per worker
+  float* scores;       // workspace: scaled scores in log2 units, or null (no mass)
+  int score_cols;      // keys per row of `scores`
+  float* mass;         // [batch, heads, width·page] or null
+  uint64_t timeout_ns;
+};
+// Floats of one partial result: O [16][width], then m, r, l [16] each.
+template <int WIDTH>
+constexpr int kCachePartFloats = kCacheRows * WIDTH + 3 * kCacheRows;
+// Width of the kernel that runs a head dimension: 64, 128 or 256.
+inline int cache_kernel_width(int64_t D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+// Warps of one CTA of that kernel.
+inline int cache_kernel_warps(int width) { return width <= 128 ? 8 : 4; }
+
+cudaError_t cache_fwd_launch(const CacheFwdParams& p, int width, bool warp_workers, bool f16,
+                             int ctas, cudaStream_t stream);
+
+}  // namespace ea

@@ -1,0 +1,868 @@
+// cache_fwd_sm103.cu — attention of a few new query tokens over the 8-bit
+// cache on GB300 (sm_103a).
+//
+// Per query row: t_j = scale·log2e·k_scale·(q·code_j), the running maximum m
+// and sum l of 2^(t_j - m), and out = Σ 2^(t_j - m)·v_scale·code_j / l.
+//
+// What bounds it is reading the cache once: 2·D bytes a key and head, against
+// 4·D·G multiply-adds (G query heads a key head) that the tensor cores take at
+// 16-bit rate.  So the work is cut for bytes in flight.  The unit is a chunk
+// of 64 keys of one (sequence, head), a warp's step; the chunks of all
+// (sequence, head, row tile) stand in one line that is dealt evenly to
+// `workers`, whatever the lengths.  A warp feeds itself: its lane-elected TMA
+// loads bring the pages of its next K and V chunks into its own ring of
+// shared memory (128-byte swizzle; columns past D read as zero) while it works
+// on the current one, so no warp waits for another.
+//
+// Arithmetic of a chunk, 16 query rows (one mma tile): codes become fp16
+// exactly; q is brought to fp16 by a power of two per row chosen from its
+// largest element, which keeps bf16's 8 bits over 2^28 of range; S = Q·Kᵀ and
+// O += P·V are mma.m16n8k16 with fp32 sums.  A 16-channel unit of a key row is
+// one 16-byte load per lane: a lane's four consecutive channels of each k-step
+// are the same channels that its Q fragment holds, so no data moves between
+// lanes.  V, stored like K, comes transposed out of ldmatrix.  A 128-row
+// tcgen05 tile would hold 16 rows of queries at best, an eighth of its work.
+//
+// Page scales of V enter P: O is kept relative to r, the running maximum of
+// t + log2(v_scale), and P = 2^(t + log2 v_scale - r + 14) fits fp16 however the
+// pages' scales differ; its smallest step, 2^-38 of the largest term, is far
+// below the 11 bits it is rounded to.
+//
+// A worker that covers a segment (one sequence, head and row tile) writes the
+// result; others write O, m, r, l to the workspace and a second kernel joins
+// them in a fixed order.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "cache_common.cuh"
+
+namespace ea {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2f = 0.6931471805599453f;
+constexpr int kRows = kCacheRows;
+constexpr int kPShift = 14;  // P is 2^14 times the weight relative to r
+constexpr int kFar = 0x3fffffff;  // position of a token that is not there
+constexpr uint64_t kDrainNs = 1000000000ull;
+
+enum : int { kSiteCacheK = 0x7500, kSiteCacheV = 0x7600 };
+
+// WIDTH: 64, 128 or 256 channels; WORKER: warps of one worker (all of the CTA's, or 1)
+template <int WIDTH, int WORKER>
+struct CacheFwdLayout {
+  static constexpr int kWarps = WIDTH <= 128 ? 8 : 4;
+  static constexpr int kRowBytes = WIDTH >= 128 ? 128 : 64;  // one swizzled row
+  static constexpr int kBlocks = WIDTH / kRowBytes;          // column blocks of a chunk
+  static constexpr int kBlockBytes = kCacheChunk * kRowBytes;
+  static constexpr int kSlot = kBlocks * kBlockBytes;        // one chunk of K or V
+  static constexpr int kSlots = 192 * 1024 / (kWarps * kSlot);
+  static constexpr int kWorkers = kWarps / WORKER;           // workers of a CTA
+  static constexpr int kQPitch = 2 * WIDTH;                  // bytes of a Q row
+  // chunks whose page data is held: those whose K has been asked for and the current one
+  static constexpr int kMeta = kSlots / 2 + 1;
+  static constexpr int kJoinCols = 32;                       // columns joined at a time
+  static constexpr int kRingOff = 0;
+  static constexpr int kQOff = kWarps * kSlots * kSlot;
+  static constexpr int kQsOff = kQOff + kWorkers * kRows * kQPitch;  // row factors
+  static constexpr int kMetaOff = kQsOff + kWorkers * kRows * 4;
+  static constexpr int kBarOff = kMetaOff + kWarps * kMeta * 4 * 16;
+  static constexpr int kMiscOff = kBarOff + kWarps * kSlots * 8;
+  static constexpr int kStatOff = kMiscOff + 16;
+  static constexpr int kJoinOff = kStatOff + (WORKER > 1 ? kWarps * kRows * 12 : 0);
+  static constexpr int kJoinPitch = kJoinCols + 4;
+  static constexpr int kEnd = kJoinOff + (WORKER > 1 ? kWarps * kRows * kJoinPitch * 4 : 0);
+  static constexpr int kAlloc = kEnd + 1024;
+  static_assert(kAlloc <= 232448, "shared memory budget exceeded");
+  static_assert(kSlots >= 3, "a K, a V and the next K in flight");
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two 16 x 16 byte matrices, transposed: a lane gets, of matrix i, column
+// lane/4 (r[2i]) and lane/4 + 8 (r[2i + 1]) of rows 4·(lane%4) .. +3.
+__device__ __forceinline__ void ldmatrix_b8_trans_x2(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(addr)
+               : "memory");
+  return r;
+}
+
+__device__ __forceinline__ void tma_load_3d_plain(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                                  int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 1);
+  return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+
+// Chunks of each of sequence b's segments (0: nothing to do).
+__device__ __forceinline__ int seq_chunks(const CacheFwdParams& p, int b, bool report, int* len, int* n) {
+  load_seq(p.s, p.c, b, report, len, n);
+  if (*n == 0) return 0;
+  const int pages = (*len + p.c.page - 1) >> p.c.log2_page;
+  const int read = p.list != nullptr ? min(pages, p.listed) : pages;
+  // a segment without keys still has rows to write
+  return max(1, ((read << p.c.log2_page) + kCacheChunk - 1) / kCacheChunk);
+}
+
+// The deal: chunks of every segment in line, sequence by sequence.
+struct Deal {
+  int total;  // chunks in line
+  int per;    // chunks of a worker
+};
+__device__ __forceinline__ Deal deal_chunks(const CacheFwdParams& p, bool report) {
+  const int lane = threadIdx.x & 31, hr = p.c.heads * p.row_tiles;
+  int sum = 0;
+  for (int b = lane; b < p.s.batch; b += 32) {
+    int len, n;
+    sum += hr * seq_chunks(p, b, report, &len, &n);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  Deal d;
+  d.total = sum;
+  d.per = max((sum + p.workers - 1) / p.workers, p.min_chunks);
+  return d;
+}
+
+// A segment in the line: sequence, head and row tile.
+struct Segment {
+  int b, hr;     // hr = head · row_tiles + row tile
+  int first, nc; // its chunks: first .. first + nc - 1
+  int len, n;
+};
+// The segment that holds chunk `at` (< total).  Whole warp.
+__device__ __forceinline__ Segment find_segment(const CacheFwdParams& p, int at) {
+  const int lane = threadIdx.x & 31, hr = p.c.heads * p.row_tiles;
+  int before = 0;
+  for (int b0 = 0;; b0 += 32) {
+    const int b = b0 + lane;
+    int len = 0, n = 0;
+    const int nc = b < p.s.batch ? seq_chunks(p, b, false, &len, &n) : 0;
+    int upto = nc * hr;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += o;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, before + upto > at);
+    if (hit != 0 || b0 + 32 >= p.s.batch) {
+      const int src = hit != 0 ? __ffs(hit) - 1 : 0;
+      Segment s;
+      s.b = b0 + src;
+      s.nc = __shfl_sync(0xffffffffu, nc, src);
+      s.len = __shfl_sync(0xffffffffu, len, src);
+      s.n = __shfl_sync(0xffffffffu, n, src);
+      const int base = before + __shfl_sync(0xffffffffu, upto, src) - s.nc * hr;
+      s.hr = s.nc > 0 ? (at - base) / s.nc : 0;
+      s.first = base + s.hr * s.nc;
+      return s;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+}
+// Moves to the next segment; false behind the last.
+__device__ __forceinline__ bool next_segment(const CacheFwdParams& p, Segment& s) {
+  s.first += s.nc;
+  if (++s.hr < p.c.heads * p.row_tiles) return true;
+  s.hr = 0;
+  do {
+    if (++s.b >= p.s.batch) return false;
+    s.nc = seq_chunks(p, s.b, false, &s.len, &s.n);
+  } while (s.nc == 0);
+  return true;
+}
+
+// Row `row` (query head in the group · T + token) of a segment: its place in
+// q, out (rows of D) and lse.
+__device__ __forceinline__ int64_t row_place(const CacheFwdParams& p, int b, int h, int row) {
+  return (static_cast<int64_t>(b) * p.c.heads + h) * (p.G * p.s.T) + row;
+}
+
+template <bool F16>
+__device__ __forceinline__ void store_pair(uint16_t* at, float x, float y) {
+  *reinterpret_cast<uint32_t*>(at) = pack_x2<F16>(x, y);
+}
+
+template <int WIDTH, int WORKER, bool F16>
+__global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER>::kWarps * 32, 1)
+    cache_fwd_kernel(const __grid_constant__ CacheFwdParams p) {
+  using L = CacheFwdLayout<WIDTH, WORKER>;
+  constexpr int kKSteps = WIDTH / 64;  // 64-channel blocks of Q·Kᵀ
+  constexpr int kTiles = WIDTH / 8;    // 8-channel tiles of O
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t sb = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gid = lane >> 2, t4 = lane & 3;
+  const int worker_in_cta = warp / WORKER, wi = warp % WORKER;
+  const uint32_t ring = sb + L::kRingOff + warp * L::kSlots * L::kSlot;
+  const uint32_t bars = sb + L::kBarOff + warp * L::kSlots * 8;
+  const uint32_t meta = sb + L::kMetaOff + warp * L::kMeta * 64;
+  const uint32_t qs = sb + L::kQOff + worker_in_cta * kRows * L::kQPitch;
+  const uint32_t qf = sb + L::kQsOff + worker_in_cta * kRows * 4;
+  const uint32_t abort_addr = sb + L::kMiscOff;
+  if (lane == 0) {
+    for (int s = 0; s < L::kSlots; ++s) mbar_init(bars + 8 * s, 1);
+    fence_barrier_init();
+    if (warp == 0) st_volatile_shared(abort_addr, 0);
+  }
+  __syncthreads();
+  const WaitCtl ctl{abort_addr, p.s.status, p.timeout_ns};
+
+  const int worker = blockIdx.x * L::kWorkers + worker_in_cta;
+  const Deal deal = deal_chunks(p, blockIdx.x == 0 && warp == 0);
+  // workers are few enough that worker · per stays below 2^31 (total < 2^30)
+  const int begin = min(static_cast<int64_t>(worker) * deal.per, static_cast<int64_t>(deal.total));
+  const int end = min(begin + deal.per, deal.total);
+  if (begin >= end) return;  // the whole worker; with WORKER > 1 the whole CTA
+
+  const int seg_rows = p.G * p.s.T;
+  const int log2p = p.c.log2_page, page_mask = p.c.page - 1;
+
+  // ---------------- fetching: chunks begin + wi, + WORKER, ... of the line
+  Segment fs = find_segment(p, begin);
+  int f_at = begin + wi;      // next chunk to fetch K of
+  int f_page = -1, f_pos = kFar;  // this lane's 16-token group (t4) of it
+  int f_h = 0;                // its head
+  bool f_have = false;
+  int i_slot = 0;             // slot of the next item
+  int f_meta = 0;             // page data entry of the chunk f_at
+  float pend_ks = 0.f, pend_vs = 0.f;  // page data on its way
+  int pend_pos = kFar, pend_meta = -1;
+  int issued = 0, used = 0;   // items (K or V of a chunk)
+
+  auto look_up = [&]() {  // pages of chunk f_at
+    f_have = f_at < end;
+    f_page = -1;
+    f_pos = kFar;
+    if (!f_have) return;
+    while (f_at >= fs.first + fs.nc) next_segment(p, fs);
+    f_h = fs.hr / p.row_tiles;
+    const int tok = (f_at - fs.first) * kCacheChunk + 16 * t4;
+    int i = tok >> log2p;
+    bool in = true;
+    if (p.list != nullptr) {
+      in = i < p.listed;
+      if (in) {
+        const int* l = p.list + (static_cast<int64_t>(fs.b) * p.c.heads + f_h) * p.listed;
+        const int e = l[i];
+        const int prev = i > 0 ? l[i - 1] : -1;
+        in = e >= 0;
+        if (in && (e >= p.s.width || e <= prev)) {
+          dbg_fail(p.s.status, kChkCacheList);
+          in = false;
+        }
+        i = e;
+      }
+    }
+    const int pos = in ? (i << log2p) + (tok & page_mask) : kFar;
+    if (in && pos < fs.len) {
+      f_page = p.s.table[static_cast<int64_t>(fs.b) * p.s.width + i];
+      f_pos = pos;
+    }
+  };
+  auto flush_pending = [&]() {
+    if (pend_meta >= 0) {
+      // v_scale as a power of two and a factor in [1, 2)
+      const uint32_t u = __float_as_uint(pend_vs);
+      const float ev = static_cast<float>(static_cast<int>((u >> 23) & 0xffu) - 127);
+      const float vm = __uint_as_float((u & 0x807fffffu) | 0x3f800000u);
+      if (lane < 4)
+        st_shared_v4(meta + pend_meta * 64 + lane * 16, static_cast<uint32_t>(pend_pos),
+                     __float_as_uint(pend_ks), __float_as_uint(ev), __float_as_uint(vm));
+      pend_meta = -1;
+      __syncwarp();
+    }
+  };
+  // K (then V) of chunk f_at into the next slot; V moves on to the next chunk
+  bool f_is_v = false;
+  auto issue = [&]() {
+    if (!f_is_v) flush_pending();
+    if (!f_have) return;
+    if (!f_is_v && f_pos != kFar && (f_page < 0 || f_page >= p.c.pages)) {
+      dbg_fail(p.s.status, kChkCacheTable);
+      f_page = -1;
+      f_pos = kFar;
+    }
+    const bool lead = lane < 4 && ((16 * t4) & page_mask) == 0 && f_pos != kFar;
+    const uint32_t leads = __ballot_sync(0xffffffffu, lead);
+    const uint32_t bar = bars + 8 * i_slot;
+    if (lane == 0) {
+      if (leads != 0) mbar_arrive_expect_tx(bar, __popc(leads) * L::kBlocks * p.c.page * L::kRowBytes);
+      else mbar_arrive(bar);
+    }
+    __syncwarp();
+    const int64_t gh = static_cast<int64_t>(f_page) * p.c.heads + f_h;
+    if (lead) {
+#pragma unroll
+      for (int cb = 0; cb < L::kBlocks; ++cb)
+        tma_load_3d_plain(ring + i_slot * L::kSlot + cb * L::kBlockBytes + 16 * t4 * L::kRowBytes,
+                          f_is_v ? &p.tm_v : &p.tm_k, bar, cb * L::kRowBytes, 0, static_cast<int>(gh));
+    }
+    if (!f_is_v) {
+      pend_pos = f_pos;
+      pend_ks = f_pos != kFar ? __ldg(p.c.k_scale + gh) : 0.f;
+      pend_vs = f_pos != kFar ? __ldg(p.c.v_scale + gh) : 1.f;
+      pend_meta = f_meta;
+    } else {
+      f_at += WORKER;
+      f_meta = (f_meta + 1) % L::kMeta;
+      look_up();
+    }
+    f_is_v = !f_is_v;
+    if (++i_slot == L::kSlots) i_slot = 0;
+    ++issued;
+  };
+  look_up();
+#pragma unroll 1
+  for (int s = 0; s < L::kSlots; ++s) issue();
+
+  // ---------------- the worker's segments
+  const int row0 = 4 * (gid >> 1) + (gid & 1);  // key row of this lane in a pair of K tiles
+  Segment cs = find_segment(p, begin);
+  int at = begin + wi, u_slot = 0, u_parity = 0, u_meta = 0;
+  bool alive = true;
+  for (int seg_at = begin; seg_at < end;) {
+    while (seg_at >= cs.first + cs.nc) next_segment(p, cs);
+    const int seg_end = min(end, cs.first + cs.nc);
+    const int h = cs.hr / p.row_tiles, rt = cs.hr % p.row_tiles;
+    const int tile_row = rt * kRows, tile_rows = min(kRows, seg_rows - tile_row);
+
+    // ---- Q to fp16 with a power of two per row
+    {
+      constexpr int kMine = kRows / WORKER, kLanes = 32 / kMine;  // rows of a warp, lanes of a row
+      const int r = wi * kMine + lane / kLanes, part = lane % kLanes;
+      const bool in = r < tile_rows;
+      const uint16_t* q = p.q + row_place(p, cs.b, h, tile_row + (in ? r : 0)) * p.c.D;
+      float a = 0.f;
+      for (int c = 8 * part; c < p.c.D; c += 8 * kLanes) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(q + c));
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 x = pair_to_float2<F16>(ws[e]);
+          a = fmaxf(a, fmaxf(finite_abs(x.x), finite_abs(x.y)));
+        }
+      }
+#pragma unroll
+      for (int d = kLanes / 2; d > 0; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+      // up = 2^(14 - e) for a in [2^e, 2^(e+1)); kept in range for tiny and huge a
+      int e = static_cast<int>(__float_as_uint(a) >> 23) - 127;
+      e = max(-100, e);
+      const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
+      for (int c = 8 * part; c < WIDTH; c += 8 * kLanes) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (in && c < p.c.D) w = __ldg(reinterpret_cast<const uint4*>(q + c));
+        uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 x = pair_to_float2<F16>(ws[k]);
+          ws[k] = pack_f16x2(x.x * up, x.y * up);
+        }
+        // odd rows swap the halves of each 32 bytes: a fragment load of two
+        // rows then meets every bank once
+        st_shared_v4(qs + r * L::kQPitch + ((2 * c) ^ ((r & 1) << 4)), ws[0], ws[1], ws[2], ws[3]);
+      }
+      if (part == 0)
+        st_shared_f32(qf + 4 * r, p.scale_log2 * __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23));
+      if constexpr (WORKER > 1) __syncthreads();
+      else __syncwarp();
+    }
+    const float q0 = ld_shared_f32(qf + 4 * gid), q1 = ld_shared_f32(qf + 4 * (gid + 8));
+    // last position a row may attend to; rows that are not there see every key
+    auto last_of = [&](int r) {
+      const int i = (tile_row + r) % p.s.T;
+      return r < tile_rows && i < cs.n ? cs.len - cs.n + i : cs.len - 1;
+    };
+    const int last0 = last_of(gid), last1 = last_of(gid + 8);
+    const int first_last = cs.len - cs.n;  // every row sees the keys up to here
+
+    float o[kTiles][4];
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, r0 = -INFINITY, r1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+#pragma unroll 1
+    for (; at < seg_end; at += WORKER) {
+      // ---- S = Q·Kᵀ
+      if (alive) alive = __all_sync(0xffffffffu, wait_bounded(bars + 8 * u_slot, u_parity, ctl, kSiteCacheK));
+      if (!alive) continue;
+      const uint32_t kslot = ring + u_slot * L::kSlot;
+      float s[8][4];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+#pragma unroll
+      for (int kb = 0; kb < kKSteps; ++kb) {
+        const uint32_t qa = qs + gid * L::kQPitch + kb * 128 + 32 * t4 + ((gid & 1) << 4);
+        const uint32_t qb = qa ^ 16u;  // rows gid and gid + 8 are odd together
+        const uint4 x0 = ld_shared_v4(qa), x1 = ld_shared_v4(qb);
+        const uint4 y0 = ld_shared_v4(qa + 8 * L::kQPitch), y1 = ld_shared_v4(qb + 8 * L::kQPitch);
+        const uint32_t xa[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+        const uint32_t ya[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+        const int unit = kb * 4 + t4;  // 16 channels
+        constexpr int kUnits = L::kRowBytes / 16;
+        const uint32_t block = kslot + (unit / kUnits) * L::kBlockBytes;
+        const int cu = unit % kUnits;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int row = row0 + 16 * (j >> 1) + 2 * (j & 1);
+          const int sw = kUnits == 8 ? (row & 7) : ((row >> 1) & 3);
+          const uint4 kw = ld_shared_v4(block + row * L::kRowBytes + ((cu ^ sw) << 4));
+          const uint32_t kc[4] = {kw.x, kw.y, kw.z, kw.w};
+#pragma unroll
+          for (int st = 0; st < 4; ++st) {
+            uint32_t b0, b1;
+            e4m3x4_to_f16(kc[st], &b0, &b1);
+            mma_f16(s[j], xa[2 * st], ya[2 * st], xa[2 * st + 1], ya[2 * st + 1], b0, b1);
+          }
+        }
+      }
+      ++used;
+      if (++u_slot == L::kSlots) u_slot = 0, u_parity ^= 1;
+      __syncwarp();
+      issue();
+
+      // ---- softmax of the chunk.  Lane's keys: 16·g + 4·t4 + 2·j + e (tile 2·g + j)
+      float mx0 = -INFINITY, mx1 = -INFINITY, rx0 = -INFINITY, rx1 = -INFINITY;
+      float ev[4], vm[4];
+      int gpos[4];
+      bool tail = false;  // some key is hidden from some row
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const uint4 md = ld_shared_v4(meta + u_meta * 64 + g * 16);
+        gpos[g] = static_cast<int>(md.x);
+        ev[g] = __uint_as_float(md.z);
+        vm[g] = __uint_as_float(md.w);
+        tail = tail || gpos[g] + 15 > first_last;
+        const float f0 = q0 * __uint_as_float(md.y), f1 = q1 * __uint_as_float(md.y);
+#pragma unroll
+        for (int j = 2 * g; j < 2 * g + 2; ++j) {
+          s[j][0] *= f0, s[j][1] *= f0;
+          s[j][2] *= f1, s[j][3] *= f1;
+        }
+      }
+      if (tail) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int pos = gpos[j >> 1] + 4 * t4 + 2 * (j & 1);
+          if (pos > last0) s[j][0] = -INFINITY;
+          if (pos + 1 > last0) s[j][1] = -INFINITY;
+          if (pos > last1) s[j][2] = -INFINITY;
+          if (pos + 1 > last1) s[j][3] = -INFINITY;
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float a0 = fmaxf(fmaxf(s[2 * g][0], s[2 * g][1]), fmaxf(s[2 * g + 1][0], s[2 * g + 1][1]));
+        const float a1 = fmaxf(fmaxf(s[2 * g][2], s[2 * g][3]), fmaxf(s[2 * g + 1][2], s[2 * g + 1][3]));
+        mx0 = fmaxf(mx0, a0), mx1 = fmaxf(mx1, a1);
+        rx0 = fmaxf(rx0, a0 + ev[g]), rx1 = fmaxf(rx1, a1 + ev[g]);
+      }
+      if (p.scores != nullptr) {
+        const int64_t srow = row_place(p, cs.b, h, tile_row + gid) * p.score_cols +
+                             (at - cs.first) * kCacheChunk + 4 * t4;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          if (gid < tile_rows)
+            *reinterpret_cast<float4*>(p.scores + srow + 16 * g) =
+                make_float4(s[2 * g][0], s[2 * g][1], s[2 * g + 1][0], s[2 * g + 1][1]);
+          if (gid + 8 < tile_rows)
+            *reinterpret_cast<float4*>(p.scores + srow + 8ll * p.score_cols + 16 * g) =
+                make_float4(s[2 * g][2], s[2 * g][3], s[2 * g + 1][2], s[2 * g + 1][3]);
+        }
+      }
+      const float mn0 = fmaxf(m0, quad_max(mx0)), mn1 = fmaxf(m1, quad_max(mx1));
+      const float rn0 = fmaxf(r0, quad_max(rx0)), rn1 = fmaxf(r1, quad_max(rx1));
+      // references: 0 where no key has been allowed yet
+      const float mr0 = mn0 == -INFINITY ? 0.f : mn0, mr1 = mn1 == -INFINITY ? 0.f : mn1;
+      const float rr0 = rn0 == -INFINITY ? 0.f : rn0, rr1 = rn1 == -INFINITY ? 0.f : rn1;
+      l0 *= ex2_approx(m0 - mr0), l1 *= ex2_approx(m1 - mr1);
+      const float b0 = ex2_approx(r0 - rr0), b1 = ex2_approx(r1 - rr1);
+      m0 = mn0, m1 = mn1;
+      if (__any_sync(0xffffffffu, rn0 != r0 || rn1 != r1)) {
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) o[j][0] *= b0, o[j][1] *= b0, o[j][2] *= b1, o[j][3] *= b1;
+      }
+      r0 = rn0, r1 = rn1;
+      uint32_t pa[4][4];  // P, A fragments of the four 16-key steps
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        // a group whose weights are far below the chunk's has a factor beyond
+        // range; its P is held finite
+        const float f0 = ex2_approx(fminf(ev[g] + (mr0 - rr0) + kPShift, 126.f)) * vm[g];
+        const float f1 = ex2_approx(fminf(ev[g] + (mr1 - rr1) + kPShift, 126.f)) * vm[g];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float* x = s[2 * g + j];
+          const float p0 = ex2_approx(x[0] - mr0), p1 = ex2_approx(x[1] - mr0);
+          const float p2 = ex2_approx(x[2] - mr1), p3 = ex2_approx(x[3] - mr1);
+          l0 += p0 + p1, l1 += p2 + p3;
+          pa[g][2 * j] = pack_f16x2(p0 * f0, p1 * f0);
+          pa[g][2 * j + 1] = pack_f16x2(p2 * f1, p3 * f1);
+        }
+      }
+
+      // ---- O += P·V
+      if (alive) alive = __all_sync(0xffffffffu, wait_bounded(bars + 8 * u_slot, u_parity, ctl, kSiteCacheV));
+      if (!alive) continue;
+      const uint32_t vslot = ring + u_slot * L::kSlot;
+      uint32_t vmask[4];  // bytes of this lane's four tokens of each step that exist
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int n = min(4, max(0, cs.len - (gpos[g] + 4 * t4)));
+        vmask[g] = n == 4 ? 0xffffffffu : (1u << (8 * n)) - 1u;
+      }
+      constexpr int kUnits = L::kRowBytes / 16;
+      const int vrow = lane & 15;
+      uint32_t nan_seen = 0;
+#pragma unroll
+      for (int u = 0; u < WIDTH / 16; u += 2) {
+        if (16 * u < p.c.D) {
+          const int unit = u + (lane >> 4);
+          const uint32_t block = vslot + (u / kUnits) * L::kBlockBytes;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int row = 16 * g + vrow;
+            const int sw = kUnits == 8 ? (row & 7) : ((row >> 1) & 3);
+            uint32_t w[4];
+            ldmatrix_b8_trans_x2(block + row * L::kRowBytes + (((unit % kUnits) ^ sw) << 4), w);
+            if (tail) {
+              // slots that hold no token of the sequence count as zero; so do
+              // NaN codes here, which rows that may not see them must not meet
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                w[i] &= vmask[g];
+                const uint32_t nan = __vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                nan_seen |= nan;
+                w[i] &= ~nan;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t b0, b1;
+              e4m3x4_to_f16(w[i], &b0, &b1);
+              mma_f16(o[2 * u + i], pa[g][0], pa[g][1], pa[g][2], pa[g][3], b0, b1);
+            }
+          }
+        }
+      }
+      if (tail && __any_sync(0xffffffffu, nan_seen != 0)) {
+        // rows that may see a NaN code get it: a count of the NaN codes each
+        // row sees per channel
+        uint32_t see[4][4];
+        auto one = [](bool a, bool b) { return (a ? 0x3c00u : 0u) | (b ? 0x3c000000u : 0u); };
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int pos = gpos[g] + 4 * t4 + 2 * j;
+            see[g][2 * j] = one(pos <= last0, pos + 1 <= last0);
+            see[g][2 * j + 1] = one(pos <= last1, pos + 1 <= last1);
+          }
+#pragma unroll
+        for (int u = 0; u < WIDTH / 16; u += 2) {
+          if (16 * u < p.c.D) {
+            const int unit = u + (lane >> 4);
+            const uint32_t block = vslot + (u / kUnits) * L::kBlockBytes;
+            float c[4][4] = {};
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const int row = 16 * g + vrow;
+              const int sw = kUnits == 8 ? (row & 7) : ((row >> 1) & 3);
+              uint32_t w[4];
+              ldmatrix_b8_trans_x2(block + row * L::kRowBytes + (((unit % kUnits) ^ sw) << 4), w);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t nan = __vcmpeq4(w[i] & vmask[g] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                mma_f16(c[i], see[g][0], see[g][1], see[g][2], see[g][3],
+                        one(nan & 1u, nan & 0x100u), one(nan & 0x10000u, nan & 0x1000000u));
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (c[i][e] > 0.f) o[2 * u + i][e] = __int_as_float(0x7fffffff);
+          }
+        }
+      }
+      ++used;
+      if (++u_slot == L::kSlots) u_slot = 0, u_parity ^= 1;
+      if (++u_meta == L::kMeta) u_meta = 0;
+      __syncwarp();
+      issue();
+    }
+    l0 = quad_sum(l0), l1 = quad_sum(l1);
+
+    // ---- the segment's result, or this worker's part of it
+    const bool whole = seg_at == cs.first && seg_end == cs.first + cs.nc;
+    float* part = p.part + (2ll * worker + (seg_at == cs.first ? 1 : 0)) * kCachePartFloats<WIDTH>;
+    auto live = [&](int r) { return r < tile_rows && (tile_row + r) % p.s.T < cs.n; };
+    // 2^(r - 14 - m) / l: what an entry of O is multiplied by
+    auto factor = [](float m, float r, float l) {
+      return m == -INFINITY ? 0.f : ex2_approx(r - m - kPShift) / l;
+    };
+    if constexpr (WORKER == 1) {
+      if (whole) {
+        const float w0 = factor(m0, r0, l0), w1 = factor(m1, r1, l1);
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const int r = gid + 8 * hh;
+          if (live(r)) {
+            const int64_t at_row = row_place(p, cs.b, h, tile_row + r);
+            const float w = hh ? w1 : w0, mm = hh ? m1 : m0, ll = hh ? l1 : l0;
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j)
+              if (8 * j < p.c.D) {
+                const float x = mm == -INFINITY ? 0.f : o[j][2 * hh] * w;
+                const float y = mm == -INFINITY ? 0.f : o[j][2 * hh + 1] * w;
+                store_pair<F16>(p.out + at_row * p.c.D + 8 * j + 2 * t4, x, y);
+              }
+            if (t4 == 0) p.lse[at_row] = (mm + log2f(ll)) * kLn2f;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) {
+          *reinterpret_cast<float2*>(part + gid * WIDTH + 8 * j + 2 * t4) = make_float2(o[j][0], o[j][1]);
+          *reinterpret_cast<float2*>(part + (gid + 8) * WIDTH + 8 * j + 2 * t4) = make_float2(o[j][2], o[j][3]);
+        }
+        if (t4 == 0) {
+          float* st = part + kRows * WIDTH;
+          st[gid] = m0, st[gid + 8] = m1;
+          st[16 + gid] = r0, st[16 + gid + 8] = r1;
+          st[32 + gid] = l0, st[32 + gid + 8] = l1;
+        }
+      }
+      __syncwarp();  // Q is rewritten for the next segment
+    } else {
+      // the warps' parts joined, 32 columns at a time, in the order of the warps
+      const uint32_t stat = sb + L::kStatOff, join = sb + L::kJoinOff;
+      if (t4 == 0) {
+        st_shared_f32(stat + (warp * kRows + gid) * 12, m0);
+        st_shared_f32(stat + (warp * kRows + gid) * 12 + 4, r0);
+        st_shared_f32(stat + (warp * kRows + gid) * 12 + 8, l0);
+        st_shared_f32(stat + (warp * kRows + gid + 8) * 12, m1);
+        st_shared_f32(stat + (warp * kRows + gid + 8) * 12 + 4, r1);
+        st_shared_f32(stat + (warp * kRows + gid + 8) * 12 + 8, l1);
+      }
+      __syncthreads();
+      auto joined = [&](int r, float* m, float* rr, float* l) {
+        float M = -INFINITY, R = -INFINITY, S = 0.f;
+        for (int w = 0; w < L::kWarps; ++w) {
+          M = fmaxf(M, ld_shared_f32(stat + (w * kRows + r) * 12));
+          R = fmaxf(R, ld_shared_f32(stat + (w * kRows + r) * 12 + 4));
+        }
+        for (int w = 0; w < L::kWarps; ++w) {
+          const float mw = ld_shared_f32(stat + (w * kRows + r) * 12);
+          S += mw == -INFINITY ? 0.f : ld_shared_f32(stat + (w * kRows + r) * 12 + 8) * ex2_approx(mw - M);
+        }
+        *m = M, *rr = R, *l = S;
+      };
+      float M0, R0, S0, M1, R1, S1;
+      joined(gid, &M0, &R0, &S0);
+      joined(gid + 8, &M1, &R1, &S1);
+      const float b0 = r0 == -INFINITY ? 0.f : ex2_approx(r0 - R0);
+      const float b1 = r1 == -INFINITY ? 0.f : ex2_approx(r1 - R1);
+      // the row and column pair this thread sums
+      constexpr int kThreads = L::kWarps * 32, kPairs = kRows * L::kJoinCols / 2;
+#pragma unroll
+      for (int c = 0; c < WIDTH / L::kJoinCols; ++c) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t a = join + ((warp * kRows + gid) * L::kJoinPitch + 8 * j + 2 * t4) * 4;
+          const float* x = o[4 * c + j];
+          st_shared_f32(a, x[0] * b0), st_shared_f32(a + 4, x[1] * b0);
+          st_shared_f32(a + 8 * L::kJoinPitch * 4, x[2] * b1), st_shared_f32(a + 8 * L::kJoinPitch * 4 + 4, x[3] * b1);
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < kPairs; i += kThreads) {
+          const int r = i / (L::kJoinCols / 2), col = 2 * (i % (L::kJoinCols / 2));
+          float x = 0.f, y = 0.f;
+          for (int w = 0; w < L::kWarps; ++w) {
+            const uint32_t a = join + ((w * kRows + r) * L::kJoinPitch + col) * 4;
+            x += ld_shared_f32(a), y += ld_shared_f32(a + 4);
+          }
+          const int ch = L::kJoinCols * c + col;
+          if (!whole) {
+            *reinterpret_cast<float2*>(part + r * WIDTH + ch) = make_float2(x, y);
+          } else if (ch < p.c.D && live(r)) {
+            float M, R, S;
+            joined(r, &M, &R, &S);
+            const float w = factor(M, R, S);
+            store_pair<F16>(p.out + row_place(p, cs.b, h, tile_row + r) * p.c.D + ch,
+                            M == -INFINITY ? 0.f : x * w, M == -INFINITY ? 0.f : y * w);
+          }
+        }
+        __syncthreads();
+      }
+      if (warp == 0 && t4 == 0) {
+        if (whole) {
+          if (live(gid)) p.lse[row_place(p, cs.b, h, tile_row + gid)] = (M0 + log2f(S0)) * kLn2f;
+          if (live(gid + 8)) p.lse[row_place(p, cs.b, h, tile_row + gid + 8)] = (M1 + log2f(S1)) * kLn2f;
+        } else {
+          float* st = part + kRows * WIDTH;
+          st[gid] = M0, st[gid + 8] = M1;
+          st[16 + gid] = R0, st[16 + gid + 8] = R1;
+          st[32 + gid] = S0, st[32 + gid + 8] = S1;
+        }
+      }
+    }
+    seg_at = seg_end;
+  }
+
+  // after a wait that ran out: the copies still in flight land before the CTA
+  // gives its shared memory back
+  if (lane == 0)
+    for (; used < issued; ++used) {
+      wait_drain(bars + 8 * u_slot, u_parity, kDrainNs);
+      if (++u_slot == L::kSlots) u_slot = 0, u_parity ^= 1;
+    }
+}
+
+// Joins the parts of a segment that several workers shared.  CTA (segment of
+// the widest line, 32-column block): 128 threads, 4 columns each of 16 rows.
+constexpr int kJoinThreads = 128;
+
+template <int WIDTH, bool F16>
+__global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ CacheFwdParams p) {
+  const int hr = p.c.heads * p.row_tiles;
+  const int b = blockIdx.x / hr, x = blockIdx.x % hr;
+  const Deal deal = deal_chunks(p, false);
+  int len, n;
+  const int nc = seq_chunks(p, b, false, &len, &n);
+  if (nc == 0) return;
+  int before = 0;  // chunks of the sequences before b
+  for (int i = threadIdx.x & 31; i < b; i += 32) {
+    int l2, n2;
+    before += hr * seq_chunks(p, i, false, &l2, &n2);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) before += __shfl_xor_sync(0xffffffffu, before, d);
+  const int first = before + x * nc;
+  const int w0 = first / deal.per, w1 = (first + nc - 1) / deal.per;
+  if (w0 == w1) return;  // one worker had it all
+  const int h = x / p.row_tiles, tile_row = (x % p.row_tiles) * kRows;
+  const int r = threadIdx.x / 8, col = blockIdx.y * 32 + 4 * (threadIdx.x % 8);
+  if (tile_row + r >= p.G * p.s.T || (tile_row + r) % p.s.T >= n) return;
+  auto part = [&](int w) { return p.part + (2ll * w + (w == w0 ? 1 : 0)) * kCachePartFloats<WIDTH>; };
+  float M = -INFINITY;
+  for (int w = w0; w <= w1; ++w) M = fmaxf(M, part(w)[kRows * WIDTH + r]);
+  float S = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (M != -INFINITY) {
+    for (int w = w0; w <= w1; ++w) {
+      const float* q = part(w);
+      const float m = q[kRows * WIDTH + r];
+      if (m == -INFINITY) continue;
+      S += q[kRows * WIDTH + 32 + r] * ex2_approx(m - M);
+      const float f = ex2_approx(q[kRows * WIDTH + 16 + r] - M - kPShift);
+      const float4 v = *reinterpret_cast<const float4*>(q + r * WIDTH + col);
+      acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
+    }
+    acc.x /= S, acc.y /= S, acc.z /= S, acc.w /= S;
+  }
+  const int64_t row = row_place(p, b, h, tile_row + r);
+  if (col < p.c.D) {
+    store_pair<F16>(p.out + row * p.c.D + col, acc.x, acc.y);
+    store_pair<F16>(p.out + row * p.c.D + col + 2, acc.z, acc.w);
+  }
+  if (col == 0) p.lse[row] = (M + log2f(S)) * kLn2f;
+}
+
+// mass[key] += Σ over the head's rows of 2^(t - lse): one thread a key.
+constexpr int kMassThreads = 256;
+
+__global__ void __launch_bounds__(kMassThreads) cache_mass_kernel(const __grid_constant__ CacheFwdParams p) {
+  const int h = blockIdx.y, b = blockIdx.z;
+  int len, n;
+  const int nc = seq_chunks(p, b, false, &len, &n);
+  const int key = blockIdx.x * kMassThreads + threadIdx.x;
+  if (key >= nc * kCacheChunk) return;
+  const int64_t bh = static_cast<int64_t>(b) * p.c.heads + h;
+  int pos = key;
+  if (p.list != nullptr) {
+    const int e = key >> p.c.log2_page;
+    if (e >= p.listed) return;
+    const int i = p.list[bh * p.listed + e];
+    const int prev = e > 0 ? p.list[bh * p.listed + e - 1] : -1;
+    if (i < 0 || i >= p.s.width || i <= prev) return;
+    pos = (i << p.c.log2_page) + (key & (p.c.page - 1));
+  }
+  if (pos >= len) return;
+  const int rows = p.G * p.s.T;
+  const float* s = p.scores + bh * rows * static_cast<int64_t>(p.score_cols) + key;
+  float sum = 0.f;
+  for (int r = 0; r < rows; ++r) {
+    if (r % p.s.T >= n) continue;
+    const float z = p.lse[bh * rows + r];
+    if (z == -INFINITY) continue;
+    sum += ex2_approx(s[static_cast<int64_t>(r) * p.score_cols] - z * kLog2e);
+  }
+  p.mass[bh * (static_cast<int64_t>(p.s.width) << p.c.log2_page) + pos] += sum;
+}
+
+template <int WIDTH, int WORKER, bool F16>
+cudaError_t launch_fwd(const CacheFwdParams& p, int ctas, cudaStream_t stream) {
+  using L = CacheFwdLayout<WIDTH, WORKER>;
+  auto kern = cache_fwd_kernel<WIDTH, WORKER, F16>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+  if (e != cudaSuccess) return e;
+  kern<<<ctas, L::kWarps * 32, L::kAlloc, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cache_join_kernel<WIDTH, F16><<<dim3(p.s.batch * p.c.heads * p.row_tiles, WIDTH / 32), kJoinThreads, 0, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.mass == nullptr) return e;
+  cache_mass_kernel<<<dim3((p.score_cols + kMassThreads - 1) / kMassThreads, p.c.heads, p.s.batch), kMassThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int WIDTH, bool F16>
+cudaError_t launch_fwd_w(const CacheFwdParams& p, bool warp_workers, int ctas, cudaStream_t stream) {
+  return warp_workers ? launch_fwd<WIDTH, 1, F16>(p, ctas, stream)
+                      : launch_fwd<WIDTH, CacheFwdLayout<WIDTH, 1>::kWarps, F16>(p, ctas, stream);
+}
+
+}  // namespace
+
+cudaError_t cache_fwd_launch(const CacheFwdParams& p, int width, bool warp_workers, bool f16,
+                             int ctas, cudaStream_t stream) {
+  switch (width) {
+    case 64: return f16 ? launch_fwd_w<64, true>(p, warp_workers, ctas, stream)
+                        : launch_fwd_w<64, false>(p, warp_workers, ctas, stream);
+    case 128: return f16 ? launch_fwd_w<128, true>(p, warp_workers, ctas, stream)
+                         : launch_fwd_w<128, false>(p, warp_workers, ctas, stream);
+    case 256: return f16 ? launch_fwd_w<256, true>(p, warp_workers, ctas, stream)
+                         : launch_fwd_w<256, false>(p, warp_workers, ctas, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace ea
