@@ -68,8 +68,8 @@ cudaError_t cache_select_launch(const CacheSelectParams& p, bool f16, cudaStream
 
 // Tokens of one chunk, the unit of work of the attention: one warp's step.
 constexpr int kCacheChunk = 64;
-// Query rows of one pass over a (sequence, head)'s keys.
-constexpr int kCacheRows = 16;
+// Query rows of a tile; a pass over a (sequence, head)'s keys takes one or two.
+constexpr int kCacheTileRows = 8;
 
 struct CacheFwdParams {
   CUtensorMap tm_k, tm_v;  // (channel, slot, page·head), box: a swizzled row x one page
@@ -80,25 +80,28 @@ struct CacheFwdParams {
   float* lse;
   const int* list;     // [batch, heads, listed] or null
   int listed;
-  int G, row_tiles;    // query heads per key head; ceil(G·T / kCacheRows)
+  bool f16;            // q and out are fp16 (else bf16)
+  int G, row_tiles;    // query heads per key head; passes over a head's keys
   float scale_log2;
   int workers;         // parts the chunks of all (sequence, head, row tile) are dealt to
   int min_chunks;      // fewest chunks worth a worker of their own
   float* part;         // workspace: partial results, two slots per worker
   float* scores;       // workspace: scaled scores in log2 units, or null (no mass)
-  int score_cols;      // keys per row of `scores`
+  int score_cols;      // keys of a head in `scores`
+  int score_rows;      // rows of a key
   float* mass;         // [batch, heads, width·page] or null
   uint64_t timeout_ns;
 };
-// Floats of one partial result: O [16][width], then m, r, l [16] each.
-template <int WIDTH>
-constexpr int kCachePartFloats = kCacheRows * WIDTH + 3 * kCacheRows;
+// Floats of one partial result of `rows` query rows: O [rows][width], then m, r, l [rows] each.
+template <int WIDTH, int TILES>
+constexpr int kCachePartFloats = kCacheTileRows * TILES * (WIDTH + 3);
 // Width of the kernel that runs a head dimension: 64, 128 or 256.
 inline int cache_kernel_width(int64_t D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 // Warps of one CTA of that kernel.
 inline int cache_kernel_warps(int width) { return width <= 128 ? 8 : 4; }
 
-cudaError_t cache_fwd_launch(const CacheFwdParams& p, int width, bool warp_workers, bool f16,
-                             int ctas, cudaStream_t stream);
+// tiles: 8-row tiles of one pass, 1 or 2.
+cudaError_t cache_fwd_launch(const CacheFwdParams& p, int width, int tiles, bool warp_workers, int ctas,
+                             cudaStream_t stream);
 
 }  // namespace ea

@@ -101,6 +101,13 @@ ea::SeqView seqs_of(const attn_cache_seqs_t* s, int64_t T, int* status) {
   return v;
 }
 
+// 8-row tiles of one pass over a head's keys, and the passes `rows` query rows need.
+int tiles_of(int64_t rows) { return rows <= ea::kCacheTileRows ? 1 : 2; }
+int64_t passes_of(int64_t rows) {
+  const int64_t per = ea::kCacheTileRows * tiles_of(rows);
+  return (rows + per - 1) / per;
+}
+
 // Sizes of the queries; touches no CUDA API.
 attn_status_t check_queries(const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t q_heads,
                             int64_t T) {
@@ -108,14 +115,13 @@ attn_status_t check_queries(const attn_cache_t* c, const attn_cache_seqs_t* s, i
       q_heads % c->heads != 0)
     return ATTN_ERR_INVALID_ARG;
   // query rows and the chunks of the longest call are counted in 32 bits
-  const int64_t G = q_heads / c->heads, tiles = (G * T + ea::kCacheRows - 1) / ea::kCacheRows;
   const int64_t chunks = (s->width * c->page + ea::kCacheChunk - 1) / ea::kCacheChunk;
-  const int64_t segments = s->batch * c->heads * tiles;  // < 2^48
+  const int64_t segments = s->batch * c->heads * passes_of(q_heads / c->heads * T);  // < 2^52
   if (s->batch * q_heads > INT32_MAX / T || segments > (1ll << 30) / chunks) return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
 }
 
-// Floats of the score workspace's rows: whole chunks.
+// Keys of a head in the score workspace: whole chunks.
 int64_t score_cols(const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t listed, bool has_list) {
   const int64_t pages = has_list && listed < s->width ? listed : s->width;
   return (pages * c->page + ea::kCacheChunk - 1) / ea::kCacheChunk * ea::kCacheChunk;
@@ -126,15 +132,17 @@ int64_t score_cols(const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t li
 // warps' results are joined in shared memory, an eighth of the parts go
 // through the workspace.
 struct Plan {
-  int width, ctas, workers;
+  int width, tiles, passes, ctas, workers;
   bool warp_workers;
 };
 Plan plan_of(const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t q_heads, int64_t T, int sms) {
   Plan p;
   p.width = ea::cache_kernel_width(c->head_dim);
   const int warps = ea::cache_kernel_warps(p.width);
-  const int64_t tiles = (q_heads / c->heads * T + ea::kCacheRows - 1) / ea::kCacheRows;
-  p.warp_workers = s->batch * c->heads * tiles >= static_cast<int64_t>(sms) * warps / 2;
+  const int64_t rows = q_heads / c->heads * T;
+  p.tiles = tiles_of(rows);
+  p.passes = static_cast<int>(passes_of(rows));
+  p.warp_workers = s->batch * c->heads * p.passes >= static_cast<int64_t>(sms) * warps / 2;
   p.ctas = sms;
   p.workers = p.warp_workers ? sms * warps : sms;
   return p;
@@ -142,11 +150,14 @@ Plan plan_of(const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t q_heads,
 
 // Two parts for each worker: the segment it begins in and the one it ends in.
 size_t part_bytes(const Plan& p) {
-  const size_t floats = p.width == 64    ? ea::kCachePartFloats<64>
-                        : p.width == 128 ? ea::kCachePartFloats<128>
-                                         : ea::kCachePartFloats<256>;
+  const size_t floats = p.tiles * (p.width == 64    ? ea::kCachePartFloats<64, 1>
+                                   : p.width == 128 ? ea::kCachePartFloats<128, 1>
+                                                    : ea::kCachePartFloats<256, 1>);
   return 2 * static_cast<size_t>(p.workers) * floats * 4;  // a multiple of 16
 }
+
+// Rows of the score workspace: whole tiles.
+size_t score_rows(const Plan& p) { return static_cast<size_t>(p.passes) * p.tiles * ea::kCacheTileRows; }
 
 bool sm_count(int* sms) {
   int dev = -1;
@@ -217,9 +228,11 @@ size_t attn_cache_fwd_workspace(const attn_cache_t* cache, const attn_cache_seqs
   if (check_cache(cache, seqs) != ATTN_OK || listed < 0 ||
       check_queries(cache, seqs, q_heads, T) != ATTN_OK || !sm_count(&sms))
     return 0;
-  size_t bytes = part_bytes(plan_of(cache, seqs, q_heads, T, sms));
+  const Plan plan = plan_of(cache, seqs, q_heads, T, sms);
+  size_t bytes = part_bytes(plan);
   if (with_mass)
-    bytes += static_cast<size_t>(seqs->batch * q_heads * T) * score_cols(cache, seqs, listed, listed > 0) * 4;
+    bytes += static_cast<size_t>(seqs->batch * cache->heads) * score_rows(plan) *
+             score_cols(cache, seqs, listed, listed > 0) * 4;
   return bytes;
 }
 
@@ -274,7 +287,9 @@ attn_status_t attn_cache_fwd(const attn_cache_t* cache, const attn_cache_seqs_t*
   p.list = pages;
   p.listed = static_cast<int>(listed);
   p.G = static_cast<int>(q_heads / cache->heads);
-  p.row_tiles = static_cast<int>((p.G * T + ea::kCacheRows - 1) / ea::kCacheRows);
+  p.f16 = dtype == ATTN_F16;
+  p.row_tiles = plan.passes;
+  p.score_rows = static_cast<int>(score_rows(plan));
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.workers = plan.workers;
   p.min_chunks = plan.warp_workers ? 1 : 4;
@@ -283,7 +298,7 @@ attn_status_t attn_cache_fwd(const attn_cache_t* cache, const attn_cache_seqs_t*
   p.score_cols = static_cast<int>(score_cols(cache, seqs, listed, pages != nullptr));
   p.scores = mass ? reinterpret_cast<float*>(static_cast<char*>(workspace) + part_bytes(plan)) : nullptr;
   p.timeout_ns = wait_timeout_ns;
-  return launched(ea::cache_fwd_launch(p, plan.width, plan.warp_workers, dtype == ATTN_F16, plan.ctas, stream));
+  return launched(ea::cache_fwd_launch(p, plan.width, plan.tiles, plan.warp_workers, plan.ctas, stream));
 }
 
 attn_status_t attn_cache_select(const attn_cache_t* cache, const attn_cache_seqs_t* seqs,

@@ -14,14 +14,18 @@
 // shared memory (128-byte swizzle; columns past D read as zero) while it works
 // on the current one, so no warp waits for another.
 //
-// Arithmetic of a chunk, 16 query rows (one mma tile): codes become fp16
-// exactly; q is brought to fp16 by a power of two per row chosen from its
-// largest element, which keeps bf16's 8 bits over 2^28 of range; S = Q·Kᵀ and
-// O += P·V are mma.m16n8k16 with fp32 sums.  A 16-channel unit of a key row is
-// one 16-byte load per lane: a lane's four consecutive channels of each k-step
-// are the same channels that its Q fragment holds, so no data moves between
-// lanes.  V, stored like K, comes transposed out of ldmatrix.  A 128-row
-// tcgen05 tile would hold 16 rows of queries at best, an eighth of its work.
+// Arithmetic of a chunk, 8 query rows a tile: codes become fp16 exactly; q is
+// brought to fp16 by a power of two per row chosen from its largest element,
+// which keeps bf16's 8 bits over 2^28 of range; Sᵀ = K·Qᵀ and Oᵀ += Vᵀ·Pᵀ are
+// mma.m16n8k16 with fp32 sums, the cache as the 16-row operand: with at most 8
+// rows of queries (a group of heads) no row of a tile is idle, and a code is
+// converted once for up to 16 rows.  (Queries as the 16-row operand ran 1676
+// instructions a chunk instead of about half, 321 us instead of 2xx us.)  A
+// 16-channel unit of a key row is one 16-byte load per lane: a lane's four
+// consecutive channels of each k-step are the channels that its Q fragment
+// holds, so no data moves between lanes.  V, stored like K, comes transposed
+// out of ldmatrix; P crosses the lanes by movmatrix.  A tcgen05 tile has 128
+// rows for these 8, and the tensor pipe is not what bounds the kernel.
 //
 // Page scales of V enter P: O is kept relative to r, the running maximum of
 // t + log2(v_scale), and P = 2^(t + log2 v_scale - r + 14) fits fp16 however the
@@ -41,16 +45,17 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2f = 0.6931471805599453f;
-constexpr int kRows = kCacheRows;
 constexpr int kPShift = 14;  // P is 2^14 times the weight relative to r
 constexpr int kFar = 0x3fffffff;  // position of a token that is not there
 constexpr uint64_t kDrainNs = 1000000000ull;
 
 enum : int { kSiteCacheK = 0x7500, kSiteCacheV = 0x7600 };
 
-// WIDTH: 64, 128 or 256 channels; WORKER: warps of one worker (all of the CTA's, or 1)
-template <int WIDTH, int WORKER>
+// WIDTH: 64, 128 or 256 channels; WORKER: warps of one worker (all of the
+// CTA's, or 1); NT: 8-row tiles of queries in one pass
+template <int WIDTH, int WORKER, int NT>
 struct CacheFwdLayout {
+  static constexpr int kRows = 8 * NT;
   static constexpr int kWarps = WIDTH <= 128 ? 8 : 4;
   static constexpr int kRowBytes = WIDTH >= 128 ? 128 : 64;  // one swizzled row
   static constexpr int kBlocks = WIDTH / kRowBytes;          // column blocks of a chunk
@@ -61,7 +66,7 @@ struct CacheFwdLayout {
   static constexpr int kQPitch = 2 * WIDTH;                  // bytes of a Q row
   // chunks whose page data is held: those whose K has been asked for and the current one
   static constexpr int kMeta = kSlots / 2 + 1;
-  static constexpr int kJoinCols = 32;                       // columns joined at a time
+  static constexpr int kJoinCols = 64 / NT;                  // columns joined at a time
   static constexpr int kRingOff = 0;
   static constexpr int kQOff = kWarps * kSlots * kSlot;
   static constexpr int kQsOff = kQOff + kWorkers * kRows * kQPitch;  // row factors
@@ -83,6 +88,14 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// An 8 x 8 matrix of 16-bit values over the warp (lane: row lane/4, columns
+// 2·(lane%4), +1), transposed.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 
 // Two 16 x 16 byte matrices, transposed: a lane gets, of matrix i, column
@@ -112,13 +125,35 @@ __device__ __forceinline__ void tma_load_3d_plain(uint32_t dst, const CUtensorMa
       : "memory");
 }
 
-__device__ __forceinline__ float quad_max(float x) {
-  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+// wait_bounded behind a poll that does not suspend the thread, so that a bound
+// of 0 ends the first wait whose copy has not landed yet.
+__device__ __forceinline__ bool wait_copy(uint32_t bar, uint32_t parity, const WaitCtl& ctl, int site) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  if (ok) return true;
+  if (ctl.timeout_ns == 0) {
+    raise_abort(ctl, site);
+    return false;
+  }
+  return wait_bounded(bar, parity, ctl, site);
 }
-__device__ __forceinline__ float quad_sum(float x) {
-  x += __shfl_xor_sync(0xffffffffu, x, 1);
-  return x + __shfl_xor_sync(0xffffffffu, x, 2);
+
+// Over the eight lanes that hold the same query rows.
+__device__ __forceinline__ float keys_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float keys_sum(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 4);
+  x += __shfl_xor_sync(0xffffffffu, x, 8);
+  return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 
 // Chunks of each of sequence b's segments (0: nothing to do).
@@ -199,23 +234,32 @@ __device__ __forceinline__ bool next_segment(const CacheFwdParams& p, Segment& s
   return true;
 }
 
+// Whether entry i >= 0 of a page list may follow the one before it: a list that
+// does not ascend, or goes on behind a negative entry, breaks this somewhere.
+__device__ __forceinline__ bool follows(const int* list, int i) {
+  return i == 0 || (list[i - 1] >= 0 && list[i] > list[i - 1]);
+}
+
 // Row `row` (query head in the group · T + token) of a segment: its place in
 // q, out (rows of D) and lse.
 __device__ __forceinline__ int64_t row_place(const CacheFwdParams& p, int b, int h, int row) {
   return (static_cast<int64_t>(b) * p.c.heads + h) * (p.G * p.s.T) + row;
 }
 
-template <bool F16>
-__device__ __forceinline__ void store_pair(uint16_t* at, float x, float y) {
-  *reinterpret_cast<uint32_t*>(at) = pack_x2<F16>(x, y);
+__device__ __forceinline__ uint32_t pack_16bit(bool f16, float x, float y) {
+  return f16 ? pack_f16x2(x, y) : pack_bf16x2(x, y);
+}
+__device__ __forceinline__ float2 unpack_16bit(bool f16, uint32_t w) {
+  return f16 ? pair_to_float2<true>(w) : pair_to_float2<false>(w);
 }
 
-template <int WIDTH, int WORKER, bool F16>
-__global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER>::kWarps * 32, 1)
+template <int WIDTH, int WORKER, int NT>
+__global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32, 1)
     cache_fwd_kernel(const __grid_constant__ CacheFwdParams p) {
-  using L = CacheFwdLayout<WIDTH, WORKER>;
-  constexpr int kKSteps = WIDTH / 64;  // 64-channel blocks of Q·Kᵀ
-  constexpr int kTiles = WIDTH / 8;    // 8-channel tiles of O
+  using L = CacheFwdLayout<WIDTH, WORKER, NT>;
+  constexpr int kRows = L::kRows;
+  constexpr int kKSteps = WIDTH / 64;  // 64-channel blocks of K·Qᵀ
+  constexpr int kTiles = WIDTH / 16;   // 16-channel tiles of Oᵀ
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sb = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -272,9 +316,8 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER>::kWarps * 32, 1)
       if (in) {
         const int* l = p.list + (static_cast<int64_t>(fs.b) * p.c.heads + f_h) * p.listed;
         const int e = l[i];
-        const int prev = i > 0 ? l[i - 1] : -1;
         in = e >= 0;
-        if (in && (e >= p.s.width || e <= prev)) {
+        if (in && (e >= p.s.width || !follows(l, i))) {
           dbg_fail(p.s.status, kChkCacheList);
           in = false;
         }
@@ -344,7 +387,7 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER>::kWarps * 32, 1)
   for (int s = 0; s < L::kSlots; ++s) issue();
 
   // ---------------- the worker's segments
-  const int row0 = 4 * (gid >> 1) + (gid & 1);  // key row of this lane in a pair of K tiles
+  const int row0 = 4 * (gid >> 1) + (gid & 1);  // this lane's key of a 16-key tile; the other is row0 + 2
   Segment cs = find_segment(p, begin);
   int at = begin + wi, u_slot = 0, u_parity = 0, u_meta = 0;
   bool alive = true;
@@ -366,7 +409,7 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER>::kWarps * 32, 1)
         const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 x = pair_to_float2<F16>(ws[e]);
+          const float2 x = unpack_16bit(p.f16, ws[e]);
           a = fmaxf(a, fmaxf(finite_abs(x.x), finite_abs(x.y)));
         }
       }
@@ -382,7 +425,7 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER>::kWarps * 32, 1)
         uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float2 x = pair_to_float2<F16>(ws[k]);
+          const float2 x = unpack_16bit(p.f16, ws[k]);
           ws[k] = pack_f16x2(x.x * up, x.y * up);
         }
         // odd rows swap the halves of each 32 bytes: a fragment load of two
@@ -394,52 +437,75 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER>::kWarps * 32, 1)
       if constexpr (WORKER > 1) __syncthreads();
       else __syncwarp();
     }
-    const float q0 = ld_shared_f32(qf + 4 * gid), q1 = ld_shared_f32(qf + 4 * (gid + 8));
-    // last position a row may attend to; rows that are not there see every key
+    // this lane's rows: 8·b + 2·t4 + i
+    float qk[NT][2];
+    int last[NT][2];  // last position a row may attend to; rows that are not there see every key
     auto last_of = [&](int r) {
       const int i = (tile_row + r) % p.s.T;
       return r < tile_rows && i < cs.n ? cs.len - cs.n + i : cs.len - 1;
     };
-    const int last0 = last_of(gid), last1 = last_of(gid + 8);
+#pragma unroll
+    for (int b = 0; b < NT; ++b)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        qk[b][i] = ld_shared_f32(qf + 4 * (8 * b + 2 * t4 + i));
+        last[b][i] = last_of(8 * b + 2 * t4 + i);
+      }
     const int first_last = cs.len - cs.n;  // every row sees the keys up to here
 
-    float o[kTiles][4];
+    float o[kTiles][NT][4];  // channel 16·u + gid (+ 8), row i of tile b: [u][b][i (+ 2)]
 #pragma unroll
-    for (int j = 0; j < kTiles; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, r0 = -INFINITY, r1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    for (int u = 0; u < kTiles; ++u)
+#pragma unroll
+      for (int b = 0; b < NT; ++b) o[u][b][0] = o[u][b][1] = o[u][b][2] = o[u][b][3] = 0.f;
+    float m[NT][2], r[NT][2], l[NT][2];
+#pragma unroll
+    for (int b = 0; b < NT; ++b)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) m[b][i] = r[b][i] = -INFINITY, l[b][i] = 0.f;
 
 #pragma unroll 1
     for (; at < seg_end; at += WORKER) {
-      // ---- S = Q·Kᵀ
-      if (alive) alive = __all_sync(0xffffffffu, wait_bounded(bars + 8 * u_slot, u_parity, ctl, kSiteCacheK));
+      // ---- Sᵀ = K·Qᵀ
+      if (alive) alive = __all_sync(0xffffffffu, wait_copy(bars + 8 * u_slot, u_parity, ctl, kSiteCacheK));
       if (!alive) continue;
       const uint32_t kslot = ring + u_slot * L::kSlot;
-      float s[8][4];
+      constexpr int kUnits = L::kRowBytes / 16;
+      float s[4][NT][4];  // key row0 (+ 2) of 16-key tile g, row i of tile b: [g][b][i (+ 2)]
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int b = 0; b < NT; ++b) s[g][b][0] = s[g][b][1] = s[g][b][2] = s[g][b][3] = 0.f;
 #pragma unroll
       for (int kb = 0; kb < kKSteps; ++kb) {
-        const uint32_t qa = qs + gid * L::kQPitch + kb * 128 + 32 * t4 + ((gid & 1) << 4);
-        const uint32_t qb = qa ^ 16u;  // rows gid and gid + 8 are odd together
-        const uint4 x0 = ld_shared_v4(qa), x1 = ld_shared_v4(qb);
-        const uint4 y0 = ld_shared_v4(qa + 8 * L::kQPitch), y1 = ld_shared_v4(qb + 8 * L::kQPitch);
-        const uint32_t xa[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-        const uint32_t ya[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+        uint32_t qw[NT][8];
+#pragma unroll
+        for (int b = 0; b < NT; ++b) {
+          const uint32_t qa = qs + (8 * b + gid) * L::kQPitch + kb * 128 + 32 * t4 + ((gid & 1) << 4);
+          const uint4 x0 = ld_shared_v4(qa), x1 = ld_shared_v4(qa ^ 16u);
+          qw[b][0] = x0.x, qw[b][1] = x0.y, qw[b][2] = x0.z, qw[b][3] = x0.w;
+          qw[b][4] = x1.x, qw[b][5] = x1.y, qw[b][6] = x1.z, qw[b][7] = x1.w;
+        }
         const int unit = kb * 4 + t4;  // 16 channels
-        constexpr int kUnits = L::kRowBytes / 16;
         const uint32_t block = kslot + (unit / kUnits) * L::kBlockBytes;
         const int cu = unit % kUnits;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int row = row0 + 16 * (j >> 1) + 2 * (j & 1);
-          const int sw = kUnits == 8 ? (row & 7) : ((row >> 1) & 3);
-          const uint4 kw = ld_shared_v4(block + row * L::kRowBytes + ((cu ^ sw) << 4));
-          const uint32_t kc[4] = {kw.x, kw.y, kw.z, kw.w};
+        for (int g = 0; g < 4; ++g) {
+          uint4 kw[2];
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const int row = row0 + 16 * g + 2 * hf;
+            const int sw = kUnits == 8 ? (row & 7) : ((row >> 1) & 3);
+            kw[hf] = ld_shared_v4(block + row * L::kRowBytes + ((cu ^ sw) << 4));
+          }
+          const uint32_t x[4] = {kw[0].x, kw[0].y, kw[0].z, kw[0].w}, y[4] = {kw[1].x, kw[1].y, kw[1].z, kw[1].w};
 #pragma unroll
           for (int st = 0; st < 4; ++st) {
-            uint32_t b0, b1;
-            e4m3x4_to_f16(kc[st], &b0, &b1);
-            mma_f16(s[j], xa[2 * st], ya[2 * st], xa[2 * st + 1], ya[2 * st + 1], b0, b1);
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16(x[st], &a0, &a2);
+            e4m3x4_to_f16(y[st], &a1, &a3);
+#pragma unroll
+            for (int b = 0; b < NT; ++b) mma_f16(s[g][b], a0, a1, a2, a3, qw[b][2 * st], qw[b][2 * st + 1]);
           }
         }
       }
@@ -448,8 +514,7 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER>::kWarps * 32, 1)
       __syncwarp();
       issue();
 
-      // ---- softmax of the chunk.  Lane's keys: 16·g + 4·t4 + 2·j + e (tile 2·g + j)
-      float mx0 = -INFINITY, mx1 = -INFINITY, rx0 = -INFINITY, rx1 = -INFINITY;
+      // ---- softmax of the chunk
       float ev[4], vm[4];
       int gpos[4];
       bool tail = false;  // some key is hidden from some row
@@ -460,101 +525,138 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER>::kWarps * 32, 1)
         ev[g] = __uint_as_float(md.z);
         vm[g] = __uint_as_float(md.w);
         tail = tail || gpos[g] + 15 > first_last;
-        const float f0 = q0 * __uint_as_float(md.y), f1 = q1 * __uint_as_float(md.y);
 #pragma unroll
-        for (int j = 2 * g; j < 2 * g + 2; ++j) {
-          s[j][0] *= f0, s[j][1] *= f0;
-          s[j][2] *= f1, s[j][3] *= f1;
+        for (int b = 0; b < NT; ++b) {
+          const float f0 = qk[b][0] * __uint_as_float(md.y), f1 = qk[b][1] * __uint_as_float(md.y);
+          s[g][b][0] *= f0, s[g][b][2] *= f0;
+          s[g][b][1] *= f1, s[g][b][3] *= f1;
         }
       }
       if (tail) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int pos = gpos[j >> 1] + 4 * t4 + 2 * (j & 1);
-          if (pos > last0) s[j][0] = -INFINITY;
-          if (pos + 1 > last0) s[j][1] = -INFINITY;
-          if (pos > last1) s[j][2] = -INFINITY;
-          if (pos + 1 > last1) s[j][3] = -INFINITY;
-        }
-      }
+        for (int g = 0; g < 4; ++g)
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const float a0 = fmaxf(fmaxf(s[2 * g][0], s[2 * g][1]), fmaxf(s[2 * g + 1][0], s[2 * g + 1][1]));
-        const float a1 = fmaxf(fmaxf(s[2 * g][2], s[2 * g][3]), fmaxf(s[2 * g + 1][2], s[2 * g + 1][3]));
-        mx0 = fmaxf(mx0, a0), mx1 = fmaxf(mx1, a1);
-        rx0 = fmaxf(rx0, a0 + ev[g]), rx1 = fmaxf(rx1, a1 + ev[g]);
+          for (int b = 0; b < NT; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (gpos[g] + row0 + (e & 2) > last[b][e & 1]) s[g][b][e] = -INFINITY;
       }
       if (p.scores != nullptr) {
-        const int64_t srow = row_place(p, cs.b, h, tile_row + gid) * p.score_cols +
-                             (at - cs.first) * kCacheChunk + 4 * t4;
+        // [key][row]: the 8 rows of a key side by side
+        const int64_t row_len = static_cast<int64_t>(p.row_tiles) * kRows;
+        float* sc = p.scores + ((static_cast<int64_t>(cs.b) * p.c.heads + h) * p.score_cols +
+                                static_cast<int64_t>(at - cs.first) * kCacheChunk + row0) * row_len + tile_row + 2 * t4;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          if (gid < tile_rows)
-            *reinterpret_cast<float4*>(p.scores + srow + 16 * g) =
-                make_float4(s[2 * g][0], s[2 * g][1], s[2 * g + 1][0], s[2 * g + 1][1]);
-          if (gid + 8 < tile_rows)
-            *reinterpret_cast<float4*>(p.scores + srow + 8ll * p.score_cols + 16 * g) =
-                make_float4(s[2 * g][2], s[2 * g][3], s[2 * g + 1][2], s[2 * g + 1][3]);
-        }
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int b = 0; b < NT; ++b)
+              *reinterpret_cast<float2*>(sc + (16 * g + 2 * hf) * row_len + 8 * b) =
+                  make_float2(s[g][b][2 * hf], s[g][b][2 * hf + 1]);
       }
-      const float mn0 = fmaxf(m0, quad_max(mx0)), mn1 = fmaxf(m1, quad_max(mx1));
-      const float rn0 = fmaxf(r0, quad_max(rx0)), rn1 = fmaxf(r1, quad_max(rx1));
-      // references: 0 where no key has been allowed yet
-      const float mr0 = mn0 == -INFINITY ? 0.f : mn0, mr1 = mn1 == -INFINITY ? 0.f : mn1;
-      const float rr0 = rn0 == -INFINITY ? 0.f : rn0, rr1 = rn1 == -INFINITY ? 0.f : rn1;
-      l0 *= ex2_approx(m0 - mr0), l1 *= ex2_approx(m1 - mr1);
-      const float b0 = ex2_approx(r0 - rr0), b1 = ex2_approx(r1 - rr1);
-      m0 = mn0, m1 = mn1;
-      if (__any_sync(0xffffffffu, rn0 != r0 || rn1 != r1)) {
+      float mr[NT][2], rr[NT][2], beta[NT][2];  // references: 0 where no key has been allowed yet
+      bool moved = false;
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j) o[j][0] *= b0, o[j][1] *= b0, o[j][2] *= b1, o[j][3] *= b1;
-      }
-      r0 = rn0, r1 = rn1;
-      uint32_t pa[4][4];  // P, A fragments of the four 16-key steps
+      for (int b = 0; b < NT; ++b)
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        // a group whose weights are far below the chunk's has a factor beyond
-        // range; its P is held finite
-        const float f0 = ex2_approx(fminf(ev[g] + (mr0 - rr0) + kPShift, 126.f)) * vm[g];
-        const float f1 = ex2_approx(fminf(ev[g] + (mr1 - rr1) + kPShift, 126.f)) * vm[g];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float* x = s[2 * g + j];
-          const float p0 = ex2_approx(x[0] - mr0), p1 = ex2_approx(x[1] - mr0);
-          const float p2 = ex2_approx(x[2] - mr1), p3 = ex2_approx(x[3] - mr1);
-          l0 += p0 + p1, l1 += p2 + p3;
-          pa[g][2 * j] = pack_f16x2(p0 * f0, p1 * f0);
-          pa[g][2 * j + 1] = pack_f16x2(p2 * f1, p3 * f1);
-        }
-      }
-
-      // ---- O += P·V
-      if (alive) alive = __all_sync(0xffffffffu, wait_bounded(bars + 8 * u_slot, u_parity, ctl, kSiteCacheV));
-      if (!alive) continue;
-      const uint32_t vslot = ring + u_slot * L::kSlot;
-      uint32_t vmask[4];  // bytes of this lane's four tokens of each step that exist
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int n = min(4, max(0, cs.len - (gpos[g] + 4 * t4)));
-        vmask[g] = n == 4 ? 0xffffffffu : (1u << (8 * n)) - 1u;
-      }
-      constexpr int kUnits = L::kRowBytes / 16;
-      const int vrow = lane & 15;
-      uint32_t nan_seen = 0;
-#pragma unroll
-      for (int u = 0; u < WIDTH / 16; u += 2) {
-        if (16 * u < p.c.D) {
-          const int unit = u + (lane >> 4);
-          const uint32_t block = vslot + (u / kUnits) * L::kBlockBytes;
+        for (int i = 0; i < 2; ++i) {
+          float mx = -INFINITY, rx = -INFINITY;
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const int row = 16 * g + vrow;
-            const int sw = kUnits == 8 ? (row & 7) : ((row >> 1) & 3);
-            uint32_t w[4];
-            ldmatrix_b8_trans_x2(block + row * L::kRowBytes + (((unit % kUnits) ^ sw) << 4), w);
-            if (tail) {
-              // slots that hold no token of the sequence count as zero; so do
-              // NaN codes here, which rows that may not see them must not meet
+            const float a = fmaxf(s[g][b][i], s[g][b][i + 2]);
+            mx = fmaxf(mx, a), rx = fmaxf(rx, a + ev[g]);
+          }
+          const float mn = fmaxf(m[b][i], keys_max(mx)), rn = fmaxf(r[b][i], keys_max(rx));
+          mr[b][i] = mn == -INFINITY ? 0.f : mn;
+          rr[b][i] = rn == -INFINITY ? 0.f : rn;
+          l[b][i] *= ex2_approx(m[b][i] - mr[b][i]);
+          beta[b][i] = ex2_approx(r[b][i] - rr[b][i]);
+          moved = moved || rn != r[b][i];
+          m[b][i] = mn, r[b][i] = rn;
+        }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int u = 0; u < kTiles; ++u)
+#pragma unroll
+          for (int b = 0; b < NT; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[u][b][e] *= beta[b][e & 1];
+      }
+      uint32_t pb[4][NT][2];  // P, B fragments of the four 16-key steps
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int b = 0; b < NT; ++b) {
+          float pw[4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            // a page whose weights are far below the chunk's has a factor
+            // beyond range; its P is held finite
+            const float f = ex2_approx(fminf(ev[g] + (mr[b][i] - rr[b][i]) + kPShift, 126.f)) * vm[g];
+            const float p0 = ex2_approx(s[g][b][i] - mr[b][i]), p1 = ex2_approx(s[g][b][i + 2] - mr[b][i]);
+            l[b][i] += p0 + p1;
+            pw[i] = p0 * f, pw[i + 2] = p1 * f;
+          }
+          pb[g][b][0] = movmatrix_trans(pack_f16x2(pw[0], pw[1]));
+          pb[g][b][1] = movmatrix_trans(pack_f16x2(pw[2], pw[3]));
+        }
+
+      // ---- Oᵀ += Vᵀ·Pᵀ
+      if (alive) alive = __all_sync(0xffffffffu, wait_copy(bars + 8 * u_slot, u_parity, ctl, kSiteCacheV));
+      if (!alive) continue;
+      const uint32_t vslot = ring + u_slot * L::kSlot;
+      const int vrow = lane & 15;
+      // four 16-bit-packed words of units u, u + 1 for the keys of step g
+      auto load_v = [&](int u, int g, uint32_t (&w)[4]) {
+        const int row = 16 * g + vrow, unit = (u + (lane >> 4)) % kUnits;
+        const int sw = kUnits == 8 ? (row & 7) : ((row >> 1) & 3);
+        ldmatrix_b8_trans_x2(vslot + (u / kUnits) * L::kBlockBytes + row * L::kRowBytes + ((unit ^ sw) << 4), w);
+      };
+      if (!tail) {
+#pragma unroll
+        for (int u = 0; u < kTiles; u += 2) {
+          if (16 * u < p.c.D) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              uint32_t w[4];
+              load_v(u, g, w);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                uint32_t a0, a1, a2, a3;
+                e4m3x4_to_f16(w[2 * i], &a0, &a2);
+                e4m3x4_to_f16(w[2 * i + 1], &a1, &a3);
+#pragma unroll
+                for (int b = 0; b < NT; ++b) mma_f16(o[u + i][b], a0, a1, a2, a3, pb[g][b][0], pb[g][b][1]);
+              }
+            }
+          }
+        }
+      } else {
+        // Slots that hold no token of the sequence count as zero, and so do NaN
+        // codes, which rows that may not see them must not meet; the rows that
+        // may, get them by a count of the NaN codes they see per channel.
+        auto one = [](bool x, bool y) { return (x ? 0x3c00u : 0u) | (y ? 0x3c000000u : 0u); };
+        uint32_t vmask[4], see[4][NT][2];  // bytes of this lane's four tokens of each step that exist
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int pos = gpos[g] + 4 * t4, n = min(4, max(0, cs.len - pos));
+          vmask[g] = n == 4 ? 0xffffffffu : (1u << (8 * n)) - 1u;
+#pragma unroll
+          for (int b = 0; b < NT; ++b) {
+            const int z = last_of(8 * b + gid);
+            see[g][b][0] = one(pos <= z, pos + 1 <= z);
+            see[g][b][1] = one(pos + 2 <= z, pos + 3 <= z);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kTiles; u += 2) {
+          if (16 * u < p.c.D) {
+            uint32_t nan_seen = 0;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              uint32_t w[4];
+              load_v(u, g, w);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 w[i] &= vmask[g];
@@ -562,53 +664,41 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER>::kWarps * 32, 1)
                 nan_seen |= nan;
                 w[i] &= ~nan;
               }
-            }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t b0, b1;
-              e4m3x4_to_f16(w[i], &b0, &b1);
-              mma_f16(o[2 * u + i], pa[g][0], pa[g][1], pa[g][2], pa[g][3], b0, b1);
-            }
-          }
-        }
-      }
-      if (tail && __any_sync(0xffffffffu, nan_seen != 0)) {
-        // rows that may see a NaN code get it: a count of the NaN codes each
-        // row sees per channel
-        uint32_t see[4][4];
-        auto one = [](bool a, bool b) { return (a ? 0x3c00u : 0u) | (b ? 0x3c000000u : 0u); };
+              for (int i = 0; i < 2; ++i) {
+                uint32_t a0, a1, a2, a3;
+                e4m3x4_to_f16(w[2 * i], &a0, &a2);
+                e4m3x4_to_f16(w[2 * i + 1], &a1, &a3);
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int pos = gpos[g] + 4 * t4 + 2 * j;
-            see[g][2 * j] = one(pos <= last0, pos + 1 <= last0);
-            see[g][2 * j + 1] = one(pos <= last1, pos + 1 <= last1);
-          }
-#pragma unroll
-        for (int u = 0; u < WIDTH / 16; u += 2) {
-          if (16 * u < p.c.D) {
-            const int unit = u + (lane >> 4);
-            const uint32_t block = vslot + (u / kUnits) * L::kBlockBytes;
-            float c[4][4] = {};
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const int row = 16 * g + vrow;
-              const int sw = kUnits == 8 ? (row & 7) : ((row >> 1) & 3);
-              uint32_t w[4];
-              ldmatrix_b8_trans_x2(block + row * L::kRowBytes + (((unit % kUnits) ^ sw) << 4), w);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t nan = __vcmpeq4(w[i] & vmask[g] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                mma_f16(c[i], see[g][0], see[g][1], see[g][2], see[g][3],
-                        one(nan & 1u, nan & 0x100u), one(nan & 0x10000u, nan & 0x1000000u));
+                for (int b = 0; b < NT; ++b) mma_f16(o[u + i][b], a0, a1, a2, a3, pb[g][b][0], pb[g][b][1]);
               }
             }
+            if (__any_sync(0xffffffffu, nan_seen != 0)) {
+              float c[2][NT][4] = {};
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+              for (int g = 0; g < 4; ++g) {
+                uint32_t w[4], a[4][2];
+                load_v(u, g, w);
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (c[i][e] > 0.f) o[2 * u + i][e] = __int_as_float(0x7fffffff);
+                for (int i = 0; i < 4; ++i) {
+                  const uint32_t nan = __vcmpeq4(w[i] & vmask[g] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                  a[i][0] = one(nan & 1u, nan & 0x100u);
+                  a[i][1] = one(nan & 0x10000u, nan & 0x1000000u);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                  for (int b = 0; b < NT; ++b)
+                    mma_f16(c[i][b], a[2 * i][0], a[2 * i + 1][0], a[2 * i][1], a[2 * i + 1][1], see[g][b][0], see[g][b][1]);
+              }
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int b = 0; b < NT; ++b)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    if (c[i][b][e] > 0.f) o[u + i][b][e] = __int_as_float(0x7fffffff);
+            }
           }
         }
       }
@@ -618,121 +708,135 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER>::kWarps * 32, 1)
       __syncwarp();
       issue();
     }
-    l0 = quad_sum(l0), l1 = quad_sum(l1);
+#pragma unroll
+    for (int b = 0; b < NT; ++b)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) l[b][i] = keys_sum(l[b][i]);
 
     // ---- the segment's result, or this worker's part of it
     const bool whole = seg_at == cs.first && seg_end == cs.first + cs.nc;
-    float* part = p.part + (2ll * worker + (seg_at == cs.first ? 1 : 0)) * kCachePartFloats<WIDTH>;
-    auto live = [&](int r) { return r < tile_rows && (tile_row + r) % p.s.T < cs.n; };
+    float* part = p.part + (2ll * worker + (seg_at == cs.first ? 1 : 0)) * kCachePartFloats<WIDTH, NT>;
+    float* part_stat = part + kRows * WIDTH;
+    auto live = [&](int row) { return row < tile_rows && (tile_row + row) % p.s.T < cs.n; };
     // 2^(r - 14 - m) / l: what an entry of O is multiplied by
-    auto factor = [](float m, float r, float l) {
-      return m == -INFINITY ? 0.f : ex2_approx(r - m - kPShift) / l;
+    auto factor = [](float mm, float rr, float ll) {
+      return mm == -INFINITY ? 0.f : ex2_approx(rr - mm - kPShift) / ll;
     };
     if constexpr (WORKER == 1) {
-      if (whole) {
-        const float w0 = factor(m0, r0, l0), w1 = factor(m1, r1, l1);
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int r = gid + 8 * hh;
-          if (live(r)) {
-            const int64_t at_row = row_place(p, cs.b, h, tile_row + r);
-            const float w = hh ? w1 : w0, mm = hh ? m1 : m0, ll = hh ? l1 : l0;
+      for (int b = 0; b < NT; ++b)
 #pragma unroll
-            for (int j = 0; j < kTiles; ++j)
-              if (8 * j < p.c.D) {
-                const float x = mm == -INFINITY ? 0.f : o[j][2 * hh] * w;
-                const float y = mm == -INFINITY ? 0.f : o[j][2 * hh + 1] * w;
-                store_pair<F16>(p.out + at_row * p.c.D + 8 * j + 2 * t4, x, y);
+        for (int i = 0; i < 2; ++i) {
+          const int row = 8 * b + 2 * t4 + i;
+          if (whole) {
+            if (!live(row)) continue;
+            const int64_t to = row_place(p, cs.b, h, tile_row + row);
+            const float w = factor(m[b][i], r[b][i], l[b][i]);
+#pragma unroll
+            for (int u = 0; u < kTiles; ++u)
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                const int ch = 16 * u + gid + 8 * hf;
+                const float x = m[b][i] == -INFINITY ? 0.f : o[u][b][i + 2 * hf] * w;
+                if (ch < p.c.D) p.out[to * p.c.D + ch] = static_cast<uint16_t>(pack_16bit(p.f16, x, 0.f));
               }
-            if (t4 == 0) p.lse[at_row] = (mm + log2f(ll)) * kLn2f;
+            if (gid == 0) p.lse[to] = (m[b][i] + log2f(l[b][i])) * kLn2f;
+          } else {
+#pragma unroll
+            for (int u = 0; u < kTiles; ++u)
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) part[row * WIDTH + 16 * u + gid + 8 * hf] = o[u][b][i + 2 * hf];
+            if (gid == 0) {
+              part_stat[row] = m[b][i];
+              part_stat[kRows + row] = r[b][i];
+              part_stat[2 * kRows + row] = l[b][i];
+            }
           }
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < kTiles; ++j) {
-          *reinterpret_cast<float2*>(part + gid * WIDTH + 8 * j + 2 * t4) = make_float2(o[j][0], o[j][1]);
-          *reinterpret_cast<float2*>(part + (gid + 8) * WIDTH + 8 * j + 2 * t4) = make_float2(o[j][2], o[j][3]);
-        }
-        if (t4 == 0) {
-          float* st = part + kRows * WIDTH;
-          st[gid] = m0, st[gid + 8] = m1;
-          st[16 + gid] = r0, st[16 + gid + 8] = r1;
-          st[32 + gid] = l0, st[32 + gid + 8] = l1;
-        }
-      }
       __syncwarp();  // Q is rewritten for the next segment
     } else {
-      // the warps' parts joined, 32 columns at a time, in the order of the warps
+      // the warps' parts joined, kJoinCols columns at a time, in the order of the warps
       const uint32_t stat = sb + L::kStatOff, join = sb + L::kJoinOff;
-      if (t4 == 0) {
-        st_shared_f32(stat + (warp * kRows + gid) * 12, m0);
-        st_shared_f32(stat + (warp * kRows + gid) * 12 + 4, r0);
-        st_shared_f32(stat + (warp * kRows + gid) * 12 + 8, l0);
-        st_shared_f32(stat + (warp * kRows + gid + 8) * 12, m1);
-        st_shared_f32(stat + (warp * kRows + gid + 8) * 12 + 4, r1);
-        st_shared_f32(stat + (warp * kRows + gid + 8) * 12 + 8, l1);
+      if (gid == 0) {
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t to = stat + (warp * kRows + 8 * b + 2 * t4 + i) * 12;
+            st_shared_f32(to, m[b][i]);
+            st_shared_f32(to + 4, r[b][i]);
+            st_shared_f32(to + 8, l[b][i]);
+          }
       }
       __syncthreads();
-      auto joined = [&](int r, float* m, float* rr, float* l) {
+      auto joined = [&](int row, float* mm, float* rr, float* ll) {
         float M = -INFINITY, R = -INFINITY, S = 0.f;
         for (int w = 0; w < L::kWarps; ++w) {
-          M = fmaxf(M, ld_shared_f32(stat + (w * kRows + r) * 12));
-          R = fmaxf(R, ld_shared_f32(stat + (w * kRows + r) * 12 + 4));
+          M = fmaxf(M, ld_shared_f32(stat + (w * kRows + row) * 12));
+          R = fmaxf(R, ld_shared_f32(stat + (w * kRows + row) * 12 + 4));
         }
         for (int w = 0; w < L::kWarps; ++w) {
-          const float mw = ld_shared_f32(stat + (w * kRows + r) * 12);
-          S += mw == -INFINITY ? 0.f : ld_shared_f32(stat + (w * kRows + r) * 12 + 8) * ex2_approx(mw - M);
+          const float mw = ld_shared_f32(stat + (w * kRows + row) * 12);
+          S += mw == -INFINITY ? 0.f : ld_shared_f32(stat + (w * kRows + row) * 12 + 8) * ex2_approx(mw - M);
         }
-        *m = M, *rr = R, *l = S;
+        *mm = M, *rr = R, *ll = S;
       };
-      float M0, R0, S0, M1, R1, S1;
-      joined(gid, &M0, &R0, &S0);
-      joined(gid + 8, &M1, &R1, &S1);
-      const float b0 = r0 == -INFINITY ? 0.f : ex2_approx(r0 - R0);
-      const float b1 = r1 == -INFINITY ? 0.f : ex2_approx(r1 - R1);
-      // the row and column pair this thread sums
-      constexpr int kThreads = L::kWarps * 32, kPairs = kRows * L::kJoinCols / 2;
+      float beta[NT][2];
+#pragma unroll
+      for (int b = 0; b < NT; ++b)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float M, R, S;
+          joined(8 * b + 2 * t4 + i, &M, &R, &S);
+          beta[b][i] = r[b][i] == -INFINITY ? 0.f : ex2_approx(r[b][i] - R);
+        }
+      // two neighbouring columns of a row per thread
+      constexpr int kThreads = L::kWarps * 32, kPairs = kRows * L::kJoinCols / 2, kUPer = L::kJoinCols / 16;
 #pragma unroll
       for (int c = 0; c < WIDTH / L::kJoinCols; ++c) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t a = join + ((warp * kRows + gid) * L::kJoinPitch + 8 * j + 2 * t4) * 4;
-          const float* x = o[4 * c + j];
-          st_shared_f32(a, x[0] * b0), st_shared_f32(a + 4, x[1] * b0);
-          st_shared_f32(a + 8 * L::kJoinPitch * 4, x[2] * b1), st_shared_f32(a + 8 * L::kJoinPitch * 4 + 4, x[3] * b1);
-        }
+        for (int u = 0; u < kUPer; ++u)
+#pragma unroll
+          for (int b = 0; b < NT; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              st_shared_f32(join + ((warp * kRows + 8 * b + 2 * t4 + (e & 1)) * L::kJoinPitch + 16 * u + gid + 4 * (e & 2)) * 4,
+                            o[c * kUPer + u][b][e] * beta[b][e & 1]);
         __syncthreads();
         for (int i = threadIdx.x; i < kPairs; i += kThreads) {
-          const int r = i / (L::kJoinCols / 2), col = 2 * (i % (L::kJoinCols / 2));
+          const int row = i / (L::kJoinCols / 2), col = 2 * (i % (L::kJoinCols / 2));
           float x = 0.f, y = 0.f;
           for (int w = 0; w < L::kWarps; ++w) {
-            const uint32_t a = join + ((w * kRows + r) * L::kJoinPitch + col) * 4;
-            x += ld_shared_f32(a), y += ld_shared_f32(a + 4);
+            const uint32_t from = join + ((w * kRows + row) * L::kJoinPitch + col) * 4;
+            x += ld_shared_f32(from), y += ld_shared_f32(from + 4);
           }
           const int ch = L::kJoinCols * c + col;
           if (!whole) {
-            *reinterpret_cast<float2*>(part + r * WIDTH + ch) = make_float2(x, y);
-          } else if (ch < p.c.D && live(r)) {
+            *reinterpret_cast<float2*>(part + row * WIDTH + ch) = make_float2(x, y);
+          } else if (ch < p.c.D && live(row)) {
             float M, R, S;
-            joined(r, &M, &R, &S);
+            joined(row, &M, &R, &S);
             const float w = factor(M, R, S);
-            store_pair<F16>(p.out + row_place(p, cs.b, h, tile_row + r) * p.c.D + ch,
-                            M == -INFINITY ? 0.f : x * w, M == -INFINITY ? 0.f : y * w);
+            const bool none = M == -INFINITY;
+            *reinterpret_cast<uint32_t*>(p.out + row_place(p, cs.b, h, tile_row + row) * p.c.D + ch) =
+                pack_16bit(p.f16, none ? 0.f : x * w, none ? 0.f : y * w);
           }
         }
         __syncthreads();
       }
-      if (warp == 0 && t4 == 0) {
-        if (whole) {
-          if (live(gid)) p.lse[row_place(p, cs.b, h, tile_row + gid)] = (M0 + log2f(S0)) * kLn2f;
-          if (live(gid + 8)) p.lse[row_place(p, cs.b, h, tile_row + gid + 8)] = (M1 + log2f(S1)) * kLn2f;
-        } else {
-          float* st = part + kRows * WIDTH;
-          st[gid] = M0, st[gid + 8] = M1;
-          st[16 + gid] = R0, st[16 + gid + 8] = R1;
-          st[32 + gid] = S0, st[32 + gid + 8] = S1;
+      if (threadIdx.x < kRows) {
+        const int row = threadIdx.x;
+        float M, R, S;
+        joined(row, &M, &R, &S);
+        if (!whole) {
+          part_stat[row] = M;
+          part_stat[kRows + row] = R;
+          part_stat[2 * kRows + row] = S;
+        } else if (live(row)) {
+          p.lse[row_place(p, cs.b, h, tile_row + row)] = (M + log2f(S)) * kLn2f;
         }
       }
+      __syncthreads();  // the statistics are rewritten for the next segment
     }
     seg_at = seg_end;
   }
@@ -746,12 +850,13 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER>::kWarps * 32, 1)
     }
 }
 
-// Joins the parts of a segment that several workers shared.  CTA (segment of
-// the widest line, 32-column block): 128 threads, 4 columns each of 16 rows.
-constexpr int kJoinThreads = 128;
+// Joins the parts of a segment that several workers shared.  CTA: a segment of
+// the line and 32 columns; a thread takes 4 columns of a row.
+constexpr int kJoinThreads = 64;
 
-template <int WIDTH, bool F16>
-__global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ CacheFwdParams p) {
+template <int WIDTH, int NT>
+__global__ void __launch_bounds__(kJoinThreads * NT) cache_join_kernel(const __grid_constant__ CacheFwdParams p) {
+  constexpr int kRows = 8 * NT;
   const int hr = p.c.heads * p.row_tiles;
   const int b = blockIdx.x / hr, x = blockIdx.x % hr;
   const Deal deal = deal_chunks(p, false);
@@ -771,7 +876,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   const int h = x / p.row_tiles, tile_row = (x % p.row_tiles) * kRows;
   const int r = threadIdx.x / 8, col = blockIdx.y * 32 + 4 * (threadIdx.x % 8);
   if (tile_row + r >= p.G * p.s.T || (tile_row + r) % p.s.T >= n) return;
-  auto part = [&](int w) { return p.part + (2ll * w + (w == w0 ? 1 : 0)) * kCachePartFloats<WIDTH>; };
+  auto part = [&](int w) { return p.part + (2ll * w + (w == w0 ? 1 : 0)) * kCachePartFloats<WIDTH, NT>; };
   float M = -INFINITY;
   for (int w = w0; w <= w1; ++w) M = fmaxf(M, part(w)[kRows * WIDTH + r]);
   float S = 0.f;
@@ -781,18 +886,17 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
       const float* q = part(w);
       const float m = q[kRows * WIDTH + r];
       if (m == -INFINITY) continue;
-      S += q[kRows * WIDTH + 32 + r] * ex2_approx(m - M);
-      const float f = ex2_approx(q[kRows * WIDTH + 16 + r] - M - kPShift);
+      S += q[kRows * WIDTH + 2 * kRows + r] * ex2_approx(m - M);
+      const float f = ex2_approx(q[kRows * WIDTH + kRows + r] - M - kPShift);
       const float4 v = *reinterpret_cast<const float4*>(q + r * WIDTH + col);
       acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
     }
     acc.x /= S, acc.y /= S, acc.z /= S, acc.w /= S;
   }
   const int64_t row = row_place(p, b, h, tile_row + r);
-  if (col < p.c.D) {
-    store_pair<F16>(p.out + row * p.c.D + col, acc.x, acc.y);
-    store_pair<F16>(p.out + row * p.c.D + col + 2, acc.z, acc.w);
-  }
+  if (col < p.c.D)
+    *reinterpret_cast<uint2*>(p.out + row * p.c.D + col) =
+        make_uint2(pack_16bit(p.f16, acc.x, acc.y), pack_16bit(p.f16, acc.z, acc.w));
   if (col == 0) p.lse[row] = (M + log2f(S)) * kLn2f;
 }
 
@@ -810,57 +914,57 @@ __global__ void __launch_bounds__(kMassThreads) cache_mass_kernel(const __grid_c
   if (p.list != nullptr) {
     const int e = key >> p.c.log2_page;
     if (e >= p.listed) return;
-    const int i = p.list[bh * p.listed + e];
-    const int prev = e > 0 ? p.list[bh * p.listed + e - 1] : -1;
-    if (i < 0 || i >= p.s.width || i <= prev) return;
+    const int* l = p.list + bh * p.listed;
+    const int i = l[e];
+    if (i < 0 || i >= p.s.width || !follows(l, e)) return;
     pos = (i << p.c.log2_page) + (key & (p.c.page - 1));
   }
   if (pos >= len) return;
   const int rows = p.G * p.s.T;
-  const float* s = p.scores + bh * rows * static_cast<int64_t>(p.score_cols) + key;
+  const float* s = p.scores + (bh * p.score_cols + key) * p.score_rows;
   float sum = 0.f;
   for (int r = 0; r < rows; ++r) {
     if (r % p.s.T >= n) continue;
     const float z = p.lse[bh * rows + r];
     if (z == -INFINITY) continue;
-    sum += ex2_approx(s[static_cast<int64_t>(r) * p.score_cols] - z * kLog2e);
+    sum += ex2_approx(s[r] - z * kLog2e);
   }
   p.mass[bh * (static_cast<int64_t>(p.s.width) << p.c.log2_page) + pos] += sum;
 }
 
-template <int WIDTH, int WORKER, bool F16>
+template <int WIDTH, int WORKER, int NT>
 cudaError_t launch_fwd(const CacheFwdParams& p, int ctas, cudaStream_t stream) {
-  using L = CacheFwdLayout<WIDTH, WORKER>;
-  auto kern = cache_fwd_kernel<WIDTH, WORKER, F16>;
+  using L = CacheFwdLayout<WIDTH, WORKER, NT>;
+  auto kern = cache_fwd_kernel<WIDTH, WORKER, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
   if (e != cudaSuccess) return e;
   kern<<<ctas, L::kWarps * 32, L::kAlloc, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cache_join_kernel<WIDTH, F16><<<dim3(p.s.batch * p.c.heads * p.row_tiles, WIDTH / 32), kJoinThreads, 0, stream>>>(p);
+  cache_join_kernel<WIDTH, NT>
+      <<<dim3(p.s.batch * p.c.heads * p.row_tiles, WIDTH / 32), kJoinThreads * NT, 0, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.mass == nullptr) return e;
   cache_mass_kernel<<<dim3((p.score_cols + kMassThreads - 1) / kMassThreads, p.c.heads, p.s.batch), kMassThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
-template <int WIDTH, bool F16>
-cudaError_t launch_fwd_w(const CacheFwdParams& p, bool warp_workers, int ctas, cudaStream_t stream) {
-  return warp_workers ? launch_fwd<WIDTH, 1, F16>(p, ctas, stream)
-                      : launch_fwd<WIDTH, CacheFwdLayout<WIDTH, 1>::kWarps, F16>(p, ctas, stream);
+template <int WIDTH>
+cudaError_t launch_width(const CacheFwdParams& p, bool warp_workers, int tiles, int ctas, cudaStream_t stream) {
+  constexpr int kWarps = CacheFwdLayout<WIDTH, 1, 1>::kWarps;
+  if (tiles == 1)
+    return warp_workers ? launch_fwd<WIDTH, 1, 1>(p, ctas, stream) : launch_fwd<WIDTH, kWarps, 1>(p, ctas, stream);
+  return warp_workers ? launch_fwd<WIDTH, 1, 2>(p, ctas, stream) : launch_fwd<WIDTH, kWarps, 2>(p, ctas, stream);
 }
 
 }  // namespace
 
-cudaError_t cache_fwd_launch(const CacheFwdParams& p, int width, bool warp_workers, bool f16,
-                             int ctas, cudaStream_t stream) {
+cudaError_t cache_fwd_launch(const CacheFwdParams& p, int width, int tiles, bool warp_workers, int ctas,
+                             cudaStream_t stream) {
   switch (width) {
-    case 64: return f16 ? launch_fwd_w<64, true>(p, warp_workers, ctas, stream)
-                        : launch_fwd_w<64, false>(p, warp_workers, ctas, stream);
-    case 128: return f16 ? launch_fwd_w<128, true>(p, warp_workers, ctas, stream)
-                         : launch_fwd_w<128, false>(p, warp_workers, ctas, stream);
-    case 256: return f16 ? launch_fwd_w<256, true>(p, warp_workers, ctas, stream)
-                         : launch_fwd_w<256, false>(p, warp_workers, ctas, stream);
+    case 64: return launch_width<64>(p, warp_workers, tiles, ctas, stream);
+    case 128: return launch_width<128>(p, warp_workers, tiles, ctas, stream);
+    case 256: return launch_width<256>(p, warp_workers, tiles, ctas, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -118,9 +118,11 @@ ATTN_API size_t attn_cache_fwd_workspace(const attn_cache_t* cache, const attn_c
  *   q        device, 16-bit [batch, q_heads, T, head_dim] contiguous, 16-byte aligned
  *   pages    device int32 [batch, heads, listed], or NULL: every page.  Each
  *            head reads only the pages listed for it: page indices of the
- *            sequence (columns of `table`), ascending; a negative entry names
- *            none.  An entry not above the one before it, or not below width,
- *            is left out and reported.
+ *            sequence (columns of `table`), strictly ascending, negative
+ *            entries behind the last.  Pages behind the sequence's end hold no
+ *            token.  An entry not below width is left out and reported; so is
+ *            one not above the entry before it or behind a negative one, and
+ *            which of that list's further entries count is not specified.
  *   listed   entries per head (0 with pages = NULL)
  *   out      device, 16-bit [batch, q_heads, T, head_dim], 16-byte aligned
  *   lse      device fp32 [batch, q_heads, T]
