@@ -111,7 +111,8 @@ def cache_alloc(pages: int, heads: int, head_dim: int, page: int = 64, device="c
 
 
 def _want(name, t, dtype, shape, device):
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+    """The address of a tensor that has to be just so."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
         raise TypeError(f"{name} must be a {dtype} tensor")
     if t.shape != shape or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} on {device}")
@@ -123,20 +124,22 @@ def _views(cache, table, lens, fresh):
     k, v, k_scale, v_scale, k_bounds, head_dim = cache
     if not isinstance(k, torch.Tensor) or not k.is_cuda:
         raise TypeError("the cache must be CUDA tensors")
-    if k.dim() != 4:
+    shape = k.shape
+    if len(shape) != 4:
         raise ValueError("cache.k must be [pages, heads, page, pitch]")
-    dev, (pages, heads, page, pitch) = k.device, k.shape
+    dev, (pages, heads, page, pitch) = k.device, shape
     if pitch != (head_dim + 15) // 16 * 16:
         raise ValueError("the cache's rows must be head_dim rounded up to a multiple of 16")
-    c = _Cache(_want("cache.k", k, torch.uint8, k.shape, dev), _want("cache.v", v, torch.uint8, k.shape, dev),
-               _want("cache.k_scale", k_scale, torch.float32, (pages, heads), dev),
-               _want("cache.v_scale", v_scale, torch.float32, (pages, heads), dev),
+    per_head = (pages, heads)
+    c = _Cache(_want("cache.k", k, torch.uint8, shape, dev), _want("cache.v", v, torch.uint8, shape, dev),
+               _want("cache.k_scale", k_scale, torch.float32, per_head, dev),
+               _want("cache.v_scale", v_scale, torch.float32, per_head, dev),
                _want("cache.k_bounds", k_bounds, torch.int8, (pages, heads, 2, pitch), dev),
                pages, heads, head_dim, page)
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("table must be an int32 [batch, width] tensor")
-    batch, width = table.shape
-    s = _Seqs(_want("table", table, torch.int32, table.shape, dev), _want("lens", lens, torch.int32, (batch,), dev),
+    batch, width = shape = table.shape
+    s = _Seqs(_want("table", table, torch.int32, shape, dev), _want("lens", lens, torch.int32, (batch,), dev),
               None if fresh is None else _want("fresh", fresh, torch.int32, (batch,), dev), batch, width)
     return c, s, dev
 
@@ -153,20 +156,30 @@ def _rows(name, t, batch, head_dim, dev):
 
 def _call(name, dev, stream, *args):
     """The entry point on `stream` (default: the current one) of `dev`."""
-    st = torch.cuda.current_stream(dev) if stream is None else stream
-    fn = getattr(_library(), name)
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, st.cuda_stream)
+    index = dev.index
+    st = _current_raw_stream(index) if stream is None else stream.cuda_stream
+    fn = getattr(_lib or _library(), name)
+    if index == torch.cuda.current_device():
+        rc = fn(*args, st)
     else:
-        with torch.cuda.device(dev):
-            rc = fn(*args, st.cuda_stream)
+        with torch.cuda.device(index):
+            rc = fn(*args, st)
     if rc != ATTN_OK:
         raise AttnError(rc, name)
 
 
+def _current_raw_stream(index):
+    """torch.cuda.current_stream(index).cuda_stream without the objects between."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def _size(name, dev, *args):
-    with torch.cuda.device(dev):
-        n = getattr(_library(), name)(*args)
+    fn = getattr(_lib or _library(), name)
+    if dev.index == torch.cuda.current_device():
+        n = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            n = fn(*args)
     if n == 0:
         raise AttnError(ATTN_ERR_INVALID_ARG, name)
     return n

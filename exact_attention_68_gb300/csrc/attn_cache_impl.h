@@ -68,8 +68,13 @@ cudaError_t cache_select_launch(const CacheSelectParams& p, bool f16, cudaStream
 
 // Tokens of one chunk, the unit of work of the attention: one warp's step.
 constexpr int kCacheChunk = 64;
-// Query rows of a tile; a pass over a (sequence, head)'s keys takes one or two.
+// Query rows of a tile; a pass over a (sequence, head)'s keys takes up to four
+// (two above 128 channels, where their sums fill the registers).
 constexpr int kCacheTileRows = 8;
+// Tiles up to which a warp may be a worker of its own: each worker's Q takes
+// shared memory from the rings.
+constexpr int kCacheWarpWorkerTiles = 2;
+inline int cache_max_tiles(int width) { return width <= 128 ? 4 : 2; }
 
 struct CacheFwdParams {
   CUtensorMap tm_k, tm_v;  // (channel, slot, page·head), box: a swizzled row x one page
@@ -83,6 +88,7 @@ struct CacheFwdParams {
   bool f16;            // q and out are fp16 (else bf16)
   int G, row_tiles;    // query heads per key head; passes over a head's keys
   float scale_log2;
+  int by_segment;      // a CTA for each segment: nothing to join
   int workers;         // parts the chunks of all (sequence, head, row tile) are dealt to
   int min_chunks;      // fewest chunks worth a worker of their own
   float* part;         // workspace: partial results, two slots per worker
@@ -100,8 +106,8 @@ inline int cache_kernel_width(int64_t D) { return D <= 64 ? 64 : D <= 128 ? 128 
 // Warps of one CTA of that kernel.
 inline int cache_kernel_warps(int width) { return width <= 128 ? 8 : 4; }
 
-// tiles: 8-row tiles of one pass, 1 or 2.
-cudaError_t cache_fwd_launch(const CacheFwdParams& p, int width, int tiles, bool warp_workers, int ctas,
+// tiles: 8-row tiles of one pass.
+cudaError_t cache_fwd_launch(const CacheFwdParams& p, int width, int tiles, bool warp_workers, int dev, int ctas,
                              cudaStream_t stream);
 
 }  // namespace ea

@@ -1,5 +1,6 @@
 // cache_api.cu — the C ABI declared in include/attn_cache.h: argument checks,
 // tensor maps, workspaces, launch.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -101,11 +102,15 @@ ea::SeqView seqs_of(const attn_cache_seqs_t* s, int64_t T, int* status) {
   return v;
 }
 
-// 8-row tiles of one pass over a head's keys, and the passes `rows` query rows need.
-int tiles_of(int64_t rows) { return rows <= ea::kCacheTileRows ? 1 : 2; }
-int64_t passes_of(int64_t rows) {
-  const int64_t per = ea::kCacheTileRows * tiles_of(rows);
+// The passes over a head's keys that `rows` query rows need, and the 8-row
+// tiles of one: as few passes as registers allow, as few tiles as those need.
+int64_t passes_of(int64_t rows, int width) {
+  const int64_t per = ea::kCacheTileRows * ea::cache_max_tiles(width);
   return (rows + per - 1) / per;
+}
+int tiles_of(int64_t rows, int width) {
+  const int64_t per = passes_of(rows, width) * ea::kCacheTileRows;
+  return static_cast<int>((rows + per - 1) / per);
 }
 
 // Sizes of the queries; touches no CUDA API.
@@ -116,7 +121,7 @@ attn_status_t check_queries(const attn_cache_t* c, const attn_cache_seqs_t* s, i
     return ATTN_ERR_INVALID_ARG;
   // query rows and the chunks of the longest call are counted in 32 bits
   const int64_t chunks = (s->width * c->page + ea::kCacheChunk - 1) / ea::kCacheChunk;
-  const int64_t segments = s->batch * c->heads * passes_of(q_heads / c->heads * T);  // < 2^52
+  const int64_t segments = s->batch * c->heads * passes_of(q_heads / c->heads * T, ea::cache_kernel_width(c->head_dim));  // < 2^52
   if (s->batch * q_heads > INT32_MAX / T || segments > (1ll << 30) / chunks) return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
 }
@@ -133,18 +138,25 @@ int64_t score_cols(const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t li
 // through the workspace.
 struct Plan {
   int width, tiles, passes, ctas, workers;
-  bool warp_workers;
+  bool by_segment, warp_workers;
 };
-Plan plan_of(const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t q_heads, int64_t T, int sms) {
+// Steps of a warp up to which a segment is left to one CTA.
+constexpr int64_t kSegmentSteps = 4;
+Plan plan_of(const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t listed, int64_t q_heads, int64_t T,
+             int sms) {
   Plan p;
   p.width = ea::cache_kernel_width(c->head_dim);
   const int warps = ea::cache_kernel_warps(p.width);
   const int64_t rows = q_heads / c->heads * T;
-  p.tiles = tiles_of(rows);
-  p.passes = static_cast<int>(passes_of(rows));
-  p.warp_workers = s->batch * c->heads * p.passes >= static_cast<int64_t>(sms) * warps / 2;
-  p.ctas = sms;
-  p.workers = p.warp_workers ? sms * warps : sms;
+  p.tiles = tiles_of(rows, p.width);
+  p.passes = static_cast<int>(passes_of(rows, p.width));
+  const int64_t segments = s->batch * c->heads * p.passes;
+  const int64_t chunks = score_cols(c, s, listed, listed > 0) / ea::kCacheChunk;  // at most, of a segment
+  p.by_segment = segments <= sms && chunks <= kSegmentSteps * warps;
+  p.warp_workers = !p.by_segment && p.tiles <= ea::kCacheWarpWorkerTiles &&
+                   segments >= static_cast<int64_t>(sms) * warps / 2;
+  p.ctas = p.by_segment ? static_cast<int>(segments) : sms;
+  p.workers = p.by_segment ? 0 : p.warp_workers ? sms * warps : sms;
   return p;
 }
 
@@ -159,10 +171,22 @@ size_t part_bytes(const Plan& p) {
 // Rows of the score workspace: whole tiles.
 size_t score_rows(const Plan& p) { return static_cast<size_t>(p.passes) * p.tiles * ea::kCacheTileRows; }
 
-bool sm_count(int* sms) {
-  int dev = -1;
-  return ea::current_device_bound(&dev) == cudaSuccess &&
-         cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+// The current device and its number of SMs (asked for once per device).
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_sms[kMaxDevices];
+bool sm_count(int* dev, int* sms) {
+  if (cudaGetDevice(dev) != cudaSuccess || *dev < 0 || *dev >= kMaxDevices) return false;
+  *sms = g_sms[*dev].load(std::memory_order_relaxed);
+  if (*sms > 0) return true;
+  if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess || *sms < 1) return false;
+  g_sms[*dev].store(*sms, std::memory_order_relaxed);
+  return true;
+}
+
+// The attention's workspace (never 0): parts, then scores.
+size_t fwd_bytes(const Plan& plan, const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t listed, bool with_mass) {
+  const size_t keys = static_cast<size_t>(s->batch * c->heads) * score_cols(c, s, listed, listed > 0);
+  return 16 + part_bytes(plan) + (with_mass ? keys * score_rows(plan) * 4 : 0);
 }
 
 // (channel, slot, page·head) map of a pool's codes; the box is one swizzled
@@ -224,16 +248,11 @@ attn_status_t attn_cache_append(const attn_cache_t* cache, const attn_cache_seqs
 
 size_t attn_cache_fwd_workspace(const attn_cache_t* cache, const attn_cache_seqs_t* seqs,
                                 int64_t listed, int64_t q_heads, int64_t T, int with_mass) {
-  int sms = 0;
+  int dev = -1, sms = 0;
   if (check_cache(cache, seqs) != ATTN_OK || listed < 0 ||
-      check_queries(cache, seqs, q_heads, T) != ATTN_OK || !sm_count(&sms))
+      check_queries(cache, seqs, q_heads, T) != ATTN_OK || !sm_count(&dev, &sms))
     return 0;
-  const Plan plan = plan_of(cache, seqs, q_heads, T, sms);
-  size_t bytes = part_bytes(plan);
-  if (with_mass)
-    bytes += static_cast<size_t>(seqs->batch * cache->heads) * score_rows(plan) *
-             score_cols(cache, seqs, listed, listed > 0) * 4;
-  return bytes;
+  return fwd_bytes(plan_of(cache, seqs, listed, q_heads, T, sms), cache, seqs, listed, with_mass != 0);
 }
 
 attn_status_t attn_cache_fwd(const attn_cache_t* cache, const attn_cache_seqs_t* seqs, const void* q,
@@ -257,8 +276,10 @@ attn_status_t attn_cache_fwd(const attn_cache_t* cache, const attn_cache_seqs_t*
   int* status = nullptr;
   s = ea::current_status_words(&status);
   if (s != ATTN_OK) return s;
-  const size_t need = attn_cache_fwd_workspace(cache, seqs, listed, q_heads, T, mass != nullptr);
-  if (need == 0) return ATTN_ERR_CUDA;
+  int dev = -1, sms = 0;
+  if (!sm_count(&dev, &sms)) return ATTN_ERR_CUDA;
+  const Plan plan = plan_of(cache, seqs, listed, q_heads, T, sms);
+  const size_t need = fwd_bytes(plan, cache, seqs, listed, mass != nullptr);
   if (workspace_bytes < need) return ATTN_ERR_INVALID_ARG;
   Span spans[14];
   int n = cache_spans(cache, seqs, false, spans);
@@ -272,9 +293,6 @@ attn_status_t attn_cache_fwd(const attn_cache_t* cache, const attn_cache_seqs_t*
   spans[n++] = {workspace, need, true};
   if (any_overlap(spans, n)) return ATTN_ERR_INVALID_ARG;
 
-  int sms = 0;
-  if (!sm_count(&sms)) return ATTN_ERR_CUDA;
-  const Plan plan = plan_of(cache, seqs, q_heads, T, sms);
   ea::CacheFwdParams p;
   std::memset(&p, 0, sizeof(p));
   p.c = view_of(cache);
@@ -291,6 +309,7 @@ attn_status_t attn_cache_fwd(const attn_cache_t* cache, const attn_cache_seqs_t*
   p.row_tiles = plan.passes;
   p.score_rows = static_cast<int>(score_rows(plan));
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.by_segment = plan.by_segment ? 1 : 0;
   p.workers = plan.workers;
   p.min_chunks = plan.warp_workers ? 1 : 4;
   p.part = static_cast<float*>(workspace);
@@ -298,7 +317,7 @@ attn_status_t attn_cache_fwd(const attn_cache_t* cache, const attn_cache_seqs_t*
   p.score_cols = static_cast<int>(score_cols(cache, seqs, listed, pages != nullptr));
   p.scores = mass ? reinterpret_cast<float*>(static_cast<char*>(workspace) + part_bytes(plan)) : nullptr;
   p.timeout_ns = wait_timeout_ns;
-  return launched(ea::cache_fwd_launch(p, plan.width, plan.tiles, plan.warp_workers, plan.ctas, stream));
+  return launched(ea::cache_fwd_launch(p, plan.width, plan.tiles, plan.warp_workers, dev, plan.ctas, stream));
 }
 
 attn_status_t attn_cache_select(const attn_cache_t* cache, const attn_cache_seqs_t* seqs,

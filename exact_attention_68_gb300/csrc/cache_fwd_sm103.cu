@@ -35,6 +35,9 @@
 // A worker that covers a segment (one sequence, head and row tile) writes the
 // result; others write O, m, r, l to the workspace and a second kernel joins
 // them in a fixed order.
+#include <atomic>
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -66,7 +69,7 @@ struct CacheFwdLayout {
   static constexpr int kQPitch = 2 * WIDTH;                  // bytes of a Q row
   // chunks whose page data is held: those whose K has been asked for and the current one
   static constexpr int kMeta = kSlots / 2 + 1;
-  static constexpr int kJoinCols = 64 / NT;                  // columns joined at a time
+  static constexpr int kJoinCols = NT == 1 ? 64 : NT == 2 ? 32 : 16;  // columns joined at a time
   static constexpr int kRingOff = 0;
   static constexpr int kQOff = kWarps * kSlots * kSlot;
   static constexpr int kQsOff = kQOff + kWorkers * kRows * kQPitch;  // row factors
@@ -142,6 +145,15 @@ __device__ __forceinline__ bool wait_copy(uint32_t bar, uint32_t parity, const W
     return false;
   }
   return wait_bounded(bar, parity, ctl, site);
+}
+
+// Programmatic dependent launch: the next kernel of the stream may be set up
+// once every CTA has said so or ended; its wait ends when this grid has.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Over the eight lanes that hold the same query rows.
@@ -280,17 +292,30 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
   const WaitCtl ctl{abort_addr, p.s.status, p.timeout_ns};
 
   const int worker = blockIdx.x * L::kWorkers + worker_in_cta;
-  const Deal deal = deal_chunks(p, blockIdx.x == 0 && warp == 0);
-  // workers are few enough that worker · per stays below 2^31 (total < 2^30)
-  const int begin = min(static_cast<int64_t>(worker) * deal.per, static_cast<int64_t>(deal.total));
-  const int end = min(begin + deal.per, deal.total);
-  if (begin >= end) return;  // the whole worker; with WORKER > 1 the whole CTA
+  int begin, end;  // this worker's chunks of the line
+  Segment cs;
+  if (WORKER > 1 && p.by_segment) {
+    // a CTA for each segment: a line of its own
+    cs.b = blockIdx.x / (p.c.heads * p.row_tiles);
+    cs.hr = blockIdx.x % (p.c.heads * p.row_tiles);
+    cs.nc = seq_chunks(p, cs.b, cs.hr == 0 && warp == 0, &cs.len, &cs.n);
+    cs.first = begin = 0;
+    end = cs.nc;
+    if (begin >= end) return;
+  } else {
+    const Deal deal = deal_chunks(p, blockIdx.x == 0 && warp == 0);
+    // 64 bits: worker · per may pass 2^31 (total is below 2^30)
+    begin = static_cast<int>(min(static_cast<int64_t>(worker) * deal.per, static_cast<int64_t>(deal.total)));
+    end = min(begin + deal.per, deal.total);
+    if (begin >= end) return;  // the whole worker; with WORKER > 1 the whole CTA
+    cs = find_segment(p, begin);
+  }
 
   const int seg_rows = p.G * p.s.T;
   const int log2p = p.c.log2_page, page_mask = p.c.page - 1;
 
   // ---------------- fetching: chunks begin + wi, + WORKER, ... of the line
-  Segment fs = find_segment(p, begin);
+  Segment fs = cs;
   int f_at = begin + wi;      // next chunk to fetch K of
   int f_page = -1, f_pos = kFar;  // this lane's 16-token group (t4) of it
   int f_h = 0;                // its head
@@ -388,7 +413,6 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
 
   // ---------------- the worker's segments
   const int row0 = 4 * (gid >> 1) + (gid & 1);  // this lane's key of a 16-key tile; the other is row0 + 2
-  Segment cs = find_segment(p, begin);
   int at = begin + wi, u_slot = 0, u_parity = 0, u_meta = 0;
   bool alive = true;
   for (int seg_at = begin; seg_at < end;) {
@@ -399,9 +423,12 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
 
     // ---- Q to fp16 with a power of two per row
     {
-      constexpr int kMine = kRows / WORKER, kLanes = 32 / kMine;  // rows of a warp, lanes of a row
+      // rows of a warp (kRows shared out, rounded up to a power of two), lanes of a row
+      constexpr int kShare = (kRows + WORKER - 1) / WORKER;
+      constexpr int kMine = kShare <= 1 ? 1 : kShare <= 2 ? 2 : kShare <= 4 ? 4 : kShare <= 8 ? 8 : kShare <= 16 ? 16 : 32;
+      constexpr int kLanes = 32 / kMine;
       const int r = wi * kMine + lane / kLanes, part = lane % kLanes;
-      const bool in = r < tile_rows;
+      const bool here = r < kRows, in = r < tile_rows;
       const uint16_t* q = p.q + row_place(p, cs.b, h, tile_row + (in ? r : 0)) * p.c.D;
       float a = 0.f;
       for (int c = 8 * part; c < p.c.D; c += 8 * kLanes) {
@@ -422,6 +449,7 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
       for (int c = 8 * part; c < WIDTH; c += 8 * kLanes) {
         uint4 w = make_uint4(0, 0, 0, 0);
         if (in && c < p.c.D) w = __ldg(reinterpret_cast<const uint4*>(q + c));
+        if (!here) continue;
         uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -432,7 +460,7 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
         // rows then meets every bank once
         st_shared_v4(qs + r * L::kQPitch + ((2 * c) ^ ((r & 1) << 4)), ws[0], ws[1], ws[2], ws[3]);
       }
-      if (part == 0)
+      if (part == 0 && here)
         st_shared_f32(qf + 4 * r, p.scale_log2 * __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23));
       if constexpr (WORKER > 1) __syncthreads();
       else __syncwarp();
@@ -708,6 +736,7 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
       __syncwarp();
       issue();
     }
+    if (seg_end == end) launch_dependents();  // the join may be set up meanwhile
 #pragma unroll
     for (int b = 0; b < NT; ++b)
 #pragma unroll
@@ -862,7 +891,6 @@ __global__ void __launch_bounds__(kJoinThreads * NT) cache_join_kernel(const __g
   const Deal deal = deal_chunks(p, false);
   int len, n;
   const int nc = seq_chunks(p, b, false, &len, &n);
-  if (nc == 0) return;
   int before = 0;  // chunks of the sequences before b
   for (int i = threadIdx.x & 31; i < b; i += 32) {
     int l2, n2;
@@ -870,6 +898,11 @@ __global__ void __launch_bounds__(kJoinThreads * NT) cache_join_kernel(const __g
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) before += __shfl_xor_sync(0xffffffffu, before, d);
+  // every CTA waits, also one without work: this grid's end means the parts'
+  // kernel has ended too.  lens, fresh were there before that kernel began.
+  wait_for_previous();
+  launch_dependents();
+  if (nc == 0) return;
   const int first = before + x * nc;
   const int w0 = first / deal.per, w1 = (first + nc - 1) / deal.per;
   if (w0 == w1) return;  // one worker had it all
@@ -908,6 +941,7 @@ __global__ void __launch_bounds__(kMassThreads) cache_mass_kernel(const __grid_c
   int len, n;
   const int nc = seq_chunks(p, b, false, &len, &n);
   const int key = blockIdx.x * kMassThreads + threadIdx.x;
+  wait_for_previous();
   if (key >= nc * kCacheChunk) return;
   const int64_t bh = static_cast<int64_t>(b) * p.c.heads + h;
   int pos = key;
@@ -932,39 +966,72 @@ __global__ void __launch_bounds__(kMassThreads) cache_mass_kernel(const __grid_c
   p.mass[bh * (static_cast<int64_t>(p.s.width) << p.c.log2_page) + pos] += sum;
 }
 
+// A launch that may be set up before the stream's previous kernel has ended.
+template <class Kernel>
+cudaError_t launch_after(Kernel kern, dim3 grid, int threads, const CacheFwdParams& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
 template <int WIDTH, int WORKER, int NT>
-cudaError_t launch_fwd(const CacheFwdParams& p, int ctas, cudaStream_t stream) {
+cudaError_t launch_fwd(const CacheFwdParams& p, int dev, int ctas, cudaStream_t stream) {
   using L = CacheFwdLayout<WIDTH, WORKER, NT>;
   auto kern = cache_fwd_kernel<WIDTH, WORKER, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
-  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> ready{0};  // devices (bits) whose copy of the kernel has its shared memory granted
+  cudaError_t e = cudaSuccess;
+  if (!(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
   kern<<<ctas, L::kWarps * 32, L::kAlloc, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cache_join_kernel<WIDTH, NT>
-      <<<dim3(p.s.batch * p.c.heads * p.row_tiles, WIDTH / 32), kJoinThreads * NT, 0, stream>>>(p);
-  e = cudaGetLastError();
+  if (!p.by_segment)
+    e = launch_after(cache_join_kernel<WIDTH, NT>, dim3(p.s.batch * p.c.heads * p.row_tiles, WIDTH / 32),
+                     kJoinThreads * NT, p, stream);
   if (e != cudaSuccess || p.mass == nullptr) return e;
-  cache_mass_kernel<<<dim3((p.score_cols + kMassThreads - 1) / kMassThreads, p.c.heads, p.s.batch), kMassThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_after(cache_mass_kernel, dim3((p.score_cols + kMassThreads - 1) / kMassThreads, p.c.heads, p.s.batch),
+                      kMassThreads, p, stream);
 }
 
 template <int WIDTH>
-cudaError_t launch_width(const CacheFwdParams& p, bool warp_workers, int tiles, int ctas, cudaStream_t stream) {
+cudaError_t launch_width(const CacheFwdParams& p, bool warp_workers, int tiles, int dev, int ctas,
+                         cudaStream_t stream) {
   constexpr int kWarps = CacheFwdLayout<WIDTH, 1, 1>::kWarps;
-  if (tiles == 1)
-    return warp_workers ? launch_fwd<WIDTH, 1, 1>(p, ctas, stream) : launch_fwd<WIDTH, kWarps, 1>(p, ctas, stream);
-  return warp_workers ? launch_fwd<WIDTH, 1, 2>(p, ctas, stream) : launch_fwd<WIDTH, kWarps, 2>(p, ctas, stream);
+  auto go = [&](auto nt) {
+    constexpr int NT = decltype(nt)::value;
+    if constexpr (NT <= kCacheWarpWorkerTiles)
+      if (warp_workers) return launch_fwd<WIDTH, 1, NT>(p, dev, ctas, stream);
+    return launch_fwd<WIDTH, kWarps, NT>(p, dev, ctas, stream);
+  };
+  switch (tiles) {
+    case 1: return go(std::integral_constant<int, 1>());
+    case 2: return go(std::integral_constant<int, 2>());
+  }
+  if constexpr (WIDTH <= 128) {
+    if (tiles == 3) return go(std::integral_constant<int, 3>());
+    if (tiles == 4) return go(std::integral_constant<int, 4>());
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-cudaError_t cache_fwd_launch(const CacheFwdParams& p, int width, int tiles, bool warp_workers, int ctas,
+cudaError_t cache_fwd_launch(const CacheFwdParams& p, int width, int tiles, bool warp_workers, int dev, int ctas,
                              cudaStream_t stream) {
   switch (width) {
-    case 64: return launch_width<64>(p, warp_workers, tiles, ctas, stream);
-    case 128: return launch_width<128>(p, warp_workers, tiles, ctas, stream);
-    case 256: return launch_width<256>(p, warp_workers, tiles, ctas, stream);
+    case 64: return launch_width<64>(p, warp_workers, tiles, dev, ctas, stream);
+    case 128: return launch_width<128>(p, warp_workers, tiles, dev, ctas, stream);
+    case 256: return launch_width<256>(p, warp_workers, tiles, dev, ctas, stream);
   }
   return cudaErrorInvalidValue;
 }
