@@ -48,20 +48,19 @@ __device__ __forceinline__ float page_scale(float a) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// x / s with one rounding; a product where s is a power of two in range (its
-// reciprocal and the quotient are then exact).
-struct Divider {
-  float s, inv;
-  bool pow2;
-  __device__ __forceinline__ explicit Divider(float scale) : s(scale) {
-    const uint32_t u = __float_as_uint(scale);
-    pow2 = (u & 0x807fffffu) == 0u && (u >> 23) >= 2u && (u >> 23) <= 252u;
-    inv = pow2 ? __uint_as_float((254u - (u >> 23)) << 23) : 0.f;
+// Calls body with a function that divides by s with one rounding: a product
+// where s is a power of two in range (its reciprocal and the quotient are then
+// exact), as every scale written here is; a division for others.
+template <class Body>
+__device__ __forceinline__ void with_divider(float s, Body body) {
+  const uint32_t u = __float_as_uint(s);
+  if ((u & 0x807fffffu) == 0u && (u >> 23) >= 2u && (u >> 23) <= 252u) {
+    const float inv = __uint_as_float((254u - (u >> 23)) << 23);
+    body([inv](float x) { return x * inv; });
+  } else {
+    body([s](float x) { return __fdiv_rn(x, s); });
   }
-  __device__ __forceinline__ float operator()(float x) const {
-    return pow2 ? x * inv : __fdiv_rn(x, s);
-  }
-};
+}
 
 // Two fp32 to e4m3 (nearest even, saturating): lo in the low byte.
 __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {

@@ -933,37 +933,45 @@ __global__ void __launch_bounds__(kJoinThreads * NT) cache_join_kernel(const __g
   if (col == 0) p.lse[row] = (M + log2f(S)) * kLn2f;
 }
 
-// mass[key] += Σ over the head's rows of 2^(t - lse): one thread a key.
-constexpr int kMassThreads = 256;
+// mass[key] += Σ over the head's rows of 2^(t - lse): one thread a key, whose
+// scores lie side by side; the rows' logsumexps wait in shared memory.
+constexpr int kMassThreads = 128, kMassRows = 256;
 
 __global__ void __launch_bounds__(kMassThreads) cache_mass_kernel(const __grid_constant__ CacheFwdParams p) {
+  __shared__ __align__(16) float z[kMassRows];  // log2 units; rows that do not count: +inf
   const int h = blockIdx.y, b = blockIdx.z;
   int len, n;
   const int nc = seq_chunks(p, b, false, &len, &n);
   const int key = blockIdx.x * kMassThreads + threadIdx.x;
-  wait_for_previous();
-  if (key >= nc * kCacheChunk) return;
   const int64_t bh = static_cast<int64_t>(b) * p.c.heads + h;
-  int pos = key;
-  if (p.list != nullptr) {
+  int pos = key < nc * kCacheChunk ? key : kFar;
+  if (p.list != nullptr && pos != kFar) {
     const int e = key >> p.c.log2_page;
-    if (e >= p.listed) return;
     const int* l = p.list + bh * p.listed;
-    const int i = l[e];
-    if (i < 0 || i >= p.s.width || !follows(l, e)) return;
-    pos = (i << p.c.log2_page) + (key & (p.c.page - 1));
+    const int i = e < p.listed ? l[e] : -1;
+    pos = i < 0 || i >= p.s.width || !follows(l, e) ? kFar : (i << p.c.log2_page) + (key & (p.c.page - 1));
   }
-  if (pos >= len) return;
+  const bool mine = pos < len;
+  wait_for_previous();
+  if (blockIdx.x * kMassThreads >= nc * kCacheChunk) return;
   const int rows = p.G * p.s.T;
   const float* s = p.scores + (bh * p.score_cols + key) * p.score_rows;
   float sum = 0.f;
-  for (int r = 0; r < rows; ++r) {
-    if (r % p.s.T >= n) continue;
-    const float z = p.lse[bh * rows + r];
-    if (z == -INFINITY) continue;
-    sum += ex2_approx(s[r] - z * kLog2e);
+  for (int r0 = 0; r0 < rows; r0 += kMassRows) {
+    __syncthreads();
+    for (int r = threadIdx.x; r < kMassRows; r += kMassThreads) {
+      const float w = r0 + r < rows && (r0 + r) % p.s.T < n ? p.lse[bh * rows + r0 + r] : -INFINITY;
+      z[r] = w == -INFINITY ? INFINITY : w * kLog2e;
+    }
+    __syncthreads();
+    if (mine)  // score rows are padded to tiles of 8
+      for (int r = 0; r < min(kMassRows, p.score_rows - r0); r += 4) {
+        const float4 t = __ldg(reinterpret_cast<const float4*>(s + r0 + r));
+        const float4 w = *reinterpret_cast<const float4*>(z + r);
+        sum += (ex2_approx(t.x - w.x) + ex2_approx(t.y - w.y)) + (ex2_approx(t.z - w.z) + ex2_approx(t.w - w.w));
+      }
   }
-  p.mass[bh * (static_cast<int64_t>(p.s.width) << p.c.log2_page) + pos] += sum;
+  if (mine) p.mass[bh * (static_cast<int64_t>(p.s.width) << p.c.log2_page) + pos] += sum;
 }
 
 // A launch that may be set up before the stream's previous kernel has ended.

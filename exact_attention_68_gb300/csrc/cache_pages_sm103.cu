@@ -17,7 +17,9 @@ namespace ea {
 namespace {
 
 constexpr int kPageThreads = 256;
-constexpr int kMaxItems = 4;  // tokens of a thread: 64 slots over at least 16 threads of a unit
+// Tokens of a thread (ITEMS): 64 slots over 32 threads of a unit or more up to
+// 128 channels, over 16 or more above.
+constexpr int items_for(int pitch) { return pitch <= 128 ? 2 : 4; }
 
 // Tokens of a 16-bit [rows, D] block.
 template <bool F16>
@@ -78,11 +80,15 @@ struct CodeSource {
 
 // Writes `count` tokens from `src` to slots held .. held+count-1 of page g,
 // head h; slots below `held` hold earlier tokens, which stay.
-template <class Src>
+//
+// Rounding keeps order, so a channel's largest code is the code of its largest
+// value: the bounds cost two comparisons a value (fmaxf and fminf pass NaN
+// over), and codes only meet at the end, four to a word.
+template <int ITEMS, class Src>
 __device__ __forceinline__ void write_page(const CacheView& c, int g, int h, bool is_v, int held,
                                            int count, const Src& src) {
   __shared__ uint32_t red[kPageThreads / 32];
-  __shared__ __align__(16) int8_t top[kPageThreads * 16], bottom[kPageThreads * 16];
+  __shared__ __align__(16) uint32_t top[kPageThreads * 4], bottom[kPageThreads * 4];
   const int units = c.pitch >> 4, tpu = kPageThreads / units;
   const int unit = threadIdx.x % units, lane_t = threadIdx.x / units;
   const bool active = lane_t < tpu;
@@ -91,19 +97,44 @@ __device__ __forceinline__ void write_page(const CacheView& c, int g, int h, boo
   float* scale = (is_v ? c.v_scale : c.k_scale) + gh;
   const float was = held > 0 ? *scale : 0.f;
 
-  typename Src::Raw raw[kMaxItems];
-  float a = 0.f;
+  typename Src::Raw raw[ITEMS];
 #pragma unroll
-  for (int i = 0; i < kMaxItems; ++i) {
-    const int t = lane_t + i * tpu;
-    if (active && t < count) {
-      raw[i] = src.load(t, unit);
+  for (int i = 0; i < ITEMS; ++i)
+    if (active && lane_t + i * tpu < count) raw[i] = src.load(lane_t + i * tpu, unit);
+  float hi[16], lo[16], a = 0.f;  // k: the thread's channels' extremes; v: the largest |x|
+  if (!is_v) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) hi[e] = -INFINITY, lo[e] = INFINITY;
+  }
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    if (active && lane_t + i * tpu < count) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float2 x = Src::pair(raw[i], e);
-        a = fmaxf(a, fmaxf(finite_abs(x.x), finite_abs(x.y)));
+        if (is_v) {
+          a = fmaxf(a, fmaxf(fabsf(x.x), fabsf(x.y)));
+        } else {
+          hi[2 * e] = fmaxf(hi[2 * e], x.x), lo[2 * e] = fminf(lo[2 * e], x.x);
+          hi[2 * e + 1] = fmaxf(hi[2 * e + 1], x.y), lo[2 * e + 1] = fminf(lo[2 * e + 1], x.y);
+        }
       }
     }
+  }
+  if (!is_v) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) a = fmaxf(a, fmaxf(hi[e], -lo[e]));
+  }
+  if (a == INFINITY) {  // infinities do not count: once more without them
+    a = 0.f;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i)
+      if (active && lane_t + i * tpu < count)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 x = Src::pair(raw[i], e);
+          a = fmaxf(a, fmaxf(finite_abs(x.x), finite_abs(x.y)));
+        }
   }
   // non-negative floats order as their bits
   const uint32_t wa = __reduce_max_sync(0xffffffffu, __float_as_uint(a));
@@ -115,35 +146,39 @@ __device__ __forceinline__ void write_page(const CacheView& c, int g, int h, boo
   const float fresh = page_scale(__uint_as_float(ua));
   const float s = held > 0 ? fmaxf(was, fresh) : fresh;
   const bool grown = held > 0 && s != was;
-  const Divider div(s);
-
-  uint32_t hi[4], lo[4];  // ordered codes, 16 channels
+  uint32_t up[4], dn[4];  // ordered codes of the extremes; 0x80 / 0x7f: none
 #pragma unroll
-  for (int w = 0; w < 4; ++w) hi[w] = 0x80808080u, lo[w] = 0x7f7f7f7fu;
-  auto bounds = [&](const uint32_t (&q)[4]) {
+  for (int w = 0; w < 4; ++w) up[w] = 0x80808080u, dn[w] = 0x7f7f7f7fu;
+  with_divider(s, [&](auto div) {
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      uint32_t nan;
-      const uint32_t o = e4m3_order4(q[w], &nan);
-      hi[w] = __vmaxs4(hi[w], (o & ~nan) | (0x80808080u & nan));
-      lo[w] = __vmins4(lo[w], (o & ~nan) | (0x7f7f7f7fu & nan));
+    for (int i = 0; i < ITEMS; ++i) {
+      const int t = lane_t + i * tpu;
+      if (active && t < count) {
+        uint32_t q[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float2 x = Src::pair(raw[i], 2 * w), y = Src::pair(raw[i], 2 * w + 1);
+          q[w] = pack_e4m3x2(div(x.x), div(x.y)) | (pack_e4m3x2(div(y.x), div(y.y)) << 16);
+        }
+        *reinterpret_cast<uint4*>(rows + static_cast<int64_t>(held + t) * c.pitch) =
+            make_uint4(q[0], q[1], q[2], q[3]);
+      }
     }
-  };
-#pragma unroll
-  for (int i = 0; i < kMaxItems; ++i) {
-    const int t = lane_t + i * tpu;
-    if (active && t < count) {
-      uint32_t q[4];
+    if (!is_v && active) {
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const float2 x = Src::pair(raw[i], 2 * w), y = Src::pair(raw[i], 2 * w + 1);
-        q[w] = pack_e4m3x2(div(x.x), div(x.y)) | (pack_e4m3x2(div(y.x), div(y.y)) << 16);
+        uint32_t nan, none = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) none |= hi[4 * w + e] < lo[4 * w + e] ? 0xffu << (8 * e) : 0u;
+        const uint32_t u = e4m3_order4(pack_e4m3x2(div(hi[4 * w]), div(hi[4 * w + 1])) |
+                                       (pack_e4m3x2(div(hi[4 * w + 2]), div(hi[4 * w + 3])) << 16), &nan);
+        const uint32_t d = e4m3_order4(pack_e4m3x2(div(lo[4 * w]), div(lo[4 * w + 1])) |
+                                       (pack_e4m3x2(div(lo[4 * w + 2]), div(lo[4 * w + 3])) << 16), &nan);
+        up[w] = (u & ~none) | (0x80808080u & none);
+        dn[w] = (d & ~none) | (0x7f7f7f7fu & none);
       }
-      *reinterpret_cast<uint4*>(rows + static_cast<int64_t>(held + t) * c.pitch) =
-          make_uint4(q[0], q[1], q[2], q[3]);
-      if (!is_v) bounds(q);
     }
-  }
+  });
   if (grown) {
     // the earlier codes move to the larger scale
     const float ratio = __fdiv_rn(was, s);
@@ -156,43 +191,47 @@ __device__ __forceinline__ void write_page(const CacheView& c, int g, int h, boo
         uint32_t h0, h1;
         e4m3x4_to_f16(q[w], &h0, &h1);
         const float2 x = half2_bits_to_float2(h0), y = half2_bits_to_float2(h1);
-        q[w] = pack_e4m3x2(x.x * ratio, x.y * ratio) |
-               (pack_e4m3x2(y.x * ratio, y.y * ratio) << 16);
+        q[w] = pack_e4m3x2(x.x * ratio, x.y * ratio) | (pack_e4m3x2(y.x * ratio, y.y * ratio) << 16);
+        uint32_t nan;
+        const uint32_t o = e4m3_order4(q[w], &nan);
+        up[w] = __vmaxs4(up[w], (o & ~nan) | (0x80808080u & nan));
+        dn[w] = __vmins4(dn[w], (o & ~nan) | (0x7f7f7f7fu & nan));
       }
       *at = make_uint4(q[0], q[1], q[2], q[3]);
-      if (!is_v) bounds(q);
     }
   }
   if (!is_v && active) {
-    *reinterpret_cast<uint4*>(&top[lane_t * c.pitch + unit * 16]) =
-        make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(&bottom[lane_t * c.pitch + unit * 16]) =
-        make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    reinterpret_cast<uint4*>(top)[lane_t * units + unit] = make_uint4(up[0], up[1], up[2], up[3]);
+    reinterpret_cast<uint4*>(bottom)[lane_t * units + unit] = make_uint4(dn[0], dn[1], dn[2], dn[3]);
   }
   __syncthreads();  // bounds staged; every thread has read the old scale
   if (threadIdx.x == 0) *scale = s;
-  if (!is_v && threadIdx.x < c.pitch) {
-    const int ch = threadIdx.x;
-    int u = -128, d = 127;
-    for (int t = 0; t < tpu; ++t) {
-      u = max(u, static_cast<int>(top[t * c.pitch + ch]));
-      d = min(d, static_cast<int>(bottom[t * c.pitch + ch]));
-    }
-    int8_t* bd = c.k_bounds + gh * 2 * c.pitch + ch;
+  const int words = c.pitch >> 2;  // of a row of bounds
+  if (!is_v && threadIdx.x < 2 * words) {
+    const bool upper = threadIdx.x < words;
+    const int w = upper ? threadIdx.x : threadIdx.x - words;
+    const uint32_t* from = (upper ? top : bottom) + w;
+    uint32_t o = from[0];
+    for (int t = 1; t < min(tpu, max(count, grown ? held : 0)); ++t)
+      o = upper ? __vmaxs4(o, from[t * words]) : __vmins4(o, from[t * words]);
+    uint32_t* bd = reinterpret_cast<uint32_t*>(c.k_bounds + (gh * 2 + (upper ? 0 : 1)) * c.pitch) + w;
     const bool keep = held > 0 && !grown;
-    int bu = u >= -127 ? bound_of_order(u, true) : 0, bl = u >= -127 ? bound_of_order(d, false) : 0;
-    if (keep) {
-      const int ou = bd[0], ol = bd[c.pitch];
-      bu = u >= -127 ? max(bu, ou) : ou;
-      bl = u >= -127 ? min(bl, ol) : ol;
+    const uint32_t old = keep ? *bd : 0u;
+    uint32_t r = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int x = static_cast<int8_t>(o >> (8 * e)), was_b = static_cast<int8_t>(old >> (8 * e));
+      const bool none = upper ? x == -128 : x == 127;
+      int bnd = none ? 0 : bound_of_order(x, upper);
+      if (keep) bnd = none ? was_b : upper ? max(bnd, was_b) : min(bnd, was_b);
+      r |= (static_cast<uint32_t>(bnd) & 0xffu) << (8 * e);
     }
-    bd[0] = static_cast<int8_t>(bu);
-    bd[c.pitch] = static_cast<int8_t>(bl);
+    *bd = r;
   }
 }
 
-template <bool F16>
-__global__ void __launch_bounds__(kPageThreads) cache_append_kernel(const CacheAppendParams p) {
+template <bool F16, int ITEMS>
+__global__ void __launch_bounds__(kPageThreads, ITEMS == 2 ? 3 : 2) cache_append_kernel(const CacheAppendParams p) {
   int x = blockIdx.x;
   const bool is_v = x & 1;
   x >>= 1;
@@ -208,7 +247,7 @@ __global__ void __launch_bounds__(kPageThreads) cache_append_kernel(const CacheA
   const int from = max(base, start), to = min(base + p.c.page, len);
   const int64_t row = (static_cast<int64_t>(b) * p.c.heads + h) * p.s.T + (from - start);
   const RowSource<F16> src{(is_v ? p.v : p.k) + row * p.c.D, p.c.D};
-  write_page(p.c, g, h, is_v, from - base, to - from, src);
+  write_page<ITEMS>(p.c, g, h, is_v, from - base, to - from, src);
 }
 
 // ---------------------------------------------------------------- evict
@@ -274,7 +313,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_evict_plan_kernel(const Ca
     }
   } else {
     const int tail = min(p.recent, len), best = p.keep - tail;
-    block_top_ascending<kPlanThreads>([&](int j) { return order_key(mass[j]); }, len - tail, best,
+    block_top_ascending<kPlanThreads, 16>([&](int j) { return order_key(mass[j]); }, len - tail, best,
                                       [&](int at, int j) {
                                         kept[at] = j;
                                         out[at] = mass[j];
@@ -289,8 +328,9 @@ __global__ void __launch_bounds__(kPlanThreads) cache_evict_plan_kernel(const Ca
     out[j] = 0.f;
 }
 
-__global__ void __launch_bounds__(kPageThreads) cache_evict_move_kernel(const CacheEvictParams p,
-                                                                        int pages_per_seq) {
+template <int ITEMS>
+__global__ void __launch_bounds__(kPageThreads, ITEMS == 2 ? 4 : 2)
+    cache_evict_move_kernel(const CacheEvictParams p, int pages_per_seq) {
   int x = blockIdx.x;
   const bool is_v = x & 1;
   x >>= 1;
@@ -303,15 +343,17 @@ __global__ void __launch_bounds__(kPageThreads) cache_evict_move_kernel(const Ca
   if (g < 0) return;
   const CodeSource src{p.c, p.s, is_v ? p.c.v : p.c.k, is_v ? p.c.v_scale : p.c.k_scale,
                        p.kept + (static_cast<int64_t>(b) * p.c.heads + h) * p.keep + base, b, h};
-  write_page(p.c, g, h, is_v, 0, min(p.c.page, left - base), src);
+  write_page<ITEMS>(p.c, g, h, is_v, 0, min(p.c.page, left - base), src);
 }
 
 }  // namespace
 
 cudaError_t cache_append_launch(const CacheAppendParams& p, bool f16, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>(2ll * p.pages_per_seq * p.c.heads * p.s.batch);
-  if (f16) cache_append_kernel<true><<<grid, kPageThreads, 0, stream>>>(p);
-  else cache_append_kernel<false><<<grid, kPageThreads, 0, stream>>>(p);
+  const bool two = items_for(p.c.pitch) == 2;
+  auto kern = f16 ? (two ? cache_append_kernel<true, 2> : cache_append_kernel<true, 4>)
+                  : (two ? cache_append_kernel<false, 2> : cache_append_kernel<false, 4>);
+  kern<<<grid, kPageThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -321,7 +363,8 @@ cudaError_t cache_evict_launch(const CacheEvictParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int pages_per_seq = (p.keep + p.c.page - 1) >> p.c.log2_page;
   const unsigned grid = static_cast<unsigned>(2ll * pages_per_seq * p.c.heads * p.s.batch);
-  cache_evict_move_kernel<<<grid, kPageThreads, 0, stream>>>(p, pages_per_seq);
+  auto kern = items_for(p.c.pitch) == 2 ? cache_evict_move_kernel<2> : cache_evict_move_kernel<4>;
+  kern<<<grid, kPageThreads, 0, stream>>>(p, pages_per_seq);
   return cudaGetLastError();
 }
 

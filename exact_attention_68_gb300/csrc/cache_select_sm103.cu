@@ -18,14 +18,15 @@ namespace {
 
 constexpr int kScoreThreads = 128;
 constexpr int kScoreGroups = kScoreThreads / 4;  // pages at a time
-constexpr int kScoreRows = 32;                   // query rows in shared memory at a time
-constexpr int kMaxPagesPerGroup = 4;
 
-template <bool F16>
+// UNITS: 16-channel units of a lane (1, 2 or 4: up to 64, 128, 256 channels);
+// ROWS: query rows held in registers while a CTA's pages go by (more rows: once
+// more over the pages, whose bounds then come from L2).
+template <int UNITS, int ROWS, bool F16>
 __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const CacheSelectParams p,
                                                                     int pages_per_group) {
-  __shared__ __align__(16) int8_t qpos[kScoreRows * 256], qneg[kScoreRows * 256];
-  __shared__ float qa[kScoreRows];
+  __shared__ __align__(16) int8_t qpos[ROWS * 256], qneg[ROWS * 256];
+  __shared__ float qa[ROWS];
   const int h = blockIdx.y, b = blockIdx.z;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane & 3, group = threadIdx.x >> 2;
@@ -34,98 +35,118 @@ __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const CacheS
   load_seq(p.s, p.c, b, threadIdx.x == 0 && blockIdx.x == 0 && h == 0, &len, &n);
   const int np = n > 0 ? (len + p.c.page - 1) >> p.c.log2_page : 0;
   const int first = blockIdx.x * kScoreGroups * pages_per_group;
-  float best[kMaxPagesPerGroup];
-#pragma unroll
-  for (int k = 0; k < kMaxPagesPerGroup; ++k) best[k] = -INFINITY;
   const int rows = p.G * p.s.T;
   const uint16_t* q = p.q + (static_cast<int64_t>(b) * p.c.heads + h) * rows * p.c.D;
-  if (first < np) {
-    for (int r0 = 0; r0 < rows; r0 += kScoreRows) {
-      const int nr = min(kScoreRows, rows - r0);
-      __syncthreads();
-      for (int r = warp; r < nr; r += kScoreThreads / 32) {
-        // one row a warp, 8 channels a lane
-        const bool in = 8 * lane < p.c.D;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (in) w = __ldg(reinterpret_cast<const uint4*>(q + static_cast<int64_t>(r0 + r) * p.c.D + 8 * lane));
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-        float a = 0.f;
+  float* scores = p.scores + (static_cast<int64_t>(b) * p.c.heads + h) * p.s.width;
+  const int stop = min(np, first + kScoreGroups * pages_per_group);
+  for (int r0 = 0; first < np && r0 < rows; r0 += ROWS) {
+    const int nr = min(ROWS, rows - r0);
+    __syncthreads();
+    for (int r = warp; r < ROWS; r += kScoreThreads / 32) {
+      // one row a warp, 8 channels a lane
+      const bool in = 8 * lane < p.c.D && r < nr;
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (in) w = __ldg(reinterpret_cast<const uint4*>(q + static_cast<int64_t>(r0 + r) * p.c.D + 8 * lane));
+      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+      float a = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 x = pair_to_float2<F16>(ws[e]);
-          a = fmaxf(a, fmaxf(finite_abs(x.x), finite_abs(x.y)));
-        }
-        a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
-        const float steps = a > 0.f ? __fdiv_rn(127.f, a) : 0.f;
-        uint32_t up[2] = {0u, 0u}, dn[2] = {0u, 0u};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 x2 = pair_to_float2<F16>(ws[e >> 1]);
-          float y = rintf(__fmul_rn((e & 1) ? x2.y : x2.x, steps));
-          if (y != y) y = 0.f;
-          const int i = static_cast<int>(fminf(fmaxf(y, -127.f), 127.f));
-          up[e >> 2] |= (static_cast<uint32_t>(max(i, 0)) & 0xffu) << (8 * (e & 3));
-          dn[e >> 2] |= (static_cast<uint32_t>(min(i, 0)) & 0xffu) << (8 * (e & 3));
-        }
-        if (8 * lane < p.c.pitch) {  // padding channels hold zero
-          *reinterpret_cast<uint2*>(&qpos[r * 256 + 8 * lane]) = make_uint2(up[0], up[1]);
-          *reinterpret_cast<uint2*>(&qneg[r * 256 + 8 * lane]) = make_uint2(dn[0], dn[1]);
-        }
-        if (lane == 0) qa[r] = (r0 + r) % p.s.T < n ? a : -1.f;  // -1: no such token
+      for (int e = 0; e < 4; ++e) {
+        const float2 x = pair_to_float2<F16>(ws[e]);
+        a = fmaxf(a, fmaxf(finite_abs(x.x), finite_abs(x.y)));
       }
-      __syncthreads();
+      a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
+      const float steps = a > 0.f ? __fdiv_rn(127.f, a) : 0.f;
+      uint32_t up[2] = {0u, 0u}, dn[2] = {0u, 0u};
 #pragma unroll
-      for (int k = 0; k < kMaxPagesPerGroup; ++k) {
-        const int i = first + k * kScoreGroups + group;
-        const bool mine = k < pages_per_group && i < np;
-        const int g = mine ? load_page(p.s, p.c, b, i, r0 == 0 && sub == 0) : -1;
-        const int64_t gh = static_cast<int64_t>(g < 0 ? 0 : g) * p.c.heads + h;
-        const int8_t* bd = p.c.k_bounds + gh * 2 * p.c.pitch;
-        uint4 hi[4], lo[4];
+      for (int e = 0; e < 8; ++e) {
+        const float2 x2 = pair_to_float2<F16>(ws[e >> 1]);
+        float y = rintf(__fmul_rn((e & 1) ? x2.y : x2.x, steps));
+        if (y != y) y = 0.f;
+        const int i = static_cast<int>(fminf(fmaxf(y, -127.f), 127.f));
+        up[e >> 2] |= (static_cast<uint32_t>(max(i, 0)) & 0xffu) << (8 * (e & 3));
+        dn[e >> 2] |= (static_cast<uint32_t>(min(i, 0)) & 0xffu) << (8 * (e & 3));
+      }
+      // padding channels, to the end of the lanes' units, hold zero
+      *reinterpret_cast<uint2*>(&qpos[r * 256 + 8 * lane]) = make_uint2(up[0], up[1]);
+      *reinterpret_cast<uint2*>(&qneg[r * 256 + 8 * lane]) = make_uint2(dn[0], dn[1]);
+      if (lane == 0) qa[r] = r < nr && (r0 + r) % p.s.T < n ? a : -1.f;  // -1: no such token
+    }
+    __syncthreads();
+    int4 x[ROWS][UNITS], y[ROWS][UNITS];
+    float a[ROWS];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int u = sub + 4 * j;
-          hi[j] = lo[j] = make_uint4(0, 0, 0, 0);
-          if (g >= 0 && u < units) {
-            hi[j] = __ldg(reinterpret_cast<const uint4*>(bd + u * 16));
-            lo[j] = __ldg(reinterpret_cast<const uint4*>(bd + p.c.pitch + u * 16));
-          }
-        }
-        const float ks = g >= 0 ? __ldg(p.c.k_scale + gh) : 0.f;
-        for (int r = 0; r < nr; ++r) {
-          const float a = qa[r];
-          if (a < 0.f) continue;
-          int sum = 0;
+    for (int r = 0; r < ROWS; ++r) {
+      a[r] = qa[r];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int u = sub + 4 * j;
-            if (u < units) {
-              const int4 x = *reinterpret_cast<const int4*>(&qpos[r * 256 + u * 16]);
-              const int4 y = *reinterpret_cast<const int4*>(&qneg[r * 256 + u * 16]);
-              sum = __dp4a(static_cast<int>(hi[j].x), x.x, sum);
-              sum = __dp4a(static_cast<int>(hi[j].y), x.y, sum);
-              sum = __dp4a(static_cast<int>(hi[j].z), x.z, sum);
-              sum = __dp4a(static_cast<int>(hi[j].w), x.w, sum);
-              sum = __dp4a(static_cast<int>(lo[j].x), y.x, sum);
-              sum = __dp4a(static_cast<int>(lo[j].y), y.y, sum);
-              sum = __dp4a(static_cast<int>(lo[j].z), y.z, sum);
-              sum = __dp4a(static_cast<int>(lo[j].w), y.w, sum);
-            }
-          }
-          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          if (g >= 0)
-            best[k] = fmaxf(best[k], __fmul_rn(__fmul_rn(static_cast<float>(sum), ks), a));
-        }
+      for (int j = 0; j < UNITS; ++j) {
+        x[r][j] = *reinterpret_cast<const int4*>(&qpos[r * 256 + (sub + 4 * j) * 16]);
+        y[r][j] = *reinterpret_cast<const int4*>(&qneg[r * 256 + (sub + 4 * j) * 16]);
       }
     }
-  }
-  float* scores = p.scores + (static_cast<int64_t>(b) * p.c.heads + h) * p.s.width;
+    // The pages of a group in turn; page numbers are asked for two steps ahead,
+    // bounds one, so that a step's loads are in flight while the last one's
+    // products run.  All lanes take all steps (the shuffles want them).
+    struct Bounds {
+      int4 hi[UNITS], lo[UNITS];
+      float ks;
+      bool have;
+    };
+    auto page_of = [&](int k) {
+      const int i = first + group + k * kScoreGroups;
+      return k < pages_per_group && i < stop ? load_page(p.s, p.c, b, i, r0 == 0 && sub == 0) : -1;
+    };
+    auto bounds_of = [&](int g, Bounds& x) {
+      const int64_t gh = static_cast<int64_t>(g < 0 ? 0 : g) * p.c.heads + h;
+      const int8_t* bd = p.c.k_bounds + gh * 2 * p.c.pitch;
+      x.have = g >= 0;
 #pragma unroll
-  for (int k = 0; k < kMaxPagesPerGroup; ++k) {
-    const int i = first + k * kScoreGroups + group;
-    if (k < pages_per_group && i < p.s.width && sub == 0) scores[i] = best[k];
+      for (int j = 0; j < UNITS; ++j) {
+        const int u = sub + 4 * j;
+        x.hi[j] = x.lo[j] = make_int4(0, 0, 0, 0);
+        if (x.have && u < units) {
+          x.hi[j] = __ldg(reinterpret_cast<const int4*>(bd + u * 16));
+          x.lo[j] = __ldg(reinterpret_cast<const int4*>(bd + p.c.pitch + u * 16));
+        }
+      }
+      x.ks = x.have ? __ldg(p.c.k_scale + gh) : 0.f;
+    };
+    Bounds now, next;
+    bounds_of(page_of(0), now);
+    int g = page_of(1);
+#pragma unroll 1
+    for (int k = 0; k < pages_per_group; ++k) {
+      const int i = first + group + k * kScoreGroups;
+      bounds_of(g, next);
+      g = page_of(k + 2);
+      float best = -INFINITY;
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        int sum = 0;
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j) {
+          sum = __dp4a(now.hi[j].x, x[r][j].x, sum);
+          sum = __dp4a(now.hi[j].y, x[r][j].y, sum);
+          sum = __dp4a(now.hi[j].z, x[r][j].z, sum);
+          sum = __dp4a(now.hi[j].w, x[r][j].w, sum);
+          sum = __dp4a(now.lo[j].x, y[r][j].x, sum);
+          sum = __dp4a(now.lo[j].y, y[r][j].y, sum);
+          sum = __dp4a(now.lo[j].z, y[r][j].z, sum);
+          sum = __dp4a(now.lo[j].w, y[r][j].w, sum);
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (a[r] >= 0.f) best = fmaxf(best, __fmul_rn(__fmul_rn(static_cast<float>(sum), now.ks), a[r]));
+      }
+      if (sub == 0 && i < stop) {
+        if (!now.have) best = -INFINITY;
+        scores[i] = r0 == 0 ? best : fmaxf(scores[i], best);
+      }
+      now = next;
+    }
   }
+  // pages behind the sequence's end
+  for (int i = max(first, np) + threadIdx.x; i < min(p.s.width, first + kScoreGroups * pages_per_group); i += kScoreThreads)
+    scores[i] = -INFINITY;
 }
 
 constexpr int kPickThreads = 512;
@@ -143,7 +164,7 @@ __global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const CacheSel
     const int first = (len - n) >> p.c.log2_page;  // from here on the new tokens' pages
     const int fresh = min(np - first, p.count);
     const int best = min(p.count - fresh, first);
-    block_top_ascending<kPickThreads>([&](int i) { return order_key(scores[i]); }, first, best,
+    block_top_ascending<kPickThreads, 8>([&](int i) { return order_key(scores[i]); }, first, best,
                                       [&](int at, int i) { pages[at] = i; });
     for (int i = threadIdx.x; i < fresh; i += kPickThreads) pages[best + i] = np - fresh + i;
     taken = best + fresh;
@@ -151,18 +172,32 @@ __global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const CacheSel
   for (int i = taken + threadIdx.x; i < p.count; i += kPickThreads) pages[i] = -1;
 }
 
+template <int UNITS, int ROWS>
+cudaError_t score(const CacheSelectParams& p, bool f16, cudaStream_t stream) {
+  // pages a group that give each of about 152 SMs three CTAs, what its registers hold
+  auto ctas = [&](int64_t k) { return static_cast<int>((p.s.width + kScoreGroups * k - 1) / (kScoreGroups * k)); };
+  const int64_t steps = static_cast<int64_t>(p.s.batch) * p.c.heads * ctas(1);
+  const int per = static_cast<int>((steps + 455) / 456);
+  const dim3 grid(ctas(per), p.c.heads, p.s.batch);
+  if (f16) cache_score_kernel<UNITS, ROWS, true><<<grid, kScoreThreads, 0, stream>>>(p, per);
+  else cache_score_kernel<UNITS, ROWS, false><<<grid, kScoreThreads, 0, stream>>>(p, per);
+  return cudaGetLastError();
+}
+template <int UNITS>
+cudaError_t score_rows(const CacheSelectParams& p, bool f16, cudaStream_t stream) {
+  const int rows = p.G * p.s.T;
+  if (rows == 1) return score<UNITS, 1>(p, f16, stream);
+  if (rows <= 4 || UNITS == 4) return score<UNITS, 4>(p, f16, stream);
+  return score<UNITS, UNITS == 4 ? 4 : 8>(p, f16, stream);
+}
+
 }  // namespace
 
 cudaError_t cache_select_launch(const CacheSelectParams& p, bool f16, cudaStream_t stream) {
-  // as many pages a CTA as leave two CTAs for each of about 152 SMs
-  int per = kMaxPagesPerGroup;
-  while (per > 1 && static_cast<int64_t>(p.s.batch) * p.c.heads *
-                            ((p.s.width + kScoreGroups * per - 1) / (kScoreGroups * per)) < 304)
-    per >>= 1;
-  const dim3 grid((p.s.width + kScoreGroups * per - 1) / (kScoreGroups * per), p.c.heads, p.s.batch);
-  if (f16) cache_score_kernel<true><<<grid, kScoreThreads, 0, stream>>>(p, per);
-  else cache_score_kernel<false><<<grid, kScoreThreads, 0, stream>>>(p, per);
-  cudaError_t e = cudaGetLastError();
+  const int units = p.c.pitch >> 4;
+  cudaError_t e = units <= 4   ? score_rows<1>(p, f16, stream)
+                  : units <= 8 ? score_rows<2>(p, f16, stream)
+                               : score_rows<4>(p, f16, stream);
   if (e != cudaSuccess) return e;
   cache_pick_kernel<<<dim3(p.c.heads, p.s.batch), kPickThreads, 0, stream>>>(p);
   return cudaGetLastError();

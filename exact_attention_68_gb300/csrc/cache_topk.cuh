@@ -8,49 +8,78 @@ namespace ea {
 
 // Calls emit(place, index) for the k largest of key(0) .. key(n-1) (equal
 // keys: the lowest indices), places 0 .. k-1 in the order of the indices.
-// key() is called up to five times per index.  Whole CTA; 0 <= k.
+// Whole CTA of at most 1024 threads; 0 <= k.  Keys are held in registers, up to
+// ITEMS to a thread, side by side; where n needs more than one such tile, key()
+// is called again per pass.
 //
-// Four passes over 8 bits each: a histogram of the keys that agree with the
-// digits found so far, then the digit in which the k-th largest lies.
-template <int THREADS, class Key, class Emit>
+// Three passes over 11, 11 and 10 bits: a histogram of the keys that agree
+// with the digits found so far, then the digit in which the k-th largest lies.
+// Floats of like size share their leading bits, so wide digits matter: with
+// four passes of 8 bits the first one's atomics fell on a few bins, and 64 rows
+// of 16384 weights took 36 us.
+template <int THREADS, int ITEMS, class Key, class Emit>
 __device__ __forceinline__ void block_top_ascending(Key key, int n, int k, Emit emit) {
-  constexpr int kWarps = THREADS / 32;
-  __shared__ int hist[256];
+  constexpr int kWarps = THREADS / 32, kBins = 2048, kPer = kBins / THREADS;
+  static_assert(kBins % THREADS == 0, "bins are shared out evenly");
+  __shared__ int hist[kBins];
   __shared__ uint32_t sh_prefix;
   __shared__ int sh_need;
-  __shared__ uint32_t counts[2][kWarps];
+  __shared__ int counts[kWarps];
+  __shared__ int2 pairs[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (k <= 0 || n <= 0) return;
+  const int per = min(ITEMS, (n + THREADS - 1) / THREADS), tile = per * THREADS;
+  const bool all = k >= n, one_tile = n <= tile;
+  const int mine = threadIdx.x * per;
+  uint32_t held[ITEMS];
+  auto load = [&](int base) {
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) {
+      const int i = base + mine + j;
+      held[j] = j < per && i < n ? key(i) : 0u;
+    }
+  };
+  if (one_tile) load(0);
   uint32_t prefix = 0;
-  int need = k < n ? k : n;  // of the keys that agree with prefix, how many are taken
-  if (k < n) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = threadIdx.x; i < 256; i += THREADS) hist[i] = 0;
+  int need = k;  // of the keys that agree with prefix, how many are taken
+  if (!all) {
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, digits = pass == 2 ? 0x3ff : 0x7ff;
+      const uint32_t mask = pass == 0 ? 0u : pass == 1 ? 0xffe00000u : 0xfffffc00u;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) hist[threadIdx.x + j * THREADS] = 0;
       __syncthreads();
-      const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-      for (int i = threadIdx.x; i < n; i += THREADS) {
-        const uint32_t u = key(i);
-        if (((u ^ prefix) & mask) == 0) atomicAdd(&hist[(u >> shift) & 255], 1);
+      for (int base = 0; base < n; base += tile) {
+        if (!one_tile) load(base);
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j)
+          if (j < per && base + mine + j < n && ((held[j] ^ prefix) & mask) == 0)
+            atomicAdd(&hist[(held[j] >> shift) & digits], 1);
       }
       __syncthreads();
-      if (warp == 0) {
-        // lane L holds digits 255-8L .. 248-8L, the highest first
-        int c[8], sum = 0;
+      // thread t holds kPer bins, the highest first; keys in higher bins by a scan
+      int c[kPer], sum = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum += c[j] = hist[255 - 8 * lane - j];
-        int before = sum;
+      for (int j = 0; j < kPer; ++j) sum += c[j] = hist[kBins - 1 - (threadIdx.x * kPer + j)];
+      int upto = sum;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int o = __shfl_up_sync(0xffffffffu, before, d);
-          if (lane >= d) before += o;
-        }
-        before -= sum;  // keys in higher digits
-        if (before < need && need <= before + sum) {
-          int rest = need - before;
-          int j = 0;
-          while (rest > c[j]) rest -= c[j], ++j;
-          sh_prefix = prefix | (static_cast<uint32_t>(255 - 8 * lane - j) << shift);
-          sh_need = rest;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += o;
+      }
+      if (lane == 31) counts[warp] = upto;
+      __syncthreads();
+      upto += __reduce_add_sync(0xffffffffu, lane < warp ? counts[lane] : 0);
+      int before = upto - sum;
+      if (before < need && need <= upto) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          if (before < need && need <= before + c[j]) {
+            sh_prefix = prefix | (static_cast<uint32_t>(kBins - 1 - (threadIdx.x * kPer + j)) << shift);
+            sh_need = need - before;
+          }
+          before += c[j];
         }
       }
       __syncthreads();
@@ -59,29 +88,43 @@ __device__ __forceinline__ void block_top_ascending(Key key, int n, int k, Emit 
     }
   }
   // keys above the k-th largest are taken, and the first `need` that equal it
-  int above = 0, equal = 0;  // counts before this step's keys
-  for (int i0 = 0, step = 0; i0 < n; i0 += THREADS, ++step) {
-    const int i = i0 + threadIdx.x;
-    const uint32_t u = i < n ? key(i) : 0u;
-    const bool all = k >= n;
-    const bool gt = i < n && (all || u > prefix), eq = i < n && !all && u == prefix;
-    const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) counts[step & 1][warp] = static_cast<uint32_t>(__popc(mg)) | (static_cast<uint32_t>(__popc(me)) << 16);
-    __syncthreads();
-    uint32_t low = 0, total = 0;  // this step's counts, packed (each at most THREADS)
+  int above = 0, equal = 0;  // counts before this tile
+  for (int base = 0; base < n; base += tile) {
+    if (!one_tile) load(base);
+    int gt = 0, eq = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const uint32_t c = counts[step & 1][w];
-      if (w < warp) low += c;
-      total += c;
+    for (int j = 0; j < ITEMS; ++j) {
+      const bool in = j < per && base + mine + j < n;
+      gt += in && (all || held[j] > prefix);
+      eq += in && !all && held[j] == prefix;
     }
-    const uint32_t below = (1u << lane) - 1u;
-    const int g = above + static_cast<int>(low & 0xffffu) + __popc(mg & below);
-    const int e = equal + static_cast<int>(low >> 16) + __popc(me & below);
-    if (gt) emit(g + (e < need ? e : need), i);
-    else if (eq && e < need) emit(g + e, i);
-    above += static_cast<int>(total & 0xffffu);
-    equal += static_cast<int>(total >> 16);
+    int ug = gt, ue = eq;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int og = __shfl_up_sync(0xffffffffu, ug, d), oe = __shfl_up_sync(0xffffffffu, ue, d);
+      if (lane >= d) ug += og, ue += oe;
+    }
+    __syncthreads();  // the last tile's pairs have been read
+    if (lane == 31) pairs[warp] = make_int2(ug, ue);
+    __syncthreads();
+    int g = above + ug - gt, e = equal + ue - eq;
+    const int2 w = lane < kWarps ? pairs[lane] : make_int2(0, 0);
+    g += __reduce_add_sync(0xffffffffu, lane < warp ? w.x : 0);
+    e += __reduce_add_sync(0xffffffffu, lane < warp ? w.y : 0);
+    above += __reduce_add_sync(0xffffffffu, w.x);
+    equal += __reduce_add_sync(0xffffffffu, w.y);
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) {
+      const int i = base + mine + j;
+      if (j >= per || i >= n) break;
+      if (all || held[j] > prefix) {
+        emit(g + min(e, need), i);
+        ++g;
+      } else if (held[j] == prefix) {
+        if (e < need) emit(g + e, i);
+        ++e;
+      }
+    }
   }
 }
 
