@@ -110,13 +110,13 @@ __device__ __forceinline__ uint32_t e4m3_order4(uint32_t w, uint32_t* nan) {
 }
 
 // The int8 bound of one ordered code: the value in steps of 448/127, rounded
-// up (upper bound) or down.  value·127 is exact, and the quotient's one rounding
-// (2^-24 of it) cannot carry it to a whole number it does not equal: with a
-// 4-bit significand it is at least 1 / (15·127) of its size away from one.
+// up (upper bound) or down.  Only 0 and ±448 are whole numbers of steps (448 =
+// 2^6·7 and 127 share no factor, a code's significand has 4 bits); at the others
+// a product's rounding, 2^-23 of it, is far from carrying over a whole number,
+// and ±448 is clamped to ±127.
 __device__ __forceinline__ int bound_of_order(int o, bool upper) {
   const uint32_t code = o < 0 ? (0x80u | static_cast<uint32_t>(-o)) : static_cast<uint32_t>(o);
-  const float x = half2_bits_to_float2(e4m3x2_to_f16x2(code)).x;
-  const float y = __fdiv_rn(x * 127.f, kE4M3Max);
+  const float y = half2_bits_to_float2(e4m3x2_to_f16x2(code)).x * (127.f / kE4M3Max);
   const int r = static_cast<int>(upper ? ceilf(y) : floorf(y));
   return max(-127, min(127, r));
 }

@@ -7,6 +7,8 @@
 // and every TPU-th token, so that a row's units lie side by side over a warp
 // (whole 128-byte rows per access) and a channel's bound is a reduction over
 // the threads of its unit.  Both operators move bytes and little else.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -16,10 +18,12 @@
 namespace ea {
 namespace {
 
-constexpr int kPageThreads = 256;
-// Tokens of a thread (ITEMS): 64 slots over 32 threads of a unit or more up to
-// 128 channels, over 16 or more above.
-constexpr int items_for(int pitch) { return pitch <= 128 ? 2 : 4; }
+// 128 threads: about half of the instructions are the same for a thread of 16
+// values as for one of 64 (256 threads, 32 values each: 24 a value).
+constexpr int kPageThreads = 128;
+// Tokens of a thread: 64 slots over the threads of a unit (16 channels).
+template <int UNITS>
+constexpr int kItems = (64 + kPageThreads / UNITS - 1) / (kPageThreads / UNITS);
 
 // Tokens of a 16-bit [rows, D] block.
 template <bool F16>
@@ -84,12 +88,14 @@ struct CodeSource {
 // Rounding keeps order, so a channel's largest code is the code of its largest
 // value: the bounds cost two comparisons a value (fmaxf and fminf pass NaN
 // over), and codes only meet at the end, four to a word.
-template <int ITEMS, class Src>
+template <int UNITS, class Src>
 __device__ __forceinline__ void write_page(const CacheView& c, int g, int h, bool is_v, int held,
                                            int count, const Src& src) {
   __shared__ uint32_t red[kPageThreads / 32];
   __shared__ __align__(16) uint32_t top[kPageThreads * 4], bottom[kPageThreads * 4];
-  const int units = c.pitch >> 4, tpu = kPageThreads / units;
+  // UNITS 0: any number up to 16
+  constexpr int ITEMS = kItems<UNITS == 0 ? 16 : UNITS>;
+  const int units = UNITS == 0 ? c.pitch >> 4 : UNITS, tpu = kPageThreads / units;
   const int unit = threadIdx.x % units, lane_t = threadIdx.x / units;
   const bool active = lane_t < tpu;
   const int64_t gh = static_cast<int64_t>(g) * c.heads + h;
@@ -146,7 +152,7 @@ __device__ __forceinline__ void write_page(const CacheView& c, int g, int h, boo
   const float fresh = page_scale(__uint_as_float(ua));
   const float s = held > 0 ? fmaxf(was, fresh) : fresh;
   const bool grown = held > 0 && s != was;
-  uint32_t up[4], dn[4];  // ordered codes of the extremes; 0x80 / 0x7f: none
+  uint32_t up[4], dn[4];  // ordered codes of the extremes; where there are none, up < dn
 #pragma unroll
   for (int w = 0; w < 4; ++w) up[w] = 0x80808080u, dn[w] = 0x7f7f7f7fu;
   with_divider(s, [&](auto div) {
@@ -167,15 +173,11 @@ __device__ __forceinline__ void write_page(const CacheView& c, int g, int h, boo
     if (!is_v && active) {
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        uint32_t nan, none = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) none |= hi[4 * w + e] < lo[4 * w + e] ? 0xffu << (8 * e) : 0u;
-        const uint32_t u = e4m3_order4(pack_e4m3x2(div(hi[4 * w]), div(hi[4 * w + 1])) |
-                                       (pack_e4m3x2(div(hi[4 * w + 2]), div(hi[4 * w + 3])) << 16), &nan);
-        const uint32_t d = e4m3_order4(pack_e4m3x2(div(lo[4 * w]), div(lo[4 * w + 1])) |
-                                       (pack_e4m3x2(div(lo[4 * w + 2]), div(lo[4 * w + 3])) << 16), &nan);
-        up[w] = (u & ~none) | (0x80808080u & none);
-        dn[w] = (d & ~none) | (0x7f7f7f7fu & none);
+        uint32_t nan;
+        up[w] = e4m3_order4(pack_e4m3x2(div(hi[4 * w]), div(hi[4 * w + 1])) |
+                            (pack_e4m3x2(div(hi[4 * w + 2]), div(hi[4 * w + 3])) << 16), &nan);
+        dn[w] = e4m3_order4(pack_e4m3x2(div(lo[4 * w]), div(lo[4 * w + 1])) |
+                            (pack_e4m3x2(div(lo[4 * w + 2]), div(lo[4 * w + 3])) << 16), &nan);
       }
     }
   });
@@ -206,38 +208,37 @@ __device__ __forceinline__ void write_page(const CacheView& c, int g, int h, boo
   }
   __syncthreads();  // bounds staged; every thread has read the old scale
   if (threadIdx.x == 0) *scale = s;
-  const int words = c.pitch >> 2;  // of a row of bounds
-  if (!is_v && threadIdx.x < 2 * words) {
-    const bool upper = threadIdx.x < words;
-    const int w = upper ? threadIdx.x : threadIdx.x - words;
-    const uint32_t* from = (upper ? top : bottom) + w;
-    uint32_t o = from[0];
-    for (int t = 1; t < min(tpu, max(count, grown ? held : 0)); ++t)
-      o = upper ? __vmaxs4(o, from[t * words]) : __vmins4(o, from[t * words]);
-    uint32_t* bd = reinterpret_cast<uint32_t*>(c.k_bounds + (gh * 2 + (upper ? 0 : 1)) * c.pitch) + w;
-    const bool keep = held > 0 && !grown;
-    const uint32_t old = keep ? *bd : 0u;
-    uint32_t r = 0;
+  const int words = units * 4;  // of a row of bounds
+  if (!is_v && threadIdx.x < words) {
+    const int w = threadIdx.x;
+    uint32_t u = top[w], d = bottom[w];
+    for (int t = 1; t < min(tpu, max(count, grown ? held : 0)); ++t) {
+      u = __vmaxs4(u, top[t * words + w]);
+      d = __vmins4(d, bottom[t * words + w]);
+    }
+    uint32_t* bu = reinterpret_cast<uint32_t*>(c.k_bounds + gh * 2 * c.pitch) + w;
+    uint32_t* bl = bu + words;
+    const bool keep = held > 0 && !grown;  // the earlier tokens' bounds still hold
+    const uint32_t ou = keep ? *bu : 0u, ol = keep ? *bl : 0u;
+    uint32_t ru = 0, rl = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int x = static_cast<int8_t>(o >> (8 * e)), was_b = static_cast<int8_t>(old >> (8 * e));
-      const bool none = upper ? x == -128 : x == 127;
-      int bnd = none ? 0 : bound_of_order(x, upper);
-      if (keep) bnd = none ? was_b : upper ? max(bnd, was_b) : min(bnd, was_b);
-      r |= (static_cast<uint32_t>(bnd) & 0xffu) << (8 * e);
+      const int x = static_cast<int8_t>(u >> (8 * e)), y = static_cast<int8_t>(d >> (8 * e));
+      const int xo = static_cast<int8_t>(ou >> (8 * e)), yo = static_cast<int8_t>(ol >> (8 * e));
+      const bool none = x < y;
+      int b1 = none ? 0 : bound_of_order(x, true), b0 = none ? 0 : bound_of_order(y, false);
+      if (keep) b1 = none ? xo : max(b1, xo), b0 = none ? yo : min(b0, yo);
+      ru |= (static_cast<uint32_t>(b1) & 0xffu) << (8 * e);
+      rl |= (static_cast<uint32_t>(b0) & 0xffu) << (8 * e);
     }
-    *bd = r;
+    *bu = ru, *bl = rl;
   }
 }
 
-template <bool F16, int ITEMS>
-__global__ void __launch_bounds__(kPageThreads, ITEMS == 2 ? 3 : 2) cache_append_kernel(const CacheAppendParams p) {
-  int x = blockIdx.x;
-  const bool is_v = x & 1;
-  x >>= 1;
-  const int j = x % p.pages_per_seq;
-  x /= p.pages_per_seq;
-  const int h = x % p.c.heads, b = x / p.c.heads;
+template <bool F16, int UNITS>
+__global__ void __launch_bounds__(kPageThreads) cache_append_kernel(const CacheAppendParams p) {
+  const bool is_v = blockIdx.x & 1;
+  const int j = blockIdx.x >> 1, h = blockIdx.y, b = blockIdx.z;
   int len, n;
   if (!load_seq(p.s, p.c, b, threadIdx.x == 0, &len, &n) || n == 0) return;
   const int start = len - n, i = (start >> p.c.log2_page) + j, base = i << p.c.log2_page;
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kPageThreads, ITEMS == 2 ? 3 : 2) cache_append
   const int from = max(base, start), to = min(base + p.c.page, len);
   const int64_t row = (static_cast<int64_t>(b) * p.c.heads + h) * p.s.T + (from - start);
   const RowSource<F16> src{(is_v ? p.v : p.k) + row * p.c.D, p.c.D};
-  write_page<ITEMS>(p.c, g, h, is_v, from - base, to - from, src);
+  write_page<UNITS>(p.c, g, h, is_v, from - base, to - from, src);
 }
 
 // ---------------------------------------------------------------- evict
@@ -328,32 +329,39 @@ __global__ void __launch_bounds__(kPlanThreads) cache_evict_plan_kernel(const Ca
     out[j] = 0.f;
 }
 
-template <int ITEMS>
-__global__ void __launch_bounds__(kPageThreads, ITEMS == 2 ? 4 : 2)
-    cache_evict_move_kernel(const CacheEvictParams p, int pages_per_seq) {
-  int x = blockIdx.x;
-  const bool is_v = x & 1;
-  x >>= 1;
-  const int i = x % pages_per_seq;
-  x /= pages_per_seq;
-  const int h = x % p.c.heads, b = x / p.c.heads;
+template <int UNITS>
+__global__ void __launch_bounds__(kPageThreads) cache_evict_move_kernel(const CacheEvictParams p) {
+  const bool is_v = blockIdx.x & 1;
+  const int i = blockIdx.x >> 1, h = blockIdx.y, b = blockIdx.z;
   const int left = p.new_lens[b], base = i << p.c.log2_page;
   if (base >= left) return;
   const int g = p.dst_page[static_cast<int64_t>(b) * p.dst_width + i];
   if (g < 0) return;
   const CodeSource src{p.c, p.s, is_v ? p.c.v : p.c.k, is_v ? p.c.v_scale : p.c.k_scale,
                        p.kept + (static_cast<int64_t>(b) * p.c.heads + h) * p.keep + base, b, h};
-  write_page<ITEMS>(p.c, g, h, is_v, 0, min(p.c.page, left - base), src);
+  write_page<UNITS>(p.c, g, h, is_v, 0, min(p.c.page, left - base), src);
+}
+
+// The kernels know the units of 64, 128 and 256 channels at compile time.
+template <class Launch>
+void by_units(const CacheView& c, Launch launch) {
+  switch (c.pitch >> 4) {
+    case 4: return launch(std::integral_constant<int, 4>());
+    case 8: return launch(std::integral_constant<int, 8>());
+    case 16: return launch(std::integral_constant<int, 16>());
+  }
+  launch(std::integral_constant<int, 0>());
 }
 
 }  // namespace
 
 cudaError_t cache_append_launch(const CacheAppendParams& p, bool f16, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(2ll * p.pages_per_seq * p.c.heads * p.s.batch);
-  const bool two = items_for(p.c.pitch) == 2;
-  auto kern = f16 ? (two ? cache_append_kernel<true, 2> : cache_append_kernel<true, 4>)
-                  : (two ? cache_append_kernel<false, 2> : cache_append_kernel<false, 4>);
-  kern<<<grid, kPageThreads, 0, stream>>>(p);
+  const dim3 grid(2u * p.pages_per_seq, p.c.heads, p.s.batch);
+  by_units(p.c, [&](auto u) {
+    constexpr int UNITS = decltype(u)::value;
+    if (f16) cache_append_kernel<true, UNITS><<<grid, kPageThreads, 0, stream>>>(p);
+    else cache_append_kernel<false, UNITS><<<grid, kPageThreads, 0, stream>>>(p);
+  });
   return cudaGetLastError();
 }
 
@@ -361,10 +369,10 @@ cudaError_t cache_evict_launch(const CacheEvictParams& p, cudaStream_t stream) {
   cache_evict_plan_kernel<<<dim3(p.c.heads, p.s.batch + 1), kPlanThreads, 0, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int pages_per_seq = (p.keep + p.c.page - 1) >> p.c.log2_page;
-  const unsigned grid = static_cast<unsigned>(2ll * pages_per_seq * p.c.heads * p.s.batch);
-  auto kern = items_for(p.c.pitch) == 2 ? cache_evict_move_kernel<2> : cache_evict_move_kernel<4>;
-  kern<<<grid, kPageThreads, 0, stream>>>(p, pages_per_seq);
+  const dim3 grid(2u * ((p.keep + p.c.page - 1) >> p.c.log2_page), p.c.heads, p.s.batch);
+  by_units(p.c, [&](auto u) {
+    cache_evict_move_kernel<decltype(u)::value><<<grid, kPageThreads, 0, stream>>>(p);
+  });
   return cudaGetLastError();
 }
 
