@@ -100,13 +100,30 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a < INFINITY ? a : 0.f;
 }
 
-// e4m3 codes as signed bytes in the order of their values (4 at a time), and
-// the mask of NaN codes.
-__device__ __forceinline__ uint32_t e4m3_order4(uint32_t w, uint32_t* nan) {
-  const uint32_t m = w & 0x7f7f7f7fu;
-  const uint32_t neg = ((w >> 7) & 0x01010101u) * 0xffu;
-  *nan = __vcmpeq4(m, 0x7f7f7f7fu);
-  return __vsub4(m ^ neg, neg);
+// Larger and smaller of two pairs of 16-bit values; a NaN loses.
+template <bool F16>
+__device__ __forceinline__ uint32_t max_x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (F16) asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t min_x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (F16) asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// e4m3 codes as unsigned bytes in the order of their values, four at a time:
+// negative codes inverted, the others above them.
+__device__ __forceinline__ uint32_t e4m3_order4(uint32_t w) {
+  return w ^ (((w >> 7) & 0x01010101u) * 0xffu | 0x80808080u);
+}
+// 0xff in the bytes that hold NaN codes.
+__device__ __forceinline__ uint32_t e4m3_nan4(uint32_t w) {
+  return ((((w & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u) * 0xffu;
 }
 
 // The int8 bound of one ordered code: the value in steps of 448/127, rounded
@@ -114,8 +131,8 @@ __device__ __forceinline__ uint32_t e4m3_order4(uint32_t w, uint32_t* nan) {
 // 2^6·7 and 127 share no factor, a code's significand has 4 bits); at the others
 // a product's rounding, 2^-23 of it, is far from carrying over a whole number,
 // and ±448 is clamped to ±127.
-__device__ __forceinline__ int bound_of_order(int o, bool upper) {
-  const uint32_t code = o < 0 ? (0x80u | static_cast<uint32_t>(-o)) : static_cast<uint32_t>(o);
+__device__ __forceinline__ int bound_of_order(uint32_t o, bool upper) {
+  const uint32_t code = o & 0x80u ? o ^ 0x80u : ~o & 0xffu;
   const float y = half2_bits_to_float2(e4m3x2_to_f16x2(code)).x * (127.f / kE4M3Max);
   const int r = static_cast<int>(upper ? ceilf(y) : floorf(y));
   return max(-127, min(127, r));

@@ -25,166 +25,156 @@ constexpr int kPageThreads = 128;
 template <int UNITS>
 constexpr int kItems = (64 + kPageThreads / UNITS - 1) / (kPageThreads / UNITS);
 
-// Tokens of a 16-bit [rows, D] block.
-template <bool F16>
-struct RowSource {
-  struct Raw {
-    uint4 a, b;
-  };
-  const uint16_t* rows;  // the page's first new token
-  int D;
-  __device__ __forceinline__ Raw load(int t, int unit) const {
-    const uint16_t* r = rows + static_cast<int64_t>(t) * D + unit * 16;
-    Raw x;
-    x.a = __ldg(reinterpret_cast<const uint4*>(r));
-    x.b = unit * 16 + 8 < D ? __ldg(reinterpret_cast<const uint4*>(r + 8)) : make_uint4(0, 0, 0, 0);
-    return x;
-  }
-  static __device__ __forceinline__ float2 pair(const Raw& x, int i) {
-    const uint32_t w = i == 0 ? x.a.x : i == 1 ? x.a.y : i == 2 ? x.a.z : i == 3 ? x.a.w
-                     : i == 4 ? x.b.x : i == 5 ? x.b.y : i == 6 ? x.b.z : x.b.w;
-    return pair_to_float2<F16>(w);
+// A thread's part of a page: one unit of 16 channels and every tpu-th token.
+// UNITS 0: any number up to 16.
+template <int UNITS>
+struct Share {
+  static constexpr int kMine = kItems<UNITS == 0 ? 16 : UNITS>;
+  int units, tpu, unit, first;
+  bool active;
+  __device__ __forceinline__ explicit Share(int pitch) {
+    units = UNITS == 0 ? pitch >> 4 : UNITS;
+    tpu = kPageThreads / units;
+    unit = threadIdx.x % units;
+    first = threadIdx.x / units;
+    active = first < tpu;
   }
 };
 
-// Tokens picked out of the cache's pages.
-struct CodeSource {
-  struct Raw {
-    uint4 w;
-    float s;
-  };
-  const CacheView& c;
-  const SeqView& s;
-  const uint8_t* codes;
-  const float* scales;
-  const int* kept;  // positions of the page's tokens
-  int b, h;
-  __device__ __forceinline__ Raw load(int t, int unit) const {
-    const int j = kept[t];
-    const int g = j >= 0 && j < (s.width << c.log2_page)
-                      ? load_page(s, c, b, j >> c.log2_page, true) : -1;
-    Raw x;
-    x.w = make_uint4(0, 0, 0, 0);
-    x.s = 0.f;
-    if (g >= 0) {
-      const int64_t gh = static_cast<int64_t>(g) * c.heads + h;
-      x.w = __ldg(reinterpret_cast<const uint4*>(
-          codes + ((gh << c.log2_page) + (j & (c.page - 1))) * c.pitch + unit * 16));
-      if (unit * 16 + 8 >= c.D) x.w.z = x.w.w = 0;  // padding channels
-      x.s = __ldg(scales + gh);
-    }
-    return x;
-  }
-  static __device__ __forceinline__ float2 pair(const Raw& x, int i) {
-    const uint32_t w = i < 2 ? x.w.x : i < 4 ? x.w.y : i < 6 ? x.w.z : x.w.w;
-    const float2 v = half2_bits_to_float2(e4m3x2_to_f16x2((i & 1) ? w >> 16 : w & 0xffffu));
-    return make_float2(v.x * x.s, v.y * x.s);
-  }
-};
-
-// Writes `count` tokens from `src` to slots held .. held+count-1 of page g,
-// head h; slots below `held` hold earlier tokens, which stay.
-//
-// Rounding keeps order, so a channel's largest code is the code of its largest
-// value: the bounds cost two comparisons a value (fmaxf and fminf pass NaN
-// over), and codes only meet at the end, four to a word.
-template <int UNITS, class Src>
-__device__ __forceinline__ void write_page(const CacheView& c, int g, int h, bool is_v, int held,
-                                           int count, const Src& src) {
+// Largest of a non-negative value over the CTA.
+__device__ __forceinline__ float block_max(float a) {
   __shared__ uint32_t red[kPageThreads / 32];
-  __shared__ __align__(16) uint32_t top[kPageThreads * 4], bottom[kPageThreads * 4];
-  // UNITS 0: any number up to 16
-  constexpr int ITEMS = kItems<UNITS == 0 ? 16 : UNITS>;
-  const int units = UNITS == 0 ? c.pitch >> 4 : UNITS, tpu = kPageThreads / units;
-  const int unit = threadIdx.x % units, lane_t = threadIdx.x / units;
-  const bool active = lane_t < tpu;
-  const int64_t gh = static_cast<int64_t>(g) * c.heads + h;
-  uint8_t* rows = (is_v ? c.v : c.k) + (gh << c.log2_page) * c.pitch + unit * 16;
-  float* scale = (is_v ? c.v_scale : c.k_scale) + gh;
-  const float was = held > 0 ? *scale : 0.f;
-
-  typename Src::Raw raw[ITEMS];
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i)
-    if (active && lane_t + i * tpu < count) raw[i] = src.load(lane_t + i * tpu, unit);
-  float hi[16], lo[16], a = 0.f;  // k: the thread's channels' extremes; v: the largest |x|
-  if (!is_v) {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) hi[e] = -INFINITY, lo[e] = INFINITY;
-  }
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    if (active && lane_t + i * tpu < count) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float2 x = Src::pair(raw[i], e);
-        if (is_v) {
-          a = fmaxf(a, fmaxf(fabsf(x.x), fabsf(x.y)));
-        } else {
-          hi[2 * e] = fmaxf(hi[2 * e], x.x), lo[2 * e] = fminf(lo[2 * e], x.x);
-          hi[2 * e + 1] = fmaxf(hi[2 * e + 1], x.y), lo[2 * e + 1] = fminf(lo[2 * e + 1], x.y);
-        }
-      }
-    }
-  }
-  if (!is_v) {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) a = fmaxf(a, fmaxf(hi[e], -lo[e]));
-  }
-  if (a == INFINITY) {  // infinities do not count: once more without them
-    a = 0.f;
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i)
-      if (active && lane_t + i * tpu < count)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 x = Src::pair(raw[i], e);
-          a = fmaxf(a, fmaxf(finite_abs(x.x), finite_abs(x.y)));
-        }
-  }
   // non-negative floats order as their bits
   const uint32_t wa = __reduce_max_sync(0xffffffffu, __float_as_uint(a));
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = wa;
   __syncthreads();
-  uint32_t ua = red[0];
+  uint32_t m = red[0];
 #pragma unroll
-  for (int w = 1; w < kPageThreads / 32; ++w) ua = max(ua, red[w]);
-  const float fresh = page_scale(__uint_as_float(ua));
+  for (int w = 1; w < kPageThreads / 32; ++w) m = max(m, red[w]);
+  return __uint_as_float(m);
+}
+
+// Writes a page's bounds from every thread's extremes (ordered codes of its 16
+// channels; up < dn: none).  Token rows from `lanes` on hold none.  keep: the
+// bounds there hold for the page's earlier tokens and are widened.
+template <int UNITS>
+__device__ __forceinline__ void write_bounds(const CacheView& c, const Share<UNITS>& sh, int64_t gh, int lanes,
+                                             bool keep, const uint32_t (&up)[4], const uint32_t (&dn)[4]) {
+  __shared__ __align__(16) uint32_t top[kPageThreads * 4], bottom[kPageThreads * 4];
+  if (sh.active) {
+    reinterpret_cast<uint4*>(top)[sh.first * sh.units + sh.unit] = make_uint4(up[0], up[1], up[2], up[3]);
+    reinterpret_cast<uint4*>(bottom)[sh.first * sh.units + sh.unit] = make_uint4(dn[0], dn[1], dn[2], dn[3]);
+  }
+  __syncthreads();
+  const int words = sh.units * 4, w = threadIdx.x;  // words of a row of bounds
+  if (w >= words) return;
+  uint32_t u = top[w], d = bottom[w];
+  for (int t = 1; t < min(sh.tpu, lanes); ++t) {
+    u = __vmaxu4(u, top[t * words + w]);
+    d = __vminu4(d, bottom[t * words + w]);
+  }
+  uint32_t* bu = reinterpret_cast<uint32_t*>(c.k_bounds + gh * 2 * c.pitch) + w;
+  uint32_t* bl = bu + words;
+  const uint32_t ou = keep ? *bu : 0u, ol = keep ? *bl : 0u;
+  uint32_t ru = 0, rl = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t x = (u >> (8 * e)) & 0xffu, y = (d >> (8 * e)) & 0xffu;
+    const int xo = static_cast<int8_t>(ou >> (8 * e)), yo = static_cast<int8_t>(ol >> (8 * e));
+    const bool none = x < y;
+    int b1 = none ? 0 : bound_of_order(x, true), b0 = none ? 0 : bound_of_order(y, false);
+    if (keep) b1 = none ? xo : max(b1, xo), b0 = none ? yo : min(b0, yo);
+    ru |= (static_cast<uint32_t>(b1) & 0xffu) << (8 * e);
+    rl |= (static_cast<uint32_t>(b0) & 0xffu) << (8 * e);
+  }
+  *bu = ru, *bl = rl;
+}
+
+// Appends `count` tokens, rows of D 16-bit values, to page g of head h, at
+// slots held, held + 1, ...; the slots below hold earlier tokens, which stay.
+//
+// Rounding keeps order, so a channel's largest code is the code of its largest
+// value: the bounds cost a packed maximum and minimum for two values, and codes
+// only meet at the end, four to a word.
+template <bool F16, int UNITS>
+__device__ __forceinline__ void append_page(const CacheView& c, int g, int h, bool is_v, int held, int count,
+                                            const uint16_t* src) {
+  const Share<UNITS> sh(c.pitch);
+  const int64_t gh = static_cast<int64_t>(g) * c.heads + h;
+  uint8_t* rows = (is_v ? c.v : c.k) + (gh << c.log2_page) * c.pitch + sh.unit * 16;
+  float* scale = (is_v ? c.v_scale : c.k_scale) + gh;
+  const float was = held > 0 ? *scale : 0.f;
+
+  uint32_t x[Share<UNITS>::kMine][8];
+#pragma unroll
+  for (int i = 0; i < Share<UNITS>::kMine; ++i) {
+    const int t = sh.first + i * sh.tpu;
+    if (sh.active && t < count) {
+      const uint16_t* r = src + static_cast<int64_t>(t) * c.D + sh.unit * 16;
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(r));
+      const uint4 b = sh.unit * 16 + 8 < c.D ? __ldg(reinterpret_cast<const uint4*>(r + 8)) : make_uint4(0, 0, 0, 0);
+      x[i][0] = a.x, x[i][1] = a.y, x[i][2] = a.z, x[i][3] = a.w;
+      x[i][4] = b.x, x[i][5] = b.y, x[i][6] = b.z, x[i][7] = b.w;
+    }
+  }
+  constexpr uint32_t kInf = F16 ? 0x7c007c00u : 0x7f807f80u, kAbs = 0x7fff7fffu;
+  uint32_t hi[8], lo[8], a2 = 0;  // k: the channels' extremes; a2: the largest |x|
+#pragma unroll
+  for (int e = 0; e < 8; ++e) hi[e] = kInf | ~kAbs, lo[e] = kInf;
+#pragma unroll
+  for (int i = 0; i < Share<UNITS>::kMine; ++i)
+    if (sh.active && sh.first + i * sh.tpu < count)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (is_v) a2 = max_x2<F16>(a2, x[i][e] & kAbs);
+        else hi[e] = max_x2<F16>(hi[e], x[i][e]), lo[e] = min_x2<F16>(lo[e], x[i][e]);
+      }
+  if (!is_v) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a2 = max_x2<F16>(a2, max_x2<F16>(hi[e], lo[e] ^ ~kAbs));
+  }
+  const float2 af = pair_to_float2<F16>(a2);
+  float a = fmaxf(af.x, af.y);
+  if (a == INFINITY) {  // infinities do not count: once more without them
+    a = 0.f;
+#pragma unroll
+    for (int i = 0; i < Share<UNITS>::kMine; ++i)
+      if (sh.active && sh.first + i * sh.tpu < count)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 v = pair_to_float2<F16>(x[i][e]);
+          a = fmaxf(a, fmaxf(finite_abs(v.x), finite_abs(v.y)));
+        }
+  }
+  const float fresh = page_scale(block_max(a));
   const float s = held > 0 ? fmaxf(was, fresh) : fresh;
   const bool grown = held > 0 && s != was;
-  uint32_t up[4], dn[4];  // ordered codes of the extremes; where there are none, up < dn
-#pragma unroll
-  for (int w = 0; w < 4; ++w) up[w] = 0x80808080u, dn[w] = 0x7f7f7f7fu;
+  if (threadIdx.x == 0) *scale = s;  // the old one has been read: block_max is a barrier
+
+  uint32_t up[4], dn[4];
   with_divider(s, [&](auto div) {
+    auto codes = [&](uint32_t w0, uint32_t w1) {
+      const float2 v0 = pair_to_float2<F16>(w0), v1 = pair_to_float2<F16>(w1);
+      return pack_e4m3x2(div(v0.x), div(v0.y)) | (pack_e4m3x2(div(v1.x), div(v1.y)) << 16);
+    };
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const int t = lane_t + i * tpu;
-      if (active && t < count) {
-        uint32_t q[4];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const float2 x = Src::pair(raw[i], 2 * w), y = Src::pair(raw[i], 2 * w + 1);
-          q[w] = pack_e4m3x2(div(x.x), div(x.y)) | (pack_e4m3x2(div(y.x), div(y.y)) << 16);
-        }
+    for (int i = 0; i < Share<UNITS>::kMine; ++i) {
+      const int t = sh.first + i * sh.tpu;
+      if (sh.active && t < count)
         *reinterpret_cast<uint4*>(rows + static_cast<int64_t>(held + t) * c.pitch) =
-            make_uint4(q[0], q[1], q[2], q[3]);
-      }
+            make_uint4(codes(x[i][0], x[i][1]), codes(x[i][2], x[i][3]), codes(x[i][4], x[i][5]),
+                       codes(x[i][6], x[i][7]));
     }
-    if (!is_v && active) {
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint32_t nan;
-        up[w] = e4m3_order4(pack_e4m3x2(div(hi[4 * w]), div(hi[4 * w + 1])) |
-                            (pack_e4m3x2(div(hi[4 * w + 2]), div(hi[4 * w + 3])) << 16), &nan);
-        dn[w] = e4m3_order4(pack_e4m3x2(div(lo[4 * w]), div(lo[4 * w + 1])) |
-                            (pack_e4m3x2(div(lo[4 * w + 2]), div(lo[4 * w + 3])) << 16), &nan);
-      }
+    for (int w = 0; w < 4; ++w) {
+      up[w] = e4m3_order4(codes(hi[2 * w], hi[2 * w + 1]));
+      dn[w] = e4m3_order4(codes(lo[2 * w], lo[2 * w + 1]));
     }
   });
   if (grown) {
     // the earlier codes move to the larger scale
     const float ratio = __fdiv_rn(was, s);
-    for (int t = lane_t; active && t < held; t += tpu) {
+    for (int t = sh.first; sh.active && t < held; t += sh.tpu) {
       uint4* at = reinterpret_cast<uint4*>(rows + static_cast<int64_t>(t) * c.pitch);
       const uint4 old = *at;
       uint32_t q[4] = {old.x, old.y, old.z, old.w};
@@ -192,46 +182,105 @@ __device__ __forceinline__ void write_page(const CacheView& c, int g, int h, boo
       for (int w = 0; w < 4; ++w) {
         uint32_t h0, h1;
         e4m3x4_to_f16(q[w], &h0, &h1);
-        const float2 x = half2_bits_to_float2(h0), y = half2_bits_to_float2(h1);
-        q[w] = pack_e4m3x2(x.x * ratio, x.y * ratio) | (pack_e4m3x2(y.x * ratio, y.y * ratio) << 16);
-        uint32_t nan;
-        const uint32_t o = e4m3_order4(q[w], &nan);
-        up[w] = __vmaxs4(up[w], (o & ~nan) | (0x80808080u & nan));
-        dn[w] = __vmins4(dn[w], (o & ~nan) | (0x7f7f7f7fu & nan));
+        const float2 v0 = half2_bits_to_float2(h0), v1 = half2_bits_to_float2(h1);
+        q[w] = pack_e4m3x2(v0.x * ratio, v0.y * ratio) | (pack_e4m3x2(v1.x * ratio, v1.y * ratio) << 16);
+        const uint32_t o = e4m3_order4(q[w]), nan = e4m3_nan4(q[w]);
+        up[w] = __vmaxu4(up[w], o & ~nan);
+        dn[w] = __vminu4(dn[w], o | nan);
       }
       *at = make_uint4(q[0], q[1], q[2], q[3]);
     }
   }
-  if (!is_v && active) {
-    reinterpret_cast<uint4*>(top)[lane_t * units + unit] = make_uint4(up[0], up[1], up[2], up[3]);
-    reinterpret_cast<uint4*>(bottom)[lane_t * units + unit] = make_uint4(dn[0], dn[1], dn[2], dn[3]);
+  if (!is_v) write_bounds(c, sh, gh, max(count, grown ? held : 0), held > 0 && !grown, up, dn);
+}
+
+// Fills page g of head h with `count` tokens of sequence b, picked out of its
+// pages: those at positions kept[0], kept[1], ...
+//
+// Codes whose page has the new page's scale, most of them, are moved as they
+// are.  The largest |code| of a token and the bounds are found among the codes.
+template <int UNITS>
+__device__ __forceinline__ void move_page(const CacheView& c, const SeqView& sq, int b, int g, int h, bool is_v,
+                                          int count, const int* kept) {
+  __shared__ int64_t where[64];  // byte offset of a token's row, -1: none
+  __shared__ float scales[64];
+  const uint8_t* codes = is_v ? c.v : c.k;
+  if (threadIdx.x < 64) {
+    const int t = threadIdx.x, j = t < count ? kept[t] : -1;
+    const int from = j >= 0 && j < (sq.width << c.log2_page) ? load_page(sq, c, b, j >> c.log2_page, true) : -1;
+    const int64_t fh = static_cast<int64_t>(from) * c.heads + h;
+    where[t] = from < 0 ? -1 : ((fh << c.log2_page) + (j & (c.page - 1))) * c.pitch;
+    scales[t] = from < 0 ? 0.f : (is_v ? c.v_scale : c.k_scale)[fh];
   }
-  __syncthreads();  // bounds staged; every thread has read the old scale
-  if (threadIdx.x == 0) *scale = s;
-  const int words = units * 4;  // of a row of bounds
-  if (!is_v && threadIdx.x < words) {
-    const int w = threadIdx.x;
-    uint32_t u = top[w], d = bottom[w];
-    for (int t = 1; t < min(tpu, max(count, grown ? held : 0)); ++t) {
-      u = __vmaxs4(u, top[t * words + w]);
-      d = __vmins4(d, bottom[t * words + w]);
-    }
-    uint32_t* bu = reinterpret_cast<uint32_t*>(c.k_bounds + gh * 2 * c.pitch) + w;
-    uint32_t* bl = bu + words;
-    const bool keep = held > 0 && !grown;  // the earlier tokens' bounds still hold
-    const uint32_t ou = keep ? *bu : 0u, ol = keep ? *bl : 0u;
-    uint32_t ru = 0, rl = 0;
+  __syncthreads();
+  const Share<UNITS> sh(c.pitch);
+  const int64_t gh = static_cast<int64_t>(g) * c.heads + h;
+  const bool half = sh.unit * 16 + 8 >= c.D;  // the unit ends in padding channels
+
+  uint32_t x[Share<UNITS>::kMine][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int x = static_cast<int8_t>(u >> (8 * e)), y = static_cast<int8_t>(d >> (8 * e));
-      const int xo = static_cast<int8_t>(ou >> (8 * e)), yo = static_cast<int8_t>(ol >> (8 * e));
-      const bool none = x < y;
-      int b1 = none ? 0 : bound_of_order(x, true), b0 = none ? 0 : bound_of_order(y, false);
-      if (keep) b1 = none ? xo : max(b1, xo), b0 = none ? yo : min(b0, yo);
-      ru |= (static_cast<uint32_t>(b1) & 0xffu) << (8 * e);
-      rl |= (static_cast<uint32_t>(b0) & 0xffu) << (8 * e);
+  for (int i = 0; i < Share<UNITS>::kMine; ++i) {
+    const int t = sh.first + i * sh.tpu;
+    if (sh.active && t < count) {
+      const int64_t at = where[t];
+      const uint4 w = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(codes + at + sh.unit * 16)) : make_uint4(0, 0, 0, 0);
+      x[i][0] = w.x, x[i][1] = w.y, x[i][2] = half ? 0u : w.z, x[i][3] = half ? 0u : w.w;
     }
-    *bu = ru, *bl = rl;
+  }
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < Share<UNITS>::kMine; ++i) {
+    const int t = sh.first + i * sh.tpu;
+    if (sh.active && t < count) {
+      uint32_t m = 0;  // largest |code| of the even and of the odd bytes
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t v = x[i][w] & 0x7f7f7f7fu & ~e4m3_nan4(x[i][w]);
+        m = __vmaxu2(m, __vmaxu2(v & 0x00ff00ffu, (v >> 8) & 0x00ff00ffu));
+      }
+      m = max(m & 0xffffu, m >> 16);
+      a = fmaxf(a, finite_abs(half2_bits_to_float2(e4m3x2_to_f16x2(m)).x * scales[t]));
+    }
+  }
+  const float s = page_scale(block_max(a));
+  if (threadIdx.x == 0) (is_v ? c.v_scale : c.k_scale)[gh] = s;
+  const float inv = 1.f / s;  // a power of two, at least 2^-120
+  uint8_t* rows = (is_v ? c.v : c.k) + (gh << c.log2_page) * c.pitch + sh.unit * 16;
+  uint32_t ue[4], uo[4], de[4], dd[4];  // extremes of the even and of the odd bytes, 16 bits each
+#pragma unroll
+  for (int w = 0; w < 4; ++w) ue[w] = uo[w] = 0u, de[w] = dd[w] = 0x00ff00ffu;
+#pragma unroll
+  for (int i = 0; i < Share<UNITS>::kMine; ++i) {
+    const int t = sh.first + i * sh.tpu;
+    if (sh.active && t < count) {
+      const float f = scales[t] * inv;
+      if (f != 1.f) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t h0, h1;
+          e4m3x4_to_f16(x[i][w], &h0, &h1);
+          const float2 v0 = half2_bits_to_float2(h0), v1 = half2_bits_to_float2(h1);
+          x[i][w] = pack_e4m3x2(v0.x * f, v0.y * f) | (pack_e4m3x2(v1.x * f, v1.y * f) << 16);
+        }
+      }
+      *reinterpret_cast<uint4*>(rows + static_cast<int64_t>(t) * c.pitch) =
+          make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
+      if (!is_v) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t o = e4m3_order4(x[i][w]), nan = e4m3_nan4(x[i][w]);
+          const uint32_t hi = o & ~nan, lo = o | nan;
+          ue[w] = __vmaxu2(ue[w], hi & 0x00ff00ffu), uo[w] = __vmaxu2(uo[w], (hi >> 8) & 0x00ff00ffu);
+          de[w] = __vminu2(de[w], lo & 0x00ff00ffu), dd[w] = __vminu2(dd[w], (lo >> 8) & 0x00ff00ffu);
+        }
+      }
+    }
+  }
+  if (!is_v) {
+    uint32_t up[4], dn[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) up[w] = ue[w] | (uo[w] << 8), dn[w] = de[w] | (dd[w] << 8);
+    write_bounds(c, sh, gh, count, false, up, dn);
   }
 }
 
@@ -247,8 +296,7 @@ __global__ void __launch_bounds__(kPageThreads) cache_append_kernel(const CacheA
   if (g < 0) return;
   const int from = max(base, start), to = min(base + p.c.page, len);
   const int64_t row = (static_cast<int64_t>(b) * p.c.heads + h) * p.s.T + (from - start);
-  const RowSource<F16> src{(is_v ? p.v : p.k) + row * p.c.D, p.c.D};
-  write_page<UNITS>(p.c, g, h, is_v, from - base, to - from, src);
+  append_page<F16, UNITS>(p.c, g, h, is_v, from - base, to - from, (is_v ? p.v : p.k) + row * p.c.D);
 }
 
 // ---------------------------------------------------------------- evict
@@ -337,9 +385,8 @@ __global__ void __launch_bounds__(kPageThreads) cache_evict_move_kernel(const Ca
   if (base >= left) return;
   const int g = p.dst_page[static_cast<int64_t>(b) * p.dst_width + i];
   if (g < 0) return;
-  const CodeSource src{p.c, p.s, is_v ? p.c.v : p.c.k, is_v ? p.c.v_scale : p.c.k_scale,
-                       p.kept + (static_cast<int64_t>(b) * p.c.heads + h) * p.keep + base, b, h};
-  write_page<UNITS>(p.c, g, h, is_v, 0, min(p.c.page, left - base), src);
+  move_page<UNITS>(p.c, p.s, b, g, h, is_v, min(p.c.page, left - base),
+                   p.kept + (static_cast<int64_t>(b) * p.c.heads + h) * p.keep + base);
 }
 
 // The kernels know the units of 64, 128 and 256 channels at compile time.
