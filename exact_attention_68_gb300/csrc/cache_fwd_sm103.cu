@@ -147,15 +147,6 @@ __device__ __forceinline__ bool wait_copy(uint32_t bar, uint32_t parity, const W
   return wait_bounded(bar, parity, ctl, site);
 }
 
-// Programmatic dependent launch: the next kernel of the stream may be set up
-// once every CTA has said so or ended; its wait ends when this grid has.
-__device__ __forceinline__ void launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_for_previous() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // Over the eight lanes that hold the same query rows.
 __device__ __forceinline__ float keys_max(float x) {
   x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
@@ -974,21 +965,6 @@ __global__ void __launch_bounds__(kMassThreads) cache_mass_kernel(const __grid_c
   if (mine) p.mass[bh * (static_cast<int64_t>(p.s.width) << p.c.log2_page) + pos] += sum;
 }
 
-// A launch that may be set up before the stream's previous kernel has ended.
-template <class Kernel>
-cudaError_t launch_after(Kernel kern, dim3 grid, int threads, const CacheFwdParams& p, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
-}
-
 template <int WIDTH, int WORKER, int NT>
 cudaError_t launch_fwd(const CacheFwdParams& p, int dev, int ctas, cudaStream_t stream) {
   using L = CacheFwdLayout<WIDTH, WORKER, NT>;
@@ -1005,10 +981,10 @@ cudaError_t launch_fwd(const CacheFwdParams& p, int dev, int ctas, cudaStream_t 
   if (e != cudaSuccess) return e;
   if (!p.by_segment)
     e = launch_after(cache_join_kernel<WIDTH, NT>, dim3(p.s.batch * p.c.heads * p.row_tiles, WIDTH / 32),
-                     kJoinThreads * NT, p, stream);
+                     kJoinThreads * NT, stream, p);
   if (e != cudaSuccess || p.mass == nullptr) return e;
   return launch_after(cache_mass_kernel, dim3((p.score_cols + kMassThreads - 1) / kMassThreads, p.c.heads, p.s.batch),
-                      kMassThreads, p, stream);
+                      kMassThreads, stream, p);
 }
 
 template <int WIDTH>

@@ -227,18 +227,30 @@ __device__ __forceinline__ void move_page(const CacheView& c, const SeqView& sq,
       x[i][0] = w.x, x[i][1] = w.y, x[i][2] = half ? 0u : w.z, x[i][3] = half ? 0u : w.w;
     }
   }
+  constexpr uint32_t kEven = 0x00ff00ffu, kOdd = 0xff00ff00u;  // bytes, two to a 16-bit comparison each
   float a = 0.f;
+  bool nan = false;
 #pragma unroll
   for (int i = 0; i < Share<UNITS>::kMine; ++i) {
     const int t = sh.first + i * sh.tpu;
     if (sh.active && t < count) {
-      uint32_t m = 0;  // largest |code| of the even and of the odd bytes
+      uint32_t me = 0, mo = 0, top = 0;  // largest |code| of the even and of the odd bytes
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const uint32_t v = x[i][w] & 0x7f7f7f7fu & ~e4m3_nan4(x[i][w]);
-        m = __vmaxu2(m, __vmaxu2(v & 0x00ff00ffu, (v >> 8) & 0x00ff00ffu));
+        const uint32_t v = x[i][w] & 0x7f7f7f7fu;
+        top |= v + 0x01010101u;
+        me = __vmaxu2(me, v & kEven), mo = __vmaxu2(mo, v & kOdd);
       }
-      m = max(m & 0xffffu, m >> 16);
+      if (top & 0x80808080u) {  // some are NaN, which do not count
+        nan = true;
+        me = mo = 0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t v = x[i][w] & 0x7f7f7f7fu & ~e4m3_nan4(x[i][w]);
+          me = __vmaxu2(me, v & kEven), mo = __vmaxu2(mo, v & kOdd);
+        }
+      }
+      const uint32_t m = max(max(me & 0xffu, me >> 16), max((mo >> 8) & 0xffu, mo >> 24));
       a = fmaxf(a, finite_abs(half2_bits_to_float2(e4m3x2_to_f16x2(m)).x * scales[t]));
     }
   }
@@ -246,9 +258,9 @@ __device__ __forceinline__ void move_page(const CacheView& c, const SeqView& sq,
   if (threadIdx.x == 0) (is_v ? c.v_scale : c.k_scale)[gh] = s;
   const float inv = 1.f / s;  // a power of two, at least 2^-120
   uint8_t* rows = (is_v ? c.v : c.k) + (gh << c.log2_page) * c.pitch + sh.unit * 16;
-  uint32_t ue[4], uo[4], de[4], dd[4];  // extremes of the even and of the odd bytes, 16 bits each
+  uint32_t ue[4], uo[4], de[4], dd[4];  // extremes of the even and of the odd bytes
 #pragma unroll
-  for (int w = 0; w < 4; ++w) ue[w] = uo[w] = 0u, de[w] = dd[w] = 0x00ff00ffu;
+  for (int w = 0; w < 4; ++w) ue[w] = uo[w] = 0u, de[w] = kEven, dd[w] = kOdd;
 #pragma unroll
   for (int i = 0; i < Share<UNITS>::kMine; ++i) {
     const int t = sh.first + i * sh.tpu;
@@ -268,10 +280,10 @@ __device__ __forceinline__ void move_page(const CacheView& c, const SeqView& sq,
       if (!is_v) {
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const uint32_t o = e4m3_order4(x[i][w]), nan = e4m3_nan4(x[i][w]);
-          const uint32_t hi = o & ~nan, lo = o | nan;
-          ue[w] = __vmaxu2(ue[w], hi & 0x00ff00ffu), uo[w] = __vmaxu2(uo[w], (hi >> 8) & 0x00ff00ffu);
-          de[w] = __vminu2(de[w], lo & 0x00ff00ffu), dd[w] = __vminu2(dd[w], (lo >> 8) & 0x00ff00ffu);
+          const uint32_t o = e4m3_order4(x[i][w]), none = nan ? e4m3_nan4(x[i][w]) : 0u;
+          const uint32_t hi = o & ~none, lo = o | none;
+          ue[w] = __vmaxu2(ue[w], hi & kEven), uo[w] = __vmaxu2(uo[w], hi & kOdd);
+          de[w] = __vminu2(de[w], lo & kEven), dd[w] = __vminu2(dd[w], lo & kOdd);
         }
       }
     }
@@ -279,7 +291,7 @@ __device__ __forceinline__ void move_page(const CacheView& c, const SeqView& sq,
   if (!is_v) {
     uint32_t up[4], dn[4];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) up[w] = ue[w] | (uo[w] << 8), dn[w] = de[w] | (dd[w] << 8);
+    for (int w = 0; w < 4; ++w) up[w] = ue[w] | uo[w], dn[w] = de[w] | dd[w];
     write_bounds(c, sh, gh, count, false, up, dn);
   }
 }
@@ -362,7 +374,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_evict_plan_kernel(const Ca
     }
   } else {
     const int tail = min(p.recent, len), best = p.keep - tail;
-    block_top_ascending<kPlanThreads, 16>([&](int j) { return order_key(mass[j]); }, len - tail, best,
+    block_top_ascending<kPlanThreads>([&](int j) { return order_key(mass[j]); }, len - tail, best,
                                       [&](int at, int j) {
                                         kept[at] = j;
                                         out[at] = mass[j];
@@ -372,6 +384,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_evict_plan_kernel(const Ca
       out[best + j] = mass[len - tail + j];
     }
   }
+  launch_dependents();
   for (int j = left + threadIdx.x; j < p.keep; j += kPlanThreads) kept[j] = -1;
   for (int j = left + threadIdx.x; j < (p.dst_width << p.c.log2_page); j += kPlanThreads)
     out[j] = 0.f;
@@ -381,6 +394,7 @@ template <int UNITS>
 __global__ void __launch_bounds__(kPageThreads) cache_evict_move_kernel(const CacheEvictParams p) {
   const bool is_v = blockIdx.x & 1;
   const int i = blockIdx.x >> 1, h = blockIdx.y, b = blockIdx.z;
+  wait_for_previous();
   const int left = p.new_lens[b], base = i << p.c.log2_page;
   if (base >= left) return;
   const int g = p.dst_page[static_cast<int64_t>(b) * p.dst_width + i];
@@ -418,9 +432,9 @@ cudaError_t cache_evict_launch(const CacheEvictParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const dim3 grid(2u * ((p.keep + p.c.page - 1) >> p.c.log2_page), p.c.heads, p.s.batch);
   by_units(p.c, [&](auto u) {
-    cache_evict_move_kernel<decltype(u)::value><<<grid, kPageThreads, 0, stream>>>(p);
+    e = launch_after(cache_evict_move_kernel<decltype(u)::value>, grid, kPageThreads, stream, p);
   });
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace ea

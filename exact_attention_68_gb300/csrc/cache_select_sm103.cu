@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const CacheS
       now = next;
     }
   }
+  launch_dependents();
   // pages behind the sequence's end
   for (int i = max(first, np) + threadIdx.x; i < min(p.s.width, first + kScoreGroups * pages_per_group); i += kScoreThreads)
     scores[i] = -INFINITY;
@@ -158,13 +159,14 @@ __global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const CacheSel
   int* pages = p.pages + bh * p.count;
   int len, n;
   load_seq(p.s, p.c, b, false, &len, &n);
+  wait_for_previous();
   int taken = 0;
   if (n > 0) {
     const int np = (len + p.c.page - 1) >> p.c.log2_page;
     const int first = (len - n) >> p.c.log2_page;  // from here on the new tokens' pages
     const int fresh = min(np - first, p.count);
     const int best = min(p.count - fresh, first);
-    block_top_ascending<kPickThreads, 8>([&](int i) { return order_key(scores[i]); }, first, best,
+    block_top_ascending<kPickThreads>([&](int i) { return order_key(scores[i]); }, first, best,
                                       [&](int at, int i) { pages[at] = i; });
     for (int i = threadIdx.x; i < fresh; i += kPickThreads) pages[best + i] = np - fresh + i;
     taken = best + fresh;
@@ -199,8 +201,7 @@ cudaError_t cache_select_launch(const CacheSelectParams& p, bool f16, cudaStream
                   : units <= 8 ? score_rows<2>(p, f16, stream)
                                : score_rows<4>(p, f16, stream);
   if (e != cudaSuccess) return e;
-  cache_pick_kernel<<<dim3(p.c.heads, p.s.batch), kPickThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_after(cache_pick_kernel, dim3(p.c.heads, p.s.batch), kPickThreads, stream, p);
 }
 
 }  // namespace ea

@@ -423,6 +423,23 @@ def test_select_meets_the_oracle(D, P, Hq, H, T, dtype, lens, count):
     assert binding.device_status() == binding.ATTN_OK
 
 
+def test_select_among_more_pages_than_one_tile_of_registers_holds():
+    P, D, n = 16, 16, 9001
+    c = pool(n, 1, D, P, 107, stale=False)
+    g = torch.Generator().manual_seed(108)
+    hi = torch.randint(-20, 128, (n, 1, 1, 16), generator=g)
+    lo = torch.minimum(hi, torch.randint(-127, 30, (n, 1, 1, 16), generator=g))
+    c.k_bounds.copy_(torch.cat([hi, lo], dim=2).to(torch.int8))
+    c.k_scale.copy_(torch.exp2(torch.randint(-3, 3, (n, 1), generator=g).float()))
+    table = np.random.default_rng(109).permutation(n).reshape(1, n).astype(np.int32)
+    lens = [P * (n - 1) + 3]
+    q = rows((1, 3, 1, D), FP, 110)
+    for count in (700, 1, 9000):
+        pages, scores = kv.cache_select(q.to(DEV), c, ints(table), ints(lens), count)
+        rp, rs = oc.cache_select(to_np(c), table, np.array(lens), [1], q.float().numpy(), count)
+        assert np.array_equal(scores.cpu().numpy(), rs) and np.array_equal(pages.cpu().numpy(), rp)
+
+
 def test_select_equal_scores_take_the_lowest_pages():
     c, ref, table, _ = filled([640], 1, 64, 16, BF, 105)
     c.k_bounds.fill_(3), c.k_scale.fill_(1.0)
@@ -443,6 +460,7 @@ def test_select_equal_scores_take_the_lowest_pages():
     (256, 16, 2, [77, 500], 1, 1),
     (136, 64, 1, [2500], 1100, 100),
     (64, 16, 1, [5000], 4999, 4000),
+    (8, 64, 1, [40000], 2000, 100),  # more weights than one tile of registers holds
 ])
 def test_evict_meets_the_oracle(D, P, H, lens, keep, recent):
     dst_width = -(-keep // P) + 1
