@@ -35,6 +35,7 @@ __all__ = ["KVCache8", "cache_alloc", "cache_append", "cache_fwd", "cache_select
 
 CACHE_MAX_TOKENS = 64
 _PAGE_SIZES = (16, 32, 64)
+_NO_SPACE = 16  # the size that says no workspace is needed
 
 _i64, _p, _f, _i, _u64, _sz = (ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, ctypes.c_int, ctypes.c_uint64,
                                ctypes.c_size_t)
@@ -119,29 +120,59 @@ def _want(name, t, dtype, shape, device):
     return t.data_ptr()
 
 
+_u8, _i8, _i32, _f32 = torch.uint8, torch.int8, torch.int32, torch.float32
+
+
 def _views(cache, table, lens, fresh):
-    """The C structures of a pool and a call's sequences, checked; and the device."""
+    """The C structures of a pool and a call's sequences, checked; the device, and
+    (heads, head_dim, page, batch, width)."""
+    k, v, k_scale, v_scale, k_bounds, head_dim = cache
+    try:
+        dev, shape = k.device, k.shape
+        pages, heads, page, pitch = shape
+        batch, width = seqs = table.shape
+        # everything in one condition: this is most of a small call's time
+        if not (k.is_cuda and pitch == (head_dim + 15) // 16 * 16
+                and k.dtype is _u8 and k.is_contiguous()
+                and v.dtype is _u8 and v.shape == shape and v.is_contiguous() and v.device == dev
+                and k_scale.dtype is _f32 and k_scale.shape == (pages, heads) and k_scale.is_contiguous()
+                and k_scale.device == dev
+                and v_scale.dtype is _f32 and v_scale.shape == (pages, heads) and v_scale.is_contiguous()
+                and v_scale.device == dev
+                and k_bounds.dtype is _i8 and k_bounds.shape == (pages, heads, 2, pitch)
+                and k_bounds.is_contiguous() and k_bounds.device == dev
+                and table.dtype is _i32 and table.is_contiguous() and table.device == dev
+                and lens.dtype is _i32 and lens.shape == (batch,) and lens.is_contiguous() and lens.device == dev):
+            _refuse(cache, table, lens)
+        fresh_p = None if fresh is None else _want("fresh", fresh, _i32, (batch,), dev)
+        return (_Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k_bounds.data_ptr(),
+                       pages, heads, head_dim, page),
+                _Seqs(table.data_ptr(), lens.data_ptr(), fresh_p, batch, width), dev,
+                heads, head_dim, page, batch, width)
+    except (AttributeError, ValueError):
+        _refuse(cache, table, lens)
+        raise
+
+
+def _refuse(cache, table, lens):
+    """Names what _views found wrong, one tensor after the other."""
     k, v, k_scale, v_scale, k_bounds, head_dim = cache
     if not isinstance(k, torch.Tensor) or not k.is_cuda:
         raise TypeError("the cache must be CUDA tensors")
-    shape = k.shape
-    if len(shape) != 4:
+    if k.dim() != 4:
         raise ValueError("cache.k must be [pages, heads, page, pitch]")
-    dev, (pages, heads, page, pitch) = k.device, shape
+    dev, (pages, heads, page, pitch) = k.device, k.shape
     if pitch != (head_dim + 15) // 16 * 16:
         raise ValueError("the cache's rows must be head_dim rounded up to a multiple of 16")
-    per_head = (pages, heads)
-    c = _Cache(_want("cache.k", k, torch.uint8, shape, dev), _want("cache.v", v, torch.uint8, shape, dev),
-               _want("cache.k_scale", k_scale, torch.float32, per_head, dev),
-               _want("cache.v_scale", v_scale, torch.float32, per_head, dev),
-               _want("cache.k_bounds", k_bounds, torch.int8, (pages, heads, 2, pitch), dev),
-               pages, heads, head_dim, page)
+    _want("cache.k", k, _u8, k.shape, dev)
+    _want("cache.v", v, _u8, k.shape, dev)
+    _want("cache.k_scale", k_scale, _f32, (pages, heads), dev)
+    _want("cache.v_scale", v_scale, _f32, (pages, heads), dev)
+    _want("cache.k_bounds", k_bounds, _i8, (pages, heads, 2, pitch), dev)
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("table must be an int32 [batch, width] tensor")
-    batch, width = shape = table.shape
-    s = _Seqs(_want("table", table, torch.int32, shape, dev), _want("lens", lens, torch.int32, (batch,), dev),
-              None if fresh is None else _want("fresh", fresh, torch.int32, (batch,), dev), batch, width)
-    return c, s, dev
+    _want("table", table, _i32, table.shape, dev)
+    _want("lens", lens, _i32, (table.shape[0],), dev)
 
 
 def _rows(name, t, batch, head_dim, dev):
@@ -149,9 +180,10 @@ def _rows(name, t, batch, head_dim, dev):
     dt = _DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
     if dt is None:
         raise TypeError(f"{name} must be a bfloat16 or float16 tensor")
-    if (t.dim() != 4 or t.shape[0] != batch or t.shape[3] != head_dim or not t.is_contiguous() or t.device != dev):
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != batch or shape[3] != head_dim or not t.is_contiguous() or t.device != dev:
         raise ValueError(f"{name} must be a contiguous [{batch}, heads, T, {head_dim}] tensor on {dev}")
-    return dt, t.shape[1], t.shape[2]
+    return dt, shape[1], shape[2]
 
 
 def _call(name, dev, stream, *args):
@@ -203,16 +235,16 @@ def _space(workspace, dev):
 def cache_append(cache, k, v, table, lens, fresh=None, stream=None) -> None:
     """Quantises the new tokens' keys and values, 16-bit [B, heads, T, D], into
     the cache: token i < fresh[b] (default T) goes to position lens[b] - fresh[b] + i."""
-    c, s, dev = _views(cache, table, lens, fresh)
-    dt, heads, T = _rows("k", k, s.batch, c.head_dim, dev)
-    if _rows("v", v, s.batch, c.head_dim, dev) != (dt, heads, T) or heads != c.heads:
+    c, s, dev, kv_heads, D, _, B, _ = _views(cache, table, lens, fresh)
+    dt, heads, T = _rows("k", k, B, D, dev)
+    if _rows("v", v, B, D, dev) != (dt, heads, T) or heads != kv_heads:
         raise ValueError("k and v must share shape and dtype and have the cache's heads")
     _call("attn_cache_append", dev, stream, c, s, k.data_ptr(), v.data_ptr(), T, dt)
 
 
 def cache_fwd_workspace(cache, table, lens, q_heads, T, listed=0, with_mass=False) -> int:
     """Bytes of workspace cache_fwd needs for these sizes."""
-    c, s, dev = _views(cache, table, lens, None)
+    c, s, dev = _views(cache, table, lens, None)[:3]
     return _size("attn_cache_fwd_workspace", dev, c, s, listed, q_heads, T, int(with_mass))
 
 
@@ -225,35 +257,37 @@ def cache_fwd(q, cache, table, lens, fresh=None, scale=None, pages=None, mass=No
     keys' attention weights added.  Returns (out like q, lse fp32 [B, Hq, T]);
     rows of tokens from fresh[b] on are not written.
     """
-    c, s, dev = _views(cache, table, lens, fresh)
-    dt, heads, T = _rows("q", q, s.batch, c.head_dim, dev)
+    c, s, dev, kv_heads, D, page, B, width = _views(cache, table, lens, fresh)
+    dt, heads, T = _rows("q", q, B, D, dev)
     listed, list_p, mass_p = 0, None, None
     if pages is not None:
         if not isinstance(pages, torch.Tensor) or pages.dim() != 3 or pages.shape[2] < 1:
             raise ValueError("pages must be an int32 [batch, heads, n] tensor, n >= 1")
         listed = pages.shape[2]
-        list_p = _want("pages", pages, torch.int32, (s.batch, c.heads, listed), dev)
+        list_p = _want("pages", pages, torch.int32, (B, kv_heads, listed), dev)
     if mass is not None:
-        mass_p = _want("mass", mass, torch.float32, (s.batch, c.heads, s.width * c.page), dev)
+        mass_p = _want("mass", mass, torch.float32, (B, kv_heads, width * page), dev)
     if out is None:
         out = torch.empty_like(q)
         _on(stream, out)
     else:
         _want("out", out, q.dtype, q.shape, dev)
     if lse is None:
-        lse = torch.empty((s.batch, heads, T), dtype=torch.float32, device=dev)
+        lse = torch.empty((B, heads, T), dtype=torch.float32, device=dev)
         _on(stream, lse)
     else:
-        _want("lse", lse, torch.float32, (s.batch, heads, T), dev)
+        _want("lse", lse, torch.float32, (B, heads, T), dev)
     if workspace is None:
-        need = _size("attn_cache_fwd_workspace", dev, c, s, listed, heads, T, int(mass is not None))
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        _on(stream, workspace)
+        space = _size("attn_cache_fwd_workspace", dev, c, s, listed, heads, T, int(mass is not None))
+        if space > _NO_SPACE:
+            workspace = torch.empty(space, dtype=torch.uint8, device=dev)
+            _on(stream, workspace)
     else:
         _space(workspace, dev)
+        space = workspace.numel()
     _call("attn_cache_fwd", dev, stream, c, s, q.data_ptr(), list_p, listed, out.data_ptr(), lse.data_ptr(), mass_p,
-          heads, T, 1.0 / math.sqrt(c.head_dim) if scale is None else float(scale), dt, workspace.data_ptr(),
-          workspace.numel(), ATTN_DEFAULT_WAIT_TIMEOUT_NS if wait_timeout_ns is None else int(wait_timeout_ns))
+          heads, T, 1.0 / math.sqrt(D) if scale is None else float(scale), dt,
+          None if workspace is None else workspace.data_ptr(), space, ATTN_DEFAULT_WAIT_TIMEOUT_NS if wait_timeout_ns is None else int(wait_timeout_ns))
     return out, lse
 
 
@@ -262,21 +296,21 @@ def cache_select(q, cache, table, lens, count, fresh=None, pages=None, scores=No
     q [B, Hq, T, D]: those of the new tokens and the best by an 8-bit bound on
     their scores.  Returns (pages int32 [B, heads, count], ascending, -1 behind
     the last; scores fp32 [B, heads, width])."""
-    c, s, dev = _views(cache, table, lens, fresh)
-    dt, heads, T = _rows("q", q, s.batch, c.head_dim, dev)
+    c, s, dev, kv_heads, D, page, B, width = _views(cache, table, lens, fresh)
+    dt, heads, T = _rows("q", q, B, D, dev)
     count = int(count)
     if count < 1:
         raise ValueError("count must be at least 1")
     if pages is None:
-        pages = torch.empty((s.batch, c.heads, count), dtype=torch.int32, device=dev)
+        pages = torch.empty((B, kv_heads, count), dtype=torch.int32, device=dev)
         _on(stream, pages)
     else:
-        _want("pages", pages, torch.int32, (s.batch, c.heads, count), dev)
+        _want("pages", pages, torch.int32, (B, kv_heads, count), dev)
     if scores is None:
-        scores = torch.empty((s.batch, c.heads, s.width), dtype=torch.float32, device=dev)
+        scores = torch.empty((B, kv_heads, width), dtype=torch.float32, device=dev)
         _on(stream, scores)
     else:
-        _want("scores", scores, torch.float32, (s.batch, c.heads, s.width), dev)
+        _want("scores", scores, torch.float32, (B, kv_heads, width), dev)
     _call("attn_cache_select", dev, stream, c, s, q.data_ptr(), heads, T, dt, count, pages.data_ptr(),
           scores.data_ptr())
     return pages, scores
@@ -284,7 +318,7 @@ def cache_select(q, cache, table, lens, count, fresh=None, pages=None, scores=No
 
 def cache_evict_workspace(cache, table, lens, dst_width) -> int:
     """Bytes of workspace cache_evict needs for these sizes."""
-    c, s, dev = _views(cache, table, lens, None)
+    c, s, dev = _views(cache, table, lens, None)[:3]
     return _size("attn_cache_evict_workspace", dev, c, s, dst_width)
 
 
@@ -295,30 +329,30 @@ def cache_evict(cache, mass, table, lens, dst_table, keep, recent, kept=None, ne
     Returns (kept int32 [B, heads, keep], new_lens int32 [B], new_mass fp32
     [B, heads, dst_width·page]); from then on dst_table and new_lens describe
     the sequences and the old pages are free."""
-    c, s, dev = _views(cache, table, lens, None)
-    mass_p = _want("mass", mass, torch.float32, (s.batch, c.heads, s.width * c.page), dev)
+    c, s, dev, kv_heads, _, page, B, width = _views(cache, table, lens, None)
+    mass_p = _want("mass", mass, torch.float32, (B, kv_heads, width * page), dev)
     if not isinstance(dst_table, torch.Tensor) or dst_table.dim() != 2:
         raise ValueError("dst_table must be an int32 [batch, dst_width] tensor")
     dst_width = dst_table.shape[1]
-    dst_p = _want("dst_table", dst_table, torch.int32, (s.batch, dst_width), dev)
+    dst_p = _want("dst_table", dst_table, torch.int32, (B, dst_width), dev)
     keep, recent = int(keep), int(recent)
-    if keep < 1 or not 0 <= recent <= keep or keep > dst_width * c.page:
+    if keep < 1 or not 0 <= recent <= keep or keep > dst_width * page:
         raise ValueError("0 <= recent <= keep, 1 <= keep <= dst_width * page")
     if kept is None:
-        kept = torch.empty((s.batch, c.heads, keep), dtype=torch.int32, device=dev)
+        kept = torch.empty((B, kv_heads, keep), dtype=torch.int32, device=dev)
         _on(stream, kept)
     else:
-        _want("kept", kept, torch.int32, (s.batch, c.heads, keep), dev)
+        _want("kept", kept, torch.int32, (B, kv_heads, keep), dev)
     if new_lens is None:
-        new_lens = torch.empty((s.batch,), dtype=torch.int32, device=dev)
+        new_lens = torch.empty((B,), dtype=torch.int32, device=dev)
         _on(stream, new_lens)
     else:
-        _want("new_lens", new_lens, torch.int32, (s.batch,), dev)
+        _want("new_lens", new_lens, torch.int32, (B,), dev)
     if new_mass is None:
-        new_mass = torch.empty((s.batch, c.heads, dst_width * c.page), dtype=torch.float32, device=dev)
+        new_mass = torch.empty((B, kv_heads, dst_width * page), dtype=torch.float32, device=dev)
         _on(stream, new_mass)
     else:
-        _want("new_mass", new_mass, torch.float32, (s.batch, c.heads, dst_width * c.page), dev)
+        _want("new_mass", new_mass, torch.float32, (B, kv_heads, dst_width * page), dev)
     if workspace is None:
         need = _size("attn_cache_evict_workspace", dev, c, s, dst_width)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)

@@ -183,10 +183,25 @@ bool sm_count(int* dev, int* sms) {
   return true;
 }
 
-// The attention's workspace (never 0): parts, then scores.
+// The current device's status words.  They stay where they are once they are
+// there, so the set-up behind them (a lock, a device call) is gone through
+// once per device.
+std::atomic<int*> g_status[kMaxDevices];
+attn_status_t status_words(int** status) {
+  int dev = -1;
+  const bool known = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices;
+  if (known && (*status = g_status[dev].load(std::memory_order_acquire)) != nullptr) return ATTN_OK;
+  const attn_status_t s = ea::current_status_words(status);
+  if (s == ATTN_OK && known) g_status[dev].store(*status, std::memory_order_release);
+  return s;
+}
+
+// The attention's workspace: parts, then scores; 16 bytes, which no kernel
+// touches, where there are neither.
+constexpr size_t kNoSpace = 16;
 size_t fwd_bytes(const Plan& plan, const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t listed, bool with_mass) {
   const size_t keys = static_cast<size_t>(s->batch * c->heads) * score_cols(c, s, listed, listed > 0);
-  return 16 + part_bytes(plan) + (with_mass ? keys * score_rows(plan) * 4 : 0);
+  return kNoSpace + part_bytes(plan) + (with_mass ? keys * score_rows(plan) * 4 : 0);
 }
 
 // (channel, slot, page·head) map of a pool's codes; the box is one swizzled
@@ -235,7 +250,7 @@ attn_status_t attn_cache_append(const attn_cache_t* cache, const attn_cache_seqs
   spans[n++] = {v, bytes, false};
   if (any_overlap(spans, n)) return ATTN_ERR_INVALID_ARG;
   int* status = nullptr;
-  s = ea::current_status_words(&status);
+  s = status_words(&status);
   if (s != ATTN_OK) return s;
   ea::CacheAppendParams p;
   p.c = view_of(cache);
@@ -263,7 +278,7 @@ attn_status_t attn_cache_fwd(const attn_cache_t* cache, const attn_cache_seqs_t*
   if (dtype != ATTN_BF16 && dtype != ATTN_F16) return ATTN_ERR_INVALID_ARG;
   attn_status_t s = check_cache(cache, seqs);
   if (s != ATTN_OK) return s;
-  if (!q || !out || !lse || !workspace) return ATTN_ERR_INVALID_ARG;
+  if (!q || !out || !lse) return ATTN_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
   if (pages ? (listed < 1 || listed > INT32_MAX / 64) : listed != 0) return ATTN_ERR_INVALID_ARG;
   s = check_queries(cache, seqs, q_heads, T);
@@ -274,13 +289,13 @@ attn_status_t attn_cache_fwd(const attn_cache_t* cache, const attn_cache_seqs_t*
       !aligned(mass, 4) || !aligned(pages, 4))
     return ATTN_ERR_MISALIGNED;
   int* status = nullptr;
-  s = ea::current_status_words(&status);
+  s = status_words(&status);
   if (s != ATTN_OK) return s;
   int dev = -1, sms = 0;
   if (!sm_count(&dev, &sms)) return ATTN_ERR_CUDA;
   const Plan plan = plan_of(cache, seqs, listed, q_heads, T, sms);
   const size_t need = fwd_bytes(plan, cache, seqs, listed, mass != nullptr);
-  if (workspace_bytes < need) return ATTN_ERR_INVALID_ARG;
+  if (need > kNoSpace && (!workspace || workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;
   Span spans[14];
   int n = cache_spans(cache, seqs, false, spans);
   const uint64_t rows = static_cast<uint64_t>(seqs->batch * q_heads * T);
@@ -293,6 +308,9 @@ attn_status_t attn_cache_fwd(const attn_cache_t* cache, const attn_cache_seqs_t*
   spans[n++] = {workspace, need, true};
   if (any_overlap(spans, n)) return ATTN_ERR_INVALID_ARG;
 
+  // the tensor maps are encoded by a driver call, which wants a context on this thread
+  const cudaError_t bound = ea::current_device_bound(&dev);
+  if (bound != cudaSuccess) return ea::cuda_failure(static_cast<int>(bound));
   ea::CacheFwdParams p;
   std::memset(&p, 0, sizeof(p));
   p.c = view_of(cache);
@@ -340,7 +358,7 @@ attn_status_t attn_cache_select(const attn_cache_t* cache, const attn_cache_seqs
   spans[n++] = {scores, heads * seqs->width * 4, true};
   if (any_overlap(spans, n)) return ATTN_ERR_INVALID_ARG;
   int* status = nullptr;
-  s = ea::current_status_words(&status);
+  s = status_words(&status);
   if (s != ATTN_OK) return s;
   ea::CacheSelectParams p;
   p.c = view_of(cache);
@@ -391,7 +409,7 @@ attn_status_t attn_cache_evict(const attn_cache_t* cache, const attn_cache_seqs_
   spans[n++] = {workspace, need, true};
   if (any_overlap(spans, n)) return ATTN_ERR_INVALID_ARG;
   int* status = nullptr;
-  s = ea::current_status_words(&status);
+  s = status_words(&status);
   if (s != ATTN_OK) return s;
   ea::CacheEvictParams p;
   p.c = view_of(cache);

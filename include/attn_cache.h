@@ -101,8 +101,8 @@ ATTN_API attn_status_t attn_cache_append(const attn_cache_t* cache, const attn_c
 
 /*
  * attn_cache_fwd_workspace — bytes of workspace that attn_cache_fwd needs on
- * the current device for these sizes (0 on an argument it would refuse).
- * with_mass: whether mass is passed.
+ * the current device for these sizes (0 on an argument it would refuse; 16:
+ * none, workspace may be NULL).  with_mass: whether mass is passed.
  */
 ATTN_API size_t attn_cache_fwd_workspace(const attn_cache_t* cache, const attn_cache_seqs_t* seqs,
                                          int64_t listed, int64_t q_heads, int64_t T,

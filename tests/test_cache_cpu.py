@@ -99,7 +99,7 @@ def test_append_refuses(lib, kw, code):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(q=0), INV), (dict(out=0), INV), (dict(lse=0), INV), (dict(ws=0), INV), (dict(dtype=-1), INV),
+    (dict(q=0), INV), (dict(out=0), INV), (dict(lse=0), INV), (dict(dtype=-1), INV),
     (dict(scale=0.0), INV), (dict(scale=math.nan), INV), (dict(scale=math.inf), INV), (dict(scale=-1.0), INV),
     (dict(q_heads=0), INV), (dict(q_heads=6), INV), (dict(T=0), INV), (dict(T=65), INV),
     (dict(listed=4), INV), (dict(pages=A + 11 * GB, listed=0), INV), (dict(pages=A + 11 * GB, listed=-1), INV),

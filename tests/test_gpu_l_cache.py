@@ -366,10 +366,17 @@ def test_bad_entries_are_left_out_and_reported():
 
 
 def test_workspace_too_small_is_refused():
-    c, _, table, _ = filled([30], 1, 64, 16, BF, 91)
+    c, _, table, _ = filled([30], 1, 64, 16, BF, 91, width=300)
     q = rows((1, 1, 1, 64), BF, 92).to(DEV)
+    # a short table: one CTA has each segment and nothing is joined
+    assert kv.cache_fwd_workspace(c, ints(table[:, :2]), ints([30]), 1, 1) == 16
     need = kv.cache_fwd_workspace(c, ints(table), ints([30]), 1, 1)
-    assert need < kv.cache_fwd_workspace(c, ints(table), ints([30]), 1, 1, with_mass=True)
+    assert 16 < need < kv.cache_fwd_workspace(c, ints(table), ints([30]), 1, 1, with_mass=True)
+    tb, ln = ints(table), ints([30])  # kept: the structures hold their addresses only
+    lib, (cc, ss) = kv._library(), kv._views(c, tb, ln, None)[:2]
+    out, lse = torch.empty_like(q), torch.empty((1, 1, 1), device=DEV)
+    assert lib.attn_cache_fwd(cc, ss, q.data_ptr(), None, 0, out.data_ptr(), lse.data_ptr(), None, 1, 1, 0.1, 0, None,
+                              need, 0, None) == binding.ATTN_ERR_INVALID_ARG
     with pytest.raises(binding.AttnError) as e:
         kv.cache_fwd(q, c, ints(table), ints([30]), workspace=torch.empty(need - 1, dtype=torch.uint8, device=DEV))
     assert e.value.code == binding.ATTN_ERR_INVALID_ARG
