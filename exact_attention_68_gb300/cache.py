@@ -128,21 +128,22 @@ def _views(cache, table, lens, fresh):
     (heads, head_dim, page, batch, width)."""
     k, v, k_scale, v_scale, k_bounds, head_dim = cache
     try:
-        dev, shape = k.device, k.shape
+        dev, at, shape = k.device, k.get_device(), k.shape
         pages, heads, page, pitch = shape
-        batch, width = seqs = table.shape
-        # everything in one condition: this is most of a small call's time
-        if not (k.is_cuda and pitch == (head_dim + 15) // 16 * 16
-                and k.dtype is _u8 and k.is_contiguous()
-                and v.dtype is _u8 and v.shape == shape and v.is_contiguous() and v.device == dev
-                and k_scale.dtype is _f32 and k_scale.shape == (pages, heads) and k_scale.is_contiguous()
-                and k_scale.device == dev
-                and v_scale.dtype is _f32 and v_scale.shape == (pages, heads) and v_scale.is_contiguous()
-                and v_scale.device == dev
-                and k_bounds.dtype is _i8 and k_bounds.shape == (pages, heads, 2, pitch)
-                and k_bounds.is_contiguous() and k_bounds.device == dev
-                and table.dtype is _i32 and table.is_contiguous() and table.device == dev
-                and lens.dtype is _i32 and lens.shape == (batch,) and lens.is_contiguous() and lens.device == dev):
+        batch, width = table.shape
+        # everything in one condition: this is much of a small call's time
+        if (at < 0 or pitch != (head_dim + 15) // 16 * 16
+                or k.dtype is not _u8 or not k.is_contiguous()
+                or v.dtype is not _u8 or v.shape != shape or not v.is_contiguous() or v.get_device() != at
+                or k_scale.dtype is not _f32 or k_scale.shape != (pages, heads) or not k_scale.is_contiguous()
+                or k_scale.get_device() != at
+                or v_scale.dtype is not _f32 or v_scale.shape != (pages, heads) or not v_scale.is_contiguous()
+                or v_scale.get_device() != at
+                or k_bounds.dtype is not _i8 or k_bounds.shape != (pages, heads, 2, pitch)
+                or not k_bounds.is_contiguous() or k_bounds.get_device() != at
+                or table.dtype is not _i32 or not table.is_contiguous() or table.get_device() != at
+                or lens.dtype is not _i32 or lens.shape != (batch,) or not lens.is_contiguous()
+                or lens.get_device() != at):
             _refuse(cache, table, lens)
         fresh_p = None if fresh is None else _want("fresh", fresh, _i32, (batch,), dev)
         return (_Cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k_bounds.data_ptr(),
@@ -186,12 +187,23 @@ def _rows(name, t, batch, head_dim, dev):
     return dt, shape[1], shape[2]
 
 
+# the current device and its current stream's handle, without the objects
+# torch.cuda.current_stream makes on the way
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _call(name, dev, stream, *args):
     """The entry point on `stream` (default: the current one) of `dev`."""
     index = dev.index
-    st = _current_raw_stream(index) if stream is None else stream.cuda_stream
+    if stream is not None:
+        st = stream.cuda_stream
+    elif _raw_stream is not None:
+        st = _raw_stream(index)
+    else:
+        st = torch.cuda.current_stream(dev).cuda_stream
     fn = getattr(_lib or _library(), name)
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         rc = fn(*args, st)
     else:
         with torch.cuda.device(index):
@@ -200,14 +212,9 @@ def _call(name, dev, stream, *args):
         raise AttnError(rc, name)
 
 
-def _current_raw_stream(index):
-    """torch.cuda.current_stream(index).cuda_stream without the objects between."""
-    return torch._C._cuda_getCurrentRawStream(index)
-
-
 def _size(name, dev, *args):
     fn = getattr(_lib or _library(), name)
-    if dev.index == torch.cuda.current_device():
+    if dev.index == _current_device():
         n = fn(*args)
     else:
         with torch.cuda.device(dev):

@@ -68,13 +68,16 @@ cudaError_t cache_select_launch(const CacheSelectParams& p, bool f16, cudaStream
 
 // Tokens of one chunk, the unit of work of the attention: one warp's step.
 constexpr int kCacheChunk = 64;
-// Query rows of a tile; a pass over a (sequence, head)'s keys takes up to four
-// (two above 128 channels, where their sums fill the registers).
+// Query rows of a tile; a pass over a (sequence, head)'s keys takes as many
+// tiles as their sums leave registers for.  Measured at 128 channels, 128
+// segments of 4096 keys: 1 tile 27 us, 2 tiles 34 us; 24 rows in one pass of 3
+// tiles 79 us (spills), in two passes of 2 tiles 63 us.  At 64 channels 32 rows in
+// one pass 40 us, in two 48 us; at 256 channels 16 rows in one 89 us, in two 108 us.
 constexpr int kCacheTileRows = 8;
 // Tiles up to which a warp may be a worker of its own: each worker's Q takes
 // shared memory from the rings.
 constexpr int kCacheWarpWorkerTiles = 2;
-inline int cache_max_tiles(int width) { return width <= 128 ? 4 : 2; }
+inline int cache_max_tiles(int width) { return width <= 64 ? 4 : 2; }
 
 struct CacheFwdParams {
   CUtensorMap tm_k, tm_v;  // (channel, slot, page·head), box: a swizzled row x one page

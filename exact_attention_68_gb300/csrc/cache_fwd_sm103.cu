@@ -85,11 +85,11 @@ struct CacheFwdLayout {
   static_assert(kSlots >= 3, "a K, a V and the next K in flight");
 };
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+__device__ __forceinline__ void mma_f16(float2 (&c)[2], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "+f"(c[0].x), "+f"(c[0].y), "+f"(c[1].x), "+f"(c[1].y)
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
@@ -254,6 +254,65 @@ __device__ __forceinline__ uint32_t pack_16bit(bool f16, float x, float y) {
 }
 __device__ __forceinline__ float2 unpack_16bit(bool f16, uint32_t w) {
   return f16 ? pair_to_float2<true>(w) : pair_to_float2<false>(w);
+}
+
+// The last chunks of a sequence, whose V tiles need care; rare, so kept out of
+// line.  A lane has two of the chunk's 64 rows; md: the chunk's page data.  The
+// writes are ordered before the TMA copy that reuses the slot by the proxy fence
+// here and the warp's barrier before that copy is issued.
+__device__ __forceinline__ int row_position(uint32_t md, int row) {
+  return ld_volatile_shared(md + (row >> 4) * 16) + (row & 15);
+}
+// Zeroes the rows that hold no token of the sequence (they may hold anything,
+// and 0 · NaN is NaN); true if a row that only some of the queries may see
+// (positions above first_last) holds a NaN code.
+template <class L>
+__device__ __noinline__ bool clear_absent(uint32_t vslot, uint32_t md, int first_last, int len) {
+  bool nan = false;
+  for (int row = threadIdx.x & 31; row < kCacheChunk; row += 32) {
+    const int pos = row_position(md, row);
+    if (pos <= first_last) continue;
+    for (int i = 0; i < L::kSlot / kCacheChunk / 16; ++i) {
+      const uint32_t at = vslot + (16 * i / L::kRowBytes) * L::kBlockBytes + row * L::kRowBytes + 16 * i % L::kRowBytes;
+      if (pos >= len) {
+        st_shared_v4(at, 0, 0, 0, 0);
+      } else {
+        const uint4 w = ld_shared_v4(at);
+        nan = nan || (e4m3_nan4(w.x) | e4m3_nan4(w.y) | e4m3_nan4(w.z) | e4m3_nan4(w.w)) != 0;
+      }
+    }
+  }
+  fence_proxy_async_smem();
+  return nan;
+}
+// Zeroes the NaN codes of the rows between first_last and len.
+template <class L>
+__device__ __noinline__ void clear_nan(uint32_t vslot, uint32_t md, int first_last, int len) {
+  for (int row = threadIdx.x & 31; row < kCacheChunk; row += 32) {
+    const int pos = row_position(md, row);
+    if (pos <= first_last || pos >= len) continue;
+    for (int i = 0; i < L::kSlot / kCacheChunk / 16; ++i) {
+      const uint32_t at = vslot + (16 * i / L::kRowBytes) * L::kBlockBytes + row * L::kRowBytes + 16 * i % L::kRowBytes;
+      const uint4 w = ld_shared_v4(at);
+      st_shared_v4(at, w.x & ~e4m3_nan4(w.x), w.y & ~e4m3_nan4(w.y), w.z & ~e4m3_nan4(w.z), w.w & ~e4m3_nan4(w.w));
+    }
+  }
+  fence_proxy_async_smem();
+}
+// The first position above first_last whose row holds a NaN code in channel ch.
+template <class L>
+__device__ __noinline__ int first_nan(uint32_t vslot, uint32_t md, int ch, int first_last, int len) {
+  constexpr int kUnits = L::kRowBytes / 16;
+  int first = kFar;
+  for (int row = 0; row < kCacheChunk; ++row) {
+    const int pos = row_position(md, row);
+    if (pos <= first_last || pos >= len) continue;
+    const int unit = (ch >> 4) % kUnits, sw = kUnits == 8 ? (row & 7) : ((row >> 1) & 3);
+    const uint32_t at = vslot + (ch >> 4) / kUnits * L::kBlockBytes + row * L::kRowBytes + ((unit ^ sw) << 4);
+    const uint32_t w = static_cast<uint32_t>(ld_volatile_shared(at + (ch & 12)));
+    if (((w >> (8 * (ch & 3))) & 0x7fu) == 0x7fu) first = min(first, pos);
+  }
+  return first;
 }
 
 template <int WIDTH, int WORKER, int NT>
@@ -457,31 +516,29 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
       else __syncwarp();
     }
     // this lane's rows: 8·b + 2·t4 + i
-    float qk[NT][2];
+    float2 qk[NT];
     int last[NT][2];  // last position a row may attend to; rows that are not there see every key
     auto last_of = [&](int r) {
       const int i = (tile_row + r) % p.s.T;
       return r < tile_rows && i < cs.n ? cs.len - cs.n + i : cs.len - 1;
     };
 #pragma unroll
-    for (int b = 0; b < NT; ++b)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        qk[b][i] = ld_shared_f32(qf + 4 * (8 * b + 2 * t4 + i));
-        last[b][i] = last_of(8 * b + 2 * t4 + i);
-      }
+    for (int b = 0; b < NT; ++b) {
+      const int r = 8 * b + 2 * t4;
+      qk[b] = make_float2(ld_shared_f32(qf + 4 * r), ld_shared_f32(qf + 4 * r + 4));
+      last[b][0] = last_of(r), last[b][1] = last_of(r + 1);
+    }
     const int first_last = cs.len - cs.n;  // every row sees the keys up to here
 
-    float o[kTiles][NT][4];  // channel 16·u + gid (+ 8), row i of tile b: [u][b][i (+ 2)]
+    const float2 zero2 = make_float2(0.f, 0.f), none2 = make_float2(-INFINITY, -INFINITY);
+    float2 o[kTiles][NT][2];  // channel 16·u + gid + 8·hf, the two rows of tile b: [u][b][hf]
 #pragma unroll
     for (int u = 0; u < kTiles; ++u)
 #pragma unroll
-      for (int b = 0; b < NT; ++b) o[u][b][0] = o[u][b][1] = o[u][b][2] = o[u][b][3] = 0.f;
-    float m[NT][2], r[NT][2], l[NT][2];
+      for (int b = 0; b < NT; ++b) o[u][b][0] = o[u][b][1] = zero2;
+    float2 m[NT], r[NT], l[NT];
 #pragma unroll
-    for (int b = 0; b < NT; ++b)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) m[b][i] = r[b][i] = -INFINITY, l[b][i] = 0.f;
+    for (int b = 0; b < NT; ++b) m[b] = r[b] = none2, l[b] = zero2;
 
 #pragma unroll 1
     for (; at < seg_end; at += WORKER) {
@@ -490,11 +547,11 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
       if (!alive) continue;
       const uint32_t kslot = ring + u_slot * L::kSlot;
       constexpr int kUnits = L::kRowBytes / 16;
-      float s[4][NT][4];  // key row0 (+ 2) of 16-key tile g, row i of tile b: [g][b][i (+ 2)]
+      float2 s[4][NT][2];  // key row0 + 2·hf of 16-key tile g, the two rows of tile b: [g][b][hf]
 #pragma unroll
       for (int g = 0; g < 4; ++g)
 #pragma unroll
-        for (int b = 0; b < NT; ++b) s[g][b][0] = s[g][b][1] = s[g][b][2] = s[g][b][3] = 0.f;
+        for (int b = 0; b < NT; ++b) s[g][b][0] = s[g][b][1] = zero2;
 #pragma unroll
       for (int kb = 0; kb < kKSteps; ++kb) {
         uint32_t qw[NT][8];
@@ -533,7 +590,7 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
       __syncwarp();
       issue();
 
-      // ---- softmax of the chunk
+      // ---- softmax of the chunk; the two rows of a lane's tile go in pairs
       float ev[4], vm[4];
       int gpos[4];
       bool tail = false;  // some key is hidden from some row
@@ -544,11 +601,12 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
         ev[g] = __uint_as_float(md.z);
         vm[g] = __uint_as_float(md.w);
         tail = tail || gpos[g] + 15 > first_last;
+        const float2 ks = make_float2(__uint_as_float(md.y), __uint_as_float(md.y));
 #pragma unroll
         for (int b = 0; b < NT; ++b) {
-          const float f0 = qk[b][0] * __uint_as_float(md.y), f1 = qk[b][1] * __uint_as_float(md.y);
-          s[g][b][0] *= f0, s[g][b][2] *= f0;
-          s[g][b][1] *= f1, s[g][b][3] *= f1;
+          const float2 f = __fmul2_rn(qk[b], ks);
+          s[g][b][0] = __fmul2_rn(s[g][b][0], f);
+          s[g][b][1] = __fmul2_rn(s[g][b][1], f);
         }
       }
       if (tail) {
@@ -557,8 +615,11 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
 #pragma unroll
           for (int b = 0; b < NT; ++b)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (gpos[g] + row0 + (e & 2) > last[b][e & 1]) s[g][b][e] = -INFINITY;
+            for (int hf = 0; hf < 2; ++hf) {
+              const int pos = gpos[g] + row0 + 2 * hf;
+              if (pos > last[b][0]) s[g][b][hf].x = -INFINITY;
+              if (pos > last[b][1]) s[g][b][hf].y = -INFINITY;
+            }
       }
       if (p.scores != nullptr) {
         // [key][row]: the 8 rows of a key side by side
@@ -571,152 +632,105 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
           for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
             for (int b = 0; b < NT; ++b)
-              *reinterpret_cast<float2*>(sc + (16 * g + 2 * hf) * row_len + 8 * b) =
-                  make_float2(s[g][b][2 * hf], s[g][b][2 * hf + 1]);
+              *reinterpret_cast<float2*>(sc + (16 * g + 2 * hf) * row_len + 8 * b) = s[g][b][hf];
       }
-      float mr[NT][2], rr[NT][2], beta[NT][2];  // references: 0 where no key has been allowed yet
+      float2 mn[NT], rel[NT], beta[NT];  // -reference of m, reference of m minus that of r
       bool moved = false;
 #pragma unroll
-      for (int b = 0; b < NT; ++b)
+      for (int b = 0; b < NT; ++b) {
+        float mx[2], rx[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float mx = -INFINITY, rx = -INFINITY;
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const float a = fmaxf(s[g][b][i], s[g][b][i + 2]);
-            mx = fmaxf(mx, a), rx = fmaxf(rx, a + ev[g]);
-          }
-          const float mn = fmaxf(m[b][i], keys_max(mx)), rn = fmaxf(r[b][i], keys_max(rx));
-          mr[b][i] = mn == -INFINITY ? 0.f : mn;
-          rr[b][i] = rn == -INFINITY ? 0.f : rn;
-          l[b][i] *= ex2_approx(m[b][i] - mr[b][i]);
-          beta[b][i] = ex2_approx(r[b][i] - rr[b][i]);
-          moved = moved || rn != r[b][i];
-          m[b][i] = mn, r[b][i] = rn;
+        for (int g = 0; g < 4; ++g) {
+          const float a0 = fmaxf(s[g][b][0].x, s[g][b][1].x), a1 = fmaxf(s[g][b][0].y, s[g][b][1].y);
+          const float2 av = __fadd2_rn(make_float2(a0, a1), make_float2(ev[g], ev[g]));
+          mx[0] = g == 0 ? a0 : fmaxf(mx[0], a0), mx[1] = g == 0 ? a1 : fmaxf(mx[1], a1);
+          rx[0] = g == 0 ? av.x : fmaxf(rx[0], av.x), rx[1] = g == 0 ? av.y : fmaxf(rx[1], av.y);
         }
+        // references: 0 where no key has been allowed yet
+        auto update = [&](float& run, float x, float& ref) {
+          const float top = fmaxf(run, keys_max(x));
+          ref = top == -INFINITY ? 0.f : top;
+          const float f = ex2_approx(run - ref);
+          moved = moved || top != run;
+          run = top;
+          return f;
+        };
+        float2 mr, rr, alpha;
+        alpha.x = update(m[b].x, mx[0], mr.x), alpha.y = update(m[b].y, mx[1], mr.y);
+        beta[b].x = update(r[b].x, rx[0], rr.x), beta[b].y = update(r[b].y, rx[1], rr.y);
+        l[b] = __fmul2_rn(l[b], alpha);
+        mn[b] = make_float2(-mr.x, -mr.y);
+        rel[b] = make_float2(mr.x - rr.x + kPShift, mr.y - rr.y + kPShift);
+      }
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
         for (int u = 0; u < kTiles; ++u)
 #pragma unroll
           for (int b = 0; b < NT; ++b)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[u][b][e] *= beta[b][e & 1];
+            for (int hf = 0; hf < 2; ++hf) o[u][b][hf] = __fmul2_rn(o[u][b][hf], beta[b]);
       }
       uint32_t pb[4][NT][2];  // P, B fragments of the four 16-key steps
 #pragma unroll
       for (int g = 0; g < 4; ++g)
 #pragma unroll
         for (int b = 0; b < NT; ++b) {
-          float pw[4];
+          // a page whose weights are far below the chunk's has a factor beyond
+          // range; its P is held finite
+          const float2 x = __fadd2_rn(make_float2(ev[g], ev[g]), rel[b]);
+          const float2 f = make_float2(ex2_approx(fminf(x.x, 126.f)) * vm[g], ex2_approx(fminf(x.y, 126.f)) * vm[g]);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            // a page whose weights are far below the chunk's has a factor
-            // beyond range; its P is held finite
-            const float f = ex2_approx(fminf(ev[g] + (mr[b][i] - rr[b][i]) + kPShift, 126.f)) * vm[g];
-            const float p0 = ex2_approx(s[g][b][i] - mr[b][i]), p1 = ex2_approx(s[g][b][i + 2] - mr[b][i]);
-            l[b][i] += p0 + p1;
-            pw[i] = p0 * f, pw[i + 2] = p1 * f;
+          for (int hf = 0; hf < 2; ++hf) {
+            const float2 t = __fadd2_rn(s[g][b][hf], mn[b]);
+            const float2 w = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+            l[b] = __fadd2_rn(l[b], w);
+            const float2 pv = __fmul2_rn(w, f);
+            pb[g][b][hf] = movmatrix_trans(pack_f16x2(pv.x, pv.y));
           }
-          pb[g][b][0] = movmatrix_trans(pack_f16x2(pw[0], pw[1]));
-          pb[g][b][1] = movmatrix_trans(pack_f16x2(pw[2], pw[3]));
         }
 
       // ---- Oᵀ += Vᵀ·Pᵀ
       if (alive) alive = __all_sync(0xffffffffu, wait_copy(bars + 8 * u_slot, u_parity, ctl, kSiteCacheV));
       if (!alive) continue;
       const uint32_t vslot = ring + u_slot * L::kSlot;
+      if (tail) {
+        const uint32_t md = meta + u_meta * 64;
+        if (__any_sync(0xffffffffu, clear_absent<L>(vslot, md, first_last, cs.len))) {
+          // A NaN code that some rows may see and others may not: the ones that
+          // may get it now, then it counts as zero.
+#pragma unroll
+          for (int u = 0; u < kTiles; ++u)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const int from = first_nan<L>(vslot, md, 16 * u + gid + 8 * hf, first_last, cs.len);
+#pragma unroll
+              for (int b = 0; b < NT; ++b) {
+                if (from <= last[b][0]) o[u][b][hf].x = __int_as_float(0x7fffffff);
+                if (from <= last[b][1]) o[u][b][hf].y = __int_as_float(0x7fffffff);
+              }
+            }
+          __syncwarp();
+          clear_nan<L>(vslot, md, first_last, cs.len);
+        }
+        __syncwarp();
+      }
       const int vrow = lane & 15;
-      // four 16-bit-packed words of units u, u + 1 for the keys of step g
-      auto load_v = [&](int u, int g, uint32_t (&w)[4]) {
-        const int row = 16 * g + vrow, unit = (u + (lane >> 4)) % kUnits;
-        const int sw = kUnits == 8 ? (row & 7) : ((row >> 1) & 3);
-        ldmatrix_b8_trans_x2(vslot + (u / kUnits) * L::kBlockBytes + row * L::kRowBytes + ((unit ^ sw) << 4), w);
-      };
-      if (!tail) {
 #pragma unroll
-        for (int u = 0; u < kTiles; u += 2) {
-          if (16 * u < p.c.D) {
+      for (int u = 0; u < kTiles; u += 2) {
+        if (16 * u < p.c.D) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              uint32_t w[4];
-              load_v(u, g, w);
+          for (int g = 0; g < 4; ++g) {
+            const int row = 16 * g + vrow, unit = (u + (lane >> 4)) % kUnits;
+            const int sw = kUnits == 8 ? (row & 7) : ((row >> 1) & 3);
+            uint32_t w[4];
+            ldmatrix_b8_trans_x2(vslot + (u / kUnits) * L::kBlockBytes + row * L::kRowBytes + ((unit ^ sw) << 4), w);
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                uint32_t a0, a1, a2, a3;
-                e4m3x4_to_f16(w[2 * i], &a0, &a2);
-                e4m3x4_to_f16(w[2 * i + 1], &a1, &a3);
+            for (int i = 0; i < 2; ++i) {
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_to_f16(w[2 * i], &a0, &a2);
+              e4m3x4_to_f16(w[2 * i + 1], &a1, &a3);
 #pragma unroll
-                for (int b = 0; b < NT; ++b) mma_f16(o[u + i][b], a0, a1, a2, a3, pb[g][b][0], pb[g][b][1]);
-              }
-            }
-          }
-        }
-      } else {
-        // Slots that hold no token of the sequence count as zero, and so do NaN
-        // codes, which rows that may not see them must not meet; the rows that
-        // may, get them by a count of the NaN codes they see per channel.
-        auto one = [](bool x, bool y) { return (x ? 0x3c00u : 0u) | (y ? 0x3c000000u : 0u); };
-        uint32_t vmask[4], see[4][NT][2];  // bytes of this lane's four tokens of each step that exist
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int pos = gpos[g] + 4 * t4, n = min(4, max(0, cs.len - pos));
-          vmask[g] = n == 4 ? 0xffffffffu : (1u << (8 * n)) - 1u;
-#pragma unroll
-          for (int b = 0; b < NT; ++b) {
-            const int z = last_of(8 * b + gid);
-            see[g][b][0] = one(pos <= z, pos + 1 <= z);
-            see[g][b][1] = one(pos + 2 <= z, pos + 3 <= z);
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < kTiles; u += 2) {
-          if (16 * u < p.c.D) {
-            uint32_t nan_seen = 0;
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              uint32_t w[4];
-              load_v(u, g, w);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                w[i] &= vmask[g];
-                const uint32_t nan = __vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                nan_seen |= nan;
-                w[i] &= ~nan;
-              }
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                uint32_t a0, a1, a2, a3;
-                e4m3x4_to_f16(w[2 * i], &a0, &a2);
-                e4m3x4_to_f16(w[2 * i + 1], &a1, &a3);
-#pragma unroll
-                for (int b = 0; b < NT; ++b) mma_f16(o[u + i][b], a0, a1, a2, a3, pb[g][b][0], pb[g][b][1]);
-              }
-            }
-            if (__any_sync(0xffffffffu, nan_seen != 0)) {
-              float c[2][NT][4] = {};
-#pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                uint32_t w[4], a[4][2];
-                load_v(u, g, w);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const uint32_t nan = __vcmpeq4(w[i] & vmask[g] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                  a[i][0] = one(nan & 1u, nan & 0x100u);
-                  a[i][1] = one(nan & 0x10000u, nan & 0x1000000u);
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                  for (int b = 0; b < NT; ++b)
-                    mma_f16(c[i][b], a[2 * i][0], a[2 * i + 1][0], a[2 * i][1], a[2 * i + 1][1], see[g][b][0], see[g][b][1]);
-              }
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int b = 0; b < NT; ++b)
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    if (c[i][b][e] > 0.f) o[u + i][b][e] = __int_as_float(0x7fffffff);
+              for (int b = 0; b < NT; ++b) mma_f16(o[u + i][b], a0, a1, a2, a3, pb[g][b][0], pb[g][b][1]);
             }
           }
         }
@@ -729,9 +743,9 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
     }
     if (seg_end == end) launch_dependents();  // the join may be set up meanwhile
 #pragma unroll
-    for (int b = 0; b < NT; ++b)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) l[b][i] = keys_sum(l[b][i]);
+    for (int b = 0; b < NT; ++b) l[b] = make_float2(keys_sum(l[b].x), keys_sum(l[b].y));
+    // row i (0, 1) of a pair
+    auto of = [](const float2& v, int i) { return i ? v.y : v.x; };
 
     // ---- the segment's result, or this worker's part of it
     const bool whole = seg_at == cs.first && seg_end == cs.first + cs.nc;
@@ -748,28 +762,29 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int row = 8 * b + 2 * t4 + i;
+          const float mi = of(m[b], i), ri = of(r[b], i), li = of(l[b], i);
           if (whole) {
             if (!live(row)) continue;
             const int64_t to = row_place(p, cs.b, h, tile_row + row);
-            const float w = factor(m[b][i], r[b][i], l[b][i]);
+            const float w = factor(mi, ri, li);
 #pragma unroll
             for (int u = 0; u < kTiles; ++u)
 #pragma unroll
               for (int hf = 0; hf < 2; ++hf) {
                 const int ch = 16 * u + gid + 8 * hf;
-                const float x = m[b][i] == -INFINITY ? 0.f : o[u][b][i + 2 * hf] * w;
+                const float x = mi == -INFINITY ? 0.f : of(o[u][b][hf], i) * w;
                 if (ch < p.c.D) p.out[to * p.c.D + ch] = static_cast<uint16_t>(pack_16bit(p.f16, x, 0.f));
               }
-            if (gid == 0) p.lse[to] = (m[b][i] + log2f(l[b][i])) * kLn2f;
+            if (gid == 0) p.lse[to] = (mi + log2f(li)) * kLn2f;
           } else {
 #pragma unroll
             for (int u = 0; u < kTiles; ++u)
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf) part[row * WIDTH + 16 * u + gid + 8 * hf] = o[u][b][i + 2 * hf];
+              for (int hf = 0; hf < 2; ++hf) part[row * WIDTH + 16 * u + gid + 8 * hf] = of(o[u][b][hf], i);
             if (gid == 0) {
-              part_stat[row] = m[b][i];
-              part_stat[kRows + row] = r[b][i];
-              part_stat[2 * kRows + row] = l[b][i];
+              part_stat[row] = mi;
+              part_stat[kRows + row] = ri;
+              part_stat[2 * kRows + row] = li;
             }
           }
         }
@@ -783,9 +798,9 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t to = stat + (warp * kRows + 8 * b + 2 * t4 + i) * 12;
-            st_shared_f32(to, m[b][i]);
-            st_shared_f32(to + 4, r[b][i]);
-            st_shared_f32(to + 8, l[b][i]);
+            st_shared_f32(to, of(m[b], i));
+            st_shared_f32(to + 4, of(r[b], i));
+            st_shared_f32(to + 8, of(l[b], i));
           }
       }
       __syncthreads();
@@ -808,7 +823,7 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
         for (int i = 0; i < 2; ++i) {
           float M, R, S;
           joined(8 * b + 2 * t4 + i, &M, &R, &S);
-          beta[b][i] = r[b][i] == -INFINITY ? 0.f : ex2_approx(r[b][i] - R);
+          beta[b][i] = of(r[b], i) == -INFINITY ? 0.f : ex2_approx(of(r[b], i) - R);
         }
       // two neighbouring columns of a row per thread
       constexpr int kThreads = L::kWarps * 32, kPairs = kRows * L::kJoinCols / 2, kUPer = L::kJoinCols / 16;
@@ -821,7 +836,7 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               st_shared_f32(join + ((warp * kRows + 8 * b + 2 * t4 + (e & 1)) * L::kJoinPitch + 16 * u + gid + 4 * (e & 2)) * 4,
-                            o[c * kUPer + u][b][e] * beta[b][e & 1]);
+                            of(o[c * kUPer + u][b][e >> 1], e & 1) * beta[b][e & 1]);
         __syncthreads();
         for (int i = threadIdx.x; i < kPairs; i += kThreads) {
           const int row = i / (L::kJoinCols / 2), col = 2 * (i % (L::kJoinCols / 2));
@@ -1001,7 +1016,7 @@ cudaError_t launch_width(const CacheFwdParams& p, bool warp_workers, int tiles, 
     case 1: return go(std::integral_constant<int, 1>());
     case 2: return go(std::integral_constant<int, 2>());
   }
-  if constexpr (WIDTH <= 128) {
+  if constexpr (WIDTH <= 64) {
     if (tiles == 3) return go(std::integral_constant<int, 3>());
     if (tiles == 4) return go(std::integral_constant<int, 4>());
   }

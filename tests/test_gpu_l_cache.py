@@ -366,7 +366,7 @@ def test_bad_entries_are_left_out_and_reported():
 
 
 def test_workspace_too_small_is_refused():
-    c, _, table, _ = filled([30], 1, 64, 16, BF, 91, width=300)
+    c, _, table, _ = filled([30], 1, 64, 16, BF, 91, width=20000)
     q = rows((1, 1, 1, 64), BF, 92).to(DEV)
     # a short table: one CTA has each segment and nothing is joined
     assert kv.cache_fwd_workspace(c, ints(table[:, :2]), ints([30]), 1, 1) == 16
