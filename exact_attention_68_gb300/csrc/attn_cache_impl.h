@@ -91,7 +91,7 @@ struct CacheFwdParams {
   bool f16;            // q and out are fp16 (else bf16)
   int G, row_tiles;    // query heads per key head; passes over a head's keys
   float scale_log2;
-  int by_segment;      // a CTA for each segment: nothing to join
+  int cluster;         // CTAs of the cluster that has a segment; 0: chunks are dealt to workers
   int workers;         // parts the chunks of all (sequence, head, row tile) are dealt to
   int min_chunks;      // fewest chunks worth a worker of their own
   float* part;         // workspace: partial results, two slots per worker

@@ -138,13 +138,16 @@ int64_t score_cols(const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t li
 // through the workspace.
 struct Plan {
   int width, tiles, passes, ctas, workers;
-  bool by_segment, warp_workers;
+  int cluster;
+  bool warp_workers;
 };
-// Steps of a warp up to which a segment is left to one CTA: saves the deal and
-// the join, about 5 us, and one CTA streams at about twice its even share of
-// the memory's rate, so that lengths may differ by two before it loses.  128
-// segments of 2048, 4096, 8192 keys: 15, 27, 46 us, dealt 21, 32, 51 us; with
-// fewer segments than half the SMs, 32 of 4096 keys: 27 us, dealt 19 us.
+// Steps of a warp up to which a segment is left to its own cluster: that saves
+// the deal and the join, about 5 us and a launch, and one CTA streams at about
+// twice its even share of the memory's rate, so that lengths may differ by two
+// before it loses (half of that with two tiles, whose products bound the step).
+// 128 segments of 2048, 4096, 8192 keys: 15, 27, 46 us, dealt 21, 32, 51 us; 32
+// segments of 64 listed pages, clusters of 4: 13.6 us, dealt 18.6 us; 48 ragged
+// segments of up to 16384 keys, two tiles: 78 us, dealt 53 us.
 constexpr int64_t kSegmentSteps = 16, kFewSegmentSteps = 4;
 Plan plan_of(const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t listed, int64_t q_heads, int64_t T,
              int sms) {
@@ -156,11 +159,17 @@ Plan plan_of(const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t listed, 
   p.passes = static_cast<int>(passes_of(rows, p.width));
   const int64_t segments = s->batch * c->heads * p.passes;
   const int64_t chunks = score_cols(c, s, listed, listed > 0) / ea::kCacheChunk;  // at most, of a segment
-  p.by_segment = segments <= sms && chunks <= warps * (2 * segments >= sms ? kSegmentSteps : kFewSegmentSteps);
-  p.warp_workers = !p.by_segment && p.tiles <= ea::kCacheWarpWorkerTiles &&
+  // a cluster for each segment: the largest that fills no more than 128 SMs (32
+  // clusters of 4 or 16 of 8 find their place at once) and leaves each CTA four
+  // chunks of the longest segment
+  int cluster = 1;
+  while (cluster < 8 && segments * cluster * 2 <= 128 && chunks >= 8 * cluster) cluster *= 2;
+  const int64_t steps = 2 * segments * cluster >= sms ? kSegmentSteps / p.tiles : kFewSegmentSteps;
+  p.cluster = segments <= sms && chunks <= steps * warps * cluster ? cluster : 0;
+  p.warp_workers = p.cluster == 0 && p.tiles <= ea::kCacheWarpWorkerTiles &&
                    segments >= static_cast<int64_t>(sms) * warps / 2;
-  p.ctas = p.by_segment ? static_cast<int>(segments) : sms;
-  p.workers = p.by_segment ? 0 : p.warp_workers ? sms * warps : sms;
+  p.ctas = p.cluster > 0 ? static_cast<int>(segments) * p.cluster : sms;
+  p.workers = p.cluster > 0 ? 0 : p.warp_workers ? sms * warps : sms;
   return p;
 }
 
@@ -331,7 +340,7 @@ attn_status_t attn_cache_fwd(const attn_cache_t* cache, const attn_cache_seqs_t*
   p.row_tiles = plan.passes;
   p.score_rows = static_cast<int>(score_rows(plan));
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  p.by_segment = plan.by_segment ? 1 : 0;
+  p.cluster = plan.cluster;
   p.workers = plan.workers;
   p.min_chunks = plan.warp_workers ? 1 : 4;
   p.part = static_cast<float*>(workspace);

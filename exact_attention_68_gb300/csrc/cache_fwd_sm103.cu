@@ -34,7 +34,8 @@
 //
 // A worker that covers a segment (one sequence, head and row tile) writes the
 // result; others write O, m, r, l to the workspace and a second kernel joins
-// them in a fixed order.
+// them in a fixed order.  Where segments are few or short, a cluster of CTAs has
+// each segment instead and joins it through its shared memory: no second launch.
 #include <atomic>
 #include <type_traits>
 
@@ -145,6 +146,23 @@ __device__ __forceinline__ bool wait_copy(uint32_t bar, uint32_t parity, const W
     return false;
   }
   return wait_bounded(bar, parity, ctl, site);
+}
+
+// All threads of the cluster; what any wrote to shared memory before is there
+// for the others after.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A float at the same place `addr` of the shared memory of the cluster's CTA `rank`.
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, int rank) {
+  float v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
+      "ld.shared::cluster.f32 %0, [a];\n\t}"
+      : "=f"(v)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
 }
 
 // Over the eight lanes that hold the same query rows.
@@ -344,15 +362,23 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
   const int worker = blockIdx.x * L::kWorkers + worker_in_cta;
   int begin, end;  // this worker's chunks of the line
   Segment cs;
-  if (WORKER > 1 && p.by_segment) {
-    // a CTA for each segment: a line of its own
-    cs.b = blockIdx.x / (p.c.heads * p.row_tiles);
-    cs.hr = blockIdx.x % (p.c.heads * p.row_tiles);
-    cs.nc = seq_chunks(p, cs.b, cs.hr == 0 && warp == 0, &cs.len, &cs.n);
-    cs.first = begin = 0;
-    end = cs.nc;
-    if (begin >= end) return;
-  } else {
+  int cluster = 0, rank = 0;
+  if constexpr (WORKER > 1) {
+    cluster = p.cluster;
+    if (cluster > 0) {
+      // a cluster for each segment, a line of its own: every CTA an even share
+      rank = blockIdx.x % cluster;
+      const int seg = blockIdx.x / cluster;
+      cs.b = seg / (p.c.heads * p.row_tiles);
+      cs.hr = seg % (p.c.heads * p.row_tiles);
+      cs.nc = seq_chunks(p, cs.b, cs.hr == 0 && warp == 0 && rank == 0, &cs.len, &cs.n);
+      cs.first = 0;
+      begin = static_cast<int>(static_cast<int64_t>(cs.nc) * rank / cluster);
+      end = static_cast<int>(static_cast<int64_t>(cs.nc) * (rank + 1) / cluster);
+      if (cs.nc == 0) return;  // the whole cluster; a CTA without a share takes part in the join
+    }
+  }
+  if (cluster == 0) {
     const Deal deal = deal_chunks(p, blockIdx.x == 0 && warp == 0);
     // 64 bits: worker · per may pass 2^31 (total is below 2^30)
     begin = static_cast<int>(min(static_cast<int64_t>(worker) * deal.per, static_cast<int64_t>(deal.total)));
@@ -465,8 +491,9 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
   const int row0 = 4 * (gid >> 1) + (gid & 1);  // this lane's key of a 16-key tile; the other is row0 + 2
   int at = begin + wi, u_slot = 0, u_parity = 0, u_meta = 0;
   bool alive = true;
-  for (int seg_at = begin; seg_at < end;) {
-    while (seg_at >= cs.first + cs.nc) next_segment(p, cs);
+  int seg_at = begin;
+  do {
+    while (seg_at >= cs.first + cs.nc && cluster == 0) next_segment(p, cs);
     const int seg_end = min(end, cs.first + cs.nc);
     const int h = cs.hr / p.row_tiles, rt = cs.hr % p.row_tiles;
     const int tile_row = rt * kRows, tile_rows = min(kRows, seg_rows - tile_row);
@@ -790,6 +817,9 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
         }
       __syncwarp();  // Q is rewritten for the next segment
     } else {
+      // a cluster's join: O, then m, r, l, over the first warp's ring
+      constexpr int kSumStat = kRows * WIDTH * 4;
+      static_assert(kSumStat + kRows * 12 <= L::kSlots * L::kSlot, "a CTA's sums must fit the ring");
       // the warps' parts joined, kJoinCols columns at a time, in the order of the warps
       const uint32_t stat = sb + L::kStatOff, join = sb + L::kJoinOff;
       if (gid == 0) {
@@ -846,7 +876,9 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
             x += ld_shared_f32(from), y += ld_shared_f32(from + 4);
           }
           const int ch = L::kJoinCols * c + col;
-          if (!whole) {
+          if (cluster > 1) {
+            st_shared_f32(sb + (row * WIDTH + ch) * 4, x), st_shared_f32(sb + (row * WIDTH + ch) * 4 + 4, y);
+          } else if (!whole) {
             *reinterpret_cast<float2*>(part + row * WIDTH + ch) = make_float2(x, y);
           } else if (ch < p.c.D && live(row)) {
             float M, R, S;
@@ -863,7 +895,11 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
         const int row = threadIdx.x;
         float M, R, S;
         joined(row, &M, &R, &S);
-        if (!whole) {
+        if (cluster > 1) {
+          st_shared_f32(sb + kSumStat + row * 12, M);
+          st_shared_f32(sb + kSumStat + row * 12 + 4, R);
+          st_shared_f32(sb + kSumStat + row * 12 + 8, S);
+        } else if (!whole) {
           part_stat[row] = M;
           part_stat[kRows + row] = R;
           part_stat[2 * kRows + row] = S;
@@ -872,9 +908,33 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
         }
       }
       __syncthreads();  // the statistics are rewritten for the next segment
+      if (cluster > 1) {
+        // the CTAs' sums, now at the front of each one's ring (whose copies have
+        // all been used): each CTA joins every kRows · WIDTH / cluster-th pair
+        cluster_barrier();
+        for (int i = rank * kThreads + threadIdx.x; i < kRows * WIDTH / 2; i += cluster * kThreads) {
+          const int row = i / (WIDTH / 2), ch = 2 * (i % (WIDTH / 2));
+          if (ch >= p.c.D || !live(row)) continue;
+          float M = -INFINITY, S = 0.f, x = 0.f, y = 0.f;
+          for (int k = 0; k < cluster; ++k) M = fmaxf(M, ld_cluster_f32(sb + kSumStat + row * 12, k));
+          for (int k = 0; k < cluster && M != -INFINITY; ++k) {
+            const uint32_t st = sb + kSumStat + row * 12, from = sb + (row * WIDTH + ch) * 4;
+            const float mk = ld_cluster_f32(st, k);
+            if (mk == -INFINITY) continue;
+            S += ld_cluster_f32(st + 8, k) * ex2_approx(mk - M);
+            const float f = ex2_approx(ld_cluster_f32(st + 4, k) - M - kPShift);
+            x += ld_cluster_f32(from, k) * f, y += ld_cluster_f32(from + 4, k) * f;
+          }
+          const int64_t to = row_place(p, cs.b, h, tile_row + row);
+          const float inv = S > 0.f || S != S ? 1.f / S : 0.f;
+          *reinterpret_cast<uint32_t*>(p.out + to * p.c.D + ch) = pack_16bit(p.f16, x * inv, y * inv);
+          if (ch == 0) p.lse[to] = (M + log2f(S)) * kLn2f;
+        }
+        cluster_barrier();  // no CTA ends while another reads its memory
+      }
     }
     seg_at = seg_end;
-  }
+  } while (seg_at < end);
 
   // after a wait that ran out: the copies still in flight land before the CTA
   // gives its shared memory back
@@ -991,10 +1051,20 @@ cudaError_t launch_fwd(const CacheFwdParams& p, int dev, int ctas, cudaStream_t 
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  kern<<<ctas, L::kWarps * 32, L::kAlloc, stream>>>(p);
-  e = cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(L::kWarps * 32);
+  cfg.dynamicSmemBytes = L::kAlloc;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, kern, p);
   if (e != cudaSuccess) return e;
-  if (!p.by_segment)
+  if (p.cluster == 0)
     e = launch_after(cache_join_kernel<WIDTH, NT>, dim3(p.s.batch * p.c.heads * p.row_tiles, WIDTH / 32),
                      kJoinThreads * NT, stream, p);
   if (e != cudaSuccess || p.mass == nullptr) return e;
