@@ -106,8 +106,10 @@ template <int WIDTH, int TILES>
 constexpr int kCachePartFloats = kCacheTileRows * TILES * (WIDTH + 3);
 // Width of the kernel that runs a head dimension: 64, 128 or 256.
 inline int cache_kernel_width(int64_t D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
-// Warps of one CTA of that kernel.
-inline int cache_kernel_warps(int width) { return width <= 128 ? 8 : 4; }
+// Warps of one CTA of that kernel: as many as the registers of a tile's sums allow.
+template <int WIDTH, int TILES>
+constexpr int kCacheWarps = (TILES == 1 ? 12 : 8) / (WIDTH <= 128 ? 1 : 2);
+inline int cache_kernel_warps(int width, int tiles) { return (tiles == 1 ? 12 : 8) / (width <= 128 ? 1 : 2); }
 
 // tiles: 8-row tiles of one pass.
 cudaError_t cache_fwd_launch(const CacheFwdParams& p, int width, int tiles, bool warp_workers, int dev, int ctas,

@@ -153,10 +153,10 @@ Plan plan_of(const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t listed, 
              int sms) {
   Plan p;
   p.width = ea::cache_kernel_width(c->head_dim);
-  const int warps = ea::cache_kernel_warps(p.width);
   const int64_t rows = q_heads / c->heads * T;
   p.tiles = tiles_of(rows, p.width);
   p.passes = static_cast<int>(passes_of(rows, p.width));
+  const int warps = ea::cache_kernel_warps(p.width, p.tiles);
   const int64_t segments = s->batch * c->heads * p.passes;
   const int64_t chunks = score_cols(c, s, listed, listed > 0) / ea::kCacheChunk;  // at most, of a segment
   // a cluster for each segment: the largest that fills no more than 128 SMs (32
@@ -164,7 +164,7 @@ Plan plan_of(const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t listed, 
   // chunks of the longest segment
   int cluster = 1;
   while (cluster < 8 && segments * cluster * 2 <= 128 && chunks >= 8 * cluster) cluster *= 2;
-  const int64_t steps = 2 * segments * cluster >= sms ? kSegmentSteps / p.tiles : kFewSegmentSteps;
+  const int64_t steps = 2 * segments * cluster >= sms ? kSegmentSteps / (p.tiles > 1 ? 2 : 1) : kFewSegmentSteps;
   p.cluster = segments <= sms && chunks <= steps * warps * cluster ? cluster : 0;
   p.warp_workers = p.cluster == 0 && p.tiles <= ea::kCacheWarpWorkerTiles &&
                    segments >= static_cast<int64_t>(sms) * warps / 2;

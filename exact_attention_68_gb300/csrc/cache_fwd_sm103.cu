@@ -60,7 +60,7 @@ enum : int { kSiteCacheK = 0x7500, kSiteCacheV = 0x7600 };
 template <int WIDTH, int WORKER, int NT>
 struct CacheFwdLayout {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kWarps = WIDTH <= 128 ? 8 : 4;
+  static constexpr int kWarps = kCacheWarps<WIDTH, NT>;
   static constexpr int kRowBytes = WIDTH >= 128 ? 128 : 64;  // one swizzled row
   static constexpr int kBlocks = WIDTH / kRowBytes;          // column blocks of a chunk
   static constexpr int kBlockBytes = kCacheChunk * kRowBytes;
@@ -83,7 +83,7 @@ struct CacheFwdLayout {
   static constexpr int kEnd = kJoinOff + (WORKER > 1 ? kWarps * kRows * kJoinPitch * 4 : 0);
   static constexpr int kAlloc = kEnd + 1024;
   static_assert(kAlloc <= 232448, "shared memory budget exceeded");
-  static_assert(kSlots >= 3, "a K, a V and the next K in flight");
+  static_assert(kSlots >= 2, "a chunk's K and V");
 };
 
 __device__ __forceinline__ void mma_f16(float2 (&c)[2], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -1075,12 +1075,11 @@ cudaError_t launch_fwd(const CacheFwdParams& p, int dev, int ctas, cudaStream_t 
 template <int WIDTH>
 cudaError_t launch_width(const CacheFwdParams& p, bool warp_workers, int tiles, int dev, int ctas,
                          cudaStream_t stream) {
-  constexpr int kWarps = CacheFwdLayout<WIDTH, 1, 1>::kWarps;
   auto go = [&](auto nt) {
     constexpr int NT = decltype(nt)::value;
     if constexpr (NT <= kCacheWarpWorkerTiles)
       if (warp_workers) return launch_fwd<WIDTH, 1, NT>(p, dev, ctas, stream);
-    return launch_fwd<WIDTH, kWarps, NT>(p, dev, ctas, stream);
+    return launch_fwd<WIDTH, kCacheWarps<WIDTH, NT>, NT>(p, dev, ctas, stream);
   };
   switch (tiles) {
     case 1: return go(std::integral_constant<int, 1>());
