@@ -48,17 +48,17 @@ __device__ __forceinline__ float page_scale(float a) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// Calls body with a function that divides by s with one rounding: a product
-// where s is a power of two in range (its reciprocal and the quotient are then
-// exact), as every scale written here is; a division for others.
+// Calls body with a function that divides pairs by s with one rounding each: a
+// product where s is a power of two in range (its reciprocal and the quotient
+// are then exact), as every scale written here is; a division for others.
 template <class Body>
 __device__ __forceinline__ void with_divider(float s, Body body) {
   const uint32_t u = __float_as_uint(s);
   if ((u & 0x807fffffu) == 0u && (u >> 23) >= 2u && (u >> 23) <= 252u) {
     const float inv = __uint_as_float((254u - (u >> 23)) << 23);
-    body([inv](float x) { return x * inv; });
+    body([inv](float2 x) { return __fmul2_rn(x, make_float2(inv, inv)); });
   } else {
-    body([s](float x) { return __fdiv_rn(x, s); });
+    body([s](float2 x) { return make_float2(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s)); });
   }
 }
 
@@ -116,10 +116,24 @@ __device__ __forceinline__ uint32_t min_x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// Larger and smaller of two pairs of unsigned 16-bit values, one instruction each.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t min_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // e4m3 codes as unsigned bytes in the order of their values, four at a time:
 // negative codes inverted, the others above them.
 __device__ __forceinline__ uint32_t e4m3_order4(uint32_t w) {
-  return w ^ (((w >> 7) & 0x01010101u) * 0xffu | 0x80808080u);
+  uint32_t neg;  // 0xff in the bytes whose sign bit is set (a permutation that spreads it)
+  asm("prmt.b32 %0, %1, 0, 0xba98;" : "=r"(neg) : "r"(w));
+  return w ^ (neg | 0x80808080u);
 }
 // 0xff in the bytes that hold NaN codes.
 __device__ __forceinline__ uint32_t e4m3_nan4(uint32_t w) {

@@ -209,7 +209,7 @@ __device__ __forceinline__ Deal deal_chunks(const CacheFwdParams& p, bool report
 
 // A segment in the line: sequence, head and row tile.
 struct Segment {
-  int b, hr;     // hr = head · row_tiles + row tile
+  int b, h, rt;  // sequence, head, row tile
   int first, nc; // its chunks: first .. first + nc - 1
   int len, n;
 };
@@ -236,8 +236,9 @@ __device__ __forceinline__ Segment find_segment(const CacheFwdParams& p, int at)
       s.len = __shfl_sync(0xffffffffu, len, src);
       s.n = __shfl_sync(0xffffffffu, n, src);
       const int base = before + __shfl_sync(0xffffffffu, upto, src) - s.nc * hr;
-      s.hr = s.nc > 0 ? (at - base) / s.nc : 0;
-      s.first = base + s.hr * s.nc;
+      const int x = s.nc > 0 ? (at - base) / s.nc : 0;
+      s.h = x / p.row_tiles, s.rt = x % p.row_tiles;
+      s.first = base + x * s.nc;
       return s;
     }
     before += __shfl_sync(0xffffffffu, upto, 31);
@@ -246,8 +247,10 @@ __device__ __forceinline__ Segment find_segment(const CacheFwdParams& p, int at)
 // Moves to the next segment; false behind the last.
 __device__ __forceinline__ bool next_segment(const CacheFwdParams& p, Segment& s) {
   s.first += s.nc;
-  if (++s.hr < p.c.heads * p.row_tiles) return true;
-  s.hr = 0;
+  if (++s.rt < p.row_tiles) return true;
+  s.rt = 0;
+  if (++s.h < p.c.heads) return true;
+  s.h = 0;
   do {
     if (++s.b >= p.s.batch) return false;
     s.nc = seq_chunks(p, s.b, false, &s.len, &s.n);
@@ -369,9 +372,10 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
       // a cluster for each segment, a line of its own: every CTA an even share
       rank = blockIdx.x % cluster;
       const int seg = blockIdx.x / cluster;
-      cs.b = seg / (p.c.heads * p.row_tiles);
-      cs.hr = seg % (p.c.heads * p.row_tiles);
-      cs.nc = seq_chunks(p, cs.b, cs.hr == 0 && warp == 0 && rank == 0, &cs.len, &cs.n);
+      cs.rt = seg % p.row_tiles;
+      cs.h = seg / p.row_tiles % p.c.heads;
+      cs.b = seg / p.row_tiles / p.c.heads;
+      cs.nc = seq_chunks(p, cs.b, cs.rt == 0 && cs.h == 0 && warp == 0 && rank == 0, &cs.len, &cs.n);
       cs.first = 0;
       begin = static_cast<int>(static_cast<int64_t>(cs.nc) * rank / cluster);
       end = static_cast<int>(static_cast<int64_t>(cs.nc) * (rank + 1) / cluster);
@@ -394,7 +398,6 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
   Segment fs = cs;
   int f_at = begin + wi;      // next chunk to fetch K of
   int f_page = -1, f_pos = kFar;  // this lane's 16-token group (t4) of it
-  int f_h = 0;                // its head
   bool f_have = false;
   int i_slot = 0;             // slot of the next item
   int f_meta = 0;             // page data entry of the chunk f_at
@@ -408,14 +411,13 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
     f_pos = kFar;
     if (!f_have) return;
     while (f_at >= fs.first + fs.nc) next_segment(p, fs);
-    f_h = fs.hr / p.row_tiles;
     const int tok = (f_at - fs.first) * kCacheChunk + 16 * t4;
     int i = tok >> log2p;
     bool in = true;
     if (p.list != nullptr) {
       in = i < p.listed;
       if (in) {
-        const int* l = p.list + (static_cast<int64_t>(fs.b) * p.c.heads + f_h) * p.listed;
+        const int* l = p.list + (static_cast<int64_t>(fs.b) * p.c.heads + fs.h) * p.listed;
         const int e = l[i];
         in = e >= 0;
         if (in && (e >= p.s.width || !follows(l, i))) {
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
       else mbar_arrive(bar);
     }
     __syncwarp();
-    const int64_t gh = static_cast<int64_t>(f_page) * p.c.heads + f_h;
+    const int64_t gh = static_cast<int64_t>(f_page) * p.c.heads + fs.h;
     if (lead) {
 #pragma unroll
       for (int cb = 0; cb < L::kBlocks; ++cb)
@@ -495,8 +497,7 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
   do {
     while (seg_at >= cs.first + cs.nc && cluster == 0) next_segment(p, cs);
     const int seg_end = min(end, cs.first + cs.nc);
-    const int h = cs.hr / p.row_tiles, rt = cs.hr % p.row_tiles;
-    const int tile_row = rt * kRows, tile_rows = min(kRows, seg_rows - tile_row);
+    const int h = cs.h, tile_row = cs.rt * kRows, tile_rows = min(kRows, seg_rows - tile_row);
 
     // ---- Q to fp16 with a power of two per row
     {

@@ -90,8 +90,8 @@ __device__ __forceinline__ void write_bounds(const CacheView& c, const Share<UNI
   *bu = ru, *bl = rl;
 }
 
-// Appends `count` tokens, rows of D 16-bit values, to page g of head h, at
-// slots held, held + 1, ...; the slots below hold earlier tokens, which stay.
+// Appends `count` tokens, rows of D 16-bit values, to page g (-1: none, nothing
+// is done) of head h, at slots held, held + 1, ...; the slots below hold earlier tokens, which stay.
 //
 // Rounding keeps order, so a channel's largest code is the code of its largest
 // value: the bounds cost a packed maximum and minimum for two values, and codes
@@ -102,9 +102,6 @@ __device__ __forceinline__ void append_page(const CacheView& c, int g, int h, bo
   const Share<UNITS> sh(c.pitch);
   const int64_t gh = static_cast<int64_t>(g) * c.heads + h;
   uint8_t* rows = (is_v ? c.v : c.k) + (gh << c.log2_page) * c.pitch + sh.unit * 16;
-  float* scale = (is_v ? c.v_scale : c.k_scale) + gh;
-  const float was = held > 0 ? *scale : 0.f;
-
   uint32_t x[Share<UNITS>::kMine][8];
 #pragma unroll
   for (int i = 0; i < Share<UNITS>::kMine; ++i) {
@@ -117,6 +114,10 @@ __device__ __forceinline__ void append_page(const CacheView& c, int g, int h, bo
       x[i][4] = b.x, x[i][5] = b.y, x[i][6] = b.z, x[i][7] = b.w;
     }
   }
+  // behind the tokens' loads, which do not wait for the page's number
+  if (g < 0) return;
+  float* scale = (is_v ? c.v_scale : c.k_scale) + gh;
+  const float was = held > 0 ? *scale : 0.f;
   constexpr uint32_t kInf = F16 ? 0x7c007c00u : 0x7f807f80u, kAbs = 0x7fff7fffu;
   uint32_t hi[8], lo[8], a2 = 0;  // k: the channels' extremes; a2: the largest |x|
 #pragma unroll
@@ -154,8 +155,8 @@ __device__ __forceinline__ void append_page(const CacheView& c, int g, int h, bo
   uint32_t up[4], dn[4];
   with_divider(s, [&](auto div) {
     auto codes = [&](uint32_t w0, uint32_t w1) {
-      const float2 v0 = pair_to_float2<F16>(w0), v1 = pair_to_float2<F16>(w1);
-      return pack_e4m3x2(div(v0.x), div(v0.y)) | (pack_e4m3x2(div(v1.x), div(v1.y)) << 16);
+      const float2 v0 = div(pair_to_float2<F16>(w0)), v1 = div(pair_to_float2<F16>(w1));
+      return pack_e4m3x2(v0.x, v0.y) | (pack_e4m3x2(v1.x, v1.y) << 16);
     };
 #pragma unroll
     for (int i = 0; i < Share<UNITS>::kMine; ++i) {
@@ -195,18 +196,18 @@ __device__ __forceinline__ void append_page(const CacheView& c, int g, int h, bo
 }
 
 // Fills page g of head h with `count` tokens of sequence b, picked out of its
-// pages: those at positions kept[0], kept[1], ...
+// pages; thread t < count brings the position of the t-th.
 //
 // Codes whose page has the new page's scale, most of them, are moved as they
 // are.  The largest |code| of a token and the bounds are found among the codes.
 template <int UNITS>
 __device__ __forceinline__ void move_page(const CacheView& c, const SeqView& sq, int b, int g, int h, bool is_v,
-                                          int count, const int* kept) {
+                                          int count, int mine) {
   __shared__ int64_t where[64];  // byte offset of a token's row, -1: none
   __shared__ float scales[64];
   const uint8_t* codes = is_v ? c.v : c.k;
   if (threadIdx.x < 64) {
-    const int t = threadIdx.x, j = t < count ? kept[t] : -1;
+    const int t = threadIdx.x, j = t < count ? mine : -1;
     const int from = j >= 0 && j < (sq.width << c.log2_page) ? load_page(sq, c, b, j >> c.log2_page, true) : -1;
     const int64_t fh = static_cast<int64_t>(from) * c.heads + h;
     where[t] = from < 0 ? -1 : ((fh << c.log2_page) + (j & (c.page - 1))) * c.pitch;
@@ -234,24 +235,21 @@ __device__ __forceinline__ void move_page(const CacheView& c, const SeqView& sq,
   for (int i = 0; i < Share<UNITS>::kMine; ++i) {
     const int t = sh.first + i * sh.tpu;
     if (sh.active && t < count) {
-      uint32_t me = 0, mo = 0, top = 0;  // largest |code| of the even and of the odd bytes
+      uint32_t me = 0, mo = 0;  // largest |code| of the even and of the odd bytes
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint32_t v = x[i][w] & 0x7f7f7f7fu;
-        top |= v + 0x01010101u;
-        me = __vmaxu2(me, v & kEven), mo = __vmaxu2(mo, v & kOdd);
-      }
-      if (top & 0x80808080u) {  // some are NaN, which do not count
+      for (int w = 0; w < 4; ++w)
+        me = max_u16x2(me, x[i][w] & 0x007f007fu), mo = max_u16x2(mo, x[i][w] & 0x7f007f00u);
+      auto largest = [&] { return max(max(me & 0xffu, me >> 16), max((mo >> 8) & 0xffu, mo >> 24)); };
+      if (largest() == 0x7fu) {  // some are NaN, which do not count
         nan = true;
         me = mo = 0;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           const uint32_t v = x[i][w] & 0x7f7f7f7fu & ~e4m3_nan4(x[i][w]);
-          me = __vmaxu2(me, v & kEven), mo = __vmaxu2(mo, v & kOdd);
+          me = max_u16x2(me, v & kEven), mo = max_u16x2(mo, v & kOdd);
         }
       }
-      const uint32_t m = max(max(me & 0xffu, me >> 16), max((mo >> 8) & 0xffu, mo >> 24));
-      a = fmaxf(a, finite_abs(half2_bits_to_float2(e4m3x2_to_f16x2(m)).x * scales[t]));
+      a = fmaxf(a, finite_abs(half2_bits_to_float2(e4m3x2_to_f16x2(largest())).x * scales[t]));
     }
   }
   const float s = page_scale(block_max(a));
@@ -280,10 +278,11 @@ __device__ __forceinline__ void move_page(const CacheView& c, const SeqView& sq,
       if (!is_v) {
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const uint32_t o = e4m3_order4(x[i][w]), none = nan ? e4m3_nan4(x[i][w]) : 0u;
-          const uint32_t hi = o & ~none, lo = o | none;
-          ue[w] = __vmaxu2(ue[w], hi & kEven), uo[w] = __vmaxu2(uo[w], hi & kOdd);
-          de[w] = __vminu2(de[w], lo & kEven), dd[w] = __vminu2(dd[w], lo & kOdd);
+          const uint32_t o = e4m3_order4(x[i][w]);
+          uint32_t hi = o, lo = o;
+          if (nan) hi &= ~e4m3_nan4(x[i][w]), lo |= e4m3_nan4(x[i][w]);
+          ue[w] = max_u16x2(ue[w], hi & kEven), uo[w] = max_u16x2(uo[w], hi & kOdd);
+          de[w] = min_u16x2(de[w], lo & kEven), dd[w] = min_u16x2(dd[w], lo & kOdd);
         }
       }
     }
@@ -305,7 +304,6 @@ __global__ void __launch_bounds__(kPageThreads) cache_append_kernel(const CacheA
   const int start = len - n, i = (start >> p.c.log2_page) + j, base = i << p.c.log2_page;
   if (base >= len) return;
   const int g = load_page(p.s, p.c, b, i, threadIdx.x == 0);
-  if (g < 0) return;
   const int from = max(base, start), to = min(base + p.c.page, len);
   const int64_t row = (static_cast<int64_t>(b) * p.c.heads + h) * p.s.T + (from - start);
   append_page<F16, UNITS>(p.c, g, h, is_v, from - base, to - from, (is_v ? p.v : p.k) + row * p.c.D);
@@ -395,12 +393,14 @@ __global__ void __launch_bounds__(kPageThreads) cache_evict_move_kernel(const Ca
   const bool is_v = blockIdx.x & 1;
   const int i = blockIdx.x >> 1, h = blockIdx.y, b = blockIdx.z;
   wait_for_previous();
-  const int left = p.new_lens[b], base = i << p.c.log2_page;
-  if (base >= left) return;
+  // three loads at once: a page's time is its chain of dependent loads
+  const int base = i << p.c.log2_page, at = base + static_cast<int>(threadIdx.x);
+  const int left = p.new_lens[b];
   const int g = p.dst_page[static_cast<int64_t>(b) * p.dst_width + i];
-  if (g < 0) return;
-  move_page<UNITS>(p.c, p.s, b, g, h, is_v, min(p.c.page, left - base),
-                   p.kept + (static_cast<int64_t>(b) * p.c.heads + h) * p.keep + base);
+  const int mine = threadIdx.x < 64 && at < p.keep
+                       ? p.kept[(static_cast<int64_t>(b) * p.c.heads + h) * p.keep + at] : -1;
+  if (base >= left || g < 0) return;
+  move_page<UNITS>(p.c, p.s, b, g, h, is_v, min(p.c.page, left - base), mine);
 }
 
 // The kernels know the units of 64, 128 and 256 channels at compile time.
