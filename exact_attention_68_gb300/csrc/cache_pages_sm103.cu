@@ -264,7 +264,18 @@ __device__ __forceinline__ void move_page(const CacheView& c, const SeqView& sq,
     const int t = sh.first + i * sh.tpu;
     if (sh.active && t < count) {
       const float f = scales[t] * inv;
-      if (f != 1.f) {
+      const uint32_t fb = __float_as_uint(f);
+      if (f != 1.f && (fb & 0x807fffffu) == 0u && fb >= 0x33800000u && fb <= 0x47000000u) {
+        // a power of two that fp16 holds: the product of a code's 4 bits is
+        // exact there down to 2^-24, and below 2^-14 rounds to code 0 either way
+        const uint32_t ff = pack_f16x2(f, f);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t h0, h1;
+          e4m3x4_to_f16(x[i][w], &h0, &h1);
+          x[i][w] = pack_e4m3x2_f16(mul_f16x2(h0, ff)) | (pack_e4m3x2_f16(mul_f16x2(h1, ff)) << 16);
+        }
+      } else if (f != 1.f) {
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           uint32_t h0, h1;

@@ -19,6 +19,19 @@ namespace {
 constexpr int kScoreThreads = 128;
 constexpr int kScoreGroups = kScoreThreads / 4;  // pages at a time
 
+// Asynchronous copies to shared memory; `bytes` of 16 are read, the rest zero.
+__device__ __forceinline__ void copy_async_16(uint32_t to, const void* from, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_async_4(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // UNITS: 16-channel units of a lane (1, 2 or 4: up to 64, 128, 256 channels);
 // ROWS: query rows held in registers while a CTA's pages go by (more rows: once
 // more over the pages, whose bounds then come from L2).
@@ -27,6 +40,9 @@ __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const CacheS
                                                                     int pages_per_group) {
   __shared__ __align__(16) int8_t qpos[ROWS * 256], qneg[ROWS * 256];
   __shared__ float qa[ROWS];
+  constexpr int kStages = UNITS == 4 ? 2 : 4;  // 34 KB
+  __shared__ int4 ring[kStages][2 * UNITS][kScoreThreads];
+  __shared__ float scale[kStages][kScoreThreads];
   const int h = blockIdx.y, b = blockIdx.z;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane & 3, group = threadIdx.x >> 2;
@@ -83,65 +99,63 @@ __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const CacheS
         y[r][j] = *reinterpret_cast<const int4*>(&qneg[r * 256 + (sub + 4 * j) * 16]);
       }
     }
-    // The pages of a group in turn; page numbers are asked for two steps ahead,
-    // bounds one, so that a step's loads are in flight while the last one's
-    // products run.  All lanes take all steps (the shuffles want them).
-    struct Bounds {
-      int4 hi[UNITS], lo[UNITS];
-      float ks;
-      bool have;
-    };
+    // The pages of a group in turn: each lane copies the units it will need
+    // into places of its own, kStages - 1 steps ahead; page numbers come one
+    // step before that.  All lanes take all steps (the shuffles want them).
     auto page_of = [&](int k) {
       const int i = first + group + k * kScoreGroups;
       return k < pages_per_group && i < stop ? load_page(p.s, p.c, b, i, r0 == 0 && sub == 0) : -1;
     };
-    auto bounds_of = [&](int g, Bounds& x) {
+    int next = page_of(0);
+    auto fetch = [&](int k) {
+      const int g = next, at = k % kStages;
+      next = page_of(k + 1);
       const int64_t gh = static_cast<int64_t>(g < 0 ? 0 : g) * p.c.heads + h;
       const int8_t* bd = p.c.k_bounds + gh * 2 * p.c.pitch;
-      x.have = g >= 0;
 #pragma unroll
       for (int j = 0; j < UNITS; ++j) {
         const int u = sub + 4 * j;
-        x.hi[j] = x.lo[j] = make_int4(0, 0, 0, 0);
-        if (x.have && u < units) {
-          x.hi[j] = __ldg(reinterpret_cast<const int4*>(bd + u * 16));
-          x.lo[j] = __ldg(reinterpret_cast<const int4*>(bd + p.c.pitch + u * 16));
-        }
+        const uint32_t bytes = g >= 0 && u < units ? 16u : 0u;  // 0: zeros
+        const int8_t* from = bd + (bytes ? u * 16 : 0);
+        copy_async_16(smem_u32(&ring[at][2 * j][threadIdx.x]), from, bytes);
+        copy_async_16(smem_u32(&ring[at][2 * j + 1][threadIdx.x]), from + (bytes ? p.c.pitch : 0), bytes);
       }
-      x.ks = x.have ? __ldg(p.c.k_scale + gh) : 0.f;
+      // a page that is not there scores as NaN, which no comparison takes
+      if (g >= 0) copy_async_4(smem_u32(&scale[at][threadIdx.x]), p.c.k_scale + gh);
+      else scale[at][threadIdx.x] = __int_as_float(0x7fffffff);
+      copy_async_commit();
     };
-    Bounds now, next;
-    bounds_of(page_of(0), now);
-    int g = page_of(1);
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) fetch(k);
 #pragma unroll 1
     for (int k = 0; k < pages_per_group; ++k) {
-      const int i = first + group + k * kScoreGroups;
-      bounds_of(g, next);
-      g = page_of(k + 2);
+      const int i = first + group + k * kScoreGroups, at = k % kStages;
+      fetch(k + kStages - 1);
+      copy_async_wait<kStages - 1>();
+      int4 hi[UNITS], lo[UNITS];
+#pragma unroll
+      for (int j = 0; j < UNITS; ++j) hi[j] = ring[at][2 * j][threadIdx.x], lo[j] = ring[at][2 * j + 1][threadIdx.x];
+      const float ks = scale[at][threadIdx.x];
       float best = -INFINITY;
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
         int sum = 0;
 #pragma unroll
         for (int j = 0; j < UNITS; ++j) {
-          sum = __dp4a(now.hi[j].x, x[r][j].x, sum);
-          sum = __dp4a(now.hi[j].y, x[r][j].y, sum);
-          sum = __dp4a(now.hi[j].z, x[r][j].z, sum);
-          sum = __dp4a(now.hi[j].w, x[r][j].w, sum);
-          sum = __dp4a(now.lo[j].x, y[r][j].x, sum);
-          sum = __dp4a(now.lo[j].y, y[r][j].y, sum);
-          sum = __dp4a(now.lo[j].z, y[r][j].z, sum);
-          sum = __dp4a(now.lo[j].w, y[r][j].w, sum);
+          sum = __dp4a(hi[j].x, x[r][j].x, sum);
+          sum = __dp4a(hi[j].y, x[r][j].y, sum);
+          sum = __dp4a(hi[j].z, x[r][j].z, sum);
+          sum = __dp4a(hi[j].w, x[r][j].w, sum);
+          sum = __dp4a(lo[j].x, y[r][j].x, sum);
+          sum = __dp4a(lo[j].y, y[r][j].y, sum);
+          sum = __dp4a(lo[j].z, y[r][j].z, sum);
+          sum = __dp4a(lo[j].w, y[r][j].w, sum);
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        if (a[r] >= 0.f) best = fmaxf(best, __fmul_rn(__fmul_rn(static_cast<float>(sum), now.ks), a[r]));
+        if (a[r] >= 0.f) best = fmaxf(best, __fmul_rn(__fmul_rn(static_cast<float>(sum), ks), a[r]));
       }
-      if (sub == 0 && i < stop) {
-        if (!now.have) best = -INFINITY;
-        scores[i] = r0 == 0 ? best : fmaxf(scores[i], best);
-      }
-      now = next;
+      if (sub == 0 && i < stop) scores[i] = r0 == 0 ? best : fmaxf(scores[i], best);
     }
   }
   launch_dependents();
@@ -150,7 +164,7 @@ __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const CacheS
     scores[i] = -INFINITY;
 }
 
-constexpr int kPickThreads = 512;
+constexpr int kPickThreads = 1024;
 
 __global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const CacheSelectParams p) {
   const int h = blockIdx.x, b = blockIdx.y;
@@ -176,10 +190,12 @@ __global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const CacheSel
 
 template <int UNITS, int ROWS>
 cudaError_t score(const CacheSelectParams& p, bool f16, cudaStream_t stream) {
-  // pages a group that give each of about 152 SMs three CTAs, what its registers hold
+  // the fewest pages a group with which one wave, four CTAs on each of about 152
+  // SMs, covers all (a second wave of a few CTAs took as long as the first)
   auto ctas = [&](int64_t k) { return static_cast<int>((p.s.width + kScoreGroups * k - 1) / (kScoreGroups * k)); };
-  const int64_t steps = static_cast<int64_t>(p.s.batch) * p.c.heads * ctas(1);
-  const int per = static_cast<int>((steps + 455) / 456);
+  const int64_t heads = static_cast<int64_t>(p.s.batch) * p.c.heads;
+  int per = static_cast<int>((heads * ctas(1) + 607) / 608);
+  while (heads * ctas(per) > 608 && ctas(per) > 1) ++per;
   const dim3 grid(ctas(per), p.c.heads, p.s.batch);
   if (f16) cache_score_kernel<UNITS, ROWS, true><<<grid, kScoreThreads, 0, stream>>>(p, per);
   else cache_score_kernel<UNITS, ROWS, false><<<grid, kScoreThreads, 0, stream>>>(p, per);
