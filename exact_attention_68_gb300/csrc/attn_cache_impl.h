@@ -94,6 +94,7 @@ struct CacheFwdParams {
   int cluster;         // CTAs of the cluster that has a segment; 0: chunks are dealt to workers
   int workers;         // parts the chunks of all (sequence, head, row tile) are dealt to
   int min_chunks;      // fewest chunks worth a worker of their own
+  int* line;           // workspace: first chunk of each sequence in the line, then its end
   float* part;         // workspace: partial results, two slots per worker
   float* scores;       // workspace: scaled scores in log2 units, or null (no mass)
   int score_cols;      // keys of a head in `scores`

@@ -45,7 +45,7 @@ attn_status_t check_cache(const attn_cache_t* c, const attn_cache_seqs_t* s) {
   if (c->page != 16 && c->page != 32 && c->page != 64) return ATTN_ERR_UNSUPPORTED;
   if (c->heads > 65535 || s->batch > 65534 || c->pages > INT32_MAX || s->width > INT32_MAX)
     return ATTN_ERR_INVALID_ARG;
-  if (c->pages * c->heads > INT32_MAX / c->page || s->width > INT32_MAX / c->page)
+  if (c->pages * c->heads > INT32_MAX / c->page || s->width > (1 << 30) / c->page)
     return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
 }
@@ -181,6 +181,11 @@ size_t part_bytes(const Plan& p) {
   return 2 * static_cast<size_t>(p.workers) * floats * 4;  // a multiple of 16
 }
 
+// The line's sequences, where there is one.
+size_t line_bytes(const Plan& p, const attn_cache_seqs_t* s) {
+  return p.cluster > 0 ? 0 : (static_cast<size_t>(s->batch + 1) * 4 + 15) / 16 * 16;
+}
+
 // Rows of the score workspace: whole tiles.
 size_t score_rows(const Plan& p) { return static_cast<size_t>(p.passes) * p.tiles * ea::kCacheTileRows; }
 
@@ -214,7 +219,7 @@ attn_status_t status_words(int** status) {
 constexpr size_t kNoSpace = 16;
 size_t fwd_bytes(const Plan& plan, const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t listed, bool with_mass) {
   const size_t keys = static_cast<size_t>(s->batch * c->heads) * score_cols(c, s, listed, listed > 0);
-  return kNoSpace + part_bytes(plan) + (with_mass ? keys * score_rows(plan) * 4 : 0);
+  return kNoSpace + line_bytes(plan, s) + part_bytes(plan) + (with_mass ? keys * score_rows(plan) * 4 : 0);
 }
 
 // (channel, slot, page·head) map of a pool's codes; the box is one swizzled
@@ -343,10 +348,12 @@ attn_status_t attn_cache_fwd(const attn_cache_t* cache, const attn_cache_seqs_t*
   p.cluster = plan.cluster;
   p.workers = plan.workers;
   p.min_chunks = plan.warp_workers ? 1 : 4;
-  p.part = static_cast<float*>(workspace);
+  char* space = static_cast<char*>(workspace);
+  p.line = reinterpret_cast<int*>(space);
+  p.part = reinterpret_cast<float*>(space + line_bytes(plan, seqs));
   p.mass = mass;
   p.score_cols = static_cast<int>(score_cols(cache, seqs, listed, pages != nullptr));
-  p.scores = mass ? reinterpret_cast<float*>(static_cast<char*>(workspace) + part_bytes(plan)) : nullptr;
+  p.scores = mass ? reinterpret_cast<float*>(space + line_bytes(plan, seqs) + part_bytes(plan)) : nullptr;
   p.timeout_ns = wait_timeout_ns;
   return launched(ea::cache_fwd_launch(p, plan.width, plan.tiles, plan.warp_workers, dev, plan.ctas, stream));
 }

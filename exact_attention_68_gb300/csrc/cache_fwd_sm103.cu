@@ -50,10 +50,10 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2f = 0.6931471805599453f;
 constexpr int kPShift = 14;  // P is 2^14 times the weight relative to r
-constexpr int kFar = 0x3fffffff;  // position of a token that is not there
+constexpr int kFar = 0x7fffff00;  // position of a token that is not there (real ones stay below 2^30)
 constexpr uint64_t kDrainNs = 1000000000ull;
 
-enum : int { kSiteCacheK = 0x7500, kSiteCacheV = 0x7600 };
+enum : int { kSiteCacheK = 0x7500, kSiteCacheV = 0x7600, kChkCacheCopy = 0x7701 };
 
 // WIDTH: 64, 128 or 256 channels; WORKER: warps of one worker (all of the
 // CTA's, or 1); NT: 8-row tiles of queries in one pass
@@ -151,7 +151,7 @@ __device__ __forceinline__ bool wait_copy(uint32_t bar, uint32_t parity, const W
 // All threads of the cluster; what any wrote to shared memory before is there
 // for the others after.
 __device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 // A float at the same place `addr` of the shared memory of the cluster's CTA `rank`.
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, int rank) {
@@ -192,6 +192,9 @@ struct Deal {
   int total;  // chunks in line
   int per;    // chunks of a worker
 };
+__device__ __forceinline__ int chunks_per_worker(const CacheFwdParams& p, int total) {
+  return max((total + p.workers - 1) / p.workers, p.min_chunks);
+}
 __device__ __forceinline__ Deal deal_chunks(const CacheFwdParams& p, bool report) {
   const int lane = threadIdx.x & 31, hr = p.c.heads * p.row_tiles;
   int sum = 0;
@@ -201,10 +204,28 @@ __device__ __forceinline__ Deal deal_chunks(const CacheFwdParams& p, bool report
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  Deal d;
-  d.total = sum;
-  d.per = max((sum + p.workers - 1) / p.workers, p.min_chunks);
-  return d;
+  return {sum, chunks_per_worker(p, sum)};
+}
+
+// Writes where each sequence's chunks begin in the line, and its end, for the
+// join.  One warp.
+__device__ __forceinline__ void write_line(const CacheFwdParams& p) {
+  const int lane = threadIdx.x & 31, hr = p.c.heads * p.row_tiles;
+  int before = 0;
+  for (int b0 = 0; b0 < p.s.batch; b0 += 32) {
+    const int b = b0 + lane;
+    int len, n;
+    const int mine = b < p.s.batch ? hr * seq_chunks(p, b, false, &len, &n) : 0;
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += o;
+    }
+    if (b < p.s.batch) p.line[b] = before + upto - mine;
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  if (lane == 0) p.line[p.s.batch] = before;
 }
 
 // A segment in the line: sequence, head and row tile.
@@ -361,6 +382,8 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
   }
   __syncthreads();
   const WaitCtl ctl{abort_addr, p.s.status, p.timeout_ns};
+  const DbgBounds dbb{p.s.status, sb, smem_u32(smem_raw) + static_cast<uint32_t>(L::kAlloc), p.c.page, p.c.D,
+                      p.c.pages * p.c.heads};
 
   const int worker = blockIdx.x * L::kWorkers + worker_in_cta;
   int begin, end;  // this worker's chunks of the line
@@ -384,6 +407,7 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
   }
   if (cluster == 0) {
     const Deal deal = deal_chunks(p, blockIdx.x == 0 && warp == 0);
+    if (blockIdx.x == 0 && warp == 0) write_line(p);
     // 64 bits: worker · per may pass 2^31 (total is below 2^30)
     begin = static_cast<int>(min(static_cast<int64_t>(worker) * deal.per, static_cast<int64_t>(deal.total)));
     end = min(begin + deal.per, deal.total);
@@ -467,9 +491,12 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
     const int64_t gh = static_cast<int64_t>(f_page) * p.c.heads + fs.h;
     if (lead) {
 #pragma unroll
-      for (int cb = 0; cb < L::kBlocks; ++cb)
-        tma_load_3d_plain(ring + i_slot * L::kSlot + cb * L::kBlockBytes + 16 * t4 * L::kRowBytes,
-                          f_is_v ? &p.tm_v : &p.tm_k, bar, cb * L::kRowBytes, 0, static_cast<int>(gh));
+      for (int cb = 0; cb < L::kBlocks; ++cb) {
+        const uint32_t dst = ring + i_slot * L::kSlot + cb * L::kBlockBytes + 16 * t4 * L::kRowBytes;
+        // a copy left out leaves the barrier short: the bounded wait ends the kernel
+        if (dbg_tma(dbb, dst, p.c.page * L::kRowBytes, cb * L::kRowBytes, 0, static_cast<int>(gh), false, kChkCacheCopy))
+          tma_load_3d_plain(dst, f_is_v ? &p.tm_v : &p.tm_k, bar, cb * L::kRowBytes, 0, static_cast<int>(gh));
+      }
     }
     if (!f_is_v) {
       pend_pos = f_pos;
@@ -955,23 +982,16 @@ __global__ void __launch_bounds__(kJoinThreads * NT) cache_join_kernel(const __g
   constexpr int kRows = 8 * NT;
   const int hr = p.c.heads * p.row_tiles;
   const int b = blockIdx.x / hr, x = blockIdx.x % hr;
-  const Deal deal = deal_chunks(p, false);
   int len, n;
-  const int nc = seq_chunks(p, b, false, &len, &n);
-  int before = 0;  // chunks of the sequences before b
-  for (int i = threadIdx.x & 31; i < b; i += 32) {
-    int l2, n2;
-    before += hr * seq_chunks(p, i, false, &l2, &n2);
-  }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) before += __shfl_xor_sync(0xffffffffu, before, d);
+  load_seq(p.s, p.c, b, false, &len, &n);
   // every CTA waits, also one without work: this grid's end means the parts'
   // kernel has ended too.  lens, fresh were there before that kernel began.
   wait_for_previous();
   launch_dependents();
+  const int at = p.line[b], nc = (p.line[b + 1] - at) / hr, total = p.line[p.s.batch];
   if (nc == 0) return;
-  const int first = before + x * nc;
-  const int w0 = first / deal.per, w1 = (first + nc - 1) / deal.per;
+  const int per = chunks_per_worker(p, total), first = at + x * nc;
+  const int w0 = first / per, w1 = (first + nc - 1) / per;
   if (w0 == w1) return;  // one worker had it all
   const int h = x / p.row_tiles, tile_row = (x % p.row_tiles) * kRows;
   const int r = threadIdx.x / 8, col = blockIdx.y * 32 + 4 * (threadIdx.x % 8);

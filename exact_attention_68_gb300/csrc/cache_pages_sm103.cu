@@ -335,37 +335,37 @@ __global__ void __launch_bounds__(kPlanThreads) cache_evict_plan_kernel(const Ca
     uint32_t* twice = p.used + p.used_words;
     for (int w = threadIdx.x; w < 2 * p.used_words; w += kPlanThreads) p.used[w] = 0;
     __syncthreads();
-    for (int bb = 0; bb < p.s.batch; ++bb) {
-      int len, n;
-      load_seq(p.s, p.c, bb, threadIdx.x == 0, &len, &n);
-      const int np = (len + p.c.page - 1) >> p.c.log2_page;
-      for (int i = threadIdx.x; i < np; i += kPlanThreads) {
-        const int g = load_page(p.s, p.c, bb, i, true);
-        if (g >= 0) atomicOr(&once[g >> 5], 1u << (g & 31));
-      }
-    }
-    __syncthreads();
-    for (int round = 0; round < 2; ++round) {
-      for (int bb = 0; bb < p.s.batch; ++bb) {
+    // a warp takes 1024 columns of a sequence's table at a time
+    auto each = [&](int width, bool report, auto visit) {
+      const int blocks = (width + 1023) >> 10;
+      const int64_t units = static_cast<int64_t>(blocks) * p.s.batch;
+      for (int64_t u = threadIdx.x >> 5; u < units; u += kPlanThreads / 32) {
+        const int bb = static_cast<int>(u / blocks), i0 = static_cast<int>(u % blocks) << 10;
         int len, n;
-        load_seq(p.s, p.c, bb, false, &len, &n);
-        const int nd = (min(len, p.keep) + p.c.page - 1) >> p.c.log2_page;
-        for (int i = threadIdx.x; i < p.dst_width; i += kPlanThreads) {
-          const int64_t at = static_cast<int64_t>(bb) * p.dst_width + i;
-          const int g = i < nd ? p.dst_table[at] : -1;
-          const bool in = g >= 0 && g < p.c.pages;
-          const uint32_t bit = 1u << (g & 31);
-          if (round == 0) {
-            if (in && (atomicOr(&once[g >> 5], bit) & bit)) atomicOr(&twice[g >> 5], bit);
-          } else {
-            const bool ok = in && !(twice[g >> 5] & bit);
-            if (i < nd && !ok) dbg_fail(p.s.status, kChkCacheDst);
-            p.dst_page[at] = ok ? g : -1;
-          }
-        }
+        load_seq(p.s, p.c, bb, report && (threadIdx.x & 31) == 0, &len, &n);
+        for (int i = i0 + (threadIdx.x & 31); i < min(width, i0 + 1024); i += 32) visit(bb, len, i);
       }
       __syncthreads();
-    }
+    };
+    each(p.s.width, true, [&](int bb, int len, int i) {
+      if (i << p.c.log2_page >= len) return;
+      const int g = load_page(p.s, p.c, bb, i, true);
+      if (g >= 0) atomicOr(&once[g >> 5], 1u << (g & 31));
+    });
+    auto dst_of = [&](int bb, int len, int i) {  // a needed destination page, or -1
+      return i << p.c.log2_page < min(len, p.keep) ? p.dst_table[static_cast<int64_t>(bb) * p.dst_width + i] : -1;
+    };
+    each(p.dst_width, false, [&](int bb, int len, int i) {
+      const int g = dst_of(bb, len, i);
+      const uint32_t bit = 1u << (g & 31);
+      if (g >= 0 && g < p.c.pages && (atomicOr(&once[g >> 5], bit) & bit)) atomicOr(&twice[g >> 5], bit);
+    });
+    each(p.dst_width, false, [&](int bb, int len, int i) {
+      const int g = dst_of(bb, len, i);
+      const bool ok = g >= 0 && g < p.c.pages && !(twice[g >> 5] & (1u << (g & 31)));
+      if (!ok && i << p.c.log2_page < min(len, p.keep)) dbg_fail(p.s.status, kChkCacheDst);
+      p.dst_page[static_cast<int64_t>(bb) * p.dst_width + i] = ok ? g : -1;
+    });
     return;
   }
   int len, n;

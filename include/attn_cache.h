@@ -74,7 +74,7 @@ typedef struct {
   const int32_t* lens;  /* [batch] tokens in the cache, the new ones counted */
   const int32_t* fresh; /* [batch] new tokens of each sequence, or NULL: all T */
   int64_t batch;        /* 1 .. 65534 */
-  int64_t width;        /* >= 1; width·page < 2^31 */
+  int64_t width;        /* >= 1; width·page <= 2^30 */
 } attn_cache_seqs_t;
 
 /*
