@@ -417,6 +417,7 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
 
   const int seg_rows = p.G * p.s.T;
   const int log2p = p.c.log2_page, page_mask = p.c.page - 1;
+  const bool one_page = p.c.page == kCacheChunk;  // of a chunk
 
   // ---------------- fetching: chunks begin + wi, + WORKER, ... of the line
   Segment fs = cs;
@@ -517,7 +518,12 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
   for (int s = 0; s < L::kSlots; ++s) issue();
 
   // ---------------- the worker's segments
-  const int row0 = 4 * (gid >> 1) + (gid & 1);  // this lane's key of a 16-key tile; the other is row0 + 2
+  // This lane's key of a 16-key tile; the other is row0 + 2.  Keys of a tile are
+  // taken in an order in which two lanes of eight that load together are four
+  // rows apart, so that the swizzle keeps them in different banks; V's rows go to
+  // ldmatrix in the same order.
+  const int row0 = 8 * (gid >> 2) + 4 * (gid & 1) + ((gid >> 1) & 1);
+  const int vrow = (lane & 8) | ((lane & 1) << 2) | (lane & 2) | ((lane >> 2) & 1);
   int at = begin + wi, u_slot = 0, u_parity = 0, u_meta = 0;
   bool alive = true;
   int seg_at = begin;
@@ -726,20 +732,23 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
             for (int hf = 0; hf < 2; ++hf) o[u][b][hf] = __fmul2_rn(o[u][b][hf], beta[b]);
       }
       uint32_t pb[4][NT][2];  // P, B fragments of the four 16-key steps
+      float2 pf[NT];
 #pragma unroll
       for (int g = 0; g < 4; ++g)
 #pragma unroll
         for (int b = 0; b < NT; ++b) {
           // a page whose weights are far below the chunk's has a factor beyond
           // range; its P is held finite
-          const float2 x = __fadd2_rn(make_float2(ev[g], ev[g]), rel[b]);
-          const float2 f = make_float2(ex2_approx(fminf(x.x, 126.f)) * vm[g], ex2_approx(fminf(x.y, 126.f)) * vm[g]);
+          if (g == 0 || !one_page) {
+            const float2 x = __fadd2_rn(make_float2(ev[g], ev[g]), rel[b]);
+            pf[b] = make_float2(ex2_approx(fminf(x.x, 126.f)) * vm[g], ex2_approx(fminf(x.y, 126.f)) * vm[g]);
+          }
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const float2 t = __fadd2_rn(s[g][b][hf], mn[b]);
             const float2 w = make_float2(ex2_approx(t.x), ex2_approx(t.y));
             l[b] = __fadd2_rn(l[b], w);
-            const float2 pv = __fmul2_rn(w, f);
+            const float2 pv = __fmul2_rn(w, pf[b]);
             pb[g][b][hf] = movmatrix_trans(pack_f16x2(pv.x, pv.y));
           }
         }
@@ -769,7 +778,6 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
         }
         __syncwarp();
       }
-      const int vrow = lane & 15;
 #pragma unroll
       for (int u = 0; u < kTiles; u += 2) {
         if (16 * u < p.c.D) {
