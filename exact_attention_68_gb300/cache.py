@@ -16,7 +16,8 @@ checked here, all arithmetic runs in the CUDA library, and there is no fallback.
     kept, new_lens, new_mass = cache_evict(cache, mass, table, lens, dst_table, keep=4096, recent=256)
 
 Nothing synchronises.  A workspace is allocated per call unless one is passed;
-a call captured into a CUDA graph should be given its own.
+calls that may run at the same time, and graphs, need one each.  With ``stream``,
+what a call allocates belongs to that stream, as if it were the current one.
 """
 from __future__ import annotations
 
@@ -224,12 +225,13 @@ def _size(name, dev, *args):
     return n
 
 
-def _on(stream, *tensors):
-    """Tensors allocated here for a call on another stream than the current one:
-    their memory is not handed out again before that stream is done with them."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
+def _new(stream, dev, shape, dtype):
+    """Memory for a call on `stream`, from that stream's pool: no work of another
+    stream can still be using it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _space(workspace, dev):
@@ -275,20 +277,17 @@ def cache_fwd(q, cache, table, lens, fresh=None, scale=None, pages=None, mass=No
     if mass is not None:
         mass_p = _want("mass", mass, torch.float32, (B, kv_heads, width * page), dev)
     if out is None:
-        out = torch.empty_like(q)
-        _on(stream, out)
+        out = torch.empty_like(q) if stream is None else _new(stream, dev, q.shape, q.dtype)
     else:
         _want("out", out, q.dtype, q.shape, dev)
     if lse is None:
-        lse = torch.empty((B, heads, T), dtype=torch.float32, device=dev)
-        _on(stream, lse)
+        lse = _new(stream, dev, (B, heads, T), torch.float32)
     else:
         _want("lse", lse, torch.float32, (B, heads, T), dev)
     if workspace is None:
         space = _size("attn_cache_fwd_workspace", dev, c, s, listed, heads, T, int(mass is not None))
         if space > _NO_SPACE:
-            workspace = torch.empty(space, dtype=torch.uint8, device=dev)
-            _on(stream, workspace)
+            workspace = _new(stream, dev, space, torch.uint8)
     else:
         _space(workspace, dev)
         space = workspace.numel()
@@ -309,13 +308,11 @@ def cache_select(q, cache, table, lens, count, fresh=None, pages=None, scores=No
     if count < 1:
         raise ValueError("count must be at least 1")
     if pages is None:
-        pages = torch.empty((B, kv_heads, count), dtype=torch.int32, device=dev)
-        _on(stream, pages)
+        pages = _new(stream, dev, (B, kv_heads, count), torch.int32)
     else:
         _want("pages", pages, torch.int32, (B, kv_heads, count), dev)
     if scores is None:
-        scores = torch.empty((B, kv_heads, width), dtype=torch.float32, device=dev)
-        _on(stream, scores)
+        scores = _new(stream, dev, (B, kv_heads, width), torch.float32)
     else:
         _want("scores", scores, torch.float32, (B, kv_heads, width), dev)
     _call("attn_cache_select", dev, stream, c, s, q.data_ptr(), heads, T, dt, count, pages.data_ptr(),
@@ -346,24 +343,20 @@ def cache_evict(cache, mass, table, lens, dst_table, keep, recent, kept=None, ne
     if keep < 1 or not 0 <= recent <= keep or keep > dst_width * page:
         raise ValueError("0 <= recent <= keep, 1 <= keep <= dst_width * page")
     if kept is None:
-        kept = torch.empty((B, kv_heads, keep), dtype=torch.int32, device=dev)
-        _on(stream, kept)
+        kept = _new(stream, dev, (B, kv_heads, keep), torch.int32)
     else:
         _want("kept", kept, torch.int32, (B, kv_heads, keep), dev)
     if new_lens is None:
-        new_lens = torch.empty((B,), dtype=torch.int32, device=dev)
-        _on(stream, new_lens)
+        new_lens = _new(stream, dev, (B,), torch.int32)
     else:
         _want("new_lens", new_lens, torch.int32, (B,), dev)
     if new_mass is None:
-        new_mass = torch.empty((B, kv_heads, dst_width * page), dtype=torch.float32, device=dev)
-        _on(stream, new_mass)
+        new_mass = _new(stream, dev, (B, kv_heads, dst_width * page), torch.float32)
     else:
         _want("new_mass", new_mass, torch.float32, (B, kv_heads, dst_width * page), dev)
     if workspace is None:
         need = _size("attn_cache_evict_workspace", dev, c, s, dst_width)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        _on(stream, workspace)
+        workspace = _new(stream, dev, need, torch.uint8)
     else:
         _space(workspace, dev)
     _call("attn_cache_evict", dev, stream, c, s, mass_p, dst_p, dst_width, keep, recent, kept.data_ptr(),

@@ -258,7 +258,7 @@ attn_status_t attn_cache_append(const attn_cache_t* cache, const attn_cache_seqs
   if (dtype != ATTN_BF16 && dtype != ATTN_F16) return ATTN_ERR_INVALID_ARG;
   attn_status_t s = check_cache(cache, seqs);
   if (s != ATTN_OK) return s;
-  if (!k || !v || T < 1 || T > INT32_MAX) return ATTN_ERR_INVALID_ARG;
+  if (!k || !v || T < 1 || T > (1 << 30)) return ATTN_ERR_INVALID_ARG;
   const int64_t per_seq = (T + cache->page - 2) / cache->page + 1;
   if (seqs->batch * cache->heads > INT32_MAX / 2 / per_seq) return ATTN_ERR_INVALID_ARG;  // the grid
   s = check_pointers(cache, seqs);
@@ -396,7 +396,7 @@ attn_status_t attn_cache_select(const attn_cache_t* cache, const attn_cache_seqs
 
 size_t attn_cache_evict_workspace(const attn_cache_t* cache, const attn_cache_seqs_t* seqs,
                                   int64_t dst_width) {
-  if (check_cache(cache, seqs) != ATTN_OK || dst_width < 1 || dst_width > INT32_MAX / cache->page) return 0;
+  if (check_cache(cache, seqs) != ATTN_OK || dst_width < 1 || dst_width > (1 << 30) / cache->page) return 0;
   const size_t words = static_cast<size_t>((cache->pages + 31) / 32);
   return (2 * words * 4 + static_cast<size_t>(seqs->batch * dst_width) * 4 + 15) / 16 * 16;
 }
@@ -409,7 +409,7 @@ attn_status_t attn_cache_evict(const attn_cache_t* cache, const attn_cache_seqs_
   attn_status_t s = check_cache(cache, seqs);
   if (s != ATTN_OK) return s;
   if (!mass || !dst_table || !kept || !new_lens || !mass_out || !workspace) return ATTN_ERR_INVALID_ARG;
-  if (dst_width < 1 || dst_width > INT32_MAX / cache->page || keep < 1 || keep > dst_width * cache->page ||
+  if (dst_width < 1 || dst_width > (1 << 30) / cache->page || keep < 1 || keep > dst_width * cache->page ||
       recent < 0 || recent > keep)
     return ATTN_ERR_INVALID_ARG;
   const int64_t per_seq = (keep + cache->page - 1) / cache->page;

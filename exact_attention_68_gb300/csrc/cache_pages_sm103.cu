@@ -6,7 +6,14 @@
 // codes and, for k, the per-channel bounds.  A thread owns one 16-channel unit
 // and every TPU-th token, so that a row's units lie side by side over a warp
 // (whole 128-byte rows per access) and a channel's bound is a reduction over
-// the threads of its unit.  Both operators move bytes and little else.
+// the threads of its unit.
+//
+// Bytes are what both cannot do without, 6·D a token and head to append and
+// 4·D to move.  Measured at 8 heads of 128 channels: 2 x 8192 tokens appended in
+// 21.1 us = 4.8 TB/s, about 11 instructions a value issued at 57 % of the rate;
+// one token of each of 64 sequences 4.9 us (latency); 8 sequences cut to 4096
+// tokens a head moved in 42 us, 134 MB as random 128-byte rows, behind 16 us
+// for choosing them.
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -91,7 +98,8 @@ __device__ __forceinline__ void write_bounds(const CacheView& c, const Share<UNI
 }
 
 // Appends `count` tokens, rows of D 16-bit values, to page g (-1: none, nothing
-// is done) of head h, at slots held, held + 1, ...; the slots below hold earlier tokens, which stay.
+// is done) of head h, at slots held, held + 1, ...; the slots below hold earlier
+// tokens, which stay.
 //
 // Rounding keeps order, so a channel's largest code is the code of its largest
 // value: the bounds cost a packed maximum and minimum for two values, and codes
@@ -312,8 +320,9 @@ __global__ void __launch_bounds__(kPageThreads) cache_append_kernel(const CacheA
   const int j = blockIdx.x >> 1, h = blockIdx.y, b = blockIdx.z;
   int len, n;
   if (!load_seq(p.s, p.c, b, threadIdx.x == 0, &len, &n) || n == 0) return;
-  const int start = len - n, i = (start >> p.c.log2_page) + j, base = i << p.c.log2_page;
-  if (base >= len) return;
+  const int start = len - n, i = (start >> p.c.log2_page) + j;
+  if (i >= (len + p.c.page - 1) >> p.c.log2_page) return;
+  const int base = i << p.c.log2_page;
   const int g = load_page(p.s, p.c, b, i, threadIdx.x == 0);
   const int from = max(base, start), to = min(base + p.c.page, len);
   const int64_t row = (static_cast<int64_t>(b) * p.c.heads + h) * p.s.T + (from - start);

@@ -23,7 +23,8 @@
  *   v_scale    evict write powers of two; the attention takes any positive scale
  *   k_bounds   int8 [pages, heads, 2, pitch]: for each channel the upper, then
  *              the lower bound of the page's key codes in steps of 448/127
- *              (ceil(max·127/448), floor(min·127/448); NaN codes left out)
+ *              (ceil(max·127/448), floor(min·127/448); NaN codes left out, 0 where
+ *              there are no others, and tokens appended later keep that 0 inside)
  *
  * A power-of-two scale costs an e4m3 code no precision against any other
  * scale, and codes move to a larger power-of-two scale without a rounding
@@ -83,7 +84,7 @@ typedef struct {
  *   k, v   device, 16-bit [batch, heads, T, head_dim] contiguous, 16-byte
  *          aligned (read); token i < fresh[b] of sequence b goes to position
  *          lens[b] - fresh[b] + i, rows from fresh[b] on are not read
- *   T      >= 1 rows per sequence
+ *   T      1 .. 2^30 rows per sequence
  *   dtype  ATTN_BF16 or ATTN_F16
  *
  * For each page and head touched, with a the largest finite |x| of the call's
@@ -196,7 +197,7 @@ ATTN_API size_t attn_cache_evict_workspace(const attn_cache_t* cache,
  *              entries that are needed must differ from each other and from
  *              every page of the call's sequences; one that does not is not
  *              written and is reported.
- *   dst_width  dst_width·page >= keep
+ *   dst_width  keep <= dst_width·page <= 2^30
  *   keep       >= 1;  recent 0 .. keep
  *   kept       device int32 [batch, heads, keep]: the kept positions
  *              ascending, -1 behind the last

@@ -220,6 +220,43 @@ def test_batches_wider_than_a_warp_share_workers():
     check_fwd(out, lse, ro, rl, av, aq, 64, BF, fresh)
 
 
+@pytest.mark.parametrize("B,width", [(3, 4), (3, 20000), (200, 4)])
+def test_a_step_without_tokens_does_nothing(B, width):
+    c = pool(8, 4, 64, 16, 47)
+    before = to_np(c)
+    table, lens, fresh = ints(np.zeros((B, width))), ints([40] + [0] * (B - 1)), ints([0] * B)
+    table[0, :3] = ints([1, 2, 3])
+    q, k = rows((B, 8, 2, 64), BF, 48).to(DEV), rows((B, 4, 2, 64), BF, 49).to(DEV)
+    out, lse = torch.full_like(q, 5.0), torch.full((B, 8, 2), 5.0, device=DEV)
+    mass = torch.full((B, 4, width * 16), 5.0, device=DEV) if width == 4 else None
+    kv.cache_append(c, k, k, table, lens, fresh=fresh)
+    kv.cache_fwd(q, c, table, lens, fresh=fresh, out=out, lse=lse, mass=mass)
+    pages, scores = kv.cache_select(q, c, table, lens, 3, fresh=fresh)
+    torch.cuda.synchronize()
+    assert (out == 5.0).all() and (lse == 5.0).all() and (mass is None or (mass == 5.0).all())
+    assert (pages == -1).all() and torch.isneginf(scores).all()
+    after = to_np(c)
+    assert all(np.array_equal(before[n], after[n]) for n in ("k", "v", "k_scale", "v_scale", "k_bounds"))
+    assert binding.device_status() == binding.ATTN_OK
+
+
+def test_calls_at_the_same_time_on_two_streams():
+    lens = [3000, 700]
+    c, ref, table, _ = filled(lens, 2, 128, 64, BF, 55, width=400)
+    tb, ln = ints(table), ints(lens)
+    qs = [rows((2, 8, 1, 128), BF, 56 + i).to(DEV) for i in range(2)]
+    want = [kv.cache_fwd(q, c, tb, ln) for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            got[i].append(kv.cache_fwd(qs[i], c, tb, ln, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i][0]) and torch.equal(z, want[i][1]) for o, z in got[i])
+
+
 def test_v_scales_far_apart_and_other_than_powers_of_two():
     lens, P, D = [256], 16, 64
     c, ref, table, _ = filled(lens, 2, D, P, BF, 51)
@@ -350,6 +387,12 @@ def test_bad_entries_are_left_out_and_reported():
         torch.cuda.synchronize()
         assert binding.device_status() == binding.ATTN_ERR_DEVICE_CHECK
         assert (pages[2] == -1).all() and torch.isneginf(scores[2]).all()
+    t = table.copy()
+    t[1, 0] = 10 ** 9
+    pages, scores = kv.cache_select(q, c, ints(t), ints(lens), 2)
+    torch.cuda.synchronize()
+    assert binding.device_status() == binding.ATTN_ERR_DEVICE_CHECK
+    assert torch.isneginf(scores[1, :, 0]).all() and torch.isfinite(scores[1, :, 1:4]).all()
     for bad in (-1, 2):
         out, st = run(fresh=ints([1, 1, bad, 1]))
         assert st == binding.ATTN_ERR_DEVICE_CHECK and (out[2] == 3.0).all()
