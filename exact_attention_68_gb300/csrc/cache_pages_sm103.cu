@@ -392,11 +392,10 @@ __global__ void __launch_bounds__(kPlanThreads) cache_evict_plan_kernel(const Ca
     }
   } else {
     const int tail = min(p.recent, len), best = p.keep - tail;
-    block_top_ascending<kPlanThreads>([&](int j) { return order_key(mass[j]); }, len - tail, best,
-                                      [&](int at, int j) {
-                                        kept[at] = j;
-                                        out[at] = mass[j];
-                                      });
+    block_top_ascending<kPlanThreads>(mass, len - tail, best, [&](int at, int j) {
+      kept[at] = j;
+      out[at] = mass[j];
+    });
     for (int j = threadIdx.x; j < tail; j += kPlanThreads) {
       kept[best + j] = len - tail + j;
       out[best + j] = mass[len - tail + j];

@@ -187,8 +187,7 @@ __global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const CacheSel
     const int first = (len - n) >> p.c.log2_page;  // from here on the new tokens' pages
     const int fresh = min(np - first, p.count);
     const int best = min(p.count - fresh, first);
-    block_top_ascending<kPickThreads>([&](int i) { return order_key(scores[i]); }, first, best,
-                                      [&](int at, int i) { pages[at] = i; });
+    block_top_ascending<kPickThreads>(scores, first, best, [&](int at, int i) { pages[at] = i; });
     for (int i = threadIdx.x; i < fresh; i += kPickThreads) pages[best + i] = np - fresh + i;
     taken = best + fresh;
   }

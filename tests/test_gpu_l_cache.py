@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from exact_attention_68_gb300 import binding, cache as kv
+from exact_attention_68_gb300.build import build_debug_library
 from oracle import cache as oc
 
 pytestmark = pytest.mark.gpu
@@ -651,3 +652,22 @@ def test_a_captured_step_replays_on_new_lengths_and_on_another_stream():
         side.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((o2, l2, p2, mass), want))
     assert binding.device_status() == binding.ATTN_OK
+
+
+@pytest.mark.parametrize("D,P,Hq,H,T,lens", [
+    (128, 64, 4, 2, 1, [700, 64, 1]),
+    (64, 16, 2, 2, 3, [300] * 80),
+    (8, 32, 2, 1, 2, [100, 33]),
+    (136, 32, 3, 1, 20, [200, 20]),
+    (256, 16, 2, 1, 1, [50] * 400),
+])
+def test_the_debug_build_finds_no_copy_out_of_its_bounds(monkeypatch, D, P, Hq, H, T, lens):
+    c, _, table, _ = filled(lens, H, D, P, BF, 141)
+    q = rows((len(lens), Hq, T, D), BF, 142, 2.0).to(DEV)
+    want = kv.cache_fwd(q, c, ints(table), ints(lens))
+    lib = kv.declare(binding.load_library(build_debug_library()))
+    monkeypatch.setattr(kv, "_lib", lib)
+    got = kv.cache_fwd(q, c, ints(table), ints(lens))
+    stream = torch.cuda.current_stream().cuda_stream
+    assert lib.attn_device_status(stream) == binding.ATTN_OK
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
