@@ -61,25 +61,62 @@ __device__ __forceinline__ float block_max(float a) {
   return __uint_as_float(m);
 }
 
+// Running extremes of the bytes of words: of the odd bytes in the high halves of
+// 16-bit lanes, where the byte below decides only between equal ones, and of the
+// even bytes moved there.
+struct ByteMax {
+  uint32_t even = 0u, odd = 0u;
+  __device__ __forceinline__ void add(uint32_t w) { even = max_u16x2(even, w << 8), odd = max_u16x2(odd, w); }
+  __device__ __forceinline__ uint32_t get() const { return __byte_perm(even, odd, 0x7351); }
+  __device__ __forceinline__ uint32_t largest() const {
+    const uint32_t m = max_u16x2(even, odd);
+    return max(m >> 24, (m >> 8) & 0xffu);
+  }
+};
+struct ByteMin {
+  uint32_t even = ~0u, odd = ~0u;
+  __device__ __forceinline__ void add(uint32_t w) { even = min_u16x2(even, w << 8), odd = min_u16x2(odd, w); }
+  __device__ __forceinline__ uint32_t get() const { return __byte_perm(even, odd, 0x7351); }
+};
+
 // Writes a page's bounds from every thread's extremes (ordered codes of its 16
 // channels; up < dn: none).  Token rows from `lanes` on hold none.  keep: the
 // bounds there hold for the page's earlier tokens and are widened.
+//
+// Rows are parted among neighbouring lanes, four to each, and joined by shuffles;
+// the rows' pitch of 5 words a unit leaves their reads without bank conflicts.
+// (One warp that reads all rows of a word took 1/6 of an eviction's time.)
 template <int UNITS>
 __device__ __forceinline__ void write_bounds(const CacheView& c, const Share<UNITS>& sh, int64_t gh, int lanes,
                                              bool keep, const uint32_t (&up)[4], const uint32_t (&dn)[4]) {
-  __shared__ __align__(16) uint32_t top[kPageThreads * 4], bottom[kPageThreads * 4];
+  constexpr int kParts = UNITS == 0 ? 1 : kPageThreads / (UNITS == 0 ? 1 : UNITS * 4), kPitch = UNITS == 0 ? 4 : 5;
+  __shared__ __align__(16) uint32_t top[kPageThreads * kPitch], bottom[kPageThreads * kPitch];
+  const int row = sh.units * kPitch;
   if (sh.active) {
-    reinterpret_cast<uint4*>(top)[sh.first * sh.units + sh.unit] = make_uint4(up[0], up[1], up[2], up[3]);
-    reinterpret_cast<uint4*>(bottom)[sh.first * sh.units + sh.unit] = make_uint4(dn[0], dn[1], dn[2], dn[3]);
+    reinterpret_cast<uint4*>(top + sh.first * row)[sh.unit] = make_uint4(up[0], up[1], up[2], up[3]);
+    reinterpret_cast<uint4*>(bottom + sh.first * row)[sh.unit] = make_uint4(dn[0], dn[1], dn[2], dn[3]);
   }
   __syncthreads();
-  const int words = sh.units * 4, w = threadIdx.x;  // words of a row of bounds
+  const int words = sh.units * 4, w = threadIdx.x / kParts, part = threadIdx.x % kParts;  // words of a row of bounds
   if (w >= words) return;
-  uint32_t u = top[w], d = bottom[w];
-  for (int t = 1; t < min(sh.tpu, lanes); ++t) {
-    u = __vmaxu4(u, top[t * words + w]);
-    d = __vminu4(d, bottom[t * words + w]);
+  ByteMax most;
+  ByteMin least;
+  if constexpr (UNITS == 0) {
+    for (int t = 0; t < min(sh.tpu, lanes); ++t) most.add(top[t * row + w]), least.add(bottom[t * row + w]);
+  } else {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int at = (t * kParts + part) * row + w;
+      most.add(top[at]), least.add(bottom[at]);
+    }
+#pragma unroll
+    for (int d = 1; d < kParts; d <<= 1) {
+      most.add(__shfl_xor_sync(0xffffffffu, most.get(), d));
+      least.add(__shfl_xor_sync(0xffffffffu, least.get(), d));
+    }
+    if (part != 0) return;
   }
+  const uint32_t u = most.get(), d = least.get();
   uint32_t* bu = reinterpret_cast<uint32_t*>(c.k_bounds + gh * 2 * c.pitch) + w;
   uint32_t* bl = bu + words;
   const uint32_t ou = keep ? *bu : 0u, ol = keep ? *bl : 0u;
@@ -214,12 +251,13 @@ __device__ __forceinline__ void move_page(const CacheView& c, const SeqView& sq,
   __shared__ int64_t where[64];  // byte offset of a token's row, -1: none
   __shared__ float scales[64];
   const uint8_t* codes = is_v ? c.v : c.k;
+  float my_scale = 0.f;
   if (threadIdx.x < 64) {
     const int t = threadIdx.x, j = t < count ? mine : -1;
     const int from = j >= 0 && j < (sq.width << c.log2_page) ? load_page(sq, c, b, j >> c.log2_page, true) : -1;
     const int64_t fh = static_cast<int64_t>(from) * c.heads + h;
     where[t] = from < 0 ? -1 : ((fh << c.log2_page) + (j & (c.page - 1))) * c.pitch;
-    scales[t] = from < 0 ? 0.f : (is_v ? c.v_scale : c.k_scale)[fh];
+    if (from >= 0) my_scale = (is_v ? c.v_scale : c.k_scale)[fh];
   }
   __syncthreads();
   const Share<UNITS> sh(c.pitch);
@@ -236,37 +274,33 @@ __device__ __forceinline__ void move_page(const CacheView& c, const SeqView& sq,
       x[i][0] = w.x, x[i][1] = w.y, x[i][2] = half ? 0u : w.z, x[i][3] = half ? 0u : w.w;
     }
   }
-  constexpr uint32_t kEven = 0x00ff00ffu, kOdd = 0xff00ff00u;  // bytes, two to a 16-bit comparison each
+  // the codes' loads do not wait for the scales
+  if (threadIdx.x < 64) scales[threadIdx.x] = my_scale;
+  __syncthreads();
   float a = 0.f;
   bool nan = false;
 #pragma unroll
   for (int i = 0; i < Share<UNITS>::kMine; ++i) {
     const int t = sh.first + i * sh.tpu;
     if (sh.active && t < count) {
-      uint32_t me = 0, mo = 0;  // largest |code| of the even and of the odd bytes
+      ByteMax most;  // |code|
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
-        me = max_u16x2(me, x[i][w] & 0x007f007fu), mo = max_u16x2(mo, x[i][w] & 0x7f007f00u);
-      auto largest = [&] { return max(max(me & 0xffu, me >> 16), max((mo >> 8) & 0xffu, mo >> 24)); };
-      if (largest() == 0x7fu) {  // some are NaN, which do not count
+      for (int w = 0; w < 4; ++w) most.add(x[i][w] & 0x7f7f7f7fu);
+      if (most.largest() == 0x7fu) {  // some are NaN, which do not count
         nan = true;
-        me = mo = 0;
+        most = ByteMax();
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t v = x[i][w] & 0x7f7f7f7fu & ~e4m3_nan4(x[i][w]);
-          me = max_u16x2(me, v & kEven), mo = max_u16x2(mo, v & kOdd);
-        }
+        for (int w = 0; w < 4; ++w) most.add(x[i][w] & 0x7f7f7f7fu & ~e4m3_nan4(x[i][w]));
       }
-      a = fmaxf(a, finite_abs(half2_bits_to_float2(e4m3x2_to_f16x2(largest())).x * scales[t]));
+      a = fmaxf(a, finite_abs(half2_bits_to_float2(e4m3x2_to_f16x2(most.largest())).x * scales[t]));
     }
   }
   const float s = page_scale(block_max(a));
   if (threadIdx.x == 0) (is_v ? c.v_scale : c.k_scale)[gh] = s;
-  const float inv = 1.f / s;  // a power of two, at least 2^-120
+  const float inv = __uint_as_float((254u << 23) - __float_as_uint(s));  // 1 / s, a power of two
   uint8_t* rows = (is_v ? c.v : c.k) + (gh << c.log2_page) * c.pitch + sh.unit * 16;
-  uint32_t ue[4], uo[4], de[4], dd[4];  // extremes of the even and of the odd bytes
-#pragma unroll
-  for (int w = 0; w < 4; ++w) ue[w] = uo[w] = 0u, de[w] = kEven, dd[w] = kOdd;
+  ByteMax high[4];
+  ByteMin low[4];
 #pragma unroll
   for (int i = 0; i < Share<UNITS>::kMine; ++i) {
     const int t = sh.first + i * sh.tpu;
@@ -294,14 +328,17 @@ __device__ __forceinline__ void move_page(const CacheView& c, const SeqView& sq,
       }
       *reinterpret_cast<uint4*>(rows + static_cast<int64_t>(t) * c.pitch) =
           make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
-      if (!is_v) {
+      if (!is_v && !nan) {
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           const uint32_t o = e4m3_order4(x[i][w]);
-          uint32_t hi = o, lo = o;
-          if (nan) hi &= ~e4m3_nan4(x[i][w]), lo |= e4m3_nan4(x[i][w]);
-          ue[w] = max_u16x2(ue[w], hi & kEven), uo[w] = max_u16x2(uo[w], hi & kOdd);
-          de[w] = min_u16x2(de[w], lo & kEven), dd[w] = min_u16x2(dd[w], lo & kOdd);
+          high[w].add(o), low[w].add(o);
+        }
+      } else if (!is_v) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t o = e4m3_order4(x[i][w]), no = e4m3_nan4(x[i][w]);
+          high[w].add(o & ~no), low[w].add(o | no);
         }
       }
     }
@@ -309,7 +346,7 @@ __device__ __forceinline__ void move_page(const CacheView& c, const SeqView& sq,
   if (!is_v) {
     uint32_t up[4], dn[4];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) up[w] = ue[w] | uo[w], dn[w] = de[w] | dd[w];
+    for (int w = 0; w < 4; ++w) up[w] = high[w].get(), dn[w] = low[w].get();
     write_bounds(c, sh, gh, count, false, up, dn);
   }
 }
