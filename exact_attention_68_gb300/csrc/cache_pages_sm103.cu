@@ -10,10 +10,10 @@
 //
 // Bytes are what both cannot do without, 6·D a token and head to append and
 // 4·D to move.  Measured at 8 heads of 128 channels: 2 x 8192 tokens appended in
-// 21.1 us = 4.8 TB/s, about 11 instructions a value issued at 57 % of the rate;
-// one token of each of 64 sequences 4.9 us (latency); 8 sequences cut to 4096
-// tokens a head moved in 42 us, 134 MB as random 128-byte rows, behind 16 us
-// for choosing them.
+// 20.8 us = 4.8 TB/s, about 11 instructions a value issued at 57 % of the rate;
+// one token of each of 64 sequences 4.8 us (latency); 8 sequences cut to 4096
+// tokens a head moved in 39 us, 134 MB as random 128-byte rows (a page's chain of
+// loads, position, page, codes; 55 % of the issue rate), behind 13 us for choosing them.
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -85,7 +85,7 @@ struct ByteMin {
 //
 // Rows are parted among neighbouring lanes, four to each, and joined by shuffles;
 // the rows' pitch of 5 words a unit leaves their reads without bank conflicts.
-// (One warp that reads all rows of a word took 1/6 of an eviction's time.)
+// (With one warp that read all rows an eviction's batch took 55.7 us, so 53.8.)
 template <int UNITS>
 __device__ __forceinline__ void write_bounds(const CacheView& c, const Share<UNITS>& sh, int64_t gh, int lanes,
                                              bool keep, const uint32_t (&up)[4], const uint32_t (&dn)[4]) {
@@ -444,8 +444,12 @@ __global__ void __launch_bounds__(kPlanThreads) cache_evict_plan_kernel(const Ca
     out[j] = 0.f;
 }
 
+// Twelve CTAs an SM where 128 channels or fewer allow it, at 40 registers with a few
+// spilled: more loads in flight (a batch's eviction 50.5 us, at 48 registers and ten
+// CTAs 51.7; one CTA for a page's keys and values, with one look-up, 55.2).
 template <int UNITS>
-__global__ void __launch_bounds__(kPageThreads) cache_evict_move_kernel(const CacheEvictParams p) {
+__global__ void __launch_bounds__(kPageThreads, UNITS == 4 || UNITS == 8 ? 12 : 7)
+    cache_evict_move_kernel(const CacheEvictParams p) {
   const bool is_v = blockIdx.x & 1;
   const int i = blockIdx.x >> 1, h = blockIdx.y, b = blockIdx.z;
   wait_for_previous();
