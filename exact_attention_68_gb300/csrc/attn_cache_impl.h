@@ -112,6 +112,12 @@ template <int WIDTH, int TILES>
 constexpr int kCacheWarps = (TILES == 1 ? 12 : 8) / (WIDTH <= 128 ? 1 : 2);
 inline int cache_kernel_warps(int width, int tiles) { return (tiles == 1 ? 12 : 8) / (width <= 128 ? 1 : 2); }
 
+// CTAs of the largest cluster, and how many clusters of `size` the device holds
+// at once (asked for once per device; it depends on how its SMs are grouped, which
+// differs between devices of one kind).
+constexpr int kCacheMaxCluster = 8;
+int cache_fwd_clusters(int dev, int size);
+
 // tiles: 8-row tiles of one pass.
 cudaError_t cache_fwd_launch(const CacheFwdParams& p, int width, int tiles, bool warp_workers, int dev, int ctas,
                              cudaStream_t stream);

@@ -153,7 +153,7 @@ struct Plan {
 // segments of up to 16384 keys, two tiles: 78 us, dealt 53 us.
 constexpr int64_t kSegmentSteps = 16, kFewSegmentSteps = 4;
 Plan plan_of(const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t listed, int64_t q_heads, int64_t T,
-             int sms) {
+             int dev, int sms) {
   Plan p;
   p.width = ea::cache_kernel_width(c->head_dim);
   const int64_t rows = q_heads / c->heads * T;
@@ -162,11 +162,13 @@ Plan plan_of(const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t listed, 
   const int warps = ea::cache_kernel_warps(p.width, p.tiles);
   const int64_t segments = s->batch * c->heads * p.passes;
   const int64_t chunks = score_cols(c, s, listed, listed > 0) / ea::kCacheChunk;  // at most, of a segment
-  // a cluster for each segment: the largest that fills no more than 128 SMs (32
-  // clusters of 4 or 16 of 8 find their place at once) and leaves each CTA four
-  // chunks of the longest segment
+  // a cluster for each segment: the largest of which all find their place at once
+  // (of 8 CTAs 15 or 16 on 152 SMs; one cluster that has to wait doubles the time)
+  // and that leaves each CTA four chunks of the longest segment
   int cluster = 1;
-  while (cluster < 8 && segments * cluster * 2 <= 128 && chunks >= 8 * cluster) cluster *= 2;
+  while (cluster < ea::kCacheMaxCluster && chunks >= 8 * cluster &&
+         segments <= ea::cache_fwd_clusters(dev, 2 * cluster))
+    cluster *= 2;
   const int64_t steps = 2 * segments * cluster >= sms ? kSegmentSteps / (p.tiles > 1 ? 2 : 1) : kFewSegmentSteps;
   p.cluster = segments <= sms && chunks <= steps * warps * cluster ? cluster : 0;
   p.warp_workers = p.cluster == 0 && p.tiles <= ea::kCacheWarpWorkerTiles &&
@@ -288,7 +290,7 @@ size_t attn_cache_fwd_workspace(const attn_cache_t* cache, const attn_cache_seqs
   if (check_cache(cache, seqs) != ATTN_OK || listed < 0 ||
       check_queries(cache, seqs, q_heads, T) != ATTN_OK || !sm_count(&dev, &sms))
     return 0;
-  return fwd_bytes(plan_of(cache, seqs, listed, q_heads, T, sms), cache, seqs, listed, with_mass != 0);
+  return fwd_bytes(plan_of(cache, seqs, listed, q_heads, T, dev, sms), cache, seqs, listed, with_mass != 0);
 }
 
 attn_status_t attn_cache_fwd(const attn_cache_t* cache, const attn_cache_seqs_t* seqs, const void* q,
@@ -314,7 +316,7 @@ attn_status_t attn_cache_fwd(const attn_cache_t* cache, const attn_cache_seqs_t*
   if (s != ATTN_OK) return s;
   int dev = -1, sms = 0;
   if (!sm_count(&dev, &sms)) return ATTN_ERR_CUDA;
-  const Plan plan = plan_of(cache, seqs, listed, q_heads, T, sms);
+  const Plan plan = plan_of(cache, seqs, listed, q_heads, T, dev, sms);
   const size_t need = fwd_bytes(plan, cache, seqs, listed, mass != nullptr);
   if (need > kNoSpace && (!workspace || workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;
   Span spans[14];

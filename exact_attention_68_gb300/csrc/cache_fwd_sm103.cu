@@ -58,6 +58,7 @@ constexpr float kLn2f = 0.6931471805599453f;
 constexpr int kPShift = 14;  // P is 2^14 times the weight relative to r
 constexpr int kFar = 0x7fffff00;  // position of a token that is not there (real ones stay below 2^30)
 constexpr uint64_t kDrainNs = 1000000000ull;
+constexpr int kMaxCluster = kCacheMaxCluster;
 
 enum : int { kSiteCacheK = 0x7500, kSiteCacheV = 0x7600, kChkCacheCopy = 0x7701 };
 
@@ -166,6 +167,17 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, int rank) {
       "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
       "ld.shared::cluster.f32 %0, [a];\n\t}"
       : "=f"(v)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr, int rank) {
+  float2 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\t"
+      "ld.shared::cluster.v2.f32 {%0, %1}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y)
       : "r"(addr), "r"(rank)
       : "memory");
   return v;
@@ -876,25 +888,41 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
           }
       }
       __syncthreads();
-      auto joined = [&](int row, float* mm, float* rr, float* ll) {
-        float M = -INFINITY, R = -INFINITY, S = 0.f;
+      // Thread `row` joins the warps' statistics of its row, once for all: m, r and
+      // the factor of O then stand in the first warp's place, which only it reads.
+      if (threadIdx.x < kRows) {
+        const int row = threadIdx.x;
+        float mw[L::kWarps], M = -INFINITY, R = -INFINITY, S = 0.f;
+#pragma unroll
         for (int w = 0; w < L::kWarps; ++w) {
-          M = fmaxf(M, ld_shared_f32(stat + (w * kRows + row) * 12));
-          R = fmaxf(R, ld_shared_f32(stat + (w * kRows + row) * 12 + 4));
+          mw[w] = ld_shared_f32(stat + (w * kRows + row) * 12);
+          M = fmaxf(M, mw[w]), R = fmaxf(R, ld_shared_f32(stat + (w * kRows + row) * 12 + 4));
         }
-        for (int w = 0; w < L::kWarps; ++w) {
-          const float mw = ld_shared_f32(stat + (w * kRows + row) * 12);
-          S += mw == -INFINITY ? 0.f : ld_shared_f32(stat + (w * kRows + row) * 12 + 8) * ex2_approx(mw - M);
+#pragma unroll
+        for (int w = 0; w < L::kWarps; ++w)
+          S += mw[w] == -INFINITY ? 0.f : ld_shared_f32(stat + (w * kRows + row) * 12 + 8) * ex2_approx(mw[w] - M);
+        st_shared_f32(stat + row * 12, M);
+        st_shared_f32(stat + row * 12 + 4, R);
+        st_shared_f32(stat + row * 12 + 8, factor(M, R, S));
+        if (cluster > 1) {
+          st_shared_f32(sb + kSumStat + row * 12, M);
+          st_shared_f32(sb + kSumStat + row * 12 + 4, R);
+          st_shared_f32(sb + kSumStat + row * 12 + 8, S);
+        } else if (!whole) {
+          part_stat[row] = M;
+          part_stat[kRows + row] = R;
+          part_stat[2 * kRows + row] = S;
+        } else if (live(row)) {
+          p.lse[row_place(p, cs.b, h, tile_row + row)] = (M + log2f(S)) * kLn2f;
         }
-        *mm = M, *rr = R, *ll = S;
-      };
+      }
+      __syncthreads();
       float beta[NT][2];
 #pragma unroll
       for (int b = 0; b < NT; ++b)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float M, R, S;
-          joined(8 * b + 2 * t4 + i, &M, &R, &S);
+          const float R = ld_shared_f32(stat + (8 * b + 2 * t4 + i) * 12 + 4);
           beta[b][i] = of(r[b], i) == -INFINITY ? 0.f : ex2_approx(of(r[b], i) - R);
         }
       // two neighbouring columns of a row per thread
@@ -923,54 +951,56 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
           } else if (!whole) {
             *reinterpret_cast<float2*>(part + row * WIDTH + ch) = make_float2(x, y);
           } else if (ch < p.c.D && live(row)) {
-            float M, R, S;
-            joined(row, &M, &R, &S);
-            const float w = factor(M, R, S);
-            const bool none = M == -INFINITY;
+            const float w = ld_shared_f32(stat + row * 12 + 8);
+            const bool none = ld_shared_f32(stat + row * 12) == -INFINITY;
             *reinterpret_cast<uint32_t*>(p.out + row_place(p, cs.b, h, tile_row + row) * p.c.D + ch) =
                 pack_16bit(p.f16, none ? 0.f : x * w, none ? 0.f : y * w);
           }
         }
         __syncthreads();
       }
-      if (threadIdx.x < kRows) {
-        const int row = threadIdx.x;
-        float M, R, S;
-        joined(row, &M, &R, &S);
-        if (cluster > 1) {
-          st_shared_f32(sb + kSumStat + row * 12, M);
-          st_shared_f32(sb + kSumStat + row * 12 + 4, R);
-          st_shared_f32(sb + kSumStat + row * 12 + 8, S);
-        } else if (!whole) {
-          part_stat[row] = M;
-          part_stat[kRows + row] = R;
-          part_stat[2 * kRows + row] = S;
-        } else if (live(row)) {
-          p.lse[row_place(p, cs.b, h, tile_row + row)] = (M + log2f(S)) * kLn2f;
-        }
-      }
-      __syncthreads();  // the statistics are rewritten for the next segment
       if (cluster > 1) {
         // the CTAs' sums, now at the front of each one's ring (whose copies have
         // all been used): each CTA joins every kRows · WIDTH / cluster-th pair
         cluster_barrier();
+        // thread `row` first: each CTA's factor, in the place of the warps' statistics
+        static_assert((kMaxCluster + 1) * 4 <= L::kWarps * 12, "a row's factors must fit its statistics");
+        if (threadIdx.x < kRows) {
+          const int row = threadIdx.x;
+          float mk[kMaxCluster], f[kMaxCluster], M = -INFINITY, S = 0.f;
+#pragma unroll
+          for (int k = 0; k < kMaxCluster; ++k) {
+            mk[k] = k < cluster ? ld_cluster_f32(sb + kSumStat + row * 12, k) : -INFINITY;
+            f[k] = k < cluster ? ld_cluster_f32(sb + kSumStat + row * 12 + 4, k) : 0.f;
+            M = fmaxf(M, mk[k]);
+          }
+#pragma unroll
+          for (int k = 0; k < kMaxCluster; ++k) {
+            if (mk[k] != -INFINITY) S += ld_cluster_f32(sb + kSumStat + row * 12 + 8, k) * ex2_approx(mk[k] - M);
+            f[k] = mk[k] == -INFINITY ? 0.f : ex2_approx(f[k] - M - kPShift);
+          }
+#pragma unroll
+          for (int k = 0; k < kMaxCluster; ++k) st_shared_f32(stat + (k * kRows + row) * 4, f[k]);
+          st_shared_f32(stat + (kMaxCluster * kRows + row) * 4, S > 0.f || S != S ? 1.f / S : 0.f);
+          if (rank == 0 && live(row)) p.lse[row_place(p, cs.b, h, tile_row + row)] = (M + log2f(S)) * kLn2f;
+        }
+        __syncthreads();
         for (int i = rank * kThreads + threadIdx.x; i < kRows * WIDTH / 2; i += cluster * kThreads) {
           const int row = i / (WIDTH / 2), ch = 2 * (i % (WIDTH / 2));
           if (ch >= p.c.D || !live(row)) continue;
-          float M = -INFINITY, S = 0.f, x = 0.f, y = 0.f;
-          for (int k = 0; k < cluster; ++k) M = fmaxf(M, ld_cluster_f32(sb + kSumStat + row * 12, k));
-          for (int k = 0; k < cluster && M != -INFINITY; ++k) {
-            const uint32_t st = sb + kSumStat + row * 12, from = sb + (row * WIDTH + ch) * 4;
-            const float mk = ld_cluster_f32(st, k);
-            if (mk == -INFINITY) continue;
-            S += ld_cluster_f32(st + 8, k) * ex2_approx(mk - M);
-            const float f = ex2_approx(ld_cluster_f32(st + 4, k) - M - kPShift);
-            x += ld_cluster_f32(from, k) * f, y += ld_cluster_f32(from + 4, k) * f;
+          float2 v[kMaxCluster];
+#pragma unroll
+          for (int k = 0; k < kMaxCluster; ++k)
+            v[k] = k < cluster ? ld_cluster_f32x2(sb + (row * WIDTH + ch) * 4, k) : make_float2(0.f, 0.f);
+          float x = 0.f, y = 0.f;
+#pragma unroll
+          for (int k = 0; k < kMaxCluster; ++k) {
+            const float f = ld_shared_f32(stat + (k * kRows + row) * 4);
+            if (f != 0.f) x += v[k].x * f, y += v[k].y * f;
           }
-          const int64_t to = row_place(p, cs.b, h, tile_row + row);
-          const float inv = S > 0.f || S != S ? 1.f / S : 0.f;
-          *reinterpret_cast<uint32_t*>(p.out + to * p.c.D + ch) = pack_16bit(p.f16, x * inv, y * inv);
-          if (ch == 0) p.lse[to] = (M + log2f(S)) * kLn2f;
+          const float inv = ld_shared_f32(stat + (kMaxCluster * kRows + row) * 4);
+          *reinterpret_cast<uint32_t*>(p.out + row_place(p, cs.b, h, tile_row + row) * p.c.D + ch) =
+              pack_16bit(p.f16, x * inv, y * inv);
         }
         cluster_barrier();  // no CTA ends while another reads its memory
       }
@@ -1128,6 +1158,35 @@ cudaError_t launch_width(const CacheFwdParams& p, bool warp_workers, int tiles, 
 }
 
 }  // namespace
+
+int cache_fwd_clusters(int dev, int size) {
+  if (size <= 1 || size > kMaxCluster) return 0;
+  constexpr int kSizes = kMaxCluster + 1;
+  static std::atomic<int> known[64 * kSizes];  // one more than the answer; 0: not asked yet
+  std::atomic<int>& slot = known[dev * kSizes + size];
+  int n = slot.load(std::memory_order_relaxed) - 1;
+  if (n >= 0) return n;
+  // any of the kernels: each fills an SM with one CTA
+  using L = CacheFwdLayout<128, kCacheWarps<128, 1>, 1>;
+  auto kern = cache_fwd_kernel<128, kCacheWarps<128, 1>, 1>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(size);
+  cfg.blockDim = dim3(L::kWarps * 32);
+  cfg.dynamicSmemBytes = L::kAlloc;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  slot.store(n + 1, std::memory_order_relaxed);
+  return n;
+}
 
 cudaError_t cache_fwd_launch(const CacheFwdParams& p, int width, int tiles, bool warp_workers, int dev, int ctas,
                              cudaStream_t stream) {
