@@ -93,8 +93,9 @@ struct CacheFwdParams {
   float scale_log2;
   int cluster;         // CTAs of the cluster that has a segment; 0: chunks are dealt to workers
   int workers;         // parts the chunks of all (sequence, head, row tile) are dealt to
-  int min_chunks;      // fewest chunks worth a worker of their own
-  int* line;           // workspace: first chunk of each sequence in the line, then its end
+  int lead;            // what a segment costs by itself, in chunks
+  int min_units;       // fewest chunks, with a lead, worth a worker of their own
+  int* line;           // workspace: first unit of each sequence in the line, then its end
   float* part;         // workspace: partial results, two slots per worker
   float* scores;       // workspace: scaled scores in log2 units, or null (no mass)
   int score_cols;      // keys of a head in `scores`

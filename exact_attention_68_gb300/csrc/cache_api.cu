@@ -113,6 +113,12 @@ int tiles_of(int64_t rows, int width) {
   return static_cast<int>((rows + per - 1) / per);
 }
 
+// What a segment costs besides its chunks (Q, the join, the output), in a worker's
+// chunks.  480 segments of 1 to 32 chunks, a CTA a worker: 52.8 us at 0, 44.7 at 4,
+// 31.0 at 12, 30.3 at 16, 31.3 at 24; 960 of two tiles, a warp a worker: 99 us at 0,
+// 79 at 1, 72 at 2, but 720 of 3 chunks 21.9, 19.8 and 22.0.
+constexpr int kWarpLead = 1, kCtaLead = 16;
+
 // Sizes of the queries; touches no CUDA API.
 attn_status_t check_queries(const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t q_heads,
                             int64_t T) {
@@ -122,7 +128,7 @@ attn_status_t check_queries(const attn_cache_t* c, const attn_cache_seqs_t* s, i
   // query rows and the chunks of the longest call are counted in 32 bits
   const int64_t chunks = (s->width * c->page + ea::kCacheChunk - 1) / ea::kCacheChunk;
   const int64_t segments = s->batch * c->heads * passes_of(q_heads / c->heads * T, ea::cache_kernel_width(c->head_dim));  // < 2^52
-  if (s->batch * q_heads > INT32_MAX / T || segments > (1ll << 30) / chunks) return ATTN_ERR_INVALID_ARG;
+  if (s->batch * q_heads > INT32_MAX / T || segments > (1ll << 30) / (chunks + kCtaLead)) return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
 }
 
@@ -132,12 +138,12 @@ int64_t score_cols(const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t li
   return (pages * c->page + ea::kCacheChunk - 1) / ea::kCacheChunk * ea::kCacheChunk;
 }
 
-// How the chunks are dealt.  With many segments, or more than SMs and short
-// ones, a warp is a worker: nothing has to be joined but at a worker's two ends.
-// Otherwise a CTA is one: its warps' results are joined in shared memory, a
-// twelfth of the parts go through the workspace.  160 segments of 16, 63 chunks:
-// a warp each 20.6, 45.6 us, a CTA 22.4, 40.9 us; 720 of 3 chunks 21 and 36 us; 512
-// of 16 chunks 40 and 46 us.
+// How the chunks are dealt.  With more short segments than SMs a warp is a
+// worker: nothing has to be joined but at a worker's two ends.  Otherwise a CTA is
+// one: its warps' results are joined in shared memory, a twelfth of the parts go
+// through the workspace.  320 segments of 8, 32 chunks: a warp each 19, 43 us, a
+// CTA 21, 40 us; 720 of 3, 16 chunks 18, 48 and 30, 51 us; 1024 of 16, 32, 64 chunks 64,
+// 101, 181 and 68, 96, 168 us, of 2 to 32 chunks 70 and 79 us.
 constexpr int64_t kShortSegment = 16;
 struct Plan {
   int width, tiles, passes, ctas, workers;
@@ -147,11 +153,13 @@ struct Plan {
 // Steps of a warp up to which a segment is left to its own cluster: that saves
 // the deal and the join, about 5 us and a launch, and one CTA streams at about
 // twice its even share of the memory's rate, so that lengths may differ by two
-// before it loses (half of that with two tiles, whose products bound the step).
-// 128 segments of 2048, 4096, 8192 keys: 15, 27, 46 us, dealt 21, 32, 51 us; 32
-// segments of 64 listed pages, clusters of 4: 13.6 us, dealt 18.6 us; 48 ragged
-// segments of up to 16384 keys, two tiles: 78 us, dealt 53 us.
-constexpr int64_t kSegmentSteps = 16, kFewSegmentSteps = 4;
+// before it loses; fewer with two tiles, whose products bound the step, and where
+// the clusters leave a quarter of the SMs empty.  128 segments of 2048, 4096, 8192
+// keys: 14, 28, 46 us, dealt 19, 32, 54 us; of 128 to 2048, 256 to 4096, 512 to 8192
+// keys 14, 22, 38 and 18, 23, 37 us; 32 segments of 64 listed pages, clusters of 4: 12.7
+// us, dealt 18 us; 48 segments of 4096, 8192 keys, clusters of 2: 15, 24 us, dealt 17, 22
+// us.
+constexpr int64_t kSegmentSteps = 12, kTilesSegmentSteps = 8, kFewSegmentSteps = 4;
 Plan plan_of(const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t listed, int64_t q_heads, int64_t T,
              int dev, int sms) {
   Plan p;
@@ -169,10 +177,13 @@ Plan plan_of(const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t listed, 
   while (cluster < ea::kCacheMaxCluster && chunks >= 8 * cluster &&
          segments <= ea::cache_fwd_clusters(dev, 2 * cluster))
     cluster *= 2;
-  const int64_t steps = 2 * segments * cluster >= sms ? kSegmentSteps / (p.tiles > 1 ? 2 : 1) : kFewSegmentSteps;
+  const int64_t steps = 4 * segments * cluster < 3 * sms ? kFewSegmentSteps
+                        : p.tiles > 1                   ? kTilesSegmentSteps
+                                                        : kSegmentSteps;
   p.cluster = segments <= sms && chunks <= steps * warps * cluster ? cluster : 0;
   p.warp_workers = p.cluster == 0 && p.tiles <= ea::kCacheWarpWorkerTiles &&
-                   (segments >= static_cast<int64_t>(sms) * warps / 2 || (segments > sms && chunks <= kShortSegment));
+                   segments > sms &&
+                   chunks <= kShortSegment * (segments >= static_cast<int64_t>(sms) * warps / 2 ? 2 : 1);
   p.ctas = p.cluster > 0 ? static_cast<int>(segments) * p.cluster : sms;
   p.workers = p.cluster > 0 ? 0 : p.warp_workers ? sms * warps : sms;
   return p;
@@ -352,7 +363,8 @@ attn_status_t attn_cache_fwd(const attn_cache_t* cache, const attn_cache_seqs_t*
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.cluster = plan.cluster;
   p.workers = plan.workers;
-  p.min_chunks = plan.warp_workers ? 1 : 4;
+  p.lead = plan.cluster > 0 ? 0 : plan.warp_workers ? kWarpLead : kCtaLead;
+  p.min_units = p.lead + (plan.warp_workers ? 1 : 4);
   char* space = static_cast<char*>(workspace);
   p.line = reinterpret_cast<int*>(space);
   p.part = reinterpret_cast<float*>(space + line_bytes(plan, seqs));

@@ -205,27 +205,32 @@ __device__ __forceinline__ int seq_chunks(const CacheFwdParams& p, int b, bool r
   return max(1, ((read << p.c.log2_page) + kCacheChunk - 1) / kCacheChunk);
 }
 
-// The deal: chunks of every segment in line, sequence by sequence.
+// The deal: the segments in line, sequence by sequence, each p.lead units for what
+// a segment costs by itself (Q, the join, the output) and one for each chunk.  A
+// worker has the chunks of an even piece of the line; without the lead the ones
+// that met many short segments ended last.
 struct Deal {
-  int total;  // chunks in line
-  int per;    // chunks of a worker
+  int total;  // units in line
+  int per;    // units of a worker
 };
-__device__ __forceinline__ int chunks_per_worker(const CacheFwdParams& p, int total) {
-  return max((total + p.workers - 1) / p.workers, p.min_chunks);
+// Units of a segment of nc chunks.
+__device__ __forceinline__ int segment_units(const CacheFwdParams& p, int nc) { return nc > 0 ? nc + p.lead : 0; }
+__device__ __forceinline__ int units_per_worker(const CacheFwdParams& p, int total) {
+  return max((total + p.workers - 1) / p.workers, p.min_units);
 }
 __device__ __forceinline__ Deal deal_chunks(const CacheFwdParams& p, bool report) {
   const int lane = threadIdx.x & 31, hr = p.c.heads * p.row_tiles;
   int sum = 0;
   for (int b = lane; b < p.s.batch; b += 32) {
     int len, n;
-    sum += hr * seq_chunks(p, b, report, &len, &n);
+    sum += hr * segment_units(p, seq_chunks(p, b, report, &len, &n));
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  return {sum, chunks_per_worker(p, sum)};
+  return {sum, units_per_worker(p, sum)};
 }
 
-// Writes where each sequence's chunks begin in the line, and its end, for the
+// Writes where each sequence's segments begin in the line, and its end, for the
 // join.  One warp.
 __device__ __forceinline__ void write_line(const CacheFwdParams& p) {
   const int lane = threadIdx.x & 31, hr = p.c.heads * p.row_tiles;
@@ -233,7 +238,7 @@ __device__ __forceinline__ void write_line(const CacheFwdParams& p) {
   for (int b0 = 0; b0 < p.s.batch; b0 += 32) {
     const int b = b0 + lane;
     int len, n;
-    const int mine = b < p.s.batch ? hr * seq_chunks(p, b, false, &len, &n) : 0;
+    const int mine = b < p.s.batch ? hr * segment_units(p, seq_chunks(p, b, false, &len, &n)) : 0;
     int upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -252,7 +257,8 @@ struct Segment {
   int first, nc; // its chunks: first .. first + nc - 1
   int len, n;
 };
-// The segment that holds chunk `at` (< total).  Whole warp.
+// The segment that holds unit `at` (< total); its chunks are counted by their
+// units.  Whole warp.
 __device__ __forceinline__ Segment find_segment(const CacheFwdParams& p, int at) {
   const int lane = threadIdx.x & 31, hr = p.c.heads * p.row_tiles;
   int before = 0;
@@ -260,7 +266,7 @@ __device__ __forceinline__ Segment find_segment(const CacheFwdParams& p, int at)
     const int b = b0 + lane;
     int len = 0, n = 0;
     const int nc = b < p.s.batch ? seq_chunks(p, b, false, &len, &n) : 0;
-    int upto = nc * hr;
+    int upto = segment_units(p, nc) * hr;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xffffffffu, upto, d);
@@ -274,16 +280,17 @@ __device__ __forceinline__ Segment find_segment(const CacheFwdParams& p, int at)
       s.nc = __shfl_sync(0xffffffffu, nc, src);
       s.len = __shfl_sync(0xffffffffu, len, src);
       s.n = __shfl_sync(0xffffffffu, n, src);
-      const int base = before + __shfl_sync(0xffffffffu, upto, src) - s.nc * hr;
-      const int x = s.nc > 0 ? (at - base) / s.nc : 0;
+      const int units = segment_units(p, s.nc), base = before + __shfl_sync(0xffffffffu, upto, src) - units * hr;
+      const int x = units > 0 ? (at - base) / units : 0;
       s.h = x / p.row_tiles, s.rt = x % p.row_tiles;
-      s.first = base + x * s.nc;
+      s.first = base + x * units + p.lead;
       return s;
     }
     before += __shfl_sync(0xffffffffu, upto, 31);
   }
 }
-// Moves to the next segment; false behind the last.
+// Moves to the next segment, whose chunks are counted on without its lead; false
+// behind the last.
 __device__ __forceinline__ bool next_segment(const CacheFwdParams& p, Segment& s) {
   s.first += s.nc;
   if (++s.rt < p.row_tiles) return true;
@@ -431,6 +438,8 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
     end = min(begin + deal.per, deal.total);
     if (begin >= end) return;  // the whole worker; with WORKER > 1 the whole CTA
     cs = find_segment(p, begin);
+    begin = max(begin, cs.first);
+    if (begin >= end) return;  // a piece of a lead
   }
 
   const int seg_rows = p.G * p.s.T;
@@ -440,6 +449,7 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
   // ---------------- fetching: chunks begin + wi, + WORKER, ... of the line
   Segment fs = cs;
   int f_at = begin + wi;      // next chunk to fetch K of
+  int f_end = end;            // past the last, less the leads up to here
   int f_page = -1, f_pos = kFar;  // this lane's 16-token group (t4) of it
   bool f_have = false;
   int i_slot = 0;             // slot of the next item
@@ -449,11 +459,14 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
   int issued = 0, used = 0;   // items (K or V of a chunk)
 
   auto look_up = [&]() {  // pages of chunk f_at
-    f_have = f_at < end;
     f_page = -1;
     f_pos = kFar;
+    while (f_at < f_end && f_at >= fs.first + fs.nc) {
+      next_segment(p, fs);
+      f_end -= p.lead;
+    }
+    f_have = f_at < f_end;
     if (!f_have) return;
-    while (f_at >= fs.first + fs.nc) next_segment(p, fs);
     const int tok = (f_at - fs.first) * kCacheChunk + 16 * t4;
     int i = tok >> log2p;
     bool in = true;
@@ -546,7 +559,11 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
   bool alive = true;
   int seg_at = begin;
   do {
-    while (seg_at >= cs.first + cs.nc && cluster == 0) next_segment(p, cs);
+    while (seg_at < end && seg_at >= cs.first + cs.nc) {
+      next_segment(p, cs);
+      end -= p.lead;
+    }
+    if (seg_at >= end && cluster == 0) break;
     const int seg_end = min(end, cs.first + cs.nc);
     const int h = cs.h, tile_row = cs.rt * kRows, tile_rows = min(kRows, seg_rows - tile_row);
 
@@ -822,7 +839,7 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
       __syncwarp();
       issue();
     }
-    if (seg_end == end) launch_dependents();  // the join may be set up meanwhile
+    if (end - seg_end <= p.lead) launch_dependents();  // no chunk behind: the join may be set up meanwhile
 #pragma unroll
     for (int b = 0; b < NT; ++b) l[b] = make_float2(keys_sum(l[b].x), keys_sum(l[b].y));
     // row i (0, 1) of a pair
@@ -1032,9 +1049,9 @@ __global__ void __launch_bounds__(kJoinThreads * NT) cache_join_kernel(const __g
   // kernel has ended too.  lens, fresh were there before that kernel began.
   wait_for_previous();
   launch_dependents();
-  const int at = p.line[b], nc = (p.line[b + 1] - at) / hr, total = p.line[p.s.batch];
-  if (nc == 0) return;
-  const int per = chunks_per_worker(p, total), first = at + x * nc;
+  const int at = p.line[b], units = (p.line[b + 1] - at) / hr, total = p.line[p.s.batch];
+  if (units == 0) return;
+  const int nc = units - p.lead, per = units_per_worker(p, total), first = at + x * units + p.lead;
   const int w0 = first / per, w1 = (first + nc - 1) / per;
   if (w0 == w1) return;  // one worker had it all
   const int h = x / p.row_tiles, tile_row = (x % p.row_tiles) * kRows;
