@@ -63,9 +63,17 @@ constexpr int kMaxCluster = kCacheMaxCluster;
 enum : int { kSiteCacheK = 0x7500, kSiteCacheV = 0x7600, kChkCacheCopy = 0x7701 };
 
 // WIDTH: 64, 128 or 256 channels; WORKER: warps of one worker (all of the
-// CTA's, or 1); NT: 8-row tiles of queries in one pass
-template <int WIDTH, int WORKER, int NT>
+// CTA's, or 1); NT: 8-row tiles of queries in one pass; PACKED: a chunk's rows lie
+// in shared memory as in the pool, one behind the other.
+//
+// Tiled copies swizzle rows of 64 or 128 bytes, but where a token's row is an odd
+// number of 16-byte units its start is off the 32-byte sectors every other time,
+// and they slow down: 48 segments of 48000 keys of 80 channels took 135 us, of 96
+// channels 87.  Such rows need no swizzle, since an odd pitch keeps eight rows in
+// different banks, so that whole pages come as one run of bytes: 70 to 77 us.
+template <int WIDTH, int WORKER, int NT, bool PACKED>
 struct CacheFwdLayout {
+  static constexpr bool kPacked = PACKED;
   static constexpr int kRows = 8 * NT;
   static constexpr int kWarps = kCacheWarps<WIDTH, NT>;
   static constexpr int kRowBytes = WIDTH >= 128 ? 128 : 64;  // one swizzled row
@@ -133,6 +141,14 @@ __device__ __forceinline__ void tma_load_3d_plain(uint32_t dst, const CUtensorMa
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5}], [%2];"
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// `bytes` from global memory, all multiples of 16.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+      ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
       : "memory");
 }
 
@@ -330,17 +346,25 @@ __device__ __forceinline__ float2 unpack_16bit(bool f16, uint32_t w) {
 __device__ __forceinline__ int row_position(uint32_t md, int row) {
   return ld_volatile_shared(md + (row >> 4) * 16) + (row & 15);
 }
+// Address of unit i (16 channels) of a chunk's row.
+template <class L>
+__device__ __forceinline__ uint32_t code_at(uint32_t slot, int row, int i, int pitch) {
+  if constexpr (L::kPacked) return slot + row * pitch + 16 * i;
+  constexpr int kUnits = L::kRowBytes / 16;
+  const int sw = kUnits == 8 ? (row & 7) : ((row >> 1) & 3);
+  return slot + (i / kUnits) * L::kBlockBytes + row * L::kRowBytes + (((i % kUnits) ^ sw) << 4);
+}
 // Zeroes the rows that hold no token of the sequence (they may hold anything,
 // and 0 · NaN is NaN); true if a row that only some of the queries may see
 // (positions above first_last) holds a NaN code.
 template <class L>
-__device__ __noinline__ bool clear_absent(uint32_t vslot, uint32_t md, int first_last, int len) {
+__device__ __noinline__ bool clear_absent(uint32_t vslot, uint32_t md, int first_last, int len, int pitch) {
   bool nan = false;
   for (int row = threadIdx.x & 31; row < kCacheChunk; row += 32) {
     const int pos = row_position(md, row);
     if (pos <= first_last) continue;
-    for (int i = 0; i < L::kSlot / kCacheChunk / 16; ++i) {
-      const uint32_t at = vslot + (16 * i / L::kRowBytes) * L::kBlockBytes + row * L::kRowBytes + 16 * i % L::kRowBytes;
+    for (int i = 0; i < pitch / 16; ++i) {
+      const uint32_t at = code_at<L>(vslot, row, i, pitch);
       if (pos >= len) {
         st_shared_v4(at, 0, 0, 0, 0);
       } else {
@@ -354,12 +378,12 @@ __device__ __noinline__ bool clear_absent(uint32_t vslot, uint32_t md, int first
 }
 // Zeroes the NaN codes of the rows between first_last and len.
 template <class L>
-__device__ __noinline__ void clear_nan(uint32_t vslot, uint32_t md, int first_last, int len) {
+__device__ __noinline__ void clear_nan(uint32_t vslot, uint32_t md, int first_last, int len, int pitch) {
   for (int row = threadIdx.x & 31; row < kCacheChunk; row += 32) {
     const int pos = row_position(md, row);
     if (pos <= first_last || pos >= len) continue;
-    for (int i = 0; i < L::kSlot / kCacheChunk / 16; ++i) {
-      const uint32_t at = vslot + (16 * i / L::kRowBytes) * L::kBlockBytes + row * L::kRowBytes + 16 * i % L::kRowBytes;
+    for (int i = 0; i < pitch / 16; ++i) {
+      const uint32_t at = code_at<L>(vslot, row, i, pitch);
       const uint4 w = ld_shared_v4(at);
       st_shared_v4(at, w.x & ~e4m3_nan4(w.x), w.y & ~e4m3_nan4(w.y), w.z & ~e4m3_nan4(w.z), w.w & ~e4m3_nan4(w.w));
     }
@@ -368,24 +392,21 @@ __device__ __noinline__ void clear_nan(uint32_t vslot, uint32_t md, int first_la
 }
 // The first position above first_last whose row holds a NaN code in channel ch.
 template <class L>
-__device__ __noinline__ int first_nan(uint32_t vslot, uint32_t md, int ch, int first_last, int len) {
-  constexpr int kUnits = L::kRowBytes / 16;
+__device__ __noinline__ int first_nan(uint32_t vslot, uint32_t md, int ch, int first_last, int len, int pitch) {
   int first = kFar;
   for (int row = 0; row < kCacheChunk; ++row) {
     const int pos = row_position(md, row);
     if (pos <= first_last || pos >= len) continue;
-    const int unit = (ch >> 4) % kUnits, sw = kUnits == 8 ? (row & 7) : ((row >> 1) & 3);
-    const uint32_t at = vslot + (ch >> 4) / kUnits * L::kBlockBytes + row * L::kRowBytes + ((unit ^ sw) << 4);
-    const uint32_t w = static_cast<uint32_t>(ld_volatile_shared(at + (ch & 12)));
+    const uint32_t w = static_cast<uint32_t>(ld_volatile_shared(code_at<L>(vslot, row, ch >> 4, pitch) + (ch & 12)));
     if (((w >> (8 * (ch & 3))) & 0x7fu) == 0x7fu) first = min(first, pos);
   }
   return first;
 }
 
-template <int WIDTH, int WORKER, int NT>
-__global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32, 1)
+template <int WIDTH, int WORKER, int NT, bool PACKED>
+__global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT, PACKED>::kWarps * 32, 1)
     cache_fwd_kernel(const __grid_constant__ CacheFwdParams p) {
-  using L = CacheFwdLayout<WIDTH, WORKER, NT>;
+  using L = CacheFwdLayout<WIDTH, WORKER, NT, PACKED>;
   constexpr int kRows = L::kRows;
   constexpr int kKSteps = WIDTH / 64;  // 64-channel blocks of K·Qᵀ
   constexpr int kTiles = WIDTH / 16;   // 16-channel tiles of Oᵀ
@@ -444,6 +465,8 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
 
   const int seg_rows = p.G * p.s.T;
   const int log2p = p.c.log2_page, page_mask = p.c.page - 1;
+  // bytes of a row that hold channels: all that are read where rows are packed
+  const int row_pitch = PACKED ? p.c.pitch : L::kBlocks * L::kRowBytes;
   const bool one_page = p.c.page == kCacheChunk;  // of a chunk
 
   // ---------------- fetching: chunks begin + wi, + WORKER, ... of the line
@@ -516,12 +539,16 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
     const uint32_t leads = __ballot_sync(0xffffffffu, lead);
     const uint32_t bar = bars + 8 * i_slot;
     if (lane == 0) {
-      if (leads != 0) mbar_arrive_expect_tx(bar, __popc(leads) * L::kBlocks * p.c.page * L::kRowBytes);
+      if (leads != 0) mbar_arrive_expect_tx(bar, __popc(leads) * p.c.page * row_pitch);
       else mbar_arrive(bar);
     }
     __syncwarp();
     const int64_t gh = static_cast<int64_t>(f_page) * p.c.heads + fs.h;
-    if (lead) {
+    if (PACKED) {
+      const uint32_t dst = ring + i_slot * L::kSlot + 16 * t4 * row_pitch, bytes = p.c.page * row_pitch;
+      if (lead && dbg_smem(dbb, dst, bytes, 16, kChkCacheCopy) && dbg(gh >= 0 && gh < dbb.slices, dbb, kChkCacheCopy))
+        bulk_load(dst, (f_is_v ? p.c.v : p.c.k) + gh * static_cast<int64_t>(bytes), bytes, bar);
+    } else if (lead) {
 #pragma unroll
       for (int cb = 0; cb < L::kBlocks; ++cb) {
         const uint32_t dst = ring + i_slot * L::kSlot + cb * L::kBlockBytes + 16 * t4 * L::kRowBytes;
@@ -642,7 +669,6 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
       if (alive) alive = __all_sync(0xffffffffu, wait_copy(bars + 8 * u_slot, u_parity, ctl, kSiteCacheK));
       if (!alive) continue;
       const uint32_t kslot = ring + u_slot * L::kSlot;
-      constexpr int kUnits = L::kRowBytes / 16;
       float2 s[4][NT][2];  // key row0 + 2·hf of 16-key tile g, the two rows of tile b: [g][b][hf]
 #pragma unroll
       for (int g = 0; g < 4; ++g)
@@ -659,16 +685,16 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
           qw[b][4] = x1.x, qw[b][5] = x1.y, qw[b][6] = x1.z, qw[b][7] = x1.w;
         }
         const int unit = kb * 4 + t4;  // 16 channels
-        const uint32_t block = kslot + (unit / kUnits) * L::kBlockBytes;
-        const int cu = unit % kUnits;
+        // packed rows end with the pool's channels, their last unit perhaps in padding,
+        // which may hold anything (Q is zero there, but 0 · NaN is NaN)
+        const bool none = PACKED && 16 * unit >= p.c.D, half = PACKED && 16 * unit + 8 >= p.c.D;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           uint4 kw[2];
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            const int row = row0 + 16 * g + 2 * hf;
-            const int sw = kUnits == 8 ? (row & 7) : ((row >> 1) & 3);
-            kw[hf] = ld_shared_v4(block + row * L::kRowBytes + ((cu ^ sw) << 4));
+            kw[hf] = none ? make_uint4(0, 0, 0, 0) : ld_shared_v4(code_at<L>(kslot, row0 + 16 * g + 2 * hf, unit, row_pitch));
+            if (half) kw[hf].z = kw[hf].w = 0;
           }
           const uint32_t x[4] = {kw[0].x, kw[0].y, kw[0].z, kw[0].w}, y[4] = {kw[1].x, kw[1].y, kw[1].z, kw[1].w};
 #pragma unroll
@@ -794,14 +820,14 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
       const uint32_t vslot = ring + u_slot * L::kSlot;
       if (tail) {
         const uint32_t md = meta + u_meta * 64;
-        if (__any_sync(0xffffffffu, clear_absent<L>(vslot, md, first_last, cs.len))) {
+        if (__any_sync(0xffffffffu, clear_absent<L>(vslot, md, first_last, cs.len, row_pitch))) {
           // A NaN code that some rows may see and others may not: the ones that
           // may get it now, then it counts as zero.
 #pragma unroll
           for (int u = 0; u < kTiles; ++u)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-              const int from = first_nan<L>(vslot, md, 16 * u + gid + 8 * hf, first_last, cs.len);
+              const int from = first_nan<L>(vslot, md, 16 * u + gid + 8 * hf, first_last, cs.len, row_pitch);
 #pragma unroll
               for (int b = 0; b < NT; ++b) {
                 if (from <= last[b][0]) o[u][b][hf].x = __int_as_float(0x7fffffff);
@@ -809,7 +835,7 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
               }
             }
           __syncwarp();
-          clear_nan<L>(vslot, md, first_last, cs.len);
+          clear_nan<L>(vslot, md, first_last, cs.len, row_pitch);
         }
         __syncwarp();
       }
@@ -818,10 +844,8 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT>::kWarps * 32
         if (16 * u < p.c.D) {
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const int row = 16 * g + vrow, unit = (u + (lane >> 4)) % kUnits;
-            const int sw = kUnits == 8 ? (row & 7) : ((row >> 1) & 3);
             uint32_t w[4];
-            ldmatrix_b8_trans_x2(vslot + (u / kUnits) * L::kBlockBytes + row * L::kRowBytes + ((unit ^ sw) << 4), w);
+            ldmatrix_b8_trans_x2(code_at<L>(vslot, 16 * g + vrow, u + (lane >> 4), row_pitch), w);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               uint32_t a0, a1, a2, a3;
@@ -1122,10 +1146,10 @@ __global__ void __launch_bounds__(kMassThreads) cache_mass_kernel(const __grid_c
   if (mine) p.mass[bh * (static_cast<int64_t>(p.s.width) << p.c.log2_page) + pos] += sum;
 }
 
-template <int WIDTH, int WORKER, int NT>
+template <int WIDTH, int WORKER, int NT, bool PACKED>
 cudaError_t launch_fwd(const CacheFwdParams& p, int dev, int ctas, cudaStream_t stream) {
-  using L = CacheFwdLayout<WIDTH, WORKER, NT>;
-  auto kern = cache_fwd_kernel<WIDTH, WORKER, NT>;
+  using L = CacheFwdLayout<WIDTH, WORKER, NT, PACKED>;
+  auto kern = cache_fwd_kernel<WIDTH, WORKER, NT, PACKED>;
   static std::atomic<uint64_t> ready{0};  // devices (bits) whose copy of the kernel has its shared memory granted
   cudaError_t e = cudaSuccess;
   if (!(ready.load(std::memory_order_relaxed) >> dev & 1)) {
@@ -1154,14 +1178,14 @@ cudaError_t launch_fwd(const CacheFwdParams& p, int dev, int ctas, cudaStream_t 
                       kMassThreads, stream, p);
 }
 
-template <int WIDTH>
+template <int WIDTH, bool PACKED>
 cudaError_t launch_width(const CacheFwdParams& p, bool warp_workers, int tiles, int dev, int ctas,
                          cudaStream_t stream) {
   auto go = [&](auto nt) {
     constexpr int NT = decltype(nt)::value;
     if constexpr (NT <= kCacheWarpWorkerTiles)
-      if (warp_workers) return launch_fwd<WIDTH, 1, NT>(p, dev, ctas, stream);
-    return launch_fwd<WIDTH, kCacheWarps<WIDTH, NT>, NT>(p, dev, ctas, stream);
+      if (warp_workers) return launch_fwd<WIDTH, 1, NT, PACKED>(p, dev, ctas, stream);
+    return launch_fwd<WIDTH, kCacheWarps<WIDTH, NT>, NT, PACKED>(p, dev, ctas, stream);
   };
   switch (tiles) {
     case 1: return go(std::integral_constant<int, 1>());
@@ -1184,8 +1208,8 @@ int cache_fwd_clusters(int dev, int size) {
   int n = slot.load(std::memory_order_relaxed) - 1;
   if (n >= 0) return n;
   // any of the kernels: each fills an SM with one CTA
-  using L = CacheFwdLayout<128, kCacheWarps<128, 1>, 1>;
-  auto kern = cache_fwd_kernel<128, kCacheWarps<128, 1>, 1>;
+  using L = CacheFwdLayout<128, kCacheWarps<128, 1>, 1, false>;
+  auto kern = cache_fwd_kernel<128, kCacheWarps<128, 1>, 1, false>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(size);
   cfg.blockDim = dim3(L::kWarps * 32);
@@ -1207,10 +1231,16 @@ int cache_fwd_clusters(int dev, int size) {
 
 cudaError_t cache_fwd_launch(const CacheFwdParams& p, int width, int tiles, bool warp_workers, int dev, int ctas,
                              cudaStream_t stream) {
+  const bool packed = p.c.pitch / 16 % 2 != 0;
+  auto go = [&](auto w) {
+    constexpr int W = decltype(w)::value;
+    return packed ? launch_width<W, true>(p, warp_workers, tiles, dev, ctas, stream)
+                  : launch_width<W, false>(p, warp_workers, tiles, dev, ctas, stream);
+  };
   switch (width) {
-    case 64: return launch_width<64>(p, warp_workers, tiles, dev, ctas, stream);
-    case 128: return launch_width<128>(p, warp_workers, tiles, dev, ctas, stream);
-    case 256: return launch_width<256>(p, warp_workers, tiles, dev, ctas, stream);
+    case 64: return go(std::integral_constant<int, 64>());
+    case 128: return go(std::integral_constant<int, 128>());
+    case 256: return go(std::integral_constant<int, 256>());
   }
   return cudaErrorInvalidValue;
 }
