@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT, PACKED>::kWa
       for (int g = 0; g < 4; ++g)
 #pragma unroll
         for (int b = 0; b < NT; ++b) s[g][b][0] = s[g][b][1] = zero2;
-#pragma unroll
+#pragma unroll(WIDTH > 128 && NT > 1 ? 1 : kKSteps)  // (fewer addresses held where registers are short)
       for (int kb = 0; kb < kKSteps; ++kb) {
         uint32_t qw[NT][8];
 #pragma unroll
