@@ -671,3 +671,40 @@ def test_the_debug_build_finds_no_copy_out_of_its_bounds(monkeypatch, D, P, Hq, 
     stream = torch.cuda.current_stream().cuda_stream
     assert lib.attn_device_status(stream) == binding.ATTN_OK
     assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+@pytest.mark.parametrize("D,P,Hq,H,T,lens", [
+    (128, 64, 2, 2, 1, [1, 64, 65, 1500, 17, 0, 300] * 12),   # dealt to CTAs, many segments of one chunk
+    (80, 16, 8, 4, 3, [3, 1100, 64, 66, 129] * 9),
+    (200, 32, 2, 2, 8, [8, 1100, 64, 66, 129] * 16),
+    (64, 16, 32, 16, 1, [1, 900, 64, 17, 130, 2] * 10),       # dealt to warps
+    (48, 16, 16, 16, 2, [2, 900, 64, 17, 130, 3] * 10),
+    (112, 64, 6, 2, 3, [4, 2500]),                            # a cluster each
+])
+def test_segments_of_one_chunk_beside_long_ones(D, P, Hq, H, T, lens):
+    """What a segment costs by itself is counted when the chunks are dealt: every chunk is still read once."""
+    c, ref, table, _ = filled(lens, H, D, P, FP, 151)
+    q = rows((len(lens), Hq, T, D), FP, 152)
+    fresh = np.minimum(T, np.array(lens))
+    out = torch.full((len(lens), Hq, T, D), 7.0, dtype=FP, device=DEV)
+    lse = torch.full((len(lens), Hq, T), 7.0, device=DEV)
+    kv.cache_fwd(q.to(DEV), c, ints(table), ints(lens), fresh=ints(fresh), out=out, lse=lse)
+    ro, rl, _, av, aq = oc.cache_attention(ref, table, np.array(lens), fresh, q.double().numpy(), D ** -0.5)
+    check_fwd(out, lse, ro, rl, av, aq, D, FP, fresh)
+    for b, n in enumerate(fresh):
+        assert (out[b, :, n:] == 7.0).all() and (lse[b, :, n:] == 7.0).all()
+    assert binding.device_status() == binding.ATTN_OK
+
+
+@pytest.mark.parametrize("D", [8, 40, 72, 136, 200, 248])
+@pytest.mark.parametrize("P", [16, 64])
+def test_padding_channels_may_hold_anything(D, P):
+    lens = [200, 31]
+    c, _, table, _ = filled(lens, 2, D, P, BF, 161)
+    q = rows((2, 4, 2, D), BF, 162).to(DEV)
+    want = kv.cache_fwd(q, c, ints(table), ints(lens))
+    c.k[..., D:] = 0x7f  # NaN codes
+    c.v[..., D:] = 0xff
+    got = kv.cache_fwd(q, c, ints(table), ints(lens))
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+    assert torch.isfinite(got[0].float()).all()
