@@ -70,9 +70,10 @@ cudaError_t cache_select_launch(const CacheSelectParams& p, bool f16, cudaStream
 constexpr int kCacheChunk = 64;
 // Query rows of a tile; a pass over a (sequence, head)'s keys takes as many
 // tiles as their sums leave registers for.  Measured at 128 channels, 128
-// segments of 4096 keys: 1 tile 27 us, 2 tiles 34 us; 24 rows in one pass of 3
-// tiles 79 us (spills), in two passes of 2 tiles 63 us.  At 64 channels 32 rows in
-// one pass 40 us, in two 48 us; at 256 channels 16 rows in one 89 us, in two 108 us.
+// segments of 4096 keys: 1 tile 27 us, 2 tiles 32 us; 24 rows in two passes of 2
+// tiles 58 us (in one pass of 3, which spills, 79 us when two took 63).  At 64
+// channels 32 rows in one pass 40.5 us, in two 43.7 us; at 256 channels 16 rows in one
+// 82 us, in two 92 us.
 constexpr int kCacheTileRows = 8;
 // Tiles up to which a warp may be a worker of its own: each worker's Q takes
 // shared memory from the rings.

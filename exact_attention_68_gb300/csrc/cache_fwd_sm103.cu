@@ -8,11 +8,12 @@
 // 4·D·G multiply-adds (G query heads a key head) that the tensor cores take at
 // 16-bit rate.  So the work is cut for bytes in flight.  The unit is a chunk
 // of 64 keys of one (sequence, head), a warp's step; the chunks of all
-// (sequence, head, row tile) stand in one line that is dealt evenly to
-// `workers`, whatever the lengths.  A warp feeds itself: its lane-elected TMA
+// (sequence, head, row tile), each of these with a lead for what it costs by
+// itself, stand in one line that is dealt evenly to `workers`, whatever the
+// lengths.  A warp feeds itself: its lane-elected TMA
 // loads bring the pages of its next K and V chunks into its own ring of
-// shared memory (128-byte swizzle; columns past D read as zero) while it works
-// on the current one, so no warp waits for another.
+// shared memory (128-byte swizzle; columns past D read as zero; or runs of
+// bytes) while it works on the current one, so no warp waits for another.
 //
 // Arithmetic of a chunk, 8 query rows a tile: codes become fp16 exactly; q is
 // brought to fp16 by a power of two per row chosen from its largest element,
@@ -38,9 +39,9 @@
 // each segment instead and joins it through its shared memory: no second launch.
 //
 // Measured (8 key heads, 4 query heads each, 128 channels): 64 sequences of
-// 8000-16384 keys 253 us = 6.33 TB/s, 93 % of the measured copy rate; 16 of
-// 500-8192 keys 37.5 us = 4.2 TB/s (the longest bound it: a CTA streams at most
-// about 65 GB/s); one of 1000 keys 8.7 us (latency).  About 1060 instructions a
+// 8000-16384 keys 249 us = 6.42 TB/s, 94 % of the measured copy rate; 16 of
+// 500-8192 keys 37.2 us = 4.2 TB/s (the longest bound it: a CTA streams at most
+// about 65 GB/s); one of 1000 keys 8.5 us (latency).  About 1040 instructions a
 // chunk, 256 of them conversions of codes.
 #include <atomic>
 #include <type_traits>
@@ -674,7 +675,9 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT, PACKED>::kWa
       for (int g = 0; g < 4; ++g)
 #pragma unroll
         for (int b = 0; b < NT; ++b) s[g][b][0] = s[g][b][1] = zero2;
-#pragma unroll(WIDTH > 128 && NT > 1 ? 1 : kKSteps)  // (fewer addresses held where registers are short)
+// rolled where registers are short (21 sequences of 996-4114 keys, 24 rows of 256
+// channels: 200 us, unrolled 290 us; 128 channels or 8 rows: no change or slower)
+#pragma unroll(WIDTH > 128 && NT > 1 ? 1 : kKSteps)
       for (int kb = 0; kb < kKSteps; ++kb) {
         uint32_t qw[NT][8];
 #pragma unroll

@@ -10,7 +10,7 @@
 //
 // Bound: 2·D bytes a page and head (the page's keys and values are 2·D·page),
 // read as 256-byte rows at random: 8 sequences of 50001-65536 tokens in pages of
-// 16, 8 heads of 128 channels: 26.6 us for 61.6 MB, of which 9 us choosing 256 of
+// 16, 8 heads of 128 channels: 26.7 us for 61.6 MB, of which 9 us choosing 256 of
 // 4096 pages, 64 CTAs each on its own row of scores; slope 3.1 TB/s.  One
 // sequence of 256 pages 7.3 us (latency of two kernels).
 #include <cuda_bf16.h>
