@@ -1127,6 +1127,8 @@ __global__ void __launch_bounds__(kMassThreads) cache_mass_kernel(const __grid_c
     pos = i < 0 || i >= p.s.width || !follows(l, e) ? kFar : (i << p.c.log2_page) + (key & (p.c.page - 1));
   }
   const bool mine = pos < len;
+  float* mass = p.mass + bh * (static_cast<int64_t>(p.s.width) << p.c.log2_page) + pos;
+  const float before = mine ? *mass : 0.f;
   wait_for_previous();
   if (blockIdx.x * kMassThreads >= nc * kCacheChunk) return;
   const int rows = p.G * p.s.T;
@@ -1139,14 +1141,15 @@ __global__ void __launch_bounds__(kMassThreads) cache_mass_kernel(const __grid_c
       z[r] = w == -INFINITY ? INFINITY : w * kLog2e;
     }
     __syncthreads();
-    if (mine)  // score rows are padded to tiles of 8
+    if (mine)  // score rows are padded to tiles of 8; four loads at once
+#pragma unroll 4
       for (int r = 0; r < min(kMassRows, p.score_rows - r0); r += 4) {
         const float4 t = __ldg(reinterpret_cast<const float4*>(s + r0 + r));
         const float4 w = *reinterpret_cast<const float4*>(z + r);
         sum += (ex2_approx(t.x - w.x) + ex2_approx(t.y - w.y)) + (ex2_approx(t.z - w.z) + ex2_approx(t.w - w.w));
       }
   }
-  if (mine) p.mass[bh * (static_cast<int64_t>(p.s.width) << p.c.log2_page) + pos] += sum;
+  if (mine) *mass = before + sum;
 }
 
 template <int WIDTH, int WORKER, int NT, bool PACKED>
