@@ -708,3 +708,25 @@ def test_padding_channels_may_hold_anything(D, P):
     got = kv.cache_fwd(q, c, ints(table), ints(lens))
     assert all(torch.equal(g, w) for g, w in zip(got, want))
     assert torch.isfinite(got[0].float()).all()
+
+
+def test_weights_and_scores_off_a_16_byte_boundary():
+    """Weights and scores need 4-byte alignment only; the selection loads vectors where it can."""
+    lens, H, D, P, keep = [3000, 5500], 2, 64, 16, 900
+    dst_width = -(-keep // P)
+    c, ref, table, free = filled(lens, H, D, P, BF, 171, extra=2 * dst_width)
+    q = rows((2, 4, 1, D), BF, 172)
+    off = lambda shape: torch.empty(int(np.prod(shape)) + 1, device=DEV)[1:].view(shape)
+    scores = off((2, H, table.shape[1]))
+    pages, _ = kv.cache_select(q.to(DEV), c, ints(table), ints(lens), 40, scores=scores)
+    rp, rs = oc.cache_select(ref, table, np.array(lens), [1, 1], q.float().numpy(), 40)
+    assert np.array_equal(scores.cpu().numpy(), rs) and np.array_equal(pages.cpu().numpy(), rp)
+    dst = free[:2 * dst_width].reshape(2, dst_width).astype(np.int32)
+    mass = np.random.default_rng(173).random((2, H, table.shape[1] * P)).astype(np.float32)
+    want = oc.cache_evict(ref, mass, table, np.array(lens), dst, keep, 100)
+    given, new_mass = off(mass.shape).copy_(torch.from_numpy(mass)), off((2, H, dst_width * P))
+    got = kv.cache_evict(c, given, ints(table), ints(lens), ints(dst), keep, 100, new_mass=new_mass)
+    for g, w in zip(got, want):
+        assert np.array_equal(g.cpu().numpy(), w)
+    same_cache(c, ref)
+    assert binding.device_status() == binding.ATTN_OK
