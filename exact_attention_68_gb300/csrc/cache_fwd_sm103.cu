@@ -1108,12 +1108,16 @@ __global__ void __launch_bounds__(kJoinThreads * NT) cache_join_kernel(const __g
   if (col == 0) p.lse[row] = (M + log2f(S)) * kLn2f;
 }
 
-// mass[key] += Σ over the head's rows of 2^(t - lse): one thread a key, whose
-// scores lie side by side; the rows' logsumexps wait in shared memory.
+// mass[key] += Σ over the rows that may see the key of 2^(t - lse): one thread a
+// key, whose scores lie side by side; the rows' logsumexps and last positions wait
+// in shared memory.  Which rows count is a comparison of positions, not a logsumexp
+// of +inf: rows that are not there were scored too, and inf - inf and NaN - inf
+// would reach every key.
 constexpr int kMassThreads = 128, kMassRows = 256;
 
 __global__ void __launch_bounds__(kMassThreads) cache_mass_kernel(const __grid_constant__ CacheFwdParams p) {
-  __shared__ __align__(16) float z[kMassRows];  // log2 units; rows that do not count: +inf
+  __shared__ __align__(16) float z[kMassRows];   // log2 units
+  __shared__ __align__(16) int last[kMassRows];  // position; -1: a row that is not there or sees no key
   const int h = blockIdx.y, b = blockIdx.z;
   int len, n;
   const int nc = seq_chunks(p, b, false, &len, &n);
@@ -1137,8 +1141,10 @@ __global__ void __launch_bounds__(kMassThreads) cache_mass_kernel(const __grid_c
   for (int r0 = 0; r0 < rows; r0 += kMassRows) {
     __syncthreads();
     for (int r = threadIdx.x; r < kMassRows; r += kMassThreads) {
-      const float w = r0 + r < rows && (r0 + r) % p.s.T < n ? p.lse[bh * rows + r0 + r] : -INFINITY;
-      z[r] = w == -INFINITY ? INFINITY : w * kLog2e;
+      const int i = (r0 + r) % p.s.T;
+      const float w = r0 + r < rows && i < n ? p.lse[bh * rows + r0 + r] : -INFINITY;
+      z[r] = w * kLog2e;
+      last[r] = w == -INFINITY ? -1 : len - n + i;
     }
     __syncthreads();
     if (mine)  // score rows are padded to tiles of 8; four loads at once
@@ -1146,7 +1152,9 @@ __global__ void __launch_bounds__(kMassThreads) cache_mass_kernel(const __grid_c
       for (int r = 0; r < min(kMassRows, p.score_rows - r0); r += 4) {
         const float4 t = __ldg(reinterpret_cast<const float4*>(s + r0 + r));
         const float4 w = *reinterpret_cast<const float4*>(z + r);
-        sum += (ex2_approx(t.x - w.x) + ex2_approx(t.y - w.y)) + (ex2_approx(t.z - w.z) + ex2_approx(t.w - w.w));
+        const int4 e = *reinterpret_cast<const int4*>(last + r);
+        auto weight = [&](float x, float ref, int to) { return pos <= to ? ex2_approx(x - ref) : 0.f; };
+        sum += (weight(t.x, w.x, e.x) + weight(t.y, w.y, e.y)) + (weight(t.z, w.z, e.z) + weight(t.w, w.w, e.w));
       }
   }
   if (mine) *mass = before + sum;

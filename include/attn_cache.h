@@ -139,9 +139,10 @@ ATTN_API size_t attn_cache_fwd_workspace(const attn_cache_t* cache, const attn_c
  *   wait_timeout_ns  bound on each in-kernel wait (ATTN_DEFAULT_WAIT_TIMEOUT_NS)
  *
  * A query that may attend to no key gets out = 0 and lse = -inf.  Rows of
- * tokens from fresh[b] on, and sequences left out, are not written.  Slots
- * behind a sequence's end may hold anything.  Results do not depend on the
- * order in which the GPU ran the work: every sum has a fixed order.
+ * tokens from fresh[b] on, and sequences left out, are not written; what q
+ * holds there, and slots behind a sequence's end, may be anything.  Results do
+ * not depend on the order in which the GPU ran the work: every sum has a fixed
+ * order.
  */
 ATTN_API attn_status_t attn_cache_fwd(const attn_cache_t* cache, const attn_cache_seqs_t* seqs,
                                       const void* q, const int32_t* pages, int64_t listed,
