@@ -33,6 +33,11 @@
 // pages' scales differ; its smallest step, 2^-38 of the largest term, is far
 // below the 11 bits it is rounded to.
 //
+// m is -inf only for a row that has met no key it may see: once it has, m is at
+// least kLowest, also where all its scores are -inf (l is 0, and the row NaN as
+// 0 / 0) or NaN, which the maximum drops and l keeps.  So the joins may leave out
+// parts with m = -inf, and a row's answer does not depend on how the work was cut.
+//
 // A worker that covers a segment (one sequence, head and row tile) writes the
 // result; others write O, m, r, l to the workspace and a second kernel joins
 // them in a fixed order.  Where segments are few or short, a cluster of CTAs has
@@ -57,6 +62,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2f = 0.6931471805599453f;
 constexpr int kPShift = 14;  // P is 2^14 times the weight relative to r
+constexpr float kLowest = -3.402823466e38f;  // the running maximum of a row that has met a key
 constexpr int kFar = 0x7fffff00;  // position of a token that is not there (real ones stay below 2^30)
 constexpr uint64_t kDrainNs = 1000000000ull;
 constexpr int kMaxCluster = kCacheMaxCluster;
@@ -198,6 +204,13 @@ __device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr, int rank) {
       : "r"(addr), "r"(rank)
       : "memory");
   return v;
+}
+
+// A row's logsumexp out of its maximum and sum in log2 units: NaN where all scores
+// are -inf, -inf where there are none.
+__device__ __forceinline__ float row_lse(float m, float l) {
+  const float z = (m + log2f(l)) * kLn2f;
+  return l == 0.f && m != -INFINITY ? __int_as_float(0x7fffffff) : z;
 }
 
 // Over the eight lanes that hold the same query rows.
@@ -719,6 +732,7 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT, PACKED>::kWa
       float ev[4], vm[4];
       int gpos[4];
       bool tail = false;  // some key is hidden from some row
+      int nearest = kFar;  // the chunk's first position
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const uint4 md = ld_shared_v4(meta + u_meta * 64 + g * 16);
@@ -726,6 +740,7 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT, PACKED>::kWa
         ev[g] = __uint_as_float(md.z);
         vm[g] = __uint_as_float(md.w);
         tail = tail || gpos[g] + 15 > first_last;
+        nearest = min(nearest, gpos[g]);
         const float2 ks = make_float2(__uint_as_float(md.y), __uint_as_float(md.y));
 #pragma unroll
         for (int b = 0; b < NT; ++b) {
@@ -763,12 +778,14 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT, PACKED>::kWa
       bool moved = false;
 #pragma unroll
       for (int b = 0; b < NT; ++b) {
-        float mx[2], rx[2];
+        // a row that may see a key of the chunk
+        float mx[2] = {nearest <= last[b][0] ? kLowest : -INFINITY, nearest <= last[b][1] ? kLowest : -INFINITY};
+        float rx[2];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const float a0 = fmaxf(s[g][b][0].x, s[g][b][1].x), a1 = fmaxf(s[g][b][0].y, s[g][b][1].y);
           const float2 av = __fadd2_rn(make_float2(a0, a1), make_float2(ev[g], ev[g]));
-          mx[0] = g == 0 ? a0 : fmaxf(mx[0], a0), mx[1] = g == 0 ? a1 : fmaxf(mx[1], a1);
+          mx[0] = fmaxf(mx[0], a0), mx[1] = fmaxf(mx[1], a1);
           rx[0] = g == 0 ? av.x : fmaxf(rx[0], av.x), rx[1] = g == 0 ? av.y : fmaxf(rx[1], av.y);
         }
         // references: 0 where no key has been allowed yet
@@ -900,7 +917,7 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT, PACKED>::kWa
                 const float x = mi == -INFINITY ? 0.f : of(o[u][b][hf], i) * w;
                 if (ch < p.c.D) p.out[to * p.c.D + ch] = static_cast<uint16_t>(pack_16bit(p.f16, x, 0.f));
               }
-            if (gid == 0) p.lse[to] = (mi + log2f(li)) * kLn2f;
+            if (gid == 0) p.lse[to] = row_lse(mi, li);
           } else {
 #pragma unroll
             for (int u = 0; u < kTiles; ++u)
@@ -957,7 +974,7 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT, PACKED>::kWa
           part_stat[kRows + row] = R;
           part_stat[2 * kRows + row] = S;
         } else if (live(row)) {
-          p.lse[row_place(p, cs.b, h, tile_row + row)] = (M + log2f(S)) * kLn2f;
+          p.lse[row_place(p, cs.b, h, tile_row + row)] = row_lse(M, S);
         }
       }
       __syncthreads();
@@ -1025,8 +1042,8 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT, PACKED>::kWa
           }
 #pragma unroll
           for (int k = 0; k < kMaxCluster; ++k) st_shared_f32(stat + (k * kRows + row) * 4, f[k]);
-          st_shared_f32(stat + (kMaxCluster * kRows + row) * 4, S > 0.f || S != S ? 1.f / S : 0.f);
-          if (rank == 0 && live(row)) p.lse[row_place(p, cs.b, h, tile_row + row)] = (M + log2f(S)) * kLn2f;
+          st_shared_f32(stat + (kMaxCluster * kRows + row) * 4, M == -INFINITY ? 0.f : 1.f / S);
+          if (rank == 0 && live(row)) p.lse[row_place(p, cs.b, h, tile_row + row)] = row_lse(M, S);
         }
         __syncthreads();
         for (int i = rank * kThreads + threadIdx.x; i < kRows * WIDTH / 2; i += cluster * kThreads) {
@@ -1039,8 +1056,9 @@ __global__ void __launch_bounds__(CacheFwdLayout<WIDTH, WORKER, NT, PACKED>::kWa
           float x = 0.f, y = 0.f;
 #pragma unroll
           for (int k = 0; k < kMaxCluster; ++k) {
+            // 0 for a CTA without keys, whose sums are 0, or far below: a NaN there stays
             const float f = ld_shared_f32(stat + (k * kRows + row) * 4);
-            if (f != 0.f) x += v[k].x * f, y += v[k].y * f;
+            x += v[k].x * f, y += v[k].y * f;
           }
           const float inv = ld_shared_f32(stat + (kMaxCluster * kRows + row) * 4);
           *reinterpret_cast<uint32_t*>(p.out + row_place(p, cs.b, h, tile_row + row) * p.c.D + ch) =
@@ -1105,7 +1123,7 @@ __global__ void __launch_bounds__(kJoinThreads * NT) cache_join_kernel(const __g
   if (col < p.c.D)
     *reinterpret_cast<uint2*>(p.out + row * p.c.D + col) =
         make_uint2(pack_16bit(p.f16, acc.x, acc.y), pack_16bit(p.f16, acc.z, acc.w));
-  if (col == 0) p.lse[row] = (M + log2f(S)) * kLn2f;
+  if (col == 0) p.lse[row] = row_lse(M, S);
 }
 
 // mass[key] += Σ over the rows that may see the key of 2^(t - lse): one thread a

@@ -138,7 +138,10 @@ ATTN_API size_t attn_cache_fwd_workspace(const attn_cache_t* cache, const attn_c
  *   T        1 .. ATTN_CACHE_MAX_TOKENS; q_heads a multiple of heads
  *   wait_timeout_ns  bound on each in-kernel wait (ATTN_DEFAULT_WAIT_TIMEOUT_NS)
  *
- * A query that may attend to no key gets out = 0 and lse = -inf.  Rows of
+ * A query that may attend to no key gets out = 0 and lse = -inf.  One that may,
+ * and has a NaN score, a score of +inf or no score but -inf, gets NaN in out and
+ * lse and adds NaN to the mass of the keys it may attend to, as the formula does;
+ * a NaN value code makes its channel of out NaN.  Rows of
  * tokens from fresh[b] on, and sequences left out, are not written; what q
  * holds there, and slots behind a sequence's end, may be anything.  Results do
  * not depend on the order in which the GPU ran the work: every sum has a fixed

@@ -53,3 +53,134 @@ def test_rows_behind_the_fresh_tokens_may_hold_anything(route, G):
     for g, w in zip(got, want):
         assert torch.equal(g, w)
     assert binding.device_status() == binding.ATTN_OK
+
+
+# ---------------------------------------------------------------- NaN and infinities
+def meets(out, lse, mass, ref, D, dtype, fresh):
+    """check_fwd where the oracle is finite; where it is NaN, NaN."""
+    ro, rl, rm, av, aq = (np.array(x) for x in ref)
+    live = np.zeros(rl.shape, bool)
+    for b, n in enumerate(fresh):
+        live[b, :, :n] = True
+    lost = np.isnan(rl) & live
+    o, z, m = out.clone(), lse.clone(), mass.double().cpu().numpy()
+    none = torch.from_numpy(np.isnan(ro) & live[..., None]).to(DEV)
+    gone = torch.from_numpy(lost).to(DEV)
+    assert torch.equal(torch.isnan(z) & torch.from_numpy(live).to(DEV), gone)
+    assert torch.equal(torch.isnan(o) & torch.from_numpy(live[..., None]).to(DEV), none)
+    assert np.array_equal(np.isnan(m), np.isnan(rm))
+    for x in (ro, rl, av, aq):
+        x[~np.isfinite(x) & ~np.isneginf(x)] = 0.0
+    aq[lost] = 0.0
+    check_fwd(o.masked_fill(none, 0.0), z.masked_fill(gone, 0.0), ro, rl, av, aq, D, dtype, fresh)
+    fine = ~np.isnan(rm)
+    # a weight is off by 2·dt and 2^-19 (ex2, the stored logsumexp), sums of rows fp32; ex2
+    # gives 0 below 2^-126
+    dt = (D + 16) * 2.0 ** -23 * aq.max() + 2.0 ** -21 * np.abs(rl[np.isfinite(rl)]).max(initial=0.0)
+    assert (np.abs(m[fine] - rm[fine]) <= (2 * dt + 2.0 ** -19) * rm[fine] + 2.0 ** -23 * rm[fine] + 2.0 ** -120).all()
+
+
+def attend(c, ref, q, table, lens, fresh, dtype):
+    D = c.head_dim
+    with np.errstate(invalid="ignore", over="ignore"):
+        want = oc.cache_attention(ref, table, np.array(lens), fresh, q.double().numpy(), D ** -0.5)
+    meets(*call(c, q, table, lens, fresh), want, D, dtype, fresh)
+    # without weights the same
+    assert all(torch.equal(torch.nan_to_num(a, 5.0), torch.nan_to_num(b, 5.0))
+               for a, b in zip(call(c, q, table, lens, fresh)[:2], call(c, q, table, lens, fresh, mass=False)[:2]))
+    assert binding.device_status() == binding.ATTN_OK
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("G", [2, 18])  # one pass, two
+@pytest.mark.parametrize("route", ROUTES)
+def test_nan_and_infinite_queries(route, G, dtype):
+    """A row's NaN stays in that row: out and lse NaN, and the weights of the keys it may see."""
+    lens, width = ROUTES[route]
+    T, D = 2, 128
+    c, ref, table, _ = filled(lens, 1, D, 64, dtype, 21, width=width)
+    fresh = np.minimum(T, lens)
+    q = rows((len(lens), G, T, D), dtype, 22)
+    q[0, 0, 0, 7] = float("nan")   # the first of two tokens: the last key keeps a finite weight
+    q[1, 1, 1] = float("nan")
+    q[1, 0, 0, 3] = float("inf")
+    q[2, G - 1, 0, 100] = float("-inf")
+    attend(c, ref, q, table, lens, fresh, dtype)
+
+
+@pytest.mark.parametrize("route", ROUTES)
+def test_a_nan_key_alone_in_its_chunk(route):
+    """The last key's chunk holds no other key: its NaN is not taken for a chunk without keys."""
+    lens, width = ROUTES[route]
+    D = 128
+    c, ref, table, _ = filled(lens, 1, D, 64, BF, 31, width=width)
+    for b, n in enumerate(lens[:3]):
+        g, slot = int(table[b, (n - 1) // 64]), (n - 1) % 64
+        c.k[g, 0, slot, 5] = 0x7f
+        ref["k"][g, 0, slot, 5] = 0x7f
+    attend(c, ref, rows((len(lens), 2, 1, D), BF, 32), table, lens, [1] * len(lens), BF)
+
+
+@pytest.mark.parametrize("route", ROUTES)
+def test_a_nan_value_far_below_the_rest_still_counts(route):
+    """A NaN value code makes its channel NaN, however small its weight and wherever the work is cut."""
+    lens, width = ROUTES[route]
+    D = 128
+    c, ref, table, _ = filled(lens, 1, D, 64, BF, 41, width=width)
+    q = rows((len(lens), 2, 1, D), BF, 42)
+    for b, n in enumerate(lens[:2]):
+        g, slot = int(table[b, (n - 1) // 64]), (n - 1) % 64
+        for d in (c, ref):
+            k, v = (d.k, d.v) if d is c else (d["k"], d["v"])
+            k[g, 0, slot] = 0x78  # 256 in every channel: 256·scale, against q of one sign far below the others
+            v[g, 0, slot, 9] = 0xff
+        q[b] = -8.0
+    attend(c, ref, q, table, lens, [1] * len(lens), BF)
+
+
+@pytest.mark.parametrize("route", ROUTES)
+def test_scores_of_minus_infinity(route):
+    """Beside finite scores a weight of 0; a row of nothing else is NaN, unlike one that sees no key."""
+    lens, width = ROUTES[route]
+    D = 128
+    c, ref, table, _ = filled(lens, 1, D, 64, BF, 51, width=width)
+    for b, n in enumerate(lens[:3]):
+        for i in range(-(-n // 64)):
+            held = 0x38 if b != 1 or i == 0 else 0xb8  # 1, and -1 behind the first page of sequence 1
+            c.k[int(table[b, i])], ref["k"][table[b, i]] = held, held
+    q = rows((len(lens), 2, 1, D), BF, 52)
+    q[0, 0, 0, 3] = float("-inf")
+    q[1, 0, 0, 3] = float("inf")
+    q[2, 1, 0, 3] = float("-inf")
+    attend(c, ref, q, table, lens, [1] * len(lens), BF)
+    # finite queries whose scores pass fp32's range behind a first page of zero keys
+    for b, n in enumerate(lens[:2]):
+        c.k[int(table[b, 0])], ref["k"][table[b, 0]] = 0, 0
+        c.k_scale[table[b, 0]], ref["k_scale"][table[b, 0]] = 1.0, 1.0
+        for i in range(1, -(-n // 64)):
+            c.k_scale[int(table[b, i])], ref["k_scale"][table[b, i]] = 2.0 ** 90, 2.0 ** 90
+    q = torch.full((len(lens), 2, 1, D), -(2.0 ** 60)).to(BF)
+    q[2:] = 1.0
+    out, lse, mass = call(c, q, table, lens, [1] * len(lens))
+    # sequence 0: the zero keys of its first page have all the weight, evenly
+    g = int(table[0, 0])
+    v = oc.e4m3_values()[ref["v"][g, 0]] * float(ref["v_scale"][g, 0])
+    assert np.abs(out[0].double().cpu().numpy() - v.mean(0)).max() <= 2.0 ** -8 * np.abs(v).max()
+    assert torch.allclose(mass[0, 0, :64], torch.full((64,), 2.0 / 64, device=DEV), rtol=2.0 ** -18)
+    assert (mass[0, 0, 64:] == 0).all() and torch.isfinite(lse[0]).all()
+
+
+@pytest.mark.parametrize("width", [12, 2000])
+def test_rows_of_a_list_without_keys_beside_nan_rows(width):
+    """No key listed: 0 and -inf. NaN query over an empty list: still no key."""
+    lens, D, H = [700, 130], 128, 2
+    c, ref, table, _ = filled(lens, H, D, 64, BF, 61, width=width)
+    pages = np.array([[[0, 10, -1], [-1, -1, -1]], [[2, -1, -1], [0, 1, 2]]], np.int32)
+    q = rows((2, 4, 1, D), BF, 62)
+    q[0, 0], q[0, 2], q[1, 1], q[1, 3, 0, 5] = [float("nan")] * 4
+    out, lse = kv.cache_fwd(q.to(DEV), c, ints(table), ints(lens), pages=ints(pages))
+    o, z = out.cpu().float(), lse.cpu()
+    assert torch.isnan(o[0, 0]).all() and torch.isnan(z[0, 0]).all()
+    assert (o[0, 2:] == 0).all() and torch.isneginf(z[0, 2:]).all()
+    assert torch.isnan(o[1, [1, 3]]).all() and torch.isnan(z[1, [1, 3]]).all()
+    assert torch.isfinite(o[[0, 1, 1], [1, 0, 2]]).all() and torch.isfinite(z[[0, 1, 1], [1, 0, 2]]).all()
