@@ -1131,7 +1131,7 @@ __global__ void __launch_bounds__(kJoinThreads * NT) cache_join_kernel(const __g
 // in shared memory.  Which rows count is a comparison of positions, not a logsumexp
 // of +inf: rows that are not there were scored too, and inf - inf and NaN - inf
 // would reach every key.
-constexpr int kMassThreads = 128, kMassRows = 256;
+constexpr int kMassThreads = 128, kMassRows = 256, kMassLoads = 4;
 
 __global__ void __launch_bounds__(kMassThreads) cache_mass_kernel(const __grid_constant__ CacheFwdParams p) {
   __shared__ __align__(16) float z[kMassRows];   // log2 units
@@ -1165,15 +1165,24 @@ __global__ void __launch_bounds__(kMassThreads) cache_mass_kernel(const __grid_c
       last[r] = w == -INFINITY ? -1 : len - n + i;
     }
     __syncthreads();
-    if (mine)  // score rows are padded to tiles of 8; four loads at once
-#pragma unroll 4
-      for (int r = 0; r < min(kMassRows, p.score_rows - r0); r += 4) {
-        const float4 t = __ldg(reinterpret_cast<const float4*>(s + r0 + r));
-        const float4 w = *reinterpret_cast<const float4*>(z + r);
-        const int4 e = *reinterpret_cast<const int4*>(last + r);
+    const int stop = mine ? min(kMassRows, p.score_rows - r0) : 0;  // score rows are padded to tiles of 8
+    for (int r = 0; r < stop; r += 4 * kMassLoads) {
+      // ordinary loads, since the scores are still being written when this kernel
+      // begins; all in flight at once (one after the other: drafts 61 us, so 51 us)
+      float4 t[kMassLoads];
+#pragma unroll
+      for (int j = 0; j < kMassLoads; ++j)
+        if (r + 4 * j < stop) t[j] = *reinterpret_cast<const float4*>(s + r0 + r + 4 * j);
+#pragma unroll
+      for (int j = 0; j < kMassLoads; ++j) {
+        if (r + 4 * j >= stop) break;
+        const float4 w = *reinterpret_cast<const float4*>(z + r + 4 * j);
+        const int4 e = *reinterpret_cast<const int4*>(last + r + 4 * j);
         auto weight = [&](float x, float ref, int to) { return pos <= to ? ex2_approx(x - ref) : 0.f; };
-        sum += (weight(t.x, w.x, e.x) + weight(t.y, w.y, e.y)) + (weight(t.z, w.z, e.z) + weight(t.w, w.w, e.w));
+        sum += (weight(t[j].x, w.x, e.x) + weight(t[j].y, w.y, e.y)) +
+               (weight(t[j].z, w.z, e.z) + weight(t[j].w, w.w, e.w));
       }
+    }
   }
   if (mine) *mass = before + sum;
 }

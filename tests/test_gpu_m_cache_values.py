@@ -184,3 +184,27 @@ def test_rows_of_a_list_without_keys_beside_nan_rows(width):
     assert (o[0, 2:] == 0).all() and torch.isneginf(z[0, 2:]).all()
     assert torch.isnan(o[1, [1, 3]]).all() and torch.isnan(z[1, [1, 3]]).all()
     assert torch.isfinite(o[[0, 1, 1], [1, 0, 2]]).all() and torch.isfinite(z[[0, 1, 1], [1, 0, 2]]).all()
+
+
+# ---------------------------------------------------------------- one call behind another
+@pytest.mark.parametrize("route", ROUTES)
+def test_weights_are_those_of_their_own_call(route):
+    """The weights' pass begins while the attention still writes the scores it reads: calls on
+    one workspace, one right behind the other, get what each gets by itself."""
+    lens, width = ROUTES[route]
+    c, _, table, _ = filled(lens, 2, 128, 64, BF, 71, width=width)
+    tb, ln = ints(table), ints(lens)
+    qs = [rows((len(lens), 8, 1, 128), BF, 72 + i, 3.0).to(DEV) for i in range(3)]
+    ws = torch.empty(kv.cache_fwd_workspace(c, tb, ln, 8, 1, with_mass=True), dtype=torch.uint8, device=DEV)
+    mass = [torch.zeros((len(lens), 2, width * 64), device=DEV) for _ in range(33)]
+    want = []
+    for i, q in enumerate(qs):
+        kv.cache_fwd(q, c, tb, ln, mass=mass[i], workspace=ws)
+        torch.cuda.synchronize()
+        want.append(mass[i].clone())
+    for i in range(3, 33):
+        kv.cache_fwd(qs[i % 3], c, tb, ln, mass=mass[i], workspace=ws)
+    torch.cuda.synchronize()
+    assert not torch.equal(want[0], want[1])
+    for i in range(3, 33):
+        assert torch.equal(mass[i], want[i % 3])
