@@ -24,7 +24,10 @@
  *   k_bounds   int8 [pages, heads, 2, pitch]: for each channel the upper, then
  *              the lower bound of the page's key codes in steps of 448/127
  *              (ceil(max·127/448), floor(min·127/448); NaN codes left out, 0 where
- *              there are no others, and tokens appended later keep that 0 inside)
+ *              there are no others).  An append to a page that holds tokens widens
+ *              them while the scale stays, so that such a 0, or what tokens taken
+ *              back since (a smaller lens) had, stays inside; where the scale
+ *              grows, and in evict, they are found anew from the codes
  *
  * A power-of-two scale costs an e4m3 code no precision against any other
  * scale, and codes move to a larger power-of-two scale without a rounding
@@ -92,7 +95,7 @@ typedef struct {
  * A page that holds earlier tokens of the sequence keeps the larger of its
  * scale and that one; where its scale grows, the earlier codes are requantised.
  * Codes are x / scale rounded to nearest even and saturated to ±448 (infinities
- * too); NaN stays NaN.  k_bounds follows the codes.  Slots behind the
+ * too); NaN stays NaN.  k_bounds follows as said above.  Slots behind the
  * sequence's end are left as they were.  The pages that the call writes must
  * belong to one sequence each.
  */

@@ -88,7 +88,14 @@ def cache_append(cache, table, lens, fresh, k, v) -> None:
                             page[:held] = e4m3_codes(_VALUES[page[:held]] * (was / s))
                     page[held:held + w - u] = e4m3_codes(x / s)
                     cache[name + "_scale"][g, h] = s
-                    if name == "k":
+                    if name != "k":
+                        continue
+                    if held and s == was:  # bounds are widened, by channels that have a code to widen by
+                        new, at = code_bounds(page[held:held + w - u]), cache["k_bounds"][g, h]
+                        some = ~np.isnan(_VALUES[page[held:held + w - u]]).all(0)
+                        at[0] = np.where(some, np.maximum(at[0], new[0]), at[0])
+                        at[1] = np.where(some, np.minimum(at[1], new[1]), at[1])
+                    else:
                         cache["k_bounds"][g, h] = code_bounds(page[:held + w - u])
 
 

@@ -208,3 +208,35 @@ def test_weights_are_those_of_their_own_call(route):
     assert not torch.equal(want[0], want[1])
     for i in range(3, 33):
         assert torch.equal(mass[i], want[i % 3])
+
+
+# ---------------------------------------------------------------- bounds
+@pytest.mark.parametrize("grow", [False, True])
+@pytest.mark.parametrize("D,P", [(64, 16), (72, 32), (128, 64)])
+def test_bounds_behind_a_channel_of_nan_codes_and_behind_tokens_taken_back(D, P, grow):
+    """While a page's scale stays its bounds are widened; where it grows they are found anew."""
+    c = pool(4, 2, D, P, 81)
+    ref = to_np(c)
+    table = np.array([[2, 0]], np.int32)
+
+    def append(k, v, n):
+        kv.cache_append(c, k.to(DEV), v.to(DEV), ints(table), ints([n]))
+        oc.cache_append(ref, table, np.array([n]), np.array([k.shape[2]]), k.double().numpy(), v.double().numpy())
+        same_cache(c, ref)
+
+    k, v = rows((1, 2, 6, D), BF, 82), rows((1, 2, 6, D), BF, 83)
+    k[..., 0] = 4.0  # the first tokens hold the largest
+    k[:, :, :, 3], k[:, 1, :, D - 1] = float("nan"), float("nan")
+    append(k, v, 6)
+    assert (c.k_bounds[2, :, :, 3] == 0).all() and (c.k_bounds[2, 1, :, D - 1] == 0).all()
+    # all positive behind it: the 0 stays the lower bound where the scale stays
+    k2, v2 = rows((1, 2, 3, D), BF, 84).abs() + 0.5, rows((1, 2, 3, D), BF, 85)
+    k2 = (k2 * (60.0 if grow else 0.5)).to(BF)
+    append(k2, v2, 9)
+    lower = c.k_bounds[2, :, 1, 3]
+    assert (lower > 0).all() if grow else (lower == 0).all()
+    # the last two are taken back and others take their places
+    k3, v3 = (rows((1, 2, 4, D), BF, 86 + i, 0.01) for i in range(2))
+    append(k3, v3, 11)
+    assert (c.k_bounds[2, :, 0, 3] > 0).all()
+    assert binding.device_status() == binding.ATTN_OK
