@@ -191,7 +191,7 @@ ATTN_API size_t attn_cache_evict_workspace(const attn_cache_t* cache,
  *
  * Sequence b and head h keep all tokens if lens[b] <= keep; otherwise the last
  * `recent` ones and, of the others, the keep - recent with the largest
- * mass[b, h, j] (equal ones: the lowest j; NaN counts as the lowest weight).
+ * mass[b, h, j] (equal ones: the lowest j; NaN counts as less than any weight).
  * They are copied in their order to positions 0, 1, ... of the pages
  * dst_table[b, :], quantised anew with scales and bounds as append makes them
  * (exact while no code becomes subnormal).  Every head keeps the same number,

@@ -186,8 +186,9 @@ def cache_evict(cache, mass, table, lens, dst_table, keep, recent):
             at = list(range(n))
             if n > keep:
                 tail = min(recent, n)
-                w = [-np.inf if np.isnan(x) else x for x in mass[b, h, :n - tail]]
-                best = sorted(range(n - tail), key=lambda j: (-w[j], j))[:keep - tail]
+                w = mass[b, h, :n - tail]
+                best = sorted(range(n - tail), key=lambda j: (np.isnan(w[j]), 0.0 if np.isnan(w[j]) else -w[j], j))
+                best = best[:keep - tail]
                 at = sorted(best) + list(range(n - tail, n))
             kept[b, h, :len(at)] = at
             moved[b, h, :len(at)] = mass[b, h, at]

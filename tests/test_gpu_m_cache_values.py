@@ -240,3 +240,20 @@ def test_bounds_behind_a_channel_of_nan_codes_and_behind_tokens_taken_back(D, P,
     append(k3, v3, 11)
     assert (c.k_bounds[2, :, 0, 3] > 0).all()
     assert binding.device_status() == binding.ATTN_OK
+
+
+@pytest.mark.parametrize("n,keep", [(300, 100), (3000, 1200), (20000, 9000)])
+def test_evict_takes_nan_weights_last_of_all(n, keep):
+    """NaN counts as less than every other weight, -inf among them."""
+    D, P = 64, 16
+    dw = -(-keep // P)
+    c, ref, table, free = filled([n], 1, D, P, BF, 91, extra=dw)
+    mass = np.random.default_rng(92).choice([-np.inf, np.nan, 1.0, 2.0, np.inf], (1, 1, table.shape[1] * P),
+                                            p=[0.5, 0.35, 0.05, 0.05, 0.05]).astype(np.float32)
+    dst = free[:dw].reshape(1, dw).astype(np.int32)
+    want = oc.cache_evict(ref, mass, table, np.array([n]), dst, keep, 10)
+    got = kv.cache_evict(c, torch.from_numpy(mass).to(DEV), ints(table), ints([n]), ints(dst), keep, 10)
+    assert not np.isnan(mass[0, 0, want[0][0, 0, :-10]]).any()
+    for g, w in zip(got, want):
+        assert np.array_equal(g.cpu().numpy(), w, equal_nan=True)
+    same_cache(c, ref)
