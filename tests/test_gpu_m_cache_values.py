@@ -257,3 +257,24 @@ def test_evict_takes_nan_weights_last_of_all(n, keep):
     for g, w in zip(got, want):
         assert np.array_equal(g.cpu().numpy(), w, equal_nan=True)
     same_cache(c, ref)
+
+
+# ---------------------------------------------------------------- scales
+@pytest.mark.parametrize("lo,hi", [(-100, -97), (-30, -20), (100, 119)])
+def test_scales_over_the_whole_range(lo, hi):
+    """Scales from 2^-100, the least that append writes, up to fp32's end; not powers of two."""
+    lens, D = [700, 65], 64
+    for width in (12, 2000):
+        c, ref, table, _ = filled(lens, 2, D, 64, BF, 101, width=width)
+        s = np.exp2(np.random.default_rng(102).uniform(lo, hi, c.v_scale.shape)).astype(np.float32)
+        c.v_scale.copy_(torch.from_numpy(s))
+        ref["v_scale"] = s
+        q = rows((2, 4, 1, D), BF, 103)
+        out, lse, _ = call(c, q, table, lens, [1, 1])
+        ro, rl, _, av, aq = oc.cache_attention(ref, table, np.array(lens), [1, 1], q.double().numpy(), D ** -0.5)
+        o = out.double().cpu().numpy()
+        # the output's half step, P's 2^-11 and what check_fwd allows the scores, ex2 and sums
+        dt = (D + 16) * 2.0 ** -23 * aq.max()
+        assert (np.abs(o - ro) <= 2.0 ** -8 * np.abs(ro) + (2.0 ** -11 + 2 * dt + 2.0 ** -18) * 1.01 * av).all()
+        assert np.abs(lse.cpu().numpy() - rl).max() <= dt + 2.0 ** -20 + 2.0 ** -22 * np.abs(rl).max()
+    assert binding.device_status() == binding.ATTN_OK
