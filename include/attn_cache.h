@@ -20,7 +20,8 @@
  *              up to a multiple of 16; channels from head_dim on are never read
  *              as values (append writes them as zero)
  *   k_scale,   fp32 [pages, heads]: the value held is code · scale.  append and
- *   v_scale    evict write powers of two; the attention takes any positive scale
+ *   v_scale    evict write powers of two from 2^-100 on; the attention takes any
+ *              finite scale from 2^-100 on (less: values may count as zero)
  *   k_bounds   int8 [pages, heads, 2, pitch]: for each channel the upper, then
  *              the lower bound of the page's key codes in steps of 448/127
  *              (ceil(max·127/448), floor(min·127/448); NaN codes left out, 0 where
