@@ -132,6 +132,9 @@ attn_status_t check_queries(const attn_cache_t* c, const attn_cache_seqs_t* s, i
   return ATTN_OK;
 }
 
+// Entries of a page list: their tokens are counted in 32 bits.
+constexpr int64_t kMaxListed = INT32_MAX / 64;
+
 // Keys of a head in the score workspace: whole chunks.
 int64_t score_cols(const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t listed, bool has_list) {
   const int64_t pages = has_list && listed < s->width ? listed : s->width;
@@ -298,7 +301,7 @@ attn_status_t attn_cache_append(const attn_cache_t* cache, const attn_cache_seqs
 size_t attn_cache_fwd_workspace(const attn_cache_t* cache, const attn_cache_seqs_t* seqs,
                                 int64_t listed, int64_t q_heads, int64_t T, int with_mass) {
   int dev = -1, sms = 0;
-  if (check_cache(cache, seqs) != ATTN_OK || listed < 0 ||
+  if (check_cache(cache, seqs) != ATTN_OK || listed < 0 || listed > kMaxListed ||
       check_queries(cache, seqs, q_heads, T) != ATTN_OK || !sm_count(&dev, &sms))
     return 0;
   return fwd_bytes(plan_of(cache, seqs, listed, q_heads, T, dev, sms), cache, seqs, listed, with_mass != 0);
@@ -314,7 +317,7 @@ attn_status_t attn_cache_fwd(const attn_cache_t* cache, const attn_cache_seqs_t*
   if (s != ATTN_OK) return s;
   if (!q || !out || !lse) return ATTN_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
-  if (pages ? (listed < 1 || listed > INT32_MAX / 64) : listed != 0) return ATTN_ERR_INVALID_ARG;
+  if (pages ? (listed < 1 || listed > kMaxListed) : listed != 0) return ATTN_ERR_INVALID_ARG;
   s = check_queries(cache, seqs, q_heads, T);
   if (s != ATTN_OK) return s;
   s = check_pointers(cache, seqs);

@@ -278,3 +278,15 @@ def test_scales_over_the_whole_range(lo, hi):
         assert (np.abs(o - ro) <= 2.0 ** -8 * np.abs(ro) + (2.0 ** -11 + 2 * dt + 2.0 ** -18) * 1.01 * av).all()
         assert np.abs(lse.cpu().numpy() - rl).max() <= dt + 2.0 ** -20 + 2.0 ** -22 * np.abs(rl).max()
     assert binding.device_status() == binding.ATTN_OK
+
+
+# ---------------------------------------------------------------- workspaces
+def test_the_workspace_query_refuses_what_the_attention_refuses():
+    c, _, table, _ = filled([30], 1, 64, 16, BF, 111)
+    tb, ln = ints(table), ints([30])
+    assert kv.cache_fwd_workspace(c, tb, ln, 1, 1, listed=(2 ** 31 - 1) // 64) >= 16
+    for kw in (dict(listed=(2 ** 31 - 1) // 64 + 1), dict(listed=2 ** 40), dict(listed=-1), dict(q_heads=0),
+               dict(T=0), dict(T=65)):
+        with pytest.raises(binding.AttnError) as e:
+            kv.cache_fwd_workspace(c, tb, ln, **{**dict(q_heads=1, T=1), **kw})
+        assert e.value.code == binding.ATTN_ERR_INVALID_ARG
