@@ -63,6 +63,7 @@ struct CacheSelectParams {
   int count;
   int* pages;     // [batch, heads, count]
   float* scores;  // [batch, heads, width]
+  int sms;        // of the device
 };
 cudaError_t cache_select_launch(const CacheSelectParams& p, bool f16, cudaStream_t stream);
 

@@ -400,7 +400,10 @@ attn_status_t attn_cache_select(const attn_cache_t* cache, const attn_cache_seqs
   int* status = nullptr;
   s = status_words(&status);
   if (s != ATTN_OK) return s;
+  int dev = -1, sms = 0;
+  if (!sm_count(&dev, &sms)) return ATTN_ERR_CUDA;
   ea::CacheSelectParams p;
+  p.sms = sms;
   p.c = view_of(cache);
   p.s = seqs_of(seqs, T, status);
   p.q = static_cast<const uint16_t*>(q);

@@ -196,12 +196,14 @@ __global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const CacheSel
 
 template <int UNITS, int ROWS>
 cudaError_t score(const CacheSelectParams& p, bool f16, cudaStream_t stream) {
-  // the fewest pages a group with which one wave, four CTAs on each of about 152
-  // SMs, covers all (a second wave of a few CTAs took as long as the first)
+  // the fewest pages a group with which four CTAs on each SM cover all: one wave, as
+  // the registers of 8 rows of 128 channels allow (a second wave of a few CTAs took as
+  // long as the first; variants of fewer registers were not measured apart)
+  const int64_t wave = 4ll * p.sms;
   auto ctas = [&](int64_t k) { return static_cast<int>((p.s.width + kScoreGroups * k - 1) / (kScoreGroups * k)); };
   const int64_t heads = static_cast<int64_t>(p.s.batch) * p.c.heads;
-  int per = static_cast<int>((heads * ctas(1) + 607) / 608);
-  while (heads * ctas(per) > 608 && ctas(per) > 1) ++per;
+  int per = static_cast<int>((heads * ctas(1) + wave - 1) / wave);
+  while (heads * ctas(per) > wave && ctas(per) > 1) ++per;
   const dim3 grid(ctas(per), p.c.heads, p.s.batch);
   if (f16) cache_score_kernel<UNITS, ROWS, true><<<grid, kScoreThreads, 0, stream>>>(p, per);
   else cache_score_kernel<UNITS, ROWS, false><<<grid, kScoreThreads, 0, stream>>>(p, per);

@@ -290,3 +290,18 @@ def test_the_workspace_query_refuses_what_the_attention_refuses():
         with pytest.raises(binding.AttnError) as e:
             kv.cache_fwd_workspace(c, tb, ln, **{**dict(q_heads=1, T=1), **kw})
         assert e.value.code == binding.ATTN_ERR_INVALID_ARG
+
+
+# ---------------------------------------------------------------- select
+@pytest.mark.parametrize("B,H,G,D,width", [(40, 16, 1, 64, 100), (10, 64, 2, 128, 70), (3, 2, 12, 128, 40000)])
+def test_select_where_a_group_takes_several_pages(B, H, G, D, width):
+    """More heads and pages than one wave of CTAs takes one page a group of."""
+    P = 16
+    lens = [int(n) for n in np.random.default_rng(121).integers(1, 60 * P, B)]
+    c, ref, table, _ = filled(lens, H, D, P, FP, 122, width=width)
+    q = rows((B, H * G, 1, D), FP, 123)
+    pages, scores = kv.cache_select(q.to(DEV), c, ints(table), ints(lens), 7)
+    rp, rs = oc.cache_select(ref, table, np.array(lens), [1] * B, q.float().numpy(), 7)
+    assert np.array_equal(scores.cpu().numpy(), rs)
+    assert np.array_equal(pages.cpu().numpy(), rp)
+    assert binding.device_status() == binding.ATTN_OK
