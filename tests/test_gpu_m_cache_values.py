@@ -305,3 +305,36 @@ def test_select_where_a_group_takes_several_pages(B, H, G, D, width):
     assert np.array_equal(scores.cpu().numpy(), rs)
     assert np.array_equal(pages.cpu().numpy(), rp)
     assert binding.device_status() == binding.ATTN_OK
+
+
+# ---------------------------------------------------------------- every kernel of the attention
+ROWS = {8: (4, 2), 16: (8, 2), 24: (8, 3), 32: (16, 2), 40: (8, 5)}  # query rows of a head: heads of a group, tokens
+
+
+@pytest.mark.parametrize("D,n", [(D, n) for D in (64, 48) for n in ROWS] +
+                         [(D, n) for D in (128, 112, 256, 208) for n in (8, 16, 24)])
+@pytest.mark.parametrize("route", ROUTES)
+def test_every_width_and_number_of_rows_on_every_route(route, D, n):
+    """Rows of whole 32 bytes and of odd 16-byte units; up to 32 rows a pass at 64 channels, 16 at more, and two
+    or three passes."""
+    lens, width = ROUTES[route]
+    G, T = ROWS[n]
+    c, ref, table, _ = filled(lens, 1, D, 64, FP, 131, width=width)
+    q = rows((len(lens), G, T, D), FP, 132)
+    attend(c, ref, q, table, lens, np.minimum(T, lens), FP)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("P,D", [(16, 64), (32, 80), (64, 256)])
+def test_drafted_tokens_of_which_some_see_no_key_of_the_last_chunk(P, D, wide):
+    """Tokens at 61 .. 65: the first three see none of the chunk of 64 and 65, where keys hold NaN."""
+    lens, T = [66, 130, 5], 5
+    c, ref, table, _ = filled(lens, 2, D, P, BF, 141, width=-(-130 // P) + (120000 // P if wide else 0))
+    for b, n in enumerate(lens):
+        at = n - 1 if b < 2 else 3  # the last token's key; of five tokens the fourth's
+        for held in (c.k, ref["k"]):
+            held[int(table[b, at // P]), 1, at % P, 2] = 0x7f
+    q = rows((3, 6, T, D), BF, 142)
+    q[1, 0, 1] = float("inf")
+    q[0, 3, 4, 1], q[0, 1, 2, 1] = float("nan"), float("-inf")
+    attend(c, ref, q, table, lens, [T, T - 2, T], BF)
