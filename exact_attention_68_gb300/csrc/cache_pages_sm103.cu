@@ -317,7 +317,7 @@ __device__ __forceinline__ void move_page(const CacheView& c, const SeqView& sq,
           e4m3x4_to_f16(x[i][w], &h0, &h1);
           x[i][w] = pack_e4m3x2_f16(mul_f16x2(h0, ff)) | (pack_e4m3x2_f16(mul_f16x2(h1, ff)) << 16);
         }
-      } else if (f != 1.f) {
+      } else if (f != 1.f && f < INFINITY) {  // inf: codes are 0 (those of a token have |code| <= 448 / f) or NaN, and stay
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           uint32_t h0, h1;

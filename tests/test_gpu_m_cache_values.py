@@ -338,3 +338,35 @@ def test_drafted_tokens_of_which_some_see_no_key_of_the_last_chunk(P, D, wide):
     q[1, 0, 1] = float("inf")
     q[0, 3, 4, 1], q[0, 1, 2, 1] = float("nan"), float("-inf")
     attend(c, ref, q, table, lens, [T, T - 2, T], BF)
+
+
+# ---------------------------------------------------------------- what evict moves
+@pytest.mark.parametrize("D,P", [(64, 16), (72, 32), (128, 64), (256, 16)])
+def test_evict_moves_zeros_and_nans_of_pages_of_any_scale(D, P):
+    """Kept tokens that are all zero stay zero whatever the scale of the page they come from."""
+    n, keep, H = 6 * P, 3 * P - 1, 2
+    c, ref, table, free = filled([n], H, D, P, BF, 151, extra=3)
+    codes = np.random.default_rng(152).integers(0, 256, ref["k"].shape).astype(np.uint8)  # NaN codes among them
+    for name in "kv":
+        for i in range(4):  # zeros of both signs; in the second and fourth page NaN beside them
+            codes[table[0, i]] = np.where(codes[table[0, i]] & 1, 0x80, 0)
+            if i % 2:
+                codes[table[0, i], :, ::3, 1::5] = 0x7f
+        codes[..., D:] = 0
+        ref[name][:] = codes
+        getattr(c, name).copy_(torch.from_numpy(codes))
+        s = np.exp2(np.random.default_rng(153).integers(-90, 119, ref[name + "_scale"].shape)).astype(np.float32)
+        s[table[0, :4]] = 2.0 ** np.array([119, 100, 28, 27])[:, None]
+        s[table[0, 4:]] = 2.0 ** np.array([3, -20])[:, None]
+        ref[name + "_scale"][:] = s
+        getattr(c, name + "_scale").copy_(torch.from_numpy(s))
+    dst = free[:3].reshape(1, 3).astype(np.int32)
+    mass = np.zeros((1, H, n), np.float32)
+    mass[0, 0, :2 * P] = 1.0     # head 0 keeps the first pages and the last tokens
+    mass[0, 1, P:4 * P:2] = 1.0  # head 1 parts of three
+    want = oc.cache_evict(ref, mass, table, np.array([n]), dst, keep, P // 2)
+    got = kv.cache_evict(c, torch.from_numpy(mass).to(DEV), ints(table), ints([n]), ints(dst), keep, P // 2)
+    for g, w in zip(got, want):
+        assert np.array_equal(g.cpu().numpy(), w)
+    same_cache(c, ref)
+    assert binding.device_status() == binding.ATTN_OK
