@@ -199,7 +199,8 @@ ATTN_API size_t attn_cache_evict_workspace(const attn_cache_t* cache,
  * so the sequence stays one: its table is dst_table and its length new_lens
  * from then on, and its old pages are free.
  *
- *   seqs       fresh is ignored
+ *   seqs       fresh is ignored; a sequence left out counts as empty, tokens whose
+ *              table entry is out of range are moved as zeros
  *   mass       device fp32 [batch, heads, width·page] (read)
  *   dst_table  device int32 [batch, dst_width]: pages of the same pool.  The
  *              entries that are needed must differ from each other and from

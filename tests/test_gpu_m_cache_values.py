@@ -370,3 +370,133 @@ def test_evict_moves_zeros_and_nans_of_pages_of_any_scale(D, P):
         assert np.array_equal(g.cpu().numpy(), w)
     same_cache(c, ref)
     assert binding.device_status() == binding.ATTN_OK
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("D,P", [(64, 16), (72, 32), (256, 64)])
+def test_append_of_extremes_in_both_types(D, P, dtype):
+    """Largest and smallest values, infinities, NaN and zeros of both signs, in pages fresh and in use."""
+    c = pool(4, 2, D, P, 161)
+    ref = to_np(c)
+    table = np.array([[2, 0, 1]], np.int32)
+    big, least = torch.finfo(dtype).max, 2.0 ** (-24 if dtype is FP else -133)
+    rng = np.random.default_rng(162)
+    n = 0
+    for step, T in enumerate([P // 2, 3, P // 2, 1, P // 4]):
+        pick = [[0.0, -0.0, least, -3 * least], [1.0, -2.5, np.nan, 0.0], [big, -big, 1e-3, np.inf], [-np.inf, 1.0, 5.0, -0.0],
+                [np.nan, np.inf, -np.inf, 0.0]][step]
+        k, v = (torch.from_numpy(rng.choice(pick, (1, 2, T, D))).to(dtype) for _ in range(2))
+        n += T
+        kv.cache_append(c, k.to(DEV), v.to(DEV), ints(table), ints([n]))
+        oc.cache_append(ref, table, np.array([n]), np.array([T]), k.double().numpy(), v.double().numpy())
+        same_cache(c, ref)
+    assert binding.device_status() == binding.ATTN_OK
+
+
+# ---------------------------------------------------------------- sizes
+@pytest.mark.parametrize("D", [256, 208])  # tiled copies, runs of bytes
+def test_a_pool_beyond_4_gib(D):
+    """Pages whose offset passes 32 bits hold what the same pages of a small pool do."""
+    H, P, n, T = 2, 64, 500, 70
+    M, keep = -(-n // P), 200
+    kx, vx = (rows((2, H, n, D), BF, 171 + i).to(DEV) for i in range(2))
+    q = rows((2, 8, 3, D), BF, 173).to(DEV)
+    got = []
+    for total in (163840, 2 * M + 8):
+        c = kv.cache_alloc(total, H, D, P, device=DEV)
+        assert total < 1000 or c.k.numel() > 2 ** 32
+        table = ints(np.random.default_rng(174).permutation(2 * M).reshape(2, M) + total - 2 * M - 8)
+        dst = ints(np.arange(8).reshape(2, 4) + total - 8)
+        mass = torch.zeros((2, H, M * P), device=DEV)
+        kv.cache_append(c, kx[:, :, :n - T].contiguous(), vx[:, :, :n - T].contiguous(), table, ints([n - T] * 2))
+        kv.cache_append(c, kx[:, :, n - T:].contiguous(), vx[:, :, n - T:].contiguous(), table, ints([n] * 2))
+        out, lse = kv.cache_fwd(q, c, table, ints([n] * 2), mass=mass)
+        pages, scores = kv.cache_select(q, c, table, ints([n] * 2), 4)
+        out2, lse2 = kv.cache_fwd(q, c, table, ints([n] * 2), pages=pages)
+        kept, lens, mass2 = kv.cache_evict(c, mass, table, ints([n] * 2), dst, keep, 20)
+        out3, lse3 = kv.cache_fwd(q, c, dst, lens)
+        got.append((out, lse, mass, pages, scores, out2, lse2, kept, lens, mass2, out3, lse3))
+    assert all(torch.isfinite(x).all() for x in (got[0][0].float(), got[0][1], got[0][10].float()))
+    assert got[0][0].float().abs().max() > 0
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert binding.device_status() == binding.ATTN_OK
+
+
+def test_thousands_of_sequences_of_which_many_have_nothing_to_do():
+    B, D, P = 5000, 64, 16
+    rng = np.random.default_rng(181)
+    lens = rng.integers(0, 40, B)
+    fresh = np.minimum(rng.integers(0, 2, B), lens)
+    c, ref, table, _ = filled([int(x) for x in lens], 1, D, P, BF, 182)
+    q = rows((B, 2, 1, D), BF, 183)
+    out, lse, _ = call(c, q, table, lens, fresh, mass=False)
+    ro, rl, _, av, aq = oc.cache_attention(ref, table, lens, fresh, q.double().numpy(), 0.125)
+    check_fwd(out, lse, ro, rl, av, aq, D, BF, fresh)
+    idle = torch.from_numpy(fresh == 0).to(DEV)
+    assert (out[idle] == 7.0).all() and (lse[idle] == 7.0).all()
+    pages, scores = kv.cache_select(q.to(DEV), c, ints(table), ints(lens), 2, fresh=ints(fresh))
+    rp, rs = oc.cache_select(ref, table, lens, fresh, q.float().numpy(), 2)
+    assert np.array_equal(scores.cpu().numpy(), rs) and np.array_equal(pages.cpu().numpy(), rp)
+    assert binding.device_status() == binding.ATTN_OK
+
+
+# ---------------------------------------------------------------- eviction in a graph, and of what is left out
+def test_a_captured_eviction_replays_on_new_lengths_and_weights():
+    D, P, H, keep, recent = 128, 16, 2, 60, 10
+    dw = -(-keep // P)
+    c, ref, table, free = filled([200, 130], H, D, P, BF, 191, extra=2 * dw)
+    dst = free[:2 * dw].reshape(2, dw).astype(np.int32)
+    tb, ds, lens = ints(table), ints(dst), ints([200, 130])
+    mass = torch.zeros((2, H, table.shape[1] * P), device=DEV)
+    kept, new_lens = torch.empty((2, H, keep), dtype=torch.int32, device=DEV), ints([0, 0])
+    new_mass = torch.empty((2, H, dw * P), device=DEV)
+    ws = torch.empty(kv.cache_evict_workspace(c, tb, lens, dw), dtype=torch.uint8, device=DEV)
+
+    def evict():
+        kv.cache_evict(c, mass, tb, lens, ds, keep, recent, kept=kept, new_lens=new_lens, new_mass=new_mass,
+                       workspace=ws)
+
+    evict()
+    torch.cuda.synchronize()
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(g, stream=side):
+            evict()
+    torch.cuda.current_stream().wait_stream(side)
+    for i, n in enumerate([[200, 130], [61, 60], [5, 0], [199, 64]]):
+        m = np.random.default_rng(192 + i).random(tuple(mass.shape)).astype(np.float32)
+        mass.copy_(torch.from_numpy(m)), lens.copy_(ints(n))
+        before = to_np(c)
+        g.replay()
+        torch.cuda.synchronize()
+        want = oc.cache_evict(before, m, table, np.array(n), dst, keep, recent)
+        for a, w in zip((kept, new_lens, new_mass), want):
+            assert np.array_equal(a.cpu().numpy(), w)
+        same_cache(c, before)
+    assert binding.device_status() == binding.ATTN_OK
+
+
+@pytest.mark.parametrize("bad", [-1, 200, 2 ** 31 - 1])
+def test_evict_counts_a_sequence_left_out_as_empty_and_tokens_without_a_page_as_zeros(bad):
+    D, P, keep = 64, 16, 20
+    c, ref, table, free = filled([60, 50, 40], 1, D, P, BF, 201, extra=6)
+    dst = free[:6].reshape(3, 2).astype(np.int32)
+    m = np.random.default_rng(202).random((3, 1, table.shape[1] * P)).astype(np.float32)
+    t = table.copy()
+    t[2, 0] = bad  # no page of the pool (for 200: of 19)
+    n = np.array([60, bad, 40])
+    kept, lens, mass = kv.cache_evict(c, torch.from_numpy(m).to(DEV), ints(t), ints(n), ints(dst), keep, 4)
+    torch.cuda.synchronize()
+    assert binding.device_status() == binding.ATTN_ERR_DEVICE_CHECK
+    assert lens.tolist() == [20, 0, 20] and (kept[1] == -1).all() and (mass[1] == 0).all()
+    # as if the tokens of that page were zeros, and the sequence empty
+    for name in "kv":
+        ref[name][table[2, 0]] = 0
+    want = oc.cache_evict(ref, m, table, np.array([60, 0, 40]), dst, keep, 4)
+    for a, w in zip((kept, lens, mass), want):
+        assert np.array_equal(a.cpu().numpy(), w)
+    for name in "kv":
+        ref[name][table[2, 0]] = getattr(c, name)[int(table[2, 0])].cpu().numpy()
+    same_cache(c, ref)
