@@ -148,6 +148,9 @@ int64_t score_cols(const attn_cache_t* c, const attn_cache_seqs_t* s, int64_t li
 // CTA 21, 40 us; 720 of 3, 16 chunks 18, 48 and 30, 51 us; 1024 of 16, 32, 64 chunks 64,
 // 101, 181 and 68, 96, 168 us, of 2 to 32 chunks 70 and 79 us.
 constexpr int64_t kShortSegment = 16;
+// Sizes here are those of the table, since lengths are on the device: under a table of
+// 2048 pages one sequence of 1000 keys takes 13.1 us (tight 8.7), 720 segments of up to 3
+// chunks 32.5 (18.9), 16 sequences of 500-8192 keys 37.6 (37.0).
 struct Plan {
   int width, tiles, passes, ctas, workers;
   int cluster;

@@ -25,13 +25,18 @@
 // instead of 243.)  A 16-channel unit of a key row is one 16-byte load per lane: a lane's four
 // consecutive channels of each k-step are the channels that its Q fragment
 // holds, so no data moves between lanes.  V, stored like K, comes transposed
-// out of ldmatrix; P crosses the lanes by movmatrix.  A tcgen05 tile has 128
-// rows for these 8, and the tensor pipe is not what bounds the kernel.
+// out of ldmatrix; P crosses the lanes by movmatrix.  tcgen05 with the cache as
+// its M operand, 64 keys or channels by 8 to 256 rows, would take a copy of the codes
+// in fp16 in shared memory: nothing to gain up to 16 rows, where the memory is the
+// bound, but it would take 17 and more in one pass, where this kernel reads and
+// converts the cache once for every 16 (32 at 64 channels).
 //
 // Page scales of V enter P: O is kept relative to r, the running maximum of
 // t + log2(v_scale), and P = 2^(t + log2 v_scale - r + 14) fits fp16 however the
 // pages' scales differ; its smallest step, 2^-38 of the largest term, is far
-// below the 11 bits it is rounded to.
+// below the 11 bits it is rounded to.  Those 11 bits are 3 more than a bf16 output
+// keeps and as many as an fp16 one (2.2e-4 from the exact output, with fp32 weights
+// 2.0e-4); more would take a second product for the rest of P.
 //
 // m is -inf only for a row that has met no key it may see: once it has, m is at
 // least kLowest, also where all its scores are -inf (l is 0, and the row NaN as
@@ -44,9 +49,10 @@
 // each segment instead and joins it through its shared memory: no second launch.
 //
 // Measured (8 key heads, 4 query heads each, 128 channels): 64 sequences of
-// 8000-16384 keys 249 us = 6.42 TB/s, 94 % of the measured copy rate; 16 of
-// 500-8192 keys 37.2 us = 4.2 TB/s (the longest bound it: a CTA streams at most
-// about 65 GB/s); one of 1000 keys 8.5 us (latency).  About 1040 instructions a
+// 8000-16384 keys 246 us = 6.5 TB/s, 96 % of the measured copy rate; 16 of
+// 500-8192 keys 36.9 us = 4.2 TB/s (a CTA has each segment, 24 of 152 SMs none, and
+// the longest end last at about 65 GB/s a CTA; dealt evenly, the second launch costs
+// more than that); one of 1000 keys 8.6 us (latency).  About 1040 instructions a
 // chunk, 256 of them conversions of codes.
 #include <atomic>
 #include <type_traits>

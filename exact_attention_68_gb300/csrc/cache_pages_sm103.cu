@@ -10,7 +10,7 @@
 //
 // Bytes are what both cannot do without, 6·D a token and head to append and
 // 4·D to move.  Measured at 8 heads of 128 channels: 2 x 8192 tokens appended in
-// 21.1 us = 4.8 TB/s, about 12 instructions a value issued at 59 % of the rate;
+// 21.2 us = 4.7 TB/s, about 12 instructions a value issued at 61 % of the rate;
 // one token of each of 64 sequences 5.0 us (latency); 8 sequences cut to 4096
 // tokens a head moved in 38 us, 134 MB as random 128-byte rows (a page's chain of
 // loads, position, page, codes; 55 % of the issue rate), behind 13 us for choosing them.

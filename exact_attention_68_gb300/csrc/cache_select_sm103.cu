@@ -10,9 +10,10 @@
 //
 // Bound: 2·D bytes a page and head (the page's keys and values are 2·D·page),
 // read as 256-byte rows at random: 8 sequences of 50001-65536 tokens in pages of
-// 16, 8 heads of 128 channels: 26.7 us for 61.6 MB, of which 9 us choosing 256 of
-// 4096 pages, 64 CTAs each on its own row of scores; slope 3.1 TB/s.  One
-// sequence of 256 pages 7.3 us (latency of two kernels).
+// 16, 8 heads of 128 channels: 26.9 us for 61.6 MB, of which 9 us choosing 256 of
+// 4096 pages, 64 CTAs each on its own row of scores; slope 3.1 TB/s with 20 % of the
+// warps active, so that too few bytes are in flight.  One sequence of 256 pages 7.2
+// us (latency of two kernels).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -196,9 +197,12 @@ __global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const CacheSel
 
 template <int UNITS, int ROWS>
 cudaError_t score(const CacheSelectParams& p, bool f16, cudaStream_t stream) {
-  // the fewest pages a group with which four CTAs on each SM cover all: one wave, as
-  // the registers of 8 rows of 128 channels allow (a second wave of a few CTAs took as
-  // long as the first; variants of fewer registers were not measured apart)
+  // the fewest pages a group with which four CTAs on each SM cover all: one wave with
+  // the registers of 4 rows of 128 channels (a second wave of a few CTAs took as long as
+  // the first).  Measured there; of the other variants, 64 to 189 registers, two to
+  // eight CTAs fit.  The steps go by the width of the table: pages behind a sequence's end
+  // cost theirs (8 sequences of 50001-65536 tokens in pages of 16: 26.9 us, under a
+  // table twice as wide 39.4 us)
   const int64_t wave = 4ll * p.sms;
   auto ctas = [&](int64_t k) { return static_cast<int>((p.s.width + kScoreGroups * k - 1) / (kScoreGroups * k)); };
   const int64_t heads = static_cast<int64_t>(p.s.batch) * p.c.heads;

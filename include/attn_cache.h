@@ -145,9 +145,19 @@ ATTN_API size_t attn_cache_fwd_workspace(const attn_cache_t* cache, const attn_c
  * A query that may attend to no key gets out = 0 and lse = -inf.  One that may,
  * and has a NaN score, a score of +inf or no score but -inf, gets NaN in out and
  * lse and adds NaN to the mass of the keys it may attend to, as the formula does;
- * a NaN value code makes its channel of out NaN.  Rows of
- * tokens from fresh[b] on, and sequences left out, are not written; what q
- * holds there, and slots behind a sequence's end, may be anything.  Results do
+ * a NaN value code makes its channel of out NaN.
+ *
+ * Scores, maxima, sums and out's sums are fp32.  For the product with V the
+ * weights are rounded to fp16 (half a step: 2^-11 of a weight), whatever `dtype`:
+ * that is 1/8 of bf16's half step, and as much as fp16's, so that fp16 results
+ * stand about a tenth further from the exact ones than with fp32 weights.  A
+ * weight in mass is 2^(t - lse) of the stored lse, whose rounding adds |lse|·2^-23
+ * to its relative error.  How work is cut, and the workspace, go by `width` (or
+ * `listed`), not by lens, which are on the device: a table cut to the longest
+ * sequence's pages saves small calls up to a half of their time.
+ *
+ * Rows of tokens from fresh[b] on, and sequences left out, are not written; what
+ * q holds there, and slots behind a sequence's end, may be anything.  Results do
  * not depend on the order in which the GPU ran the work: every sum has a fixed
  * order.
  */
