@@ -197,3 +197,34 @@ def test_oracle_attention_meets_the_dense_oracle():
         ro, rl = attention_fwd(q[:, h:h + 1], held["k"][:, h // 2:h // 2 + 1], held["v"][:, h // 2:h // 2 + 1], 0.25, True)
         assert np.allclose(out[:, h], ro[:, 0, -T:], atol=1e-12) and np.allclose(lse[:, h], rl[:, 0, -T:], atol=1e-12)
     assert np.allclose(mass.sum(2), 2 * T)
+
+
+def test_oracle_bounds_widen_while_the_scale_stays():
+    """A channel of NaN codes leaves 0 inside, tokens taken back their bounds, until the scale grows."""
+    pool = dict(k=np.zeros((2, 1, 16, 16), np.uint8), v=np.zeros((2, 1, 16, 16), np.uint8),
+                k_scale=np.ones((2, 1), np.float32), v_scale=np.ones((2, 1), np.float32),
+                k_bounds=np.full((2, 1, 2, 16), 99, np.int8), head_dim=16)
+    table = np.array([[1]])
+
+    def append(x, n):
+        x = np.asarray(x, float).reshape(1, 1, -1, 1) * np.ones(16)
+        x[..., 0] = np.where(np.isnan(x[..., 1]), 448.0, x[..., 1])
+        oc.cache_append(pool, table, np.array([n]), np.array([x.shape[2]]), x, x)
+        return pool["k_bounds"][1, 0, :, 1].tolist()
+
+    assert append([np.nan, np.nan], 2) == [0, 0]
+    assert append([112.0], 3) == [math.ceil(112 * 127 / 448), 0]
+    assert append([224.0, 224.0], 5) == [math.ceil(224 * 127 / 448), 0]
+    assert append([56.0], 4) == [math.ceil(224 * 127 / 448), 0]  # one of the two taken back, another in its place
+    assert append([896.0], 5)[1] == math.floor(28 * 127 / 448)   # a larger scale: found anew, 56 / 2 the least
+    assert (pool["k_bounds"][0] == 99).all()
+
+
+def test_oracle_evicts_nan_weights_first():
+    pool = {n: np.zeros((3, 1, 16, 16), np.uint8) for n in "kv"}
+    pool.update(k_scale=np.ones((3, 1), np.float32), v_scale=np.ones((3, 1), np.float32),
+                k_bounds=np.zeros((3, 1, 2, 16), np.int8), head_dim=16)
+    mass = np.full((1, 1, 16), -np.inf, np.float32)
+    mass[0, 0, [0, 1, 5]], mass[0, 0, [3, 7]] = np.nan, 1.0
+    kept, lens, _ = oc.cache_evict(pool, mass, np.array([[0]]), np.array([10]), np.array([[2]]), 6, 1)
+    assert kept[0, 0].tolist() == [2, 3, 4, 6, 7, 9] and lens.tolist() == [6]

@@ -75,7 +75,7 @@ def meets(out, lse, mass, ref, D, dtype, fresh):
     check_fwd(o.masked_fill(none, 0.0), z.masked_fill(gone, 0.0), ro, rl, av, aq, D, dtype, fresh)
     fine = ~np.isnan(rm)
     # a weight is off by 2·dt and 2^-19 (ex2, the stored logsumexp), sums of rows fp32; ex2
-    # gives 0 below 2^-126
+    # gives 0 below 2^-126, for at most 64 rows of a key here
     dt = (D + 16) * 2.0 ** -23 * aq.max() + 2.0 ** -21 * np.abs(rl[np.isfinite(rl)]).max(initial=0.0)
     assert (np.abs(m[fine] - rm[fine]) <= (2 * dt + 2.0 ** -19) * rm[fine] + 2.0 ** -23 * rm[fine] + 2.0 ** -120).all()
 
