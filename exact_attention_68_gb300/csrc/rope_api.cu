@@ -1,0 +1,305 @@
+// rope_api.cu — the C ABI declared in include/attn_rope.h: argument checks,
+// the angles' fixed-point fractions, launch.
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include <cuda_runtime.h>
+
+#include "attn_host.h"
+#include "attn_rope.h"
+#include "rope_impl.h"
+
+static_assert(ea::kRopeMaxParts == ATTN_ROPE_MAX_PARTS, "parts of a call");
+
+namespace {
+
+using ea::overlaps;
+
+constexpr size_t kNoSpace = 16;  // the size that says no workspace is needed
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// A tensor [B, S, heads, D] by its strides, in bytes from its first value to behind its last.
+struct View {
+  const void* p;
+  int64_t b, s, h;
+};
+
+// Strides a view may have: sizes and products stay below 2^62.
+bool strides_ok(int64_t b, int64_t s, int64_t h) {
+  constexpr int64_t most = int64_t(1) << 30;
+  return b >= 0 && s >= 0 && h >= 0 && h <= most && s <= most * 4 && b <= (int64_t(1) << 40) && b % 8 == 0 &&
+         s % 8 == 0 && h % 8 == 0;
+}
+uint64_t extent(const View& v, int64_t B, int64_t S, int64_t H, int64_t D) {
+  return static_cast<uint64_t>((B - 1) * v.b + (S - 1) * v.s + (H - 1) * v.h + D) * 2;
+}
+
+// Whether no two of a view's values share a place: each stride, from the
+// smallest on, goes past all that the smaller ones reach.
+bool separate(const View& v, int64_t B, int64_t S, int64_t H, int64_t D) {
+  int64_t stride[3] = {v.b, v.s, v.h}, size[3] = {B, S, H};
+  int64_t reach = D;
+  for (int done = 0; done < 3; ++done) {
+    int at = -1;
+    for (int i = 0; i < 3; ++i)
+      if (size[i] > 1 && (at < 0 || stride[i] < stride[at])) at = i;
+    if (at < 0) return true;
+    if (stride[at] < reach) return false;
+    reach += stride[at] * (size[at] - 1);
+    size[at] = 1;
+  }
+  return true;
+}
+
+// Whether two views of the same strides for batch and token, as parts of a packed
+// tensor have, lie beside one another in every token.
+bool beside(const View& a, int64_t ha, const View& b, int64_t hb, int64_t B, int64_t S, int64_t D) {
+  if (a.b != b.b || a.s != b.s) return false;
+  const char *pa = static_cast<const char*>(a.p), *pb = static_cast<const char*>(b.p);
+  if (pb < pa) return beside(b, hb, a, ha, B, S, D);
+  const int64_t gap = (pb - pa) / 2;
+  const int64_t wa = (ha - 1) * a.h + D, wb = (hb - 1) * b.h + D;
+  if (gap < wa) return false;
+  if (S > 1 && gap + wb > a.s) return false;
+  return B == 1 || gap + wb + (S - 1) * a.s <= a.b || (S == 1 && gap + wb <= a.b);
+}
+
+attn_status_t check_sizes(const attn_rope_part_t* parts, int n, int64_t B, int64_t S, int64_t D) {
+  if (!parts || n < 1 || n > ATTN_ROPE_MAX_PARTS) return ATTN_ERR_INVALID_ARG;
+  if (B < 1 || S < 1 || D < 1) return ATTN_ERR_INVALID_ARG;
+  if (D > 256 || D % 8 != 0) return ATTN_ERR_UNSUPPORTED;
+  constexpr int64_t tokens = (int64_t(1) << 30) - 1;
+  if (B > tokens || S > tokens / B) return ATTN_ERR_INVALID_ARG;
+  for (int i = 0; i < n; ++i)
+    if (parts[i].heads < 1 || parts[i].heads > 65535 || parts[i].heads > INT32_MAX / (B * S)) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+attn_status_t check(const attn_rope_part_t* parts, int n, const attn_rope_t* rope,
+                    const attn_rope_positions_t* at, int64_t B, int64_t S, int64_t D, float eps, int dtype,
+                    bool bwd) {
+  attn_status_t s = check_sizes(parts, n, B, S, D);
+  if (s != ATTN_OK) return s;
+  if (dtype != ATTN_BF16 && dtype != ATTN_F16) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(eps) || eps < 0.f) return ATTN_ERR_INVALID_ARG;
+  bool turn = false;
+  for (int i = 0; i < n; ++i) {
+    const attn_rope_part_t& q = parts[i];
+    const bool reads_x = !bwd || q.weight;
+    if ((reads_x && !q.x) || !q.y || (bwd && !q.dx)) return ATTN_ERR_INVALID_ARG;
+    if ((q.turn != 0 && q.turn != 1) || (q.weight_f32 != 0 && q.weight_f32 != 1)) return ATTN_ERR_INVALID_ARG;
+    if (bwd && q.dweight && !q.weight) return ATTN_ERR_INVALID_ARG;
+    if (reads_x && !strides_ok(q.stride_b, q.stride_s, q.stride_h)) return ATTN_ERR_INVALID_ARG;
+    if (bwd && (!strides_ok(q.dx_stride_b, q.dx_stride_s, q.dx_stride_h) ||
+                !separate({q.dx, q.dx_stride_b, q.dx_stride_s, q.dx_stride_h}, B, S, q.heads, D)))
+      return ATTN_ERR_INVALID_ARG;
+    if ((reads_x && !aligned(q.x, 16)) || !aligned(q.y, 16) || (bwd && !aligned(q.dx, 16)) ||
+        !aligned(q.weight, 4) || (bwd && !aligned(q.dweight, 4)))
+      return ATTN_ERR_MISALIGNED;
+    turn = turn || q.turn;
+  }
+  if (turn) {
+    if (!rope || !at || !at->at || (rope->pairs > 0 && !rope->inv_freq)) return ATTN_ERR_INVALID_ARG;
+    if (rope->pairs < 0 || rope->pairs > D / 2) return ATTN_ERR_INVALID_ARG;
+    if (rope->interleaved != 0 && rope->interleaved != 1) return ATTN_ERR_INVALID_ARG;
+    if (at->axes < 1 || at->axes > ATTN_ROPE_MAX_AXES) return ATTN_ERR_INVALID_ARG;
+    constexpr int64_t most = int64_t(1) << 40;
+    if (at->stride_b < 0 || at->stride_s < 0 || at->stride_a < 0 || at->stride_b > most || at->stride_s > most ||
+        at->stride_a > most / 8 || (B - 1) > most / (at->stride_b + 1) || (S - 1) > most / (at->stride_s + 1))
+      return ATTN_ERR_INVALID_ARG;
+    if (!aligned(at->at, 4)) return ATTN_ERR_MISALIGNED;
+    for (int64_t i = 0; i < rope->pairs; ++i) {
+      if (!std::isfinite(rope->inv_freq[i]) || std::fabs(rope->inv_freq[i]) > 1048576.0) return ATTN_ERR_INVALID_ARG;
+      if (rope->axis && rope->axis[i] >= at->axes) return ATTN_ERR_INVALID_ARG;
+    }
+  }
+  // a tensor that is written overlaps nothing that is read, nor another one
+  const uint64_t pos_bytes = turn ? static_cast<uint64_t>((B - 1) * at->stride_b + (S - 1) * at->stride_s +
+                                                          (at->axes - 1) * at->stride_a + 1) * 4
+                                  : 0;
+  for (int i = 0; i < n; ++i) {
+    const attn_rope_part_t& q = parts[i];
+    const uint64_t yn = static_cast<uint64_t>(B * q.heads * S * D) * 2;
+    const View dx = {q.dx, q.dx_stride_b, q.dx_stride_s, q.dx_stride_h};
+    const void* w = bwd ? q.dx : q.y;
+    const uint64_t wn = bwd ? extent(dx, B, S, q.heads, D) : yn;
+    const uint64_t gn = bwd && q.dweight ? static_cast<uint64_t>(D) * (q.weight_f32 ? 4 : 2) : 0;
+    auto hit = [&](const void* p, uint64_t bytes) {
+      return p && bytes && (overlaps(w, wn, p, bytes) || (gn && overlaps(q.dweight, gn, p, bytes)));
+    };
+    if (turn && hit(at->at, pos_bytes)) return ATTN_ERR_INVALID_ARG;
+    if (gn && overlaps(q.dweight, gn, w, wn)) return ATTN_ERR_INVALID_ARG;
+    for (int j = 0; j < n; ++j) {
+      const attn_rope_part_t& r = parts[j];
+      if (!bwd || r.weight) {
+        const View x = {r.x, r.stride_b, r.stride_s, r.stride_h};
+        if (hit(r.x, extent(x, B, S, r.heads, D))) return ATTN_ERR_INVALID_ARG;
+      }
+      if (hit(r.weight, static_cast<uint64_t>(D) * (r.weight_f32 ? 4 : 2))) return ATTN_ERR_INVALID_ARG;
+      const uint64_t rn = static_cast<uint64_t>(B * r.heads * S * D) * 2;
+      if (bwd ? hit(r.y, rn) : (j != i && hit(r.y, rn))) return ATTN_ERR_INVALID_ARG;
+      if (!bwd || j <= i) continue;
+      const View other = {r.dx, r.dx_stride_b, r.dx_stride_s, r.dx_stride_h};
+      const uint64_t on = extent(other, B, S, r.heads, D);
+      if (overlaps(w, wn, r.dx, on) && !beside(dx, q.heads, other, r.heads, B, S, D)) return ATTN_ERR_INVALID_ARG;
+      if (r.dweight) {
+        const uint64_t dn = static_cast<uint64_t>(D) * (r.weight_f32 ? 4 : 2);
+        if (hit(r.dweight, dn)) return ATTN_ERR_INVALID_ARG;
+      }
+      if (gn && overlaps(q.dweight, gn, r.dx, on)) return ATTN_ERR_INVALID_ARG;
+    }
+  }
+  return ATTN_OK;
+}
+
+// f radians as a fraction of a turn in units of 2^-64, modulo one turn.  f / 2π
+// in two doubles: the product with the rounded 1/2π, and what that and the
+// product's rounding left out.
+uint64_t turn_fraction(double f) {
+  constexpr double inv = 0x1.45f306dc9c883p-3, inv_low = -0x1.6b01ec5417056p-57;  // 1/2π and the rest
+  const double hi = f * inv;
+  const double lo = std::fma(f, inv, -hi) + f * inv_low;
+  const double part = hi - std::rint(hi);  // exact
+  const int64_t a = std::llrint(part * 0x1p62), b = std::llrint(lo * 0x1p64);
+  return (static_cast<uint64_t>(a) << 2) + static_cast<uint64_t>(b);
+}
+
+int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return sms;
+}
+
+// How the tokens are cut into blocks.  Eight tokens a block let the angles serve
+// eight times the heads and a warp's stores run on; a call with few tokens takes
+// smaller blocks, and then several CTAs a block, until the SMs have one each.
+void plan(ea::RopeParams& p, int sms) {
+  const int64_t tokens = static_cast<int64_t>(p.B) * p.S;
+  p.log2_tokens = 3;
+  while (p.log2_tokens > 0 && ((tokens + (1 << p.log2_tokens) - 1) >> p.log2_tokens) < 2 * sms) --p.log2_tokens;
+  p.blocks = static_cast<int>((tokens + (1 << p.log2_tokens) - 1) >> p.log2_tokens);
+  int heads = 1;
+  for (int i = 0; i < p.n_parts; ++i)
+    if (p.part[i].heads > heads) heads = p.part[i].heads;
+  p.head_split = 1;
+  while (p.head_split < 8 && p.blocks * p.head_split * 2 <= sms && p.head_split * 16 < (heads << p.log2_tokens)) p.head_split *= 2;
+}
+
+attn_status_t run(const attn_rope_part_t* parts, int n, const attn_rope_t* rope,
+                  const attn_rope_positions_t* at, int64_t B, int64_t S, int64_t D, float eps, int dtype,
+                  void* workspace, size_t space, bool bwd, cudaStream_t stream) {
+  int* status = nullptr;
+  attn_status_t st = ea::current_status_words(&status);
+  if (st != ATTN_OK) return st;
+  const int sms = sm_count();
+  ea::RopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.n_parts = n;
+  p.B = static_cast<int>(B), p.S = static_cast<int>(S), p.D = static_cast<int>(D);
+  p.eps = eps, p.inv_d = 1.f / static_cast<float>(D);
+  p.status = status;
+  bool turn = false;
+  for (int i = 0; i < n; ++i) {
+    const attn_rope_part_t& q = parts[i];
+    ea::RopePart& r = p.part[i];
+    r.x = static_cast<const uint16_t*>(q.x);
+    r.xb = q.stride_b, r.xs = q.stride_s, r.xh = q.stride_h;
+    r.y = static_cast<uint16_t*>(q.y);
+    r.weight = q.weight;
+    r.weight_f32 = q.weight_f32;
+    r.heads = static_cast<int>(q.heads);
+    r.turn = q.turn && rope->pairs > 0;
+    if (bwd) {
+      r.dx = static_cast<uint16_t*>(q.dx);
+      r.db = q.dx_stride_b, r.ds = q.dx_stride_s, r.dh = q.dx_stride_h;
+      r.dweight = q.dweight;
+    }
+    turn = turn || r.turn;
+  }
+  ea::RopeShape shape = {false, 8};
+  if (turn) {
+    p.pairs = static_cast<int>(rope->pairs);
+    p.at = at->at;
+    p.pb = at->stride_b, p.ps = at->stride_s, p.pa = at->stride_a;
+    for (int i = 0; i < p.pairs; ++i) {
+      p.turns[i] = turn_fraction(rope->inv_freq[i]);
+      p.axis[i] = rope->axis ? rope->axis[i] : 0;
+    }
+    shape.interleaved = rope->interleaved != 0;
+  }
+  // pairs half a row apart: vectors that divide the turned half and the rest's
+  const int half = static_cast<int>(D) / 2;
+  shape.width = shape.interleaved ? 4 : gcd(gcd(8, p.pairs), half - p.pairs);
+  // a part that is not turned beside one that is has its pairs half of D apart
+  for (int i = 0; i < n && !shape.interleaved; ++i)
+    if (!p.part[i].turn && p.part[i].weight) shape.width = gcd(shape.width, half);
+  plan(p, sms);
+  cudaError_t e;
+  if (bwd) {
+    const int ctas = ea::rope_bwd_grid(p, sms);
+    size_t need = 0;
+    for (int i = 0; i < n; ++i)
+      if (p.part[i].dweight) {
+        p.part[i].sums = static_cast<float*>(workspace) + need / 4;
+        need += static_cast<size_t>(ctas) * D * 4;
+      }
+    if (need && (!workspace || space < need)) return ATTN_ERR_INVALID_ARG;
+    if (need && !aligned(workspace, 16)) return ATTN_ERR_MISALIGNED;
+    e = ea::rope_bwd_launch(p, shape, dtype == ATTN_F16, sms, stream);
+  } else {
+    e = ea::rope_fwd_launch(p, shape, dtype == ATTN_F16, stream);
+  }
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return ea::cuda_failure(static_cast<int>(e));
+  }
+  return ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+attn_status_t attn_rope_fwd(const attn_rope_part_t* parts, int n, const attn_rope_t* rope,
+                            const attn_rope_positions_t* positions, int64_t B, int64_t S, int64_t D,
+                            float eps, attn_dtype_t dtype, cudaStream_t stream) {
+  const attn_status_t s = check(parts, n, rope, positions, B, S, D, eps, dtype, false);
+  if (s != ATTN_OK) return s;
+  return run(parts, n, rope, positions, B, S, D, eps, dtype, nullptr, 0, false, stream);
+}
+
+size_t attn_rope_bwd_workspace(const attn_rope_part_t* parts, int n, int64_t B, int64_t S, int64_t D) {
+  if (check_sizes(parts, n, B, S, D) != ATTN_OK) return 0;
+  bool any = false;
+  for (int i = 0; i < n; ++i) any = any || parts[i].dweight;
+  if (!any) return kNoSpace;
+  const int sms = sm_count();
+  if (sms == 0) return 0;
+  ea::RopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.n_parts = n;
+  p.B = static_cast<int>(B), p.S = static_cast<int>(S), p.D = static_cast<int>(D);
+  for (int i = 0; i < n; ++i) p.part[i].heads = static_cast<int>(parts[i].heads);
+  plan(p, sms);
+  size_t bytes = 0;
+  for (int i = 0; i < n; ++i)
+    if (parts[i].dweight) bytes += static_cast<size_t>(ea::rope_bwd_grid(p, sms)) * D * 4;
+  return bytes < kNoSpace ? kNoSpace : bytes;
+}
+
+attn_status_t attn_rope_bwd(const attn_rope_part_t* parts, int n, const attn_rope_t* rope,
+                            const attn_rope_positions_t* positions, int64_t B, int64_t S, int64_t D,
+                            float eps, attn_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream) {
+  const attn_status_t s = check(parts, n, rope, positions, B, S, D, eps, dtype, true);
+  if (s != ATTN_OK) return s;
+  return run(parts, n, rope, positions, B, S, D, eps, dtype, workspace, workspace_bytes, true, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,188 @@
+"""CPU checks of the heads' norm and rotation: the oracle against differences and
+hand-worked values, the plan, and the library's refusals (no CUDA call is reached)."""
+import ctypes
+import os
+import re
+
+import numpy as np
+import pytest
+import torch
+
+from exact_attention_68_gb300 import binding, rope
+from exact_attention_68_gb300.build import build_library
+from oracle import rope as oracle
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return rope.declare(binding.load_library(build_library()))
+
+
+def test_header_declares_the_bound_symbols(lib):
+    with open(os.path.join(ROOT, "include", "attn_rope.h")) as f:
+        names = re.findall(r"ATTN_API\s+[\w\s\*]+?\b(attn_\w+)\s*\(", f.read())
+    assert sorted(names) == sorted(rope.ROPE_SYMBOLS)
+    for n in names:
+        assert hasattr(lib, n)
+
+
+def test_oracle_hand_worked():
+    x = np.array([[[[3.0, 4.0, 0.0, 0.0]]]])
+    # mean of squares 25/4; one pair, channels 0 and 1: a quarter turn takes (a, c) to (-c, a)
+    y = oracle.rope_fwd(x, [1, 1, 1, 1], np.array([[[1]]]), [np.pi / 2], interleaved=False, eps=0.0)
+    np.testing.assert_allclose(y[0, 0, 0], [-1.6, 1.2, 0, 0], atol=1e-15)
+    y = oracle.rope_fwd(x, None, np.array([[[2]]]), [np.pi / 2], interleaved=True)
+    np.testing.assert_allclose(y[0, 0, 0], [-3, -4, 0, 0], atol=1e-15)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_oracle_gradient_against_differences(interleaved, weighted):
+    rng = np.random.default_rng(3)
+    B, S, H, D, n = 1, 2, 2, 8, 3
+    x, w = rng.standard_normal((B, S, H, D)), rng.standard_normal(D)
+    pos, freq, axis = rng.integers(-9, 9, (B, S, 2)), rng.random(n), [0, 1, 1]
+    dy = rng.standard_normal((B, H, S, D))
+    kw = dict(positions=pos, inv_freq=freq, axis=axis, interleaved=interleaved, eps=1e-3)
+    f = lambda xx, ww: float((oracle.rope_fwd(xx, ww if weighted else None, **kw) * dy).sum())  # noqa: E731
+    dx, dw = oracle.rope_bwd(dy, x, w if weighted else None, **kw)[:2]
+    h = 1e-6
+    for i in np.ndindex(x.shape):
+        e = np.zeros_like(x)
+        e[i] = h
+        assert abs((f(x + e, w) - f(x - e, w)) / (2 * h) - dx[i]) < 1e-7
+    if weighted:
+        for d in range(D):
+            e = np.zeros(D)
+            e[d] = h
+            assert abs((f(x, w + e) - f(x, w - e)) / (2 * h) - dw[d]) < 1e-7
+
+
+def test_plan():
+    p = rope.rope_plan((4, 8), base=100.0)
+    assert p.inv_freq.tolist() == pytest.approx([1.0, 0.1, 1.0, 100 ** -0.25, 0.1, 100 ** -0.75])
+    assert p.axis.tolist() == [0, 0, 1, 1, 1, 1] and not p.interleaved
+    assert rope.rope_plan(8).inv_freq.numel() == 4
+    for bad in ((3,), (), (-2,), (2,) * 9):
+        with pytest.raises(ValueError):
+            rope.rope_plan(bad)
+
+
+# Fake, never dereferenced device addresses: validation runs before any CUDA call.
+A, T = 0x7F0000000000, 1 << 30
+
+
+def _args(n=1, B=2, S=16, D=64, H=4, bwd=False, **over):
+    parts = (rope._Part * max(n, 1))()
+    for i in range(n):
+        parts[i] = rope._Part(A + i * T, S * H * D, H * D, D, H, A + 8 * T + i * 1024, 0, 1, A + (10 + i) * T,
+                              A + (20 + i) * T, S * H * D, H * D, D, A + 9 * T + i * 1024)
+    for name, value in over.items():
+        setattr(parts[0], name, value)
+    return parts
+
+
+FREQ = (ctypes.c_double * 32)(*[0.5] * 32)
+AXIS = (ctypes.c_uint8 * 32)(*[0] * 32)
+
+
+def _rope_struct(freq=FREQ, axis=AXIS, pairs=32, interleaved=0):
+    return rope._Rope(ctypes.cast(freq, ctypes.c_void_p) if freq else None,
+                      ctypes.cast(axis, ctypes.c_void_p) if axis else None, pairs, interleaved)
+
+
+def _at(at=A + 30 * T, b=16, s=1, a=0, axes=1):
+    return rope._Positions(at, b, s, a, axes)
+
+
+def _call(lib, bwd, parts, n=1, r=None, at=None, B=2, S=16, D=64, eps=1e-6, dtype=0, ws=A + 31 * T, space=1 << 28):
+    r, at = _rope_struct() if r is None else r, _at() if at is None else at
+    if bwd:
+        return lib.attn_rope_bwd(parts, n, r, at, B, S, D, eps, dtype, ws, space, None)
+    return lib.attn_rope_fwd(parts, n, r, at, B, S, D, eps, dtype, None)
+
+
+BAD, UNSUP, MIS = binding.ATTN_ERR_INVALID_ARG, binding.ATTN_ERR_UNSUPPORTED, binding.ATTN_ERR_MISALIGNED
+
+
+@pytest.mark.parametrize("bwd", [False, True])
+@pytest.mark.parametrize("over,code", [
+    (dict(x=0), BAD), (dict(y=0), BAD), (dict(heads=0), BAD), (dict(heads=1 << 27), BAD), (dict(turn=2), BAD),
+    (dict(weight_f32=-1), BAD), (dict(stride_s=-256), BAD), (dict(stride_h=12), BAD), (dict(stride_b=1 << 41), BAD),
+    (dict(x=A + 8), MIS), (dict(y=A + 10 * T + 4), MIS), (dict(weight=A + 8 * T + 2), MIS),
+])
+def test_refused_parts(lib, bwd, over, code):
+    assert _call(lib, bwd, _args(**over)) == code
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(dx=0), BAD), (dict(dx=A + 20 * T + 8), MIS), (dict(dweight=A + 9 * T + 1), MIS),
+    (dict(dx_stride_h=0), BAD),                 # heads share a place
+    (dict(dx_stride_s=128), BAD),               # tokens overlap
+    (dict(weight=None), BAD),                   # dweight without weight
+    (dict(dx=A), BAD),                          # dx is x
+    (dict(dx=A + 10 * T), BAD),                 # dx is dy
+    (dict(dweight=A + 64), BAD),                # dweight in x
+    (dict(dweight=A + 8 * T), BAD),             # dweight is weight
+])
+def test_refused_gradients(lib, over, code):
+    assert _call(lib, True, _args(**over)) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n=0), BAD), (dict(n=5), BAD), (dict(B=0), BAD), (dict(S=0), BAD), (dict(B=1 << 20, S=1 << 20), BAD),
+    (dict(D=60), UNSUP), (dict(D=264), UNSUP), (dict(D=0), BAD), (dict(eps=-1.0), BAD), (dict(eps=float("nan")), BAD),
+    (dict(dtype=2), BAD),
+    (dict(r=_rope_struct(pairs=33)), BAD), (dict(r=_rope_struct(pairs=-1)), BAD), (dict(r=_rope_struct(freq=None)), BAD),
+    (dict(r=_rope_struct(interleaved=2)), BAD),
+    (dict(r=_rope_struct(freq=(ctypes.c_double * 32)(*[float("inf")] * 32))), BAD),
+    (dict(r=_rope_struct(freq=(ctypes.c_double * 32)(*[2e6] * 32))), BAD),
+    (dict(r=_rope_struct(axis=(ctypes.c_uint8 * 32)(*[1] * 32))), BAD),
+    (dict(at=_at(at=0)), BAD), (dict(at=_at(at=A + 2)), MIS), (dict(at=_at(axes=0)), BAD), (dict(at=_at(axes=9)), BAD),
+    (dict(at=_at(b=-1)), BAD), (dict(at=_at(s=1 << 41)), BAD),
+])
+def test_refused_calls(lib, kw, code):
+    for bwd in (False, True):
+        assert _call(lib, bwd, _args(), **kw) == code
+
+
+def test_refused_overlaps(lib):
+    two = _args(2)
+    two[1].y = two[0].y + 4096
+    assert _call(lib, False, two, n=2) == BAD
+    two = _args(2)
+    two[1].x = two[0].y + 64
+    assert _call(lib, False, two, n=2) == BAD
+    one = _args(1)
+    assert _call(lib, False, one, at=_at(at=one[0].y + 128)) == BAD
+    # gradients of a packed projection lie beside one another; shifted by less than a head they do not
+    B, S, H, D = 2, 16, 4, 64
+    for shift, code in ((H * D, None), (H * D - 8, BAD), (3 * H * D, BAD)):
+        two = _args(2, bwd=True)
+        for i in range(2):
+            two[i].dx_stride_b, two[i].dx_stride_s = S * 2 * H * D, 2 * H * D
+            two[i].dx = A + 20 * T + i * shift * 2
+        # a sound layout goes on to the first CUDA call, which fails here
+        got = _call(lib, True, two, n=2)
+        assert (got == code) if code else (got not in (BAD, MIS))
+
+
+def test_workspace_sizes_without_weights(lib):
+    parts = _args(1)
+    parts[0].dweight = None
+    assert lib.attn_rope_bwd_workspace(parts, 1, 2, 16, 64) == 16
+    assert lib.attn_rope_bwd_workspace(parts, 0, 2, 16, 64) == 0
+    assert lib.attn_rope_bwd_workspace(parts, 1, 2, 16, 60) == 0
+
+
+def test_binding_refuses_bad_tensors():
+    x = torch.zeros(1, 4, 2, 8, dtype=torch.bfloat16)
+    plan = rope.rope_plan(8)
+    with pytest.raises(ValueError):
+        rope.rope_fwd((x,), plan, torch.zeros(1, 4, dtype=torch.int32))  # not on the GPU
+    with pytest.raises(TypeError):
+        rope.rope_fwd((x.float(),), plan, None)
+    with pytest.raises(ValueError):
+        rope.rope_fwd((), plan, None)
