@@ -41,12 +41,12 @@ def _sources():
     return [os.path.join(CSRC, f) for f in ("attn_api.cu", "attn_fwd_1q_sm103.cu", "attn_fwd_1qp_sm103.cu",
                                             "attn_noalloc.cu", "attn_bwd_api.cu", "attn_bwd_sm103.cu", "attn_bwd256_sm103.cu",
                                             "cache_api.cu", "cache_fwd_sm103.cu", "cache_pages_sm103.cu", "cache_select_sm103.cu",
-                                            "rope_api.cu", "rope_sm103.cu")]
+                                            "rope_api.cu", "rope_sm103.cu", "cross_api.cu", "cross_join_sm103.cu")]
 
 
 def _deps():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files += [os.path.join(ROOT, "include", f) for f in ("attn.h", "attn_cache.h", "attn_rope.h")]
+    files += [os.path.join(ROOT, "include", f) for f in ("attn.h", "attn_cache.h", "attn_rope.h", "attn_cross.h")]
     return files
 
 

@@ -192,8 +192,8 @@ attn_status_t launch_with_status(const void* q, const void* k, const void* v, vo
   p.sched = plan_schedule(BH, p.n_qt, S, D, causal != 0, kL2GroupBytes, sms);
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.timeout_ns = timeout_ns;
-  e = persistent ? fwd1qp_launch(p, dk, causal != 0, f16, stream)
-                 : fwd1q_launch(p, dk, causal != 0, f16, stream);
+  const int mask = causal != 0 ? kMaskCausal : kMaskFull;
+  e = persistent ? fwd1qp_launch(p, dk, mask, f16, stream) : fwd1q_launch(p, dk, mask, f16, stream);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return cuda_failure(static_cast<int>(e));

@@ -35,6 +35,8 @@ struct BwdParams {
   const uint16_t* out;   // 16-bit [B·H, S, d_cols]: forward output (rows read for delta)
   const uint16_t* dout;  // 16-bit [B·H, S, d_cols]
   const float* lse;      // [B·H, S]: natural-log logsumexp saved by the forward
+  uint16_t* dk;          // 16-bit [B·H, Sk, d_cols] (kMaskCross: rows without keys are zeroed)
+  uint16_t* dv;
   float* delta;          // [B·H, S]: rowsum(dout ⊙ out), written by the dq kernel
   int* status;           // device status word pair (error bits, first wait site)
   int BH, S;
@@ -47,15 +49,26 @@ struct BwdParams {
   float scale;           // softmax scale
   float scale_log2;      // scale · log2(e)
   uint64_t timeout_ns;
+  // kMaskCross only (attn_fwd.h).  Rows of a slice are the G·Sq queries of the heads
+  // that share its key head, S of them in n_qt tiles.
+  int Sk;               // keys of a slice: k, v, dk, dv are (D, Sk, BH)
+  const int* lens;      // [BH / heads] keys that are there; null: all Sk
+  int heads;            // key heads of one sequence
+  int n_qt, n_kt;       // ceil(S / 128), ceil(Sk / 128)
+  int q_split;          // runs of K/V tiles that a Q tile's dq is summed over
+  int kv_split;         // runs of Q tiles that a K/V tile's dk, dv are summed over
+  float* part_dq;       // [q_split, BH, S, d_cols] if q_split > 1: each run's sum, unscaled
+  float* part_dk;       // [kv_split, BH, Sk, d_cols] if kv_split > 1: the same of dk and dv
+  float* part_dv;
 };
 
 // Launches the dq kernel (which also writes delta) and then the dk/dv kernel
 // on `stream`.  f16: the 16-bit tensors are fp16 (else bf16).
-cudaError_t bwd_launch(const BwdParams& p, int D, bool causal, bool f16, cudaStream_t stream);
+cudaError_t bwd_launch(const BwdParams& p, int D, int mask, bool f16, cudaStream_t stream);
 
 // The same for head dimensions above 128 (kernels 256 columns wide): the dq
 // kernel, then the dk/dv kernel with one CTA per K/V tile and half of the
 // head dimension.
-cudaError_t bwd256_launch(const BwdParams& p, bool causal, bool f16, cudaStream_t stream);
+cudaError_t bwd256_launch(const BwdParams& p, int mask, bool f16, cudaStream_t stream);
 
 }  // namespace ea

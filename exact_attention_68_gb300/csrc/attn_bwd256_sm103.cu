@@ -43,6 +43,7 @@
 
 #include "attn_bwd.h"
 #include "bwd_common.cuh"
+#include "cross_common.cuh"
 #include "ptx.cuh"
 #include "umma.cuh"
 
@@ -100,9 +101,10 @@ struct Dq256Layout {
   static constexpr uint32_t kTmemCols = 512, kSCol = 0, kPCol = 64, kQCol = 128, kDqCol = 256;
 };
 
-template <bool CAUSAL, bool F16>
+template <int MASK, bool F16>
 __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dq256_kernel(const __grid_constant__ BwdParams p) {
   using L = Dq256Layout;
+  constexpr bool CAUSAL = MASK == kMaskCausal, CROSS = MASK == kMaskCross;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sb = (smem_u32(smem_raw) + 1023u) & ~1023u;
   auto bar = [sb](int idx) -> uint32_t { return sb + L::kBarOff + 8u * idx; };
@@ -112,12 +114,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dq256_kernel(const __
   const int lane = threadIdx.x & 31;
   const DbgBounds dbb{p.status, sb, smem_u32(smem_raw) + static_cast<uint32_t>(L::kAlloc), p.S,
                       p.d_cols, p.BH};
+  const DbgBounds dbk = key_bounds<MASK>(dbb, p.Sk);
   int bh, i;
-  schedule_unit(p.sched, static_cast<int>(blockIdx.x), &bh, &i);
+  BwdUnit un{};
+  if constexpr (CROSS) {
+    un = cross_dq_unit<kStepW>(p, static_cast<int>(blockIdx.x));
+    bh = un.bh, i = un.tile;
+  } else {
+    schedule_unit(p.sched, static_cast<int>(blockIdx.x), &bh, &i);
+  }
+  const int s0 = CROSS ? un.first : 0;
   // 64-key steps: up to the Q tile's last row under the mask, and never one
   // that starts past the last key
   const int n_k64 = (p.S + kStepW - 1) / kStepW;
-  const int nsteps = CAUSAL ? min(2 * (i + 1), n_k64) : n_k64;
+  const int nsteps = CROSS ? un.n : CAUSAL ? min(2 * (i + 1), n_k64) : n_k64;
 
   if (threadIdx.x == 0) {
     mbar_init(bar(L::kDoFull), 1);
@@ -187,7 +197,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dq256_kernel(const __
     const float delta = ld_shared_f32(sb + L::kPartOff + 4 * row) +
                         ld_shared_f32(sb + L::kPartOff + 4 * (kRowsW + row));
     const bool row_ok = valid && dbg_row(dbb, bh, grow, 0, 0, kChkWRowLoad);
-    if (g == 0 && row_ok) p.delta[(int64_t)bh * p.S + grow] = delta;
+    if (g == 0 && row_ok && (!CROSS || un.part == 0)) p.delta[(int64_t)bh * p.S + grow] = delta;
     const float lse2 = row_ok ? p.lse[(int64_t)bh * p.S + grow] * kLog2eW : 0.f;
     const float sl2 = p.scale_log2;
     const uint32_t tS = tmem_base + lane_bits + L::kSCol + 32 * g;
@@ -210,8 +220,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dq256_kernel(const __
       reg_fence(sv);
       reg_fence(dpv);
       // allowed key columns of this warpgroup's 32: 0 .. lim (causal: key <= query; key < S)
-      const int c0 = s * kStepW + 32 * g;
-      int lim = p.S - 1 - c0;
+      const int c0 = (s0 + s) * kStepW + 32 * g;
+      int lim = (CROSS ? un.len : p.S) - 1 - c0;
       if (CAUSAL) lim = min(lim, grow - c0);
       if (!valid) lim = -1;
       const bool edge = lim < 31;
@@ -224,8 +234,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dq256_kernel(const __
           if (2 * e2 > lim) p0 = 0.f;
           if (2 * e2 + 1 > lim) p1 = 0.f;
         }
-        pk[e2] = pack_x2<F16>(p0 * (__uint_as_float(dpv[2 * e2]) - delta),
-                              p1 * (__uint_as_float(dpv[2 * e2 + 1]) - delta));
+        float ds0 = p0 * (__uint_as_float(dpv[2 * e2]) - delta);
+        float ds1 = p1 * (__uint_as_float(dpv[2 * e2 + 1]) - delta);
+        if (CROSS && edge) {  // a key that is not there may make dP anything
+          if (2 * e2 > lim) ds0 = 0.f;
+          if (2 * e2 + 1 > lim) ds1 = 0.f;
+        }
+        pk[e2] = pack_x2<F16>(ds0, ds1);
       }
       tmem_st_32x32b_x16(tS, pk);
       tmem_st_wait();
@@ -236,7 +251,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dq256_kernel(const __
     // ---- epilogue: dQ · scale → 16-bit → swizzled staging (the K ring, idle
     // once every MMA has completed) → TMA store; warpgroup g stores blocks g, g+2
     if (ok) ok = __all_sync(0xffffffffu, wait_bounded(bar(L::kOFull), 0, ctl, kSiteW2ElemO));
-    if (ok) {
+    if (CROSS && ok && p.q_split > 1) {  // this run's sum, to be added to the others
+      tc_fence_after_sync();
+      const int64_t at = (((int64_t)un.part * p.BH + bh) * p.S + grow) * p.d_cols;
+#pragma unroll 1
+      for (int c = 4 * g; c < 4 * g + 4; ++c)
+        store_part(tmem_base + lane_bits + L::kDqCol + 32 * c, p.part_dq + at, 32 * c, 1.f, valid, dbb,
+                   bh, grow, kChkStore);
+    } else if (ok) {
       tc_fence_after_sync();
       for (int c = g; c < 4; c += 2)
         store_chunk<F16>(tmem_base + lane_bits + L::kDqCol + 64 * c, sb + L::kKOff + c * kBlk128, row,
@@ -273,8 +295,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dq256_kernel(const __
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const uint32_t dst = sb + L::kKOff + ks * kTile64 + c * kBlk64;
-          if (dbg_tma(dbb, dst, kBlk64, c * 64, s * kStepW, bh, false, kChkWLoadA))
-            tma_load_3d(dst, &p.tm_k64, bar(L::kKFull + ks), c * 64, s * kStepW, bh, pol);
+          if (dbg_tma(dbk, dst, kBlk64, c * 64, (s0 + s) * kStepW, bh, false, kChkWLoadA))
+            tma_load_3d(dst, &p.tm_k64, bar(L::kKFull + ks), c * 64, (s0 + s) * kStepW, bh, pol);
         }
         k_issued = s + 1;
         const int vs = s % L::kVStages;
@@ -285,8 +307,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dq256_kernel(const __
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const uint32_t dst = sb + L::kVOff + vs * kTile64 + c * kBlk64;
-          if (dbg_tma(dbb, dst, kBlk64, c * 64, s * kStepW, bh, false, kChkWLoadB))
-            tma_load_3d(dst, &p.tm_v64, bar(L::kVFull + vs), c * 64, s * kStepW, bh, pol);
+          if (dbg_tma(dbk, dst, kBlk64, c * 64, (s0 + s) * kStepW, bh, false, kChkWLoadB))
+            tma_load_3d(dst, &p.tm_v64, bar(L::kVFull + vs), c * 64, (s0 + s) * kStepW, bh, pol);
         }
         v_issued = s + 1;
       }
@@ -331,6 +353,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dq256_kernel(const __
       if (ok) ok = wait_warp(bar(L::kVFull + vs), (s / L::kVStages) & 1,
                              kSiteW2MmaKV | 0x80 | (s & 0x7f));
       if (!ok) break;
+      if (CROSS)  // dQ's product multiplies dS = 0 by the rows of K behind the end
+        clear_tail<4>(sb + L::kKOff + ks * kTile64, kStepW, un.len - (s0 + s) * kStepW, un.len < p.Sk,
+                      lane, dbb, kChkWMmaA);
       tc_fence_after_sync();
       if (dbg_smem(dbb, sb + L::kKOff + ks * kTile64, kTile64, 1024, kChkWMmaA) &&
           dbg_smem(dbb, sb + L::kVOff + vs * kTile64, kTile64, 1024, kChkWMmaB)) {
@@ -419,9 +444,10 @@ __device__ __forceinline__ void tmem_st_row(uint32_t taddr, const uint32_t (&w)[
   }
 }
 
-template <int D, bool CAUSAL, bool F16>
+template <int D, int MASK, bool F16>
 __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_q64_kernel(const __grid_constant__ BwdParams p) {
   using L = KvQ64Layout<D>;
+  constexpr bool CAUSAL = MASK == kMaskCausal, CROSS = MASK == kMaskCross;
   constexpr bool kSplit = L::kSplit;
   constexpr int kCols = L::kCols;
   constexpr int kTileQ = L::kTileQ;
@@ -437,12 +463,30 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_q64_kernel(const
                       p.d_cols, p.BH};
   // with the head dimension split, the two halves of one K/V tile are neighbouring CTAs
   const int half = kSplit ? static_cast<int>(blockIdx.x & 1u) : 0;
-  int bh, level;
-  schedule_unit(p.sched, static_cast<int>(kSplit ? blockIdx.x >> 1 : blockIdx.x), &bh, &level);
-  const int j = p.n_t - 1 - level;  // K/V tile
-  const int n_q64 = (p.S + kStepW - 1) / kStepW;
-  const int u0 = CAUSAL ? 2 * j : 0;  // first 64-query tile that sees this K/V tile
-  const int n_sub = n_q64 - u0;
+  const int unit = static_cast<int>(kSplit ? blockIdx.x >> 1 : blockIdx.x);
+  int bh, j;      // slice and K/V tile
+  int u0, n_sub;  // first 64-query tile that sees it, and how many
+  int keys;       // rows of the slice's keys that are there
+  BwdUnit un{};
+  if constexpr (CROSS) {
+    un = cross_kv_unit<kStepW>(p, unit);
+    bh = un.bh, j = un.tile, u0 = un.first, n_sub = un.n, keys = un.len;
+    if (j * kRowsW >= keys) {
+      if (un.part == 0)
+        cross_no_keys(p.dk, p.dv, (int64_t)bh * p.Sk + j * kRowsW, min(kRowsW, p.Sk - j * kRowsW),
+                      p.d_cols, kCols * half, kCols, kBwdThreads);
+      return;
+    }
+  } else {
+    int level;
+    schedule_unit(p.sched, unit, &bh, &level);
+    j = p.n_t - 1 - level;
+    const int n_q64 = (p.S + kStepW - 1) / kStepW;
+    u0 = CAUSAL ? 2 * j : 0;
+    n_sub = n_q64 - u0;
+    keys = p.S;
+  }
+  const DbgBounds dbk = key_bounds<MASK>(dbb, p.Sk);
 
   if (threadIdx.x == 0) {
     mbar_init(bar(L::kVFull), 1);
@@ -481,13 +525,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_q64_kernel(const
       // TMEM; rows past the end and columns past d_cols hold zero
       constexpr int kU = D / 16;  // 16-byte groups in half a row
       uint32_t kw[4 * kU], vw[4 * kU];
-      const bool in_row = gk < p.S;
-      const int64_t base = ((int64_t)bh * p.S + (in_row ? gk : 0)) * p.d_cols + g * (D / 2);
+      const bool in_row = gk < keys;
+      const int64_t base = ((int64_t)bh * (CROSS ? p.Sk : p.S) + (in_row ? gk : 0)) * p.d_cols + g * (D / 2);
       const int lim = p.d_cols - g * (D / 2);
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const bool in = in_row && 8 * u < lim &&
-                        dbg_row(dbb, bh, gk, g * (D / 2) + 8 * u, 8, kChkWRowLoad);
+                        dbg_row(dbk, bh, gk, g * (D / 2) + 8 * u, 8, kChkWRowLoad);
         const uint4 z = make_uint4(0u, 0u, 0u, 0u);
         const uint4 kv = in ? __ldg(reinterpret_cast<const uint4*>(p.k + base) + u) : z;
         kw[4 * u] = kv.x, kw[4 * u + 1] = kv.y, kw[4 * u + 2] = kv.z, kw[4 * u + 3] = kv.w;
@@ -531,7 +575,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_q64_kernel(const
       const int c0 = u * kStepW + 32 * g;
       const int hi = p.S - 1 - c0;
       int lo = CAUSAL ? gk - c0 : 0;
-      if (gk >= p.S) lo = 32;  // key row past the end: nothing
+      if (gk >= keys) lo = 32;  // key row past the end: nothing
       const bool edge = lo > 0 || hi < 31;
       // (lse·log2e, delta) of these 32 query columns, two columns per load
       const float4* stat = reinterpret_cast<const float4*>(smem_gen + L::kStatOff +
@@ -548,8 +592,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_q64_kernel(const
           if (c + 1 < lo || c + 1 > hi) p1 = 0.f;
         }
         ppk[e2] = pack_x2<F16>(p0, p1);
-        dpk[e2] = pack_x2<F16>(p0 * (__uint_as_float(dpv[c]) - sd.y),
-                               p1 * (__uint_as_float(dpv[c + 1]) - sd.w));
+        float ds0 = p0 * (__uint_as_float(dpv[c]) - sd.y);
+        float ds1 = p1 * (__uint_as_float(dpv[c + 1]) - sd.w);
+        if (CROSS && edge) {  // a key that is not there may make dP anything
+          if (c < lo || c > hi) ds0 = 0.f;
+          if (c + 1 < lo || c + 1 > hi) ds1 = 0.f;
+        }
+        dpk[e2] = pack_x2<F16>(ds0, ds1);
       }
       tmem_st_32x32b_x16(tS, ppk);
       tmem_st_32x32b_x16(tP, dpk);
@@ -567,13 +616,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_q64_kernel(const
       const uint32_t stage = sb + L::kQOff + g * (kCols / 64) * kBlk128;
       const CUtensorMap* map = g == 0 ? &p.tm_dv : &p.tm_dk;
       const float mul = g == 0 ? 1.f : p.scale;
+      if (CROSS && p.kv_split > 1) {  // this run's sum, to be added to the others
+        float* to = (g == 0 ? p.part_dv : p.part_dk) +
+                    (((int64_t)un.part * p.BH + bh) * p.Sk + gk) * p.d_cols;
+#pragma unroll 1
+        for (int cc = 0; cc < kCols / 32; ++cc)
+          store_part(tAcc + 32 * cc, to, kCols * half + 32 * cc, 1.f, gk < keys, dbk, bh, gk, kChkStore);
+      } else {
 #pragma unroll
-      for (int cc = 0; cc < kCols / 64; ++cc)
-        store_chunk<F16>(tAcc + 64 * cc, stage + cc * kBlk128, r, mul, map, kCols * half + 64 * cc,
-                         j * kRowsW, bh, wq, lane, dbb);
-      if (lane == 0) {
-        tma_store_commit();
-        tma_store_wait_all();
+        for (int cc = 0; cc < kCols / 64; ++cc)
+          store_chunk<F16>(tAcc + 64 * cc, stage + cc * kBlk128, r, mul, map, kCols * half + 64 * cc,
+                           j * kRowsW, bh, wq, lane, dbk, CROSS && gk >= keys);
+        if (lane == 0) {
+          tma_store_commit();
+          tma_store_wait_all();
+        }
       }
     }
     tc_fence_before_sync();
@@ -591,7 +648,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_q64_kernel(const
 #pragma unroll
         for (int c = 0; c < L::kChunks; ++c) {
           const uint32_t dst = sb + L::kVOff + c * kBlk128;
-          if (dbg_tma(dbb, dst, kBlk128, c * 64, j * kRowsW, bh, false, kChkWLoadB))
+          if (dbg_tma(dbk, dst, kBlk128, c * 64, j * kRowsW, bh, false, kChkWLoadB))
             tma_load_3d(dst, &p.tm_v, bar(L::kVFull), c * 64, j * kRowsW, bh, pol);
         }
       }
@@ -724,42 +781,53 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_q64_kernel(const
   }
 }
 
-template <int D, bool CAUSAL, bool F16>
+template <int D, int MASK, bool F16>
 cudaError_t dkdv_q64_launch(const BwdParams& p, cudaStream_t stream) {
   using L = KvQ64Layout<D>;
-  auto kkv = attn_bwd_dkdv_q64_kernel<D, CAUSAL, F16>;
+  auto kkv = attn_bwd_dkdv_q64_kernel<D, MASK, F16>;
   cudaError_t e = cudaFuncSetAttribute(kkv, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
   if (e != cudaSuccess) return e;
+  const long long units = MASK == kMaskCross ? (long long)p.n_kt * p.kv_split : p.n_t;
   cudaLaunchConfig_t cfg = {};
   // with the head dimension split, two CTAs (column halves) per K/V tile
-  cfg.gridDim = dim3(static_cast<unsigned>((L::kSplit ? 2ll : 1ll) * p.BH * p.n_t), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>((L::kSplit ? 2ll : 1ll) * p.BH * units), 1, 1);
   cfg.blockDim = dim3(kBwdThreads, 1, 1);
   cfg.stream = stream;
   cfg.dynamicSmemBytes = L::kAlloc;
   return cudaLaunchKernelEx(&cfg, kkv, p);
 }
 
-template <bool CAUSAL, bool F16>
+template <int MASK, bool F16>
 cudaError_t launch_256(const BwdParams& p, cudaStream_t stream) {
-  auto kdq = attn_bwd_dq256_kernel<CAUSAL, F16>;
+  auto kdq = attn_bwd_dq256_kernel<MASK, F16>;
   cudaError_t e = cudaFuncSetAttribute(kdq, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        Dq256Layout::kAlloc);
   if (e != cudaSuccess) return e;
+  const long long units = MASK == kMaskCross ? (long long)p.n_qt * p.q_split : p.n_t;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((long long)p.BH * p.n_t), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.BH * units), 1, 1);
   cfg.blockDim = dim3(kBwdThreads, 1, 1);
   cfg.stream = stream;
   cfg.dynamicSmemBytes = Dq256Layout::kAlloc;
   e = cudaLaunchKernelEx(&cfg, kdq, p);
   if (e != cudaSuccess) return e;
-  return dkdv_q64_launch<256, CAUSAL, F16>(p, stream);
+  return dkdv_q64_launch<256, MASK, F16>(p, stream);
+}
+
+template <bool F16>
+cudaError_t launch_masked(const BwdParams& p, int mask, cudaStream_t stream) {
+  switch (mask) {
+    case kMaskFull: return launch_256<kMaskFull, F16>(p, stream);
+    case kMaskCausal: return launch_256<kMaskCausal, F16>(p, stream);
+    case kMaskCross: return launch_256<kMaskCross, F16>(p, stream);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-cudaError_t bwd256_launch(const BwdParams& p, bool causal, bool f16, cudaStream_t stream) {
-  if (f16) return causal ? launch_256<true, true>(p, stream) : launch_256<false, true>(p, stream);
-  return causal ? launch_256<true, false>(p, stream) : launch_256<false, false>(p, stream);
+cudaError_t bwd256_launch(const BwdParams& p, int mask, bool f16, cudaStream_t stream) {
+  return f16 ? launch_masked<true>(p, mask, stream) : launch_masked<false>(p, mask, stream);
 }
 
 }  // namespace ea

@@ -8,6 +8,7 @@
 
 #include "attn.h"
 #include "attn_bwd.h"
+#include "attn_fwd.h"
 #include "attn_host.h"
 #include "tmap.h"
 
@@ -103,8 +104,9 @@ attn_status_t attn_bwd_ex(const void* q, const void* k, const void* v, const voi
   p.timeout_ns = wait_timeout_ns;
   // kernels of 64, 128 or 256 columns; the tensor maps carry the real column
   // count (zeros read past it, those columns never stored)
-  const cudaError_t e = width == 256 ? ea::bwd256_launch(p, causal != 0, f16, stream)
-                                     : ea::bwd_launch(p, width, causal != 0, f16, stream);
+  const int mask = causal != 0 ? ea::kMaskCausal : ea::kMaskFull;
+  const cudaError_t e = width == 256 ? ea::bwd256_launch(p, mask, f16, stream)
+                                     : ea::bwd_launch(p, width, mask, f16, stream);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return ea::cuda_failure(static_cast<int>(e));

@@ -28,6 +28,13 @@ constexpr int kBlockM = 128;
 template <bool F16>
 constexpr float kRescaleThreshold = F16 ? 8.0f : 32.0f;
 
+// Which keys a query meets.
+enum : int {
+  kMaskFull = 0,    // all S
+  kMaskCausal = 1,  // those up to its own row
+  kMaskCross = 2    // the first lens[b] of another sequence's Sk
+};
+
 // Parameters of the forward kernels: one 128-row Q tile at a time, Q in TMEM,
 // BN-row K/V tiles (BN = 64 at D = 256, else 128).
 struct Fwd1QParams {
@@ -46,15 +53,23 @@ struct Fwd1QParams {
   UnitSchedule sched;  // CTA index -> (b·H + h, Q tile): a unit is one Q tile here
   float scale_log2;
   uint64_t timeout_ns;
+  // kMaskCross only.  Rows of a slice are the G·Sq queries of the heads that share
+  // its key head; a unit is one Q tile and one of n_split runs of its K/V tiles.
+  int Sk;              // keys of a slice, k and v being (D, Sk, BH)
+  const int* lens;     // [BH / heads] keys that are there; null: all Sk
+  int heads;           // key heads of one sequence
+  int n_split;
+  float* part_o;       // [n_split, BH, S, d_cols] if n_split > 1: each run's own result
+  float* part_lse;     // [n_split, BH, S]
 };
 
 // One Q tile per CTA, Q in TMEM: D = 256 (64-row K/V tiles) and D = 128
 // (128-row K/V tiles).  The library runs D = 256 on it.
-cudaError_t fwd1q_launch(const Fwd1QParams& p, int D, bool causal, bool f16, cudaStream_t stream);
+cudaError_t fwd1q_launch(const Fwd1QParams& p, int D, int mask, bool f16, cudaStream_t stream);
 
 // The same computation with one CTA per SM walking Q tiles (D = 64 or 128):
 // a running CTA takes over the Q tile of the next CTA of the grid that has not
 // been launched yet, so the next tile's start overlaps this tile's end.
-cudaError_t fwd1qp_launch(const Fwd1QParams& p, int D, bool causal, bool f16, cudaStream_t stream);
+cudaError_t fwd1qp_launch(const Fwd1QParams& p, int D, int mask, bool f16, cudaStream_t stream);
 
 }  // namespace ea

@@ -31,6 +31,7 @@
 #include <cuda_runtime.h>
 
 #include "attn_fwd.h"
+#include "cross_common.cuh"
 #include "ptx.cuh"
 #include "umma.cuh"
 
@@ -77,9 +78,10 @@ enum : int { kSiteProdK = 0x3100, kSiteProdV = 0x3200, kSiteMmaQ = 0x3300, kSite
 enum : int { kChkQLoad = 0x5101, kChkQTmem, kChkSTmem, kChkPTmem, kChkOTmem, kChkStage, kChkStore,
              kChkLse, kChkLoadK, kChkLoadV, kChkMmaK, kChkMmaV, kChkMmaTmem };
 
-template <int D, int BN, bool CAUSAL, bool F16>
+template <int D, int BN, int MASK, bool F16>
 __global__ void __launch_bounds__(kThreads1Q, 1) attn_fwd_1q_kernel(const __grid_constant__ Fwd1QParams p) {
   using L = Layout1Q<D, BN>;
+  constexpr bool CAUSAL = MASK == kMaskCausal, CROSS = MASK == kMaskCross;
   constexpr int kKvRows = BN;
   constexpr int kChunkBytes = L::kChunkBytes;
   constexpr int kD = D;
@@ -102,10 +104,10 @@ __global__ void __launch_bounds__(kThreads1Q, 1) attn_fwd_1q_kernel(const __grid
 
   // Q tile i of slice bh, in the order of the grid schedule (schedule.h):
   // heavy tiles by L2-sized groups of heads, then the light ones over all heads
-  int bh, i;
-  schedule_unit(p.sched, static_cast<int>(blockIdx.x), &bh, &i);
-  int nkv = CAUSAL ? (i + 1) * (kQRows / BN) : p.n_kt;  // K/V tiles this Q tile meets
-  if (nkv > p.n_kt) nkv = p.n_kt;
+  const DbgBounds dbk = key_bounds<MASK>(dbb, p.Sk);
+  const FwdUnit un = fwd_unit<MASK, BN>(p, static_cast<int>(blockIdx.x));
+  const int bh = un.bh, i = un.i;
+  const int nkv = un.nkv;  // K/V tiles this Q tile meets
 
   // A softmax thread's row of Q, requested before the set-up below so that
   // the load's latency overlaps it: all of the row's 16-byte loads are in
@@ -197,7 +199,7 @@ __global__ void __launch_bounds__(kThreads1Q, 1) attn_fwd_1q_kernel(const __grid
 #pragma unroll
       for (int g = 0; g < BN / 32; ++g) reg_fence(s[g]);
       // allowed key columns of this tile: 0 .. lim (causal: key <= query; key < S)
-      int lim = p.S - 1 - j * kKvRows;
+      int lim = CROSS ? un.len - 1 - (un.j0 + j) * kKvRows : p.S - 1 - j * kKvRows;
       if (CAUSAL) lim = min(lim, grow - j * kKvRows);
       if (!valid) lim = -1;
       if (lim < BN - 1) {
@@ -283,7 +285,15 @@ __global__ void __launch_bounds__(kThreads1Q, 1) attn_fwd_1q_kernel(const __grid
 
     // ---- epilogue: O / lq → 16-bit → swizzled staging (K ring) → TMA store; lse
     if (ok) ok = __all_sync(0xffffffffu, wait_bounded(bar(kOFull), 0, ctl, kSiteSoftO));
-    if (ok) {
+    if (CROSS && ok && p.n_split > 1) {  // this run's own result, to be joined
+      tc_fence_after_sync();
+      const int64_t at = ((int64_t)(blockIdx.x % p.n_split) * p.BH + bh) * p.S + grow;
+      const float inv_l = lq > 0.f ? 1.f / lq : 0.f;
+#pragma unroll 1
+      for (int c2 = 0; c2 < kD / 32 && dbg_warp(dbg_tmem(dbb, tO + 32 * c2, 32, warp, kChkOTmem)); ++c2)
+        store_part(tO + 32 * c2, p.part_o + at * p.d_cols, 32 * c2, inv_l, valid, dbb, bh, grow, kChkStore);
+      if (valid && dbg_row(dbb, bh, grow, 0, 0, kChkLse)) p.part_lse[at] = (m + __log2f(l)) * kLn2;
+    } else if (ok) {
       tc_fence_after_sync();
       const float inv_l = lq > 0.f ? 1.f / lq : 0.f;
       // column blocks of 64 (128 bytes per row), 128 rows each (16 KB); the
@@ -348,8 +358,8 @@ __global__ void __launch_bounds__(kThreads1Q, 1) attn_fwd_1q_kernel(const __grid
           // a skipped copy leaves the stage's transaction count short: the
           // consumer's bounded wait then ends the kernel
           const uint32_t dst = sb + kKOff + ks * kTile + c * kChunkBytes;
-          if (dbg_tma(dbb, dst, kChunkBytes, c * 64, j * kKvRows, bh, false, kChkLoadK))
-            tma_load_3d(dst, &p.tm_k, bar(kKFull + ks), c * 64, j * kKvRows, bh, pol);
+          if (dbg_tma(dbk, dst, kChunkBytes, c * 64, (un.j0 + j) * kKvRows, bh, false, kChkLoadK))
+            tma_load_3d(dst, &p.tm_k, bar(kKFull + ks), c * 64, (un.j0 + j) * kKvRows, bh, pol);
         }
         k_issued = j + 1;
         const int vs = j % kVStages;
@@ -359,8 +369,8 @@ __global__ void __launch_bounds__(kThreads1Q, 1) attn_fwd_1q_kernel(const __grid
 #pragma unroll
         for (int c = 0; c < kD / 64; ++c) {
           const uint32_t dst = sb + kVOff + vs * kTile + c * kChunkBytes;
-          if (dbg_tma(dbb, dst, kChunkBytes, c * 64, j * kKvRows, bh, false, kChkLoadV))
-            tma_load_3d(dst, &p.tm_v, bar(kVFull + vs), c * 64, j * kKvRows, bh, pol);
+          if (dbg_tma(dbk, dst, kChunkBytes, c * 64, (un.j0 + j) * kKvRows, bh, false, kChkLoadV))
+            tma_load_3d(dst, &p.tm_v, bar(kVFull + vs), c * 64, (un.j0 + j) * kKvRows, bh, pol);
         }
         v_issued = j + 1;
       }
@@ -420,6 +430,9 @@ __global__ void __launch_bounds__(kThreads1Q, 1) attn_fwd_1q_kernel(const __grid
       ok = wait_warp(bar(kPFull + b), (j >> 1) & 1, kSiteMmaP | (j & 0xff));
       if (ok) ok = wait_warp(bar(kVFull + j % kVStages), (j / kVStages) & 1, kSiteMmaV | (j & 0xff));
       if (!ok) break;
+      if (CROSS)
+        clear_tail<kD / 64>(sb + kVOff + (j % kVStages) * kTile, kKvRows, un.len - (un.j0 + j) * kKvRows,
+                            un.len < p.Sk, lane, dbb, kChkMmaV);
       tc_fence_after_sync();
       if (dbg_smem(dbb, sb + kVOff + (j % kVStages) * kTile, kTile, 1024, kChkMmaV) &&
           dbg_tmem_cols(dbb, tmem_base + kOCol, kD, kChkMmaTmem)) {
@@ -454,31 +467,35 @@ __global__ void __launch_bounds__(kThreads1Q, 1) attn_fwd_1q_kernel(const __grid
   }
 }
 
-template <int D, int BN, bool CAUSAL, bool F16>
+template <int D, int BN, int MASK, bool F16>
 cudaError_t launch_1q(const Fwd1QParams& p, cudaStream_t stream) {
-  auto kern = attn_fwd_1q_kernel<D, BN, CAUSAL, F16>;
+  auto kern = attn_fwd_1q_kernel<D, BN, MASK, F16>;
   constexpr int kAlloc = Layout1Q<D, BN>::kAlloc;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kAlloc);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((long long)p.BH * p.n_qt), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>((long long)p.BH * p.n_qt * (MASK == kMaskCross ? p.n_split : 1)), 1, 1);
   cfg.blockDim = dim3(kThreads1Q, 1, 1);
   cfg.dynamicSmemBytes = kAlloc;
   cfg.stream = stream;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-}  // namespace
-
-template <int D>
-cudaError_t launch_1q_d(const Fwd1QParams& p, bool causal, bool f16, cudaStream_t stream) {
-  if (f16) return causal ? launch_1q<D, 64, true, true>(p, stream) : launch_1q<D, 64, false, true>(p, stream);
-  return causal ? launch_1q<D, 64, true, false>(p, stream) : launch_1q<D, 64, false, false>(p, stream);
+template <int D, bool F16>
+cudaError_t launch_1q_d(const Fwd1QParams& p, int mask, cudaStream_t stream) {
+  switch (mask) {
+    case kMaskFull: return launch_1q<D, 64, kMaskFull, F16>(p, stream);
+    case kMaskCausal: return launch_1q<D, 64, kMaskCausal, F16>(p, stream);
+    case kMaskCross: return launch_1q<D, 64, kMaskCross, F16>(p, stream);
+  }
+  return cudaErrorInvalidValue;
 }
 
-cudaError_t fwd1q_launch(const Fwd1QParams& p, int D, bool causal, bool f16, cudaStream_t stream) {
-  if (D == 192) return launch_1q_d<192>(p, causal, f16, stream);
-  if (D == 256) return launch_1q_d<256>(p, causal, f16, stream);
+}  // namespace
+
+cudaError_t fwd1q_launch(const Fwd1QParams& p, int D, int mask, bool f16, cudaStream_t stream) {
+  if (D == 192) return f16 ? launch_1q_d<192, true>(p, mask, stream) : launch_1q_d<192, false>(p, mask, stream);
+  if (D == 256) return f16 ? launch_1q_d<256, true>(p, mask, stream) : launch_1q_d<256, false>(p, mask, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -47,6 +47,7 @@
 #include <cuda_runtime.h>
 
 #include "attn_fwd.h"
+#include "cross_common.cuh"
 #include "ptx.cuh"
 #include "umma.cuh"
 
@@ -106,12 +107,6 @@ enum : int { kChkPQLoad = 0x5301, kChkPQTmem, kChkPSTmem, kChkPPTmem, kChkPOTmem
              kChkPStore, kChkPLse, kChkPLoadK, kChkPLoadV, kChkPMmaK, kChkPMmaV, kChkPMmaTmem,
              kChkPTile };
 
-// K/V tiles Q tile i meets.
-template <bool CAUSAL>
-__device__ __forceinline__ int kv_steps(int i, int n_kt) {
-  return CAUSAL ? (i + 1 < n_kt ? i + 1 : n_kt) : n_kt;
-}
-
 // QCP selects how a tile's Q rows reach tensor memory.  false: the softmax
 // warps load them (the next tile's while the current one drains) and store
 // them with tcgen05.st.  true: the producer brings them into the K ring with
@@ -119,9 +114,10 @@ __device__ __forceinline__ int kv_steps(int i, int n_kt) {
 // tcgen05.cp, so the softmax warps go straight from a tile's last step to its
 // epilogue; that shortens every tile hand-over, and pays off for short tiles
 // (fwd1qp_launch chooses).
-template <int D, bool CAUSAL, bool F16, bool QCP>
+template <int D, int MASK, bool F16, bool QCP>
 __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid_constant__ Fwd1QParams p) {
   using L = LayoutP<D>;
+  constexpr bool CAUSAL = MASK == kMaskCausal, CROSS = MASK == kMaskCross;
   constexpr int kTile = L::kTile, kChunkBytes = L::kChunkBytes;
   constexpr int kKStages = L::kKStages, kVStages = L::kVStages;
   constexpr uint32_t kQCol = L::kQCol, kOCol = L::kOCol;
@@ -135,14 +131,15 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
   const int lane = threadIdx.x & 31;
   const DbgBounds dbb{p.status, sb, smem_u32(smem_raw) + static_cast<uint32_t>(L::kAlloc), p.S,
                       p.d_cols, p.BH};
-  const int n_units = p.BH * p.n_qt;  // CTAs of the grid, one per Q tile
+  const DbgBounds dbk = key_bounds<MASK>(dbb, p.Sk);
+  const int n_units = p.BH * p.n_qt * (CROSS ? p.n_split : 1);  // CTAs of the grid
 
   // The first tile is this CTA's own.  A softmax thread's row of its Q is
   // requested before the set-up below, so that the load's latency overlaps it.
   uint32_t qw[D / 2];
   if (!QCP && warp < 4) {
     int bh0, i0;
-    schedule_unit(p.sched, static_cast<int>(blockIdx.x), &bh0, &i0);
+    fwd_tile<MASK>(p, static_cast<int>(blockIdx.x), &bh0, &i0);
     const int grow = i0 * kRowsP + warp * 32 + lane;
     const bool valid = grow < p.S;
     const uint16_t* qr = p.q + (valid ? (int64_t)bh0 * p.S + grow : 0) * p.d_cols;
@@ -185,7 +182,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
     fence_barrier_init();
     if constexpr (QCP) {
       int bh0, i0;
-      schedule_unit(p.sched, static_cast<int>(blockIdx.x), &bh0, &i0);
+      fwd_tile<MASK>(p, static_cast<int>(blockIdx.x), &bh0, &i0);
       mbar_arrive_expect_tx(bar(L::kKFull + 0), kTile);
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
@@ -244,9 +241,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
         ok = false;
         break;
       }
-      int bh, i;
-      schedule_unit(p.sched, x, &bh, &i);
-      const int nkv = kv_steps<CAUSAL>(i, p.n_kt);
+      const FwdUnit un = fwd_unit<MASK, kRowsP>(p, x);
+      const int bh = un.bh, i = un.i, nkv = un.nkv;
       const int grow = i * kRowsP + row;
       const bool valid = grow < p.S;
       float m = -INFINITY;  // reference max (log2 units) of the exponentials in O and l
@@ -271,7 +267,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
 #pragma unroll
         for (int q4 = 0; q4 < 4; ++q4) reg_fence(s[q4]);
         // allowed key columns of this tile: 0 .. lim (causal: key <= query; key < S)
-        int lim = p.S - 1 - j * kRowsP;
+        int lim = CROSS ? un.len - 1 - (un.j0 + j) * kRowsP : p.S - 1 - j * kRowsP;
         if (CAUSAL) lim = min(lim, grow - j * kRowsP);
         if (!valid) lim = -1;
         if (lim < kRowsP - 1) {
@@ -363,7 +359,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
       if (!ok) break;
       if (!QCP && nx >= 0 && dbg(nx < n_units, dbb, kChkPTile)) {
         int nbh, ni;
-        schedule_unit(p.sched, nx, &nbh, &ni);
+        fwd_tile<MASK>(p, nx, &nbh, &ni);
         const int ngrow = ni * kRowsP + row;
         const bool nvalid = ngrow < p.S;
         const uint16_t* qr = p.q + (nvalid ? (int64_t)nbh * p.S + ngrow : 0) * p.d_cols;
@@ -394,6 +390,17 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
       if (lane == 0) tma_store_wait_read();  // this warp's previous store has read the staging rows
       __syncwarp();
       const float inv_l = lq > 0.f ? 1.f / lq : 0.f;
+      if (CROSS && p.n_split > 1) {  // this run's own result, to be joined
+        const int64_t at = ((int64_t)(x % p.n_split) * p.BH + bh) * p.S + grow;
+#pragma unroll 1
+        for (int c2 = 0; c2 < D / 32 && dbg_warp(dbg_tmem(dbb, tO + 32 * c2, 32, warp, kChkPOTmem));
+             ++c2)
+          store_part(tO + 32 * c2, p.part_o + at * p.d_cols, 32 * c2, inv_l, valid, dbb, bh, grow,
+                     kChkPStore);
+        if (valid && dbg_row(dbb, bh, grow, 0, 0, kChkPLse)) p.part_lse[at] = (m + __log2f(l)) * kLn2P;
+        x = nx;
+        continue;
+      }
 #pragma unroll 1
       for (int c2 = 0; c2 < D / 64 && dbg_warp(dbg_tmem(dbb, tO + 64 * c2, 64, warp, kChkPOTmem));
            ++c2) {
@@ -472,9 +479,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
       ok = publish(0, x);
       int g = 0;
       for (int k = 0; ok && x >= 0; ++k) {
-        int bh, i;
-        schedule_unit(p.sched, x, &bh, &i);
-        const int nkv = kv_steps<CAUSAL>(i, p.n_kt);
+        const FwdUnit un = fwd_unit<MASK, kRowsP>(p, x);
+        const int bh = un.bh, i = un.i, nkv = un.nkv;
         const int jr = nkv > kAskAhead ? nkv - 1 - kAskAhead : 0;  // ask for the next tile
         int nx = -1;
         if (QCP && k > 0) {  // the tile's Q rows, ahead of its K tiles
@@ -504,8 +510,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
             // a skipped copy leaves the stage's transaction count short: the
             // consumer's bounded wait then ends the kernel
             const uint32_t dst = sb + L::kKOff + ks * kTile + c * kChunkBytes;
-            if (dbg_tma(dbb, dst, kChunkBytes, c * 64, j * kRowsP, bh, false, kChkPLoadK))
-              tma_load_3d(dst, &p.tm_k, bar(L::kKFull + ks), c * 64, j * kRowsP, bh, pol);
+            if (dbg_tma(dbk, dst, kChunkBytes, c * 64, (un.j0 + j) * kRowsP, bh, false, kChkPLoadK))
+              tma_load_3d(dst, &p.tm_k, bar(L::kKFull + ks), c * 64, (un.j0 + j) * kRowsP, bh, pol);
           }
           k_issued = kp + 1;
           const int vs = gj % kVStages;
@@ -516,8 +522,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
 #pragma unroll
           for (int c = 0; c < D / 64; ++c) {
             const uint32_t dst = sb + L::kVOff + vs * kTile + c * kChunkBytes;
-            if (dbg_tma(dbb, dst, kChunkBytes, c * 64, j * kRowsP, bh, false, kChkPLoadV))
-              tma_load_3d(dst, &p.tm_v, bar(L::kVFull + vs), c * 64, j * kRowsP, bh, pol);
+            if (dbg_tma(dbk, dst, kChunkBytes, c * 64, (un.j0 + j) * kRowsP, bh, false, kChkPLoadV))
+              tma_load_3d(dst, &p.tm_v, bar(L::kVFull + vs), c * 64, (un.j0 + j) * kRowsP, bh, pol);
           }
           v_issued = gj + 1;
           if (j == jr) request();
@@ -535,7 +541,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
             if (!ok) break;
             if (!QCP && nx >= 0) {
               int nbh, ni;
-              schedule_unit(p.sched, nx, &nbh, &ni);
+              fwd_tile<MASK>(p, nx, &nbh, &ni);
 #pragma unroll
               for (int c = 0; c < D / 64; ++c) tma_prefetch_l2_3d(&p.tm_q, c * 64, ni * kRowsP, nbh);
             }
@@ -636,10 +642,10 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
     int x = read_info(0, kSitePMmaInfo, &ok);
     int g = 0;
     int nkv = 0;
+    FwdUnit un{};
     if (ok && x >= 0) {
-      int bh, i;
-      schedule_unit(p.sched, x, &bh, &i);
-      nkv = kv_steps<CAUSAL>(i, p.n_kt);
+      un = fwd_unit<MASK, kRowsP>(p, x);
+      nkv = un.nkv;
       ok = start_tile(0, nkv, 0, 0);
     }
     for (int k = 0; ok && x >= 0; ++k) {
@@ -650,6 +656,9 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
         // V of this step has normally landed long before P: waiting for it
         // first keeps that wait off the path from P to its product
         ok = wait_warp(bar(L::kVFull + gj % kVStages), (gj / kVStages) & 1, kSitePMmaV | (gj & 0xff));
+        if (CROSS && ok)
+          clear_tail<D / 64>(sb + L::kVOff + (gj % kVStages) * kTile, kRowsP, un.len - (un.j0 + j) * kRowsP,
+                             un.len < p.Sk, lane, dbb, kChkPMmaV);
         if (ok) ok = wait_warp(bar(L::kPFull + b), (gj >> 1) & 1, kSitePMmaP | (gj & 0xff));
         if (!ok) break;
         tc_fence_after_sync();
@@ -681,9 +690,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
       // the next tile: its first S products queue behind this tile's last P·V
       x = read_info(k + 1, kSitePMmaInfo, &ok);
       if (!ok || x < 0 || !dbg(x < n_units, dbb, kChkPTile)) break;
-      int bh, i;
-      schedule_unit(p.sched, x, &bh, &i);
-      nkv = kv_steps<CAUSAL>(i, p.n_kt);
+      un = fwd_unit<MASK, kRowsP>(p, x);
+      nkv = un.nkv;
       ok = start_tile(g, nkv, (k + 1) & 1, k + 1);
     }
     if (leader) {
@@ -700,25 +708,28 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
   }
 }
 
-template <int D, bool CAUSAL, bool F16, bool QCP>
+template <int D, int MASK, bool F16, bool QCP>
 cudaError_t launch_1qp(const Fwd1QParams& p, cudaStream_t stream) {
-  auto kern = attn_fwd_1qp_kernel<D, CAUSAL, F16, QCP>;
+  auto kern = attn_fwd_1qp_kernel<D, MASK, F16, QCP>;
   constexpr int kAlloc = LayoutP<D>::kAlloc;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kAlloc);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((long long)p.BH * p.n_qt), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>((long long)p.BH * p.n_qt * (MASK == kMaskCross ? p.n_split : 1)), 1, 1);
   cfg.blockDim = dim3(kThreadsP, 1, 1);
   cfg.dynamicSmemBytes = kAlloc;
   cfg.stream = stream;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <int D, bool QCP>
-cudaError_t launch_1qp_q(const Fwd1QParams& p, bool causal, bool f16, cudaStream_t stream) {
-  if (f16)
-    return causal ? launch_1qp<D, true, true, QCP>(p, stream) : launch_1qp<D, false, true, QCP>(p, stream);
-  return causal ? launch_1qp<D, true, false, QCP>(p, stream) : launch_1qp<D, false, false, QCP>(p, stream);
+template <int D, bool QCP, bool F16>
+cudaError_t launch_1qp_q(const Fwd1QParams& p, int mask, cudaStream_t stream) {
+  switch (mask) {
+    case kMaskFull: return launch_1qp<D, kMaskFull, F16, QCP>(p, stream);
+    case kMaskCausal: return launch_1qp<D, kMaskCausal, F16, QCP>(p, stream);
+    case kMaskCross: return launch_1qp<D, kMaskCross, F16, QCP>(p, stream);
+  }
+  return cudaErrorInvalidValue;
 }
 
 // Q through the K ring and tcgen05.cp (QCP) when a tile meets this many K/V
@@ -728,17 +739,19 @@ cudaError_t launch_1qp_q(const Fwd1QParams& p, bool causal, bool f16, cudaStream
 constexpr int kQcpMaxAvgSteps = 24;
 
 template <int D>
-cudaError_t launch_1qp_d(const Fwd1QParams& p, bool causal, bool f16, cudaStream_t stream) {
-  const int avg_steps = causal ? (p.n_kt + 1) / 2 : p.n_kt;
-  return avg_steps <= kQcpMaxAvgSteps ? launch_1qp_q<D, true>(p, causal, f16, stream)
-                                      : launch_1qp_q<D, false>(p, causal, f16, stream);
+cudaError_t launch_1qp_d(const Fwd1QParams& p, int mask, bool f16, cudaStream_t stream) {
+  const int avg_steps = mask == kMaskCausal ? (p.n_kt + 1) / 2
+                        : mask == kMaskCross ? (p.n_kt + p.n_split - 1) / p.n_split : p.n_kt;
+  if (avg_steps <= kQcpMaxAvgSteps)
+    return f16 ? launch_1qp_q<D, true, true>(p, mask, stream) : launch_1qp_q<D, true, false>(p, mask, stream);
+  return f16 ? launch_1qp_q<D, false, true>(p, mask, stream) : launch_1qp_q<D, false, false>(p, mask, stream);
 }
 
 }  // namespace
 
-cudaError_t fwd1qp_launch(const Fwd1QParams& p, int D, bool causal, bool f16, cudaStream_t stream) {
-  if (D == 128) return launch_1qp_d<128>(p, causal, f16, stream);
-  if (D == 64) return launch_1qp_d<64>(p, causal, f16, stream);
+cudaError_t fwd1qp_launch(const Fwd1QParams& p, int D, int mask, bool f16, cudaStream_t stream) {
+  if (D == 128) return launch_1qp_d<128>(p, mask, f16, stream);
+  if (D == 64) return launch_1qp_d<64>(p, mask, f16, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -61,6 +61,24 @@ inline bool overlaps(const void* a, uint64_t na, const void* b, uint64_t nb) {
   return x < y + nb && y < x + na;
 }
 
+// One of a call's buffers: written ones may overlap no other.
+struct Span {
+  const void* p;
+  uint64_t bytes;
+  bool written;
+};
+
+inline bool any_overlap(const Span* s, int n) {
+  for (int i = 0; i < n; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if ((s[i].written || s[j].written) && s[i].p && s[j].p &&
+          overlaps(s[i].p, s[i].bytes, s[j].p, s[j].bytes))
+        return true;
+  return false;
+}
+
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
 // The current device's status word pair (allocated on first use), after the
 // architecture check.
 attn_status_t current_status_words(int** status);

@@ -49,11 +49,13 @@ __device__ __forceinline__ void st_shared_f32x2(uint32_t addr, float a, float b)
 // to bf16 in the 128-byte-swizzled staging block `chunk_base` (row = TMEM
 // lane), then one TMA store of the warp's rows.  Only lane 0 issues the store.
 // A chunk that starts at or past the tensor's last column (dbb.cols) is not
-// stored: a store box never starts outside the tensor.  Call with the full warp.
+// stored: a store box never starts outside the tensor.  `none`: this row's values
+// are zero whatever the accumulator holds.  Call with the full warp.
 template <bool F16>
 __device__ __forceinline__ void store_chunk(uint32_t tmem_col, uint32_t chunk_base, int row,
                                             float mul, const CUtensorMap* map, int x, int y0,
-                                            int z, int wq, int lane, const DbgBounds& dbb) {
+                                            int z, int wq, int lane, const DbgBounds& dbb,
+                                            bool none = false) {
   if (x >= dbb.cols) return;
   if (!dbg_warp(dbg_tmem(dbb, tmem_col, 64, wq, kChkAccTmem))) return;
 #pragma unroll
@@ -71,6 +73,7 @@ __device__ __forceinline__ void store_chunk(uint32_t tmem_col, uint32_t chunk_ba
       for (int e = 0; e < 4; ++e)
         w[e] = pack_x2<F16>(__uint_as_float(o[q4 * 8 + 2 * e]) * mul,
                            __uint_as_float(o[q4 * 8 + 2 * e + 1]) * mul);
+      if (none) w[0] = w[1] = w[2] = w[3] = 0u;
       if (dbg_smem(dbb, addr, 16, 16, kChkStage)) st_shared_v4(addr, w[0], w[1], w[2], w[3]);
     }
   }

@@ -14,25 +14,9 @@
 
 namespace {
 
-using ea::overlaps;
-
-// One of a call's buffers: written ones may overlap no other.
-struct Span {
-  const void* p;
-  uint64_t bytes;
-  bool written;
-};
-
-bool any_overlap(const Span* s, int n) {
-  for (int i = 0; i < n; ++i)
-    for (int j = i + 1; j < n; ++j)
-      if ((s[i].written || s[j].written) && s[i].p && s[j].p &&
-          overlaps(s[i].p, s[i].bytes, s[j].p, s[j].bytes))
-        return true;
-  return false;
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+using ea::aligned;
+using ea::any_overlap;
+using ea::Span;
 
 int64_t pitch_of(int64_t D) { return (D + 15) / 16 * 16; }
 

@@ -14,11 +14,10 @@ static_assert(ea::kRopeMaxParts == ATTN_ROPE_MAX_PARTS, "parts of a call");
 
 namespace {
 
+using ea::aligned;
 using ea::overlaps;
 
 constexpr size_t kNoSpace = 16;  // the size that says no workspace is needed
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // A tensor [B, S, heads, D] by its strides, in bytes from its first value to behind its last.
 struct View {
