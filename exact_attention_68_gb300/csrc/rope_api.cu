@@ -175,35 +175,46 @@ int sm_count() {
   return sms;
 }
 
-// How the tokens are cut into blocks.  Eight tokens a block let the angles serve
-// eight times the heads and a warp's stores run on; a call with few tokens takes
-// smaller blocks, and then several CTAs a block, until the SMs have one each.
-void plan(ea::RopeParams& p, int sms) {
-  const int64_t tokens = static_cast<int64_t>(p.B) * p.S;
-  p.log2_tokens = 3;
-  while (p.log2_tokens > 0 && ((tokens + (1 << p.log2_tokens) - 1) >> p.log2_tokens) < 2 * sms) --p.log2_tokens;
-  p.blocks = static_cast<int>((tokens + (1 << p.log2_tokens) - 1) >> p.log2_tokens);
-  int heads = 1;
-  for (int i = 0; i < p.n_parts; ++i)
-    if (p.part[i].heads > heads) heads = p.part[i].heads;
-  p.head_split = 1;
-  while (p.head_split < 8 && p.blocks * p.head_split * 2 <= sms && p.head_split * 16 < (heads << p.log2_tokens)) p.head_split *= 2;
+// Sizes, and the division of a token's number by S as a product: with l bits of S,
+// ceil(2^(30 + l) / S) is off by less than one in 2^(30 + l) / S, which no token
+// below 2^30 sees.
+void set_sizes(ea::RopeParams& p, int64_t B, int64_t S, int64_t D) {
+  p.N = static_cast<int>(B * S), p.S = static_cast<int>(S), p.D = static_cast<int>(D);
+  p.inv_d = 1.f / static_cast<float>(D);
+  int l = 0;
+  while ((int64_t(1) << l) < S) ++l;
+  p.s_shift = 30 + l;
+  p.s_mul = ((uint64_t(1) << p.s_shift) + S - 1) / S;
 }
 
-attn_status_t run(const attn_rope_part_t* parts, int n, const attn_rope_t* rope,
-                  const attn_rope_positions_t* at, int64_t B, int64_t S, int64_t D, float eps, int dtype,
-                  void* workspace, size_t space, bool bwd, cudaStream_t stream) {
-  int* status = nullptr;
-  attn_status_t st = ea::current_status_words(&status);
-  if (st != ATTN_OK) return st;
-  const int sms = sm_count();
+// The vectors that a call's rows go in.  Pairs half a row apart: vectors that divide
+// the turned half and the rest's.  All parts of a launch go the same way.
+ea::RopeShape shape_of(int64_t D, bool turn, int pairs, bool interleaved) {
+  if (turn && interleaved) return {true, 4};
+  return {false, gcd(gcd(8, pairs), static_cast<int>(D) / 2 - pairs)};
+}
+
+// Parts of one launch: at most two whose weights have a gradient, which a thread
+// adds up in registers.
+int parts_of_launch(const attn_rope_part_t* parts, int n, bool bwd) {
+  int weighted = 0;
+  for (int i = 0; i < n; ++i)
+    if (bwd && parts[i].dweight && ++weighted > 2) return i;
+  return n;
+}
+
+// One launch of n parts.  With `need`, only adds the workspace it needs to *need.
+attn_status_t launch(const attn_rope_part_t* parts, int n, const attn_rope_t* rope, const attn_rope_positions_t* at,
+                     int64_t B, int64_t S, int64_t D, float eps, int dtype, int sms, int* status, float* sums,
+                     size_t* need, bool bwd, cudaStream_t stream) {
   ea::RopeParams p;
   std::memset(&p, 0, sizeof(p));
+  set_sizes(p, B, S, D);
   p.n_parts = n;
-  p.B = static_cast<int>(B), p.S = static_cast<int>(S), p.D = static_cast<int>(D);
-  p.eps = eps, p.inv_d = 1.f / static_cast<float>(D);
+  p.eps = eps;
   p.status = status;
   bool turn = false;
+  int slot = 0;
   for (int i = 0; i < n; ++i) {
     const attn_rope_part_t& q = parts[i];
     ea::RopePart& r = p.part[i];
@@ -213,52 +224,64 @@ attn_status_t run(const attn_rope_part_t* parts, int n, const attn_rope_t* rope,
     r.weight = q.weight;
     r.weight_f32 = q.weight_f32;
     r.heads = static_cast<int>(q.heads);
-    r.turn = q.turn && rope->pairs > 0;
+    r.slot = -1;
     if (bwd) {
       r.dx = static_cast<uint16_t*>(q.dx);
       r.db = q.dx_stride_b, r.ds = q.dx_stride_s, r.dh = q.dx_stride_h;
       r.dweight = q.dweight;
+      if (q.dweight) r.slot = slot++;
     }
+    r.turn = q.turn && rope && rope->pairs > 0;
     turn = turn || r.turn;
   }
-  ea::RopeShape shape = {false, 8};
   if (turn) {
     p.pairs = static_cast<int>(rope->pairs);
     p.at = at->at;
     p.pb = at->stride_b, p.ps = at->stride_s, p.pa = at->stride_a;
+  }
+  const ea::RopeShape shape = shape_of(D, turn, p.pairs, turn && rope->interleaved);
+  const int ctas = ea::rope_plan(p, shape, bwd, sms);
+  if (need) {
+    *need += static_cast<size_t>(slot) * ctas * D * 4;
+    return ATTN_OK;
+  }
+  if (turn)
     for (int i = 0; i < p.pairs; ++i) {
       p.turns[i] = turn_fraction(rope->inv_freq[i]);
       p.axis[i] = rope->axis ? rope->axis[i] : 0;
     }
-    shape.interleaved = rope->interleaved != 0;
-  }
-  // pairs half a row apart: vectors that divide the turned half and the rest's
-  const int half = static_cast<int>(D) / 2;
-  shape.width = shape.interleaved ? 4 : gcd(gcd(8, p.pairs), half - p.pairs);
-  // a part that is not turned beside one that is has its pairs half of D apart
-  for (int i = 0; i < n && !shape.interleaved; ++i)
-    if (!p.part[i].turn && p.part[i].weight) shape.width = gcd(shape.width, half);
-  plan(p, sms);
-  cudaError_t e;
-  if (bwd) {
-    const int ctas = ea::rope_bwd_grid(p, sms);
-    size_t need = 0;
-    for (int i = 0; i < n; ++i)
-      if (p.part[i].dweight) {
-        p.part[i].sums = static_cast<float*>(workspace) + need / 4;
-        need += static_cast<size_t>(ctas) * D * 4;
-      }
-    if (need && (!workspace || space < need)) return ATTN_ERR_INVALID_ARG;
-    if (need && !aligned(workspace, 16)) return ATTN_ERR_MISALIGNED;
-    e = ea::rope_bwd_launch(p, shape, dtype == ATTN_F16, sms, stream);
-  } else {
-    e = ea::rope_fwd_launch(p, shape, dtype == ATTN_F16, stream);
-  }
+  for (int i = 0; i < n; ++i)
+    if (p.part[i].slot >= 0) p.part[i].sums = sums + static_cast<int64_t>(p.part[i].slot) * ctas * D;
+  const cudaError_t e = bwd ? ea::rope_bwd_launch(p, shape, dtype == ATTN_F16, ctas, stream)
+                            : ea::rope_fwd_launch(p, shape, dtype == ATTN_F16, ctas, stream);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return ea::cuda_failure(static_cast<int>(e));
   }
   return ATTN_OK;
+}
+
+attn_status_t run(const attn_rope_part_t* parts, int n, const attn_rope_t* rope,
+                  const attn_rope_positions_t* at, int64_t B, int64_t S, int64_t D, float eps, int dtype,
+                  void* workspace, size_t space, bool bwd, cudaStream_t stream) {
+  int* status = nullptr;
+  attn_status_t st = ea::current_status_words(&status);
+  if (st != ATTN_OK) return st;
+  const int sms = sm_count();
+  float* sums = static_cast<float*>(workspace);
+  size_t need = 0;
+  for (int i = 0, m; bwd && i < n; i += m) {
+    m = parts_of_launch(parts + i, n - i, bwd);
+    launch(parts + i, m, rope, at, B, S, D, eps, dtype, sms, status, nullptr, &need, bwd, stream);
+  }
+  if (need && (!workspace || space < need)) return ATTN_ERR_INVALID_ARG;
+  if (need && !aligned(workspace, 16)) return ATTN_ERR_MISALIGNED;
+  // launches follow one another on the stream: they share the workspace
+  for (int i = 0, m; i < n && st == ATTN_OK; i += m) {
+    m = parts_of_launch(parts + i, n - i, bwd);
+    st = launch(parts + i, m, rope, at, B, S, D, eps, dtype, sms, status, sums, nullptr, bwd, stream);
+  }
+  return st;
 }
 
 }  // namespace
@@ -280,15 +303,11 @@ size_t attn_rope_bwd_workspace(const attn_rope_part_t* parts, int n, int64_t B, 
   if (!any) return kNoSpace;
   const int sms = sm_count();
   if (sms == 0) return 0;
-  ea::RopeParams p;
-  std::memset(&p, 0, sizeof(p));
-  p.n_parts = n;
-  p.B = static_cast<int>(B), p.S = static_cast<int>(S), p.D = static_cast<int>(D);
-  for (int i = 0; i < n; ++i) p.part[i].heads = static_cast<int>(parts[i].heads);
-  plan(p, sms);
+  // the number of CTAs goes by the rotation too, which is not told here: the most
+  // that any has
   size_t bytes = 0;
   for (int i = 0; i < n; ++i)
-    if (parts[i].dweight) bytes += static_cast<size_t>(ea::rope_bwd_grid(p, sms)) * D * 4;
+    if (parts[i].dweight) bytes += static_cast<size_t>(ea::rope_most_ctas(sms)) * D * 4;
   return bytes < kNoSpace ? kNoSpace : bytes;
 }
 

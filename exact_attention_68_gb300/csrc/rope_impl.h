@@ -10,7 +10,6 @@ namespace ea {
 
 constexpr int kRopeMaxParts = 4;
 constexpr int kRopeMaxPairs = 128;
-constexpr int kRopeThreads = 256;
 
 struct RopePart {
   const uint16_t* x;
@@ -23,6 +22,7 @@ struct RopePart {
   float* sums;         // workspace: [CTAs of the grid][D], null without dweight
   int heads;
   int weight_f32, turn;
+  int slot;            // which of the launch's two weight gradients, -1: none
 };
 
 struct RopeParams {
@@ -32,25 +32,31 @@ struct RopeParams {
   const int* at;
   int64_t pb, ps, pa;  // strides of the positions
   int n_parts;
-  int pairs;        // 0: no part turns
-  int B, S, D;
-  int log2_tokens;  // tokens a CTA takes at once
-  int blocks;       // of that many tokens
-  int head_split;   // CTAs a block's heads are dealt to
+  int pairs;           // 0: no part turns
+  int N, S, D;         // tokens in all, tokens of a sequence, channels
+  uint64_t s_mul;      // n / S = (n · s_mul) >> s_shift for n < 2^30
+  int s_shift;
+  int lanes, per_warp; // of a row; rows a warp takes at once
+  int split, log2_split;  // units that one token is dealt to, by heads
+  int units;
   float eps, inv_d;
   int* status;
 };
 
-// How many channels of a row a thread takes, and how: see rope_sm103.cu.
+// How a row's channels go to threads: see rope_sm103.cu.
 struct RopeShape {
   bool interleaved;
   int width;  // pairs of one vector: 8, 4, 2 or 1; 4 where interleaved
 };
 
-// CTAs of the backward's grid that add to dweight.
-int rope_bwd_grid(const RopeParams& p, int sms);
+// Fills in lanes, per_warp, split and units; CTAs of the grid.
+int rope_plan(RopeParams& p, RopeShape shape, bool bwd, int sms);
 
-cudaError_t rope_fwd_launch(const RopeParams& p, RopeShape shape, bool f16, cudaStream_t stream);
-cudaError_t rope_bwd_launch(const RopeParams& p, RopeShape shape, bool f16, int sms, cudaStream_t stream);
+// The most CTAs that the gradient's grid has on a device of `sms` SMs.
+int rope_most_ctas(int sms);
+
+cudaError_t rope_fwd_launch(const RopeParams& p, RopeShape shape, bool f16, int ctas, cudaStream_t stream);
+// Then the second kernel that adds up dweight, if any part has sums.
+cudaError_t rope_bwd_launch(const RopeParams& p, RopeShape shape, bool f16, int ctas, cudaStream_t stream);
 
 }  // namespace ea

@@ -6,16 +6,18 @@
 // are shaped by three things: full-width loads and stores, enough of them in
 // flight, and few instructions a value.
 //
-//   A CTA takes a block of tokens (1 to 8) of one part and all its heads.  The
-//   angles of the block's tokens are found once, into shared memory, and serve
-//   every head: sine and cosine cost about as much as a row of 16 channels.
-//   A thread holds `width` pairs of a row, both channels of each, so that the
-//   rotation needs no exchange: two 16-byte loads where pairs are half a row
-//   apart, one where they are neighbours.  Rows go to D/16 (or D/8) neighbouring
-//   lanes, whatever that number is: the sums over a row are shuffles that stop at
-//   its last lane.  Rows are dealt token first, head second, so that a warp's
-//   stores run on through y, where a head's tokens follow one another.
-//   The next row's loads are issued before this row is worked on.
+//   A warp works by itself, on one unit after the other: a token's heads of all
+//   parts, or a share of them where tokens are few.  It finds the angles of the
+//   token once, for all heads, into shared memory: a sine and a cosine cost about
+//   as much as a row's 16 values.
+//   A lane holds 16 values of a row, in pairs: `width` pairs to a vector, both
+//   channels of each, so that the rotation needs no exchange.  A row takes
+//   D/16 neighbouring lanes, whatever that number is (the sums over a row are
+//   shuffles that stop at its last lane), and a warp as many rows as fit.
+//   Rows come through a ring in shared memory that each lane fills and reads for
+//   itself (cp.async, no barrier), several rows ahead and across units: 32 to 64 KB
+//   in flight on an SM without registers to hold them.
+//   Units are dealt to the warps of one full grid, each the same number of them.
 //
 // Angles.  A position adds the fraction inv_freq / 2π of a turn.  It is kept as
 // a 64-bit integer in units of 2^-64 turns: position times it, modulo 2^64, is
@@ -23,8 +25,10 @@
 // go to sincospif.
 //
 // The gradient of the weights: each thread adds up its channels over all rows
-// that its CTA takes, the CTA adds its threads' sums in a fixed order, and a
-// second kernel the CTAs'.
+// that it takes, the CTA adds its threads' sums in a fixed order, and a second
+// kernel the CTAs'.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -36,8 +40,7 @@
 namespace ea {
 namespace {
 
-constexpr int kMaxTokens = 8;  // of a block
-enum : int { kChkRopeRow = 0x6101, kChkRopeCopy = 0x6102 };
+enum : int { kChkRopeRow = 0x6101 };
 
 template <int N>
 struct Vec;  // N 16-bit values
@@ -51,33 +54,7 @@ __device__ __forceinline__ float2 widen(uint32_t x) {
   if constexpr (F16) return f16x2_to_f32(x);
   else return make_float2(bf16_lo(x), bf16_hi(x));
 }
-
-template <bool F16, int N>
-__device__ __forceinline__ void unpack(const typename Vec<N>::T& v, float (&f)[N]) {
-  if constexpr (N == 1) {
-    f[0] = widen<F16>(v).x;
-  } else {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(&v);
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      const float2 x = widen<F16>(w[i]);
-      f[2 * i] = x.x, f[2 * i + 1] = x.y;
-    }
-  }
-}
-
-template <bool F16, int N>
-__device__ __forceinline__ typename Vec<N>::T pack(const float (&f)[N]) {
-  if constexpr (N == 1) {
-    return static_cast<uint16_t>(pack_x2<F16>(f[0], 0.f));
-  } else {
-    typename Vec<N>::T v;
-    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) w[i] = pack_x2<F16>(f[2 * i], f[2 * i + 1]);
-    return v;
-  }
-}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 template <bool F16>
 __device__ __forceinline__ float weight_at(const RopePart& q, int d) {
@@ -86,277 +63,533 @@ __device__ __forceinline__ float weight_at(const RopePart& q, int d) {
   return widen<F16>(w).x;
 }
 
-// The sum of v over a row's `lanes` lanes, in every one of them.  t: this lane's
-// place in its row, first: the row's first lane.  Lanes behind the last row pass
-// through with sums of their own.
-__device__ __forceinline__ float row_sum(float v, int t, int lanes, int first) {
-  for (int off = 1; off < lanes; off <<= 1) {
-    const float o = __shfl_down_sync(0xffffffffu, v, off);
-    if (t + off < lanes) v += o;
-  }
-  return __shfl_sync(0xffffffffu, v, first);
-}
-
-// One thread's pairs of a row: unit i of NU holds VW pairs.  Where pairs are half a
-// row apart their first channels are a .. a+VW-1, the second ones b ..; where
-// they are neighbours the unit is the 2·VW channels from a on.
-template <bool INTER, int VW>
-struct Unit {
-  int a, b;     // first channel of either half (b unused if INTER)
-  int pair;     // index of the first pair
-  bool in;      // whether the unit exists
-};
-
-
-
-template <bool F16, bool INTER, int VW, bool BWD>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int NU = VW >= 4 ? 1 : 4 / VW;  // units of a thread: a row fits a warp
-  constexpr int LV = INTER ? 2 * VW : VW;   // values of one load
-  constexpr int NL = INTER ? 1 : 2;         // loads of a unit
-  using LT = typename Vec<LV>::T;
-  __shared__ float2 s_turn[kMaxTokens * kRopeMaxPairs];  // cos, sin
-  __shared__ int2 s_tok[kMaxTokens];                     // batch, token; batch -1: behind the last
-  __shared__ float s_w[2 * kRopeMaxPairs];
-
-  const RopePart& q = p.part[blockIdx.y];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int T = 1 << p.log2_tokens;
-  const int split = blockIdx.x % p.head_split, grid = gridDim.x / p.head_split;
-  const int rows = q.heads << p.log2_tokens;
-  const bool norm = q.weight != nullptr;
-
-  // ---- a part that is only laid out: 16-byte copies
-  if (!norm && !q.turn) {
-    const int lanes = p.D / 8;
-    for (int block = blockIdx.x / p.head_split; block < p.blocks; block += grid) {
-      const int total = rows * lanes;
-      for (int c = split * kRopeThreads + tid; c < total; c += p.head_split * kRopeThreads) {
-        const int row = c / lanes, col = (c - row * lanes) * 8;
-        const int n = (block << p.log2_tokens) + (row & (T - 1)), h = row >> p.log2_tokens;
-        if (n >= p.B * p.S) continue;
-        const int b = n / p.S, s = n - b * p.S;
-        if (kDebugChecks && (h >= q.heads || col + 8 > p.D)) {
-          dbg_fail(p.status, kChkRopeCopy);
-          continue;
-        }
-        uint16_t* y = q.y + (((int64_t)b * q.heads + h) * p.S + s) * p.D + col;
-        if constexpr (BWD) {
-          *reinterpret_cast<uint4*>(q.dx + b * q.db + s * q.ds + h * q.dh + col) =
-              __ldcs(reinterpret_cast<const uint4*>(y));
-        } else {
-          *reinterpret_cast<uint4*>(y) =
-              __ldcs(reinterpret_cast<const uint4*>(q.x + b * q.xb + s * q.xs + h * q.xh + col));
-        }
-      }
+// The sums of each v over a row's `lanes` lanes, in every one of them.  t: this lane's
+// place in its row, first: the row's first lane, even: lanes is a power of two.
+// Lanes behind the last row pass through with sums of their own.
+template <int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], int t, int lanes, int first, bool even) {
+  if (even) {
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      if (off >= lanes) break;  // the same in every lane
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
     }
     return;
   }
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    if (off >= lanes) break;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float o = __shfl_down_sync(0xffffffffu, v[i], off);
+      if (t + off < lanes) v[i] += o;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, v[i], first);
+}
 
-  const int pairs = q.turn ? p.pairs : 0;
-  const int units = p.D / (2 * VW);
-  const int lanes = (units + NU - 1) / NU;  // of a row, at most 32
-  const int per_warp = 32 / lanes;
-  const int mine = lane / lanes;            // row of the warp's rows; per_warp: none
+// 4, 8 or 16 bytes global -> shared, asynchronous; 2 bytes at once.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else if constexpr (BYTES == 2)
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst), "h"(*static_cast<const uint16_t*>(src)) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Threads of a CTA (warps share nothing but the weights and, in the gradient,
+// the sum of theirs), CTAs that are to fit an SM, and rows that a ring holds.
+template <bool BWD>
+struct RopeTile {
+  static constexpr int kThreads = BWD ? 128 : 64;
+  static constexpr int kCtas = BWD ? 3 : 8;
+  static constexpr int kRing = 3;
+  static constexpr int kRows = 2;  // of a lane at once
+};
+
+// float4 of a unit's angles: of each pair cos, cos, -sin, sin where a float2 is a
+// pair; else the cosines, the sines and the negative sines (two pairs: cos, cos, sin,
+// sin, then the negative ones).
+template <int VW>
+struct RopeTurns {
+  static constexpr int kUnit = VW == 1 ? 1 : VW == 2 ? 2 : 3 * VW / 4;
+};
+
+template <bool F16, bool INTER, int VW, bool BWD>
+__global__ void __launch_bounds__(RopeTile<BWD>::kThreads, RopeTile<BWD>::kCtas)
+    rope_kernel(const __grid_constant__ RopeParams p) {
+  using RT = RopeTile<BWD>;
+  // A lane's 16 values of a row: NU units of VW pairs.  Where pairs are half a row
+  // apart unit u's first channels are a .. a+VW-1, the second ones b ..; where they
+  // are neighbours the unit is the 2·VW channels from a on.
+  constexpr int NU = 8 / VW;
+  constexpr int LV = INTER ? 2 * VW : VW;   // values of one load
+  constexpr int NL = INTER ? 1 : 2;         // loads of a unit
+  // In registers a unit is VW float2: the first channels of two pairs each, then
+  // the second ones; of one pair where VW is 1 (kByPair).
+  constexpr bool kByPair = VW == 1;
+  constexpr int kWarps = RT::kThreads / 32;
+  constexpr int kVecs = NU * NL * (BWD ? 2 : 1);  // loads of a row
+  constexpr int kTurn = RopeTurns<VW>::kUnit;
+  using LT = typename Vec<LV>::T;
+  constexpr int kRows = RT::kRows;
+  __shared__ LT s_ring[kWarps][RT::kRing][kRows][kVecs][32];
+  // (indexed by lane: constant memory would serve one lane after the other)
+  __shared__ uint64_t s_fraction[kRopeMaxPairs];
+  extern __shared__ float4 s_dyn[];  // weights [parts][4 · lanes], then per warp the angles [NU · kTurn · lanes]
+
+  // (the shuffle tells the compiler that the warp's number, and with it all that says
+  // where a warp is, is the same in every lane)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int lanes = p.lanes;
+  const bool even = (lanes & (lanes - 1)) == 0;
+  const int mine = lane / lanes;  // row of the warp's; per_warp: none
   const int t = lane - mine * lanes, first = mine * lanes;
-  Unit<INTER, VW> unit[NU];
+  const int units = p.D / (2 * VW);
+  int ca[NU], cb[NU];  // this lane's channels
+  bool in[NU];
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
     const int u = t + i * lanes;
-    unit[i].in = u < units;
-    unit[i].pair = u * VW;
-    if constexpr (INTER) {
-      unit[i].a = u * 2 * VW;
-      unit[i].b = 0;
-    } else {
-      const bool turned = u * VW < pairs;
-      unit[i].a = turned ? u * VW : 2 * pairs + (u * VW - pairs);
-      unit[i].b = unit[i].a + (turned ? pairs : p.D / 2 - pairs);
-    }
+    in[i] = u < units && mine < p.per_warp;
+    ca[i] = INTER ? u * 2 * VW : u * VW < p.pairs ? u * VW : p.pairs + u * VW;
+    cb[i] = INTER ? 0 : ca[i] + (u * VW < p.pairs ? p.pairs : p.D / 2 - p.pairs);
   }
-  if (norm)
-    for (int d = tid; d < p.D; d += kRopeThreads) s_w[d] = weight_at<F16>(q, d);
-  __syncthreads();
-  // the weights of this thread's channels: the first VW of a unit are its first half
-  float w[NU][2 * VW];
-#pragma unroll
-  for (int i = 0; i < NU; ++i)
-#pragma unroll
-    for (int e = 0; e < 2 * VW; ++e) {
-      const int d = INTER || e < VW ? unit[i].a + e : unit[i].b + e - VW;
-      w[i][e] = norm && unit[i].in ? s_w[d] : 1.f;
-    }
-  float acc[BWD ? NU : 1][2 * VW];
+  // channel of value e (0 .. 2·VW-1, in the order of the float2) of unit i
+  auto channel = [&](int i, int e) {
+    if constexpr (INTER) return ca[i] + (e < VW ? 2 * e : 2 * (e - VW) + 1);
+    else return e < VW ? ca[i] + e : cb[i] + e - VW;
+  };
+  // weights so that lanes read 16 bytes side by side (8 where VW is 1)
+  constexpr int kW = VW == 1 ? 2 : 4;
+  auto w_at = [&](int i, int e) { return ((i * (2 * VW / kW) + e / kW) * lanes + t) * kW + e % kW; };
+  float* s_w = reinterpret_cast<float*>(s_dyn);
+  float4* s_turn = s_dyn + (p.n_parts * 4 + warp * NU * kTurn) * lanes;
+  float2 acc[BWD ? 2 : 1][NU][VW];
   if constexpr (BWD) {
 #pragma unroll
-    for (int i = 0; i < NU; ++i)
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int e = 0; e < 2 * VW; ++e) acc[i][e] = 0.f;
+      for (int i = 0; i < NU; ++i)
+#pragma unroll
+        for (int e = 0; e < VW; ++e) acc[k][i][e] = both(0.f);
   }
 
-  const int stride = p.head_split * (kRopeThreads / 32) * per_warp;
-  const int row0 = (split * (kRopeThreads / 32) + warp) * per_warp + mine;
-  for (int block = blockIdx.x / p.head_split; block < p.blocks; block += grid) {
-    // ---- the block's tokens and their angles
-    __syncthreads();
-    if (tid < T) {
-      const int n = (block << p.log2_tokens) + tid;
-      const int b = n / p.S;
-      s_tok[tid] = n < p.B * p.S ? make_int2(b, n - b * p.S) : make_int2(-1, 0);
+  const uint32_t ring = smem_u32(&s_ring[warp][0][0][0][lane]);
+  // Where a warp is: a unit's part, the first head of its rows there, and the
+  // token; and this lane's first row, to read (x, and dy in y) or to write (to).
+  const int stride = gridDim.x * kWarps, step = kRows * p.per_warp * p.split;
+  const int64_t plane = (int64_t)p.S * p.D;
+  struct Place {
+    int unit, part, h, b, s;
+    const uint16_t *x, *y;
+    uint16_t* to;
+  };
+  auto token = [&](Place& c) {
+    const int n = c.unit >> p.log2_split;
+    c.b = static_cast<int>((static_cast<uint64_t>(n) * p.s_mul) >> p.s_shift);
+    c.s = n - c.b * p.S;
+    c.part = 0;
+  };
+  auto enter = [&](Place& c, bool reads) {
+    const RopePart& q = p.part[c.part];
+    c.h = (c.unit & (p.split - 1)) * kRows * p.per_warp;
+    const int h = c.h + mine;
+    const int64_t at = ((int64_t)c.b * q.heads + h) * plane + (int64_t)c.s * p.D;
+    if (reads) {
+      c.x = q.x + c.b * q.xb + c.s * q.xs + h * q.xh;
+      if constexpr (BWD) c.y = q.y + at;
+    } else {
+      c.to = BWD ? q.dx + c.b * q.db + c.s * q.ds + h * q.dh : q.y + at;
     }
-    for (int c = tid; c < pairs << p.log2_tokens; c += kRopeThreads) {
-      const int tok = c / pairs, i = c - tok * pairs;
-      const int n = (block << p.log2_tokens) + tok;
-      if (n >= p.B * p.S) break;
-      const int b = n / p.S, s = n - b * p.S;
-      const int64_t at = __ldg(p.at + b * p.pb + s * p.ps + p.axis[i] * p.pa);
-      const uint64_t turn = static_cast<uint64_t>(at) * p.turns[i];
+  };
+  // on to rows that are there: a share of a unit may have none of a part
+  auto settle = [&](Place& c, bool reads) {
+    while (c.unit < p.units && c.h >= p.part[c.part].heads) {
+      if (++c.part == p.n_parts) {
+        c.unit += stride;
+        token(c);
+      }
+      enter(c, reads);
+    }
+  };
+  auto start = [&](bool reads) {
+    Place c;
+    c.unit = static_cast<int>(blockIdx.x) * kWarps + warp;
+    token(c);
+    enter(c, reads);
+    settle(c, reads);
+    return c;
+  };
+  auto next = [&](Place& c, bool reads) {
+    const RopePart& q = p.part[c.part];
+    c.h += step;
+    if (c.h >= q.heads) return settle(c, reads);
+    if (reads) {
+      c.x += step * q.xh;
+      if constexpr (BWD) c.y += step * plane;
+    } else {
+      c.to += BWD ? step * q.dh : step * plane;
+    }
+  };
+  auto load = [&](const Place& c, int slot) {
+    if (c.unit < p.units) {
+      const RopePart& q = p.part[c.part];
+      const bool read_x = !BWD || q.weight != nullptr;
+      if (kDebugChecks && (c.b < 0 || c.s < 0 || c.s >= p.S || c.b * (int64_t)p.S + c.s >= p.N)) {
+        dbg_fail(p.status, kChkRopeRow);
+      } else {
+        const uint32_t at = ring + slot * (kRows * kVecs * 32) * static_cast<int>(sizeof(LT));
+        const int64_t next_x = p.per_warp * q.xh, next_y = p.per_warp * plane;
+#pragma unroll
+        for (int j = 0; j < kRows; ++j)
+#pragma unroll
+          for (int i = 0; i < NU; ++i)
+            if (in[i] && c.h + mine + j * p.per_warp < q.heads) {
+#pragma unroll
+              for (int k = 0; k < NL; ++k) {
+                const uint32_t dst = at + ((j * kVecs + i * NL + k) * 32) * static_cast<int>(sizeof(LT));
+                const int d = k == 0 ? ca[i] : cb[i];
+                if (read_x) copy_async<LV * 2>(dst, c.x + j * next_x + d);
+                if constexpr (BWD) copy_async<LV * 2>(dst + NU * NL * 32 * sizeof(LT), c.y + j * next_y + d);
+              }
+            }
+      }
+    }
+    copy_commit();
+  };
+
+  // positions of the next unit's token, asked for while this one's rows are worked on
+  constexpr int kAngles = kRopeMaxPairs / 32;  // of a lane
+  int pos[kAngles];
+  uint32_t axes = 0;  // a byte each
+#pragma unroll
+  for (int k = 0; k < kAngles; ++k)
+    if (lane + 32 * k < p.pairs) axes |= static_cast<uint32_t>(p.axis[lane + 32 * k]) << (8 * k);
+  auto ask = [&](int unit) {
+    if (unit >= p.units) return;
+    const int n = unit >> p.log2_split;
+    const int b = static_cast<int>((static_cast<uint64_t>(n) * p.s_mul) >> p.s_shift), s = n - b * p.S;
+    const int* at = p.at + b * p.pb + s * p.ps;
+#pragma unroll
+    for (int k = 0; k < kAngles; ++k)
+      if (lane + 32 * k < p.pairs) pos[k] = __ldg(at + (axes >> (8 * k) & 255) * p.pa);
+  };
+  auto turn_token = [&]() {
+    float* to = reinterpret_cast<float*>(s_turn);
+#pragma unroll
+    for (int k = 0; k < kAngles; ++k) {
+      const int i = lane + 32 * k;
+      if (i >= p.pairs) break;
+      const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(pos[k])) * s_fraction[i];
       // turns · 2^64, signed: half turns are its top 32 bits / 2^31
       float sn, cs;
       sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sn, &cs);
-      s_turn[c] = make_float2(cs, sn);
-    }
-    __syncthreads();
-
-    LT xv[NU][NL], gv[NU][NL];
-    int tok = 0;
-    auto load = [&](int row) {
-      const int tk = row & (T - 1), h = row >> p.log2_tokens;
-      const int2 bs = s_tok[tk];
-      if (mine >= per_warp || row >= rows || bs.x < 0) return -1;
-      if (kDebugChecks && (h >= q.heads || bs.x >= p.B || bs.y >= p.S)) {
-        dbg_fail(p.status, kChkRopeRow);
-        return -1;
-      }
-      const uint16_t* x = q.x + bs.x * q.xb + bs.y * q.xs + h * q.xh;
-      const uint16_t* y = q.y + (((int64_t)bs.x * q.heads + h) * p.S + bs.y) * p.D;
-#pragma unroll
-      for (int i = 0; i < NU; ++i)
-#pragma unroll
-        for (int k = 0; k < NL; ++k) {
-          if (!unit[i].in) continue;
-          const int d = k == 0 ? unit[i].a : unit[i].b;
-          if (!BWD || norm) xv[i][k] = __ldcs(reinterpret_cast<const LT*>(x + d));
-          if constexpr (BWD) gv[i][k] = __ldcs(reinterpret_cast<const LT*>(y + d));
-        }
-      return tk;
-    };
-    tok = load(row0);
-    for (int row = row0; row - mine < rows; row += stride) {
-      const int tk = tok, h = row >> p.log2_tokens;
-      float x[NU][2 * VW], g[NU][2 * VW];
-#pragma unroll
-      for (int i = 0; i < NU; ++i)
-#pragma unroll
-        for (int k = 0; k < NL; ++k) {
-          float f[LV];
-          const bool there = tk >= 0 && unit[i].in;
-          if (!BWD || norm) {
-            unpack<F16, LV>(xv[i][k], f);
-#pragma unroll
-            for (int e = 0; e < LV; ++e) x[i][k * LV + e] = there ? f[e] : 0.f;
-          }
-          if constexpr (BWD) {
-            unpack<F16, LV>(gv[i][k], f);
-#pragma unroll
-            for (int e = 0; e < LV; ++e) g[i][k * LV + e] = there ? f[e] : 0.f;
-          }
-        }
-      tok = load(row + stride);  // the next row's, while this one is worked on
-
-      // y = R(z), or dz = R^T dy, in place in `f`
-      auto turned = [&](float(&f)[NU][2 * VW]) {
-        if (pairs == 0 || tk < 0) return;
-#pragma unroll
-        for (int i = 0; i < NU; ++i) {
-          if (!unit[i].in || unit[i].pair >= pairs) continue;
-#pragma unroll
-          for (int e = 0; e < VW; ++e) {
-            if (INTER && unit[i].pair + e >= pairs) continue;
-            const float2 cs = s_turn[tk * pairs + unit[i].pair + e];
-            const float sn = BWD ? -cs.y : cs.y;
-            float& a = f[i][INTER ? 2 * e : e];
-            float& c = f[i][INTER ? 2 * e + 1 : VW + e];
-            const float a1 = a * cs.x - c * sn;
-            c = a * sn + c * cs.x;
-            a = a1;
-          }
-        }
-      };
-      if constexpr (!BWD) {
-        if (norm) {
-          float ss = 0.f;
-#pragma unroll
-          for (int i = 0; i < NU; ++i)
-#pragma unroll
-            for (int e = 0; e < 2 * VW; ++e) ss = fmaf(x[i][e], x[i][e], ss);
-          ss = row_sum(ss, t, lanes, first);
-          const float r = rsqrtf(fmaf(ss, p.inv_d, p.eps));
-#pragma unroll
-          for (int i = 0; i < NU; ++i)
-#pragma unroll
-            for (int e = 0; e < 2 * VW; ++e) x[i][e] *= r * w[i][e];
-        }
-        turned(x);
+      if constexpr (BWD) sn = -sn;
+      // pair i is pair i % VW of unit i / VW
+      const int u = i / VW, e = i % VW, ui = u / lanes, ut = u - ui * lanes;
+      auto place = [&](int c, int f) { return ((ui * kTurn + c) * lanes + ut) * 4 + f; };
+      if constexpr (kByPair) {
+        *reinterpret_cast<float4*>(to + place(e, 0)) = make_float4(cs, cs, -sn, sn);
+      } else if constexpr (VW == 2) {
+        to[place(0, e)] = cs, to[place(0, 2 + e)] = sn, to[place(1, e)] = -sn;
       } else {
-        turned(g);
-        if (norm) {
-          float ss = 0.f, sg = 0.f;
-#pragma unroll
-          for (int i = 0; i < NU; ++i)
-#pragma unroll
-            for (int e = 0; e < 2 * VW; ++e) {
-              ss = fmaf(x[i][e], x[i][e], ss);
-              sg = fmaf(g[i][e] * w[i][e], x[i][e], sg);
-            }
-          ss = row_sum(ss, t, lanes, first);
-          sg = row_sum(sg, t, lanes, first);
-          const float r = rsqrtf(fmaf(ss, p.inv_d, p.eps));
-          const float c = r * r * sg * p.inv_d;  // mean(g ⊙ x·r)·r
-#pragma unroll
-          for (int i = 0; i < NU; ++i)
-#pragma unroll
-            for (int e = 0; e < 2 * VW; ++e) {
-              if (tk >= 0) acc[i][e] = fmaf(g[i][e], x[i][e] * r, acc[i][e]);
-              g[i][e] = r * (g[i][e] * w[i][e] - x[i][e] * c);
-            }
-        }
+        to[place(e / 4, e % 4)] = cs;
+        to[place(VW / 4 + e / 4, e % 4)] = sn;
+        to[place(2 * (VW / 4) + e / 4, e % 4)] = -sn;
       }
-      if (tk >= 0) {
-        const int2 bs = s_tok[tk];
-        uint16_t* to = BWD ? q.dx + bs.x * q.db + bs.y * q.ds + h * q.dh
-                           : q.y + (((int64_t)bs.x * q.heads + h) * p.S + bs.y) * p.D;
-        float(&f)[NU][2 * VW] = BWD ? g : x;
+    }
+  };
+
+  Place ahead = start(true), here = start(false);
+#pragma unroll
+  for (int s = 0; s < RT::kRing - 1; ++s) {
+    load(ahead, s);
+    if (ahead.unit < p.units) next(ahead, true);
+  }
+  if (p.pairs > 0) ask(here.unit);
+  // (what a row waits for longest, its loads and positions, is on its way)
+  for (int i = tid; i < p.pairs; i += RT::kThreads) s_fraction[i] = p.turns[i];
+  if (mine == 0 && warp == 0)
+    for (int q = 0; q < p.n_parts; ++q)
+#pragma unroll
+      for (int i = 0; i < NU; ++i)
+#pragma unroll
+        for (int e = 0; e < 2 * VW; ++e)
+          s_w[q * 16 * lanes + w_at(i, e)] =
+              p.part[q].weight && in[i] ? weight_at<F16>(p.part[q], channel(i, e)) : 1.f;
+  __syncthreads();
+  int slot = 0, last_unit = -1;
+  while (here.unit < p.units) {
+    if (p.pairs > 0 && here.unit != last_unit) {
+      __syncwarp();
+      turn_token();
+      ask(here.unit + stride);
+      __syncwarp();
+    }
+    last_unit = here.unit;
+    load(ahead, slot == 0 ? RT::kRing - 1 : slot - 1);
+    if (ahead.unit < p.units) next(ahead, true);
+    copy_wait<RT::kRing - 1>();
+    const RopePart& q = p.part[here.part];
+    const bool norm = q.weight != nullptr;
+    const int left = q.heads - here.h, rows_in = left - mine;  // this lane's row j is there if j · per_warp is less
+    uint16_t* const to0 = here.to;
+    const int64_t next_to = p.per_warp * (BWD ? q.dh : plane);
+    const float* weights = s_w + here.part * 16 * lanes;
+    const LT(&landed)[kRows][kVecs][32] = s_ring[warp][slot];
+    slot = slot + 1 == RT::kRing ? 0 : slot + 1;
+    next(here, false);
+    if (!norm && !q.turn) {  // only laid out
+#pragma unroll
+      for (int j = 0; j < kRows; ++j)
 #pragma unroll
         for (int i = 0; i < NU; ++i)
 #pragma unroll
-          for (int k = 0; k < NL; ++k) {
-            if (!unit[i].in) continue;
-            float o[LV];
-#pragma unroll
-            for (int e = 0; e < LV; ++e) o[e] = f[i][k * LV + e];
-            *reinterpret_cast<LT*>(to + (k == 0 ? unit[i].a : unit[i].b)) = pack<F16, LV>(o);
-          }
-      }
+          for (int k = 0; k < NL; ++k)
+            if (in[i] && j * p.per_warp < rows_in)
+              *reinterpret_cast<LT*>(to0 + j * next_to + (k == 0 ? ca[i] : cb[i])) =
+                  landed[j][(BWD ? NU * NL : 0) + i * NL + k][lane];
+      continue;
     }
+
+    // J rows of this lane side by side: their weights and angles are read once
+    auto work = [&](auto rows) {
+      constexpr int J = decltype(rows)::value;
+      // the rows as float2; a lane's unit that is not there counts as zero (all of a
+      // row that is not there may hold anything: nobody else reads its sums)
+      auto widened = [&](int v0, float2(&f)[J][NU][VW]) {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int i = 0; i < NU; ++i) {
+            LT v[NL];
+#pragma unroll
+            for (int k = 0; k < NL; ++k) v[k] = landed[j][v0 + i * NL + k][lane];
+            if constexpr (VW == 1) {
+              f[j][i][0] = make_float2(widen<F16>(v[0]).x, widen<F16>(v[NL - 1]).x);
+            } else if constexpr (INTER) {
+              const uint32_t* wd = reinterpret_cast<const uint32_t*>(&v[0]);
+#pragma unroll
+              for (int e = 0; e < VW / 2; ++e) {
+                const float2 a = widen<F16>(wd[2 * e]), b = widen<F16>(wd[2 * e + 1]);
+                f[j][i][e] = make_float2(a.x, b.x), f[j][i][VW / 2 + e] = make_float2(a.y, b.y);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < NL; ++k) {
+                const uint32_t* wd = reinterpret_cast<const uint32_t*>(&v[k]);
+#pragma unroll
+                for (int e = 0; e < LV / 2; ++e) f[j][i][k * (LV / 2) + e] = widen<F16>(wd[e]);
+              }
+            }
+            if (NU > 1 && !in[i]) {
+#pragma unroll
+              for (int e = 0; e < VW; ++e) f[j][i][e] = both(0.f);
+            }
+          }
+      };
+      // y = R(z), or dz = R^T dy (the table holds the other way's sines), in place
+      auto turned = [&](float2(&f)[J][NU][VW]) {
+        if (!q.turn) return;
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+          const int pair = (t + i * lanes) * VW;
+          if (pair >= p.pairs) continue;
+          const float4* from = s_turn + i * kTurn * lanes + t;
+          if constexpr (VW == 1) {
+            const float4 c = from[0];  // cos, cos, -sin, sin
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+              const float2 z = f[j][i][0];
+              f[j][i][0] = __ffma2_rn(z, make_float2(c.x, c.y), __fmul2_rn(make_float2(z.y, z.x), make_float2(c.z, c.w)));
+            }
+          } else {
+            // whether pair e of the unit is turned: all are but in the last one of
+            // neighbouring pairs
+            auto there = [&](int e) { return !INTER || pair + e < p.pairs; };
+#pragma unroll
+            for (int c = 0; c < VW / 2; ++c) {
+              float2 cs, sn, ns;
+              if constexpr (VW == 2) {
+                const float4 v = from[0], o = from[lanes];
+                cs = make_float2(v.x, v.y), sn = make_float2(v.z, v.w), ns = make_float2(o.x, o.y);
+              } else {
+                const float4 cv = from[(c / 2) * lanes], sv = from[(VW / 4 + c / 2) * lanes],
+                             nv = from[(2 * (VW / 4) + c / 2) * lanes];
+                cs = c & 1 ? make_float2(cv.z, cv.w) : make_float2(cv.x, cv.y);
+                sn = c & 1 ? make_float2(sv.z, sv.w) : make_float2(sv.x, sv.y);
+                ns = c & 1 ? make_float2(nv.z, nv.w) : make_float2(nv.x, nv.y);
+              }
+#pragma unroll
+              for (int j = 0; j < J; ++j) {
+                const float2 a = f[j][i][c], b = f[j][i][VW / 2 + c];
+                const float2 a1 = __ffma2_rn(a, cs, __fmul2_rn(b, ns)), b1 = __ffma2_rn(a, sn, __fmul2_rn(b, cs));
+                f[j][i][c] = make_float2(there(2 * c) ? a1.x : a.x, there(2 * c + 1) ? a1.y : a.y);
+                f[j][i][VW / 2 + c] = make_float2(there(2 * c) ? b1.x : b.x, there(2 * c + 1) ? b1.y : b.y);
+              }
+            }
+          }
+        }
+      };
+      float2 w[NU][VW];
+      auto read_weights = [&]() {
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+          if constexpr (VW == 1) {
+            w[i][0] = *reinterpret_cast<const float2*>(weights + w_at(i, 0));
+          } else {
+#pragma unroll
+            for (int e = 0; e < VW / 2; ++e) {
+              const float4 v = *reinterpret_cast<const float4*>(weights + w_at(i, 4 * e));
+              w[i][2 * e] = make_float2(v.x, v.y), w[i][2 * e + 1] = make_float2(v.z, v.w);
+            }
+          }
+        }
+      };
+      auto store = [&](const float2(&f)[J][NU][VW]) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          if (j * p.per_warp >= rows_in) continue;
+          uint16_t* to = to0 + j * next_to;
+#pragma unroll
+          for (int i = 0; i < NU; ++i) {
+            if (!in[i]) continue;
+            const float2(&r)[VW] = f[j][i];
+            if constexpr (VW == 1) {
+              to[ca[i]] = static_cast<uint16_t>(pack_x2<F16>(r[0].x, 0.f));
+              to[cb[i]] = static_cast<uint16_t>(pack_x2<F16>(r[0].y, 0.f));
+            } else if constexpr (INTER) {
+              LT v;
+              uint32_t* wd = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+              for (int e = 0; e < VW / 2; ++e) {
+                wd[2 * e] = pack_x2<F16>(r[e].x, r[VW / 2 + e].x);
+                wd[2 * e + 1] = pack_x2<F16>(r[e].y, r[VW / 2 + e].y);
+              }
+              *reinterpret_cast<LT*>(to + ca[i]) = v;
+            } else {
+#pragma unroll
+              for (int k = 0; k < NL; ++k) {
+                LT v;
+                uint32_t* wd = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+                for (int e = 0; e < LV / 2; ++e) wd[e] = pack_x2<F16>(r[k * (LV / 2) + e].x, r[k * (LV / 2) + e].y);
+                *reinterpret_cast<LT*>(to + (k == 0 ? ca[i] : cb[i])) = v;
+              }
+            }
+          }
+        }
+      };
+
+      float2 x[J][NU][VW];
+      if (!BWD || norm) widened(0, x);
+      if constexpr (!BWD) {
+        if (norm) {
+          float ss[J];
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            float2 s2 = both(0.f);
+#pragma unroll
+            for (int i = 0; i < NU; ++i)
+#pragma unroll
+              for (int e = 0; e < VW; ++e) s2 = __ffma2_rn(x[j][i][e], x[j][i][e], s2);
+            ss[j] = s2.x + s2.y;
+          }
+          row_sums(ss, t, lanes, first, even);
+          read_weights();
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            const float2 f = both(rsqrtf(fmaf(ss[j], p.inv_d, p.eps)));
+#pragma unroll
+            for (int i = 0; i < NU; ++i)
+#pragma unroll
+              for (int e = 0; e < VW; ++e) x[j][i][e] = __fmul2_rn(x[j][i][e], __fmul2_rn(f, w[i][e]));
+          }
+        }
+        turned(x);
+        store(x);
+      } else {
+        float2 g[J][NU][VW];
+        widened(NU * NL, g);
+        turned(g);
+        if (norm) {
+          read_weights();
+          float sums[2 * J];
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            float2 s2 = both(0.f), g2 = both(0.f);
+#pragma unroll
+            for (int i = 0; i < NU; ++i)
+#pragma unroll
+              for (int e = 0; e < VW; ++e) {
+                s2 = __ffma2_rn(x[j][i][e], x[j][i][e], s2);
+                g2 = __ffma2_rn(__fmul2_rn(g[j][i][e], w[i][e]), x[j][i][e], g2);
+              }
+            sums[2 * j] = s2.x + s2.y, sums[2 * j + 1] = g2.x + g2.y;
+          }
+          row_sums(sums, t, lanes, first, even);
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            const float f = rsqrtf(fmaf(sums[2 * j], p.inv_d, p.eps));
+            const float c = f * f * sums[2 * j + 1] * p.inv_d;  // mean(g ⊙ x·r)·r
+            auto add = [&](float2(&to_acc)[NU][VW]) {
+              if (j * p.per_warp >= rows_in) return;
+#pragma unroll
+              for (int i = 0; i < NU; ++i)
+#pragma unroll
+                for (int e = 0; e < VW; ++e)
+                  to_acc[i][e] = __ffma2_rn(g[j][i][e], __fmul2_rn(x[j][i][e], both(f)), to_acc[i][e]);
+            };
+            if (q.slot == 0) add(acc[0]);
+            else if (q.slot == 1) add(acc[1]);
+#pragma unroll
+            for (int i = 0; i < NU; ++i)
+#pragma unroll
+              for (int e = 0; e < VW; ++e) {
+                const float2 d = __ffma2_rn(g[j][i][e], w[i][e], __fmul2_rn(x[j][i][e], both(-c)));
+                g[j][i][e] = __fmul2_rn(d, both(f));
+              }
+          }
+        }
+        store(g);
+      }
+    };
+    if (left > p.per_warp) work(std::integral_constant<int, kRows>{});
+    else work(std::integral_constant<int, 1>{});
   }
+  copy_wait<0>();
 
   if constexpr (BWD) {
-    if (q.sums == nullptr) return;
-    // the CTA's sum of each channel: rows of the warps, in their order
-    __shared__ float s_acc[kRopeThreads * 16];  // [rows of a pass][D]
+    // the CTA's sum of each channel: the rows of its warps in their order
+    __shared__ float s_acc[RT::kThreads * 16];
+    for (int q = 0; q < p.n_parts; ++q) {
+      const RopePart& part = p.part[q];
+      if (part.sums == nullptr) continue;
+      __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NU; ++i)
+      for (int i = 0; i < NU; ++i)
 #pragma unroll
-      for (int e = 0; e < 2 * VW; ++e)
-        if (mine < per_warp && unit[i].in)
-          s_acc[(warp * per_warp + mine) * p.D +
-                (INTER || e < VW ? unit[i].a + e : unit[i].b + e - VW)] = acc[i][e];
-    __syncthreads();
-    for (int d = tid; d < p.D; d += kRopeThreads) {
-      float s = 0.f;
-      for (int r = 0; r < (kRopeThreads / 32) * per_warp; ++r) s += s_acc[r * p.D + d];
-      q.sums[(int64_t)blockIdx.x * p.D + d] = s;
+        for (int e = 0; e < 2 * VW; ++e)
+          if (in[i]) {
+            const float2 v = part.slot == 0 ? acc[0][i][e / 2] : acc[1][i][e / 2];
+            s_acc[(warp * p.per_warp + mine) * p.D + channel(i, e)] = e & 1 ? v.y : v.x;
+          }
+      __syncthreads();
+      for (int d = tid; d < p.D; d += RT::kThreads) {
+        float s = 0.f;
+        for (int r = 0; r < kWarps * p.per_warp; ++r) s += s_acc[r * p.D + d];
+        part.sums[(int64_t)blockIdx.x * p.D + d] = s;
+      }
     }
   }
 }
@@ -384,44 +617,62 @@ __global__ void __launch_bounds__(1024) rope_dweight_kernel(const __grid_constan
   }
 }
 
-template <bool F16, bool INTER, int VW>
-cudaError_t launch(const RopeParams& p, bool bwd, int ctas, cudaStream_t stream) {
+template <bool F16, bool INTER, int VW, bool BWD>
+cudaError_t launch(const RopeParams& p, int ctas, cudaStream_t stream) {
+  constexpr int kThreads = RopeTile<BWD>::kThreads;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(p.n_parts), 1);
-  cfg.blockDim = dim3(kRopeThreads, 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  // weights of each part, angles of each warp's token
+  constexpr int kTurns = 8 / VW * RopeTurns<VW>::kUnit;  // float4 of a lane
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.n_parts * 4 + kThreads / 32 * kTurns) * p.lanes * 16;
   cfg.stream = stream;
-  return bwd ? cudaLaunchKernelEx(&cfg, rope_kernel<F16, INTER, VW, true>, p)
-             : cudaLaunchKernelEx(&cfg, rope_kernel<F16, INTER, VW, false>, p);
+  auto kern = rope_kernel<F16, INTER, VW, BWD>;
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <bool F16>
-cudaError_t launch_shape(const RopeParams& p, RopeShape s, bool bwd, int ctas, cudaStream_t stream) {
-  if (s.interleaved) return launch<F16, true, 4>(p, bwd, ctas, stream);
+template <bool F16, bool BWD>
+cudaError_t launch_shape(const RopeParams& p, RopeShape s, int ctas, cudaStream_t stream) {
+  if (s.interleaved) return launch<F16, true, 4, BWD>(p, ctas, stream);
   switch (s.width) {
-    case 8: return launch<F16, false, 8>(p, bwd, ctas, stream);
-    case 4: return launch<F16, false, 4>(p, bwd, ctas, stream);
-    case 2: return launch<F16, false, 2>(p, bwd, ctas, stream);
-    case 1: return launch<F16, false, 1>(p, bwd, ctas, stream);
+    case 8: return launch<F16, false, 8, BWD>(p, ctas, stream);
+    case 4: return launch<F16, false, 4, BWD>(p, ctas, stream);
+    case 2: return launch<F16, false, 2, BWD>(p, ctas, stream);
+    case 1: return launch<F16, false, 1, BWD>(p, ctas, stream);
   }
   return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-int rope_bwd_grid(const RopeParams& p, int sms) {
-  const int64_t most = static_cast<int64_t>(sms) * 4;
-  const int64_t all = static_cast<int64_t>(p.blocks) * p.head_split;
-  return static_cast<int>(all < most ? all : most / p.head_split * p.head_split);
+int rope_plan(RopeParams& p, RopeShape shape, bool bwd, int sms) {
+  const int units = p.D / (2 * shape.width), per_lane = 8 / shape.width;
+  p.lanes = (units + per_lane - 1) / per_lane;
+  p.per_warp = 32 / p.lanes;
+  const int warps = bwd ? RopeTile<true>::kThreads / 32 : RopeTile<false>::kThreads / 32;
+  const int resident = sms * warps * (bwd ? RopeTile<true>::kCtas : RopeTile<false>::kCtas);
+  int groups = 0;
+  const int rows = RopeTile<false>::kRows * p.per_warp;  // of a pass
+  for (int i = 0; i < p.n_parts; ++i) groups += (p.part[i].heads + rows - 1) / rows;
+  // few tokens: their rows are dealt to several warps, each of which finds the angles
+  p.log2_split = 0;
+  while (((int64_t)p.N << (p.log2_split + 1)) <= resident && (2 << p.log2_split) <= groups) ++p.log2_split;
+  p.split = 1 << p.log2_split;
+  p.units = p.N << p.log2_split;
+  // every warp the same number of units, as near as it goes
+  const int rounds = (p.units + resident - 1) / resident;
+  const int used = (p.units + rounds - 1) / rounds;
+  return (used + warps - 1) / warps;
 }
 
-cudaError_t rope_fwd_launch(const RopeParams& p, RopeShape shape, bool f16, cudaStream_t stream) {
-  const int ctas = p.blocks * p.head_split;
-  return f16 ? launch_shape<true>(p, shape, false, ctas, stream) : launch_shape<false>(p, shape, false, ctas, stream);
+int rope_most_ctas(int sms) { return sms * RopeTile<true>::kCtas; }
+
+cudaError_t rope_fwd_launch(const RopeParams& p, RopeShape shape, bool f16, int ctas, cudaStream_t stream) {
+  return f16 ? launch_shape<true, false>(p, shape, ctas, stream) : launch_shape<false, false>(p, shape, ctas, stream);
 }
 
-cudaError_t rope_bwd_launch(const RopeParams& p, RopeShape shape, bool f16, int sms, cudaStream_t stream) {
-  const int ctas = rope_bwd_grid(p, sms);
-  cudaError_t e = f16 ? launch_shape<true>(p, shape, true, ctas, stream) : launch_shape<false>(p, shape, true, ctas, stream);
+cudaError_t rope_bwd_launch(const RopeParams& p, RopeShape shape, bool f16, int ctas, cudaStream_t stream) {
+  cudaError_t e = f16 ? launch_shape<true, true>(p, shape, ctas, stream) : launch_shape<false, true>(p, shape, ctas, stream);
   if (e != cudaSuccess) return e;
   bool any = false;
   for (int i = 0; i < p.n_parts; ++i) any = any || p.part[i].sums != nullptr;
