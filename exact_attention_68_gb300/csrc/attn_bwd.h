@@ -7,6 +7,7 @@
 #include <cuda.h>
 #include <cuda_runtime_api.h>
 
+#include "cross_runs.h"
 #include "schedule.h"
 
 namespace ea {
@@ -23,6 +24,7 @@ struct BwdParams {
   CUtensorMap tm_dq;  // dq, box 64 x 32 rows (one warp's rows)
   CUtensorMap tm_dk;  // dk, same
   CUtensorMap tm_dv;  // dv, same
+  CUtensorMap tm_out; // out, box 64 x 128 rows (cross-attention's dq kernel)
   // 256-column kernels only (head dimension above 128): boxes of 64 columns x
   // 64 rows, for the 64-key (K, V) and 64-query (Q, dout) steps
   CUtensorMap tm_q64;
@@ -54,17 +56,21 @@ struct BwdParams {
   int Sk;               // keys of a slice: k, v, dk, dv are (D, Sk, BH)
   const int* lens;      // [BH / heads] keys that are there; null: all Sk
   int heads;            // key heads of one sequence
+  int sms;              // of the device
   int n_qt, n_kt;       // ceil(S / 128), ceil(Sk / 128)
   int q_split;          // runs of K/V tiles that a Q tile's dq is summed over
-  int kv_split;         // runs of Q tiles that a K/V tile's dk, dv are summed over
+  KvRuns kv;            // the runs of Q tiles that a K/V tile's dk, dv are summed over
   float* part_dq;       // [q_split, BH, S, d_cols] if q_split > 1: each run's sum, unscaled
-  float* part_dk;       // [kv_split, BH, Sk, d_cols] if kv_split > 1: the same of dk and dv
+  float* part_dk;       // [runs, BH, Sk, d_cols] if there are several: the same of dk and dv
   float* part_dv;
 };
 
 // Launches the dq kernel (which also writes delta) and then the dk/dv kernel
 // on `stream`.  f16: the 16-bit tensors are fp16 (else bf16).
-cudaError_t bwd_launch(const BwdParams& p, int D, int mask, bool f16, cudaStream_t stream);
+cudaError_t bwd_launch(const BwdParams& p, int D, bool causal, bool f16, cudaStream_t stream);
+
+// Cross-attention's dq and dk/dv kernels for head dimensions up to 128.
+cudaError_t cross_bwd_launch(const BwdParams& p, int D, bool f16, cudaStream_t stream);
 
 // The same for head dimensions above 128 (kernels 256 columns wide): the dq
 // kernel, then the dk/dv kernel with one CTA per K/V tile and half of the

@@ -467,16 +467,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_q64_kernel(const
   int bh, j;      // slice and K/V tile
   int u0, n_sub;  // first 64-query tile that sees it, and how many
   int keys;       // rows of the slice's keys that are there
+  int runs = 1;   // that the sums are cut into
   BwdUnit un{};
   if constexpr (CROSS) {
-    un = cross_kv_unit<kStepW>(p, unit);
+    // the key tiles without keys are zeroed by all; what is left has a CTA each
+    cross_zero_tiles(p, unit, static_cast<int>(gridDim.x >> 1), threadIdx.x, kBwdThreads, kCols * half, kCols);
+    runs = cross_kv_runs(p.kv, p.lens);
+    KvWalk walk = kv_walk(unit, runs);
+    if (!cross_kv_unit<kStepW>(p, walk, &un)) return;
     bh = un.bh, j = un.tile, u0 = un.first, n_sub = un.n, keys = un.len;
-    if (j * kRowsW >= keys) {
-      if (un.part == 0)
-        cross_no_keys(p.dk, p.dv, (int64_t)bh * p.Sk + j * kRowsW, min(kRowsW, p.Sk - j * kRowsW),
-                      p.d_cols, kCols * half, kCols, kBwdThreads);
-      return;
-    }
   } else {
     int level;
     schedule_unit(p.sched, unit, &bh, &level);
@@ -616,7 +615,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_q64_kernel(const
       const uint32_t stage = sb + L::kQOff + g * (kCols / 64) * kBlk128;
       const CUtensorMap* map = g == 0 ? &p.tm_dv : &p.tm_dk;
       const float mul = g == 0 ? 1.f : p.scale;
-      if (CROSS && p.kv_split > 1) {  // this run's sum, to be added to the others
+      if (CROSS && runs > 1) {  // this run's sum, to be added to the others
         float* to = (g == 0 ? p.part_dv : p.part_dk) +
                     (((int64_t)un.part * p.BH + bh) * p.Sk + gk) * p.d_cols;
 #pragma unroll 1
@@ -787,7 +786,7 @@ cudaError_t dkdv_q64_launch(const BwdParams& p, cudaStream_t stream) {
   auto kkv = attn_bwd_dkdv_q64_kernel<D, MASK, F16>;
   cudaError_t e = cudaFuncSetAttribute(kkv, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
   if (e != cudaSuccess) return e;
-  const long long units = MASK == kMaskCross ? (long long)p.n_kt * p.kv_split : p.n_t;
+  const long long units = MASK == kMaskCross ? (long long)p.n_kt * p.kv.most_runs : p.n_t;
   cudaLaunchConfig_t cfg = {};
   // with the head dimension split, two CTAs (column halves) per K/V tile
   cfg.gridDim = dim3(static_cast<unsigned>((L::kSplit ? 2ll : 1ll) * p.BH * units), 1, 1);

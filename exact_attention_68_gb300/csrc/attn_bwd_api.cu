@@ -106,7 +106,7 @@ attn_status_t attn_bwd_ex(const void* q, const void* k, const void* v, const voi
   // count (zeros read past it, those columns never stored)
   const int mask = causal != 0 ? ea::kMaskCausal : ea::kMaskFull;
   const cudaError_t e = width == 256 ? ea::bwd256_launch(p, mask, f16, stream)
-                                     : ea::bwd_launch(p, width, mask, f16, stream);
+                                     : ea::bwd_launch(p, width, causal != 0, f16, stream);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return ea::cuda_failure(static_cast<int>(e));

@@ -58,7 +58,6 @@
 
 #include "attn_bwd.h"
 #include "bwd_common.cuh"
-#include "cross_common.cuh"
 #include "ptx.cuh"
 #include "umma.cuh"
 
@@ -114,10 +113,9 @@ struct DqLayout {
   static_assert(kDoCol + D / 2 <= kTmemCols, "TMEM budget exceeded");
 };
 
-template <int D, int MASK, bool F16>
+template <int D, bool CAUSAL, bool F16>
 __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dq_kernel(const __grid_constant__ BwdParams p) {
   using L = DqLayout<D>;
-  constexpr bool CAUSAL = MASK == kMaskCausal, CROSS = MASK == kMaskCross;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sb = (smem_u32(smem_raw) + 1023u) & ~1023u;
   auto bar = [sb](int idx) -> uint32_t { return sb + L::kBarOff + 8u * idx; };
@@ -130,17 +128,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dq_kernel(const __gri
   // heavy tiles by L2-sized groups of heads, then the light ones over all heads
   const DbgBounds dbb{p.status, sb, smem_u32(smem_raw) + static_cast<uint32_t>(L::kAlloc), p.S,
                       p.d_cols, p.BH};
-  const DbgBounds dbk = key_bounds<MASK>(dbb, p.Sk);
   int bh, i;
-  BwdUnit un{};
-  if constexpr (CROSS) {
-    un = cross_dq_unit<kTileRows>(p, static_cast<int>(blockIdx.x));
-    bh = un.bh, i = un.tile;
-  } else {
-    schedule_unit(p.sched, static_cast<int>(blockIdx.x), &bh, &i);
-  }
-  const int j0 = CROSS ? un.first : 0;
-  const int nkv = CROSS ? un.n : CAUSAL ? i + 1 : p.n_t;
+  schedule_unit(p.sched, static_cast<int>(blockIdx.x), &bh, &i);
+  const int nkv = CAUSAL ? i + 1 : p.n_t;
 
   if (threadIdx.x == 0) {
     mbar_init(bar(L::kQFull), 256);
@@ -229,7 +219,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dq_kernel(const __gri
     const float delta = ld_shared_f32(sb + L::kPartOff + 4 * row) +
                         ld_shared_f32(sb + L::kPartOff + 4 * (kTileRows + row));
     const bool row_ok = valid && dbg_row(dbb, bh, grow, 0, 0, kChkRowLoad);
-    if (g == 0 && row_ok && (!CROSS || un.part == 0)) p.delta[(int64_t)bh * p.S + grow] = delta;
+    if (g == 0 && row_ok) p.delta[(int64_t)bh * p.S + grow] = delta;
     const float lse2 = row_ok ? p.lse[(int64_t)bh * p.S + grow] * kLog2e : 0.f;
     const float sl2 = p.scale_log2;
 
@@ -254,8 +244,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dq_kernel(const __gri
       reg_fence(dp[0]);
       reg_fence(dp[1]);
       // allowed key columns of this half: 0 .. lim (causal: key <= query; key < S)
-      const int c0 = (j0 + j) * kTileRows + 64 * g;
-      int lim = (CROSS ? un.len : p.S) - 1 - c0;
+      const int c0 = j * kTileRows + 64 * g;
+      int lim = p.S - 1 - c0;
       if (CAUSAL) lim = min(lim, grow - c0);
       if (!valid) lim = -1;
       const bool edge = lim < 63;
@@ -276,11 +266,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dq_kernel(const __gri
         }
         const float2 dd = __fadd2_rn(make_float2(__uint_as_float(dp[h][e]), __uint_as_float(dp[h][e + 1])),
                                      make_float2(-delta, -delta));
-        float2 ds = __fmul2_rn(make_float2(p0, p1), dd);
-        if (CROSS && edge) {  // a key that is not there may make dP anything
-          if (2 * e2 > lim) ds.x = 0.f;
-          if (2 * e2 + 1 > lim) ds.y = 0.f;
-        }
+        const float2 ds = __fmul2_rn(make_float2(p0, p1), dd);
         pk[e2] = pack_x2<F16>(ds.x, ds.y);
       }
       tmem_st_32x32b_x32(tS, pk);
@@ -294,12 +280,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dq_kernel(const __gri
     if (ok) {
       ok = __all_sync(0xffffffffu, wait_bounded(bar(L::kOFull), 0, ctl, kSiteDqElemO));
     }
-    if (CROSS && ok && p.q_split > 1) {  // this run's sum, to be added to the others
-      tc_fence_after_sync();
-      const int64_t at = (((int64_t)un.part * p.BH + bh) * p.S + grow) * p.d_cols;
-      for (int c = 2 * g; c < 2 * L::kChunks; c += (c & 1) ? 3 : 1)
-        store_part(tQ + c * 32, p.part_dq + at, c * 32, 1.f, valid, dbb, bh, grow, kChkStore);
-    } else if (ok) {
+    if (ok) {
       tc_fence_after_sync();
       for (int c = g; c < L::kChunks; c += 2)
         store_chunk<F16>(tQ + c * 64, sb + L::kKOff + c * kChunkBytes, row, p.scale, &p.tm_dq, c * 64,
@@ -330,8 +311,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dq_kernel(const __gri
           // a skipped copy leaves the stage's transaction count short: the
           // consumer's bounded wait then ends the kernel
           const uint32_t dst = sb + L::kKOff + ks * L::kTile + c * kChunkBytes;
-          if (dbg_tma(dbk, dst, kChunkBytes, c * 64, (j0 + j) * kTileRows, bh, false, kChkLoadA))
-            tma_load_3d(dst, &p.tm_k, bar(L::kKFull + ks), c * 64, (j0 + j) * kTileRows, bh, pol_kv);
+          if (dbg_tma(dbb, dst, kChunkBytes, c * 64, j * kTileRows, bh, false, kChkLoadA))
+            tma_load_3d(dst, &p.tm_k, bar(L::kKFull + ks), c * 64, j * kTileRows, bh, pol_kv);
         }
         k_issued = j + 1;
         const int vs = j % L::kVStages;
@@ -342,8 +323,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dq_kernel(const __gri
 #pragma unroll
         for (int c = 0; c < L::kChunks; ++c) {
           const uint32_t dst = sb + L::kVOff + vs * L::kTile + c * kChunkBytes;
-          if (dbg_tma(dbk, dst, kChunkBytes, c * 64, (j0 + j) * kTileRows, bh, false, kChkLoadB))
-            tma_load_3d(dst, &p.tm_v, bar(L::kVFull + vs), c * 64, (j0 + j) * kTileRows, bh, pol_kv);
+          if (dbg_tma(dbb, dst, kChunkBytes, c * 64, j * kTileRows, bh, false, kChkLoadB))
+            tma_load_3d(dst, &p.tm_v, bar(L::kVFull + vs), c * 64, j * kTileRows, bh, pol_kv);
         }
         v_issued = j + 1;
       }
@@ -413,9 +394,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dq_kernel(const __gri
                          kSiteDqMmaKV | (j & 0x7f));
       if (r) r = wait_warp(bar(L::kVFull + j % L::kVStages), (j / L::kVStages) & 1,
                            kSiteDqMmaKV | 0x80 | (j & 0x7f));
-      if (CROSS && r)  // dQ's product multiplies dS = 0 by the rows of K behind the end
-        clear_tail<L::kChunks>(sb + L::kKOff + (j % L::kKStages) * L::kTile, kTileRows,
-                               un.len - (j0 + j) * kTileRows, un.len < p.Sk, lane, dbb, kChkMmaA);
       return r;
     };
 
@@ -515,10 +493,9 @@ struct KvLayout {
   static_assert(2 * kTile <= kStages * kTile, "dK/dV staging must fit the Q ring");
 };
 
-template <int D, int MASK, bool F16>
+template <int D, bool CAUSAL, bool F16>
 __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
   using L = KvLayout<D>;
-  constexpr bool CAUSAL = MASK == kMaskCausal, CROSS = MASK == kMaskCross;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sb = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint8_t* smem_gen = smem_raw + (sb - smem_u32(smem_raw));  // same window, generic
@@ -532,27 +509,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_kernel(const __g
   // so its schedule level is n_t - 1 - j (grid order as in the dq kernel)
   const DbgBounds dbb{p.status, sb, smem_u32(smem_raw) + static_cast<uint32_t>(L::kAlloc), p.S,
                       p.d_cols, p.BH};
-  int bh, j, i0, nq;
-  int keys;  // rows of the slice's keys that are there
-  BwdUnit un{};
-  if constexpr (CROSS) {
-    un = cross_kv_unit<kTileRows>(p, static_cast<int>(blockIdx.x));
-    bh = un.bh, j = un.tile, i0 = un.first, nq = un.n, keys = un.len;
-    if (j * kTileRows >= keys) {
-      if (un.part == 0)
-        cross_no_keys(p.dk, p.dv, (int64_t)bh * p.Sk + j * kTileRows, min(kTileRows, p.Sk - j * kTileRows),
-                      p.d_cols, 0, D, kBwdThreads);
-      return;
-    }
-  } else {
-    int level;
-    schedule_unit(p.sched, static_cast<int>(blockIdx.x), &bh, &level);
-    j = p.n_t - 1 - level;
-    i0 = CAUSAL ? j : 0;
-    nq = p.n_t - i0;
-    keys = p.S;
-  }
-  const DbgBounds dbk = key_bounds<MASK>(dbb, p.Sk);
+  int bh, level;
+  schedule_unit(p.sched, static_cast<int>(blockIdx.x), &bh, &level);
+  const int j = p.n_t - 1 - level;
+  const int i0 = CAUSAL ? j : 0;
+  const int nq = p.n_t - i0;
   const int n_sub = 4 * nq;  // quarter sub-steps
 
   if (threadIdx.x == 0) {
@@ -596,14 +557,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_kernel(const __g
       // this row's K and V, half of D per warpgroup, into TMEM (rows past the end: 0)
       constexpr int kU = D / 16;  // 16-byte groups in half a row
       uint32_t kw[4 * kU], vw[4 * kU];
-      if (gk < keys) {
+      if (gk < p.S) {
         // columns past d_cols hold zero
-        const int64_t base = ((int64_t)bh * (CROSS ? p.Sk : p.S) + gk) * p.d_cols + g * (D / 2);
+        const int64_t base = ((int64_t)bh * p.S + gk) * p.d_cols + g * (D / 2);
         const int lim = p.d_cols - g * (D / 2);
         const uint4 z = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-          const bool in = 8 * u < lim && dbg_row(dbk, bh, gk, g * (D / 2) + 8 * u, 8, kChkRowLoad);
+          const bool in = 8 * u < lim && dbg_row(dbb, bh, gk, g * (D / 2) + 8 * u, 8, kChkRowLoad);
           const uint4 kv = in ? __ldg(reinterpret_cast<const uint4*>(p.k + base) + u) : z;
           const uint4 vv = in ? __ldg(reinterpret_cast<const uint4*>(p.v + base) + u) : z;
           kw[4 * u] = kv.x, kw[4 * u + 1] = kv.y, kw[4 * u + 2] = kv.z, kw[4 * u + 3] = kv.w;
@@ -648,7 +609,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_kernel(const __g
       const int c0 = i * kTileRows + 32 * q;
       const int hi = p.S - 1 - c0;
       int lo = CAUSAL ? gk - c0 : 0;
-      if (gk >= keys) lo = 32;  // key row past the end: nothing
+      if (gk >= p.S) lo = 32;  // key row past the end: nothing
       const bool edge = lo > 0 || hi < 31;
       // (−lse·log2e, −delta) of this quarter's 32 query columns, two columns per load
       const float4* stat = reinterpret_cast<const float4*>(
@@ -685,10 +646,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_kernel(const __g
           ds0 = p0 * (__uint_as_float(dp[c]) + sd.y);
           ds1 = p1 * (__uint_as_float(dp[c + 1]) + sd.w);
         }
-        if (CROSS && edge) {  // a query behind the last: nothing, whatever dP is
-          if (c < lo || c > hi) ds0 = 0.f;
-          if (c + 1 < lo || c + 1 > hi) ds1 = 0.f;
-        }
         ppk[e2] = pack_x2<F16>(p0, p1);
         dpk[e2] = pack_x2<F16>(ds0, ds1);
       }
@@ -710,21 +667,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_kernel(const __g
       const uint32_t stage = sb + L::kQOff + g * L::kTile;
       const CUtensorMap* map = g == 0 ? &p.tm_dv : &p.tm_dk;
       const float mul = g == 0 ? 1.f : p.scale;
-      if (CROSS && p.kv_split > 1) {  // this run's sum, to be added to the others
-        float* to = (g == 0 ? p.part_dv : p.part_dk) +
-                    (((int64_t)un.part * p.BH + bh) * p.Sk + gk) * p.d_cols;
-#pragma unroll 1
-        for (int c = 0; c < 2 * L::kChunks; ++c)
-          store_part(tAcc + c * 32, to, c * 32, 1.f, gk < keys, dbk, bh, gk, kChkStore);
-      } else {
 #pragma unroll
-        for (int c = 0; c < L::kChunks; ++c)
-          store_chunk<F16>(tAcc + c * 64, stage + c * kChunkBytes, r, mul, map, c * 64, j * kTileRows,
-                           bh, wq, lane, dbk, CROSS && gk >= keys);
-        if (lane == 0) {
-          tma_store_commit();
-          tma_store_wait_all();
-        }
+      for (int c = 0; c < L::kChunks; ++c)
+        store_chunk<F16>(tAcc + c * 64, stage + c * kChunkBytes, r, mul, map, c * 64, j * kTileRows,
+                         bh, wq, lane, dbb);
+      if (lane == 0) {
+        tma_store_commit();
+        tma_store_wait_all();
       }
     }
     tc_fence_before_sync();
@@ -878,11 +827,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_kernel(const __g
   }
 }
 
-template <int D, int MASK, bool F16>
+template <int D, bool CAUSAL, bool F16>
 cudaError_t launch_impl(const BwdParams& p, cudaStream_t stream) {
-  constexpr bool CROSS = MASK == kMaskCross;
-  auto kdq = attn_bwd_dq_kernel<D, MASK, F16>;
-  auto kkv = attn_bwd_dkdv_kernel<D, MASK, F16>;
+  auto kdq = attn_bwd_dq_kernel<D, CAUSAL, F16>;
+  auto kkv = attn_bwd_dkdv_kernel<D, CAUSAL, F16>;
   cudaError_t e = cudaFuncSetAttribute(kdq, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        DqLayout<D>::kAlloc);
   if (e != cudaSuccess) return e;
@@ -890,35 +838,28 @@ cudaError_t launch_impl(const BwdParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // cudaLaunchKernelEx reports this launch's own status (no reliance on the
   // thread's last-error state, which other code on the thread may have set)
-  const long long dq_units = CROSS ? (long long)p.n_qt * p.q_split : p.n_t;
-  const long long kv_units = CROSS ? (long long)p.n_kt * p.kv_split : p.n_t;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.BH * dq_units), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>((long long)p.BH * p.n_t), 1, 1);
   cfg.blockDim = dim3(kBwdThreads, 1, 1);
   cfg.stream = stream;
   cfg.dynamicSmemBytes = DqLayout<D>::kAlloc;
   e = cudaLaunchKernelEx(&cfg, kdq, p);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(p.BH * kv_units), 1, 1);
   cfg.dynamicSmemBytes = KvLayout<D>::kAlloc;
   return cudaLaunchKernelEx(&cfg, kkv, p);
 }
 
-template <int D, bool F16>
-cudaError_t launch_masked(const BwdParams& p, int mask, cudaStream_t stream) {
-  switch (mask) {
-    case kMaskFull: return launch_impl<D, kMaskFull, F16>(p, stream);
-    case kMaskCausal: return launch_impl<D, kMaskCausal, F16>(p, stream);
-    case kMaskCross: return launch_impl<D, kMaskCross, F16>(p, stream);
-  }
-  return cudaErrorInvalidValue;
+template <bool F16>
+cudaError_t launch_typed(const BwdParams& p, int D, bool causal, cudaStream_t stream) {
+  if (D == 64)
+    return causal ? launch_impl<64, true, F16>(p, stream) : launch_impl<64, false, F16>(p, stream);
+  return causal ? launch_impl<128, true, F16>(p, stream) : launch_impl<128, false, F16>(p, stream);
 }
 
 }  // namespace
 
-cudaError_t bwd_launch(const BwdParams& p, int D, int mask, bool f16, cudaStream_t stream) {
-  if (D == 64) return f16 ? launch_masked<64, true>(p, mask, stream) : launch_masked<64, false>(p, mask, stream);
-  return f16 ? launch_masked<128, true>(p, mask, stream) : launch_masked<128, false>(p, mask, stream);
+cudaError_t bwd_launch(const BwdParams& p, int D, bool causal, bool f16, cudaStream_t stream) {
+  return f16 ? launch_typed<true>(p, D, causal, stream) : launch_typed<false>(p, D, causal, stream);
 }
 
 }  // namespace ea

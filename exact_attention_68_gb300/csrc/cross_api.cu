@@ -108,21 +108,30 @@ FwdPlan plan_fwd(const Sizes& s, int sms) {
 }
 
 struct BwdPlan {
-  int width, n_qt, n_kt, q_split, kv_split;
+  int width, n_qt, n_kt, q_split;
+  ea::KvRuns kv;
   size_t dq_space, dk_space, space;  // dk_space: of dk and of dv each
 };
-BwdPlan plan_bwd(const Sizes& s, int sms) {
+BwdPlan plan_bwd(const attn_cross_t& c, const Sizes& s, int sms) {
   BwdPlan b;
   b.width = ea::kernel_head_dim(s.D);
   const int step = b.width == 256 ? 64 : 128;  // keys, or queries, of a step
   b.n_qt = static_cast<int>((s.rows + 127) / 128);
   b.n_kt = static_cast<int>((s.Sk + 127) / 128);
-  const double us = b.width == 64 ? 0.9 : b.width == 128 ? 1.2 : 1.4;
+  const double us = b.width == 64 ? 1.0 : 1.4;
   b.q_split = runs_of(s.BH * b.n_qt, (s.Sk + step - 1) / step, sms, us, 4.0, static_cast<double>(s.BH) * s.rows * s.D * 4);
-  b.kv_split = runs_of(s.BH * b.n_kt * (b.width == 256 ? 2 : 1), (s.rows + step - 1) / step, sms, us * 1.2, 4.0,
-                       static_cast<double>(s.BH) * s.Sk * s.D * 8);
+  std::memset(&b.kv, 0, sizeof(b.kv));
+  b.kv.batch = static_cast<int>(c.batch), b.kv.heads = static_cast<int>(c.heads), b.kv.Sk = static_cast<int>(s.Sk);
+  b.kv.q_steps = static_cast<int>((s.rows + step - 1) / step);
+  b.kv.ctas = b.width == 256 ? 2 : 1;
+  b.kv.sms = sms;
+  b.kv.step_us = b.width == 64 ? 1.2f : b.width == 128 ? 1.9f : 1.7f;
+  b.kv.run_us = static_cast<float>(128.0 * s.D * 8 * 2 / 5e6);
+  // runs are of use where there may be fewer key tiles than SMs, or not many more
+  const bool few = s.BH * b.n_kt * b.kv.ctas < 4 * sms;
+  b.kv.most_runs = !few ? 1 : b.kv.q_steps < 8 ? b.kv.q_steps : 8;
   b.dq_space = b.q_split > 1 ? static_cast<size_t>(b.q_split) * s.BH * s.rows * s.D * 4 : 0;
-  b.dk_space = b.kv_split > 1 ? static_cast<size_t>(b.kv_split) * s.BH * s.Sk * s.D * 4 : 0;
+  b.dk_space = b.kv.most_runs > 1 ? static_cast<size_t>(b.kv.most_runs) * s.BH * s.Sk * s.D * 4 : 0;
   b.space = b.dq_space + 2 * b.dk_space;
   if (b.space < kNoSpace) b.space = kNoSpace;
   return b;
@@ -155,7 +164,7 @@ size_t attn_cross_bwd_workspace(const attn_cross_t* sizes) {
   Sizes s;
   if (check_sizes(sizes, &s) != ATTN_OK) return 0;
   const int sms = sm_count();
-  return sms ? plan_bwd(s, sms).space : 0;
+  return sms ? plan_bwd(*sizes, s, sms).space : 0;
 }
 
 attn_status_t attn_cross_fwd(const attn_cross_t* sizes, const void* q, const void* k, const void* v,
@@ -242,7 +251,8 @@ attn_status_t attn_cross_bwd(const attn_cross_t* sizes, const void* q, const voi
   int* status = nullptr;
   st = ea::current_status_words(&status);
   if (st != ATTN_OK) return st;
-  const BwdPlan b = plan_bwd(s, sm_count());
+  const int sms = sm_count();
+  const BwdPlan b = plan_bwd(*sizes, s, sms);
   st = check_space(workspace, workspace_bytes, b.space);
   if (st != ATTN_OK) return st;
 
@@ -253,7 +263,7 @@ attn_status_t attn_cross_bwd(const attn_cross_t* sizes, const void* q, const voi
     return ea::encode_bhsd_16bit(m, t, s.BH, n, s.D, box, f16);
   };
   if (!map(&p.tm_q, q, s.rows, 128) || !map(&p.tm_k, k, s.Sk, 128) || !map(&p.tm_v, v, s.Sk, 128) ||
-      !map(&p.tm_do, dout, s.rows, 128) || !map(&p.tm_dq, dq, s.rows, 32) || !map(&p.tm_dk, dk, s.Sk, 32) ||
+      !map(&p.tm_do, dout, s.rows, 128) || !map(&p.tm_out, out, s.rows, 128) || !map(&p.tm_dq, dq, s.rows, 32) || !map(&p.tm_dk, dk, s.Sk, 32) ||
       !map(&p.tm_dv, dv, s.Sk, 32))
     return ea::cuda_failure(ea::kErrTensorMap);
   if (b.width == 256 && (!map(&p.tm_q64, q, s.rows, 64) || !map(&p.tm_k64, k, s.Sk, 64) ||
@@ -278,13 +288,14 @@ attn_status_t attn_cross_bwd(const attn_cross_t* sizes, const void* q, const voi
   p.Sk = static_cast<int>(s.Sk);
   p.lens = lens;
   p.heads = static_cast<int>(sizes->heads);
+  p.sms = sms;
   p.n_qt = b.n_qt, p.n_kt = b.n_kt;
-  p.q_split = b.q_split, p.kv_split = b.kv_split;
+  p.q_split = b.q_split, p.kv = b.kv;
   p.part_dq = static_cast<float*>(workspace);
   p.part_dk = p.part_dq + b.dq_space / 4;
   p.part_dv = p.part_dk + b.dk_space / 4;
   cudaError_t e = b.width == 256 ? ea::bwd256_launch(p, ea::kMaskCross, f16, stream)
-                                 : ea::bwd_launch(p, b.width, ea::kMaskCross, f16, stream);
+                                 : ea::cross_bwd_launch(p, b.width, f16, stream);
   ea::JoinSumParams j[2];
   std::memset(j, 0, sizeof(j));
   if (e == cudaSuccess && b.q_split > 1) {
@@ -292,12 +303,12 @@ attn_status_t attn_cross_bwd(const attn_cross_t* sizes, const void* q, const voi
     j[0].rows = s.BH * s.rows, j[0].runs = b.q_split, j[0].D = p.d_cols, j[0].mul = scale;
     e = ea::join_sum_launch(j, 1, f16, stream);
   }
-  if (e == cudaSuccess && b.kv_split > 1) {
+  if (e == cudaSuccess && b.kv.most_runs > 1) {
     for (int i = 0; i < 2; ++i) {
       j[i].part = i == 0 ? p.part_dk : p.part_dv;
       j[i].to = i == 0 ? p.dk : p.dv;
-      j[i].rows = s.BH * s.Sk, j[i].runs = b.kv_split, j[i].D = p.d_cols, j[i].mul = i == 0 ? scale : 1.f;
-      j[i].lens = lens, j[i].heads = p.heads, j[i].Sk = p.Sk;
+      j[i].rows = s.BH * s.Sk, j[i].D = p.d_cols, j[i].mul = i == 0 ? scale : 1.f;
+      j[i].of_keys = true, j[i].kv = b.kv, j[i].lens = lens;
     }
     e = ea::join_sum_launch(j, 2, f16, stream);
   }

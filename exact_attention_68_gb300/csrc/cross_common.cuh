@@ -7,6 +7,7 @@
 
 #include "attn_bwd.h"
 #include "attn_fwd.h"
+#include "cross_runs.cuh"
 #include "ptx.cuh"
 
 namespace ea {
@@ -90,30 +91,53 @@ __device__ __forceinline__ BwdUnit cross_dq_unit(const BwdParams& p, int x) {
   return u;
 }
 
-// dk and dv: runs of Q tiles of ROWS queries, at most as many as there are.
+// dk and dv: runs of Q tiles of ROWS queries, at most as many as there are, of every
+// key tile that has keys.  A CTA's units x, x + gridDim.x, ... are found one after the
+// other, counting on from the sequence the last one was in.
+struct KvWalk {
+  int x, b, before;  // unit asked for; a sequence, and the units of those before it
+  int runs;          // of a key tile's Q tiles
+};
+__device__ __forceinline__ KvWalk kv_walk(int x, int runs) { return {x, 0, 0, runs}; }
+// The unit the walk is at; false: none left.
 template <int ROWS>
-__device__ __forceinline__ BwdUnit cross_kv_unit(const BwdParams& p, int x) {
-  BwdUnit u;
-  const int y = x / p.kv_split;
-  u.part = x - y * p.kv_split;
-  u.bh = y / p.n_kt;
-  u.tile = y - u.bh * p.n_kt;
-  u.len = cross_len(p.lens, u.bh / p.heads, p.Sk, p.status);
+__device__ __forceinline__ bool cross_kv_unit(const BwdParams& p, KvWalk& w, BwdUnit* u) {
+  const int batch = p.BH / p.heads;
+  int tiles = 0;
+  for (;; ++w.b) {
+    if (w.b >= batch) return false;
+    u->len = cross_len(p.lens, w.b, p.Sk, p.status);
+    tiles = (u->len + 127) / 128;
+    const int units = p.heads * tiles * w.runs;
+    if (w.x - w.before < units) break;
+    w.before += units;
+  }
+  const int y = w.x - w.before, z = y / w.runs;
+  u->part = y - z * w.runs;
+  const int h = z / tiles;
+  u->bh = w.b * p.heads + h;
+  u->tile = z - h * tiles;
   int rows = p.S;
-  cross_run(u.part, p.kv_split, ROWS, &rows, &u.first, &u.n);
-  return u;
+  cross_run(u->part, w.runs, ROWS, &rows, &u->first, &u->n);
+  return true;
 }
 
-// The gradient of 128 keys that are not there: dk = dv = 0 (whole CTA of `threads`).
-__device__ __forceinline__ void cross_no_keys(uint16_t* dk, uint16_t* dv, int64_t row0, int rows,
-                                              int d_cols, int first_col, int cols, int threads) {
-  cols = min(cols, d_cols - first_col);
-  if (cols <= 0) return;
+// Zeroes dk and dv of the key tiles without keys (columns first_col .. +cols), dealt to
+// the grid's CTAs: `threads` threads of each, tid this one's number.
+__device__ __forceinline__ void cross_zero_tiles(const BwdParams& p, int cta, int ctas, int tid, int threads,
+                                                 int first_col, int cols) {
+  cols = min(cols, p.d_cols - first_col);
+  if (p.lens == nullptr || cols <= 0) return;
   const int units = cols / 8;
-  for (int c = threadIdx.x; c < rows * units; c += threads) {
-    const int64_t at = (row0 + c / units) * d_cols + first_col + (c % units) * 8;
-    *reinterpret_cast<uint4*>(dk + at) = make_uint4(0u, 0u, 0u, 0u);
-    *reinterpret_cast<uint4*>(dv + at) = make_uint4(0u, 0u, 0u, 0u);
+  for (int x = cta; x < p.BH * p.n_kt; x += ctas) {
+    const int bh = x / p.n_kt, j = x - bh * p.n_kt;
+    if (j * 128 < cross_len(p.lens, bh / p.heads, p.Sk, p.status)) continue;
+    const int64_t row0 = (int64_t)bh * p.Sk + j * 128;
+    for (int c = tid; c < min(128, p.Sk - j * 128) * units; c += threads) {
+      const int64_t at = (row0 + c / units) * p.d_cols + first_col + (c % units) * 8;
+      *reinterpret_cast<uint4*>(p.dk + at) = make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4*>(p.dv + at) = make_uint4(0u, 0u, 0u, 0u);
+    }
   }
 }
 

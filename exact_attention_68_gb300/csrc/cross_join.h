@@ -5,6 +5,8 @@
 #include <cstdint>
 #include <cuda_runtime_api.h>
 
+#include "cross_runs.h"
+
 namespace ea {
 
 constexpr int kMaxRuns = 64;  // of one tile's work
@@ -20,17 +22,19 @@ struct JoinFwdParams {
 };
 cudaError_t join_fwd_launch(const JoinFwdParams& p, bool f16, cudaStream_t stream);
 
-// A gradient's runs: to = mul · Σ part_r.  With keys (lens or Sk): rows are a
-// slice's Sk keys; those behind the sequence's end get 0, and whole tiles of 128
-// of them are left alone.
+// A gradient's runs: to = mul · Σ part_r.  Of keys: rows are a slice's Sk keys, the
+// number of runs is found as the gradient kernel finds it (one: nothing is left to
+// do); those behind the sequence's end get 0, and whole tiles of 128 of them are left
+// alone.
 struct JoinSumParams {
   const float* part;  // [runs, rows, D]
   uint16_t* to;       // [rows, D]
   int64_t rows;
-  int runs, D;
+  int runs, D;      // runs: of queries' gradients
   float mul;
-  const int* lens;  // null: every row is there
-  int heads, Sk;
+  bool of_keys;
+  KvRuns kv;
+  const int* lens;  // null: every key is there
 };
 // n tensors (1 or 2) of the same sizes in one launch.
 cudaError_t join_sum_launch(const JoinSumParams* p, int n, bool f16, cudaStream_t stream);

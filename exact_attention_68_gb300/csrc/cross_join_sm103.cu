@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 
 #include "cross_join.h"
+#include "cross_runs.cuh"
 #include "ptx.cuh"
 
 namespace ea {
@@ -69,6 +70,8 @@ struct JoinSums {
 template <bool F16>
 __global__ void __launch_bounds__(kJoinThreads) join_sum_kernel(const __grid_constant__ JoinSums ps) {
   const JoinSumParams& p = ps.p[blockIdx.y];
+  const int runs = p.of_keys ? cross_kv_runs(p.kv, p.lens) : p.runs;
+  if (p.of_keys && runs == 1) return;
   const int units = p.D / 8;
   const int64_t total = p.rows * units;
   for (int64_t x = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; x < total;
@@ -76,9 +79,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_sum_kernel(const __grid_con
     const int64_t row = x / units;
     bool there = true;
     if (p.lens != nullptr) {
-      const int64_t slice = row / p.Sk;
-      const int key = static_cast<int>(row - slice * p.Sk);
-      const int n = min(max(__ldg(p.lens + slice / p.heads), 0), p.Sk);
+      const int64_t slice = row / p.kv.Sk;
+      const int key = static_cast<int>(row - slice * p.kv.Sk);
+      const int n = min(max(__ldg(p.lens + slice / p.kv.heads), 0), p.kv.Sk);
       if ((key & ~127) >= n) continue;
       there = key < n;
     }
@@ -88,7 +91,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_sum_kernel(const __grid_con
     if (there) {
       const float* from = p.part + x * 8;
 #pragma unroll 4
-      for (int r = 0; r < p.runs; ++r) {
+      for (int r = 0; r < runs; ++r) {
         const float4* f = reinterpret_cast<const float4*>(from + r * p.rows * p.D);
         const float4 a = f[0], b = f[1];
         s[0] += a.x, s[1] += a.y, s[2] += a.z, s[3] += a.w;

@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 import threading
 from typing import NamedTuple, Optional
 
@@ -37,30 +38,22 @@ _NO_SPACE = 16  # the size that says no workspace is needed
 _i64, _p, _f, _i, _sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, ctypes.c_int, ctypes.c_size_t
 
 
-class _Rope(ctypes.Structure):
-    _fields_ = [("inv_freq", _p), ("axis", _p), ("pairs", _i64), ("interleaved", _i)]
+# The C structures as bytes: attn_rope_t, attn_rope_positions_t, attn_rope_part_t
+# (packing costs a third of what ctypes structures do, and a small call is mostly this).
+_pack_rope = struct.Struct("@3qi4x").pack
+_pack_positions = struct.Struct("@5q").pack
+_pack_part = struct.Struct("@6q2i6q").pack
 
-
-class _Positions(ctypes.Structure):
-    _fields_ = [("at", _p), ("stride_b", _i64), ("stride_s", _i64), ("stride_a", _i64), ("axes", _i64)]
-
-
-class _Part(ctypes.Structure):
-    _fields_ = [("x", _p), ("stride_b", _i64), ("stride_s", _i64), ("stride_h", _i64), ("heads", _i64),
-                ("weight", _p), ("weight_f32", _i), ("turn", _i), ("y", _p), ("dx", _p), ("dx_stride_b", _i64),
-                ("dx_stride_s", _i64), ("dx_stride_h", _i64), ("dweight", _p)]
-
-
-_pp, _rp, _ap = ctypes.POINTER(_Part), ctypes.POINTER(_Rope), ctypes.POINTER(_Positions)
+_b = ctypes.c_char_p
 _SIGS = {
-    "attn_rope_fwd": (_i, [_pp, _i, _rp, _ap, _i64, _i64, _i64, _f, _i, _p]),
-    "attn_rope_bwd_workspace": (_sz, [_pp, _i, _i64, _i64, _i64]),
-    "attn_rope_bwd": (_i, [_pp, _i, _rp, _ap, _i64, _i64, _i64, _f, _i, _p, _sz, _p]),
+    "attn_rope_fwd": (_i, [_b, _i, _b, _b, _i64, _i64, _i64, _f, _i, _p]),
+    "attn_rope_bwd_workspace": (_sz, [_b, _i, _i64, _i64, _i64]),
+    "attn_rope_bwd": (_i, [_b, _i, _b, _b, _i64, _i64, _i64, _f, _i, _p, _sz, _p]),
 }
 ROPE_SYMBOLS = tuple(_SIGS)
-_ARRAYS = [None] + [_Part * n for n in range(1, ROPE_MAX_PARTS + 1)]
 
 _DTYPES = {torch.bfloat16: ATTN_BF16, torch.float16: ATTN_F16}
+_f32 = torch.float32
 _lib = None
 _lock = threading.Lock()
 
@@ -105,78 +98,92 @@ def rope_plan(dims, base: float = 10000.0, interleaved: bool = False) -> Rope:
 
 
 def _views(xs, what):
-    """B, S, D, the heads, the device and the dtype code of a call's [B, S, H, D] tensors."""
+    """B, S, D, the device, its index, the dtype and, of each of a call's [B, S, H, D] tensors,
+    (address, strides of batch, token and head, heads)."""
     if not 1 <= len(xs) <= ROPE_MAX_PARTS:
         raise ValueError(f"1 to {ROPE_MAX_PARTS} tensors a call")
-    x0 = xs[0]
-    if not isinstance(x0, torch.Tensor) or x0.dtype not in _DTYPES:
-        raise TypeError(f"{what} must be bfloat16 or float16 tensors")
-    if x0.dim() != 4 or not x0.is_cuda:
-        raise ValueError(f"{what} must be CUDA tensors [B, S, heads, D]")
-    B, S, _, D = x0.shape
-    dt, dev, heads = x0.dtype, x0.device, []
+    try:
+        x0 = xs[0]
+        B, S, _, D = x0.shape
+        dt, at, got = x0.dtype, x0.get_device(), []
+        for x in xs:
+            b, s, h, d = x.shape
+            u, v, w, c = x.stride()
+            if (b != B or s != S or d != D or x.dtype is not dt or x.get_device() != at or (c != 1 and D > 1)):
+                _refuse(xs, what)
+            # a dimension of one entry has no stride to go by
+            got.append((x.data_ptr(), u if B > 1 else 0, v if S > 1 else 0, w if h > 1 else 0, h))
+        if dt not in _DTYPES or at < 0:
+            _refuse(xs, what)
+        return B, S, D, x0.device, at, dt, got
+    except (AttributeError, ValueError):
+        _refuse(xs, what)
+        raise
+
+
+def _refuse(xs, what):
+    """Names what _views found wrong, one tensor after the other."""
     for x in xs:
-        if not isinstance(x, torch.Tensor) or x.dtype != dt:
-            raise TypeError(f"{what} must share a dtype, bfloat16 or float16")
-        shape = x.shape
-        if len(shape) != 4 or shape[0] != B or shape[1] != S or shape[3] != D or x.device != dev:
-            raise ValueError(f"{what} must be [{B}, {S}, heads, {D}] tensors on {dev}")
+        if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES:
+            raise TypeError(f"{what} must be bfloat16 or float16 tensors")
+        if x.dim() != 4 or not x.is_cuda:
+            raise ValueError(f"{what} must be CUDA tensors [B, S, heads, D]")
+    B, S, _, D = xs[0].shape
+    for x in xs:
+        if x.dtype is not xs[0].dtype:
+            raise TypeError(f"{what} must share a dtype")
+        if x.shape[:2] != (B, S) or x.shape[3] != D or x.device != xs[0].device:
+            raise ValueError(f"{what} must be [{B}, {S}, heads, {D}] tensors on {xs[0].device}")
         if D > 1 and x.stride(3) != 1:
             raise ValueError(f"{what} must have adjacent channels")
-        heads.append(shape[2])
-    return B, S, D, heads, dev, dt
 
 
-def _strides(x):
-    """Strides of batch, token and head; a dimension of one entry counts as having none to go by."""
-    (B, S, H, _), (b, s, h, _) = x.shape, x.stride()
-    return (b if B > 1 else 0), (s if S > 1 else 0), (h if H > 1 else 0)
+def _weight(name, w, D, dt, at):
+    """The address of a weight and whether it is float32; (0, 0) without one."""
+    if w is None:
+        return 0, 0
+    if not isinstance(w, torch.Tensor) or (w.dtype is not dt and w.dtype is not _f32):
+        raise TypeError(f"{name} must be tensors of the heads' dtype or float32")
+    if w.shape != (D,) or not w.is_contiguous() or w.get_device() != at:
+        raise ValueError(f"{name} must be contiguous [{D}] tensors on the heads' device")
+    return w.data_ptr(), w.dtype is _f32
 
 
-def _weight(name, w, D, dt, dev):
-    if w.dtype != dt and w.dtype != torch.float32:
-        raise TypeError(f"{name} must have the heads' dtype or be float32")
-    if w.shape != (D,) or not w.is_contiguous() or w.device != dev:
-        raise ValueError(f"{name} must be a contiguous [{D}] tensor on {dev}")
-    return w.data_ptr(), w.dtype == torch.float32
-
-
-def _rope(plan, positions, B, S, dev):
+def _rope(plan, positions, B, S, at):
     """The C structures of a rotation and the tokens' positions [B, S] or [B, S, axes] (either of the first two 1)."""
     if plan is None:
         return None, None
     freq, axis, interleaved = plan
-    if not isinstance(freq, torch.Tensor) or freq.dtype != torch.float64 or freq.dim() != 1 or freq.is_cuda \
+    if not isinstance(freq, torch.Tensor) or freq.dtype is not torch.float64 or freq.dim() != 1 or freq.is_cuda \
             or not freq.is_contiguous():
         raise TypeError("inv_freq must be a contiguous float64 host tensor [pairs]")
-    if axis is not None and (not isinstance(axis, torch.Tensor) or axis.dtype != torch.uint8 or axis.is_cuda
+    if axis is not None and (not isinstance(axis, torch.Tensor) or axis.dtype is not torch.uint8 or axis.is_cuda
                              or axis.shape != freq.shape or not axis.is_contiguous()):
         raise TypeError("axis must be a contiguous uint8 host tensor [pairs]")
-    if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32:
+    if not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int32:
         raise TypeError("positions must be an int32 tensor")
     shape, stride = positions.shape, positions.stride()
     if len(shape) == 2:
         shape, stride = (*shape, 1), (*stride, 0)
-    if len(shape) != 3 or shape[0] not in (1, B) or shape[1] not in (1, S) or positions.device != dev:
-        raise ValueError(f"positions must be [{B}, {S}] or [{B}, {S}, axes] on {dev}")
-    at = _Positions(positions.data_ptr(), stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0,
-                    stride[2] if shape[2] > 1 else 0, shape[2])
-    return _Rope(freq.data_ptr(), None if axis is None else axis.data_ptr(), freq.numel(), interleaved), at
+    if len(shape) != 3 or shape[0] not in (1, B) or shape[1] not in (1, S) or positions.get_device() != at:
+        raise ValueError(f"positions must be [{B}, {S}] or [{B}, {S}, axes] on the heads' device")
+    return (_pack_rope(freq.data_ptr(), 0 if axis is None else axis.data_ptr(), freq.numel(), interleaved),
+            _pack_positions(positions.data_ptr(), stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0,
+                            stride[2] if shape[2] > 1 else 0, shape[2]))
 
 
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _call(name, dev, stream, *args):
-    """The entry point on `stream` (default: the current one) of `dev`."""
-    index = dev.index
+def _call(name, index, stream, *args):
+    """The entry point on `stream` (default: the current one) of device `index`."""
     if stream is not None:
         st = stream.cuda_stream
     elif _raw_stream is not None:
         st = _raw_stream(index)
     else:
-        st = torch.cuda.current_stream(dev).cuda_stream
+        st = torch.cuda.current_stream(index).cuda_stream
     fn = getattr(_lib or _library(), name)
     if index == _current_device():
         rc = fn(*args, st)
@@ -203,12 +210,13 @@ def _per_part(values, n, name):
     return values
 
 
-def _want_rows(name, t, shape, dt, dev):
-    if not isinstance(t, torch.Tensor) or t.dtype != dt:
+def _want_rows(name, t, shape, dt, at):
+    """The address of a contiguous tensor that has to be just so."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dt:
         raise TypeError(f"{name} must be a {dt} tensor")
-    if t.shape != shape or not t.is_contiguous() or t.device != dev:
-        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} on {dev}")
-    return t
+    if t.shape != shape or not t.is_contiguous() or t.get_device() != at:
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} on the heads' device")
+    return t.data_ptr()
 
 
 def rope_fwd(xs, plan, positions=None, weights=None, eps: float = 1e-6, turn=None, ys=None, stream=None):
@@ -217,40 +225,42 @@ def rope_fwd(xs, plan, positions=None, weights=None, eps: float = 1e-6, turn=Non
     weights[i] [D], of the heads' dtype or float32, or None: no norm.  turn[i]
     (default: all) rotates by `plan` and `positions`; without a plan nothing
     turns.  Returns the contiguous [B, H, S, D] tensors (``ys`` if given)."""
-    B, S, D, heads, dev, dt = _views(xs, "xs")
+    B, S, D, dev, at, dt, got = _views(xs, "xs")
     n = len(xs)
     weights, ys = _per_part(weights, n, "weights"), _per_part(ys, n, "ys")
     turn = (plan is not None,) * n if turn is None else _per_part(turn, n, "turn")
-    rope, at = _rope(plan, positions, B, S, dev) if any(turn) else (None, None)
-    parts, out = _ARRAYS[n](), []
-    for i, x in enumerate(xs):
-        y = ys[i]
+    rope, pos = _rope(plan, positions, B, S, at) if any(turn) else (None, None)
+    parts, out = [], []
+    for x, w, y, t in zip(got, weights, ys, turn):
+        shape = (B, x[4], S, D)
         if y is None:
-            y = _new(stream, dev, (B, heads[i], S, D), dt)
+            y = _new(stream, dev, shape, dt)
+            y_p = y.data_ptr()
         else:
-            _want_rows("ys", y, (B, heads[i], S, D), dt, dev)
+            y_p = _want_rows("ys", y, shape, dt, at)
         out.append(y)
-        w, f32 = (None, False) if weights[i] is None else _weight("weights", weights[i], D, dt, dev)
-        parts[i] = _Part(x.data_ptr(), *_strides(x), heads[i], w, f32, bool(turn[i]), y.data_ptr())
-    _call("attn_rope_fwd", dev, stream, parts, n, rope, at, B, S, D, eps, _DTYPES[dt])
+        w_p, f32 = _weight("weights", w, D, dt, at)
+        parts.append(_pack_part(*x, w_p, f32, bool(t), y_p, 0, 0, 0, 0, 0))
+    _call("attn_rope_fwd", at, stream, b"".join(parts), n, rope, pos, B, S, D, eps, _DTYPES[dt])
     return out
 
 
 def rope_bwd_workspace(xs, weights) -> int:
     """Bytes of workspace rope_bwd needs for these sizes (16: none)."""
-    B, S, D, heads, dev, _ = _views(xs, "xs")
-    parts = _ARRAYS[len(xs)]()
-    for i, w in enumerate(_per_part(weights, len(xs), "weights")):
-        parts[i].heads, parts[i].dweight = heads[i], None if w is None else w.data_ptr()
-    return _space(parts, len(xs), B, S, D, dev)
+    B, S, D, _, at, _, got = _views(xs, "xs")
+    return _space(b"".join(_pack_part(*x, 0, 0, 0, 0, 0, 0, 0, 0, 0 if w is None else w.data_ptr())
+                           for x, w in zip(got, _per_part(weights, len(xs), "weights"))), len(xs), B, S, D, at)
 
 
-def _space(parts, n, B, S, D, dev):
-    with torch.cuda.device(dev):
+def _space(parts, n, B, S, D, index):
+    with torch.cuda.device(index):
         size = _library().attn_rope_bwd_workspace(parts, n, B, S, D)
     if size == 0:
         raise AttnError(ATTN_ERR_INVALID_ARG, "attn_rope_bwd_workspace")
     return size
+
+
+_spaces = {}  # bytes by device, channels and how many weights have a gradient: nothing else decides them
 
 
 def rope_bwd(dys, xs, plan, positions=None, weights=None, eps: float = 1e-6, turn=None, dxs=None, dweights=None,
@@ -259,47 +269,48 @@ def rope_bwd(dys, xs, plan, positions=None, weights=None, eps: float = 1e-6, tur
     other arguments.  ``dxs`` may be views of one packed gradient; by default they are
     new contiguous [B, S, H, D] tensors.  Returns (dxs, dweights); dweights[i] is None
     where weights[i] is."""
-    B, S, D, heads, dev, dt = _views(xs, "xs")
+    B, S, D, dev, at, dt, got = _views(xs, "xs")
     n = len(xs)
     if len(dys) != n:
         raise ValueError("dys must have an entry for each tensor")
-    weights, dxs, dweights = (_per_part(v, n, m) for v, m in ((weights, "weights"), (dxs, "dxs"), (dweights, "dweights")))
-    if any(d is not None for d in dxs):
-        if any(d is None for d in dxs) or _views(dxs, "dxs") != (B, S, D, heads, dev, dt):
-            raise ValueError("dxs must be tensors of the shapes, dtype and device of xs")
+    weights, dweights = _per_part(weights, n, "weights"), _per_part(dweights, n, "dweights")
+    if dxs is None:
+        dxs = [_new(stream, dev, x.shape, dt) for x in xs]
+    into = _views(dxs, "dxs")
+    if into[:3] != (B, S, D) or into[4:6] != (at, dt) or [x[4] for x in into[6]] != [x[4] for x in got]:
+        raise ValueError("dxs must be tensors of the shapes, dtype and device of xs")
     turn = (plan is not None,) * n if turn is None else _per_part(turn, n, "turn")
-    rope, at = _rope(plan, positions, B, S, dev) if any(turn) else (None, None)
-    parts, out, grads = _ARRAYS[n](), [], []
-    for i, (x, dy) in enumerate(zip(xs, dys)):
-        _want_rows("dys", dy, (B, heads[i], S, D), dt, dev)
-        dx = dxs[i]
-        if dx is None:
-            dx = _new(stream, dev, x.shape, dt)
-        out.append(dx)
-        w, f32, dw = None, False, None
-        if weights[i] is not None:
-            w, f32 = _weight("weights", weights[i], D, dt, dev)
-            dw = dweights[i]
+    rope, pos = _rope(plan, positions, B, S, at) if any(turn) else (None, None)
+    parts, grads, wanted = [], [], 0
+    for x, d, dy, w, dw, t in zip(got, into[6], dys, weights, dweights, turn):
+        y_p = _want_rows("dys", dy, (B, x[4], S, D), dt, at)
+        w_p, f32 = _weight("weights", w, D, dt, at)
+        dw_p = 0
+        if w is not None:
+            wanted += 1
             if dw is None:
-                dw = _new(stream, dev, (D,), weights[i].dtype)
+                dw = _new(stream, dev, (D,), w.dtype)
+                dw_p = dw.data_ptr()
             else:
-                _want_rows("dweights", dw, (D,), weights[i].dtype, dev)
-        elif dweights[i] is not None:
+                dw_p = _want_rows("dweights", dw, (D,), w.dtype, at)
+        elif dw is not None:
             raise ValueError("dweights without weights")
         grads.append(dw)
-        parts[i] = _Part(x.data_ptr(), *_strides(x), heads[i], w, f32, bool(turn[i]), dy.data_ptr(), dx.data_ptr(),
-                         *_strides(dx), None if dw is None else dw.data_ptr())
-    space, at_ws = 0, None
-    if any(g is not None for g in grads):
+        parts.append(_pack_part(*x, w_p, f32, bool(t), y_p, *d[:4], dw_p))
+    parts, space, space_p = b"".join(parts), 0, None
+    if wanted:
         if workspace is None:
-            workspace = _new(stream, dev, _space(parts, n, B, S, D, dev), torch.uint8)
+            space = _spaces.get((at, D, wanted))
+            if space is None:
+                space = _spaces[at, D, wanted] = _space(parts, n, B, S, D, at)
+            workspace = _new(stream, dev, space, torch.uint8)
         elif not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8:
             raise TypeError("workspace must be a uint8 tensor")
         elif not workspace.is_contiguous() or workspace.device != dev:
             raise ValueError(f"workspace must be contiguous, on {dev}")
-        space, at_ws = workspace.numel(), workspace.data_ptr()
-    _call("attn_rope_bwd", dev, stream, parts, n, rope, at, B, S, D, eps, _DTYPES[dt], at_ws, space)
-    return out, grads
+        space, space_p = workspace.numel(), workspace.data_ptr()
+    _call("attn_rope_bwd", at, stream, parts, n, rope, pos, B, S, D, eps, _DTYPES[dt], space_p, space)
+    return list(dxs), grads
 
 
 class _NormRopeFn(torch.autograd.Function):

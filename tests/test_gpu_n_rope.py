@@ -273,9 +273,9 @@ def test_packed_gradient_into_a_frozen_norm(cuda_device):
     plan, pos = rope.rope_plan(D), torch.arange(S, dtype=torch.int32).cuda()[None]
     want = rope.rope_bwd((dy,), (x,), plan, pos, (w,))[0][0]
     lib, dx = rope._library(), torch.empty_like(x)
-    parts = (rope._Part * 1)(rope._Part(x.data_ptr(), *x.stride()[:3], H, w.data_ptr(), 1, 1, dy.data_ptr(), dx.data_ptr(),
-                                        *dx.stride()[:3], None))
-    r, at = rope._rope(plan, pos, B, S, x.device)
-    assert lib.attn_rope_bwd(parts, 1, r, at, B, S, D, 1e-6, 0, None, 0, torch.cuda.current_stream().cuda_stream) == 0
+    part = rope._pack_part(x.data_ptr(), *x.stride()[:3], H, w.data_ptr(), 1, 1, dy.data_ptr(), dx.data_ptr(),
+                           *dx.stride()[:3], 0)
+    r, at = rope._rope(plan, pos, B, S, 0)
+    assert lib.attn_rope_bwd(part, 1, r, at, B, S, D, 1e-6, 0, None, 0, torch.cuda.current_stream().cuda_stream) == 0
     torch.cuda.synchronize()
     assert torch.equal(dx, want)

@@ -74,13 +74,19 @@ def test_plan():
 A, T = 0x7F0000000000, 1 << 30
 
 
-def _args(n=1, B=2, S=16, D=64, H=4, bwd=False, **over):
-    parts = (rope._Part * max(n, 1))()
+class _Part(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("x", "stride_b", "stride_s", "stride_h", "heads", "weight")] + \
+               [("weight_f32", ctypes.c_int), ("turn", ctypes.c_int)] + \
+               [(n, ctypes.c_int64) for n in ("y", "dx", "dx_stride_b", "dx_stride_s", "dx_stride_h", "dweight")]
+
+
+def _args(n=1, B=2, S=16, D=64, H=4, **over):
+    parts = (_Part * max(n, 1))()
     for i in range(n):
-        parts[i] = rope._Part(A + i * T, S * H * D, H * D, D, H, A + 8 * T + i * 1024, 0, 1, A + (10 + i) * T,
-                              A + (20 + i) * T, S * H * D, H * D, D, A + 9 * T + i * 1024)
+        parts[i] = _Part(A + i * T, S * H * D, H * D, D, H, A + 8 * T + i * 1024, 0, 1, A + (10 + i) * T,
+                         A + (20 + i) * T, S * H * D, H * D, D, A + 9 * T + i * 1024)
     for name, value in over.items():
-        setattr(parts[0], name, value)
+        setattr(parts[0], name, value or 0)
     return parts
 
 
@@ -89,19 +95,27 @@ AXIS = (ctypes.c_uint8 * 32)(*[0] * 32)
 
 
 def _rope_struct(freq=FREQ, axis=AXIS, pairs=32, interleaved=0):
-    return rope._Rope(ctypes.cast(freq, ctypes.c_void_p) if freq else None,
-                      ctypes.cast(axis, ctypes.c_void_p) if axis else None, pairs, interleaved)
+    return rope._pack_rope(ctypes.addressof(freq) if freq else 0, ctypes.addressof(axis) if axis else 0, pairs, interleaved)
 
 
 def _at(at=A + 30 * T, b=16, s=1, a=0, axes=1):
-    return rope._Positions(at, b, s, a, axes)
+    return rope._pack_positions(at, b, s, a, axes)
 
 
 def _call(lib, bwd, parts, n=1, r=None, at=None, B=2, S=16, D=64, eps=1e-6, dtype=0, ws=A + 31 * T, space=1 << 28):
-    r, at = _rope_struct() if r is None else r, _at() if at is None else at
+    r, at, parts = _rope_struct() if r is None else r, _at() if at is None else at, bytes(parts)
     if bwd:
         return lib.attn_rope_bwd(parts, n, r, at, B, S, D, eps, dtype, ws, space, None)
     return lib.attn_rope_fwd(parts, n, r, at, B, S, D, eps, dtype, None)
+
+
+KEEP = []
+
+
+def _array(ctype, value):
+    """32 equal values that outlive the parametrisation."""
+    KEEP.append((ctype * 32)(*[value] * 32))
+    return KEEP[-1]
 
 
 BAD, UNSUP, MIS = binding.ATTN_ERR_INVALID_ARG, binding.ATTN_ERR_UNSUPPORTED, binding.ATTN_ERR_MISALIGNED
@@ -137,9 +151,9 @@ def test_refused_gradients(lib, over, code):
     (dict(dtype=2), BAD),
     (dict(r=_rope_struct(pairs=33)), BAD), (dict(r=_rope_struct(pairs=-1)), BAD), (dict(r=_rope_struct(freq=None)), BAD),
     (dict(r=_rope_struct(interleaved=2)), BAD),
-    (dict(r=_rope_struct(freq=(ctypes.c_double * 32)(*[float("inf")] * 32))), BAD),
-    (dict(r=_rope_struct(freq=(ctypes.c_double * 32)(*[2e6] * 32))), BAD),
-    (dict(r=_rope_struct(axis=(ctypes.c_uint8 * 32)(*[1] * 32))), BAD),
+    (dict(r=_rope_struct(freq=_array(ctypes.c_double, float("inf")))), BAD),
+    (dict(r=_rope_struct(freq=_array(ctypes.c_double, 2e6))), BAD),
+    (dict(r=_rope_struct(axis=_array(ctypes.c_uint8, 1))), BAD),
     (dict(at=_at(at=0)), BAD), (dict(at=_at(at=A + 2)), MIS), (dict(at=_at(axes=0)), BAD), (dict(at=_at(axes=9)), BAD),
     (dict(at=_at(b=-1)), BAD), (dict(at=_at(s=1 << 41)), BAD),
 ])
@@ -160,7 +174,7 @@ def test_refused_overlaps(lib):
     # gradients of a packed projection lie beside one another; shifted by less than a head they do not
     B, S, H, D = 2, 16, 4, 64
     for shift, code in ((H * D, None), (H * D - 8, BAD), (3 * H * D, BAD)):
-        two = _args(2, bwd=True)
+        two = _args(2)
         for i in range(2):
             two[i].dx_stride_b, two[i].dx_stride_s = S * 2 * H * D, 2 * H * D
             two[i].dx = A + 20 * T + i * shift * 2
@@ -170,8 +184,7 @@ def test_refused_overlaps(lib):
 
 
 def test_workspace_sizes_without_weights(lib):
-    parts = _args(1)
-    parts[0].dweight = None
+    parts = bytes(_args(1, dweight=0))
     assert lib.attn_rope_bwd_workspace(parts, 1, 2, 16, 64) == 16
     assert lib.attn_rope_bwd_workspace(parts, 0, 2, 16, 64) == 0
     assert lib.attn_rope_bwd_workspace(parts, 1, 2, 16, 60) == 0
