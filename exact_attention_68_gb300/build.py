@@ -41,7 +41,8 @@ def _sources():
     return [os.path.join(CSRC, f) for f in ("attn_api.cu", "attn_fwd_1q_sm103.cu", "attn_fwd_1qp_sm103.cu",
                                             "attn_noalloc.cu", "attn_bwd_api.cu", "attn_bwd_sm103.cu", "attn_bwd256_sm103.cu",
                                             "cache_api.cu", "cache_fwd_sm103.cu", "cache_pages_sm103.cu", "cache_select_sm103.cu",
-                                            "rope_api.cu", "rope_sm103.cu", "cross_api.cu", "cross_join_sm103.cu", "attn_cross_bwd_sm103.cu")]
+                                            "rope_api.cu", "rope_sm103.cu", "cross_api.cu", "cross_join_sm103.cu", "attn_cross_bwd_sm103.cu",
+                                            "cross_few_sm103.cu")]
 
 
 def _deps():

@@ -14,6 +14,7 @@
 #include "attn_cross.h"
 #include "attn_fwd.h"
 #include "attn_host.h"
+#include "cross_few.h"
 #include "cross_join.h"
 #include "tmap.h"
 
@@ -92,11 +93,32 @@ int runs_of(int64_t units, int64_t steps, int sms, double step_us, double start,
 }
 
 struct FwdPlan {
+  bool few;            // the kernel for few queries
+  int tiles, cluster;  // its 16-row tiles a CTA, CTAs a cluster
   int width, bn, n_qt, n_kt, runs;
   size_t space;
 };
 FwdPlan plan_fwd(const Sizes& s, int sms) {
   FwdPlan f;
+  f.few = s.rows <= ea::kFewRows;
+  if (f.few) {
+    f.width = ea::kernel_head_dim(s.D);
+    f.tiles = s.rows <= 16 || f.width == 256 ? 1 : 2;
+    f.n_qt = static_cast<int>((s.rows + 16 * f.tiles - 1) / (16 * f.tiles));
+    const int64_t slices = s.BH * f.n_qt;
+    // as many CTAs as it takes to fill the SMs, as long as each of a CTA's warps has
+    // chunks of its own: clusters where 8 CTAs a slice suffice, runs where they do not
+    const int64_t want = (2 * sms + slices - 1) / slices, chunks = (s.Sk + 127) / 128;
+    int64_t n = want < chunks ? want : chunks;
+    f.cluster = 1, f.runs = 1;
+    if (n <= 8) {
+      while (f.cluster < n) f.cluster *= 2;
+    } else {
+      f.runs = static_cast<int>(n < ea::kMaxRuns ? n : ea::kMaxRuns);
+    }
+    f.space = f.runs > 1 ? static_cast<size_t>(f.runs) * s.BH * s.rows * (s.D + 1) * 4 : kNoSpace;
+    return f;
+  }
   f.width = ea::forward_head_dim(s.D);
   f.bn = f.width > 128 ? 64 : 128;
   f.n_qt = static_cast<int>((s.rows + ea::kBlockM - 1) / ea::kBlockM);
@@ -190,6 +212,31 @@ attn_status_t attn_cross_fwd(const attn_cross_t* sizes, const void* q, const voi
   if (st != ATTN_OK) return st;
 
   const bool f16 = dtype == ATTN_F16;
+  ea::JoinFwdParams j;
+  float* const part_o = f.runs > 1 ? static_cast<float*>(workspace) : nullptr;
+  float* const part_lse = f.runs > 1 ? part_o + static_cast<int64_t>(f.runs) * s.BH * s.rows * s.D : nullptr;
+  j.part_o = part_o, j.part_lse = part_lse;
+  j.out = static_cast<uint16_t*>(out), j.lse = lse;
+  j.rows = s.BH * s.rows;
+  j.runs = f.runs, j.D = static_cast<int>(s.D);
+  const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  if (f.few) {
+    ea::FewParams p;
+    p.q = static_cast<const uint16_t*>(q);
+    p.k = static_cast<const uint16_t*>(k);
+    p.v = static_cast<const uint16_t*>(v);
+    p.lens = lens;
+    p.out = j.out, p.lse = lse;
+    p.part_o = part_o, p.part_lse = part_lse;
+    p.status = status;
+    p.BH = static_cast<int>(s.BH), p.heads = static_cast<int>(sizes->heads), p.rows = static_cast<int>(s.rows);
+    p.Sk = static_cast<int>(s.Sk), p.D = j.D;
+    p.groups = f.n_qt, p.cluster = f.cluster, p.runs = f.runs;
+    p.scale_log2 = scale_log2;
+    cudaError_t e = ea::cross_few_launch(p, f.width, f.tiles, f16, stream);
+    if (e == cudaSuccess && f.runs > 1) e = ea::join_fwd_launch(j, f16, stream);
+    return launched(e);
+  }
   ea::Fwd1QParams p;
   std::memset(&p, 0, sizeof(p));
   if (!ea::encode_bhsd_16bit(&p.tm_k, k, s.BH, s.Sk, s.D, f.bn, f16) ||
@@ -205,26 +252,16 @@ attn_status_t attn_cross_fwd(const attn_cross_t* sizes, const void* q, const voi
   p.d_cols = static_cast<int>(s.D);
   p.n_qt = f.n_qt;
   p.n_kt = f.n_kt;
-  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.scale_log2 = scale_log2;
   p.timeout_ns = wait_timeout_ns;
   p.Sk = static_cast<int>(s.Sk);
   p.lens = lens;
   p.heads = static_cast<int>(sizes->heads);
   p.n_split = f.runs;
-  if (f.runs > 1) {
-    p.part_o = static_cast<float*>(workspace);
-    p.part_lse = p.part_o + static_cast<int64_t>(f.runs) * s.BH * s.rows * s.D;
-  }
+  p.part_o = part_o, p.part_lse = part_lse;
   cudaError_t e = f.width <= 128 ? ea::fwd1qp_launch(p, f.width, ea::kMaskCross, f16, stream)
                                  : ea::fwd1q_launch(p, f.width, ea::kMaskCross, f16, stream);
-  if (e == cudaSuccess && f.runs > 1) {
-    ea::JoinFwdParams j;
-    j.part_o = p.part_o, j.part_lse = p.part_lse;
-    j.out = static_cast<uint16_t*>(out), j.lse = lse;
-    j.rows = s.BH * s.rows;
-    j.runs = f.runs, j.D = static_cast<int>(s.D);
-    e = ea::join_fwd_launch(j, f16, stream);
-  }
+  if (e == cudaSuccess && f.runs > 1) e = ea::join_fwd_launch(j, f16, stream);
   return launched(e);
 }
 
