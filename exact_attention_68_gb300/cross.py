@@ -17,7 +17,9 @@ one is passed; calls that may run at the same time, and graphs, need one each.  
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
+import struct
 import threading
 
 import torch
@@ -33,11 +35,10 @@ _i64, _p, _f, _i, _u64, _sz = (ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, 
                                ctypes.c_size_t)
 
 
-class _Sizes(ctypes.Structure):
-    _fields_ = [("batch", _i64), ("q_heads", _i64), ("heads", _i64), ("Sq", _i64), ("Sk", _i64), ("head_dim", _i64)]
+# attn_cross_t as bytes: batch, q_heads, heads, Sq, Sk, head_dim
+_pack_sizes = struct.Struct("@6q").pack
 
-
-_s = ctypes.POINTER(_Sizes)
+_s = ctypes.c_char_p
 _SIGS = {
     "attn_cross_fwd_workspace": (_sz, [_s]),
     "attn_cross_fwd": (_i, [_s, _p, _p, _p, _p, _p, _p, _f, _i, _p, _sz, _u64, _p]),
@@ -71,30 +72,45 @@ def _library() -> ctypes.CDLL:
 
 
 def _inputs(q, k, v, lens):
-    """The sizes, the dtype and its code, the device, and the address of lens."""
-    dt = q.dtype if isinstance(q, torch.Tensor) else None
-    code = _DTYPES.get(dt)
-    if code is None:
+    """The sizes packed, q's shape, the dtype and its code, the device and its index, and the address of lens."""
+    try:
+        dt, qs, ks, at = q.dtype, q.shape, k.shape, q.get_device()
+        B, Hq, Sq, D = qs
+        _, Hkv, Sk, _ = ks
+        # everything in one condition: this is much of a small call's time
+        if (at < 0 or dt not in _DTYPES or not q.is_contiguous() or ks[0] != B or ks[3] != D or k.dtype is not dt
+                or not k.is_contiguous() or k.get_device() != at or v.shape != ks or v.dtype is not dt
+                or not v.is_contiguous() or v.get_device() != at or Hkv < 1 or Hq % Hkv):
+            _refuse(q, k, v)
+        lens_p = None
+        if lens is not None:
+            if (lens.dtype is not _i32 or lens.shape != (B,) or not lens.is_contiguous() or lens.get_device() != at):
+                _want("lens", lens, _i32, (B,), q.device)
+            lens_p = lens.data_ptr()
+        return _pack_sizes(B, Hq, Hkv, Sq, Sk, D), qs, dt, _DTYPES[dt], q.device, at, lens_p
+    except (AttributeError, ValueError):
+        _refuse(q, k, v)
+        if lens is not None:
+            _want("lens", lens, _i32, (q.shape[0],), q.device)
+        raise
+
+
+def _refuse(q, k, v):
+    """Names what _inputs found wrong, one tensor after the other."""
+    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES:
         raise TypeError("q must be a bfloat16 or float16 tensor")
     for name, t in (("k", k), ("v", v)):
-        if not isinstance(t, torch.Tensor) or t.dtype != dt:
+        if not isinstance(t, torch.Tensor) or t.dtype is not q.dtype:
             raise TypeError(f"{name} must be a tensor of q's dtype")
-    dev, qs, ks = q.device, q.shape, k.shape
-    if not q.is_cuda or len(qs) != 4 or not q.is_contiguous():
+    if not q.is_cuda or q.dim() != 4 or not q.is_contiguous():
         raise ValueError("q must be a contiguous CUDA tensor [B, Hq, Sq, D]")
-    if (len(ks) != 4 or ks[0] != qs[0] or ks[3] != qs[3] or not k.is_contiguous() or k.device != dev
-            or v.shape != ks or not v.is_contiguous() or v.device != dev):
-        raise ValueError(f"k and v must be contiguous tensors [{qs[0]}, Hkv, Sk, {qs[3]}] on {dev}")
-    if ks[1] < 1 or qs[1] % ks[1]:
+    for name, t in (("k", k), ("v", v)):
+        if (t.dim() != 4 or t.shape[0] != q.shape[0] or t.shape[3] != q.shape[3] or not t.is_contiguous()
+                or t.device != q.device or t.shape != k.shape):
+            raise ValueError(f"{name} must be a contiguous tensor [{q.shape[0]}, Hkv, Sk, {q.shape[3]}] on {q.device}, "
+                             "k and v alike")
+    if k.shape[1] < 1 or q.shape[1] % k.shape[1]:
         raise ValueError("q's heads must be a multiple of k's")
-    at = None
-    if lens is not None:
-        if not isinstance(lens, torch.Tensor) or lens.dtype is not _i32:
-            raise TypeError("lens must be an int32 tensor")
-        if lens.shape != (qs[0],) or not lens.is_contiguous() or lens.device != dev:
-            raise ValueError(f"lens must be a contiguous [{qs[0]}] tensor on {dev}")
-        at = lens.data_ptr()
-    return _Sizes(qs[0], qs[1], ks[1], qs[2], ks[2], qs[3]), dt, code, dev, at
 
 
 def _want(name, t, dtype, shape, dev):
@@ -112,15 +128,14 @@ _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _call(name, dev, stream, *args):
-    """The entry point on `stream` (default: the current one) of `dev`."""
-    index = dev.index
+def _call(name, index, stream, *args):
+    """The entry point on `stream` (default: the current one) of device `index`."""
     if stream is not None:
         st = stream.cuda_stream
     elif _raw_stream is not None:
         st = _raw_stream(index)
     else:
-        st = torch.cuda.current_stream(dev).cuda_stream
+        st = torch.cuda.current_stream(index).cuda_stream
     fn = getattr(_lib or _library(), name)
     if index == _current_device():
         rc = fn(*args, st)
@@ -131,13 +146,12 @@ def _call(name, dev, stream, *args):
         raise AttnError(rc, name)
 
 
-def _size(name, dev, sizes):
+@functools.lru_cache(maxsize=4096)
+def _size(name, index, sizes):
+    """Bytes of workspace: sizes and device alone decide them."""
     fn = getattr(_lib or _library(), name)
-    if dev.index == _current_device():
+    with torch.cuda.device(index):
         n = fn(sizes)
-    else:
-        with torch.cuda.device(dev):
-            n = fn(sizes)
     if n == 0:
         raise AttnError(ATTN_ERR_INVALID_ARG, name)
     return n
@@ -152,10 +166,10 @@ def _new(stream, dev, shape, dtype):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
-def _space(name, workspace, dev, sizes, stream):
-    """Address and bytes of the workspace of a call."""
+def _space(name, workspace, dev, index, sizes, stream):
+    """The workspace of a call, its address and bytes."""
     if workspace is None:
-        need = _size(name, dev, sizes)
+        need = _size(name, index, sizes)
         if need <= _NO_SPACE:
             return None, None, 0
         workspace = _new(stream, dev, need, torch.uint8)
@@ -168,32 +182,31 @@ def _space(name, workspace, dev, sizes, stream):
 
 def cross_fwd_workspace(q, k) -> int:
     """Bytes of workspace cross_fwd needs for these tensors' sizes (16: none)."""
-    sizes, _, _, dev, _ = _inputs(q, k, k, None)
-    return _size("attn_cross_fwd_workspace", dev, sizes)
+    sizes, _, _, _, _, index, _ = _inputs(q, k, k, None)
+    return _size("attn_cross_fwd_workspace", index, sizes)
 
 
 def cross_bwd_workspace(q, k) -> int:
     """Bytes of workspace cross_bwd needs for these tensors' sizes (16: none)."""
-    sizes, _, _, dev, _ = _inputs(q, k, k, None)
-    return _size("attn_cross_bwd_workspace", dev, sizes)
+    sizes, _, _, _, _, index, _ = _inputs(q, k, k, None)
+    return _size("attn_cross_bwd_workspace", index, sizes)
 
 
 def cross_fwd(q, k, v, lens=None, scale=None, out=None, lse=None, workspace=None, stream=None,
               wait_timeout_ns: int | None = None):
     """Attention of q [B, Hq, Sq, D] over the first lens[b] of k, v [B, Hkv, Sk, D].
     Returns (out like q, lse fp32 [B, Hq, Sq]); a sequence without keys gives 0 and -inf."""
-    sizes, dt, code, dev, lens_p = _inputs(q, k, v, lens)
-    shape = q.shape
+    sizes, shape, dt, code, dev, index, lens_p = _inputs(q, k, v, lens)
     if out is None:
-        out = _new(stream, dev, shape, dt)
+        out = torch.empty_like(q) if stream is None else _new(stream, dev, shape, dt)
     else:
         _want("out", out, dt, shape, dev)
     if lse is None:
         lse = _new(stream, dev, shape[:3], _f32)
     else:
         _want("lse", lse, _f32, shape[:3], dev)
-    workspace, at, space = _space("attn_cross_fwd_workspace", workspace, dev, sizes, stream)
-    _call("attn_cross_fwd", dev, stream, sizes, q.data_ptr(), k.data_ptr(), v.data_ptr(), lens_p, out.data_ptr(),
+    workspace, at, space = _space("attn_cross_fwd_workspace", workspace, dev, index, sizes, stream)
+    _call("attn_cross_fwd", index, stream, sizes, q.data_ptr(), k.data_ptr(), v.data_ptr(), lens_p, out.data_ptr(),
           lse.data_ptr(), 1.0 / math.sqrt(shape[3]) if scale is None else float(scale), code, at, space,
           ATTN_DEFAULT_WAIT_TIMEOUT_NS if wait_timeout_ns is None else int(wait_timeout_ns))
     return out, lse
@@ -203,22 +216,32 @@ def cross_bwd(q, k, v, out, lse, dout, lens=None, scale=None, dq=None, dk=None, 
               stream=None, wait_timeout_ns: int | None = None):
     """Gradient of cross_fwd.  Returns (dq like q; dk, dv like k, 0 for keys that are not
     there; delta = rowsum(dout ⊙ out) fp32 [B, Hq, Sq])."""
-    sizes, dt, code, dev, lens_p = _inputs(q, k, v, lens)
-    shape, ks = q.shape, k.shape
+    sizes, shape, dt, code, dev, index, lens_p = _inputs(q, k, v, lens)
+    ks, rows = k.shape, shape[:3]
     out_p, dout_p = _want("out", out, dt, shape, dev), _want("dout", dout, dt, shape, dev)
-    lse_p = _want("lse", lse, _f32, shape[:3], dev)
-    grads = []
-    for name, t, sh, ty in (("dq", dq, shape, dt), ("dk", dk, ks, dt), ("dv", dv, ks, dt), ("delta", delta, shape[:3], _f32)):
-        if t is None:
-            t = _new(stream, dev, sh, ty)
-        else:
-            _want(name, t, ty, sh, dev)
-        grads.append(t)
-    workspace, at, space = _space("attn_cross_bwd_workspace", workspace, dev, sizes, stream)
-    _call("attn_cross_bwd", dev, stream, sizes, q.data_ptr(), k.data_ptr(), v.data_ptr(), lens_p, out_p, lse_p, dout_p,
-          *(t.data_ptr() for t in grads), 1.0 / math.sqrt(shape[3]) if scale is None else float(scale), code, at, space,
+    lse_p = _want("lse", lse, _f32, rows, dev)
+    if dq is None:
+        dq = torch.empty_like(q) if stream is None else _new(stream, dev, shape, dt)
+    else:
+        _want("dq", dq, dt, shape, dev)
+    if dk is None:
+        dk = torch.empty_like(k) if stream is None else _new(stream, dev, ks, dt)
+    else:
+        _want("dk", dk, dt, ks, dev)
+    if dv is None:
+        dv = torch.empty_like(k) if stream is None else _new(stream, dev, ks, dt)
+    else:
+        _want("dv", dv, dt, ks, dev)
+    if delta is None:
+        delta = _new(stream, dev, rows, _f32)
+    else:
+        _want("delta", delta, _f32, rows, dev)
+    workspace, at, space = _space("attn_cross_bwd_workspace", workspace, dev, index, sizes, stream)
+    _call("attn_cross_bwd", index, stream, sizes, q.data_ptr(), k.data_ptr(), v.data_ptr(), lens_p, out_p, lse_p, dout_p,
+          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), delta.data_ptr(),
+          1.0 / math.sqrt(shape[3]) if scale is None else float(scale), code, at, space,
           ATTN_DEFAULT_WAIT_TIMEOUT_NS if wait_timeout_ns is None else int(wait_timeout_ns))
-    return tuple(grads)
+    return dq, dk, dv, delta
 
 
 class _CrossFn(torch.autograd.Function):

@@ -29,13 +29,14 @@
 namespace ea {
 namespace {
 
-constexpr int kFewWarps = 4, kFewThreads = kFewWarps * 32;
 constexpr float kLn2F = 0.6931471805599453f;
 
 enum : int { kChkFewRow = 0x7201 };
 
 template <int W, int RT>
 struct FewLayout {
+  static constexpr int kWarps = W == 256 ? 4 : 4;
+  static constexpr int kThreads = kWarps * 32;
   static constexpr int kChunk = W == 64 ? 32 : 16;       // keys of a warp's step
   static constexpr int kStages = 3;                      // 96 KB a CTA, two of them an SM (256 columns: 192)
   static constexpr int kRow = W * 2;                     // bytes
@@ -46,9 +47,9 @@ struct FewLayout {
   static constexpr int kRingOff = kQOff + kRows * kRow;
   static constexpr int kOut = kRows * W * 4;             // one fp32 output
   // after the keys the ring holds the warps' outputs, then the CTA's
-  static constexpr int kRing = kFewWarps * kWarpRing > (kFewWarps + 1) * kOut ? kFewWarps * kWarpRing : (kFewWarps + 1) * kOut;
+  static constexpr int kRing = kWarps * kWarpRing > (kWarps + 1) * kOut ? kWarps * kWarpRing : (kWarps + 1) * kOut;
   static constexpr int kStatOff = kRingOff + kRing;      // [warps + 1][rows] of (max, sum, rounded sum, -)
-  static constexpr int kAlloc = kStatOff + (kFewWarps + 1) * kRows * 16;
+  static constexpr int kAlloc = kStatOff + (kWarps + 1) * kRows * 16;
   static_assert(kAlloc <= 232448, "shared memory budget exceeded");
 };
 
@@ -70,10 +71,10 @@ __device__ __forceinline__ void ldm4_trans(uint32_t (&r)[4], uint32_t addr) {
 template <bool F16>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (F16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
@@ -113,9 +114,10 @@ __device__ __forceinline__ void st_shared_f2(uint32_t addr, float a, float b) {
 __device__ __forceinline__ float weight_of(float m, float ref) { return ref == -INFINITY ? 1.f : ex2_approx(m - ref); }
 
 template <int W, int RT, bool F16>
-__global__ void __launch_bounds__(kFewThreads) cross_few_kernel(const __grid_constant__ FewParams p) {
+__global__ void __launch_bounds__(FewLayout<W, RT>::kThreads) cross_few_kernel(const __grid_constant__ FewParams p) {
   using L = FewLayout<W, RT>;
   constexpr int kUnits = W / 8;  // 16-byte units of a row
+  constexpr int kFewWarps = L::kWarps, kFewThreads = L::kThreads;
   extern __shared__ __align__(128) uint8_t few_smem[];
   const uint32_t sb = smem_u32(few_smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -395,7 +397,7 @@ cudaError_t launch_few(const FewParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((long long)p.BH * p.groups * p.runs * p.cluster), 1, 1);
-  cfg.blockDim = dim3(kFewThreads, 1, 1);
+  cfg.blockDim = dim3(L::kThreads, 1, 1);
   cfg.dynamicSmemBytes = L::kAlloc;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -18,48 +18,71 @@ namespace {
 
 constexpr int kJoinThreads = 256;
 
-// One warp a row: lane r holds run r's weight (and run 32 + r's), every lane four
-// (or eight) channels.
+// A CTA a row: D/4 threads side by side read a run's four channels each, as many
+// groups of them as there are threads take every so many-th run, so that all runs'
+// loads are in flight at once.  Each warp finds the runs' weights for itself.
+constexpr int kFwdThreads = 256;
 template <bool F16>
-__global__ void __launch_bounds__(kJoinThreads) join_fwd_kernel(const __grid_constant__ JoinFwdParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
-  if (row >= p.rows) return;
+__global__ void __launch_bounds__(kFwdThreads) join_fwd_kernel(const __grid_constant__ JoinFwdParams p) {
+  __shared__ float s_w[kFwdThreads / 32][kMaxRuns];
+  __shared__ float4 s_sum[kFwdThreads];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t row = blockIdx.x;
+  const int quads = p.D / 4, groups = kFwdThreads / quads;  // quads <= 64
+  const int group = tid / quads, c = tid - group * quads;
+  constexpr int kHeld = 8;
+  float4 held[kHeld];
+  const float* from = p.part_o + row * p.D + 4 * c;
+  const int64_t stride = p.rows * p.D;
+  if (group < groups) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (group + i * groups < p.runs) held[i] = __ldcg(reinterpret_cast<const float4*>(from + (group + i * groups) * stride));
+  }
   float e[2], m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = lane + 32 * i;
-    e[i] = r < p.runs ? p.part_lse[r * p.rows + row] : -INFINITY;
+    e[i] = r < p.runs ? __ldcg(p.part_lse + r * p.rows + row) : -INFINITY;
     m = fmaxf(m, e[i]);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float ref = m == -INFINITY ? 0.f : m;
-  float w[2], sum;
+  float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) w[i] = expf(e[i] - ref);
-  // NaN among the runs (fmaxf passes it over) stays NaN: it is in w
-  sum = w[0] + w[1];
+  for (int i = 0; i < 2; ++i) {
+    const float w = expf(e[i] - ref);  // NaN among the runs, which the maximum passed over, stays
+    s_w[warp][lane + 32 * i] = w;
+    sum += w;
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  for (int c0 = 0; c0 < p.D; c0 += 128) {
-    const int c = c0 + lane * 4;
-    const bool in = c < p.D;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float* from = p.part_o + row * p.D + (in ? c : 0);
-#pragma unroll 4
-    for (int r = 0; r < p.runs; ++r) {
-      const float wr = __shfl_sync(0xffffffffu, r < 32 ? w[0] : w[1], r & 31);
-      const float4 o = *reinterpret_cast<const float4*>(from + r * p.rows * p.D);
-      a.x = fmaf(wr, o.x, a.x), a.y = fmaf(wr, o.y, a.y), a.z = fmaf(wr, o.z, a.z), a.w = fmaf(wr, o.w, a.w);
-    }
-    if (!in) continue;
-    uint2 v;
-    v.x = pack_x2<F16>(a.x * inv, a.y * inv), v.y = pack_x2<F16>(a.z * inv, a.w * inv);
-    *reinterpret_cast<uint2*>(p.out + row * p.D + c) = v;
+  __syncwarp();
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](int r, const float4& o) {
+    const float w = s_w[warp][r];
+    a.x = fmaf(w, o.x, a.x), a.y = fmaf(w, o.y, a.y), a.z = fmaf(w, o.z, a.z), a.w = fmaf(w, o.w, a.w);
+  };
+  if (group < groups) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (group + i * groups < p.runs) add(group + i * groups, held[i]);
+    for (int r = group + kHeld * groups; r < p.runs; r += groups)
+      add(r, __ldcg(reinterpret_cast<const float4*>(from + r * stride)));
   }
-  if (lane == 0) p.lse[row] = m == -INFINITY && sum == 0.f ? -INFINITY : m + logf(sum);
+  s_sum[tid] = a;
+  __syncthreads();
+  if (group != 0) return;
+  for (int g = 1; g < groups; ++g) {
+    const float4 o = s_sum[g * quads + c];
+    a.x += o.x, a.y += o.y, a.z += o.z, a.w += o.w;
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint2 v;
+  v.x = pack_x2<F16>(a.x * inv, a.y * inv), v.y = pack_x2<F16>(a.z * inv, a.w * inv);
+  *reinterpret_cast<uint2*>(p.out + row * p.D + 4 * c) = v;
+  if (c == 0) p.lse[row] = sum == 0.f ? -INFINITY : m + logf(sum);
 }
 
 struct JoinSums {
@@ -90,10 +113,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_sum_kernel(const __grid_con
     for (int e = 0; e < 8; ++e) s[e] = 0.f;
     if (there) {
       const float* from = p.part + x * 8;
-#pragma unroll 4
+#pragma unroll 8
       for (int r = 0; r < runs; ++r) {
         const float4* f = reinterpret_cast<const float4*>(from + r * p.rows * p.D);
-        const float4 a = f[0], b = f[1];
+        const float4 a = __ldcg(f), b = __ldcg(f + 1);
         s[0] += a.x, s[1] += a.y, s[2] += a.z, s[3] += a.w;
         s[4] += b.x, s[5] += b.y, s[6] += b.z, s[7] += b.w;
       }
@@ -109,8 +132,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_sum_kernel(const __grid_con
 
 cudaError_t join_fwd_launch(const JoinFwdParams& p, bool f16, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((p.rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32)), 1, 1);
-  cfg.blockDim = dim3(kJoinThreads, 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.rows), 1, 1);
+  cfg.blockDim = dim3(kFwdThreads, 1, 1);
   cfg.stream = stream;
   return f16 ? cudaLaunchKernelEx(&cfg, join_fwd_kernel<true>, p) : cudaLaunchKernelEx(&cfg, join_fwd_kernel<false>, p);
 }

@@ -66,7 +66,7 @@ BAD, UNSUP, MIS = binding.ATTN_ERR_INVALID_ARG, binding.ATTN_ERR_UNSUPPORTED, bi
 
 
 def _sizes(batch=2, q_heads=8, heads=4, Sq=16, Sk=40, head_dim=64):
-    return cross._Sizes(batch, q_heads, heads, Sq, Sk, head_dim)
+    return cross._pack_sizes(batch, q_heads, heads, Sq, Sk, head_dim)
 
 
 def _fwd(lib, sizes=None, q=A, k=A + T, v=A + 2 * T, lens=A + 3 * T, out=A + 4 * T, lse=A + 5 * T, scale=0.125, dtype=0,
