@@ -181,15 +181,16 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
     st_volatile_shared(abort_addr, 0);
     fence_barrier_init();
     if constexpr (QCP) {
-      int bh0, i0;
-      fwd_tile<MASK>(p, static_cast<int>(blockIdx.x), &bh0, &i0);
-      mbar_arrive_expect_tx(bar(L::kKFull + 0), kTile);
+      const FwdUnit u0 = fwd_unit<MASK, kRowsP, false>(p, static_cast<int>(blockIdx.x));
+      if (!CROSS || u0.nkv > 0) {
+        mbar_arrive_expect_tx(bar(L::kKFull + 0), kTile);
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        const uint32_t dst = sb + L::kKOff + c * kChunkBytes;
-        if (dbg_tma(dbb, dst, kChunkBytes, c * 64, i0 * kRowsP, bh0, false, kChkPLoadK))
-          tma_load_3d(dst, &p.tm_q, bar(L::kKFull + 0), c * 64, i0 * kRowsP, bh0,
-                      l2_policy_evict_first());
+        for (int c = 0; c < D / 64; ++c) {
+          const uint32_t dst = sb + L::kKOff + c * kChunkBytes;
+          if (dbg_tma(dbb, dst, kChunkBytes, c * 64, u0.i * kRowsP, u0.bh, false, kChkPLoadK))
+            tma_load_3d(dst, &p.tm_q, bar(L::kKFull + 0), c * 64, u0.i * kRowsP, u0.bh,
+                        l2_policy_evict_first());
+        }
       }
     }
   }
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
     const uint32_t tO = tmem_base + lane_bits + kOCol;
     const float sl2 = p.scale_log2;
     // Q row of tile 0 into Q slot 0, 32 columns (64 values) per store
-    if constexpr (!QCP) {
+    if (!QCP && (!CROSS || fwd_unit<MASK, kRowsP, false>(p, static_cast<int>(blockIdx.x)).nkv > 0)) {
 #pragma unroll
       for (int c = 0; c < D / 64; ++c)
         if (dbg_warp(dbg_tmem(dbb, tmem_base + lane_bits + kQCol + 32 * c, 32, warp, kChkPQTmem)))
@@ -236,12 +237,14 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
     bool ok = true;
     int x = read_info(0, kSitePSoftInfo, &ok);
     int g = 0;  // K/V steps done by this CTA before the current tile
+    int live = 0;  // tiles before it that had any: of cross-attention some have none, and
+                   // get zeros without a product
     for (int k = 0; ok && x >= 0; ++k) {
       if (!dbg(x < n_units, dbb, kChkPTile)) {
         ok = false;
         break;
       }
-      const FwdUnit un = fwd_unit<MASK, kRowsP>(p, x);
+      const FwdUnit un = fwd_unit<MASK, kRowsP, false>(p, x);
       const int bh = un.bh, i = un.i, nkv = un.nkv;
       const int grow = i * kRowsP + row;
       const bool valid = grow < p.S;
@@ -357,13 +360,15 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
       // start while this tile's output drains
       const int nx = read_info(k + 1, kSitePSoftInfo, &ok);
       if (!ok) break;
-      if (!QCP && nx >= 0 && dbg(nx < n_units, dbb, kChkPTile)) {
+      if (!CROSS || nkv > 0) ++live;
+      if (!QCP && nx >= 0 && dbg(nx < n_units, dbb, kChkPTile) &&
+          (!CROSS || fwd_unit<MASK, kRowsP, false>(p, nx).nkv > 0)) {
         int nbh, ni;
         fwd_tile<MASK>(p, nx, &nbh, &ni);
         const int ngrow = ni * kRowsP + row;
         const bool nvalid = ngrow < p.S;
         const uint16_t* qr = p.q + (nvalid ? (int64_t)nbh * p.S + ngrow : 0) * p.d_cols;
-        const uint32_t tq = tmem_base + lane_bits + kQCol + ((k + 1) & 1) * (D / 2);
+        const uint32_t tq = tmem_base + lane_bits + kQCol + (live & 1) * (D / 2);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
           uint32_t w[32];
@@ -380,11 +385,12 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
         }
         tmem_st_wait();
         tc_fence_before_sync();
-        mbar_arrive(bar(L::kQTmem + ((k + 1) & 1)));
+        mbar_arrive(bar(L::kQTmem + (live & 1)));
       }
 
       // ---- epilogue: O / lq → 16-bit → swizzled staging → TMA store; lse
-      ok = __all_sync(0xffffffffu, wait_bounded(bar(L::kOFull), k & 1, ctl, kSitePSoftO | (k & 0xff)));
+      if (!CROSS || nkv > 0)
+        ok = __all_sync(0xffffffffu, wait_bounded(bar(L::kOFull), (live - 1) & 1, ctl, kSitePSoftO | (k & 0xff)));
       if (!ok) break;
       tc_fence_after_sync();
       if (lane == 0) tma_store_wait_read();  // this warp's previous store has read the staging rows
@@ -396,7 +402,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
         for (int c2 = 0; c2 < D / 32 && dbg_warp(dbg_tmem(dbb, tO + 32 * c2, 32, warp, kChkPOTmem));
              ++c2)
           store_part(tO + 32 * c2, p.part_o + at * p.d_cols, 32 * c2, inv_l, valid, dbb, bh, grow,
-                     kChkPStore);
+                     kChkPStore, nkv == 0);
         if (valid && dbg_row(dbb, bh, grow, 0, 0, kChkPLse)) p.part_lse[at] = (m + __log2f(l)) * kLn2P;
         x = nx;
         continue;
@@ -420,6 +426,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
           for (int e = 0; e < 4; ++e)
             w[e] = pack_x2<F16>(__uint_as_float(src[2 * e]) * inv_l,
                                 __uint_as_float(src[2 * e + 1]) * inv_l);
+          if (CROSS && nkv == 0) w[0] = w[1] = w[2] = w[3] = 0u;  // (O holds another tile's)
           if (dbg_smem(dbb, addr, 16, 16, kChkPStage)) st_shared_v4(addr, w[0], w[1], w[2], w[3]);
         }
       }
@@ -455,7 +462,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
       const uint32_t resp = sb + L::kRespOff;
       // K-ring positions / V steps whose loads were issued (with QCP the K ring
       // also carries each tile's Q rows; tile 0's went out during the set-up)
-      int k_issued = QCP ? 1 : 0, v_issued = 0;
+      int k_issued = 0, v_issued = 0;
+      if (QCP && (!CROSS || fwd_unit<MASK, kRowsP, false>(p, static_cast<int>(blockIdx.x)).nkv > 0)) k_issued = 1;
       uint32_t clc_n = 0;   // launch-control requests made
       bool clc_wait = false;  // a request is in flight
       bool ok = true;
@@ -479,10 +487,35 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
       ok = publish(0, x);
       int g = 0;
       for (int k = 0; ok && x >= 0; ++k) {
-        const FwdUnit un = fwd_unit<MASK, kRowsP>(p, x);
+        const FwdUnit un = fwd_unit<MASK, kRowsP, false>(p, x);
         const int bh = un.bh, i = un.i, nkv = un.nkv;
         const int jr = nkv > kAskAhead ? nkv - 1 - kAskAhead : 0;  // ask for the next tile
         int nx = -1;
+        // settles the next tile: the answer to the request, published for the other
+        // roles (without QCP its Q rows are brought into L2)
+        auto settle = [&]() {
+          if (clc_wait) {
+            if (!wait_bounded(bar(L::kClc), (clc_n - 1) & 1, ctl, kSitePClc | (k & 0xff))) return false;
+            clc_wait = false;
+            int first = -1;
+            if (clc_granted(resp, &first) && first >= 0 && first < n_units) nx = first;
+          }
+          if (!publish(k + 1, nx)) return false;
+          if (!QCP && nx >= 0) {
+            int nbh, ni;
+            fwd_tile<MASK>(p, nx, &nbh, &ni);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) tma_prefetch_l2_3d(&p.tm_q, c * 64, ni * kRowsP, nbh);
+          }
+          return true;
+        };
+        if (CROSS && nkv == 0) {
+          request();
+          ok = settle();
+          if (!ok) break;
+          x = nx;
+          continue;
+        }
         if (QCP && k > 0) {  // the tile's Q rows, ahead of its K tiles
           const int ks = k_issued % kKStages;
           ok = wait_bounded(bar(L::kKEmpty + ks), ((k_issued / kKStages) & 1) ^ 1, ctl,
@@ -528,23 +561,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
           v_issued = gj + 1;
           if (j == jr) request();
           if (j == nkv - 1) {
-            // settle the next tile: the answer to the request, published for
-            // the other roles (without QCP its Q rows are brought into L2)
-            if (clc_wait) {
-              ok = wait_bounded(bar(L::kClc), (clc_n - 1) & 1, ctl, kSitePClc | (k & 0xff));
-              if (!ok) break;
-              clc_wait = false;
-              int first = -1;
-              if (clc_granted(resp, &first) && first >= 0 && first < n_units) nx = first;
-            }
-            ok = publish(k + 1, nx);
+            ok = settle();
             if (!ok) break;
-            if (!QCP && nx >= 0) {
-              int nbh, ni;
-              fwd_tile<MASK>(p, nx, &nbh, &ni);
-#pragma unroll
-              for (int c = 0; c < D / 64; ++c) tma_prefetch_l2_3d(&p.tm_q, c * 64, ni * kRowsP, nbh);
-            }
           }
         }
         if (!ok) break;
@@ -644,12 +662,13 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
     int nkv = 0;
     FwdUnit un{};
     if (ok && x >= 0) {
-      un = fwd_unit<MASK, kRowsP>(p, x);
+      un = fwd_unit<MASK, kRowsP, false>(p, x);
       nkv = un.nkv;
-      ok = start_tile(0, nkv, 0, 0);
+      if (!CROSS || nkv > 0) ok = start_tile(0, nkv, 0, 0);
     }
+    int live = 0;  // tiles with any K/V steps before the current one
     for (int k = 0; ok && x >= 0; ++k) {
-      const int qs = k & 1;
+      const int qs = live & 1;
       for (int j = 0; j < nkv && ok; ++j) {
         const int gj = g + j;
         const int b = gj & 1;
@@ -687,12 +706,13 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
       }
       if (!ok) break;
       g += nkv;
+      if (!CROSS || nkv > 0) ++live;
       // the next tile: its first S products queue behind this tile's last P·V
       x = read_info(k + 1, kSitePMmaInfo, &ok);
       if (!ok || x < 0 || !dbg(x < n_units, dbb, kChkPTile)) break;
-      un = fwd_unit<MASK, kRowsP>(p, x);
+      un = fwd_unit<MASK, kRowsP, false>(p, x);
       nkv = un.nkv;
-      ok = start_tile(g, nkv, (k + 1) & 1, k + 1);
+      if (!CROSS || nkv > 0) ok = start_tile(g, nkv, live & 1, live);
     }
     if (leader) {
       mma_commit(bar(L::kDrain));

@@ -45,23 +45,25 @@ __device__ __forceinline__ void fwd_tile(const Fwd1QParams& p, int x, int* bh, i
 }
 
 // Run `part` of `parts` of a sequence's tiles, which are dealt evenly: first tile and
-// count.  A run without tiles (no keys, or more runs than tiles) gets one of which no
-// key is there, so that every unit has a step; *len is 0 then.
-__device__ __forceinline__ void cross_run(int part, int parts, int tile, int* len, int* j0, int* n) {
+// count.  A run without tiles (no keys, or more runs than tiles) gets, with
+// `some`, one of which no key is there, so that every unit has a step; *len is 0 then.
+__device__ __forceinline__ void cross_run(int part, int parts, int tile, int* len, int* j0, int* n,
+                                          bool some = true) {
   const int tiles = (*len + tile - 1) / tile;
   const int each = tiles / parts, more = tiles - each * parts;
   *j0 = part * each + min(part, more);
   *n = each + (part < more ? 1 : 0);
-  if (*n == 0) *len = 0, *j0 = 0, *n = 1;
+  if (*n == 0) *len = 0, *j0 = 0, *n = some ? 1 : 0;
 }
 
-template <int MASK, int BN>
+// SOME: every unit has a step (cross_run).
+template <int MASK, int BN, bool SOME = true>
 __device__ __forceinline__ FwdUnit fwd_unit(const Fwd1QParams& p, int x) {
   FwdUnit u;
   fwd_tile<MASK>(p, x, &u.bh, &u.i);
   if constexpr (MASK == kMaskCross) {
     u.len = cross_len(p.lens, u.bh / p.heads, p.Sk, p.status);
-    cross_run(x % p.n_split, p.n_split, BN, &u.len, &u.j0, &u.nkv);
+    cross_run(x % p.n_split, p.n_split, BN, &u.len, &u.j0, &u.nkv, SOME);
   } else {
     const int n = MASK == kMaskCausal ? (u.i + 1) * (kBlockM / BN) : p.n_kt;
     u.nkv = n < p.n_kt ? n : p.n_kt;
@@ -169,14 +171,19 @@ __device__ __forceinline__ void clear_tail(uint32_t tile, int rows, int live, bo
 }
 
 // 32 columns of this thread's row of an fp32 TMEM accumulator, times mul, to
-// columns x0 .. of the row at `to`.  Call with the full warp.
+// columns x0 .. of the row at `to` (none: zeros).  Call with the full warp.
 __device__ __forceinline__ void store_part(uint32_t taddr, float* to, int x0, float mul, bool valid,
-                                           const DbgBounds& dbb, int bh, int row, int site) {
+                                           const DbgBounds& dbb, int bh, int row, int site,
+                                           bool none = false) {
   uint32_t o[32];
   tmem_ld_32x32b_x32(taddr, o);
   tmem_ld_wait();
   reg_fence(o);
   if (!valid) return;
+  if (none) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] = 0u;
+  }
 #pragma unroll
   for (int e = 0; e < 32; e += 4)
     if (x0 + e < dbb.cols && dbg_row(dbb, bh, row, x0 + e, 4, site))
