@@ -42,7 +42,7 @@ def _sources():
                                             "attn_noalloc.cu", "attn_bwd_api.cu", "attn_bwd_sm103.cu", "attn_bwd256_sm103.cu",
                                             "cache_api.cu", "cache_fwd_sm103.cu", "cache_pages_sm103.cu", "cache_select_sm103.cu",
                                             "rope_api.cu", "rope_sm103.cu", "cross_api.cu", "cross_join_sm103.cu", "attn_cross_bwd_sm103.cu",
-                                            "cross_few_sm103.cu")]
+                                            "cross_few_sm103.cu", "cross_small_bwd_sm103.cu")]
 
 
 def _deps():

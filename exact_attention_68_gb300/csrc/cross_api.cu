@@ -134,19 +134,25 @@ FwdPlan plan_fwd(const Sizes& s, int sms) {
 }
 
 struct BwdPlan {
+  bool small;  // a CTA a slice
   int width, n_qt, n_kt, q_split;
   ea::KvRuns kv;
   size_t dq_space, dk_space, space;  // dk_space: of dk and of dv each
 };
 BwdPlan plan_bwd(const attn_cross_t& c, const Sizes& s, int sms) {
   BwdPlan b;
+  std::memset(&b, 0, sizeof(b));
   b.width = ea::kernel_head_dim(s.D);
+  b.small = s.rows <= ea::kSmallSide && s.Sk <= ea::kSmallSide;
+  if (b.small) {
+    b.space = kNoSpace;
+    return b;
+  }
   const int step = b.width == 256 ? 64 : 128;  // keys, or queries, of a step
   b.n_qt = static_cast<int>((s.rows + 127) / 128);
   b.n_kt = static_cast<int>((s.Sk + 127) / 128);
   const double us = b.width == 64 ? 1.0 : 1.4;
   b.q_split = runs_of(s.BH * b.n_qt, (s.Sk + step - 1) / step, sms, us, 4.0, static_cast<double>(s.BH) * s.rows * s.D * 4);
-  std::memset(&b.kv, 0, sizeof(b.kv));
   b.kv.batch = static_cast<int>(c.batch), b.kv.heads = static_cast<int>(c.heads), b.kv.Sk = static_cast<int>(s.Sk);
   b.kv.q_steps = static_cast<int>((s.rows + step - 1) / step);
   b.kv.ctas = b.width == 256 ? 2 : 1;
@@ -298,6 +304,19 @@ attn_status_t attn_cross_bwd(const attn_cross_t* sizes, const void* q, const voi
   if (st != ATTN_OK) return st;
 
   const bool f16 = dtype == ATTN_F16;
+  if (b.small) {
+    ea::SmallBwdParams p;
+    p.q = static_cast<const uint16_t*>(q), p.k = static_cast<const uint16_t*>(k), p.v = static_cast<const uint16_t*>(v);
+    p.lens = lens;
+    p.out = static_cast<const uint16_t*>(out), p.lse = lse, p.dout = static_cast<const uint16_t*>(dout);
+    p.dq = static_cast<uint16_t*>(dq), p.dk = static_cast<uint16_t*>(dk), p.dv = static_cast<uint16_t*>(dv);
+    p.delta = delta;
+    p.status = status;
+    p.BH = static_cast<int>(s.BH), p.heads = static_cast<int>(sizes->heads), p.rows = static_cast<int>(s.rows);
+    p.Sk = static_cast<int>(s.Sk), p.D = static_cast<int>(s.D);
+    p.scale = scale, p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    return launched(ea::cross_small_bwd_launch(p, b.width, f16, stream));
+  }
   ea::BwdParams p;
   std::memset(&p, 0, sizeof(p));
   auto map = [&](CUtensorMap* m, const void* t, int64_t n, uint32_t box) {

@@ -1,5 +1,5 @@
-// cross_few.h — parameters and launch entry of cross-attention's kernel for few
-// queries (host-compilable).
+// cross_few.h — parameters and launch entries of cross-attention's kernels for few
+// queries, and of its gradient for few queries and keys (host-compilable).
 #pragma once
 
 #include <cstdint>
@@ -28,5 +28,25 @@ struct FewParams {
 
 // width: 64, 128 or 256 columns; tiles: of 16 rows a CTA takes, 1 or 2 (256 columns: 1).
 cudaError_t cross_few_launch(const FewParams& p, int width, int tiles, bool f16, cudaStream_t stream);
+
+constexpr int kSmallSide = 64;  // queries and keys of a slice that the small gradient takes
+
+struct SmallBwdParams {
+  const uint16_t* q;  // [BH, rows, D]
+  const uint16_t* k;  // [BH, Sk, D]
+  const uint16_t* v;
+  const int* lens;    // [BH / heads] or null
+  const uint16_t* out;
+  const float* lse;   // [BH, rows]
+  const uint16_t* dout;
+  uint16_t* dq;
+  uint16_t* dk;
+  uint16_t* dv;
+  float* delta;
+  int* status;
+  int BH, heads, rows, Sk, D;
+  float scale, scale_log2;
+};
+cudaError_t cross_small_bwd_launch(const SmallBwdParams& p, int width, bool f16, cudaStream_t stream);
 
 }  // namespace ea

@@ -81,7 +81,7 @@ def check_fwd(q, k, v, lens, out, lse, scale):
     got = n64(lse)
     dead = np.isneginf(rl)
     assert np.array_equal(dead, np.isneginf(got)) and (n64(out)[dead] == 0).all()
-    assert (np.abs(got - rl)[~dead] <= 2.0 ** -13 + np.abs(rl[~dead]) * 2.0 ** -22).all()
+    assert (np.abs(got[~dead] - rl[~dead]) <= 2.0 ** -13 + np.abs(rl[~dead]) * 2.0 ** -22).all()
     return ro, rl
 
 
@@ -185,8 +185,35 @@ def test_scores_that_climb(cuda_device, dt, Sq):
     check_fwd(q, k, v, None, out, lse, D ** -0.5)
 
 
+@pytest.mark.parametrize("Sq,Sk,lens", [(1, 1, None), (1, 2, [2, 1]), (3, 7, [7, 0]), (16, 17, [17, 16]), (32, 64, [64, 33]),
+                                        (30, 5, None)])
+@pytest.mark.parametrize("heads", [(2, 2), (4, 2)])
+@pytest.mark.parametrize("D", [64, 72, 128, 200, 256])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+def test_small_gradients_round_once(cuda_device, Sq, Sk, lens, heads, D, dt):
+    """A slice of few queries and keys: P and dS enter their products in two terms each, so that besides the fp32 sums
+    only the results are rounded."""
+    q, k, v, dout, ln = problem(2, *heads, Sq, Sk, D, lens, dt, seed=Sq + Sk + D)
+    out, lse = cross.cross_fwd(q, k, v, ln)
+    bufs = [guarded(s, t) for s, t in ((q.shape, dt), (k.shape, dt), (k.shape, dt), (q.shape[:3], torch.float32))]
+    grads = [b[1] for b in bufs]
+    cross.cross_bwd(q, k, v, out, lse, dout, ln, dq=grads[0], dk=grads[1], dv=grads[2], delta=grads[3])
+    torch.cuda.synchronize()
+    assert binding.device_status() == binding.ATTN_OK and untouched(*bufs)
+    assert cross.cross_bwd_workspace(q, k) == 16
+    check_bwd(q, k, v, out, lse, dout, lens, D ** -0.5, grads)
+    kk, vv = (np.nan_to_num(n64(x), nan=0.0, posinf=0.0, neginf=0.0) for x in (k, v))
+    full = lens if lens is not None else [Sk] * 2
+    dq, dk, dv, _, (mq, mk, mv, m2q, m2k) = oracle.cross_bwd(n64(q), kk, vv, n64(out), n64(lse), n64(dout), full, D ** -0.5)
+    h = half_step(dt)
+    tiny = 2.0 ** -24 * (1 + float(np.abs(n64(q)).max() + np.abs(kk).max() + np.abs(n64(dout)).max()) * Sq * heads[0])
+    for name, got, ref, m2 in (("dq", grads[0], dq, m2q), ("dk", grads[1], dk, m2k), ("dv", grads[2], dv, mv)):
+        check(name, got, ref, h * np.abs(ref) + 2.0 ** -12 * m2 + tiny)
+
+
 def test_results_do_not_depend_on_the_padding(cuda_device):
-    for shape in ((2, 4, 2, 40, 400, [390, 5]), (2, 2, 2, 600, 300, [129, 0]), (1, 2, 2, 3, 900, [700])):
+    for shape in ((2, 4, 2, 40, 400, [390, 5]), (2, 2, 2, 600, 300, [129, 0]), (1, 2, 2, 3, 900, [700]),
+                  (3, 2, 1, 9, 60, [59, 0, 1])):
         for D in (64, 128, 256):
             q, k, v, dout, ln = problem(*shape[:5], D, shape[5], torch.bfloat16, 21)
             k2, v2 = k.nan_to_num(1.0, 2.0, 3.0), v.nan_to_num(4.0, 5.0, -6.0)
