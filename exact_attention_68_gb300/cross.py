@@ -23,6 +23,7 @@ import struct
 import threading
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from .binding import (ATTN_BF16, ATTN_DEFAULT_WAIT_TIMEOUT_NS, ATTN_ERR_INVALID_ARG, ATTN_F16, ATTN_OK, AttnError,
                       load_library)
@@ -255,6 +256,7 @@ class _CrossFn(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         q, k, v, lens, out, lse = ctx.saved_tensors
         dq, dk, dv, _ = cross_bwd(q, k, v, out, lse, dout.contiguous(), lens, ctx.scale)

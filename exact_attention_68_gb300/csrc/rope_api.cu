@@ -78,7 +78,7 @@ attn_status_t check_sizes(const attn_rope_part_t* parts, int n, int64_t B, int64
 
 attn_status_t check(const attn_rope_part_t* parts, int n, const attn_rope_t* rope,
                     const attn_rope_positions_t* at, int64_t B, int64_t S, int64_t D, float eps, int dtype,
-                    bool bwd) {
+                    bool bwd, const void* workspace, uint64_t space) {
   attn_status_t s = check_sizes(parts, n, B, S, D);
   if (s != ATTN_OK) return s;
   if (dtype != ATTN_BF16 && dtype != ATTN_F16) return ATTN_ERR_INVALID_ARG;
@@ -125,6 +125,14 @@ attn_status_t check(const attn_rope_part_t* parts, int n, const attn_rope_t* rop
     const void* w = bwd ? q.dx : q.y;
     const uint64_t wn = bwd ? extent(dx, B, S, q.heads, D) : yn;
     const uint64_t gn = bwd && q.dweight ? static_cast<uint64_t>(D) * (q.weight_f32 ? 4 : 2) : 0;
+    // the workspace is written too
+    auto in_space = [&](const void* p, uint64_t bytes) {
+      return workspace && space && p && bytes && overlaps(workspace, space, p, bytes);
+    };
+    if (bwd && (in_space(w, wn) || in_space(q.dweight, gn) || in_space(q.y, yn) || in_space(q.weight, gn ? gn : D * 4) ||
+                (q.weight && in_space(q.x, extent({q.x, q.stride_b, q.stride_s, q.stride_h}, B, S, q.heads, D))) ||
+                (turn && in_space(at->at, pos_bytes))))
+      return ATTN_ERR_INVALID_ARG;
     auto hit = [&](const void* p, uint64_t bytes) {
       return p && bytes && (overlaps(w, wn, p, bytes) || (gn && overlaps(q.dweight, gn, p, bytes)));
     };
@@ -291,7 +299,7 @@ extern "C" {
 attn_status_t attn_rope_fwd(const attn_rope_part_t* parts, int n, const attn_rope_t* rope,
                             const attn_rope_positions_t* positions, int64_t B, int64_t S, int64_t D,
                             float eps, attn_dtype_t dtype, cudaStream_t stream) {
-  const attn_status_t s = check(parts, n, rope, positions, B, S, D, eps, dtype, false);
+  const attn_status_t s = check(parts, n, rope, positions, B, S, D, eps, dtype, false, nullptr, 0);
   if (s != ATTN_OK) return s;
   return run(parts, n, rope, positions, B, S, D, eps, dtype, nullptr, 0, false, stream);
 }
@@ -315,7 +323,7 @@ attn_status_t attn_rope_bwd(const attn_rope_part_t* parts, int n, const attn_rop
                             const attn_rope_positions_t* positions, int64_t B, int64_t S, int64_t D,
                             float eps, attn_dtype_t dtype, void* workspace, size_t workspace_bytes,
                             cudaStream_t stream) {
-  const attn_status_t s = check(parts, n, rope, positions, B, S, D, eps, dtype, true);
+  const attn_status_t s = check(parts, n, rope, positions, B, S, D, eps, dtype, true, workspace, workspace_bytes);
   if (s != ATTN_OK) return s;
   return run(parts, n, rope, positions, B, S, D, eps, dtype, workspace, workspace_bytes, true, stream);
 }

@@ -25,6 +25,7 @@ import threading
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from .binding import ATTN_BF16, ATTN_ERR_INVALID_ARG, ATTN_F16, ATTN_OK, AttnError, attn_bwd, attn_fwd, load_library
 
@@ -324,6 +325,7 @@ class _NormRopeFn(torch.autograd.Function):
         return tuple(rope_fwd(xs, plan, positions, weights, eps, turn))
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, *dys):
         positions, *tensors = ctx.saved_tensors
         n = ctx.n
@@ -351,6 +353,7 @@ class _RotaryAttentionFn(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         q, k, v, positions, wq, wk, qh, kh, vh, out, lse = ctx.saved_tensors
         plan, eps, scale, causal = ctx.rest

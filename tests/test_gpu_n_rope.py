@@ -190,6 +190,46 @@ def test_norm_without_rotation_and_four_parts(cuda_device):
         close(ys[i], ref, np.abs(ref), torch.float16, 72, what=str(i))
 
 
+def test_gradients_of_four_weights(cuda_device):
+    """More weights than one launch adds up."""
+    B, S, heads, D, dt = 2, 33, (1, 2, 3, 4), 64, torch.bfloat16
+    g = torch.Generator().manual_seed(81)
+    xs = [torch.randn(B, S, h, D, generator=g).to(dt).cuda() for h in heads]
+    ws = [torch.randn(D, generator=g).add(1).cuda() for _ in heads]
+    dys = [torch.randn(B, h, S, D, generator=g).to(dt).cuda() for h in heads]
+    plan, pos = plan_of(32, 2, False), torch.randint(-99, 99, (B, S, 2), generator=g, dtype=torch.int32).cuda()
+    turn = (True, False, True, True)
+    space = rope.rope_bwd_workspace(xs, ws)
+    room = torch.full((space + 64,), 0x55, dtype=torch.uint8, device="cuda")
+    dxs, dws = rope.rope_bwd(dys, xs, plan, pos, ws, 1e-6, turn, workspace=room[:space])
+    torch.cuda.synchronize()
+    assert (room[space:] == 0x55).all()
+    for i, (dx, dw, dx_mag, dw_mag) in enumerate(refs(xs, ws, pos, plan, turn, dys)):
+        close(dxs[i], dx, dx_mag, dt, D, what=f"dx{i}")
+        close(dws[i], dw, dw_mag, torch.float32, D, chain=B * S * heads[i] + 64, what=f"dw{i}")
+    with pytest.raises(binding.AttnError):
+        rope.rope_bwd(dys, xs, plan, pos, ws, 1e-6, turn, workspace=room[:1024])
+
+
+def test_many_tokens_of_few_heads(cuda_device):
+    """More units than warps, rows that fill a fraction of one, a batch whose sequences end inside a warp's share."""
+    B, S, H, D, dt = 7, 3001, 1, 64, torch.float16
+    g = torch.Generator().manual_seed(82)
+    x = torch.randn(B, S, H, D, generator=g).to(dt).cuda()
+    w = torch.randn(D, generator=g).add(1).cuda()
+    plan, pos = rope.rope_plan(D), torch.arange(S, dtype=torch.int32).cuda()[None]
+    y = rope.rope_fwd((x,), plan, pos, (w,))[0]
+    dy = torch.randn(B, H, S, D, generator=g).to(dt).cuda()
+    dx, dw = rope.rope_bwd((dy,), (x,), plan, pos, (w,))
+    full = pos.expand(B, S)[..., None]
+    r = refs((x,), (w,), full, plan, (True,))[0]
+    close(y, r[0], r[1], dt, D, what="y")
+    rx, rw, mx, mw = refs((x,), (w,), full, plan, (True,), (dy,))[0]
+    close(dx[0], rx, mx, dt, D, what="dx")
+    # a lane adds up every so many-th token: at most B·S / 152 / 4 in a chain, then CTAs and warps
+    close(dw[0], rw, mw, torch.float32, D, chain=B * S // 600 + 700, what="dw")
+
+
 def test_no_finite_rows_stay_by_themselves(cuda_device):
     """Rows with NaN or infinities, and rows of zeros, leave every other row as it is."""
     g = torch.Generator().manual_seed(9)

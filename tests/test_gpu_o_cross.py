@@ -223,6 +223,43 @@ def test_results_do_not_depend_on_the_padding(cuda_device):
             assert all(torch.equal(x, y) for x, y in zip(ga, gb))
 
 
+@pytest.mark.parametrize("Sq,Sk", [(1, 300), (40, 30), (200, 300), (2000, 300)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_nobody_has_keys(cuda_device, Sq, Sk, D):
+    q, k, v, dout, ln = problem(2, 2, 2, Sq, Sk, D, [0, 0], torch.bfloat16, 23)
+    out, lse = cross.cross_fwd(q, k, v, ln)
+    grads = cross.cross_bwd(q, k, v, out, lse, dout, ln)
+    assert binding.device_status() == binding.ATTN_OK
+    assert (out == 0).all() and torch.isneginf(lse).all() and all((g == 0).all() for g in grads)
+
+
+def test_many_short_sequences(cuda_device):
+    """More sequences than SMs by far, most of them without keys: units are found by counting through the lengths."""
+    B, Sq, Sk, D = 700, 70, 140, 64
+    lens = [(i * 37) % 141 if i % 3 == 0 else 0 for i in range(B)]
+    q, k, v, dout, ln = problem(B, 1, 1, Sq, Sk, D, lens, torch.bfloat16, 24)
+    out, lse = cross.cross_fwd(q, k, v, ln)
+    grads = cross.cross_bwd(q, k, v, out, lse, dout, ln)
+    assert binding.device_status() == binding.ATTN_OK
+    check_fwd(q, k, v, lens, out, lse, D ** -0.5)
+    check_bwd(q, k, v, out, lse, dout, lens, D ** -0.5, grads)
+
+
+def test_shared_inputs_and_repeated_use(cuda_device):
+    """k and v one tensor, q among them; a graph of autograd used for two losses."""
+    g = torch.Generator().manual_seed(25)
+    x = torch.randn(2, 3, 90, 64, generator=g).to(torch.bfloat16).cuda()
+    out, lse = cross.cross_fwd(x, x, x)
+    check_fwd(x, x, x, None, out, lse, 0.125)
+    grads = cross.cross_bwd(x, x, x, out, lse, x)
+    check_bwd(x, x, x, out, lse, x, None, 0.125, grads)
+    q, k = x.clone().requires_grad_(), x[:, :, :40].contiguous().requires_grad_()
+    o = cross.cross_attention(q, k, k)
+    a = torch.autograd.grad(o, (q, k), torch.ones_like(o), retain_graph=True)
+    b = torch.autograd.grad(o, (q, k), torch.ones_like(o))
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
 def test_nan_and_infinite_queries_and_keys(cuda_device):
     """A NaN query makes its own row NaN and no other; a key that gives +inf or NaN scores, the rows that meet it."""
     q, k, v, _, ln = problem(2, 2, 2, 150, 300, 64, [300, 200], torch.bfloat16, 22)

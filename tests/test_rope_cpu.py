@@ -183,6 +183,12 @@ def test_refused_overlaps(lib):
         assert (got == code) if code else (got not in (BAD, MIS))
 
 
+def test_refused_workspace_overlaps(lib):
+    one = _args(1)
+    for ws in (one[0].dx + 64, one[0].y, one[0].x, one[0].weight, one[0].dweight, A + 30 * T):
+        assert _call(lib, True, one, ws=ws, space=4096) == BAD
+
+
 def test_workspace_sizes_without_weights(lib):
     parts = bytes(_args(1, dweight=0))
     assert lib.attn_rope_bwd_workspace(parts, 1, 2, 16, 64) == 16
