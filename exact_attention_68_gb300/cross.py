@@ -10,7 +10,9 @@ errors are those of the header; there is no fallback.
     dq, dk, dv, delta = cross_bwd(q, k, v, out, lse, dout, lens)
     out = cross_attention(q, k, v, lens)             # autograd
 
-Nothing synchronises.  A workspace is allocated per call where one is needed, unless
+A captured backward pass of the differentiable forms needs what torch asks of any: no
+eager graph of the same leaves may be alive, since their gradients would be added up
+on that graph's stream.  cross_bwd itself has no such bound.  Nothing synchronises.  A workspace is allocated per call where one is needed, unless
 one is passed; calls that may run at the same time, and graphs, need one each.  With
 ``stream``, what a call allocates belongs to that stream, as if it were the current one.
 """

@@ -25,11 +25,12 @@ struct View {
   int64_t b, s, h;
 };
 
-// Strides a view may have: sizes and products stay below 2^62.
-bool strides_ok(int64_t b, int64_t s, int64_t h) {
-  constexpr int64_t most = int64_t(1) << 30;
-  return b >= 0 && s >= 0 && h >= 0 && h <= most && s <= most * 4 && b <= (int64_t(1) << 40) && b % 8 == 0 &&
-         s % 8 == 0 && h % 8 == 0;
+// Strides a view may have: what they span stays below 2^60 values, so that extents in
+// bytes fit 64 bits.
+bool strides_ok(int64_t b, int64_t s, int64_t h, int64_t B, int64_t S, int64_t H) {
+  constexpr int64_t most = int64_t(1) << 58;
+  auto spans = [](int64_t stride, int64_t n) { return stride >= 0 && stride % 8 == 0 && stride <= most / n; };
+  return spans(b, B) && spans(s, S) && spans(h, H);
 }
 uint64_t extent(const View& v, int64_t B, int64_t S, int64_t H, int64_t D) {
   return static_cast<uint64_t>((B - 1) * v.b + (S - 1) * v.s + (H - 1) * v.h + D) * 2;
@@ -90,8 +91,8 @@ attn_status_t check(const attn_rope_part_t* parts, int n, const attn_rope_t* rop
     if ((reads_x && !q.x) || !q.y || (bwd && !q.dx)) return ATTN_ERR_INVALID_ARG;
     if ((q.turn != 0 && q.turn != 1) || (q.weight_f32 != 0 && q.weight_f32 != 1)) return ATTN_ERR_INVALID_ARG;
     if (bwd && q.dweight && !q.weight) return ATTN_ERR_INVALID_ARG;
-    if (reads_x && !strides_ok(q.stride_b, q.stride_s, q.stride_h)) return ATTN_ERR_INVALID_ARG;
-    if (bwd && (!strides_ok(q.dx_stride_b, q.dx_stride_s, q.dx_stride_h) ||
+    if (reads_x && !strides_ok(q.stride_b, q.stride_s, q.stride_h, B, S, q.heads)) return ATTN_ERR_INVALID_ARG;
+    if (bwd && (!strides_ok(q.dx_stride_b, q.dx_stride_s, q.dx_stride_h, B, S, q.heads) ||
                 !separate({q.dx, q.dx_stride_b, q.dx_stride_s, q.dx_stride_h}, B, S, q.heads, D)))
       return ATTN_ERR_INVALID_ARG;
     if ((reads_x && !aligned(q.x, 16)) || !aligned(q.y, 16) || (bwd && !aligned(q.dx, 16)) ||
@@ -129,7 +130,7 @@ attn_status_t check(const attn_rope_part_t* parts, int n, const attn_rope_t* rop
     auto in_space = [&](const void* p, uint64_t bytes) {
       return workspace && space && p && bytes && overlaps(workspace, space, p, bytes);
     };
-    if (bwd && (in_space(w, wn) || in_space(q.dweight, gn) || in_space(q.y, yn) || in_space(q.weight, gn ? gn : D * 4) ||
+    if (bwd && (in_space(w, wn) || in_space(q.dweight, gn) || in_space(q.y, yn) || in_space(q.weight, static_cast<uint64_t>(D) * (q.weight_f32 ? 4 : 2)) ||
                 (q.weight && in_space(q.x, extent({q.x, q.stride_b, q.stride_s, q.stride_h}, B, S, q.heads, D))) ||
                 (turn && in_space(at->at, pos_bytes))))
       return ATTN_ERR_INVALID_ARG;

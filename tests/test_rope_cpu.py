@@ -189,6 +189,19 @@ def test_refused_workspace_overlaps(lib):
         assert _call(lib, True, one, ws=ws, space=4096) == BAD
 
 
+def test_workspace_right_behind_a_weight(lib):
+    """16-bit weights end after 2 bytes a channel: what lies behind is free."""
+    one = _args(1, D=128, dweight=0)
+    got = _call(lib, True, one, D=128, ws=one[0].weight + 256, space=1 << 20)
+    assert got not in (BAD, MIS)
+
+
+@pytest.mark.parametrize("over", [dict(stride_b=1 << 50), dict(stride_s=1 << 44), dict(stride_h=1 << 57)])
+def test_refused_strides_past_64_bits(lib, over):
+    for bwd in (False, True):
+        assert _call(lib, bwd, _args(**over), B=1 << 14, S=1 << 15) == BAD
+
+
 def test_workspace_sizes_without_weights(lib):
     parts = bytes(_args(1, dweight=0))
     assert lib.attn_rope_bwd_workspace(parts, 1, 2, 16, 64) == 16
