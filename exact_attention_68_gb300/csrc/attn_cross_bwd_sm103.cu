@@ -34,6 +34,7 @@
 #include "attn_bwd.h"
 #include "bwd_common.cuh"
 #include "cross_common.cuh"
+#include "launch_after.cuh"
 #include "ptx.cuh"
 #include "umma.cuh"
 
@@ -127,6 +128,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
   const BwdUnit unit0 = cross_dq_unit<kRowsX>(p, x0);  // the grid has no more CTAs than units
 
   if (threadIdx.x == 0) {
+    launch_dependents();
 #pragma unroll
     for (int s = 0; s < L::kKStages; ++s) mbar_init(bar(L::kKFull + s), 1), mbar_init(bar(L::kKEmpty + s), 1);
 #pragma unroll
@@ -553,7 +555,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dkdv_kernel(const __grid
     return cross_kv_unit<kRowsX>(p, w, un);
   };
 
+  // This kernel is set up on each SM as the dq kernel leaves it; what waits for delta
+  // does so before the first bounded wait that depends on it, and all before the end.
   if (threadIdx.x == 0) {
+    launch_dependents();
 #pragma unroll
     for (int s = 0; s < L::kStages; ++s) mbar_init(bar(L::kFull + s), 1), mbar_init(bar(L::kEmpty + s), 1);
 #pragma unroll
@@ -587,6 +592,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dkdv_kernel(const __grid
     BwdUnit un = unit0;
     int subs = 0, pos = 0;  // sub-steps and ring positions of the units before this one
     bool ok = true;
+    wait_for_previous();
     for (int unit = 0; any; ++unit) {
       const int gk = un.tile * kRowsX + r;  // key row in the sequence
       const bool there = gk < un.len;
@@ -707,6 +713,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dkdv_kernel(const __grid
           continue;
         }
         const int y = (it < 0 ? un.tile : un.first + it) * kRowsX;
+        if (issued == 1) wait_for_previous();
         if (it >= 0) {
           // per-query-row statistics of the Q tile; rows past the end read as 0
           const uint32_t stat = sb + L::kStatOff + st * L::kStatBytes;
@@ -822,6 +829,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dkdv_kernel(const __grid
         mma_commit(bar(L::kEmpty + pos % L::kStages));
       }
       __syncwarp();
+      if (unit == 0) wait_for_previous();
       ok = full(pos + 1, kSiteXkMmaQ);
       if (!ok) break;
       tc_fence_after_sync();
@@ -886,10 +894,7 @@ cudaError_t launch_cross(const BwdParams& p, cudaStream_t stream) {
   cfg.dynamicSmemBytes = XqLayout<D>::kAlloc;
   e = cudaLaunchKernelEx(&cfg, kdq, p);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = ctas((long long)p.BH * p.n_kt * p.kv.most_runs);
-  cfg.blockDim = dim3(kBwdThreads, 1, 1);
-  cfg.dynamicSmemBytes = XkLayout<D>::kAlloc;
-  return cudaLaunchKernelEx(&cfg, kkv, p);
+  return launch_after(kkv, ctas((long long)p.BH * p.n_kt * p.kv.most_runs), kBwdThreads, stream, p, XkLayout<D>::kAlloc);
 }
 
 }  // namespace

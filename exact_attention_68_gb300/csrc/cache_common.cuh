@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 
 #include "attn_cache_impl.h"
+#include "launch_after.cuh"
 #include "ptx.cuh"
 
 namespace ea {
@@ -169,31 +170,6 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   if (x != x) return 0u;
   const uint32_t u = __float_as_uint(x + 0.f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-
-// Programmatic dependent launch: the next kernel of the stream may be set up
-// once every CTA has said so or ended; its wait ends when this grid has.
-__device__ __forceinline__ void launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_for_previous() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
-// A launch that may be set up before the stream's previous kernel has ended;
-// the kernel calls wait_for_previous before it uses that one's results or ends.
-template <class Params>
-cudaError_t launch_after(void (*kern)(Params), dim3 grid, int threads, cudaStream_t stream, const Params& p) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 }  // namespace ea

@@ -356,22 +356,22 @@ attn_status_t attn_cross_bwd(const attn_cross_t* sizes, const void* q, const voi
   p.part_dv = p.part_dk + b.dk_space / 4;
   cudaError_t e = b.width == 256 ? ea::bwd256_launch(p, ea::kMaskCross, f16, stream)
                                  : ea::cross_bwd_launch(p, b.width, f16, stream);
-  ea::JoinSumParams j[2];
+  ea::JoinSumParams j[ea::kMaxSums];
   std::memset(j, 0, sizeof(j));
-  if (e == cudaSuccess && b.q_split > 1) {
-    j[0].part = p.part_dq, j[0].to = static_cast<uint16_t*>(dq);
-    j[0].rows = s.BH * s.rows, j[0].runs = b.q_split, j[0].D = p.d_cols, j[0].mul = scale;
-    e = ea::join_sum_launch(j, 1, f16, stream);
+  int sums = 0;
+  if (b.q_split > 1) {
+    ea::JoinSumParams& r = j[sums++];
+    r.part = p.part_dq, r.to = static_cast<uint16_t*>(dq);
+    r.rows = s.BH * s.rows, r.runs = b.q_split, r.D = p.d_cols, r.mul = scale;
   }
-  if (e == cudaSuccess && b.kv.most_runs > 1) {
-    for (int i = 0; i < 2; ++i) {
-      j[i].part = i == 0 ? p.part_dk : p.part_dv;
-      j[i].to = i == 0 ? p.dk : p.dv;
-      j[i].rows = s.BH * s.Sk, j[i].D = p.d_cols, j[i].mul = i == 0 ? scale : 1.f;
-      j[i].of_keys = true, j[i].kv = b.kv, j[i].lens = lens;
-    }
-    e = ea::join_sum_launch(j, 2, f16, stream);
+  for (int i = 0; i < 2 && b.kv.most_runs > 1; ++i) {
+    ea::JoinSumParams& r = j[sums++];
+    r.part = i == 0 ? p.part_dk : p.part_dv;
+    r.to = i == 0 ? p.dk : p.dv;
+    r.rows = s.BH * s.Sk, r.D = p.d_cols, r.mul = i == 0 ? scale : 1.f;
+    r.of_keys = true, r.kv = b.kv, r.lens = lens;
   }
+  if (e == cudaSuccess && sums) e = ea::join_sum_launch(j, sums, f16, stream);
   return launched(e);
 }
 

@@ -24,6 +24,7 @@
 #include "bwd_common.cuh"
 #include "cross_common.cuh"
 #include "cross_few.h"
+#include "launch_after.cuh"
 #include "mma_sync.cuh"
 #include "ptx.cuh"
 
@@ -105,6 +106,7 @@ __global__ void __launch_bounds__(FewLayout<W, RT>::kThreads) cross_few_kernel(c
   const uint32_t sb = smem_u32(few_smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = p.cluster > 1 ? cluster_rank() : 0u;
+  if (p.runs > 1) launch_dependents();
   int x = static_cast<int>(blockIdx.x) / p.cluster;
   const int run = x % p.runs;
   x /= p.runs;

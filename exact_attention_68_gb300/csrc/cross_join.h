@@ -36,7 +36,8 @@ struct JoinSumParams {
   KvRuns kv;
   const int* lens;  // null: every key is there
 };
-// n tensors (1 or 2) of the same sizes in one launch.
+// n tensors (1 to kMaxSums) in one launch.
+constexpr int kMaxSums = 3;
 cudaError_t join_sum_launch(const JoinSumParams* p, int n, bool f16, cudaStream_t stream);
 
 }  // namespace ea

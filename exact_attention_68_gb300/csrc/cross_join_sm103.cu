@@ -11,6 +11,7 @@
 
 #include "cross_join.h"
 #include "cross_runs.cuh"
+#include "launch_after.cuh"
 #include "ptx.cuh"
 
 namespace ea {
@@ -32,6 +33,7 @@ __global__ void __launch_bounds__(kFwdThreads) join_fwd_kernel(const __grid_cons
   const int group = tid / quads, c = tid - group * quads;
   constexpr int kHeld = 8;
   float4 held[kHeld];
+  wait_for_previous();
   const float* from = p.part_o + row * p.D + 4 * c;
   const int64_t stride = p.rows * p.D;
   if (group < groups) {
@@ -86,7 +88,7 @@ __global__ void __launch_bounds__(kFwdThreads) join_fwd_kernel(const __grid_cons
 }
 
 struct JoinSums {
-  JoinSumParams p[2];
+  JoinSumParams p[kMaxSums];
 };
 
 // A thread takes eight channels of a row.
@@ -94,6 +96,7 @@ template <bool F16>
 __global__ void __launch_bounds__(kJoinThreads) join_sum_kernel(const __grid_constant__ JoinSums ps) {
   const JoinSumParams& p = ps.p[blockIdx.y];
   const int runs = p.of_keys ? cross_kv_runs(p.kv, p.lens) : p.runs;
+  wait_for_previous();
   if (p.of_keys && runs == 1) return;
   const int units = p.D / 8;
   const int64_t total = p.rows * units;
@@ -131,22 +134,22 @@ __global__ void __launch_bounds__(kJoinThreads) join_sum_kernel(const __grid_con
 }  // namespace
 
 cudaError_t join_fwd_launch(const JoinFwdParams& p, bool f16, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.rows), 1, 1);
-  cfg.blockDim = dim3(kFwdThreads, 1, 1);
-  cfg.stream = stream;
-  return f16 ? cudaLaunchKernelEx(&cfg, join_fwd_kernel<true>, p) : cudaLaunchKernelEx(&cfg, join_fwd_kernel<false>, p);
+  const dim3 grid(static_cast<unsigned>(p.rows), 1, 1);
+  return f16 ? launch_after(join_fwd_kernel<true>, grid, kFwdThreads, stream, p)
+             : launch_after(join_fwd_kernel<false>, grid, kFwdThreads, stream, p);
 }
 
 cudaError_t join_sum_launch(const JoinSumParams* p, int n, bool f16, cudaStream_t stream) {
   JoinSums ps;
-  for (int i = 0; i < 2; ++i) ps.p[i] = p[i < n ? i : 0];
-  const int64_t ctas = (p->rows * (p->D / 8) + kJoinThreads - 1) / kJoinThreads;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas < 65536 ? ctas : 65536), static_cast<unsigned>(n), 1);
-  cfg.blockDim = dim3(kJoinThreads, 1, 1);
-  cfg.stream = stream;
-  return f16 ? cudaLaunchKernelEx(&cfg, join_sum_kernel<true>, ps) : cudaLaunchKernelEx(&cfg, join_sum_kernel<false>, ps);
+  int64_t ctas = 0;
+  for (int i = 0; i < kMaxSums; ++i) {
+    ps.p[i] = p[i < n ? i : 0];
+    const int64_t c = (ps.p[i].rows * (ps.p[i].D / 8) + kJoinThreads - 1) / kJoinThreads;
+    ctas = c > ctas ? c : ctas;
+  }
+  const dim3 grid(static_cast<unsigned>(ctas < 65536 ? ctas : 65536), static_cast<unsigned>(n), 1);
+  return f16 ? launch_after(join_sum_kernel<true>, grid, kJoinThreads, stream, ps)
+             : launch_after(join_sum_kernel<false>, grid, kJoinThreads, stream, ps);
 }
 
 }  // namespace ea

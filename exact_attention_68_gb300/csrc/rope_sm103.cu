@@ -34,6 +34,7 @@
 #include <cuda_runtime.h>
 
 #include "bwd_common.cuh"
+#include "launch_after.cuh"
 #include "ptx.cuh"
 #include "rope_impl.h"
 
@@ -570,6 +571,7 @@ __global__ void __launch_bounds__(RopeTile<BWD>::kThreads, RopeTile<BWD>::kCtas)
   copy_wait<0>();
 
   if constexpr (BWD) {
+    launch_dependents();
     // the CTA's sum of each channel: the rows of its warps in their order
     __shared__ float s_acc[RT::kThreads * 16];
     for (int q = 0; q < p.n_parts; ++q) {
@@ -595,14 +597,24 @@ __global__ void __launch_bounds__(RopeTile<BWD>::kThreads, RopeTile<BWD>::kCtas)
 }
 
 // dweight[d] = Σ over CTAs: 32 channels a block, 32 runs of CTAs added in order.
+struct RopeSums {
+  RopeParams p;
+  int ctas;
+};
 template <bool F16>
-__global__ void __launch_bounds__(1024) rope_dweight_kernel(const __grid_constant__ RopeParams p, int ctas) {
+__global__ void __launch_bounds__(1024) rope_dweight_kernel(const __grid_constant__ RopeSums ps) {
+  const RopeParams& p = ps.p;
+  const int ctas = ps.ctas;
   const RopePart& q = p.part[blockIdx.y];
-  if (q.sums == nullptr) return;
+  if (q.sums == nullptr) {
+    wait_for_previous();
+    return;
+  }
   __shared__ float s[32][33];
   const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
   const int d = blockIdx.x * 32 + c;
   float v = 0.f;
+  wait_for_previous();
   if (d < p.D)
 #pragma unroll 8
     for (int i = r; i < ctas; i += 32) v += q.sums[(int64_t)i * p.D + d];
@@ -677,12 +689,10 @@ cudaError_t rope_bwd_launch(const RopeParams& p, RopeShape shape, bool f16, int 
   bool any = false;
   for (int i = 0; i < p.n_parts; ++i) any = any || p.part[i].sums != nullptr;
   if (!any) return cudaSuccess;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((p.D + 31) / 32), static_cast<unsigned>(p.n_parts), 1);
-  cfg.blockDim = dim3(1024, 1, 1);
-  cfg.stream = stream;
-  return f16 ? cudaLaunchKernelEx(&cfg, rope_dweight_kernel<true>, p, ctas)
-             : cudaLaunchKernelEx(&cfg, rope_dweight_kernel<false>, p, ctas);
+  const dim3 grid(static_cast<unsigned>((p.D + 31) / 32), static_cast<unsigned>(p.n_parts), 1);
+  const RopeSums sums = {p, ctas};
+  return f16 ? launch_after(rope_dweight_kernel<true>, grid, 1024, stream, sums)
+             : launch_after(rope_dweight_kernel<false>, grid, 1024, stream, sums);
 }
 
 }  // namespace ea
