@@ -105,12 +105,14 @@ struct XqLayout {
   static constexpr int kDrain = kStat + 1;
   static constexpr int kNumBars = kDrain + 1;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // tmem base, abort flag
-  static constexpr int kAlloc = kMiscOff + 16 + 1024;
+  static constexpr int kOrderOff = kMiscOff + 16;          // uint8 [kMaxOrder]
+  static constexpr int kAlloc = kOrderOff + kMaxOrder + 1024;
   static_assert(kAlloc <= 232448, "shared memory budget exceeded");
   static constexpr uint32_t kDqCol = 256, kQCol = 384, kDoCol = 384 + D / 2;
 };
 
-template <int D, bool F16>
+// ORDERED: units of long sequences first.
+template <int D, bool F16, bool ORDERED>
 __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_constant__ BwdParams p) {
   using L = XqLayout<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -125,7 +127,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
   const DbgBounds dbk = key_bounds<kMaskCross>(dbb, p.Sk);
   const int n_units = p.BH * p.n_qt * p.q_split;
   const int x0 = static_cast<int>(blockIdx.x), step = static_cast<int>(gridDim.x);
-  const BwdUnit unit0 = cross_dq_unit<kRowsX>(p, x0);  // the grid has no more CTAs than units
+  const uint8_t* order = ORDERED ? smem_raw + (sb - smem_u32(smem_raw)) + L::kOrderOff : nullptr;
+  BwdUnit unit0{};
+  if constexpr (ORDERED) {
+    if (warp == 9) order_by_length(p, lane, smem_raw + (sb - smem_u32(smem_raw)) + L::kOrderOff);
+  } else {
+    unit0 = cross_dq_unit<kRowsX>(p, x0);  // the grid has no more CTAs than units
+  }
+  // this CTA's unit `round`
+  auto unit_at = [&](int round) { return ORDERED ? to_and_fro(round, x0, step) : x0 + round * step; };
 
   if (threadIdx.x == 0) {
     launch_dependents();
@@ -151,6 +161,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
   tc_fence_after_sync();
   const uint32_t tmem_base = static_cast<uint32_t>(ld_volatile_shared(tmem_slot));
   const WaitCtl ctl{abort_addr, p.status, p.timeout_ns};
+  if constexpr (ORDERED) unit0 = cross_dq_unit<kRowsX>(p, x0, order);
 
   if (warp < 8) {
     // ======================= elementwise: delta, dS, dQ out =======================
@@ -166,7 +177,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
     int steps = 0;           // K/V tiles of the units before this one
     int kpos = 0, vpos = 0;  // and ring positions
     bool ok = true;
-    int x = x0;
     auto lse_of = [&](const BwdUnit& u) {
       const int grow = u.tile * kRowsX + row;
       return grow < p.S && dbg_row(dbb, u.bh, grow, 0, 0, kChkXRow) ? ldg_now(p.lse + (int64_t)u.bh * p.S + grow) : 0.f;
@@ -252,9 +262,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
       steps += un.n;
       kpos += 1 + un.n;
       vpos += 2 + un.n;
-      x += step;
+      const int x = unit_at(unit + 1);
       const bool more = x < n_units;
-      const BwdUnit nu = more ? cross_dq_unit<kRowsX>(p, x) : un;
+      const BwdUnit nu = more ? cross_dq_unit<kRowsX>(p, x, order) : un;
       if (more) lse = lse_of(nu);
 
       // dQ · scale → 16-bit → the ring's next place, swizzled → TMA store
@@ -326,7 +336,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
                    kSiteXqProd | 0x80 | (v_issued & 0x7f), kChkXLoadB);
       };
       BwdUnit un = unit0;
-      for (int x = x0; ok;) {
+      for (int unit = 0; ok;) {
         ok = put_v(&p.tm_do, dbb, un.tile * kRowsX, un.bh, pol_q) &&
              put_k(&p.tm_q, dbb, un.tile * kRowsX, un.bh, pol_q) &&
              put_v(&p.tm_out, dbb, un.tile * kRowsX, un.bh, pol_q);
@@ -338,9 +348,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
           ok = wait_bounded(bar(L::kKEmpty + st), ((k_issued / L::kKStages) & 1) ^ 1, ctl, kSiteXqProd | (k_issued & 0x7f));
           if (ok) mbar_arrive(bar(L::kKFull + st)), ++k_issued;
         }
-        x += step;
+        const int x = unit_at(++unit);
         if (x >= n_units) break;
-        un = cross_dq_unit<kRowsX>(p, x);
+        un = cross_dq_unit<kRowsX>(p, x, order);
       }
       if (ok) {
         // every stage released by the tensor core before this CTA may exit
@@ -408,7 +418,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
       return wait_warp(bar(L::kVFull + vp % L::kVStages), (vp / L::kVStages) & 1, kSiteXqMmaKV | 0x80 | (vp & 0x7f));
     };
     BwdUnit un = unit0;
-    int kpos = 0, vpos = 0, steps = 0, x = x0;  // the unit's first ring positions
+    int kpos = 0, vpos = 0, steps = 0;  // the unit's first ring positions
     bool ok = true;
     // tile j of the unit has landed; what lies behind the keys' end is silenced, as dQ's
     // product multiplies it by dS = 0
@@ -478,13 +488,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
       steps += un.n;
       kpos += 2 + un.n;
       vpos += 2 + un.n;
-      x += step;
+      const int x = unit_at(unit + 1);
       if (x >= n_units) {  // the last one's way out
         ok = wait_warp(bar(L::kOFree), unit & 1, kSiteXqMmaFree);
         if (ok && leader) mbar_arrive(bar(L::kKEmpty + (kpos - 1) % L::kKStages));
         break;
       }
-      un = cross_dq_unit<kRowsX>(p, x);
+      un = cross_dq_unit<kRowsX>(p, x, order);
     }
     if (leader) {
       mma_commit(bar(L::kDrain));
@@ -880,7 +890,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dkdv_kernel(const __grid
 
 template <int D, bool F16>
 cudaError_t launch_cross(const BwdParams& p, cudaStream_t stream) {
-  auto kdq = cross_dq_kernel<D, F16>;
+  // Long sequences first where a CTA takes few units, which may differ much: a decoder's
+  // ragged batch, 3.4 units a CTA, 93.3 us against 99.4 for the gradient (in their own
+  // order the SMs were active for 69 % of the dq kernel's time); two prompts, 6.7 units a
+  // CTA, 87.6 against 85.4, since the order has to be found and kept.
+  const long long q_units = (long long)p.BH * p.n_qt * p.q_split;
+  const bool ordered = p.lens != nullptr && p.BH / p.heads <= kMaxOrder && q_units < 5ll * p.sms;
+  auto kdq = ordered ? cross_dq_kernel<D, F16, true> : cross_dq_kernel<D, F16, false>;
   auto kkv = cross_dkdv_kernel<D, F16>;
   cudaError_t e = cudaFuncSetAttribute(kdq, cudaFuncAttributeMaxDynamicSharedMemorySize, XqLayout<D>::kAlloc);
   if (e != cudaSuccess) return e;
@@ -888,7 +904,7 @@ cudaError_t launch_cross(const BwdParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   auto ctas = [&](long long units) { return dim3(static_cast<unsigned>(units < p.sms ? units : p.sms), 1, 1); };
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = ctas((long long)p.BH * p.n_qt * p.q_split);
+  cfg.gridDim = ctas(q_units);
   cfg.blockDim = dim3(kBwdThreads, 1, 1);
   cfg.stream = stream;
   cfg.dynamicSmemBytes = XqLayout<D>::kAlloc;

@@ -13,7 +13,7 @@
 namespace ea {
 namespace {
 
-enum : int { kChkCrossLen = 0x7101, kChkCrossPart = 0x7102 };
+enum : int { kChkCrossLen = 0x5701 };
 
 // Keys of sequence b: lens[b], or all Sk.  A length outside [0, Sk] is reported
 // (every build) and brought to the nearer end.
@@ -80,17 +80,42 @@ struct BwdUnit {
   int bh, tile, first, n, len, part;
 };
 
-// dq: runs of K/V tiles of KEYS keys.
+// dq: runs of K/V tiles of KEYS keys.  order (may be null): the sequences in the order
+// in which their units are numbered.
 template <int KEYS>
-__device__ __forceinline__ BwdUnit cross_dq_unit(const BwdParams& p, int x) {
+__device__ __forceinline__ BwdUnit cross_dq_unit(const BwdParams& p, int x, const uint8_t* order = nullptr) {
   BwdUnit u;
   const int y = x / p.q_split;
   u.part = x - y * p.q_split;
   u.bh = y / p.n_qt;
   u.tile = y - u.bh * p.n_qt;
+  if (order != nullptr) {
+    const int b = u.bh / p.heads;
+    u.bh += (order[b] - b) * p.heads;
+  }
   u.len = cross_len(p.lens, u.bh / p.heads, p.Sk, p.status);
   cross_run(u.part, p.q_split, KEYS, &u.len, &u.first, &u.n);
   return u;
+}
+
+// The sequences by falling length (whole warp, batch <= 32): a sequence's rank is the
+// number of those before it.
+constexpr int kMaxOrder = 32;
+__device__ __forceinline__ void order_by_length(const BwdParams& p, int lane, uint8_t* order) {
+  const int batch = p.BH / p.heads;
+  const int len = lane < batch ? min(max(__ldg(p.lens + lane), 0), p.Sk) : -1;
+  int rank = 0;
+  for (int b = 0; b < batch; ++b) {
+    const int other = __shfl_sync(0xffffffffu, len, b);
+    rank += other > len || (other == len && b < lane) ? 1 : 0;
+  }
+  if (lane < batch) order[rank] = static_cast<uint8_t>(lane);
+}
+
+// Unit `round` of CTA cta: the units' numbers run to and fro over the CTAs, so that
+// who had the longest of one round has the shortest of the next.
+__device__ __forceinline__ int to_and_fro(int round, int cta, int ctas) {
+  return round & 1 ? (round + 1) * ctas - 1 - cta : round * ctas + cta;
 }
 
 // dk and dv: runs of Q tiles of ROWS queries, at most as many as there are, of every

@@ -33,7 +33,7 @@ namespace {
 
 constexpr float kLn2F = 0.6931471805599453f;
 
-enum : int { kChkFewRow = 0x7201 };
+enum : int { kChkFewRow = 0x5711 };
 
 template <int W, int RT>
 struct FewLayout {

@@ -25,7 +25,7 @@ namespace ea {
 namespace {
 
 constexpr int kSmallThreads = 256;
-enum : int { kChkSmallRow = 0x7301 };
+enum : int { kChkSmallRow = 0x5721 };
 
 template <int W>
 struct SmallLayout {

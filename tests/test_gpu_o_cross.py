@@ -245,6 +245,20 @@ def test_many_short_sequences(cuda_device):
     check_bwd(q, k, v, out, lse, dout, lens, D ** -0.5, grads)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_gradient_of_a_ragged_batch(cuda_device, D):
+    """A few units a CTA, of very different lengths: taken longest first; equal lengths, none and one among them."""
+    B, H, Sq, Sk = 6, 20, 400, 700
+    lens = [1, 700, 0, 700, 333, 129]
+    q, k, v, dout, ln = problem(B, H, H, Sq, Sk, D, lens, torch.float16, 26)
+    out, lse = cross.cross_fwd(q, k, v, ln)
+    grads = cross.cross_bwd(q, k, v, out, lse, dout, ln)
+    again = cross.cross_bwd(q, k, v, out, lse, dout, ln)
+    assert binding.device_status() == binding.ATTN_OK
+    check_bwd(q, k, v, out, lse, dout, lens, D ** -0.5, grads)
+    assert all(torch.equal(a, b) for a, b in zip(grads, again))
+
+
 def test_shared_inputs_and_repeated_use(cuda_device):
     """k and v one tensor, q among them; a graph of autograd used for two losses."""
     g = torch.Generator().manual_seed(25)
