@@ -91,44 +91,46 @@ struct JoinSums {
   JoinSumParams p[kMaxSums];
 };
 
-// A thread takes eight channels of a row.
+// A thread takes eight channels of a row, a CTA as many rows as fit.  What needs no sums
+// (the number of runs, found by one thread; the row's sequence) is done while the
+// kernel before this one ends.
 template <bool F16>
 __global__ void __launch_bounds__(kJoinThreads) join_sum_kernel(const __grid_constant__ JoinSums ps) {
   const JoinSumParams& p = ps.p[blockIdx.y];
-  const int runs = p.of_keys ? cross_kv_runs(p.kv, p.lens) : p.runs;
-  wait_for_previous();
-  if (p.of_keys && runs == 1) return;
-  const int units = p.D / 8;
-  const int64_t total = p.rows * units;
-  for (int64_t x = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x; x < total;
-       x += (int64_t)gridDim.x * kJoinThreads) {
-    const int64_t row = x / units;
-    bool there = true;
-    if (p.lens != nullptr) {
-      const int64_t slice = row / p.kv.Sk;
-      const int key = static_cast<int>(row - slice * p.kv.Sk);
-      const int n = min(max(__ldg(p.lens + slice / p.kv.heads), 0), p.kv.Sk);
-      if ((key & ~127) >= n) continue;
-      there = key < n;
-    }
-    float s[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] = 0.f;
-    if (there) {
-      const float* from = p.part + x * 8;
-#pragma unroll 8
-      for (int r = 0; r < runs; ++r) {
-        const float4* f = reinterpret_cast<const float4*>(from + r * p.rows * p.D);
-        const float4 a = __ldcg(f), b = __ldcg(f + 1);
-        s[0] += a.x, s[1] += a.y, s[2] += a.z, s[3] += a.w;
-        s[4] += b.x, s[5] += b.y, s[6] += b.z, s[7] += b.w;
-      }
-    }
-    uint4 v;
-    v.x = pack_x2<F16>(s[0] * p.mul, s[1] * p.mul), v.y = pack_x2<F16>(s[2] * p.mul, s[3] * p.mul);
-    v.z = pack_x2<F16>(s[4] * p.mul, s[5] * p.mul), v.w = pack_x2<F16>(s[6] * p.mul, s[7] * p.mul);
-    *reinterpret_cast<uint4*>(p.to + x * 8) = v;
+  __shared__ int s_runs;
+  if (threadIdx.x == 0) s_runs = p.of_keys ? cross_kv_runs(p.kv, p.lens) : p.runs;
+  const int units = p.D / 8, per_cta = kJoinThreads / units;
+  const int r = static_cast<int>(threadIdx.x) / units, c = static_cast<int>(threadIdx.x) - r * units;
+  const int64_t row = (int64_t)blockIdx.x * per_cta + r;
+  bool mine = r < per_cta && row < p.rows, there = true;
+  if (mine && p.lens != nullptr) {
+    const int slice = static_cast<int>(row) / p.kv.Sk, key = static_cast<int>(row) - slice * p.kv.Sk;
+    const int n = min(max(__ldg(p.lens + slice / p.kv.heads), 0), p.kv.Sk);
+    there = key < n;
+    mine = (key & ~127) < n;
   }
+  __syncthreads();
+  const int runs = s_runs;
+  wait_for_previous();
+  if (!mine || (p.of_keys && runs == 1)) return;
+  const int64_t at = row * p.D + 8 * c;
+  float s[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s[e] = 0.f;
+  if (there) {
+    const float* from = p.part + at;
+#pragma unroll 8
+    for (int i = 0; i < runs; ++i) {
+      const float4* f = reinterpret_cast<const float4*>(from + i * p.rows * p.D);
+      const float4 a = __ldcg(f), b = __ldcg(f + 1);
+      s[0] += a.x, s[1] += a.y, s[2] += a.z, s[3] += a.w;
+      s[4] += b.x, s[5] += b.y, s[6] += b.z, s[7] += b.w;
+    }
+  }
+  uint4 v;
+  v.x = pack_x2<F16>(s[0] * p.mul, s[1] * p.mul), v.y = pack_x2<F16>(s[2] * p.mul, s[3] * p.mul);
+  v.z = pack_x2<F16>(s[4] * p.mul, s[5] * p.mul), v.w = pack_x2<F16>(s[6] * p.mul, s[7] * p.mul);
+  *reinterpret_cast<uint4*>(p.to + at) = v;
 }
 
 }  // namespace
@@ -144,10 +146,13 @@ cudaError_t join_sum_launch(const JoinSumParams* p, int n, bool f16, cudaStream_
   int64_t ctas = 0;
   for (int i = 0; i < kMaxSums; ++i) {
     ps.p[i] = p[i < n ? i : 0];
-    const int64_t c = (ps.p[i].rows * (ps.p[i].D / 8) + kJoinThreads - 1) / kJoinThreads;
+    // work is cut into runs only where its tiles are few: fewer rows than 4 tiles an SM
+    if (ps.p[i].rows > INT32_MAX) return cudaErrorInvalidValue;
+    const int per_cta = kJoinThreads / (ps.p[i].D / 8);
+    const int64_t c = (ps.p[i].rows + per_cta - 1) / per_cta;
     ctas = c > ctas ? c : ctas;
   }
-  const dim3 grid(static_cast<unsigned>(ctas < 65536 ? ctas : 65536), static_cast<unsigned>(n), 1);
+  const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(n), 1);
   return f16 ? launch_after(join_sum_kernel<true>, grid, kJoinThreads, stream, ps)
              : launch_after(join_sum_kernel<false>, grid, kJoinThreads, stream, ps);
 }
