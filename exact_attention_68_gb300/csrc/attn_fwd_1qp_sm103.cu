@@ -272,7 +272,9 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
         // allowed key columns of this tile: 0 .. lim (causal: key <= query; key < S)
         int lim = CROSS ? un.len - 1 - (un.j0 + j) * kRowsP : p.S - 1 - j * kRowsP;
         if (CAUSAL) lim = min(lim, grow - j * kRowsP);
-        if (!valid) lim = -1;
+        // (cross-attention's rows behind the last query keep their zero scores: a row without
+        // a reference would have its warp compute every step's exponentials twice)
+        if (!CROSS && !valid) lim = -1;
         if (lim < kRowsP - 1) {
 #pragma unroll
           for (int c = 0; c < kRowsP; ++c)

@@ -93,25 +93,28 @@ int runs_of(int64_t units, int64_t steps, int sms, double step_us, double start,
 }
 
 struct FwdPlan {
-  bool few;            // the kernel for few queries
-  int tiles, cluster;  // its 16-row tiles a CTA, CTAs a cluster
+  bool few;     // the kernel for few queries
+  int cluster;  // its CTAs a slice
   int width, bn, n_qt, n_kt, runs;
   size_t space;
 };
 FwdPlan plan_fwd(const Sizes& s, int sms) {
   FwdPlan f;
-  f.few = s.rows <= ea::kFewRows;
+  // Few queries of up to 64 channels.  Against the persistent kernel, 16 rows: 128
+  // slices of 1500 keys 11.5 us and 13.6, 4 slices of 16384 keys 10.3 and 9.9 (one row
+  // 8.3 and 9.7), 256 of 2000 keys 25.2 and 30.3, 16 of 300 keys 6.1 and 6.7.  Two tiles
+  // of 16 rows: 16.0 and 13.9, 12.7 and 10.3, 30.8 and 30.3, 8.4 and 6.6; 128 channels,
+  // one row: 18.5 and 15.7, 10.8 and 10.6, 44.3 and 42.9, 6.9 and 7.4; 256 channels: 47
+  // and 34, 38 and 13.
+  f.few = s.rows <= ea::kFewRows && s.D <= ea::kFewWidth;
   if (f.few) {
-    f.width = ea::kernel_head_dim(s.D);
-    f.tiles = s.rows <= 16 || f.width == 256 ? 1 : 2;
-    f.n_qt = static_cast<int>((s.rows + 16 * f.tiles - 1) / (16 * f.tiles));
-    const int64_t slices = s.BH * f.n_qt;
-    // As many CTAs as the SMs hold at once (two each, one of 256 channels), not more:
+    const int64_t slices = s.BH;
+    // As many CTAs as the SMs hold at once (two each), not more:
     // 128 slices of 64 channels, 300 to 1500 keys, took 14.1 us with one a slice, 11.4
     // with two, 14.2 with four, 22.4 with eight.  A cluster of up to 8 shares a
     // slice; where those leave half of the SMs idle, and there are chunks of keys for
     // more, the keys are cut into runs.
-    const int64_t resident = f.width == 256 ? sms : 2 * sms, chunks = (s.Sk + 127) / 128;
+    const int64_t resident = 2 * sms, chunks = (s.Sk + 127) / 128;
     f.cluster = 1, f.runs = 1;
     while (f.cluster < 8 && slices * f.cluster * 2 <= resident && f.cluster * 2 <= chunks) f.cluster *= 2;
     if (f.cluster == 8) {
@@ -143,6 +146,9 @@ BwdPlan plan_bwd(const attn_cross_t& c, const Sizes& s, int sms) {
   BwdPlan b;
   std::memset(&b, 0, sizeof(b));
   b.width = ea::kernel_head_dim(s.D);
+  // Less than a tile both ways: a CTA a slice.  64 queries and keys, 16 slices of 64
+  // channels 5.8 us against 10.4, 512 of them 16.1 against 30.4; of 128 channels 9.0
+  // against 12.3 and 26.3 against 38.2.
   b.small = s.rows <= ea::kSmallSide && s.Sk <= ea::kSmallSide;
   if (b.small) {
     b.space = kNoSpace;
@@ -241,9 +247,9 @@ attn_status_t attn_cross_fwd(const attn_cross_t* sizes, const void* q, const voi
     p.status = status;
     p.BH = static_cast<int>(s.BH), p.heads = static_cast<int>(sizes->heads), p.rows = static_cast<int>(s.rows);
     p.Sk = static_cast<int>(s.Sk), p.D = j.D;
-    p.groups = f.n_qt, p.cluster = f.cluster, p.runs = f.runs;
+    p.cluster = f.cluster, p.runs = f.runs;
     p.scale_log2 = scale_log2;
-    cudaError_t e = ea::cross_few_launch(p, f.width, f.tiles, f16, stream);
+    cudaError_t e = ea::cross_few_launch(p, f16, stream);
     if (e == cudaSuccess && f.runs > 1) e = ea::join_fwd_launch(j, f16, stream);
     return launched(e);
   }

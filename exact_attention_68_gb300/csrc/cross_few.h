@@ -7,7 +7,7 @@
 
 namespace ea {
 
-constexpr int kFewRows = 32;  // rows of a slice that it is made for
+constexpr int kFewRows = 16, kFewWidth = 64;  // rows and channels of a slice that it is made for
 
 struct FewParams {
   const uint16_t* q;  // [BH, rows, D]
@@ -20,14 +20,12 @@ struct FewParams {
   float* part_lse;    // [runs, BH, rows]
   int* status;
   int BH, heads, rows, Sk, D;
-  int groups;         // of 16 · tiles rows
-  int cluster;        // CTAs that share a group's keys: 1, 2, 4 or 8
+  int cluster;        // CTAs that share a slice's keys: 1, 2, 4 or 8
   int runs;           // into which they are cut first
   float scale_log2;
 };
 
-// width: 64, 128 or 256 columns; tiles: of 16 rows a CTA takes, 1 or 2 (256 columns: 1).
-cudaError_t cross_few_launch(const FewParams& p, int width, int tiles, bool f16, cudaStream_t stream);
+cudaError_t cross_few_launch(const FewParams& p, bool f16, cudaStream_t stream);
 
 constexpr int kSmallSide = 64;  // queries and keys of a slice that the small gradient takes
 

@@ -1,14 +1,16 @@
 // cross_few_sm103.cu — cross-attention of few queries (a decoder's next tokens) on
-// GB300 (sm_103a): up to 32 rows a slice, the G query heads of a key head together.
+// GB300 (sm_103a): up to 16 rows a slice, the G query heads of a key head together, of up
+// to 64 channels.
 //
 // Bound by the memory: K and V are read once for a handful of rows.  The persistent
 // kernel pads them to 128 rows and pays its pipeline's start for a few steps; here
 // what counts is how soon all SMs have enough loads in flight and how short the
-// chain behind the last one is.
+// chain behind the last one is.  (Beyond 16 rows, or 64 channels, the persistent
+// kernel is the faster one: cross_api.cu.)
 //
-//   A warp works by itself: it takes chunks of 32 keys (16 beyond 64 channels), brings K
+//   A warp works by itself: it takes chunks of 32 keys, brings K
 //   and V of the next ones into its own ring in shared memory (cp.async), and keeps
-//   its own running maximum, sums and output for 16 or 32 rows in registers:
+//   its own running maximum, sums and output for 16 rows in registers:
 //   S = Q·Kᵀ and O += P·V by mma.sync m16n8k16, P from S's registers.  16 rows cost
 //   what one does; the products take a fifth of the memory's time at 16 rows.
 //   Keys behind the sequence's end are not read: their copies fill in zeros.
@@ -17,6 +19,11 @@
 //   shared memory, each CTA a share of the values: one launch, no workspace.  Where
 //   even clusters of 8 leave SMs idle (few slices, long keys) the keys are cut
 //   into runs first, which a second kernel joins.
+//
+// Measured on a GB300, calls in a graph: 8 x 16 slices of one query, 300 to 1500 keys of
+// 64 channels in fp16 11 us, 2.7 TB/s; the persistent kernel takes 13.5.  By then all of K
+// and V has long been asked for; the rest is launch, length, first chunk and the two joins
+// one after the other.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -35,16 +42,16 @@ constexpr float kLn2F = 0.6931471805599453f;
 
 enum : int { kChkFewRow = 0x5711 };
 
-template <int W, int RT>
 struct FewLayout {
+  static constexpr int W = 64;
   static constexpr int kWarps = 4;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kChunk = W == 64 ? 32 : 16;       // keys of a warp's step
-  static constexpr int kStages = 3;                      // 96 KB a CTA, two of them an SM (256 columns: 192)
+  static constexpr int kChunk = 32;                      // keys of a warp's step
+  static constexpr int kStages = 3;                      // 96 KB a CTA, two of them an SM
   static constexpr int kRow = W * 2;                     // bytes
   static constexpr int kPart = kChunk * kRow;            // K or V of a chunk
   static constexpr int kWarpRing = kStages * 2 * kPart;
-  static constexpr int kRows = 16 * RT;
+  static constexpr int kRows = kFewRows;
   static constexpr int kQOff = 0;
   static constexpr int kRingOff = kQOff + kRows * kRow;
   static constexpr int kOut = kRows * W * 4;             // one fp32 output
@@ -97,9 +104,10 @@ __device__ __forceinline__ void st_shared_f2(uint32_t addr, float a, float b) {
 // neither has a finite score (its sums are then 0, or NaN, which stays)
 __device__ __forceinline__ float weight_of(float m, float ref) { return ref == -INFINITY ? 1.f : ex2_approx(m - ref); }
 
-template <int W, int RT, bool F16>
-__global__ void __launch_bounds__(FewLayout<W, RT>::kThreads) cross_few_kernel(const __grid_constant__ FewParams p) {
-  using L = FewLayout<W, RT>;
+template <bool F16>
+__global__ void __launch_bounds__(FewLayout::kThreads) cross_few_kernel(const __grid_constant__ FewParams p) {
+  using L = FewLayout;
+  constexpr int W = L::W;
   constexpr int kUnits = W / 8;  // 16-byte units of a row
   constexpr int kFewWarps = L::kWarps, kFewThreads = L::kThreads;
   extern __shared__ __align__(128) uint8_t few_smem[];
@@ -109,9 +117,7 @@ __global__ void __launch_bounds__(FewLayout<W, RT>::kThreads) cross_few_kernel(c
   if (p.runs > 1) launch_dependents();
   int x = static_cast<int>(blockIdx.x) / p.cluster;
   const int run = x % p.runs;
-  x /= p.runs;
-  const int group = x % p.groups, bh = x / p.groups;
-  const int row0 = group * L::kRows, rows = min(L::kRows, p.rows - row0);
+  const int bh = x / p.runs, rows = p.rows;
   const int len = cross_len(p.lens, bh / p.heads, p.Sk, p.status);
   const int ksteps = (p.D + 15) / 16;
 
@@ -149,8 +155,8 @@ __global__ void __launch_bounds__(FewLayout<W, RT>::kThreads) cross_few_kernel(c
   for (int i = threadIdx.x; i < L::kRows * kUnits; i += kFewThreads) {
     const int r = i / kUnits, u = i % kUnits;
     const bool in = r < rows && 8 * u < p.D;
-    if (kDebugChecks && in && row0 + r >= p.rows) dbg_fail(p.status, kChkFewRow);
-    const uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(p.q + ((int64_t)bh * p.rows + row0 + r) * p.D + 8 * u))
+    if (kDebugChecks && in && (bh >= p.BH || rows > L::kRows)) dbg_fail(p.status, kChkFewRow);
+    const uint4 v = in ? __ldg(reinterpret_cast<const uint4*>(p.q + ((int64_t)bh * p.rows + r) * p.D + 8 * u))
                        : make_uint4(0u, 0u, 0u, 0u);
     st_shared_v4(sb + L::kQOff + at(r, u), v.x, v.y, v.z, v.w);
   }
@@ -159,17 +165,14 @@ __global__ void __launch_bounds__(FewLayout<W, RT>::kThreads) cross_few_kernel(c
       st_shared_v4(ring + (i / L::kChunk) * 2 * L::kPart + at(i % L::kChunk, p.D / 8), 0u, 0u, 0u, 0u);
   __syncthreads();
 
-  float o[RT][kUnits][4];  // O: rows lane/4 and + 8 of a tile, channels 8n + 2·(lane % 4), + 1
-  float m[RT][2], l[RT][2], lq[RT][2];
+  float o[kUnits][4];  // O: rows lane/4 and + 8, channels 8n + 2·(lane % 4), + 1
+  float m[2], l[2], lq[2];
 #pragma unroll
-  for (int t = 0; t < RT; ++t) {
+  for (int n = 0; n < kUnits; ++n)
 #pragma unroll
-    for (int n = 0; n < kUnits; ++n)
+    for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[t][n][e] = 0.f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) m[t][h] = -INFINITY, l[t][h] = lq[t][h] = 0.f;
-  }
+  for (int h = 0; h < 2; ++h) m[h] = -INFINITY, l[h] = lq[h] = 0.f;
   constexpr int kTiles = L::kChunk / 8;  // of 8 keys
   const int mi = lane >> 3, mr = lane & 7;  // matrix and row of this lane's ldmatrix address
   int stage = 0;
@@ -177,28 +180,22 @@ __global__ void __launch_bounds__(FewLayout<W, RT>::kThreads) cross_few_kernel(c
     copies_wait<L::kStages - 2>();
     __syncwarp();
     const uint32_t kt = ring + stage * 2 * L::kPart, vt = kt + L::kPart;
-    float s[RT][kTiles][4];
+    float s[kTiles][4];
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
+    for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-      for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[t][n][e] = 0.f;
+      for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
 #pragma unroll
     for (int kk = 0; kk < W / 16; ++kk) {
       if (kk >= ksteps) break;
-      uint32_t a[RT][4];
-#pragma unroll
-      for (int t = 0; t < RT; ++t) ldm4(a[t], sb + L::kQOff + at(16 * t + (mi & 1) * 8 + mr, 2 * kk + (mi >> 1)));
+      uint32_t a[4];
+      ldm4(a, sb + L::kQOff + at((mi & 1) * 8 + mr, 2 * kk + (mi >> 1)));
 #pragma unroll
       for (int n = 0; n < kTiles; n += 2) {
         uint32_t b[4];  // keys 8n .. +7: channels lo, hi; keys 8n + 8 ..: lo, hi
         ldm4(b, kt + at(8 * n + (mi >> 1) * 8 + mr, 2 * kk + (mi & 1)));
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          mma16816<F16>(s[t][n], a[t], b[0], b[1]);
-          mma16816<F16>(s[t][n + 1], a[t], b[2], b[3]);
-        }
+        mma16816<F16>(s[n], a, b[0], b[1]);
+        mma16816<F16>(s[n + 1], a, b[2], b[3]);
       }
     }
     // keys that are not there
@@ -208,69 +205,58 @@ __global__ void __launch_bounds__(FewLayout<W, RT>::kThreads) cross_few_kernel(c
       for (int n = 0; n < kTiles; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (8 * n + 2 * (lane & 3) + (e & 1) >= left)
-#pragma unroll
-            for (int t = 0; t < RT; ++t) s[t][n][e] = -INFINITY;
+          if (8 * n + 2 * (lane & 3) + (e & 1) >= left) s[n][e] = -INFINITY;
     }
-    uint32_t pk[RT][kTiles][2];  // P of the two rows, packed
+    uint32_t pk[kTiles][2];  // P of the two rows, packed
+    float alpha[2];
+    bool moved = false;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      float alpha[2];
-      bool moved = false;
+    for (int h = 0; h < 2; ++h) {
+      float mx = -INFINITY;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float mx = -INFINITY;
+      for (int n = 0; n < kTiles; ++n) mx = fmaxf(mx, fmaxf(s[n][2 * h], s[n][2 * h + 1]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float to = fmaxf(m[h], mx * p.scale_log2);
+      alpha[h] = m[h] == to ? 1.f : ex2_approx(m[h] - to);  // 0 from -inf
+      moved = moved || (alpha[h] != 1.f && m[h] != -INFINITY);
+      m[h] = to;
+      const float neg = to == -INFINITY ? 0.f : -to;
+      float sum = 0.f, sum_q = 0.f;
 #pragma unroll
-        for (int n = 0; n < kTiles; ++n) mx = fmaxf(mx, fmaxf(s[t][n][2 * h], s[t][n][2 * h + 1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float to = fmaxf(m[t][h], mx * p.scale_log2);
-        alpha[h] = m[t][h] == to ? 1.f : ex2_approx(m[t][h] - to);  // 0 from -inf
-        moved = moved || (alpha[h] != 1.f && m[t][h] != -INFINITY);
-        m[t][h] = to;
-        const float neg = to == -INFINITY ? 0.f : -to;
-        float sum = 0.f, sum_q = 0.f;
-#pragma unroll
-        for (int n = 0; n < kTiles; ++n) {
-          const float p0 = ex2_approx(fmaf(s[t][n][2 * h], p.scale_log2, neg));
-          const float p1 = ex2_approx(fmaf(s[t][n][2 * h + 1], p.scale_log2, neg));
-          sum += p0 + p1;
-          pk[t][n][h] = pack_x2<F16>(p0, p1);
-          // what the products weigh with: it normalises the output
-          if constexpr (F16) {
-            const float2 q2 = f16x2_to_f32(pk[t][n][h]);
-            sum_q += q2.x + q2.y;
-          } else {
-            sum_q += bf16_lo(pk[t][n][h]) + bf16_hi(pk[t][n][h]);
-          }
+      for (int n = 0; n < kTiles; ++n) {
+        const float p0 = ex2_approx(fmaf(s[n][2 * h], p.scale_log2, neg));
+        const float p1 = ex2_approx(fmaf(s[n][2 * h + 1], p.scale_log2, neg));
+        sum += p0 + p1;
+        pk[n][h] = pack_x2<F16>(p0, p1);
+        // what the products weigh with: it normalises the output
+        if constexpr (F16) {
+          const float2 q2 = f16x2_to_f32(pk[n][h]);
+          sum_q += q2.x + q2.y;
+        } else {
+          sum_q += bf16_lo(pk[n][h]) + bf16_hi(pk[n][h]);
         }
-        l[t][h] = l[t][h] * alpha[h] + sum;
-        lq[t][h] = lq[t][h] * alpha[h] + sum_q;
       }
-      if (__any_sync(0xffffffffu, moved)) {
+      l[h] = l[h] * alpha[h] + sum;
+      lq[h] = lq[h] * alpha[h] + sum_q;
+    }
+    if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int n = 0; n < kUnits; ++n) {
-          o[t][n][0] *= alpha[0], o[t][n][1] *= alpha[0];
-          o[t][n][2] *= alpha[1], o[t][n][3] *= alpha[1];
-        }
+      for (int n = 0; n < kUnits; ++n) {
+        o[n][0] *= alpha[0], o[n][1] *= alpha[0];
+        o[n][2] *= alpha[1], o[n][3] *= alpha[1];
       }
     }
 #pragma unroll
     for (int kg = 0; kg < kTiles / 2; ++kg) {  // 16 keys
-      uint32_t a[RT][4];
-#pragma unroll
-      for (int t = 0; t < RT; ++t)
-        a[t][0] = pk[t][2 * kg][0], a[t][1] = pk[t][2 * kg][1], a[t][2] = pk[t][2 * kg + 1][0], a[t][3] = pk[t][2 * kg + 1][1];
+      const uint32_t a[4] = {pk[2 * kg][0], pk[2 * kg][1], pk[2 * kg + 1][0], pk[2 * kg + 1][1]};
 #pragma unroll
       for (int n = 0; n < kUnits; n += 2) {
         if (n / 2 >= ksteps) break;
         uint32_t b[4];  // channels 8n .. +7: keys lo, hi; channels 8n + 8 ..: lo, hi
         ldm4_trans(b, vt + at(16 * kg + (mi & 1) * 8 + mr, n + (mi >> 1)));
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          mma16816<F16>(o[t][n], a[t], b[0], b[1]);
-          mma16816<F16>(o[t][n + 1], a[t], b[2], b[3]);
-        }
+        mma16816<F16>(o[n], a, b[0], b[1]);
+        mma16816<F16>(o[n + 1], a, b[2], b[3]);
       }
     }
     __syncwarp();
@@ -282,23 +268,21 @@ __global__ void __launch_bounds__(FewLayout<W, RT>::kThreads) cross_few_kernel(c
 
   const uint32_t outs = sb + L::kRingOff, stats = sb + L::kStatOff;
 #pragma unroll
-  for (int t = 0; t < RT; ++t)
+  for (int h = 0; h < 2; ++h) {
+    const int r = 8 * h + (lane >> 2);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = 16 * t + 8 * h + (lane >> 2);
-#pragma unroll
-      for (int d = 1; d <= 2; d <<= 1) {  // the row's four lanes
-        l[t][h] += __shfl_xor_sync(0xffffffffu, l[t][h], d);
-        lq[t][h] += __shfl_xor_sync(0xffffffffu, lq[t][h], d);
-      }
-      if (r < rows) {
-        if ((lane & 3) == 0) st_shared_f4(stats + (warp * L::kRows + r) * 16, make_float4(m[t][h], l[t][h], lq[t][h], 0.f));
-#pragma unroll
-        for (int n = 0; n < kUnits; ++n)
-          if (8 * n < p.D)
-            st_shared_f2(outs + ((warp * L::kRows + r) * W + 8 * n + 2 * (lane & 3)) * 4, o[t][n][2 * h], o[t][n][2 * h + 1]);
-      }
+    for (int d = 1; d <= 2; d <<= 1) {  // the row's four lanes
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], d);
+      lq[h] += __shfl_xor_sync(0xffffffffu, lq[h], d);
     }
+    if (r < rows) {
+      if ((lane & 3) == 0) st_shared_f4(stats + (warp * L::kRows + r) * 16, make_float4(m[h], l[h], lq[h], 0.f));
+#pragma unroll
+      for (int n = 0; n < kUnits; ++n)
+        if (8 * n < p.D)
+          st_shared_f2(outs + ((warp * L::kRows + r) * W + 8 * n + 2 * (lane & 3)) * 4, o[n][2 * h], o[n][2 * h + 1]);
+    }
+  }
   __syncthreads();
   // the CTA's part: its warps' joined.  Where it is alone, the result.
   const uint32_t cta_out = outs + kFewWarps * L::kOut, cta_stat = stats + kFewWarps * L::kRows * 16;
@@ -306,7 +290,7 @@ __global__ void __launch_bounds__(FewLayout<W, RT>::kThreads) cross_few_kernel(c
   auto finish = [&](int r, int c, float4 a, float mx, float sum, float sum_q) {
     const float inv = sum_q == 0.f ? 0.f : 1.f / sum_q;
     a.x *= inv, a.y *= inv, a.z *= inv, a.w *= inv;
-    const int64_t row = (int64_t)bh * p.rows + row0 + r;
+    const int64_t row = (int64_t)bh * p.rows + r;
     const float lse = (mx + log2f(sum)) * kLn2F;
     if (p.runs > 1) {
       const int64_t part = (int64_t)run * p.BH * p.rows + row;
@@ -374,14 +358,14 @@ __global__ void __launch_bounds__(FewLayout<W, RT>::kThreads) cross_few_kernel(c
   cluster_sync();  // nobody leaves while others read its part
 }
 
-template <int W, int RT, bool F16>
+template <bool F16>
 cudaError_t launch_few(const FewParams& p, cudaStream_t stream) {
-  using L = FewLayout<W, RT>;
-  auto kern = cross_few_kernel<W, RT, F16>;
+  using L = FewLayout;
+  auto kern = cross_few_kernel<F16>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((long long)p.BH * p.groups * p.runs * p.cluster), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>((long long)p.BH * p.runs * p.cluster), 1, 1);
   cfg.blockDim = dim3(L::kThreads, 1, 1);
   cfg.dynamicSmemBytes = L::kAlloc;
   cfg.stream = stream;
@@ -394,17 +378,10 @@ cudaError_t launch_few(const FewParams& p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <bool F16>
-cudaError_t launch_width(const FewParams& p, int width, int tiles, cudaStream_t stream) {
-  if (width == 64) return tiles == 1 ? launch_few<64, 1, F16>(p, stream) : launch_few<64, 2, F16>(p, stream);
-  if (width == 128) return tiles == 1 ? launch_few<128, 1, F16>(p, stream) : launch_few<128, 2, F16>(p, stream);
-  return launch_few<256, 1, F16>(p, stream);
-}
-
 }  // namespace
 
-cudaError_t cross_few_launch(const FewParams& p, int width, int tiles, bool f16, cudaStream_t stream) {
-  return f16 ? launch_width<true>(p, width, tiles, stream) : launch_width<false>(p, width, tiles, stream);
+cudaError_t cross_few_launch(const FewParams& p, bool f16, cudaStream_t stream) {
+  return f16 ? launch_few<true>(p, stream) : launch_few<false>(p, stream);
 }
 
 }  // namespace ea

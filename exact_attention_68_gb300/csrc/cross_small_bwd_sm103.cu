@@ -8,6 +8,9 @@
 // products as two 16-bit terms each (a value and what its rounding left, together 16
 // bits or more), which a kernel of this size has the time for.
 //
+// (Rounded once, the gradients of such slices were up to 1.5 times as far from the
+// definition as those of a plain form in the same types.)
+//
 //   q, k, v and dout lie in shared memory, 128-byte-swizzled rows; S = q·kᵀ and dP =
 //   dout·vᵀ by mma.sync in 16 x 32 tiles of 8 warps; P and dS from the registers to
 //   shared memory; then dq, dk, dv, each warp a 16-row tile and half of the channels.

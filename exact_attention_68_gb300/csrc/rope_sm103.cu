@@ -26,7 +26,16 @@
 //
 // The gradient of the weights: each thread adds up its channels over all rows
 // that it takes, the CTA adds its threads' sums in a fixed order, and a second
-// kernel the CTAs'.
+// kernel, set up while the first ends, the CTAs'.
+//
+// Measured on a GB300, calls in a graph.  2 x 4096 tokens of 32 + 8 + 8 heads of 128
+// channels: 39 us, 5.1 TB/s, 77 % of what a plain copy gets; the gradient 61.5 us, 4.6
+// TB/s.  12720 tokens of 3 x 16 heads of 72 channels in neighbouring pairs: 51 and 81
+// us, 52 % and 43 %: a row of 144 bytes fills four and a half lanes, and both run at
+// half of the issue slots with the latency of shared memory in between.  One token of 16
+// sequences: 8 us, a chain of positions, angles, rows and stores.  A CTA for eight
+// tokens with its rows in registers took 60 us for the first; one row a lane, 42 to
+// 47; rings of 2 or 4 and other numbers of CTAs, 40 to 52.
 #include <type_traits>
 
 #include <cuda_bf16.h>
