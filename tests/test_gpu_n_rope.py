@@ -230,6 +230,39 @@ def test_many_tokens_of_few_heads(cuda_device):
     close(dw[0], rw, mw, torch.float32, D, chain=B * S // 600 + 700, what="dw")
 
 
+def test_gradients_that_overlap(cuda_device):
+    """Two launches a call, the second set up while the first ends: on two streams at once, again and again, each
+    input written just before and each result read just after."""
+    cases = []
+    for seed, (D, dt) in enumerate(((64, torch.bfloat16), (128, torch.float16))):
+        plan = plan_of(D // 2, 1, False)
+        _, xs, ws, pos, dys = problem(2, 301, (4, 2, 2), D, D // 2, 1, dt, "same", 90 + seed)
+        cases.append((xs, ws, pos, dys, plan, rope.rope_bwd(dys, xs, plan, pos, ws, 1e-6, (True, True, False))))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(8):
+        got = []
+        for (xs, ws, pos, dys, plan, _), st in zip(cases, streams):
+            with torch.cuda.stream(st):
+                fresh = [d.clone() for d in dys]
+                dxs, dws = rope.rope_bwd(fresh, xs, plan, pos, ws, 1e-6, (True, True, False))
+                got.append([x.clone() for x in (*dxs, *dws[:2])])
+                for x in (*fresh, *dxs, *dws[:2]):
+                    x.zero_()
+    torch.cuda.synchronize()
+    for (*_, (dxs, dws)), g in zip(cases, got):
+        assert all(torch.equal(a, b) for a, b in zip((*dxs, *dws[:2]), g))
+
+
+def test_second_derivatives_are_refused(cuda_device):
+    x = torch.randn(1, 4, 2, 64, device="cuda").to(torch.bfloat16).requires_grad_()
+    pos = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+    y = rope.norm_rope((x,), rope.rope_plan(64), pos)[0]
+    (dx,) = torch.autograd.grad(y.float().square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(dx.float().sum(), x)
+
+
 def test_no_finite_rows_stay_by_themselves(cuda_device):
     """Rows with NaN or infinities, and rows of zeros, leave every other row as it is."""
     g = torch.Generator().manual_seed(9)

@@ -330,6 +330,32 @@ def test_calls_that_overlap(cuda_device):
         assert torch.equal(w[0], g[0]) and torch.equal(w[1], g[1])
 
 
+def test_gradients_that_overlap(cuda_device):
+    """Calls of several kernels each, which are set up while one another end, on three streams at once and over and
+    over on one; inputs that the kernel before wrote, results that the next one reads."""
+    shapes = (((4, 12, 12, 300, 600, [600, 1, 0, 333]), 64), ((2, 8, 2, 100, 900, [900, 400]), 128),
+              ((1, 2, 2, 700, 400, [399]), 256))
+    calls = [problem(*s[:5], D, s[5], torch.bfloat16, 43 + i) for i, (s, D) in enumerate(shapes)]
+    fwd = [cross.cross_fwd(*c[:3], c[4]) for c in calls]
+    want = [cross.cross_bwd(*c[:3], *f, c[3], c[4]) for c, f in zip(calls, fwd)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(8):
+        got = []
+        for c, st in zip(calls, streams):
+            with torch.cuda.stream(st):
+                dout = c[3].clone()
+                f = cross.cross_fwd(*c[:3], c[4])
+                g = cross.cross_bwd(*c[:3], *f, dout, c[4])
+                got.append([x.clone() for x in g])
+                for x in (dout, *f, *g):
+                    x.zero_()
+    torch.cuda.synchronize()
+    assert binding.device_status() == binding.ATTN_OK
+    for w, g in zip(want, got):
+        assert all(torch.equal(a, b) for a, b in zip(w, g))
+
+
 def test_bad_lengths_are_reported(cuda_device):
     q, k, v, dout, _ = problem(3, 2, 2, 20, 100, 64, None, torch.bfloat16, 51)
     for Sq in (20, 1):
