@@ -470,12 +470,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_q64_kernel(const
   int runs = 1;   // that the sums are cut into
   BwdUnit un{};
   if constexpr (CROSS) {
-    // the key tiles without keys are zeroed by all; what is left has a CTA each
-    cross_zero_tiles(p, unit, static_cast<int>(gridDim.x >> 1), threadIdx.x, kBwdThreads, kCols * half, kCols);
+    // a CTA for as many runs as there may be, those that there are first; a tile without
+    // keys is zeroed by its first
     runs = cross_kv_runs(p.kv, p.lens);
-    KvWalk walk = kv_walk(unit, runs);
-    if (!cross_kv_unit<kStepW>(p, walk, &un)) return;
-    bh = un.bh, j = un.tile, u0 = un.first, n_sub = un.n, keys = un.len;
+    const int tiles = p.BH * p.n_kt;
+    un.part = unit / tiles;
+    const int z = unit - un.part * tiles;
+    bh = z / p.n_kt, j = z - bh * p.n_kt;
+    keys = cross_len(p.lens, bh / p.heads, p.Sk, p.status);
+    if (un.part >= runs) return;
+    if (j * kRowsW >= keys) {
+      if (un.part == 0) cross_zero_tiles(p, z, tiles, threadIdx.x, kBwdThreads, kCols * half, kCols);
+      return;
+    }
+    int rows = p.S;
+    cross_run(un.part, runs, kStepW, &rows, &u0, &n_sub);
   } else {
     int level;
     schedule_unit(p.sched, unit, &bh, &level);

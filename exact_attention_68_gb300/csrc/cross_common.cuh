@@ -125,9 +125,11 @@ struct KvWalk {
   int x, b, before;  // unit asked for; a sequence, and the units of those before it
   int runs;          // of a key tile's Q tiles
 };
+constexpr int kWalkBy = 8;
 __device__ __forceinline__ KvWalk kv_walk(int x, int runs) { return {x, 0, 0, runs}; }
-// The unit the walk is at; false: none left.
-template <int ROWS>
+// The unit the walk is at; false: none left.  MANY: by kWalkBy sequences at a time
+// where it may go that far.
+template <int ROWS, bool MANY>
 __device__ __forceinline__ bool cross_kv_unit(const BwdParams& p, KvWalk& w, BwdUnit* u) {
   const int batch = p.BH / p.heads;
   int tiles = 0;
@@ -138,6 +140,18 @@ __device__ __forceinline__ bool cross_kv_unit(const BwdParams& p, KvWalk& w, Bwd
     const int units = p.heads * tiles * w.runs;
     if (w.x - w.before < units) break;
     w.before += units;
+    if constexpr (MANY) {
+      // Eight sequences further at least, whatever their lengths: these are asked for
+      // together.  A length out of range is reported where its queries are.
+      const int each = p.heads * w.runs;
+      while (w.x - w.before >= each * kWalkBy * p.n_kt && w.b + kWalkBy < batch) {
+        int sum = 0;
+#pragma unroll
+        for (int i = 1; i <= kWalkBy; ++i) sum += (min(max(__ldg(p.lens + w.b + i), 0), p.Sk) + 127) / 128;
+        w.before += each * sum;
+        w.b += kWalkBy;
+      }
+    }
   }
   const int y = w.x - w.before, z = y / w.runs;
   u->part = y - z * w.runs;

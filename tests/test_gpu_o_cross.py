@@ -259,6 +259,27 @@ def test_gradient_of_a_ragged_batch(cuda_device, D):
     assert all(torch.equal(a, b) for a, b in zip(grads, again))
 
 
+@pytest.mark.parametrize("D,B", [(64, 1500), (128, 700), (256, 300)])
+def test_gradients_of_very_many_sequences(cuda_device, D, B):
+    """Several rounds of a unit a CTA, sequences of one tile or none; and a wrong length among them is found."""
+    lens = [(i * 53) % 101 if i % 4 else 0 for i in range(B)]
+    q, k, v, dout, ln = problem(B, 1, 1, 70, 100, D, lens, torch.float16, 27)
+    out, lse = cross.cross_fwd(q, k, v, ln)
+    grads = cross.cross_bwd(q, k, v, out, lse, dout, ln)
+    assert binding.device_status() == binding.ATTN_OK
+    check_bwd(q, k, v, out, lse, dout, lens, D ** -0.5, grads)
+    for at, wrong, meant in ((B - 2, 101, 100), (B // 2, -3, 0)):
+        bad, good = ln.clone(), ln.clone()
+        bad[at], good[at] = wrong, meant
+        out, lse = cross.cross_fwd(q, k, v, good)
+        want = cross.cross_bwd(q, k, v, out, lse, dout, good)
+        assert binding.device_status() == binding.ATTN_OK
+        got = cross.cross_bwd(q, k, v, out, lse, dout, bad)
+        assert binding.device_status() == binding.ATTN_ERR_DEVICE_CHECK
+        # in bits: keys that were behind the end, and with them the gradients, hold NaN
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(want, got))
+
+
 def test_shared_inputs_and_repeated_use(cuda_device):
     """k and v one tensor, q among them; a graph of autograd used for two losses."""
     g = torch.Generator().manual_seed(25)
