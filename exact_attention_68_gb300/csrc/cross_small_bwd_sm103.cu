@@ -144,7 +144,9 @@ __global__ void __launch_bounds__(kSmallThreads) cross_small_bwd_kernel(const __
   // ---- the gradients: a 16-row tile (of queries or keys) and half of the channels a warp
   const int tile = warp >> 1, unit0 = (warp & 1) * (kUnits / 2);
   constexpr int kN = kUnits / 2;  // 8-channel blocks
-  auto store = [&](const float(&c)[kN][4], uint16_t* to, int64_t first, int rows, float mul) {
+  // rows from `live` on get 0: their weights are, but 0 times a query or dout that is not
+  // finite is not
+  auto store = [&](const float(&c)[kN][4], uint16_t* to, int64_t first, int rows, int live, float mul) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = 16 * tile + 8 * h + (lane >> 2);
@@ -153,7 +155,8 @@ __global__ void __launch_bounds__(kSmallThreads) cross_small_bwd_kernel(const __
       for (int n = 0; n < kN; ++n) {
         const int ch = 8 * (unit0 + n) + 2 * (lane & 3);
         if (ch < p.D)
-          *reinterpret_cast<uint32_t*>(to + (first + r) * p.D + ch) = pack_x2<F16>(c[n][2 * h] * mul, c[n][2 * h + 1] * mul);
+          *reinterpret_cast<uint32_t*>(to + (first + r) * p.D + ch) =
+              r < live ? pack_x2<F16>(c[n][2 * h] * mul, c[n][2 * h + 1] * mul) : 0u;
       }
     }
   };
@@ -187,13 +190,13 @@ __global__ void __launch_bounds__(kSmallThreads) cross_small_bwd_kernel(const __
   float c[kN][4];
   if (tile < row_tiles) {
     product(c, 2, false, L::kK, key_tiles);
-    store(c, p.dq, q0, p.rows, p.scale);
+    store(c, p.dq, q0, p.rows, p.rows, p.scale);
   }
-  if (16 * tile < p.Sk) {  // keys that are not there: their columns of P and dS are zero
+  if (16 * tile < p.Sk) {
     product(c, 2, true, L::kQ, tile < key_tiles ? row_tiles : 0);
-    store(c, p.dk, k0, p.Sk, p.scale);
+    store(c, p.dk, k0, p.Sk, len, p.scale);
     product(c, 0, true, L::kDo, tile < key_tiles ? row_tiles : 0);
-    store(c, p.dv, k0, p.Sk, 1.f);
+    store(c, p.dv, k0, p.Sk, len, 1.f);
   }
 }
 
