@@ -154,20 +154,12 @@ BwdPlan plan_bwd(const attn_cross_t& c, const Sizes& s, int sms) {
     b.space = kNoSpace;
     return b;
   }
-  const int step = b.width == 256 ? 64 : 128;  // keys, or queries, of a step
+  const int step = b.width == 256 ? 64 : 128;  // keys of a step
   b.n_qt = static_cast<int>((s.rows + 127) / 128);
   b.n_kt = static_cast<int>((s.Sk + 127) / 128);
   const double us = b.width == 64 ? 1.0 : 1.4;
   b.q_split = runs_of(s.BH * b.n_qt, (s.Sk + step - 1) / step, sms, us, 4.0, static_cast<double>(s.BH) * s.rows * s.D * 4);
-  b.kv.batch = static_cast<int>(c.batch), b.kv.heads = static_cast<int>(c.heads), b.kv.Sk = static_cast<int>(s.Sk);
-  b.kv.q_steps = static_cast<int>((s.rows + step - 1) / step);
-  b.kv.ctas = b.width == 256 ? 2 : 1;
-  b.kv.sms = sms;
-  b.kv.step_us = b.width == 64 ? 1.2f : b.width == 128 ? 1.9f : 1.7f;
-  b.kv.run_us = static_cast<float>(128.0 * s.D * 8 * 2 / 5e6);
-  // runs are of use where there may be fewer key tiles than SMs, or not many more
-  const bool few = s.BH * b.n_kt * b.kv.ctas < 4 * sms;
-  b.kv.most_runs = !few ? 1 : b.kv.q_steps < 8 ? b.kv.q_steps : 8;
+  b.kv = ea::plan_kv_runs(c.batch, c.heads, s.Sk, s.rows, s.D, b.width, sms);
   b.dq_space = b.q_split > 1 ? static_cast<size_t>(b.q_split) * s.BH * s.rows * s.D * 4 : 0;
   b.dk_space = b.kv.most_runs > 1 ? static_cast<size_t>(b.kv.most_runs) * s.BH * s.Sk * s.D * 4 : 0;
   b.space = b.dq_space + 2 * b.dk_space;
