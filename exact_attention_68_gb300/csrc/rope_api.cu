@@ -53,17 +53,31 @@ bool separate(const View& v, int64_t B, int64_t S, int64_t H, int64_t D) {
   return true;
 }
 
-// Whether two views of the same strides for batch and token, as parts of a packed
-// tensor have, lie beside one another in every token.
-bool beside(const View& a, int64_t ha, const View& b, int64_t hb, int64_t B, int64_t S, int64_t D) {
-  if (a.b != b.b || a.s != b.s) return false;
+// Whether two views, as parts of a packed tensor are, share no place; neither has two
+// values in one place (separate).  They lie apart as ranges, or do so in each block of
+// the outermost dimension: its stride T is that of both, and block i of both lies
+// within the same T values.
+bool apart(const View& a, int64_t ha, const View& b, int64_t hb, int64_t B, int64_t S, int64_t D) {
   const char *pa = static_cast<const char*>(a.p), *pb = static_cast<const char*>(b.p);
-  if (pb < pa) return beside(b, hb, a, ha, B, S, D);
-  const int64_t gap = (pb - pa) / 2;
-  const int64_t wa = (ha - 1) * a.h + D, wb = (hb - 1) * b.h + D;
-  if (gap < wa) return false;
-  if (S > 1 && gap + wb > a.s) return false;
-  return B == 1 || gap + wb + (S - 1) * a.s <= a.b || (S == 1 && gap + wb <= a.b);
+  if (pb < pa) return apart(b, hb, a, ha, B, S, D);
+  const int64_t delta = (pb - pa) / 2;
+  const int64_t sa[3] = {a.b, a.s, a.h}, sb[3] = {b.b, b.s, b.h}, na[3] = {B, S, ha}, nb[3] = {B, S, hb};
+  bool done[3] = {false, false, false};
+  int64_t ra = D, rb = D;  // what a block reaches
+  for (int i = 0; i < 3; ++i) ra += (na[i] - 1) * sa[i], rb += (nb[i] - 1) * sb[i];
+  for (;;) {
+    if (delta >= ra) return true;
+    int top = -1;
+    int64_t T = 0;
+    for (int i = 0; i < 3; ++i) {
+      const int64_t stride = na[i] > 1 ? sa[i] : nb[i] > 1 ? sb[i] : 0;
+      if (!done[i] && stride > T) top = i, T = stride;
+    }
+    if (top < 0 || (na[top] > 1 && nb[top] > 1 && sa[top] != sb[top])) return false;
+    ra -= (na[top] - 1) * sa[top], rb -= (nb[top] - 1) * sb[top];
+    if (ra > T || delta + rb > T) return false;
+    done[top] = true;
+  }
 }
 
 attn_status_t check_sizes(const attn_rope_part_t* parts, int n, int64_t B, int64_t S, int64_t D) {
@@ -151,7 +165,7 @@ attn_status_t check(const attn_rope_part_t* parts, int n, const attn_rope_t* rop
       if (!bwd || j <= i) continue;
       const View other = {r.dx, r.dx_stride_b, r.dx_stride_s, r.dx_stride_h};
       const uint64_t on = extent(other, B, S, r.heads, D);
-      if (overlaps(w, wn, r.dx, on) && !beside(dx, q.heads, other, r.heads, B, S, D)) return ATTN_ERR_INVALID_ARG;
+      if (overlaps(w, wn, r.dx, on) && !apart(dx, q.heads, other, r.heads, B, S, D)) return ATTN_ERR_INVALID_ARG;
       if (r.dweight) {
         const uint64_t dn = static_cast<uint64_t>(D) * (r.weight_f32 ? 4 : 2);
         if (hit(r.dweight, dn)) return ATTN_ERR_INVALID_ARG;

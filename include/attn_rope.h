@@ -99,8 +99,10 @@ ATTN_API size_t attn_rope_bwd_workspace(const attn_rope_part_t* parts, int n, in
  *   dweight = Σ_{b,s,h} dz ⊙ x·r,   dx = r·(g − x·r · mean(g ⊙ x·r)),  g = weight ⊙ dz
  *
  * or dx = dz where the part has no norm (its x is then not read and may be NULL).
- * dx may be a view of a packed gradient of the projection, beside other parts'
- * dx; it must not overlap anything read.  A second launch adds up dweight, from
+ * dx may be a view of a packed gradient of the projection, in any order of its
+ * dimensions, beside other parts' dx: where two dx interleave along a dimension they
+ * have the same stride there and lie in the same blocks of it.  It must not overlap
+ * anything read, as a range from its first value to its last.  A second launch adds up dweight, from
  * fp32 sums in the workspace (16-byte aligned, contents mean nothing before or
  * after; calls that may run at the same time need one each).
  */

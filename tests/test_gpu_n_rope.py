@@ -352,3 +352,26 @@ def test_packed_gradient_into_a_frozen_norm(cuda_device):
     assert lib.attn_rope_bwd(part, 1, r, at, B, S, D, 1e-6, 0, None, 0, torch.cuda.current_stream().cuda_stream) == 0
     torch.cuda.synchronize()
     assert torch.equal(dx, want)
+
+
+@pytest.mark.parametrize("order", ["bsphd", "sbphd", "bshpd", "sbhpd", "bphsd", "hbspd"])
+def test_packed_gradients_of_any_order(cuda_device, order):
+    """q, k and v of one packed projection whose dimensions (p: which of the three) lie in any order, forward and back:
+    the same bits as from and into tensors of their own."""
+    B, S, H, D, dt = 3, 7, 4, 72, torch.bfloat16
+    size = dict(b=B, s=S, h=H, d=D, p=3)
+    g = torch.Generator().manual_seed(14)
+    packed = torch.randn(*(size[c] for c in order), generator=g).to(dt).cuda()
+    into = torch.full_like(packed, SENTINEL)
+    parts = lambda t: t.permute(*(order.index(c) for c in "pbshd")).unbind(0)  # noqa: E731
+    plan, pos = plan_of(36, 2, True), torch.randint(-99, 99, (B, S, 2), generator=g, dtype=torch.int32).cuda()
+    ws = [torch.randn(D, generator=g).add(1).cuda() for _ in "qk"] + [None]
+    dys = [torch.randn(B, H, S, D, generator=g).to(dt).cuda() for _ in "qkv"]
+    turn, own = (True, True, False), [x.contiguous() for x in parts(packed)]
+    want = rope.rope_fwd(own, plan, pos, ws, 1e-6, turn)
+    assert all(torch.equal(a, b) for a, b in zip(rope.rope_fwd(parts(packed), plan, pos, ws, 1e-6, turn), want))
+    wdx, wdw = rope.rope_bwd(dys, own, plan, pos, ws, 1e-6, turn)
+    _, dw = rope.rope_bwd(dys, parts(packed), plan, pos, ws, 1e-6, turn, dxs=parts(into))
+    assert all(torch.equal(a, b) for a, b in zip(parts(into), wdx))
+    assert all(torch.equal(a, b) for a, b in zip(dw[:2], wdw[:2]))
+    assert binding.device_status() == binding.ATTN_OK

@@ -218,3 +218,79 @@ def test_binding_refuses_bad_tensors():
         rope.rope_fwd((x.float(),), plan, None)
     with pytest.raises(ValueError):
         rope.rope_fwd((), plan, None)
+
+
+def _packed(lib, B, S, D, views, own=20):
+    """The status of a gradient whose parts' dx are views (offset, strides of batch, token and head, heads) of one buffer."""
+    parts = _args(len(views), B=B, S=S, D=D, dweight=0)
+    for i, (at, sb, ss, sh, h) in enumerate(views):
+        parts[i].dx, parts[i].dx_stride_b, parts[i].dx_stride_s, parts[i].dx_stride_h = A + own * T + 2 * at, sb, ss, sh
+        parts[i].heads, parts[i].dweight = h, 0
+    return _call(lib, True, parts, n=len(views), B=B, S=S, D=D, r=_rope_struct(pairs=4))
+
+
+B_, S_, H_, D_ = 3, 5, 4, 64
+LAYOUTS = {  # of q, k and v in one buffer of B·S·3·H·D values: strides of batch, token and head, and how far apart they begin
+    "[B,S,3,H,D]": (S_ * 3 * H_ * D_, 3 * H_ * D_, D_, H_ * D_),
+    "[S,B,3,H,D]": (3 * H_ * D_, B_ * 3 * H_ * D_, D_, H_ * D_),
+    "[B,S,H,3,D]": (S_ * 3 * H_ * D_, 3 * H_ * D_, 3 * D_, D_),
+    "[S,B,H,3,D]": (3 * H_ * D_, B_ * 3 * H_ * D_, 3 * D_, D_),
+    "[B,3,H,S,D]": (3 * H_ * S_ * D_, D_, S_ * D_, H_ * S_ * D_),
+    "[B,H,3,S,D]": (3 * H_ * S_ * D_, D_, 3 * S_ * D_, S_ * D_),
+    "[H,B,S,3,D]": (S_ * 3 * D_, 3 * D_, B_ * S_ * 3 * D_, D_),
+}
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_packed_gradients_of_any_order(lib, layout):
+    sb, ss, sh, step = LAYOUTS[layout]
+    views = [(i * step, sb, ss, sh, H_) for i in range(3)]
+    # a sound layout goes on to the first CUDA call, which fails here
+    assert _packed(lib, B_, S_, D_, views) not in (BAD, MIS)
+    assert _packed(lib, B_, S_, D_, views[::-1]) not in (BAD, MIS)
+    for i in range(3):
+        for shift in (8, -8, D_ - 8):
+            moved = [(at + (shift if j == i else 0), *rest) for j, (at, *rest) in enumerate(views)]
+            assert _packed(lib, B_, S_, D_, moved) == BAD
+
+
+def test_packed_gradients_of_shared_heads(lib):
+    """q's heads, then k's and v's in pairs, of one token after the other; and with batch and tokens swapped."""
+    B, S, D, Hq, Hkv = 2, 7, 64, 8, 2
+    W = (Hq + 2 * Hkv) * D
+    for sb, ss in ((S * W, W), (W, B * W)):
+        views = [(0, sb, ss, D, Hq), (Hq * D, sb, ss, 2 * D, Hkv), ((Hq + 1) * D, sb, ss, 2 * D, Hkv)]
+        assert _packed(lib, B, S, D, views) not in (BAD, MIS)
+        views[1] = (Hq * D - D, sb, ss, 2 * D, Hkv)
+        assert _packed(lib, B, S, D, views) == BAD
+
+
+def _places(view, B, S, D):
+    at, sb, ss, sh, h = view
+    return {at + b * sb + s * ss + i * sh + d for b in range(B) for s in range(S) for i in range(h) for d in range(D)}
+
+
+def test_packed_gradients_against_the_places_themselves(lib):
+    """Random views: refused where any two values share a place; and taken as parts of a packed tensor with its
+    dimensions in random order."""
+    rng = np.random.default_rng(17)
+    D, shared = 8, 0
+    for _ in range(4000):
+        B, S, h = (int(x) for x in rng.integers(1, 4, 3))
+        sizes, reach, strides = [B, S, h], D, [0, 0, 0]
+        for i in rng.permutation(3):  # each dimension past what the inner ones reach, with room or none
+            strides[i] = reach + 8 * int(rng.integers(0, 9)) * int(rng.integers(0, 2))
+            reach += strides[i] * (sizes[i] - 1)
+        views = [(0, *strides, h),
+                 (8 * int(rng.integers(-40, 41)), *(x + 8 * int(rng.integers(0, 3)) * int(rng.integers(0, 2)) for x in strides),
+                  int(rng.integers(1, h + 1)))]
+        if _places(views[0], B, S, D) & _places(views[1], B, S, D):
+            shared += 1
+            assert _packed(lib, B, S, D, views) == BAD, (B, S, views)
+        sizes, inner, strides = [B, S, h, 3], D, [0] * 4
+        for i in rng.permutation(4):
+            strides[i] = inner
+            inner *= sizes[i]
+        views = [(p * strides[3], *strides[:3], h) for p in rng.permutation(3)]
+        assert _packed(lib, B, S, D, views) not in (BAD, MIS), (B, S, views)
+    assert shared > 400
