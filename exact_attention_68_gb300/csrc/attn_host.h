@@ -42,6 +42,16 @@ inline cudaError_t current_device_bound(int* dev) {
   return e;
 }
 
+// SMs of the current device.
+inline attn_status_t device_sms(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && *sms > 0) return ATTN_OK;
+  (void)cudaGetLastError();
+  return cuda_failure(static_cast<int>(e));
+}
+
 // Columns of the kernel that runs a head dimension D (a multiple of 8, at
 // most 256): the smallest of 64, 128, 256 that holds D.
 inline int kernel_head_dim(int64_t D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }

@@ -62,14 +62,6 @@ attn_status_t check_values(float scale, int dtype) {
   return ATTN_OK;
 }
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return sms;
-}
-
 // Into how many runs the `steps` of each of `units` pieces of work are cut, each
 // run on one of `sms` SMs: the number with the shortest expected time.  A run costs
 // its steps and `start` more of them; joining costs a launch and the bytes of the
@@ -186,15 +178,15 @@ extern "C" {
 size_t attn_cross_fwd_workspace(const attn_cross_t* sizes) {
   Sizes s;
   if (check_sizes(sizes, &s) != ATTN_OK) return 0;
-  const int sms = sm_count();
-  return sms ? plan_fwd(s, sms).space : 0;
+  int sms = 0;
+  return ea::device_sms(&sms) == ATTN_OK ? plan_fwd(s, sms).space : 0;
 }
 
 size_t attn_cross_bwd_workspace(const attn_cross_t* sizes) {
   Sizes s;
   if (check_sizes(sizes, &s) != ATTN_OK) return 0;
-  const int sms = sm_count();
-  return sms ? plan_bwd(*sizes, s, sms).space : 0;
+  int sms = 0;
+  return ea::device_sms(&sms) == ATTN_OK ? plan_bwd(*sizes, s, sms).space : 0;
 }
 
 attn_status_t attn_cross_fwd(const attn_cross_t* sizes, const void* q, const void* k, const void* v,
@@ -213,9 +205,11 @@ attn_status_t attn_cross_fwd(const attn_cross_t* sizes, const void* q, const voi
                          {lse, s.row_bytes, true}, {workspace, workspace_bytes, true}};
   if (any_overlap(spans, 7)) return ATTN_ERR_INVALID_ARG;
   int* status = nullptr;
+  int sms = 0;
   st = ea::current_status_words(&status);
+  if (st == ATTN_OK) st = ea::device_sms(&sms);
   if (st != ATTN_OK) return st;
-  const FwdPlan f = plan_fwd(s, sm_count());
+  const FwdPlan f = plan_fwd(s, sms);
   st = check_space(workspace, workspace_bytes, f.space);
   if (st != ATTN_OK) return st;
 
@@ -294,9 +288,10 @@ attn_status_t attn_cross_bwd(const attn_cross_t* sizes, const void* q, const voi
                           {workspace, workspace_bytes, true}};
   if (any_overlap(spans, 12)) return ATTN_ERR_INVALID_ARG;
   int* status = nullptr;
+  int sms = 0;
   st = ea::current_status_words(&status);
+  if (st == ATTN_OK) st = ea::device_sms(&sms);
   if (st != ATTN_OK) return st;
-  const int sms = sm_count();
   const BwdPlan b = plan_bwd(*sizes, s, sms);
   st = check_space(workspace, workspace_bytes, b.space);
   if (st != ATTN_OK) return st;

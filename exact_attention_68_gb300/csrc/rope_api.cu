@@ -190,14 +190,6 @@ uint64_t turn_fraction(double f) {
 
 int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return sms;
-}
-
 // Sizes, and the division of a token's number by S as a product: with l bits of S,
 // ceil(2^(30 + l) / S) is off by less than one in 2^(30 + l) / S, which no token
 // below 2^30 sees.
@@ -288,9 +280,10 @@ attn_status_t run(const attn_rope_part_t* parts, int n, const attn_rope_t* rope,
                   const attn_rope_positions_t* at, int64_t B, int64_t S, int64_t D, float eps, int dtype,
                   void* workspace, size_t space, bool bwd, cudaStream_t stream) {
   int* status = nullptr;
+  int sms = 0;
   attn_status_t st = ea::current_status_words(&status);
+  if (st == ATTN_OK) st = ea::device_sms(&sms);
   if (st != ATTN_OK) return st;
-  const int sms = sm_count();
   float* sums = static_cast<float*>(workspace);
   size_t need = 0;
   for (int i = 0, m; bwd && i < n; i += m) {
@@ -324,8 +317,8 @@ size_t attn_rope_bwd_workspace(const attn_rope_part_t* parts, int n, int64_t B, 
   bool any = false;
   for (int i = 0; i < n; ++i) any = any || parts[i].dweight;
   if (!any) return kNoSpace;
-  const int sms = sm_count();
-  if (sms == 0) return 0;
+  int sms = 0;
+  if (ea::device_sms(&sms) != ATTN_OK) return 0;
   // the number of CTAs goes by the rotation too, which is not told here: the most
   // that any has
   size_t bytes = 0;
