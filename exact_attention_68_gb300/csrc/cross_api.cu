@@ -84,13 +84,16 @@ int runs_of(int64_t units, int64_t steps, int sms, double step_us, double start,
   return best;
 }
 
+// The plans.  Each is one function and not inlined: a workspace query and the call
+// compare the same times, which a compiler that contracts products and sums in one copy
+// and not in the other could settle differently.
 struct FwdPlan {
   bool few;     // the kernel for few queries
   int cluster;  // its CTAs a slice
   int width, bn, n_qt, n_kt, runs;
   size_t space;
 };
-FwdPlan plan_fwd(const Sizes& s, int sms) {
+__attribute__((noinline)) FwdPlan plan_fwd(const Sizes& s, int sms) {
   FwdPlan f;
   // Few queries of up to 64 channels.  Against the persistent kernel, 16 rows: 128
   // slices of 1500 keys 11.5 us and 13.6, 4 slices of 16384 keys 10.3 and 9.9 (one row
@@ -134,7 +137,7 @@ struct BwdPlan {
   ea::KvRuns kv;
   size_t dq_space, dk_space, space;  // dk_space: of dk and of dv each
 };
-BwdPlan plan_bwd(const attn_cross_t& c, const Sizes& s, int sms) {
+__attribute__((noinline)) BwdPlan plan_bwd(const attn_cross_t& c, const Sizes& s, int sms) {
   BwdPlan b;
   std::memset(&b, 0, sizeof(b));
   b.width = ea::kernel_head_dim(s.D);

@@ -3,6 +3,7 @@ for the host against stand-ins for the CUDA runtime and the launches
 (tests/cuda/entry_fakes.cpp): what they do behind their first CUDA call."""
 import ctypes
 import os
+import random
 import shutil
 import subprocess
 import sys
@@ -34,20 +35,20 @@ def load(path):
     return lib
 
 
-A, T = 0x7F0000000000, 1 << 30  # device addresses that nobody reads
+A, T = 0x700000000000, 1 << 36  # device addresses that nobody reads
 
 
-def cross_fwd(lib, sizes, ws=A + 20 * T, space=1 << 29):
+def cross_fwd(lib, sizes, ws=A + 20 * T, space=1 << 34):
     return lib.attn_cross_fwd(cross._pack_sizes(*sizes), A, A + T, A + 2 * T, None, A + 3 * T, A + 4 * T, 0.125, 0, ws, space,
                               0, None)
 
 
-def cross_bwd(lib, sizes, ws=A + 20 * T, space=1 << 29):
+def cross_bwd(lib, sizes, ws=A + 20 * T, space=1 << 34):
     return lib.attn_cross_bwd(cross._pack_sizes(*sizes), *(A + i * T for i in range(3)), None, *(A + i * T for i in range(3, 10)),
                               0.125, 0, ws, space, 0, None)
 
 
-def rope_call(lib, bwd, ws=A + 20 * T, space=1 << 29):
+def rope_call(lib, bwd, ws=A + 20 * T, space=1 << 34):
     B, S, H, D = 2, 16, 4, 64
     part = rope._pack_part(A, S * H * D, H * D, D, H, A + T, 0, 0, A + 2 * T, A + 3 * T, S * H * D, H * D, D, A + 4 * T)
     if bwd:
@@ -88,3 +89,20 @@ def test_workspace_queries_without_a_device(entry):
     for s in SIZES.values():
         packed = cross._pack_sizes(*s)
         assert lib.attn_cross_fwd_workspace(packed) == 0 and lib.attn_cross_bwd_workspace(packed) == 0
+
+
+def test_workspace_queries_tell_what_the_calls_need(entry):
+    """Over random sizes: what the query says is enough, and a byte less is not."""
+    lib, rng, needed = load(entry), random.Random(5), 0
+    for _ in range(1500):
+        G, Hkv, D = rng.choice([1, 1, 2, 8]), rng.choice([1, 2, 5, 16]), rng.randrange(8, 257, 8)
+        sizes = (rng.choice([1, 1, 2, 9]), G * Hkv, Hkv, int(2 ** rng.uniform(0, 11)), int(2 ** rng.uniform(0, 14)), D)
+        for call, query in ((cross_fwd, lib.attn_cross_fwd_workspace), (cross_bwd, lib.attn_cross_bwd_workspace)):
+            need = query(cross._pack_sizes(*sizes))
+            assert need >= 16
+            assert call(lib, sizes, space=need) == binding.ATTN_OK, sizes
+            if need > 16:
+                needed += 1
+                assert call(lib, sizes, space=need - 1) == binding.ATTN_ERR_INVALID_ARG, sizes
+                assert call(lib, sizes, ws=A + 20 * T + 8, space=need) == binding.ATTN_ERR_MISALIGNED, sizes
+    assert needed > 500
