@@ -297,7 +297,8 @@ __global__ void __launch_bounds__(kThreads1Q, 1) attn_fwd_1q_kernel(const __grid
       if (valid && dbg_row(dbb, bh, grow, 0, 0, kChkLse)) p.part_lse[at] = (m + __log2f(l)) * kLn2;
     } else if (ok) {
       tc_fence_after_sync();
-      const float inv_l = lq > 0.f ? 1.f / lq : 0.f;
+      // (cross-attention: keys with no score but -inf give 0 / 0, unlike no keys)
+      const float inv_l = lq > 0.f || (CROSS && un.len > 0 && l == 0.f) ? 1.f / lq : 0.f;
       // column blocks of 64 (128 bytes per row), 128 rows each (16 KB); the
       // two 32-column loads of a block are in flight together
 #pragma unroll 1

@@ -397,7 +397,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) attn_fwd_1qp_kernel(const __grid
       tc_fence_after_sync();
       if (lane == 0) tma_store_wait_read();  // this warp's previous store has read the staging rows
       __syncwarp();
-      const float inv_l = lq > 0.f ? 1.f / lq : 0.f;
+      // (cross-attention: keys with no score but -inf give 0 / 0, unlike no keys)
+      const float inv_l = lq > 0.f || (CROSS && nkv > 0 && p.n_split == 1 && l == 0.f) ? 1.f / lq : 0.f;
       if (CROSS && p.n_split > 1) {  // this run's own result, to be joined
         const int64_t at = ((int64_t)(x % p.n_split) * p.BH + bh) * p.S + grow;
 #pragma unroll 1

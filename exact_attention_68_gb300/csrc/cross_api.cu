@@ -224,6 +224,7 @@ attn_status_t attn_cross_fwd(const attn_cross_t* sizes, const void* q, const voi
   j.out = static_cast<uint16_t*>(out), j.lse = lse;
   j.rows = s.BH * s.rows;
   j.runs = f.runs, j.D = static_cast<int>(s.D);
+  j.lens = lens, j.seq_rows = sizes->heads * s.rows;
   const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   if (f.few) {
     ea::FewParams p;

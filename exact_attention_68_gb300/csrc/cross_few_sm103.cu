@@ -288,7 +288,8 @@ __global__ void __launch_bounds__(FewLayout::kThreads) cross_few_kernel(const __
   const uint32_t cta_out = outs + kFewWarps * L::kOut, cta_stat = stats + kFewWarps * L::kRows * 16;
   const int quads = p.D / 4;
   auto finish = [&](int r, int c, float4 a, float mx, float sum, float sum_q) {
-    const float inv = sum_q == 0.f ? 0.f : 1.f / sum_q;
+    // no sum: no keys, or (unless the join finds out) none with a score but -inf, 0 / 0
+    const float inv = sum_q == 0.f && (len == 0 || p.runs > 1) ? 0.f : 1.f / sum_q;
     a.x *= inv, a.y *= inv, a.z *= inv, a.w *= inv;
     const int64_t row = (int64_t)bh * p.rows + r;
     const float lse = (mx + log2f(sum)) * kLn2F;

@@ -19,6 +19,8 @@ struct JoinFwdParams {
   float* lse;             // [rows]
   int64_t rows;
   int runs, D;
+  const int* lens;        // [rows / seq_rows] keys that are there; null: some everywhere
+  int64_t seq_rows;       // rows of a sequence
 };
 cudaError_t join_fwd_launch(const JoinFwdParams& p, bool f16, cudaStream_t stream);
 

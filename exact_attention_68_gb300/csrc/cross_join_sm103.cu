@@ -82,7 +82,9 @@ __global__ void __launch_bounds__(kFwdThreads) join_fwd_kernel(const __grid_cons
     const float4 o = s_sum[g * quads + c];
     a.x += o.x, a.y += o.y, a.z += o.z, a.w += o.w;
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  // no sum: no keys, or none with a score but -inf, 0 / 0
+  const bool none = sum == 0.f && p.lens != nullptr && __ldg(p.lens + row / p.seq_rows) <= 0;
+  const float inv = none ? 0.f : 1.f / sum;
   uint2 v;
   v.x = pack_x2<F16>(a.x * inv, a.y * inv), v.y = pack_x2<F16>(a.z * inv, a.w * inv);
   *reinterpret_cast<uint2*>(p.out + row * p.D + 4 * c) = v;

@@ -61,7 +61,9 @@ ATTN_API size_t attn_cross_fwd_workspace(const attn_cross_t* sizes);
  *            streams, graphs that share it) need a workspace each.
  *   wait_timeout_ns  bound on each in-kernel wait (ATTN_DEFAULT_WAIT_TIMEOUT_NS)
  *
- * A query of a sequence without keys gets out = 0 and lse = -inf.  How the work is
+ * A query of a sequence without keys gets out = 0 and lse = -inf.  One of a sequence
+ * with keys, and with a NaN score or one of +inf, gets NaN in both; with no score but
+ * -inf, NaN in out and -inf in lse.  How the work is
  * cut goes by the sizes, not by lens, which is on the device.  Results do not
  * depend on the order in which the GPU ran the work.
  */

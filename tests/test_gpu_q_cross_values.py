@@ -66,3 +66,76 @@ def test_gradient_where_two_numbers_of_runs_cost_nearly_the_same(cuda_device, st
         # P and dS are rounded to bf16, the result is; fp32 for the rest
         assert ((dk[0, i].double() - refs[0]).abs() <= h * mags[0] + 2.0 ** -12 * m2 + h * refs[0].abs()).all()
         assert ((dv[0, i].double() - refs[1]).abs() <= (h + 2.0 ** -12) * mags[1] + h * refs[1].abs()).all()
+
+
+# B, Hq, Hkv, Sq, Sk, lens, D: a CTA a slice, clusters, clusters and runs; tiles and runs of them, 128 and 64 keys a step
+FORWARDS = [
+    ((3, 4, 2, 2, 40, [40, 0, 17]), 64), ((2, 2, 2, 5, 700, [650, 300]), 64), ((1, 4, 1, 3, 20000, [19999]), 64),
+    ((2, 2, 2, 150, 300, [300, 200]), 64), ((3, 2, 2, 40, 400, [390, 0, 130]), 128), ((1, 4, 2, 64, 6000, [5500]), 128),
+    ((2, 2, 2, 150, 300, [300, 200]), 192), ((1, 2, 2, 30, 6000, [5500]), 256), ((2, 2, 1, 20, 100, [90, 70]), 256),
+]
+
+
+def _live_key(lens, b, i):
+    """Places of keys that are there: the first, one in the middle, the last."""
+    return (0, lens[b] // 2, lens[b] - 1)[i % 3]
+
+
+@pytest.mark.parametrize("shape,D", FORWARDS, ids=str)
+def test_keys_and_values_that_are_not_finite(cuda_device, shape, D):
+    """A key of NaN, or of an infinity that gives +inf scores, makes the rows that meet it NaN; with -inf scores it is
+    as if it were not there; a NaN value is its channel's.  However the keys are cut, and for no other head."""
+    B, Hq, Hkv, Sq, Sk, lens = shape
+    q, k, v, _, ln = problem(B, Hq, Hkv, Sq, Sk, D, lens, torch.bfloat16, seed=Sk + D)
+    q[..., 0] = q[..., 0].abs() + 0.5
+    q[..., ::2, 0] *= -1.0  # every other query's score against an infinite key is -inf, the others' +inf
+    k[..., 0] = k[..., 0].nan_to_num(0.0)
+    G = Hq // Hkv
+    want, wantl = cross.cross_fwd(q, k, v, ln)
+    for i in range(3):
+        at = _live_key(lens, 0, i)
+        k2 = k.clone()
+        k2[0, 0, at, 1] = NAN
+        out, lse = cross.cross_fwd(q, k2, v, ln)
+        assert out[0, :G].isnan().all() and lse[0, :G].isnan().all()
+        assert torch.equal(out[0, G:], want[0, G:]) and torch.equal(out[1:], want[1:])
+        k2 = k.clone()
+        k2[0, 0, at, 0] = INF
+        out, lse = cross.cross_fwd(q, k2, v, ln)
+        assert out[0, :G, 1::2].isnan().all() and lse[0, :G, 1::2].isnan().all()
+        k3, v3 = k.clone(), v.clone()
+        k3[0, 0, at, 0], v3[0, 0, at] = -1e30, 0.0  # a score far below the others, of the sign that is -inf above
+        k3[0, 0, at, 0] *= -1.0
+        ref, refl = cross.cross_fwd(q, k3, v3, ln)
+        assert torch.equal(out[0, :G, ::2], ref[0, :G, ::2]) and torch.equal(lse[0, :G, ::2], refl[0, :G, ::2])
+        v2 = v.clone()
+        v2[0, 0, at, 3] = NAN
+        out, lse = cross.cross_fwd(q, k, v2, ln)
+        assert out[0, :G, :, 3].isnan().all() and torch.equal(lse, wantl)
+        out[0, :G, :, 3] = want[0, :G, :, 3]
+        assert torch.equal(out, want)
+    assert binding.device_status() == binding.ATTN_OK
+
+
+@pytest.mark.parametrize("shape,D", FORWARDS, ids=str)
+def test_no_score_but_minus_infinity_is_not_no_keys(cuda_device, shape, D):
+    """All of a head's keys at -inf for some queries: 0 / 0 in out, -inf in lse; a sequence without keys keeps its 0.
+    One finite key among them is the result."""
+    B, Hq, Hkv, Sq, Sk, lens = shape
+    q, k, v, _, ln = problem(B, Hq, Hkv, Sq, Sk, D, lens, torch.bfloat16, seed=Sk + D + 1)
+    q[..., 0] = q[..., 0].abs() + 0.5
+    G, full = Hq // Hkv, k[0, 0].clone()
+    want, wantl = cross.cross_fwd(q, k, v, ln)
+    k[0, 0, :lens[0], 0] = -INF
+    out, lse = cross.cross_fwd(q, k, v, ln)
+    assert out[0, :G].isnan().all() and torch.isneginf(lse[0, :G]).all()
+    assert torch.equal(out[0, G:], want[0, G:]) and torch.equal(out[1:], want[1:])
+    assert torch.equal(lse[0, G:], wantl[0, G:]) and torch.equal(lse[1:], wantl[1:])
+    for i in range(3):
+        at = _live_key(lens, 0, i)
+        k[0, 0, :lens[0], 0], k[0, 0, at] = -INF, full[at]
+        out, lse = cross.cross_fwd(q, k, v, ln)
+        t = (q[0, :G].double() @ full[at].double()) * D ** -0.5
+        assert (out[0, :G] == v[0, 0, at]).all()  # a weight of 1
+        assert ((lse[0, :G].double() - t).abs() <= 2.0 ** -13 + t.abs() * 2.0 ** -22).all()
+    assert binding.device_status() == binding.ATTN_OK
