@@ -215,6 +215,7 @@ __device__ __forceinline__ void store_part(uint32_t taddr, float* to, int x0, fl
                                            const DbgBounds& dbb, int bh, int row, int site,
                                            bool none = false) {
   uint32_t o[32];
+  __syncwarp();  // the last call's stores were by row
   tmem_ld_32x32b_x32(taddr, o);
   tmem_ld_wait();
   reg_fence(o);

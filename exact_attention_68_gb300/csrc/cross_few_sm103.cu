@@ -74,8 +74,9 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+// (not .aligned: the loops before it leave a warp's threads at different times)
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 // This CTA's shared address as that of the cluster's CTA `rank`.
 __device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {

@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kSmallThreads) cross_small_bwd_kernel(const __
   // c += M (rows of this tile) · B over `steps` 16-row steps of B; the matrix and its
   // rest, transposed for sums over queries
   auto product = [&](float(&c)[kN][4], int which, bool transposed, int b_tile, int steps) {
+    __syncwarp();  // the last one's stores were by row
 #pragma unroll
     for (int n = 0; n < kN; ++n)
 #pragma unroll

@@ -4,6 +4,7 @@ for the host against stand-ins for the CUDA runtime and the launches
 import ctypes
 import os
 import random
+import re
 import shutil
 import subprocess
 import sys
@@ -106,3 +107,14 @@ def test_workspace_queries_tell_what_the_calls_need(entry):
                 assert call(lib, sizes, space=need - 1) == binding.ATTN_ERR_INVALID_ARG, sizes
                 assert call(lib, sizes, ws=A + 20 * T + 8, space=need) == binding.ATTN_ERR_MISALIGNED, sizes
     assert needed > 500
+
+
+def test_cluster_barriers_take_diverged_warps():
+    """They stand behind loops that a warp's threads leave one by one, where the aligned form is undefined."""
+    found = 0
+    for name in os.listdir(CSRC):
+        with open(os.path.join(CSRC, name)) as f:
+            text = f.read()
+        found += text.count("barrier.cluster.arrive")
+        assert not re.search(r"barrier\.cluster\.(arrive|wait)[.\w]*\.aligned", text), name
+    assert found >= 2
