@@ -369,8 +369,10 @@ def rotary_attention(q, k, v, plan=None, positions=None, q_weight=None, k_weight
                      causal=True):
     """Differentiable self-attention from the projections on: q, k, v [B, S, H, D] views
     are normalised (where a weight is given), turned and laid out by rope_fwd, then
-    attended over by attn_fwd.  Returns out [B, H, S, D]; gradients flow to q, k, v and
-    the weights."""
+    attended over by attn_fwd, so the three share one number of heads.  Returns out
+    [B, H, S, D]; gradients flow to q, k, v and the weights."""
+    if not q.shape == k.shape == v.shape:
+        raise ValueError("q, k, v must share a shape: heads that share keys and values are not attn_fwd's")
     if scale is None:
         scale = 1.0 / math.sqrt(q.shape[-1])
     return _RotaryAttentionFn.apply(q, k, v, plan, positions, q_weight, k_weight, float(eps), float(scale), bool(causal))

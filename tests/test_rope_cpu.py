@@ -294,3 +294,11 @@ def test_packed_gradients_against_the_places_themselves(lib):
         views = [(p * strides[3], *strides[:3], h) for p in rng.permutation(3)]
         assert _packed(lib, B, S, D, views) not in (BAD, MIS), (B, S, views)
     assert shared > 400
+
+
+def test_rotary_attention_refuses_shared_heads_at_once():
+    """Before the heads are turned, with the reason."""
+    q, k = (torch.zeros(1, 4, h, 8, dtype=torch.bfloat16) for h in (4, 2))
+    for args in ((q, k, k), (q, q, k), (q, k, q)):
+        with pytest.raises(ValueError, match="share a shape"):
+            rope.rotary_attention(*args)
