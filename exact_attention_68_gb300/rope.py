@@ -316,23 +316,31 @@ def rope_bwd(dys, xs, plan, positions=None, weights=None, eps: float = 1e-6, tur
     return list(dxs), grads
 
 
+def _kept(plan):
+    """A plan's tensors, to be saved for the backward pass as the others are: torch refuses them once changed."""
+    return (None, None) if plan is None else (plan[0], plan[1])
+
+
+def _plan_of(freq, axis, interleaved):
+    return None if freq is None else Rope(freq, axis, interleaved)
+
+
 class _NormRopeFn(torch.autograd.Function):
     """rope_fwd in forward, rope_bwd in backward (both through the C ABI)."""
 
     @staticmethod
     def forward(ctx, plan, positions, eps, turn, n, *tensors):
         xs, weights = tensors[:n], tensors[n:]
-        ctx.save_for_backward(positions, *tensors)
-        ctx.plan, ctx.eps, ctx.turn, ctx.n = plan, eps, turn, n
+        ctx.save_for_backward(positions, *_kept(plan), *tensors)
+        ctx.interleaved, ctx.eps, ctx.turn, ctx.n = plan and plan[2], eps, turn, n
         return tuple(rope_fwd(xs, plan, positions, weights, eps, turn))
 
     @staticmethod
     @once_differentiable
     def backward(ctx, *dys):
-        positions, *tensors = ctx.saved_tensors
-        n = ctx.n
-        dxs, dws = rope_bwd([dy.contiguous() for dy in dys], tensors[:n], ctx.plan, positions, tensors[n:], ctx.eps,
-                            ctx.turn)
+        positions, freq, axis, *tensors = ctx.saved_tensors
+        n, plan = ctx.n, _plan_of(freq, axis, ctx.interleaved)
+        dxs, dws = rope_bwd([dy.contiguous() for dy in dys], tensors[:n], plan, positions, tensors[n:], ctx.eps, ctx.turn)
         return (None, None, None, None, None, *dxs, *dws)
 
 
@@ -350,15 +358,16 @@ class _RotaryAttentionFn(torch.autograd.Function):
     def forward(ctx, q, k, v, plan, positions, wq, wk, eps, scale, causal):
         qh, kh, vh = rope_fwd((q, k, v), plan, positions, (wq, wk, None), eps, (plan is not None, plan is not None, False))
         out, lse = attn_fwd(qh, kh, vh, scale=scale, causal=causal)
-        ctx.save_for_backward(q, k, v, positions, wq, wk, qh, kh, vh, out, lse)
-        ctx.rest = plan, eps, scale, causal
+        ctx.save_for_backward(q, k, v, positions, *_kept(plan), wq, wk, qh, kh, vh, out, lse)
+        ctx.rest = plan and plan[2], eps, scale, causal
         return out
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
-        q, k, v, positions, wq, wk, qh, kh, vh, out, lse = ctx.saved_tensors
-        plan, eps, scale, causal = ctx.rest
+        q, k, v, positions, freq, axis, wq, wk, qh, kh, vh, out, lse = ctx.saved_tensors
+        interleaved, eps, scale, causal = ctx.rest
+        plan = _plan_of(freq, axis, interleaved)
         dq, dk, dv, _ = attn_bwd(qh, kh, vh, out, lse, dout.contiguous(), scale=scale, causal=causal)
         dxs, dws = rope_bwd((dq, dk, dv), (q, k, v), plan, positions, (wq, wk, None), eps,
                             (plan is not None, plan is not None, False))

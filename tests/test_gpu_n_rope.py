@@ -375,3 +375,17 @@ def test_packed_gradients_of_any_order(cuda_device, order):
     assert all(torch.equal(a, b) for a, b in zip(parts(into), wdx))
     assert all(torch.equal(a, b) for a, b in zip(dw[:2], wdw[:2]))
     assert binding.device_status() == binding.ATTN_OK
+
+
+def test_a_plan_changed_before_the_backward_pass_is_refused(cuda_device):
+    """As torch refuses any saved tensor that was changed in place; a plan left alone serves any number of calls."""
+    x = torch.randn(1, 4, 2, 64, device="cuda").to(torch.bfloat16).requires_grad_()
+    pos = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+    for call in (lambda p: rope.norm_rope((x,), p, pos)[0], lambda p: rope.rotary_attention(x, x, x, p, pos)):
+        for plan in (rope.rope_plan(64), rope.Rope(rope.rope_plan(64).inv_freq, None, True)):
+            a, b = (torch.autograd.grad(call(plan), x, torch.ones(1, 2, 4, 64, device="cuda").to(x.dtype))[0] for _ in "ab")
+            assert torch.equal(a, b)
+            y = call(plan)
+            plan.inv_freq.mul_(2.0)
+            with pytest.raises(RuntimeError, match="inplace"):
+                y.backward(torch.ones_like(y))
