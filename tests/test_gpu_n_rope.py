@@ -389,3 +389,23 @@ def test_a_plan_changed_before_the_backward_pass_is_refused(cuda_device):
             plan.inv_freq.mul_(2.0)
             with pytest.raises(RuntimeError, match="inplace"):
                 y.backward(torch.ones_like(y))
+
+
+@pytest.mark.parametrize("D,pairs", [(256, 127), (200, 33), (64, 31)])
+def test_odd_numbers_of_pairs_in_four_parts(cuda_device, D, pairs):
+    """One pair a vector and the most parts of a call, two of them with weights: the most a CTA keeps."""
+    B, S, heads, dt = 2, 19, (3, 2, 1, 5), torch.float16
+    g = torch.Generator().manual_seed(D)
+    xs = [torch.randn(B, S, h, D, generator=g).to(dt).cuda() for h in heads]
+    ws = [torch.randn(D, generator=g).add(1).cuda() if i % 2 == 0 else None for i in range(4)]
+    dys = [torch.randn(B, h, S, D, generator=g).to(dt).cuda() for h in heads]
+    plan, pos = plan_of(pairs, 3, False), torch.randint(-99, 99, (B, S, 3), generator=g, dtype=torch.int32).cuda()
+    turn = (True, True, False, True)
+    ys = rope.rope_fwd(xs, plan, pos, ws, 1e-6, turn)
+    dxs, dws = rope.rope_bwd(dys, xs, plan, pos, ws, 1e-6, turn)
+    for i, (y, mag) in enumerate(refs(xs, ws, pos, plan, turn)):
+        close(ys[i], y, mag, dt, D, what=f"y{i}")
+    for i, (dx, dw, dx_mag, dw_mag) in enumerate(refs(xs, ws, pos, plan, turn, dys)):
+        close(dxs[i], dx, dx_mag, dt, D, what=f"dx{i}")
+        if dw is not None:
+            close(dws[i], dw, dw_mag, torch.float32, D, chain=B * S * heads[i] + 64, what=f"dw{i}")

@@ -139,3 +139,47 @@ def test_no_score_but_minus_infinity_is_not_no_keys(cuda_device, shape, D):
         assert (out[0, :G] == v[0, 0, at]).all()  # a weight of 1
         assert ((lse[0, :G].double() - t).abs() <= 2.0 ** -13 + t.abs() * 2.0 ** -22).all()
     assert binding.device_status() == binding.ATTN_OK
+
+
+def test_gradients_past_four_gigabytes(cuda_device):
+    """dq, delta, dk and dv of both heads, the second of which lies past 2^32 bytes and 2^31 values of k: dq as the
+    sum over all keys, dk and dv at the first, the last and some keys between.  As the bounds of test_gpu_o_cross.py."""
+    H, Sk, D, n = 2, 9_000_001, 128, 9_000_001 - 3
+    g = torch.Generator(device="cuda").manual_seed(72)
+    q, dout = (torch.randn(1, H, 2, D, generator=g, device="cuda").to(torch.bfloat16) for _ in "qd")
+    k, v = (torch.empty(1, H, Sk, D, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    for t in (k, v):
+        for h in range(H):
+            for i in range(0, Sk, 1 << 20):
+                part = t[0, h, i:i + (1 << 20)]
+                part.copy_(torch.randn(part.shape, generator=g, device="cuda"))
+    k[0, :, -1000:] += 0.5 * q[0, :, :1]  # what lies far back decides
+    v[0, :, -1000:] += 4.0
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    out, lse = cross.cross_fwd(q, k, v, lens)
+    dq, dk, dv, delta = cross.cross_bwd(q, k, v, out, lse, dout, lens)
+    torch.cuda.synchronize()
+    assert binding.device_status() == binding.ATTN_OK
+    scale, h_step = D ** -0.5, 2.0 ** -8
+    want_delta = (dout.double() * out.double()).sum(-1)
+    assert ((delta.double() - want_delta).abs() <= 2.0 ** -16 * (dout.double() * out.double()).abs().sum(-1)).all()
+    for h in range(H):
+        Q, dO, z, d = q[0, h].double(), dout[0, h].double(), lse[0, h].double()[:, None], delta[0, h].double()[:, None]
+        ref, mag, mag2 = (torch.zeros(2, D, dtype=torch.double, device="cuda") for _ in range(3))
+        for i in range(0, n, 1 << 20):
+            kk, vv = (t[0, h, i:min(n, i + (1 << 20))].double() for t in (k, v))
+            p = torch.exp(scale * (Q @ kk.T) - z)
+            ds = p * (dO @ vv.T - d)
+            ref += scale * ds @ kk
+            mag += scale * ds.abs() @ kk.abs()
+            mag2 += scale * (p * (dO.abs() @ vv.abs().T + d.abs())) @ kk.abs()
+            last = i + (1 << 20) >= n
+            at = torch.arange(kk.shape[0] - 1100, kk.shape[0], device="cuda") if last else torch.arange(64, device="cuda")
+            w, s = p[:, at], ds[:, at]
+            for got, r, m in ((dv[0, h, i + at], w.T @ dO, w.T @ dO.abs()),
+                              (dk[0, h, i + at], scale * s.T @ Q, scale * s.abs().T @ Q.abs())):
+                m2 = scale * (w * (dO.abs() @ vv[at].abs().T + d.abs())).T @ Q.abs() + w.T @ dO.abs()
+                assert ((got.double() - r).abs() <= h_step * m + 2.0 ** -12 * m2 + h_step * r.abs()).all(), (h, i)
+        # runs of 1e5 keys and more: their fp32 sums add 2^-10 of the magnitude at most
+        assert ((dq[0, h].double() - ref).abs() <= (h_step + 2.0 ** -10) * mag + 2.0 ** -12 * mag2 + h_step * ref.abs()).all(), h
+        assert dq[0, h].abs().min() > 0 and (dk[0, h, n:] == 0).all() and (dv[0, h, n:] == 0).all()
