@@ -58,7 +58,7 @@ def _check(shim, D, rows, tiles, sms):
     args = (1, tiles, 128, rows, D, _width(D), sms)
     t = _times(D, rows, tiles, sms, shim.most_runs(*args))
     n = shim.runs_of(*args, tiles)
-    assert n == 1 + t.index(min(t)), (D, rows, tiles, sms)
+    assert t[n - 1] < min(t) + Fraction(1, 1000), (D, rows, tiles, sms)  # whole nanoseconds
     return sorted(t)
 
 
@@ -68,7 +68,7 @@ def test_near_ties(shim):
     for steps in (63, 83, 84, 103, 104, 124):
         first, second = _check(shim, 56, 128 * steps, 497, 152)[:2]
         assert second - first < first / 2 ** 24
-        assert shim.runs_of(1, 497, 128, 128 * steps, 56, 64, 152, 497) == 3
+        assert shim.runs_of(1, 497, 128, 128 * steps, 56, 64, 152, 497) == 2
 
 
 def test_the_cheapest_number_of_runs(shim):
@@ -82,7 +82,7 @@ def test_bounds(shim):
         assert shim.most_runs(1, 4, 128, rows, 64, 64, 152) == most
     assert shim.most_runs(1, 608, 128, 5000, 64, 64, 152) == 1 and shim.most_runs(1, 607, 128, 5000, 64, 64, 152) == 8
     assert shim.most_runs(1, 304, 128, 5000, 256, 256, 152) == 1
-    # the longest sums do not pass 64 bits
+    # the longest sums do not overflow
     for tiles in (1, 500, 607):
         _check(shim, 128, (1 << 31) - 200, tiles, 152)
         _check(shim, 64, (1 << 31) - 200, tiles, 152)
