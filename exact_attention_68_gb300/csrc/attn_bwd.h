@@ -65,6 +65,15 @@ struct BwdParams {
   float* part_dv;
 };
 
+// kMaskCross: whether P and dS enter their products in two 16-bit terms each, as in the
+// kernel of at most 64 queries and keys.  Rounded once, a gradient is 1.4 times as far
+// from the definition as the plain form's, its own rounding and theirs; but where a call
+// has few queries a handful of weights decide: of calls with at most 512, 40 of 1152
+// gradients were 1.5 to 2.1 times as far off, of larger ones 1 of 1584 (1.53).  Two terms
+// cost 128 slices of one query over 1500 keys of 64 channels 55.8 us against 50.0, of
+// 128 channels 79.9 against 73.4, of 256 224 against 207.
+inline bool two_terms(const BwdParams& p) { return p.S <= 128 && (long long)p.BH * p.S <= 512; }
+
 // Launches the dq kernel (which also writes delta) and then the dk/dv kernel
 // on `stream`.  f16: the 16-bit tensors are fp16 (else bf16).
 cudaError_t bwd_launch(const BwdParams& p, int D, bool causal, bool f16, cudaStream_t stream);

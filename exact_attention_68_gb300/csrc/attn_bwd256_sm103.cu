@@ -101,7 +101,8 @@ struct Dq256Layout {
   static constexpr uint32_t kTmemCols = 512, kSCol = 0, kPCol = 64, kQCol = 128, kDqCol = 256;
 };
 
-template <int MASK, bool F16>
+// TWO: dS enters its product in two terms, the 16-bit value and what rounding to it left.
+template <int MASK, bool F16, bool TWO>
 __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dq256_kernel(const __grid_constant__ BwdParams p) {
   using L = Dq256Layout;
   constexpr bool CAUSAL = MASK == kMaskCausal, CROSS = MASK == kMaskCross;
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dq256_kernel(const __
       if (CAUSAL) lim = min(lim, grow - c0);
       if (!valid) lim = -1;
       const bool edge = lim < 31;
-      uint32_t pk[16];
+      uint32_t pk[16], rest[TWO ? 16 : 1];
 #pragma unroll
       for (int e2 = 0; e2 < 16; ++e2) {
         float p0 = ex2_approx(fmaf(__uint_as_float(sv[2 * e2]), sl2, -lse2));
@@ -241,8 +242,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dq256_kernel(const __
           if (2 * e2 + 1 > lim) ds1 = 0.f;
         }
         pk[e2] = pack_x2<F16>(ds0, ds1);
+        if constexpr (TWO) rest[e2] = rest_x2<F16>(make_float2(ds0, ds1), pk[e2]);
       }
       tmem_st_32x32b_x16(tS, pk);
+      if constexpr (TWO) tmem_st_32x32b_x16(tS + 16, rest);
       tmem_st_wait();
       tc_fence_before_sync();
       mbar_arrive(bar(L::kPFull));
@@ -377,8 +380,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dq256_kernel(const __
       // dQ += dS · K_s (16 keys per step; K_s as an MN-major operand)
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        mma_ts_p(leader, tmem_base + L::kDqCol, tmem_base + L::kSCol + split_col(kk),
-                 d_kmn + ks * kTileUnits + kk * (2048 >> 4), kIdescQ, (s > 0 || kk > 0) ? 1u : 0u);
+#pragma unroll
+        for (int r = 0; r <= (TWO ? 1 : 0); ++r)
+          mma_ts_p(leader, tmem_base + L::kDqCol, tmem_base + L::kSCol + split_col(kk) + 16 * r,
+                   d_kmn + ks * kTileUnits + kk * (2048 >> 4), kIdescQ, (s > 0 || kk > 0 || r > 0) ? 1u : 0u);
       mma_commit_p(leader, bar(L::kKEmpty + ks));  // the next S overwrites dS: issued after these
     }
     if (leader) {
@@ -444,7 +449,8 @@ __device__ __forceinline__ void tmem_st_row(uint32_t taddr, const uint32_t (&w)[
   }
 }
 
-template <int D, int MASK, bool F16>
+// TWO: P and dS in two terms, as above.
+template <int D, int MASK, bool F16, bool TWO>
 __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_q64_kernel(const __grid_constant__ BwdParams p) {
   using L = KvQ64Layout<D>;
   constexpr bool CAUSAL = MASK == kMaskCausal, CROSS = MASK == kMaskCross;
@@ -588,7 +594,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_q64_kernel(const
       // (lse·log2e, delta) of these 32 query columns, two columns per load
       const float4* stat = reinterpret_cast<const float4*>(smem_gen + L::kStatOff +
                                                            st * L::kStatBytes + 8 * 32 * g);
-      uint32_t ppk[16], dpk[16];
+      uint32_t ppk[16], dpk[16], prest[TWO ? 16 : 1], drest[TWO ? 16 : 1];
 #pragma unroll
       for (int e2 = 0; e2 < 16; ++e2) {
         const int c = 2 * e2;
@@ -607,9 +613,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_q64_kernel(const
           if (c + 1 < lo || c + 1 > hi) ds1 = 0.f;
         }
         dpk[e2] = pack_x2<F16>(ds0, ds1);
+        if constexpr (TWO) {
+          prest[e2] = rest_x2<F16>(make_float2(p0, p1), ppk[e2]);
+          drest[e2] = rest_x2<F16>(make_float2(ds0, ds1), dpk[e2]);
+        }
       }
       tmem_st_32x32b_x16(tS, ppk);
       tmem_st_32x32b_x16(tP, dpk);
+      if constexpr (TWO) {
+        tmem_st_32x32b_x16(tS + 16, prest);
+        tmem_st_32x32b_x16(tP + 16, drest);
+      }
       tmem_st_wait();
       tc_fence_before_sync();
       mbar_arrive(bar(L::kPFull));
@@ -765,12 +779,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_q64_kernel(const
       // dV += Pᵀ · dO_t and dK += dSᵀ · Q_t over this CTA's columns (16 queries per step)
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
-        const uint32_t acc = (t > 0 || kk > 0) ? 1u : 0u;
         const uint32_t bo = st * kTileUnits + kk * (2048 >> 4);
-        mma_ts_p(leader, tmem_base + L::kDvCol, tmem_base + L::kSCol + split_col(kk), d_do_mn + bo,
-                 kIdescG, acc);
-        mma_ts_p(leader, tmem_base + L::kDkCol, tmem_base + L::kPCol + split_col(kk), d_q_mn + bo,
-                 kIdescG, acc);
+#pragma unroll
+        for (int r = 0; r <= (TWO ? 1 : 0); ++r) {
+          const uint32_t acc = (t > 0 || kk > 0 || r > 0) ? 1u : 0u;
+          mma_ts_p(leader, tmem_base + L::kDvCol, tmem_base + L::kSCol + split_col(kk) + 16 * r, d_do_mn + bo,
+                   kIdescG, acc);
+          mma_ts_p(leader, tmem_base + L::kDkCol, tmem_base + L::kPCol + split_col(kk) + 16 * r, d_q_mn + bo,
+                   kIdescG, acc);
+        }
       }
       mma_commit_p(leader, bar(L::kEmpty + st));  // the next Sᵀ, dPᵀ overwrite Pᵀ, dSᵀ: issued after these
     }
@@ -789,10 +806,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_q64_kernel(const
   }
 }
 
-template <int D, int MASK, bool F16>
+template <int D, int MASK, bool F16, bool TWO>
 cudaError_t dkdv_q64_launch(const BwdParams& p, cudaStream_t stream) {
   using L = KvQ64Layout<D>;
-  auto kkv = attn_bwd_dkdv_q64_kernel<D, MASK, F16>;
+  auto kkv = attn_bwd_dkdv_q64_kernel<D, MASK, F16, TWO>;
   cudaError_t e = cudaFuncSetAttribute(kkv, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
   if (e != cudaSuccess) return e;
   const long long units = MASK == kMaskCross ? (long long)p.n_kt * p.kv.most_runs : p.n_t;
@@ -805,9 +822,9 @@ cudaError_t dkdv_q64_launch(const BwdParams& p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kkv, p);
 }
 
-template <int MASK, bool F16>
+template <int MASK, bool F16, bool TWO = false>
 cudaError_t launch_256(const BwdParams& p, cudaStream_t stream) {
-  auto kdq = attn_bwd_dq256_kernel<MASK, F16>;
+  auto kdq = attn_bwd_dq256_kernel<MASK, F16, TWO>;
   cudaError_t e = cudaFuncSetAttribute(kdq, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        Dq256Layout::kAlloc);
   if (e != cudaSuccess) return e;
@@ -819,7 +836,7 @@ cudaError_t launch_256(const BwdParams& p, cudaStream_t stream) {
   cfg.dynamicSmemBytes = Dq256Layout::kAlloc;
   e = cudaLaunchKernelEx(&cfg, kdq, p);
   if (e != cudaSuccess) return e;
-  return dkdv_q64_launch<256, MASK, F16>(p, stream);
+  return dkdv_q64_launch<256, MASK, F16, TWO>(p, stream);
 }
 
 template <bool F16>
@@ -827,7 +844,8 @@ cudaError_t launch_masked(const BwdParams& p, int mask, cudaStream_t stream) {
   switch (mask) {
     case kMaskFull: return launch_256<kMaskFull, F16>(p, stream);
     case kMaskCausal: return launch_256<kMaskCausal, F16>(p, stream);
-    case kMaskCross: return launch_256<kMaskCross, F16>(p, stream);
+    case kMaskCross:
+      return two_terms(p) ? launch_256<kMaskCross, F16, true>(p, stream) : launch_256<kMaskCross, F16>(p, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -121,8 +121,9 @@ struct XqLayout {
   static constexpr uint32_t kDqCol = 256, kQCol = 384, kDoCol = 384 + D / 2;
 };
 
-// ORDERED: units of long sequences first.
-template <int D, bool F16, bool ORDERED>
+// ORDERED: units of long sequences first.  TWO: dS enters its product in two terms, the
+// 16-bit value and what rounding to it left, which has its place behind it.
+template <int D, bool F16, bool ORDERED, bool TWO>
 __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_constant__ BwdParams p) {
   using L = XqLayout<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
         reg_fence(dp[1]);
         // key columns of this half that are there: 0 .. lim
         const int lim = un.len - 1 - ((un.first + j) * kRowsX + 64 * g);
-        uint32_t pk[32];
+        uint32_t pk[32], rest[TWO ? 32 : 1];
         // with or without keys that are not: most steps pay for no comparison.  (A row
         // behind the last query is zero in Q and dO and never stored.)
         auto weigh = [&](auto masked) {
@@ -259,11 +260,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
               if (2 * e2 + 1 > lim) ds.y = 0.f;
             }
             pk[e2] = pack_x2<F16>(ds.x, ds.y);
+            if constexpr (TWO) rest[e2] = rest_x2<F16>(ds, pk[e2]);
           }
         };
         if (lim < 63) weigh(std::true_type{});  // the same in every thread of the warpgroup
         else weigh(std::false_type{});
         tmem_st_32x32b_x32(tS, pk);
+        if constexpr (TWO) tmem_st_32x32b_x32(tS + 32, rest);
         tmem_st_wait();
         tc_fence_before_sync();
         mbar_arrive(bar(L::kPFull + g));
@@ -417,9 +420,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
       const int ks = kp % L::kKStages;
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        mma_ts_p(leader, tmem_base + L::kDqCol, tmem_base + 128 * h + kk * 8,
-                 dk_mn + ks * kTileUnits + (4 * h + kk) * (2048 >> 4), kIdescQ,
-                 (first && kk == 0) ? 0u : 1u);
+#pragma unroll
+        for (int r = 0; r <= (TWO ? 1 : 0); ++r)
+          mma_ts_p(leader, tmem_base + L::kDqCol, tmem_base + 128 * h + 32 * r + kk * 8,
+                   dk_mn + ks * kTileUnits + (4 * h + kk) * (2048 >> 4), kIdescQ,
+                   (first && kk == 0 && r == 0) ? 0u : 1u);
     };
     auto k_full = [&](int kp) {
       return wait_warp(bar(L::kKFull + kp % L::kKStages), (kp / L::kKStages) & 1, kSiteXqMmaKV | (kp & 0x7f));
@@ -558,8 +563,9 @@ __device__ __forceinline__ int sub_steps(const BwdUnit& u, int S) {
   return 4 * u.n - (S - (u.first + u.n - 1) * kRowsX <= 64 ? 2 : 0);
 }
 
-// MANY: more sequences between a CTA's units than are worth looking at one by one.
-template <int D, bool F16, bool MANY>
+// MANY: more sequences between a CTA's units than are worth looking at one by one.  TWO:
+// P and dS in two terms, as in the dq kernel.
+template <int D, bool F16, bool MANY, bool TWO>
 __global__ void __launch_bounds__(kBwdThreads, 1) cross_dkdv_kernel(const __grid_constant__ BwdParams p) {
   using L = XkLayout<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -646,7 +652,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dkdv_kernel(const __grid
         // (−lse·log2e, −delta) of this quarter's 32 query columns, two columns per load
         const float4* stat = reinterpret_cast<const float4*>(
             smem_gen + L::kStatOff + ((pos + 1 + it) % L::kStages) * L::kStatBytes + 8 * 32 * q);
-        uint32_t ppk[16], dpk[16];
+        uint32_t ppk[16], dpk[16], prest[TWO ? 16 : 1], drest[TWO ? 16 : 1];
         auto weigh = [&](auto masked) {
           constexpr bool kMasked = decltype(masked)::value;
 #pragma unroll
@@ -665,12 +671,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dkdv_kernel(const __grid
             }
             ppk[e2] = pack_x2<F16>(p0, p1);
             dpk[e2] = pack_x2<F16>(ds.x, ds.y);
+            if constexpr (TWO) {
+              prest[e2] = rest_x2<F16>(make_float2(p0, p1), ppk[e2]);
+              drest[e2] = rest_x2<F16>(ds, dpk[e2]);
+            }
           }
         };
         if (__any_sync(0xffffffffu, hi < 31)) weigh(std::true_type{});
         else weigh(std::false_type{});
         tmem_st_32x32b_x16(tS, ppk);
         tmem_st_32x32b_x16(tP, dpk);
+        if constexpr (TWO) {
+          tmem_st_32x32b_x16(tS + 16, prest);
+          tmem_st_32x32b_x16(tP + 16, drest);
+        }
         tmem_st_wait();
         tc_fence_before_sync();
         mbar_arrive(bar(L::kPFull + g));
@@ -834,11 +848,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dkdv_kernel(const __grid
       const int b = t & 1, q = t & 3, st = (pos + 1 + (t >> 2)) % L::kStages;
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
-        const uint32_t a = 64 * b + kk * 8;
         const uint32_t bo = st * kTileUnits + (2 * q + kk) * (2048 >> 4);
-        const uint32_t acc = (t == 0 && kk == 0) ? 0u : 1u;
-        mma_ts_p(leader, tmem_base + L::kDvCol, tmem_base + a, ddo_mn + bo, kIdescG, acc);
-        mma_ts_p(leader, tmem_base + L::kDkCol, tmem_base + a + 32, dq_mn + bo, kIdescG, acc);
+#pragma unroll
+        for (int r = 0; r <= (TWO ? 1 : 0); ++r) {
+          const uint32_t a = 64 * b + 16 * r + kk * 8;
+          const uint32_t acc = (t == 0 && kk == 0 && r == 0) ? 0u : 1u;
+          mma_ts_p(leader, tmem_base + L::kDvCol, tmem_base + a, ddo_mn + bo, kIdescG, acc);
+          mma_ts_p(leader, tmem_base + L::kDkCol, tmem_base + a + 32, dq_mn + bo, kIdescG, acc);
+        }
       }
     };
     KvWalk walk = walk0;
@@ -907,7 +924,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dkdv_kernel(const __grid
   }
 }
 
-template <int D, bool F16>
+template <int D, bool F16, bool TWO>
 cudaError_t launch_cross(const BwdParams& p, cudaStream_t stream) {
   // Long sequences first where a CTA takes few units, which may differ much: a decoder's
   // ragged batch, 3.4 units a CTA, 93.3 us against 99.4 for the gradient (in their own
@@ -915,12 +932,12 @@ cudaError_t launch_cross(const BwdParams& p, cudaStream_t stream) {
   // CTA, 87.6 against 85.4, since the order has to be found and kept.
   const long long q_units = (long long)p.BH * p.n_qt * p.q_split;
   const bool ordered = p.lens != nullptr && p.BH / p.heads <= kMaxOrder && q_units < 5ll * p.sms;
-  auto kdq = ordered ? cross_dq_kernel<D, F16, true> : cross_dq_kernel<D, F16, false>;
+  auto kdq = ordered ? cross_dq_kernel<D, F16, true, TWO> : cross_dq_kernel<D, F16, false, TWO>;
   // Whether a CTA passes eight sequences and more from one unit to its next.  10000
   // sequences of one tile: 744 us against 1512, whose walk alone took longer than the
   // work; in every call, 300 sequences of 8 heads of 3 tiles 218 us against 204.
   const bool many = p.lens != nullptr && 8ll * p.heads * p.n_kt <= p.sms;
-  auto kkv = many ? cross_dkdv_kernel<D, F16, true> : cross_dkdv_kernel<D, F16, false>;
+  auto kkv = many ? cross_dkdv_kernel<D, F16, true, TWO> : cross_dkdv_kernel<D, F16, false, TWO>;
   cudaError_t e = cudaFuncSetAttribute(kdq, cudaFuncAttributeMaxDynamicSharedMemorySize, XqLayout<D>::kAlloc);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(kkv, cudaFuncAttributeMaxDynamicSharedMemorySize, XkLayout<D>::kAlloc);
@@ -936,11 +953,16 @@ cudaError_t launch_cross(const BwdParams& p, cudaStream_t stream) {
   return launch_after(kkv, ctas((long long)p.BH * p.n_kt * p.kv.most_runs), kBwdThreads, stream, p, XkLayout<D>::kAlloc);
 }
 
+template <int D, bool F16>
+cudaError_t launch_terms(const BwdParams& p, cudaStream_t stream) {
+  return two_terms(p) ? launch_cross<D, F16, true>(p, stream) : launch_cross<D, F16, false>(p, stream);
+}
+
 }  // namespace
 
 cudaError_t cross_bwd_launch(const BwdParams& p, int D, bool f16, cudaStream_t stream) {
-  if (D == 64) return f16 ? launch_cross<64, true>(p, stream) : launch_cross<64, false>(p, stream);
-  if (D == 128) return f16 ? launch_cross<128, true>(p, stream) : launch_cross<128, false>(p, stream);
+  if (D == 64) return f16 ? launch_terms<64, true>(p, stream) : launch_terms<64, false>(p, stream);
+  if (D == 128) return f16 ? launch_terms<128, true>(p, stream) : launch_terms<128, false>(p, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -41,6 +41,15 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b) {
   return s;
 }
 
+// What rounding a and b to the 16-bit pair `hi` left, as such a pair: the second term of
+// a product whose factor is to keep 16 bits and more.  (What is infinite becomes NaN.)
+template <bool F16>
+__device__ __forceinline__ uint32_t rest_x2(float2 v, uint32_t hi) {
+  const float2 back = F16 ? f16x2_to_f32(hi) : make_float2(bf16_lo(hi), bf16_hi(hi));
+  const float2 x = __ffma2_rn(back, make_float2(-1.f, -1.f), v);
+  return pack_x2<F16>(x.x, x.y);
+}
+
 __device__ __forceinline__ void st_shared_f32x2(uint32_t addr, float a, float b) {
   asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
 }

@@ -128,8 +128,7 @@ __global__ void __launch_bounds__(kSmallThreads) cross_small_bwd_kernel(const __
         }
         auto put = [&](int which, float a, float b) {  // the values, then what their rounding left
           const uint32_t hi = pack_x2<F16>(a, b);
-          const float2 back = F16 ? f16x2_to_f32(hi) : make_float2(bf16_lo(hi), bf16_hi(hi));
-          const uint32_t lo = pack_x2<F16>(a - back.x, b - back.y);
+          const uint32_t lo = rest_x2<F16>(make_float2(a, b), hi);
           const uint32_t to = sb + L::kP + which * L::kPair + pair_at(r, key >> 3) + 2 * (key & 7);
           asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(hi) : "memory");
           asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + L::kPair), "r"(lo) : "memory");

@@ -1,9 +1,12 @@
-"""GPU tests of what cross-attention and its gradient answer where values are not finite."""
+"""GPU tests of what cross-attention and its gradient answer where values are not finite, where a gradient's
+sums have few terms or are cut at a near tie, and past 4 GiB (the oracle is oracle/cross.py)."""
+import numpy as np
 import pytest
 import torch
 
 from exact_attention_68_gb300 import binding, cross
-from test_gpu_o_cross import problem
+from oracle import cross as oracle
+from test_gpu_o_cross import check, check_bwd, half_step, n64, problem
 
 pytestmark = pytest.mark.gpu
 
@@ -183,3 +186,32 @@ def test_gradients_past_four_gigabytes(cuda_device):
         # runs of 1e5 keys and more: their fp32 sums add 2^-10 of the magnitude at most
         assert ((dq[0, h].double() - ref).abs() <= (h_step + 2.0 ** -10) * mag + 2.0 ** -12 * mag2 + h_step * ref.abs()).all(), h
         assert dq[0, h].abs().min() > 0 and (dk[0, h, n:] == 0).all() and (dv[0, h, n:] == 0).all()
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,Sq,Sk,lens", [
+    (1, 1, 1, 1, 70, None), (2, 2, 2, 1, 700, [699, 130]), (1, 4, 2, 2, 5000, [4801]), (3, 2, 1, 20, 300, [300, 0, 129]),
+    (1, 3, 3, 64, 257, None), (2, 6, 1, 20, 400, [257, 400]), (1, 2, 2, 128, 129, [128]), (40, 2, 2, 3, 200, None)])
+@pytest.mark.parametrize("D", [64, 72, 128, 200, 256])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+def test_gradients_of_few_queries_round_once(cuda_device, B, Hq, Hkv, Sq, Sk, lens, D, dt):
+    """Slices whose queries are one tile: P and dS enter their products in two terms each, so that besides the fp32 sums
+    only the results are rounded.  An fp16 term below 2^-14 loses 2^-25 at most.  Of the norm the results' own rounding
+    is then all but a tenth: the rest is 2^-12 of the terms and less, against 2^-9 or 2^-12 that a rounding takes
+    on average, and adds up as squares do."""
+    q, k, v, dout, ln = problem(B, Hq, Hkv, Sq, Sk, D, lens, dt, seed=Sq + Sk + D)
+    out, lse = cross.cross_fwd(q, k, v, ln)
+    dq, dk, dv, delta = cross.cross_bwd(q, k, v, out, lse, dout, ln)
+    torch.cuda.synchronize()
+    assert binding.device_status() == binding.ATTN_OK
+    check_bwd(q, k, v, out, lse, dout, lens, D ** -0.5, (dq, dk, dv, delta))
+    full = lens if lens is not None else [Sk] * B
+    kk, vv = (np.nan_to_num(n64(x), nan=0.0, posinf=0.0, neginf=0.0) for x in (k, v))
+    rq, rk, rv, _, (mq, mk, mv, m2q, m2k) = oracle.cross_bwd(n64(q), kk, vv, n64(out), n64(lse), n64(dout), full, D ** -0.5)
+    h, tiny, G = half_step(dt), 2.0 ** -25 if dt == torch.float16 else 0.0, Hq // Hkv
+    sq = np.stack([[D ** -0.5 * np.abs(kk[b, i // G, :full[b]]).sum(0) + 1 for i in range(Hq)] for b in range(B)])[:, :, None]
+    sk = D ** -0.5 * np.abs(n64(q)).reshape(B, Hkv, -1, D).sum(2, keepdims=True) + 1
+    sv = np.abs(n64(dout)).reshape(B, Hkv, -1, D).sum(2, keepdims=True) + 1
+    for name, got, ref, m2, s in (("dq", dq, rq, m2q, sq), ("dk", dk, rk, m2k, sk), ("dv", dv, rv, mv, sv)):
+        check(name, got, ref, h * np.abs(ref) + 2.0 ** -12 * m2 + tiny * s)
+        err, own = (np.linalg.norm(n64(x) - ref) for x in (got, torch.from_numpy(ref).to(dt)))
+        assert err <= 1.1 * own, (name, err / own)
