@@ -454,6 +454,7 @@ template <int D, int MASK, bool F16, bool TWO>
 __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_q64_kernel(const __grid_constant__ BwdParams p) {
   using L = KvQ64Layout<D>;
   constexpr bool CAUSAL = MASK == kMaskCausal, CROSS = MASK == kMaskCross;
+  constexpr float kTimes = CROSS ? kPTimes<F16> : 1.f;  // of P in dv's product
   constexpr bool kSplit = L::kSplit;
   constexpr int kCols = L::kCols;
   constexpr int kTileQ = L::kTileQ;
@@ -605,7 +606,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_q64_kernel(const
           if (c < lo || c > hi) p0 = 0.f;
           if (c + 1 < lo || c + 1 > hi) p1 = 0.f;
         }
-        ppk[e2] = pack_x2<F16>(p0, p1);
+        const float2 pt = make_float2(p0 * kTimes, p1 * kTimes);
+        ppk[e2] = pack_x2<F16>(pt.x, pt.y);
         float ds0 = p0 * (__uint_as_float(dpv[c]) - sd.y);
         float ds1 = p1 * (__uint_as_float(dpv[c + 1]) - sd.w);
         if (CROSS && edge) {  // a key that is not there may make dP anything
@@ -614,7 +616,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_q64_kernel(const
         }
         dpk[e2] = pack_x2<F16>(ds0, ds1);
         if constexpr (TWO) {
-          prest[e2] = rest_x2<F16>(make_float2(p0, p1), ppk[e2]);
+          prest[e2] = rest_x2<F16>(pt, ppk[e2]);
           drest[e2] = rest_x2<F16>(make_float2(ds0, ds1), dpk[e2]);
         }
       }
@@ -637,13 +639,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_bwd_dkdv_q64_kernel(const
       const uint32_t tAcc = tmem_base + lane_bits + (g == 0 ? L::kDvCol : L::kDkCol);
       const uint32_t stage = sb + L::kQOff + g * (kCols / 64) * kBlk128;
       const CUtensorMap* map = g == 0 ? &p.tm_dv : &p.tm_dk;
-      const float mul = g == 0 ? 1.f : p.scale;
+      const float mul = g == 0 ? 1.f / kTimes : p.scale;
       if (CROSS && runs > 1) {  // this run's sum, to be added to the others
         float* to = (g == 0 ? p.part_dv : p.part_dk) +
                     (((int64_t)un.part * p.BH + bh) * p.Sk + gk) * p.d_cols;
 #pragma unroll 1
         for (int cc = 0; cc < kCols / 32; ++cc)
-          store_part(tAcc + 32 * cc, to, kCols * half + 32 * cc, 1.f, gk < keys, dbk, bh, gk, kChkStore);
+          store_part(tAcc + 32 * cc, to, kCols * half + 32 * cc, g == 0 ? 1.f / kTimes : 1.f, gk < keys, dbk, bh, gk, kChkStore);
       } else {
 #pragma unroll
         for (int cc = 0; cc < kCols / 64; ++cc)

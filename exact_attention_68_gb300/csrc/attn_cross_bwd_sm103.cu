@@ -669,10 +669,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dkdv_kernel(const __grid
               if (c > hi) p0 = 0.f, ds.x = 0.f;
               if (c + 1 > hi) p1 = 0.f, ds.y = 0.f;
             }
-            ppk[e2] = pack_x2<F16>(p0, p1);
+            const float2 pt = F16 ? __fmul2_rn(make_float2(p0, p1), make_float2(kPTimes<F16>, kPTimes<F16>))
+                                  : make_float2(p0, p1);
+            ppk[e2] = pack_x2<F16>(pt.x, pt.y);
             dpk[e2] = pack_x2<F16>(ds.x, ds.y);
             if constexpr (TWO) {
-              prest[e2] = rest_x2<F16>(make_float2(p0, p1), ppk[e2]);
+              prest[e2] = rest_x2<F16>(pt, ppk[e2]);
               drest[e2] = rest_x2<F16>(ds, dpk[e2]);
             }
           }
@@ -706,12 +708,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dkdv_kernel(const __grid
                     (((int64_t)un.part * p.BH + un.bh) * p.Sk + gk) * p.d_cols;
 #pragma unroll 1
         for (int c = 0; c < 2 * L::kChunks; ++c)
-          store_part(tAcc + c * 32, to, c * 32, 1.f, there, dbk, un.bh, gk, kChkStore);
+          store_part(tAcc + c * 32, to, c * 32, g == 0 ? 1.f / kPTimes<F16> : 1.f, there, dbk, un.bh, gk, kChkStore);
       } else {
 #pragma unroll 1
         for (int c = 0; c < L::kChunks; ++c)
           store_chunk<F16>(tAcc + c * 64, sb + (g == 0 ? L::kQOff : L::kDoOff) + st * L::kTile + c * kBlockX, r,
-                           g == 0 ? 1.f : p.scale, g == 0 ? &p.tm_dv : &p.tm_dk, c * 64, un.tile * kRowsX,
+                           g == 0 ? 1.f / kPTimes<F16> : p.scale, g == 0 ? &p.tm_dv : &p.tm_dk, c * 64, un.tile * kRowsX,
                            un.bh, wq, lane, dbk, !there);
         if (lane == 0) {
           tma_store_commit();

@@ -209,6 +209,11 @@ __device__ __forceinline__ void clear_tail(uint32_t tile, int rows, int live, bo
   __syncwarp();
 }
 
+// P enters dv's product times this, and dv is divided by it: fp16 holds values below
+// 2^-14 in steps of 2^-24 only, and weights are as small as one over the keys.
+template <bool F16>
+constexpr float kPTimes = F16 ? 4096.f : 1.f;
+
 // 32 columns of this thread's row of an fp32 TMEM accumulator, times mul, to
 // columns x0 .. of the row at `to` (none: zeros).  Call with the full warp.
 __device__ __forceinline__ void store_part(uint32_t taddr, float* to, int x0, float mul, bool valid,

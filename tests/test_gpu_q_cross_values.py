@@ -215,3 +215,30 @@ def test_gradients_of_few_queries_round_once(cuda_device, B, Hq, Hkv, Sq, Sk, le
         check(name, got, ref, h * np.abs(ref) + 2.0 ** -12 * m2 + tiny * s)
         err, own = (np.linalg.norm(n64(x) - ref) for x in (got, torch.from_numpy(ref).to(dt)))
         assert err <= 1.1 * own, (name, err / own)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Sk", [30000, 400000])
+def test_fp16_weights_of_very_many_keys(cuda_device, D, Sk):
+    """dv where most weights are below fp16's smallest normal value, 2^-14: as far off as with large ones, which is
+    P's rounding and dv's own, each h of a value at most and of equal size: 1.42 times dv's own by norm."""
+    Sq, dt = 300, torch.float16
+    g = torch.Generator(device="cuda").manual_seed(Sk + D)
+    q, dout = (torch.randn(1, 1, Sq, D, generator=g, device="cuda").to(dt) for _ in "qd")
+    k, v = (torch.randn(1, 1, Sk, D, generator=g, device="cuda").to(dt) for _ in "kv")
+    out, lse = cross.cross_fwd(q, k, v)
+    dv = cross.cross_bwd(q, k, v, out, lse, dout)[2][0, 0].double()
+    torch.cuda.synchronize()
+    assert binding.device_status() == binding.ATTN_OK
+    ref = torch.empty_like(dv)
+    for i in range(0, Sk, 1 << 16):
+        t = q[0, 0].double() @ k[0, 0, i:i + (1 << 16)].double().T * D ** -0.5
+        ref[i:i + (1 << 16)] = torch.exp(t - lse[0, 0].double()[:, None]).T @ dout[0, 0].double()
+    # dv itself is partly below 2^-14: its own rounding counts that
+    own = (ref.to(dt).double() - ref).norm()
+    assert (dv - ref).norm() <= 1.5 * own
+    h, mag = 2.0 ** -11, torch.zeros_like(ref)
+    for i in range(0, Sk, 1 << 16):
+        t = q[0, 0].double() @ k[0, 0, i:i + (1 << 16)].double().T * D ** -0.5
+        mag[i:i + (1 << 16)] = torch.exp(t - lse[0, 0].double()[:, None]).T @ dout[0, 0].double().abs()
+    assert ((dv - ref).abs() <= (h + 2.0 ** -12) * mag + h * ref.abs() + 2.0 ** -25).all()
