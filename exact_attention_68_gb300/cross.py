@@ -12,9 +12,10 @@ errors are those of the header; there is no fallback.
 
 A captured backward pass of the differentiable forms needs what torch asks of any: no
 eager graph of the same leaves may be alive, since their gradients would be added up
-on that graph's stream.  cross_bwd itself has no such bound.  Nothing synchronises.  A workspace is allocated per call where one is needed, unless
-one is passed; calls that may run at the same time, and graphs, need one each.  With
-``stream``, what a call allocates belongs to that stream, as if it were the current one.
+on that graph's stream.  cross_bwd itself has no such bound.  Nothing synchronises.  A
+workspace is allocated per call where one is needed, unless one is passed; calls that may
+run at the same time, and graphs, need one each.  With ``stream``, what a call allocates
+belongs to that stream, as if it were the current one.
 """
 from __future__ import annotations
 

@@ -25,9 +25,9 @@
 // us a unit of two steps on average); else the exchange between the elementwise warps
 // and the warp that issues products, and at 64 channels that warp itself.
 // Measured on a GB300, both kernels and the joins, calls in a graph: 2 x 16 heads,
-// 4096 queries, 300 and 100 keys of 128 channels 82.6 us (dq 44, dk and dv 38); 8 x 16
-// heads, 500 queries, 300 to 1500 keys of 64 channels 93.7 us; 2 x 16 heads on 4 of
-// keys, 4000 queries, 6000 keys of 128 channels 924 us, 1060 TFLOP/s of the formula's
+// 4096 queries, 300 and 100 keys of 128 channels 83.9 us (dq 44, dk and dv 38); 8 x 16
+// heads, 500 queries, 300 to 1500 keys of 64 channels 94.6 us; 2 x 16 heads on 4 of
+// keys, 4000 queries, 6000 keys of 128 channels 936 us, 1050 TFLOP/s of the formula's
 // five products.  One CTA a tile: 156, 131 and 1022 us.
 //
 // Roles as there: warps 0-7 elementwise, warp 8 issues tcgen05.mma, warp 9 feeds the

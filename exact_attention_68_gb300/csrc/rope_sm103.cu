@@ -15,8 +15,9 @@
 //   D/16 neighbouring lanes, whatever that number is (the sums over a row are
 //   shuffles that stop at its last lane), and a warp as many rows as fit.
 //   Rows come through a ring in shared memory that each lane fills and reads for
-//   itself (cp.async, no barrier), several rows ahead and across units: 32 to 64 KB
-//   in flight on an SM without registers to hold them.
+//   itself (cp.async, no barrier), two slots ahead and across units: up to 64 KB in
+//   flight on an SM (16 warps, slots of 2 KB), 96 KB in the gradient (12 warps, x and
+//   dy in 4 KB), without registers to hold them.
 //   Units are dealt to the warps of one full grid, each the same number of them.
 //
 // Angles.  A position adds the fraction inv_freq / 2π of a turn.  It is kept as
@@ -33,7 +34,10 @@
 // TB/s.  12720 tokens of 3 x 16 heads of 72 channels in neighbouring pairs: 51 and 81
 // us, 52 % and 43 %: a row of 144 bytes fills four and a half lanes, and both run at
 // half of the issue slots with the latency of shared memory in between.  One token of 16
-// sequences: 8 us, a chain of positions, angles, rows and stores.  A CTA for eight
+// sequences: 8 us, a chain of positions, angles, rows and stores.  Pairs half a row
+// apart that 8 does not divide go in narrower vectors: of the first case 60, 62 and 63
+// pairs in place of 64 take 44, 55 and 108 us (75, 101 and 245 the gradient); one pair a
+// vector has no asynchronous copies, and its gradient spills 48 bytes.  A CTA for eight
 // tokens with its rows in registers took 60 us for the first; one row a lane, 42 to
 // 47; rings of 2 or 4 and other numbers of CTAs, 40 to 52.
 #include <type_traits>

@@ -15,8 +15,8 @@ formulas, the layouts and the errors are the header's; there is no fallback.
 
 A captured backward pass of the differentiable forms needs what torch asks of any: no
 eager graph of the same leaves may be alive, since their gradients would be added up
-on that graph's stream.  rope_bwd itself has no such bound.  Nothing synchronises.  With ``stream``, what a call allocates belongs to that
-stream, as if it were the current one.
+on that graph's stream.  rope_bwd itself has no such bound.  Nothing synchronises.  With
+``stream``, what a call allocates belongs to that stream, as if it were the current one.
 """
 from __future__ import annotations
 

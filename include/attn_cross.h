@@ -10,9 +10,9 @@
  *
  * These entry points come from the same library, return attn.h's status codes,
  * record device-side findings in the status word that attn_device_status reads,
- * validate every argument before touching CUDA, enqueue on the caller's stream
- * without synchronising, and allocate nothing beyond the status words that
- * attn_fwd also uses.  Make the first call on a device before any stream capture.
+ * validate every argument before touching CUDA (but for the workspace's size, which
+ * goes by the device), enqueue on the caller's stream without synchronising, and
+ * allocate nothing beyond the status words that attn_fwd also uses.  Make the first call on a device before any stream capture.
  *
  * What k and v hold behind a sequence's end may be anything, NaN and infinities
  * included; it is never used.  lens is read on the device: an entry outside
@@ -41,7 +41,7 @@ typedef struct {
 /*
  * attn_cross_fwd_workspace — bytes of workspace that attn_cross_fwd needs on the
  * current device for these sizes (16: none, workspace may be NULL; 0: on sizes it
- * would refuse).
+ * would refuse, or where the device cannot be asked).
  */
 ATTN_API size_t attn_cross_fwd_workspace(const attn_cross_t* sizes);
 
@@ -79,6 +79,12 @@ ATTN_API size_t attn_cross_bwd_workspace(const attn_cross_t* sizes);
 /*
  * attn_cross_bwd — gradient of attn_cross_fwd with respect to q, k and v: attn_bwd's
  * formulas, with sums over the query heads that share a key head.
+ *
+ * P and dS are rounded to the 16-bit type for their products; where a call has few
+ * queries (q_heads / heads · Sq <= 128, and 512 in all; or at most 64 queries and 64 keys)
+ * they enter in two terms.  fp16 holds a dS below 2^-14 in steps of 2^-24, and one above
+ * 65504 as an infinity, whose sums are infinite or NaN: scale the loss between the two,
+ * or use bf16.
  *
  *   q, k, v, lens, out, lse   the forward's inputs and results (read)
  *   dout     device, 16-bit, shaped as q, 16-byte aligned (read)

@@ -25,9 +25,11 @@
  * stays below |position| · inv_freq · 2^-52 + 2^-21 radians.
  *
  * The entry points come from the same library as attn.h's, return its status
- * codes, validate every argument before touching CUDA, enqueue on the caller's
- * stream without synchronising and allocate nothing.  Results do not depend on
- * the order in which the GPU ran the work.
+ * codes, validate every argument before touching CUDA (but for a workspace's size,
+ * which goes by the device), enqueue on the caller's stream without synchronising and
+ * allocate nothing beyond the status words that attn_fwd also uses.  Make the first
+ * call on a device before any stream capture.  Results do not depend on the order in
+ * which the GPU ran the work.
  */
 #ifndef EXACT_ATTENTION_68_ATTN_ROPE_H_
 #define EXACT_ATTENTION_68_ATTN_ROPE_H_
@@ -60,7 +62,7 @@ typedef struct {
 typedef struct {
   const void* x;        /* device, 16-bit, 16-byte aligned: x[b, s, h, d] */
   int64_t stride_b, stride_s, stride_h; /* of x in values, multiples of 8, >= 0; channels are adjacent */
-  int64_t heads;        /* >= 1 */
+  int64_t heads;        /* 1 .. 65535 */
   const void* weight;   /* device [D], 4-byte aligned: the norm's weight; NULL: no norm */
   int weight_f32;       /* 1: weight (and dweight) fp32; 0: the call's 16-bit type */
   int turn;             /* 1: rotate */
@@ -88,7 +90,7 @@ ATTN_API attn_status_t attn_rope_fwd(const attn_rope_part_t* parts, int n, const
                                      int64_t D, float eps, attn_dtype_t dtype, cudaStream_t stream);
 
 /* Bytes of workspace attn_rope_bwd needs on the current device (16: none, NULL
- * will do; 0: on an argument it would refuse). */
+ * will do; 0: on an argument it would refuse, or where the device cannot be asked). */
 ATTN_API size_t attn_rope_bwd_workspace(const attn_rope_part_t* parts, int n, int64_t B, int64_t S,
                                         int64_t D);
 
